@@ -478,6 +478,166 @@ OL_API ol_status ol_chunk_step(int32_t layout, const void* cache_desc, void* upd
                                void* workspace, size_t ws_bytes, ol_stream stream);
 
 /*
+ * Rotary positions. A head's leading rot_dim elements form rot_dim / 2 pairs
+ * (x, y); at position p pair i turns by the angle p * f_i:
+ *   x' = magnitude * (x cos - y sin),  y' = magnitude * (x sin + y cos),
+ * in fp32, rounded once to the row's dtype; the elements past rot_dim keep
+ * their bits. OL_ROPE_HALF pairs element i with i + rot_dim / 2,
+ * OL_ROPE_INTERLEAVED 2i with 2i + 1.
+ *   turns     device [rot_dim / 2]: f_i / (2 pi), the turns per position, in
+ *             units of 2^-64 turn (ol_rope_turns fills such a table). The angle
+ *             is taken modulo a turn in 64-bit integers, so it loses nothing at
+ *             far positions.
+ *   rot_dim   even, 2 .. head_dim
+ *   magnitude factor of the rotated part, positive and finite (1: a pure rotation)
+ */
+typedef enum ol_rope_style { OL_ROPE_HALF = 0, OL_ROPE_INTERLEAVED = 1 } ol_rope_style;
+typedef struct ol_rope {
+  const uint64_t* turns;
+  int32_t rot_dim;
+  int32_t style;
+  float magnitude;
+} ol_rope;
+
+/*
+ * A view of vectors [batch, heads, tokens, head_dim] with any strides, in
+ * elements; the head_dim elements of a vector are consecutive. Strides are
+ * not negative. An input's strides may be 0 (a broadcast) and its vectors may
+ * lie in a fused projection's output; vectors that a call writes must not
+ * overlap one another (OL_ERR_SHAPE). `data` needs its element's alignment
+ * only (OL_ERR_ALIGN): 16-byte aligned views are the fast ones.
+ */
+typedef struct ol_rows {
+  void* data;
+  int64_t stride_batch, stride_head, stride_token;
+} ol_rows;
+
+/*
+ * Scalings for contexts longer than the original one, as ol_rope_turns
+ * computes f_i from f0_i = base^(-2i / rot_dim):
+ *   OL_ROPE_UNSCALED  f_i = f0_i
+ *   OL_ROPE_LINEAR    f_i = f0_i / factor
+ *   OL_ROPE_NTK       f0 of the base base * factor^(rot_dim / (rot_dim - 2)); rot_dim >= 4
+ *   OL_ROPE_BY_PARTS  with r = original_len * f0_i / (2 pi), the pair's turns over
+ *                     the original context, and k = clamp((r - low) / (high - low), 0, 1):
+ *                     f_i = (1 - k) * f0_i / factor + k * f0_i. Such scalings often go
+ *                     with magnitude 0.1 * ln(factor) + 1.
+ */
+typedef enum ol_rope_scaling {
+  OL_ROPE_UNSCALED = 0, OL_ROPE_LINEAR = 1, OL_ROPE_NTK = 2, OL_ROPE_BY_PARTS = 3
+} ol_rope_scaling;
+
+/*
+ * Fill turns_host [rot_dim / 2] (host memory) for ol_rope.turns. base > 1 and
+ * factor >= 1 (finite); original_len > 0 and 0 <= low < high (finite) are read
+ * by OL_ROPE_BY_PARTS alone. Errors: NULL, SHAPE.
+ */
+OL_API ol_status ol_rope_turns(int32_t scaling, int32_t rot_dim, double base, double factor, double original_len,
+                               double low, double high, uint64_t* turns_host);
+
+/*
+ * Rotate vectors [batch, heads, tokens, head_dim] (OL_BF16 or OL_F32) of `in`
+ * into `out`, for example q and new K/V before ol_decode_step, or K before a
+ * quantized append. positions_dev is int32 [batch, tokens] with per_token != 0,
+ * else [batch]: row b's token t sits at positions_dev[b] + t. Any int32
+ * position is taken, negative ones too. `out` may equal `in` (same pointer and
+ * strides: in place); any other overlap of their extents is OL_ERR_ALIAS.
+ * Errors: NULL, SHAPE, DTYPE, ALIAS, ALIGN, UNSUPPORTED (head_dim > 1024, or
+ * batch * tokens >= 2^31), CUDA.
+ */
+OL_API ol_status ol_rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch, int32_t heads, int32_t tokens,
+                              int32_t head_dim, const ol_rows* in, const ol_rows* out, const int32_t* positions_dev,
+                              int32_t per_token, ol_stream stream);
+
+/*
+ * Append with rotary positions, one launch: for every row b, tokens
+ * t = 0 .. counts[b] - 1 of k are rotated and, with the same tokens of v
+ * unrotated, written at cache positions positions[b] + t (contiguous or paged
+ * cache, in place, `updated` aliasing the descriptor's data pointer); the same
+ * tokens of q (if given) are rotated into q_out. The views have new_len tokens
+ * per row, kv_heads (k, v) or q_heads (q, q_out) heads and the cache's dtype.
+ *   counts   [batch] tokens appended per row, 0 .. new_len (both NULL: new_len).
+ *            Cache slots and q_out vectors past a row's count are not written.
+ *   angles_dev  int32 [batch, new_len] (NULL: positions[b] + t): the positions
+ *            that the rotation uses where they are not the cache's, as for a tree
+ *            of drafted tokens (its depths) or a context whose start was dropped.
+ *   q, q_out both NULL with q_heads 0: K and V alone. q_out may equal q (in
+ *            place), also where q, k and v interleave in one projection's output;
+ *            any other q_out must not overlap the extents of q, k or v.
+ * Every written page must be in [0, num_pages) and is written once: by one row,
+ * through one entry of its table (OL_ERR_PAGE). The kernel reads positions, counts and the block table
+ * on the device, so a captured launch replays with the values it finds there;
+ * a token whose place is not in the cache is skipped.
+ * Errors: NULL, ALIAS, READONLY, CAPACITY, SHAPE, DTYPE, BUSY, PAGE, ALIGN,
+ * UNSUPPORTED (other layouts; head_dim > 1024), CUDA.
+ */
+OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* updated, const ol_rope* rope,
+                                int32_t new_len, const ol_rows* k, const ol_rows* v, int32_t q_heads,
+                                const ol_rows* q, const ol_rows* q_out, const int32_t* positions_host,
+                                const int32_t* positions_dev, const int32_t* counts_host, const int32_t* counts_dev,
+                                const int32_t* angles_dev, ol_stream stream);
+
+/*
+ * Attention of a tree of drafted tokens over a contiguous or paged cache
+ * (read-only use of the cache). The last counts[b] of row b's lens[b] cached
+ * tokens are its drafted nodes 0 .. counts[b] - 1, in that order; the tokens
+ * before them are the row's prefix. Node i attends the prefix and the drafted
+ * tokens that its mask bits name:
+ *   mask_dev  uint64 [batch, nodes, (nodes + 63) / 64]: bit j % 64 of word
+ *             j / 64 set: node i sees drafted token j. A tree gives each node its
+ *             ancestors' bits and its own; any bits are taken, bits past the
+ *             row's count are ignored. NULL: a chain (node i sees 0 .. i).
+ *   counts    [batch] nodes per row, 0 .. nodes and at most lens[b] (both NULL:
+ *             nodes). Outputs past a row's count are not written.
+ *   node_positions_dev  int32 [batch, nodes], read only with a window (window
+ *             >= 0): the nodes' positions; values below the row's prefix length
+ *             count as that length. A node at position p sees only tokens t with
+ *             p - position(t) <= window (a prefix token's position is its index).
+ *             NULL: prefix length + i; required with both a mask and a window.
+ * q and out [batch, q_heads, nodes, head_dim] (q in the cache's dtype, out in
+ * out_dtype), as ol_chunk_step. scale <= 0 selects 1/sqrt(head_dim). A node that
+ * sees nothing gives 0; what a node does not see has no influence on its output,
+ * whatever K and V hold there (drafted tokens hidden from some nodes and visible
+ * to others may hold infinities or NaN; a prefix token behind a window must be
+ * finite while other nodes still see it).
+ * ws_bytes >= ol_workspace_size_tree(batch, q_heads, kv_heads, head_dim, nodes);
+ * the workspace needs ol_workspace_init once. Lengths, counts and the block
+ * table are read on the device: a captured launch replays with the values it
+ * finds there (up to the capacity); out-of-range ones are clamped and recorded
+ * as OL_DEVICE_GUARD. Two launches. In the statistics attended_tokens counts
+ * every drafted token as seen (the mask is on the device) and
+ * kv_payload_bytes_read the tokens that some node may see, once.
+ * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
+ * UNSUPPORTED (other layouts, head_dim > 256, nodes > 512), CUDA.
+ */
+OL_API size_t ol_workspace_size_tree(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                     int32_t nodes);
+OL_API ol_status ol_tree_attention(int32_t layout, const void* cache_desc, const void* q, int32_t q_heads,
+                                   int32_t nodes, const int32_t* lens_host, const int32_t* lens_dev,
+                                   const int32_t* counts_host, const int32_t* counts_dev, const uint64_t* mask_dev,
+                                   const int32_t* node_positions_dev, float scale, int32_t window, void* out,
+                                   int32_t out_dtype, void* workspace, size_t ws_bytes, ol_stream stream);
+
+/*
+ * Keep the accepted path of a tree: for every row b, the K and V of drafted
+ * tokens kept[b][0] < kept[b][1] < ... (kept_counts[b] of them, each in
+ * [0, nodes)) move to cache positions starts[b], starts[b] + 1, ..., in place;
+ * starts[b] is the row's prefix length, the position of its drafted token 0.
+ * Nothing else is written. kept_dev int32 [batch, nodes] and kept_counts_dev
+ * [batch] are read on the device only (a verifier's result needs no copy to
+ * the host): a row whose count is outside [0, nodes], whose kept list does not
+ * ascend strictly inside [0, nodes) or whose tokens leave the cache is left as
+ * it was, with OL_DEVICE_GUARD in the status word of `workspace` (may be NULL).
+ * The host checks starts[b] >= 0 and starts[b] + nodes <= capacity, and that
+ * every page of those tokens is in the pool and named once.
+ * Errors: NULL, ALIAS, READONLY, CAPACITY, SHAPE, DTYPE, BUSY, PAGE, ALIGN,
+ * UNSUPPORTED (other layouts), CUDA.
+ */
+OL_API ol_status ol_tree_keep(int32_t layout, const void* cache_desc, void* updated, int32_t nodes,
+                              const int32_t* starts_host, const int32_t* starts_dev, const int32_t* kept_dev,
+                              const int32_t* kept_counts_dev, void* workspace, ol_stream stream);
+
+/*
  * Storage statistics of a call (page "Persistent input/output feedback",
  * sections Opt-in storage auditing through runtime events and Optional
  * heterogeneous paged KV: the storage_* reports and the direct call's

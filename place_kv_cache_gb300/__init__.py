@@ -32,6 +32,8 @@ PAGE_FORMAT_DTYPE = np.dtype([("kf", "<i4"), ("ks", "<f4"), ("kz", "<i4"), ("vf"
                               ("vz", "<i4")])
 OL_Q_DYNAMIC, OL_Q_FIXED = 0, 1
 OL_DEVICE_OK, OL_DEVICE_GUARD = 0, 1
+OL_ROPE_HALF, OL_ROPE_INTERLEAVED = 0, 1
+OL_ROPE_UNSCALED, OL_ROPE_LINEAR, OL_ROPE_NTK, OL_ROPE_BY_PARTS = range(4)
 
 SYMBOLS = ("ol_status_string", "ol_version", "ol_workspace_size", "ol_workspace_init", "ol_workspace_status",
            "ol_cache_bind", "ol_cache_unbind", "ol_cache_update", "ol_cache_update_rows",
@@ -39,7 +41,8 @@ SYMBOLS = ("ol_status_string", "ol_version", "ol_workspace_size", "ol_workspace_
            "ol_int4kv_decode_attention", "ol_decode_step", "ol_decode_step_noalloc", "ol_noalloc_status", "ol_workspace_size_host",
            "ol_decode_step_host", "ol_last_call_stats", "ol_total_stats", "ol_reset_stats",
            "ol_workspace_size_chunk", "ol_chunk_step", "ol_hpaged_append", "ol_hpaged_decode_attention",
-           "ol_hpaged_decode_step", "ol_hpaged_quantize", "ol_hpaged_chunk_step")
+           "ol_hpaged_decode_step", "ol_hpaged_quantize", "ol_hpaged_chunk_step", "ol_rope_turns", "ol_rope_rows",
+           "ol_rope_append", "ol_workspace_size_tree", "ol_tree_attention", "ol_tree_keep")
 
 
 class Stats(ctypes.Structure):
@@ -101,6 +104,18 @@ class HPagedKV(ctypes.Structure):
                 ("access", ctypes.c_int32), ("owner", ctypes.c_uint64)]
 
 
+class Rope(ctypes.Structure):
+    """ol_rope: a rotation's table of turns per position, its size, pairing and magnitude."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    """ol_rows: a strided view of vectors [batch, heads, tokens, head_dim]."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_head", ctypes.c_int64),
+                ("stride_token", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -127,7 +142,7 @@ def load(build_if_missing: bool = True, variant: str = ""):
     L._variant = variant
     vp, i32, i64, u64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float,
                                   ctypes.c_size_t)
-    st = ctypes.c_int
+    f64, st = ctypes.c_double, ctypes.c_int
     sig = {
         "ol_status_string": (ctypes.c_char_p, [st]),
         "ol_version": (i32, []),
@@ -163,6 +178,12 @@ def load(build_if_missing: bool = True, variant: str = ""):
                                     vp]),
         "ol_hpaged_chunk_step": (st, [ctypes.POINTER(HPagedKV), vp, vp, i32, i32, vp, ctypes.POINTER(PageFormat), vp,
                                       vp, f32, i32, vp, i32, vp, sz, vp]),
+        "ol_rope_turns": (st, [i32, i32, f64, f64, f64, f64, f64, vp]),
+        "ol_rope_rows": (st, [vp, i32, i32, i32, i32, i32, vp, vp, vp, i32, vp]),
+        "ol_rope_append": (st, [i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "ol_workspace_size_tree": (sz, [i32, i32, i32, i32, i32]),
+        "ol_tree_attention": (st, [i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, f32, i32, vp, i32, vp, sz, vp]),
+        "ol_tree_keep": (st, [i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -317,6 +338,31 @@ def hpaged_kv(pool, formats, formats_host, block_table, block_table_host, *, kv_
                  page_size, head_dim, B, M, access, owner)
     d._refs = (pool, formats, formats_host, block_table, bt_host)  # keeps the buffers alive
     return d
+
+
+def rows(t) -> Rows:
+    """View of a tensor [batch, heads, tokens, head_dim] with any strides (the elements of a vector consecutive), for
+    example a slice of a projection's output ``qkv.view(B, T, heads, D).transpose(1, 2)[:, :q_heads]``."""
+    if t.dim() != 4:
+        raise ValueError(f"rows takes a tensor [batch, heads, tokens, head_dim], not {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError("the elements of a vector must be consecutive")
+    r = Rows(_ptr(t), t.stride(0), t.stride(1), t.stride(2))
+    r._refs = (t,)
+    return r
+
+
+def rope(rot_dim: int, *, style: int = OL_ROPE_HALF, base: float = 10000.0, scaling: int = OL_ROPE_UNSCALED,
+         factor: float = 1.0, original_len: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 1.0,
+         device="cuda") -> Rope:
+    """A rotation whose table is computed by ol_rope_turns and kept on `device`."""
+    import torch
+    turns = torch.empty(max(rot_dim, 0) // 2, dtype=torch.int64)
+    ol_rope_turns(scaling, rot_dim, base, factor, original_len, low, high, turns)
+    turns = turns.to(device)
+    r = Rope(_ptr(turns), rot_dim, style, magnitude)
+    r._refs = (turns,)
+    return r
 
 
 # ------------------------------------------------------------------ calls
@@ -513,3 +559,65 @@ def ol_hpaged_chunk_step(kv: HPagedKV, updated, q, q_heads: int, new_len: int, n
     _check(load().ol_hpaged_chunk_step(ctypes.byref(kv), _ptr(updated), _ptr(q), q_heads, new_len, _ptr(new_kv),
                                        ctypes.byref(new_pages), _ptr(lh), _ptr(lens_dev), scale, window, _ptr(out),
                                        out_dtype, _ptr(workspace), ws_bytes, _stream(stream)), "ol_hpaged_chunk_step")
+
+
+def _ref(struct):
+    """The address of a descriptor (None stays NULL)."""
+    return None if struct is None else ctypes.addressof(struct)
+
+
+def _rows(x):
+    """A view as it is, or that of a tensor (None stays None)."""
+    return x if x is None or type(x) is Rows else rows(x)
+
+
+def ol_rope_turns(scaling: int, rot_dim: int, base: float, factor: float, original_len: float, low: float,
+                  high: float, turns_host):
+    """Fill turns_host (rot_dim / 2 64-bit integers in host memory) with the turns per position of a rotation."""
+    _check(load().ol_rope_turns(scaling, rot_dim, base, factor, original_len, low, high, _ptr(turns_host)),
+           "ol_rope_turns")
+
+
+def ol_rope_rows(rope: Rope, dtype: int, batch: int, heads: int, tokens: int, head_dim: int, in_rows, out_rows,
+                 positions_dev, per_token: bool, stream=None):
+    """Rotate in_rows into out_rows (views, or tensors [B, H, T, D]; the same one: in place). positions_dev is
+    [B, T] with per_token, else [B] first positions."""
+    i, o = _rows(in_rows), _rows(out_rows)
+    _check(load().ol_rope_rows(_ref(rope), dtype, batch, heads, tokens, head_dim, _ref(i), _ref(o),
+                               _ptr(positions_dev), int(per_token), _stream(stream)), "ol_rope_rows")
+
+
+def ol_rope_append(layout: int, desc, updated, rope: Rope, new_len: int, k, v, q_heads: int, q, q_out,
+                   positions_host, positions_dev, counts_host=None, counts_dev=None, angles_dev=None, stream=None):
+    """Rotated k and v appended at positions[b], q rotated into q_out: views, or tensors [B, H, new_len, D] (q and
+    q_out None with q_heads 0). counts: tokens per row; angles_dev [B, new_len]: positions of the rotation."""
+    ph, ch = _host_i32(positions_host), _host_i32(counts_host)
+    k, v, q, q_out = _rows(k), _rows(v), _rows(q), _rows(q_out)
+    _check(load().ol_rope_append(layout, _ref(desc), _ptr(updated), _ref(rope), new_len, _ref(k), _ref(v), q_heads,
+                                 _ref(q), _ref(q_out), _ptr(ph), _ptr(positions_dev), _ptr(ch), _ptr(counts_dev),
+                                 _ptr(angles_dev), _stream(stream)), "ol_rope_append")
+
+
+def ol_workspace_size_tree(batch: int, q_heads: int, kv_heads: int, head_dim: int, nodes: int) -> int:
+    return load().ol_workspace_size_tree(batch, q_heads, kv_heads, head_dim, nodes)
+
+
+def ol_tree_attention(layout: int, desc, q, q_heads: int, nodes: int, lens_host, lens_dev, counts_host, counts_dev,
+                      mask_dev, node_positions_dev, scale: float, window: int, out, out_dtype: int, workspace,
+                      ws_bytes: int, stream=None):
+    """Attention of drafted trees over a contiguous or paged cache: q and out [B, Hq, nodes, D], the last counts[b]
+    cached tokens of a row are its nodes (None: all rows have `nodes`), mask_dev [B, nodes, ceil(nodes / 64)] 64-bit
+    words name the drafted tokens a node sees (None: a chain)."""
+    lh, ch = _host_i32(lens_host), _host_i32(counts_host)
+    _check(load().ol_tree_attention(layout, _ref(desc), _ptr(q), q_heads, nodes, _ptr(lh), _ptr(lens_dev), _ptr(ch),
+                                    _ptr(counts_dev), _ptr(mask_dev), _ptr(node_positions_dev), scale, window,
+                                    _ptr(out), out_dtype, _ptr(workspace), ws_bytes, _stream(stream)),
+           "ol_tree_attention")
+
+
+def ol_tree_keep(layout: int, desc, updated, nodes: int, starts_host, starts_dev, kept_dev, kept_counts_dev,
+                 workspace=None, stream=None):
+    """Move the accepted drafted tokens kept[b][:kept_counts[b]] of every row to starts[b], starts[b] + 1, ..."""
+    sh = _host_i32(starts_host)
+    _check(load().ol_tree_keep(layout, _ref(desc), _ptr(updated), nodes, _ptr(sh), _ptr(starts_dev), _ptr(kept_dev),
+                               _ptr(kept_counts_dev), _ptr(workspace), _stream(stream)), "ol_tree_keep")

@@ -14,16 +14,10 @@
 #include <string>
 #include <vector>
 
-#include "ol_internal.h"
-#include "ol_launch.h"
+#include "ol_host.h"
 
 namespace ol {
-namespace {
 
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool empty() const { return hi <= lo; }
-};
 Range range_of(const void* p, size_t bytes) {
   uintptr_t a = reinterpret_cast<uintptr_t>(p);
   return {a, a + bytes};
@@ -257,18 +251,6 @@ int sm_count_cached() {
 }
 
 // ----------------------------------------------------------- descriptors
-
-struct CacheView {
-  int layout;
-  int dtype;
-  int batch, kv_heads, head_dim, capacity;
-  int access;
-  bool history_stable;
-  uint64_t owner;
-  void* alias_ptr;  // pointer that `updated` must equal
-  Range ranges[3];  // cache storage (INT4: three planes)
-  int nranges;
-};
 
 ol_status view_contiguous(const ol_kv_cache* c, CacheView& v) {
   if (!c || !c->data) return OL_ERR_NULL;
@@ -802,8 +784,6 @@ ol_status run_attention(int layout, const void* desc, const CacheView& v, const 
   }
   return e == cudaSuccess ? OL_OK : OL_ERR_CUDA;
 }
-
-}  // namespace
 
 ol_status decode_step_impl(int32_t layout, const void* cache_desc, void* updated, const void* q, int32_t q_heads,
                            const void* new_kv, const int32_t* lens_host, const int32_t* lens_dev, float scale,

@@ -1,0 +1,122 @@
+// ol_draft.h -- parameter blocks, shared arithmetic and launchers of the
+// operators around drafted tokens: rotary positions and the rotating append
+// (ol_rope.cu), attention of a tree over a cache (ol_tree.cu, ol_fast_tree.cu)
+// and the accepted path's move (ol_tree.cu). Not part of the public ABI.
+#pragma once
+
+#include "ol_internal.h"
+
+#if defined(__CUDACC__)
+#define OL_HD __host__ __device__
+#else
+#define OL_HD
+#endif
+
+namespace ol {
+
+// Where a token of a contiguous or paged cache lives.
+struct CacheRef {
+  void* base;                  // cache or pool
+  const int32_t* block_table;  // NULL: contiguous [2, batch, kv_heads, capacity, D]
+  int batch, kv_heads, capacity;
+  int num_pages, page_size, max_pages;
+};
+
+// ------------------------------------------------------------ rotary positions
+
+struct RopeView {  // strides in elements
+  char* data;
+  int64_t sb, sh, st;
+};
+
+struct RopeParams {
+  const uint64_t* turns;
+  int rot_dim, style;
+  float magnitude;
+  int dtype, head_dim, batch, tokens;
+  int q_heads, kv_heads;        // kv_heads 0: rotation of q alone
+  RopeView q, q_out, k, v;
+  CacheRef cache;               // destination of k and v
+  const int32_t* positions;     // [batch] first positions, or NULL
+  const int32_t* counts;        // [batch], or NULL
+  const int32_t* angles;        // [batch, tokens], or NULL: positions[b] + t
+  int vec;                      // 1: every vector and its rotated part is 16-byte aligned
+};
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
+
+// ------------------------------------------------------------- tree attention
+
+constexpr int kTreeMaxNodes = 512;
+constexpr int kTreeMaxCtas = 192;  // CTAs of the tensor-core kernel, one per SM
+constexpr int kTreeGenRows = 32;   // (head, node) rows of a CUDA-core unit
+constexpr int kTreeGenTile = 32;   // tokens of its tile
+constexpr int kTreeFastTile = 128;
+
+struct TreeParams {
+  CacheRef cache;
+  int dtype, batch, q_heads, kv_heads, group, head_dim;
+  int nodes, words;             // mask words per node
+  const void* q;                // [batch, q_heads, nodes, D]
+  const int32_t* lens;
+  const int32_t* counts;        // [batch], or NULL: nodes
+  const uint64_t* mask;         // NULL: a chain
+  const int32_t* node_pos;      // NULL: prefix + i
+  float scale_log2;             // softmax scale * log2(e)
+  int window;                   // < 0: unbounded
+  void* out;
+  int out_dtype;
+  int32_t* status;
+  float* partials;
+  // work split
+  int rows_per_unit;            // (head, node) rows r = head * nodes + node of a unit
+  int units_per_head;           // ceil(group * nodes / rows_per_unit)
+  int tile;                     // tokens per tile
+  int nctas;                    // the tiles of all units in contiguous equal shares
+};
+
+// A row's tokens as the work split sees them: drafted tokens are
+// [prefix, len), tokens [start, len) form ntiles tiles (start is a multiple of
+// the tile at or below the lowest token that any node may see).
+struct TreeRow {
+  int len, count, prefix, start, ntiles;
+};
+OL_HD inline TreeRow tree_row(int len, int count, int window, int tile) {
+  TreeRow r;
+  r.len = len;
+  r.count = count;
+  r.prefix = len - count;
+  const int lo = window < 0 || r.prefix <= window ? 0 : r.prefix - window;
+  r.start = lo / tile * tile;
+  r.ntiles = count > 0 ? (len - r.start + tile - 1) / tile : 0;
+  return r;
+}
+
+// One partial slot: m[rows] (log2 domain), l[rows], o[ceil(D / 4)][rows] float4.
+OL_HD inline size_t tree_slot_floats(int rows, int head_dim) { return (size_t)rows * (2 + (head_dim + 3) / 4 * 4); }
+inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }
+inline size_t tree_workspace_bytes(int q_heads, int kv_heads, int head_dim, int nodes) {
+  const size_t fast = 2ull * kTreeMaxCtas * tree_slot_floats(tree_fast_rows(q_heads / kv_heads, nodes), head_dim);
+  const size_t gen = 2ull * 2 * kTreeMaxCtas * tree_slot_floats(kTreeGenRows, head_dim);
+  return kStatusBytes + sizeof(float) * (fast > gen ? fast : gen);
+}
+
+bool fast_tree_supported(const TreeParams& p);
+cudaError_t launch_fast_tree(TreeParams& p, int sms, cudaStream_t s);
+cudaError_t launch_generic_tree(TreeParams& p, int sms, cudaStream_t s);
+cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s);
+
+// --------------------------------------------------------------- accepted path
+
+struct KeepParams {
+  CacheRef cache;
+  int dtype, head_dim, nodes;
+  const int32_t* starts;  // [batch]
+  const int32_t* kept;    // [batch, nodes]
+  const int32_t* counts;  // [batch]
+  int32_t* status;        // or NULL
+};
+cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s);
+
+}  // namespace ol
+
+#undef OL_HD

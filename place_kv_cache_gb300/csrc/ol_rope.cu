@@ -1,0 +1,175 @@
+// ol_rope.cu -- rotary positions: q, K (and any view of vectors) rotated on
+// their way to the output or to the cache, V copied along, in one launch.
+//
+// Pair i of a vector at position p turns by p * f_i. The table holds
+// f_i / (2 pi) in units of 2^-64 turn, so p * turns[i] in wrapping 64-bit
+// integers is the angle modulo a turn, exact to p * 2^-65 turns: positions of a
+// million lose nothing, where p * f_i in fp32 is off by 2^-24 * p radians. The
+// signed product over 2^63 is the angle in half turns, in [-1, 1): sincospif's
+// argument. Rotation in fp32, one rounding to the row's type.
+//
+// Bounds: 2 * D * elt bytes per vector against 3 * rot_dim flops: memory, or
+// the launch itself for a decode step. One CTA takes one token of one row and
+// all of its q, k and v vectors, so the token's sines and cosines are computed
+// once (rot_dim / 2 threads, through shared memory) and serve every head.
+#include "ol_common.cuh"
+#include "ol_draft.h"
+
+namespace ol {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 4;  // vectors in flight per thread
+constexpr int kRopeMaxHalf = 512;
+
+template <typename T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_float<uint16_t>(uint16_t x) { return bf16_bits_to_float(x); }
+template <typename T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ uint16_t from_float<uint16_t>(float x) { return float_to_bf16_bits(x); }
+
+// VE consecutive elements, moved as one access (16 bytes, or one element).
+template <typename T, int VE>
+struct alignas(sizeof(T) * VE) Piece {
+  T e[VE];
+};
+
+// The work item i of a vector covers pieces a and b: in the half style the
+// two halves of VE pairs, in the interleaved one VE / 2 pairs in one piece
+// (or, element by element, the two elements of a pair). Items past the rotated
+// part are single pieces that are copied.
+template <int VE, bool HALF>
+struct Items {
+  static constexpr bool kTwo = HALF || VE == 1;  // a rotated item has two pieces
+  int rotated, total;                            // items
+  __device__ Items(int rot_dim, int head_dim)
+      : rotated(kTwo ? rot_dim / 2 / VE : rot_dim / VE), total(rotated + (head_dim - rot_dim) / VE) {}
+  __device__ int first(int i, int rot_dim) const {
+    if (i >= rotated) return rot_dim + (i - rotated) * VE;
+    return HALF || VE > 1 ? i * VE : 2 * i;
+  }
+  __device__ int second(int i, int rot_dim) const { return HALF ? rot_dim / 2 + i * VE : 2 * i + 1; }
+};
+
+template <typename T, int VE, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  using P = Piece<T, VE>;
+  __shared__ float2 turn[kRopeMaxHalf];  // (cos, sin) * magnitude of this token
+  const int b = blockIdx.x / p.tokens, t = blockIdx.x % p.tokens;
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthreads = blockDim.x * blockDim.y;
+  pdl_wait();
+  if (p.counts && t >= p.counts[b]) return;
+  const int start = p.positions ? p.positions[b] : 0;
+  const long long at = p.angles ? p.angles[(size_t)b * p.tokens + t] : (long long)start + t;
+  // where this token's K and V go: element offset of (plane 0, head 0), and the strides
+  size_t slot = 0, head_stride = 0, plane_stride = 0;
+  if (p.kv_heads) {
+    const CacheRef& c = p.cache;
+    const long long pos = (long long)start + t;
+    if (start < 0 || pos >= c.capacity) return;  // device guard
+    if (c.block_table) {
+      const int page = c.block_table[(size_t)b * c.max_pages + pos / c.page_size];
+      if (page < 0 || page >= c.num_pages) return;  // device guard
+      head_stride = (size_t)c.page_size * p.head_dim;
+      slot = (size_t)page * c.kv_heads * head_stride + (size_t)(pos % c.page_size) * p.head_dim;
+      plane_stride = (size_t)c.num_pages * c.kv_heads * head_stride;
+    } else {
+      head_stride = (size_t)c.capacity * p.head_dim;
+      slot = (size_t)b * c.kv_heads * head_stride + (size_t)pos * p.head_dim;
+      plane_stride = (size_t)c.batch * c.kv_heads * head_stride;
+    }
+  }
+  for (int i = tid; i < p.rot_dim / 2; i += nthreads) {
+    const long long phase = (long long)((unsigned long long)at * p.turns[i]);
+    float s, c;
+    sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
+    turn[i] = make_float2(c * p.magnitude, s * p.magnitude);
+  }
+  __syncthreads();
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  const Items<VE, HALF> items(p.rot_dim, p.head_dim);
+  for (int i = threadIdx.x; i < items.total; i += blockDim.x) {
+    const bool rotated = i < items.rotated;
+    const bool two = rotated && Items<VE, HALF>::kTwo;
+    const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
+    constexpr int NP = Items<VE, HALF>::kTwo ? VE : VE / 2;  // pairs of an item
+    float2 cs[NP];
+    if (rotated)
+#pragma unroll
+      for (int j = 0; j < NP; ++j) cs[j] = turn[i * NP + j];
+    for (int h0 = threadIdx.y; h0 < heads; h0 += blockDim.y * kRopeUnroll) {
+      P a[kRopeUnroll], c[kRopeUnroll];
+      T* to[kRopeUnroll];
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const int h = h0 + u * blockDim.y;
+        to[u] = nullptr;
+        if (h >= heads) continue;
+        const T* from;
+        if (h < p.q_heads) {
+          from = reinterpret_cast<const T*>(p.q.data) + b * p.q.sb + h * p.q.sh + t * p.q.st;
+          to[u] = reinterpret_cast<T*>(p.q_out.data) + b * p.q_out.sb + h * p.q_out.sh + t * p.q_out.st;
+        } else {
+          const int plane = h - p.q_heads >= p.kv_heads, g = h - p.q_heads - (plane ? p.kv_heads : 0);
+          const RopeView& w = plane ? p.v : p.k;
+          from = reinterpret_cast<const T*>(w.data) + b * w.sb + g * w.sh + t * w.st;
+          to[u] = reinterpret_cast<T*>(p.cache.base) + plane * plane_stride + slot + g * head_stride;
+        }
+        a[u] = *reinterpret_cast<const P*>(from + ea);
+        if (two) c[u] = *reinterpret_cast<const P*>(from + eb);
+      }
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        if (!to[u]) continue;
+        if (rotated && h0 + u * blockDim.y < p.q_heads + p.kv_heads) {
+#pragma unroll
+          for (int j = 0; j < NP; ++j) {
+            T& ex = Items<VE, HALF>::kTwo ? a[u].e[j] : a[u].e[2 * j];
+            T& ey = Items<VE, HALF>::kTwo ? c[u].e[j] : a[u].e[(2 * j + 1) % VE];
+            const float x = to_float<T>(ex), y = to_float<T>(ey);
+            ex = from_float<T>(x * cs[j].x - y * cs[j].y);
+            ey = from_float<T>(x * cs[j].y + y * cs[j].x);
+          }
+        }
+        *reinterpret_cast<P*>(to[u] + ea) = a[u];
+        if (two) *reinterpret_cast<P*>(to[u] + eb) = c[u];
+      }
+    }
+  }
+}
+
+template <typename T, int VE>
+cudaError_t launch_style(const RopeParams& p, cudaStream_t s) {
+  const bool half = p.style == OL_ROPE_HALF;
+  const int items = (half || VE == 1 ? p.rot_dim / 2 : p.rot_dim) / VE + (p.head_dim - p.rot_dim) / VE;
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  const int x = items < kRopeThreads ? items : kRopeThreads;
+  const int y = kRopeThreads / x < heads ? kRopeThreads / x : heads;
+  cfg.gridDim = dim3(p.batch * p.tokens, 1, 1);
+  cfg.blockDim = dim3(x, y, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return half ? cudaLaunchKernelEx(&cfg, rope_kernel<T, VE, true>, p)
+              : cudaLaunchKernelEx(&cfg, rope_kernel<T, VE, false>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
+  if (p.dtype == OL_F32) return p.vec ? launch_style<float, 4>(p, s) : launch_style<float, 1>(p, s);
+  return p.vec ? launch_style<uint16_t, 8>(p, s) : launch_style<uint16_t, 1>(p, s);
+}
+
+}  // namespace ol

@@ -1,0 +1,354 @@
+// ol_tree.cu -- attention of drafted trees over a cache on CUDA cores (every
+// dtype and head size that the tensor-core kernel of ol_fast_tree.cu does not
+// take), the merge of both kernels' partial results, and the move of an
+// accepted path.
+//
+// A unit is 32 (head, node) rows of one row's kv head; its tokens form tiles of
+// 32. All units' tiles in order are cut into equal contiguous shares, one per
+// CTA (TreeWalk). A CTA runs the online softmax over its segment of a unit with
+// the scores S = Q K^T and the sums O += P V in registers: 4 rows x 2 tokens of
+// S, 4 rows x D / 16 dimensions of O per thread, operands from shared memory in
+// float4. Bound by fp32 FMA issue: 4 * 32 * D flops per token against 2 * D
+// elements read.
+#include "ol_tree.cuh"
+
+namespace ol {
+namespace {
+
+constexpr int RB = kTreeGenRows, TB = kTreeGenTile;
+constexpr int kGenThreads = 128;
+constexpr int kPStride = RB + 4;  // P is kept [token][row]
+
+__host__ __device__ inline int padded(int D) { return (D + 3) / 4 * 4; }
+inline size_t gen_smem(int D) { return sizeof(float) * ((size_t)(RB + 2 * TB) * (padded(D) + 4) + TB * kPStride); }
+
+// Vectors [0, n) of D elements (row r at src(r), NULL: zeros) as fp32 in shared
+// memory, row stride ld, zeros up to the padded size and past n up to `rows`.
+template <typename T, typename Src>
+__device__ __forceinline__ void load_rows(float* dst, int ld, int rows, int D, float factor, Src src) {
+  const int Dp = padded(D);
+  constexpr int VE = 16 / sizeof(T);
+  if (D % VE == 0) {
+    const int pieces = D / VE;
+    for (int i = threadIdx.x; i < rows * pieces; i += kGenThreads) {
+      const int r = i / pieces, c = i % pieces;
+      const T* from = src(r);
+      float f[VE];
+      if (from) {
+        const uint4 w = reinterpret_cast<const uint4*>(from)[c];
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < VE; ++j)
+          f[j] = sizeof(T) == 4 ? __uint_as_float(x[j % 4])
+                                : bf16_bits_to_float((uint16_t)(x[j / 2 % 4] >> (16 * (j & 1))));
+      }
+#pragma unroll
+      for (int j = 0; j < VE; ++j) dst[r * ld + c * VE + j] = from ? f[j] * factor : 0.f;
+    }
+  } else {
+    for (int i = threadIdx.x; i < rows * Dp; i += kGenThreads) {
+      const int r = i / Dp, d = i % Dp;
+      const T* from = src(r);
+      float f = 0.f;
+      if (from && d < D) {
+        if constexpr (sizeof(T) == 4)
+          f = from[d];
+        else
+          f = bf16_bits_to_float(from[d]);
+      }
+      dst[r * ld + d] = f * factor;
+    }
+  }
+}
+
+// NC: chunks of 64 dimensions (16 threads x 4)
+template <typename T, int NC>
+__global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
+  extern __shared__ __align__(16) float smem[];
+  const int D = p.head_dim, Dp = padded(D), ld = Dp + 4;
+  float* const sq = smem;
+  float* const sk = sq + RB * ld;
+  float* const sv = sk + TB * ld;
+  float* const sp = sv + TB * ld;
+  const int tid = threadIdx.x, rg = tid / 16, cg = tid % 16;  // rows 4 rg .. 4 rg + 3
+  const int R = p.group * p.nodes;
+  pdl_wait();
+  pdl_launch_dependents();
+  TreeWalk w(p);
+  while (w.next(p)) {
+    const int r0 = w.qg * RB;
+    const T* const q = reinterpret_cast<const T*>(p.q) +
+                       ((size_t)w.b * p.q_heads + (size_t)w.g * p.group) * p.nodes * D;
+    __syncthreads();  // the last segment's tiles are read
+    load_rows<T>(sq, ld, RB, D, p.scale_log2,
+                 [&](int r) { return r0 + r < R ? q + (size_t)(r0 + r) * D : (const T*)nullptr; });
+    int node[4];
+    int low[4];  // lowest prefix token of the row
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      node[r] = (r0 + 4 * rg + r) % p.nodes;
+      low[r] = p.window < 0 ? 0 : tree_low(p, w.row, w.b, node[r]);
+    }
+    float m[4], l[4];
+    float4 o[4][NC];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int tile = w.tile0; tile < w.tile1; ++tile) {
+      const int t0 = w.row.start + tile * TB;
+      __syncthreads();  // the last tile is read
+      auto token = [&](int plane, int j) -> const T* {
+        const int t = t0 + j;
+        if (t >= w.row.len || (p.window >= 0 && t < w.row.prefix - p.window)) return nullptr;
+        const long long at = cache_row(p.cache, plane, w.b, w.g, t);
+        if (at < 0) set_status(p.status, OL_DEVICE_GUARD);
+        return at < 0 ? nullptr : reinterpret_cast<const T*>(p.cache.base) + at * D;
+      };
+      load_rows<T>(sk, ld, TB, D, 1.f, [&](int j) { return token(0, j); });
+      load_rows<T>(sv, ld, TB, D, 1.f, [&](int j) { return token(1, j); });
+      __syncthreads();
+      float s[4][2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.f;
+      for (int d = 0; d < Dp; d += 4) {
+        const float4 k0 = *reinterpret_cast<const float4*>(sk + cg * ld + d);
+        const float4 k1 = *reinterpret_cast<const float4*>(sk + (cg + 16) * ld + d);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float4 a = *reinterpret_cast<const float4*>(sq + (4 * rg + r) * ld + d);
+          s[r][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
+          s[r][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
+        }
+      }
+      const bool edge = p.window >= 0 || t0 + TB > w.row.prefix;  // some row may not see some token
+      if (edge) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (!tree_sees(p, w.row, w.b, node[r], low[r], t0 + cg + 16 * u)) s[r][u] = -INFINITY;
+      }
+      float pr[4][2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float top = fmaxf(s[r][0], s[r][1]);
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float mn = fmaxf(m[r], top);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float keep = m[r] == mn ? 1.f : exp2f(m[r] - base);
+        m[r] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          pr[r][u] = exp2f(s[r][u] - base);
+          sum += pr[r][u];
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        l[r] = l[r] * keep + sum;
+        if (keep != 1.f)
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            o[r][c].x *= keep;
+            o[r][c].y *= keep;
+            o[r][c].z *= keep;
+            o[r][c].w *= keep;
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        *reinterpret_cast<float4*>(sp + (cg + 16 * u) * kPStride + 4 * rg) =
+            make_float4(pr[0][u], pr[1][u], pr[2][u], pr[3][u]);
+      __syncthreads();
+      for (int j = 0; j < TB; ++j) {
+        const float4 p4 = *reinterpret_cast<const float4*>(sp + j * kPStride + 4 * rg);
+        const float pj[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = c * 64 + cg * 4;
+          if (d >= Dp) continue;
+          const float4 v = *reinterpret_cast<const float4*>(sv + j * ld + d);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if (edge && pj[r] == 0.f) continue;  // a hidden token's V may hold infinities or NaN
+            o[r][c].x += pj[r] * v.x;
+            o[r][c].y += pj[r] * v.y;
+            o[r][c].z += pj[r] * v.z;
+            o[r][c].w += pj[r] * v.w;
+          }
+        }
+      }
+    }
+    // the rows that this segment holds alone are done; others go to its slot
+    float* const slot = w.whole() ? nullptr : tree_slot(p, w.slot);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 4 * rg + r;
+      if (r0 + row >= R) continue;
+      if (slot) {
+        if (cg == 0) {
+          slot[row] = m[r];
+          slot[RB + row] = l[r];
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d4 = c * 16 + cg;
+          if (d4 * 4 < Dp) reinterpret_cast<float4*>(slot + 2 * RB)[d4 * RB + row] = o[r][c];
+        }
+      } else if (node[r] < w.row.count) {
+        const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+        const size_t at = tree_out_row(p, w.b, w.g, r0 + row) * D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = c * 64 + cg * 4;
+          const float v[4] = {o[r][c].x, o[r][c].y, o[r][c].z, o[r][c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (d + j < D) store_out(p.out, p.out_dtype, at + d + j, v[j] * inv);
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int NC>
+cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
+  const size_t smem = gen_smem(p.head_dim);
+  static const cudaError_t attr = cudaFuncSetAttribute(
+      tree_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gen_smem(64 * NC));
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(tree_kernel<T, NC>, dim3(p.nctas), dim3(kGenThreads), smem, s, p);
+}
+
+// ------------------------------------------------------------------- the merge
+
+// CTA x merges the unit whose tokens reach from CTA x's share into the next
+// one's (if there is one and it began in share x): rows [32 y, 32 y + 32),
+// lane = row, warps over groups of four dimensions.
+//   M = max m_s, L = sum l_s 2^(m_s - M), y = sum o_s 2^(m_s - M) / L
+constexpr int kMergeThreads = 256;
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  TreeWalk w(p);
+  const int first = blockIdx.x;  // the unit's shares are first .. last
+  int last;
+  if (!w.split_after(p, last)) return;
+  const int RU = p.rows_per_unit, D = p.head_dim;
+  const int row = blockIdx.y * 32 + lane;  // of the unit
+  const int r = w.qg * RU + row;
+  if (row >= RU || r >= p.group * p.nodes || r % p.nodes >= w.row.count) return;
+  // the later shares begin with the unit's segment
+  auto slot_of = [&](int c) { return tree_slot(p, c == first ? w.slot : 2 * c); };
+  float M = -INFINITY;
+  for (int c = first; c <= last; ++c) M = fmaxf(M, __ldcg(slot_of(c) + row));
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  for (int c = first; c <= last; ++c) {
+    const float* const s = slot_of(c);
+    L += __ldcg(s + RU + row) * exp2f(__ldcg(s + row) - base);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t at = tree_out_row(p, w.b, w.g, r) * D;
+  for (int d4 = warp; d4 * 4 < D; d4 += kMergeThreads / 32) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = first; c <= last; ++c) {
+      const float* const s = slot_of(c);
+      const float f = exp2f(__ldcg(s + row) - base);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(s + 2 * RU) + (size_t)d4 * RU + row);
+      acc.x += o.x * f;
+      acc.y += o.y * f;
+      acc.z += o.z * f;
+      acc.w += o.w * f;
+    }
+    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (d4 * 4 + j < D) store_out(p.out, p.out_dtype, at + d4 * 4 + j, v[j]);
+  }
+}
+
+// --------------------------------------------------------------- accepted path
+
+// One CTA per (row, kv head, plane) moves the kept tokens' vectors. kept ascends
+// strictly, so kept[j] >= j and vector j's source is behind every place written
+// before it: a pass reads its vectors, waits for the CTA, then writes them.
+constexpr int kKeepThreads = 256;
+constexpr int kKeepUnroll = 4;
+
+template <typename P>  // the piece that a thread moves
+__global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const KeepParams p, int pieces) {
+  const CacheRef& c = p.cache;
+  const int g = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads, plane = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int start = p.starts[b], n = p.counts[b];
+  const int32_t* const kept = p.kept + (size_t)b * p.nodes;
+  bool bad = n < 0 || n > p.nodes || start < 0 || (long long)start + p.nodes > c.capacity;
+  if (!bad)
+    for (int j = threadIdx.x; j < n; j += kKeepThreads) {
+      const int k = kept[j];
+      bad |= k < 0 || k >= p.nodes || (j > 0 && kept[j - 1] >= k) || cache_row(c, 0, b, g, start + k) < 0 ||
+             cache_row(c, 0, b, g, start + j) < 0;
+    }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(p.status, OL_DEVICE_GUARD);
+    return;
+  }
+  P* const base = reinterpret_cast<P*>(c.base);
+  const int total = n * pieces;
+  for (int i0 = 0; i0 < total; i0 += kKeepThreads * kKeepUnroll) {
+    P v[kKeepUnroll];
+#pragma unroll
+    for (int u = 0; u < kKeepUnroll; ++u) {
+      const int i = i0 + u * kKeepThreads + threadIdx.x;
+      if (i < total) v[u] = base[cache_row(c, plane, b, g, start + kept[i / pieces]) * pieces + i % pieces];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kKeepUnroll; ++u) {
+      const int i = i0 + u * kKeepThreads + threadIdx.x;
+      if (i < total) base[cache_row(c, plane, b, g, start + i / pieces) * pieces + i % pieces] = v[u];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_generic_tree(TreeParams& p, int sms, cudaStream_t s) {
+  p.rows_per_unit = RB;
+  p.units_per_head = (p.group * p.nodes + RB - 1) / RB;
+  p.tile = TB;
+  p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
+  const int nc = (p.head_dim + 63) / 64;
+  if (p.dtype == OL_F32)
+    return nc == 1 ? launch_tree<float, 1>(p, s)
+           : nc == 2 ? launch_tree<float, 2>(p, s)
+           : nc == 3 ? launch_tree<float, 3>(p, s)
+                     : launch_tree<float, 4>(p, s);
+  return nc == 1 ? launch_tree<uint16_t, 1>(p, s)
+         : nc == 2 ? launch_tree<uint16_t, 2>(p, s)
+         : nc == 3 ? launch_tree<uint16_t, 3>(p, s)
+                   : launch_tree<uint16_t, 4>(p, s);
+}
+
+cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
+  const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
+  return launch_pdl(tree_merge_kernel, dim3(p.nctas, (rows + 31) / 32), dim3(kMergeThreads), 0, s, p);
+}
+
+cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {
+  const size_t bytes = (size_t)p.head_dim * (p.dtype == OL_F32 ? 4 : 2);
+  const dim3 grid(p.cache.batch * p.cache.kv_heads, 2);
+  if (bytes % 16 == 0) return launch_pdl(tree_keep_kernel<uint4>, grid, dim3(kKeepThreads), 0, s, p, (int)(bytes / 16));
+  return launch_pdl(tree_keep_kernel<uint16_t>, grid, dim3(kKeepThreads), 0, s, p, (int)(bytes / 2));
+}
+
+}  // namespace ol

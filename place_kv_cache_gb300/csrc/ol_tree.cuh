@@ -1,0 +1,193 @@
+// ol_tree.cuh -- device helpers of the tree kernels: the walk over a CTA's
+// share of the work, visibility, addresses of cache rows, outputs and slots.
+#pragma once
+
+#include "ol_common.cuh"
+#include "ol_draft.h"
+
+namespace ol {
+
+// Row index (in head_dim elements) of token t in a cache plane; -1 where the
+// block table names no page of the pool.
+__device__ __forceinline__ long long cache_row(const CacheRef& c, int plane, int b, int g, int t) {
+  if (!c.block_table) return (((long long)plane * c.batch + b) * c.kv_heads + g) * c.capacity + t;
+  const int page = c.block_table[(size_t)b * c.max_pages + t / c.page_size];
+  if (page < 0 || page >= c.num_pages) return -1;
+  return (((long long)plane * c.num_pages + page) * c.kv_heads + g) * c.page_size + t % c.page_size;
+}
+
+// Row of q and out of the (head, node) row r of kv head g.
+__device__ __forceinline__ size_t tree_out_row(const TreeParams& p, int b, int g, int r) {
+  return ((size_t)b * p.q_heads + (size_t)g * p.group) * p.nodes + r;
+}
+
+__device__ __forceinline__ float* tree_slot(const TreeParams& p, int slot) {
+  return p.partials + slot * tree_slot_floats(p.rows_per_unit, p.head_dim);
+}
+
+// Position of a node: no lower than its row's prefix length.
+__device__ __forceinline__ int tree_position(const TreeParams& p, const TreeRow& row, int b, int node) {
+  if (!p.node_pos) return row.prefix + node;
+  return max(row.prefix, p.node_pos[(size_t)b * p.nodes + node]);
+}
+
+// Lowest prefix token that a node sees (with a window).
+__device__ __forceinline__ int tree_low(const TreeParams& p, const TreeRow& row, int b, int node) {
+  const int at = tree_position(p, row, b, node);
+  return at <= p.window ? 0 : at - p.window;
+}
+
+// Whether a node sees drafted token j (j < count).
+__device__ __forceinline__ bool tree_sees_drafted(const TreeParams& p, const TreeRow& row, int b, int node, int j) {
+  if (p.mask) {
+    const uint64_t w = p.mask[((size_t)b * p.nodes + node) * p.words + j / 64];
+    if (!(w >> (j % 64) & 1)) return false;
+  } else if (j > node) {
+    return false;
+  }
+  return p.window < 0 ||
+         (long long)tree_position(p, row, b, node) - tree_position(p, row, b, j) <= p.window;
+}
+
+__device__ __forceinline__ bool tree_sees(const TreeParams& p, const TreeRow& row, int b, int node, int low, int t) {
+  if (t >= row.len) return false;
+  return t < row.prefix ? t >= low : tree_sees_drafted(p, row, b, node, t - row.prefix);
+}
+
+__device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
+  int n = p.lens[b], c = p.counts ? p.counts[b] : p.nodes;
+  if (n < 0 || n > p.cache.capacity) {
+    set_status(p.status, OL_DEVICE_GUARD);
+    n = n < 0 ? 0 : p.cache.capacity;
+  }
+  if (c < 0 || c > p.nodes || c > n) {
+    set_status(p.status, OL_DEVICE_GUARD);
+    c = c < 0 ? 0 : min(min(c, p.nodes), n);
+  }
+  return tree_row(n, c, p.window, p.tile);
+}
+
+// The tiles of all units, in the order (row, kv head, row group of the unit,
+// tile), are cut into n = min(CTAs, T) contiguous shares of equal size, none of
+// them empty: CTA c has tiles [c T / n, (c + 1) T / n). A walk gives the CTA its share's segments,
+// one unit's tiles [tile0, tile1) each. A segment that is not its whole unit
+// puts its state into a slot; a share has at most two of them, its first and
+// its last segment: slot 2 c for the one that starts the share, else 2 c + 1.
+// Equal shares keep ragged batches balanced to one tile per SM.
+// The constructor is for whole warps; next() may be called by single threads.
+struct TreeWalk {
+  int b, g, qg;
+  TreeRow row;
+  int tile0, tile1;
+  int slot;
+  long long at, end;       // next tile of the share; its end
+  long long share, total;  // its first tile; all tiles
+  long long shares;
+
+  __device__ __forceinline__ explicit TreeWalk(const TreeParams& p) {
+    const int lane = threadIdx.x & 31;
+    total = 0;
+    for (int base = 0; base < p.batch; base += 32) {
+      int nt = base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
+      total += nt;
+    }
+    total *= p.kv_heads * p.units_per_head;
+    shares = total < gridDim.x ? total : gridDim.x;
+    at = share = end = 0;
+    if (blockIdx.x < shares) {
+      at = share = blockIdx.x * total / shares;
+      end = (blockIdx.x + 1) * total / shares;
+    }
+    tile0 = slot = 0;
+    tile1 = at < end ? locate(p, at) : 0;
+  }
+
+  // Finds the unit of tile x (x < total); returns the tile's index in it.
+  __device__ __forceinline__ int locate(const TreeParams& p, long long x) {
+    const int lane = threadIdx.x & 31;
+    const int per_row = p.kv_heads * p.units_per_head;
+    b = g = qg = 0;
+    row = TreeRow{0, 0, 0, 0, 1};
+    for (int base = 0; base < p.batch; base += 32) {
+      const int nt = base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
+      int incl = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const long long all = (long long)__shfl_sync(0xffffffffu, incl, 31) * per_row;
+      if (x < all) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, x < (long long)incl * per_row)) - 1;
+        x -= (long long)__shfl_sync(0xffffffffu, incl - nt, src) * per_row;
+        b = base + src;
+        row = read_tree_row(p, b);
+        const int unit = (int)(x / row.ntiles);
+        g = unit / p.units_per_head;
+        qg = unit % p.units_per_head;
+        return (int)(x % row.ntiles);
+      }
+      x -= all;
+    }
+    return 0;
+  }
+
+  // Moves to the share's next segment.
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    if (at >= end) return false;
+    if (tile1 == row.ntiles) {  // the unit is done: the next one
+      tile1 = 0;
+      if (++qg == p.units_per_head) {
+        qg = 0;
+        if (++g == p.kv_heads) {
+          g = 0;
+          do {
+            if (++b >= p.batch) return false;
+            row = read_tree_row(p, b);
+          } while (row.ntiles == 0);
+        }
+      }
+    }
+    tile0 = tile1;
+    slot = 2 * blockIdx.x + (at == share ? 0 : 1);
+    const long long left = end - at;
+    tile1 = left < row.ntiles - tile0 ? tile0 + (int)left : row.ntiles;
+    at += tile1 - tile0;
+    return true;
+  }
+
+  __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == row.ntiles; }
+
+  // For the merge: whether a unit begins in this share and reaches past its
+  // end. It is found, `slot` is that of its first segment and `last` its last share.
+  __device__ __forceinline__ bool split_after(const TreeParams& p, int& last) {
+    if (at >= end || end == total) return false;
+    const long long begin = end - 1 - locate(p, end - 1), unit_end = begin + row.ntiles;
+    if (begin < share || unit_end == end) return false;
+    slot = 2 * blockIdx.x + (begin == share ? 0 : 1);
+    last = (int)((unit_end * shares - 1) / total);
+    return true;
+  }
+};
+
+// A launch that may begin while the kernel ahead of it in the stream drains;
+// the kernels wait for it (griddepcontrol.wait) before they touch memory.
+template <typename... Args>
+inline cudaError_t launch_pdl(void (*kernel)(Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace ol

@@ -1,0 +1,467 @@
+"""GPU parity of tree attention (ol_tree_attention) and of the accepted path's
+move (ol_tree_keep) against a plain 64-bit form: contiguous and paged caches,
+bf16 and fp32, head sizes and groups on both kernels, one to 512 nodes, rows
+without prefix, without nodes, with hidden nodes, ragged counts, windows,
+infinities and NaN in what is hidden, poison in every slot past a row, replayed
+and concurrent calls, lengths and pages that disagree on the device."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import place_kv_cache_gb300 as ol
+from tests import draft_util as du
+from tests.gpu_util import DEV, canaries_intact, guarded
+
+pytestmark = pytest.mark.gpu
+CODE = {torch.float32: ol.OL_F32, torch.bfloat16: ol.OL_BF16}
+TORCH = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+class Tree:
+    """A cache of poisoned slots with the rows' tokens in place, q, trees and the call on them."""
+
+    def __init__(self, dt, layout, B, Hq, H, D, page, nodes, lens, counts=None, window=-1, mask="tree", out=None,
+                 seed=1, spare=3, positions=True):
+        self.dtype, self.B, self.Hq, self.H, self.D, self.nodes, self.window = TORCH[dt], B, Hq, H, D, nodes, window
+        self.rng = np.random.default_rng(seed)
+        self.gen = torch.Generator(device=DEV).manual_seed(seed)
+        self.lens = np.array(lens, np.int32)
+        self.counts = np.full(B, nodes, np.int32) if counts is None else np.array(counts, np.int32)
+        self.ragged = counts is not None
+        self.out_dtype = TORCH[out or dt]
+        C = max(int(self.lens.max()), 1) + spare
+        self.layout, self.page, self.table = layout, page, None
+        if layout == "contiguous":
+            shape = (2, B, H, C, D)
+        else:
+            M = -(-C // page)
+            self.table = self.rng.permutation(B * M + 2)[: B * M].astype(np.int32).reshape(B, M)
+            shape = (2, B * M + 2, H, page, D)
+        self.cache = torch.full(shape, float("nan"), device=DEV, dtype=self.dtype)
+        for b in range(B):
+            n = int(self.lens[b])
+            for plane in (0, 1):
+                self.put(plane, b, torch.randn((H, n, D), generator=self.gen, device=DEV, dtype=self.dtype))
+        self.q = torch.randn((B, Hq, nodes, D), generator=self.gen, device=DEV, dtype=self.dtype)
+        if mask == "tree":
+            self.sees, depth = du.random_trees(self.rng, B, nodes)
+        elif mask == "random":  # any bits: rows that see nothing drafted, later tokens, not themselves
+            self.sees, depth = self.rng.random((B, nodes, nodes)) < 0.3, self.rng.integers(0, 9, (B, nodes))
+        elif mask == "empty":
+            self.sees, depth = np.zeros((B, nodes, nodes), bool), np.zeros((B, nodes), np.int64)
+        else:
+            self.sees, depth = None, np.broadcast_to(np.arange(nodes), (B, nodes))
+        self.at = ((self.lens - self.counts)[:, None] + depth).astype(np.int32) if positions else None
+        self.mask = None if self.sees is None else torch.from_numpy(du.pack_mask(self.sees)).to(DEV)
+        self.at_d = None if self.at is None else torch.from_numpy(self.at).to(DEV)
+        self.lens_d, self.counts_d = torch.from_numpy(self.lens).to(DEV), torch.from_numpy(self.counts).to(DEV)
+        if layout == "contiguous":
+            self.code, self.desc = ol.OL_LAYOUT_CONTIGUOUS, ol.kv_cache(self.cache, access=ol.OL_READ_ONLY)
+        else:
+            self.table_d = torch.from_numpy(self.table).to(DEV)
+            self.code = ol.OL_LAYOUT_PAGED
+            self.desc = ol.paged_kv(self.cache, self.table_d, self.table, access=ol.OL_READ_ONLY)
+        self.ws_bytes = ol.ol_workspace_size_tree(B, Hq, H, D, nodes)
+        self.ws_buf, self.ws = guarded(self.ws_bytes)
+        ol.ol_workspace_init(self.ws, self.ws_bytes)
+        self.out_buf, payload = guarded(B * Hq * nodes * D * (4 if self.out_dtype == torch.float32 else 2))
+        self.out = payload.view(self.out_dtype).view(B, Hq, nodes, D)
+        self.out.fill_(-77.0)
+
+    def row(self, plane, b, n):
+        if self.table is None:
+            return self.cache[plane, b, :, :n]
+        pages = [self.cache[plane, p] for p in self.table[b, : -(-n // self.page)].tolist()]
+        return torch.cat(pages, 1)[:, :n] if pages else self.cache[plane, 0, :, :0]
+
+    def put(self, plane, b, x, first=0):
+        for t0 in range(0, x.shape[1], self.page or x.shape[1] or 1):
+            part = x[:, t0: t0 + self.page] if self.page else x
+            if self.page:
+                assert first % self.page == 0
+                self.cache[plane, int(self.table[b, (first + t0) // self.page]), :, : part.shape[1]] = part
+            else:
+                self.cache[plane, b, :, first: first + part.shape[1]] = part
+
+    def token(self, plane, b, t):
+        """View [Hkv, D] of one cached token."""
+        return self.cache[plane, b, :, t] if self.table is None else \
+            self.cache[plane, int(self.table[b, t // self.page]), :, t % self.page]
+
+    def call(self, stream=None, scale=0.0):
+        ol.ol_tree_attention(self.code, self.desc, self.q, self.Hq, self.nodes, self.lens, self.lens_d,
+                             self.counts if self.ragged else None, self.counts_d if self.ragged else None, self.mask,
+                             self.at_d, scale, self.window, self.out, CODE[self.out_dtype], self.ws, self.ws_bytes,
+                             stream=stream)
+
+    def check(self, scale=None, lens=None, counts=None, status=ol.OL_DEVICE_OK):
+        torch.cuda.synchronize()
+        assert ol.ol_workspace_status(self.ws) == status
+        scale = 1 / math.sqrt(self.D) if scale is None else scale
+        lens, counts = self.lens if lens is None else lens, self.counts if counts is None else counts
+        G = self.Hq // self.H
+        for b in range(self.B):
+            n, t = int(lens[b]), int(counts[b])
+            assert bool((self.out[b, :, t:] == -77.0).all()), "an output past the row's count was written"
+            if t == 0:
+                continue
+            ok = du.visible(n, t, None if self.sees is None else self.sees[b],
+                            None if self.at is None else self.at[b], self.window)
+            k, v = self.row(0, b, n), self.row(1, b, n)
+            for g in range(self.H):
+                q = self.q[b, g * G: (g + 1) * G, :t]
+                want, pv, rms, size = du.tree_attention(q, k[g], v[g], ok, scale)
+                got = self.out[b, g * G: (g + 1) * G, :t].double()
+                weights = self.dtype == torch.bfloat16
+                tol = du.tree_tolerance(want, pv, size, self.D, n, self.out_dtype, weights)
+                fine = torch.isfinite(want)
+                assert torch.equal(torch.isnan(got), torch.isnan(want))
+                assert torch.equal(got[~fine & ~torch.isnan(want)], want[~fine & ~torch.isnan(want)])
+                off = ((got - want).abs() - tol)[fine]
+                assert not off.numel() or float(off.max()) <= 0, \
+                    f"row {b} head {g}: {float(off.max()):.3e} more than the bound"
+                if weights and bool(fine.all()):
+                    # roundings of the weights are independent: their root mean square is at most 2^-8 / sqrt(3) of
+                    # sqrt(sum p^2 v^2), the output's 2^-8 / sqrt(3) of itself; 2 covers the spread of a finite sample
+                    # (and the fp32 part is added whole)
+                    step = torch.finfo(self.out_dtype).eps / 2
+                    rest = du.tree_tolerance(want, pv, size, self.D, n, torch.float64, False)
+                    bound = 2 * ((2.0 ** -8 / 3 ** 0.5 * rms).norm() + (step / 3 ** 0.5 * want).norm()) + rest.norm()
+                    assert float((got - want).norm()) <= float(bound)
+        assert canaries_intact(self.out_buf) and canaries_intact(self.ws_buf)
+
+
+CASES = [
+    # dt, layout, B, Hq, Hkv, D, page, nodes, lens, counts, window, mask, out
+    # --- bf16, the tensor-core kernel's head sizes
+    ("bf16", "contiguous", 1, 1, 1, 128, 0, 1, [1]),
+    ("bf16", "contiguous", 1, 28, 4, 128, 0, 8, [4097 + 8]),
+    ("bf16", "contiguous", 3, 32, 8, 128, 0, 16, [16, 17, 700]),
+    ("bf16", "contiguous", 2, 8, 8, 128, 0, 5, [127, 130]),
+    ("bf16", "contiguous", 2, 16, 2, 64, 0, 63, [64, 513]),
+    ("bf16", "contiguous", 2, 32, 8, 128, 0, 64, [300, 64]),
+    ("bf16", "contiguous", 2, 14, 2, 128, 0, 65, [65, 400]),
+    ("bf16", "contiguous", 1, 16, 1, 64, 0, 200, [1111]),
+    ("bf16", "contiguous", 1, 4, 2, 128, 0, 512, [512 + 77]),
+    ("bf16", "contiguous", 5, 12, 4, 128, 0, 7, [7, 128, 129, 255, 1000], [7, 0, 1, 3, 6]),
+    ("bf16", "contiguous", 3, 8, 2, 128, 0, 9, [0, 9, 5], [0, 9, 5]),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 12, [12, 600], None, -1, "random"),
+    ("bf16", "contiguous", 3, 8, 2, 128, 0, 6, [6, 128, 600], None, -1, "empty"),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 33, [33, 600], None, -1, "chain"),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 10, [500, 60], None, 0, "tree"),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 10, [500, 600], None, 3, "tree"),
+    ("bf16", "contiguous", 3, 8, 2, 64, 0, 10, [500, 200, 10], [10, 2, 9], 150, "random"),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 40, [500, 60], None, 20, "chain"),
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 4, [300, 60], None, -1, "tree", "f32"),
+    ("bf16", "paged", 3, 32, 8, 128, 16, 16, [16, 100, 1000]),
+    ("bf16", "paged", 2, 28, 4, 128, 64, 256, [256, 900]),
+    ("bf16", "paged", 3, 8, 2, 128, 48, 7, [7, 130, 500], [3, 7, 0]),
+    ("bf16", "paged", 2, 8, 2, 64, 128, 20, [333, 20]),
+    ("bf16", "paged", 2, 8, 2, 128, 256, 20, [600, 20]),
+    ("bf16", "paged", 2, 8, 2, 128, 16, 10, [500, 300], None, 100, "tree"),
+    ("bf16", "paged", 40, 8, 2, 128, 16, 3, list(range(3, 203, 5))),
+    ("bf16", "contiguous", 170, 4, 4, 64, 0, 2, [2 + (7 * i) % 300 for i in range(170)]),
+    # --- CUDA cores
+    ("bf16", "paged", 2, 8, 2, 128, 8, 10, [100, 33]),
+    ("bf16", "paged", 2, 8, 2, 128, 7, 10, [100, 33]),
+    ("bf16", "contiguous", 2, 6, 2, 96, 0, 11, [100, 11]),
+    ("bf16", "contiguous", 1, 6, 2, 256, 0, 11, [257]),
+    ("bf16", "contiguous", 1, 3, 1, 20, 0, 4, [77]),
+    ("f32", "contiguous", 1, 1, 1, 4, 0, 1, [1]),
+    ("f32", "contiguous", 2, 6, 3, 5, 0, 3, [40, 3]),
+    ("f32", "contiguous", 3, 28, 4, 128, 0, 8, [8, 500, 1500], [8, 3, 0]),
+    ("f32", "paged", 2, 16, 2, 80, 16, 33, [400, 33], None, -1, "random"),
+    ("f32", "paged", 2, 16, 2, 64, 5, 40, [400, 40], None, 50, "tree", "bf16"),
+    ("f32", "contiguous", 2, 4, 1, 256, 0, 70, [200, 70], None, 10, "chain"),
+    ("f32", "contiguous", 2, 4, 1, 192, 0, 6, [200, 6], None, -1, "empty"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c[:8]) + ("" if len(c) < 11 else
+                                                                                       f"-w{c[10]}-{c[11]}"))
+def test_tree_attention(case):
+    t = Tree(*case)
+    t.call()
+    t.check()
+
+
+def test_tree_attention_explicit_scale_and_no_positions():
+    t = Tree("bf16", "contiguous", 2, 8, 2, 128, 0, 9, [200, 100], positions=False)
+    t.call(scale=0.25)
+    t.check(scale=0.25)
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("bf16", 64), ("bf16", 96), ("f32", 128)])
+def test_hidden_infinities_and_nan(dt, D):
+    """K and V of a drafted token that some nodes see and others do not: only those that see it are touched."""
+    t = Tree(dt, "paged", 2, 8, 2, D, 16, 12, [150, 60], seed=9)
+    for b in range(2):
+        first = int(t.lens[b]) - 12
+        t.sees[b, :, 4:9] = False
+        t.sees[b, 3, 4], t.sees[b, 5, 5], t.sees[b, 7, 6], t.sees[b, 8, 7] = True, True, True, True
+        t.token(1, b, first + 4)[:, 3] = float("inf")
+        t.token(1, b, first + 5)[:, D - 1] = float("nan")
+        t.token(1, b, first + 6)[:] = -float("inf")
+        t.token(1, b, first + 7)[:, 0] = float("inf")
+        t.token(0, b, first + 8)[:] = float("nan")      # seen by none
+        t.token(1, b, first + 8)[:] = float("nan")
+    t.mask = torch.from_numpy(du.pack_mask(t.sees)).to(DEV)
+    t.call()
+    t.check()
+    assert not torch.isfinite(t.out[:, :, 3, 3]).any() and torch.isfinite(t.out[:, :, 0]).all()
+
+
+def test_large_scores_and_equal_scores():
+    t = Tree("bf16", "contiguous", 1, 4, 1, 128, 0, 6, [900], seed=4)
+    t.q.mul_(16)                                     # weights concentrate: the running maximum moves often
+    t.cache[0, :, :, :300].mul_(0.1)
+    t.call()
+    t.check()
+    t.q.zero_()                                      # a plain mean
+    t.out.fill_(-77.0)
+    t.call()
+    t.check()
+
+
+def test_one_long_row_past_32_bit_offsets():
+    """The last tokens of a cache of more than 2^31 elements."""
+    H, D, C = 4, 128, 2200000                        # 2 * 4 * 2.2e6 * 128 = 2.25e9 elements
+    cache = torch.zeros((2, 1, H, C, D), device=DEV, dtype=torch.bfloat16)
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    n, nodes, window = C - 1, 5, 700
+    live = window + nodes + 300
+    for plane in (0, 1):
+        cache[plane, 0, :, n - live: n] = torch.randn((H, live, D), generator=gen, device=DEV, dtype=torch.bfloat16)
+    q = torch.randn((1, 8, nodes, D), generator=gen, device=DEV, dtype=torch.bfloat16)
+    out = torch.empty_like(q)
+    lens = np.array([n], np.int32)
+    size = ol.ol_workspace_size_tree(1, 8, H, D, nodes)
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    ol.ol_tree_attention(ol.OL_LAYOUT_CONTIGUOUS, ol.kv_cache(cache), q, 8, nodes, lens, torch.from_numpy(lens).to(DEV),
+                         None, None, None, None, 0.0, window, out, ol.OL_BF16, ws, size)
+    ok = du.visible(live, nodes, None, None, window)
+    for g in range(H):
+        k, v = cache[0, 0, g, n - live: n], cache[1, 0, g, n - live: n]
+        want, pv, _, s = du.tree_attention(q[0, 2 * g: 2 * g + 2], k, v, ok, D ** -0.5)
+        tol = du.tree_tolerance(want, pv, s, D, live, torch.bfloat16, True)
+        assert bool(((out[0, 2 * g: 2 * g + 2].double() - want).abs() <= tol).all())
+    assert ol.ol_workspace_status(ws) == ol.OL_DEVICE_OK
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_replays_follow_the_device_lengths(dt):
+    """A captured call replays with the lengths, counts and masks on the device; two captured calls with workspaces
+    of their own run side by side."""
+    trees = [Tree(dt, layout, 3, 8, 2, 128, page, 10, [500, 77, 300], [10, 3, 0], seed=s)
+             for layout, page, s in (("contiguous", 0, 5), ("paged", 16, 6))]
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for t, s in zip(trees, streams):
+        s.wait_stream(torch.cuda.current_stream())
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            t.call()
+        graphs.append(g)
+    for lens, counts in (([500, 77, 300], [10, 3, 0]), ([20, 60, 299], [0, 10, 9]), ([0, 1, 500 - 7], [0, 1, 4])):
+        lens, counts = np.array(lens, np.int32), np.array(counts, np.int32)
+        for t in trees:
+            t.lens, t.counts = lens, counts
+            for b in range(3):  # rows that grow keep finite tokens: fill what is new
+                for plane in (0, 1):
+                    x = t.row(plane, b, int(lens[b]))
+                    t.put(plane, b, torch.where(torch.isnan(x), torch.ones_like(x), x))
+            t.lens_d.copy_(torch.from_numpy(lens))
+            t.counts_d.copy_(torch.from_numpy(counts))
+            t.at = ((lens - counts)[:, None] + np.arange(10)).astype(np.int32)
+            t.at_d.copy_(torch.from_numpy(t.at))
+            t.out.fill_(-77.0)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for t in trees:
+            t.check()
+
+
+def test_calls_in_a_row_share_a_workspace_and_repeat_bits():
+    t = Tree("bf16", "contiguous", 2, 28, 4, 128, 0, 16, [3000, 400])
+    t.call()
+    torch.cuda.synchronize()
+    first = t.out.clone()
+    u = Tree("bf16", "contiguous", 1, 28, 4, 128, 0, 16, [2000], seed=8)
+    u.ws, u.ws_bytes, u.ws_buf = t.ws, t.ws_bytes, t.ws_buf
+    for _ in range(5):
+        u.call()
+        t.call()
+    t.check()
+    u.check()
+    assert torch.equal(first, t.out)
+
+
+def test_device_lengths_and_pages_that_disagree_are_recorded():
+    t = Tree("bf16", "paged", 2, 8, 2, 128, 16, 4, [100, 50], [4, 4])
+    t.lens_d.copy_(torch.tensor([100000, -5], dtype=torch.int32))  # clamped to the capacity, and to nothing
+    t.counts_d.copy_(torch.tensor([4, 4], dtype=torch.int32))
+    t.call()
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_GUARD
+    assert bool((t.out[1] == -77.0).all()) and canaries_intact(t.out_buf)
+    t = Tree("bf16", "paged", 2, 8, 2, 128, 16, 4, [100, 50])
+    t.table_d[0, 2] = 10 ** 6
+    t.call()
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_GUARD
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+
+
+# ------------------------------------------------------------- the accepted path
+
+KEEPS = [
+    # dt, layout, B, Hkv, D, page, nodes, capacity, starts, kept
+    ("bf16", "contiguous", 3, 4, 128, 0, 8, 40, [0, 32, 9], [[0, 2, 5], [], [7]]),
+    ("bf16", "paged", 3, 8, 128, 16, 16, 64, [15, 48, 0], [[0, 1, 2, 9, 15], list(range(16)), [3, 4]]),
+    ("f32", "paged", 2, 2, 80, 5, 11, 40, [3, 29], [[1, 3, 5, 7, 9, 10], [10]]),
+    ("bf16", "contiguous", 1, 1, 5, 0, 3, 5, [2], [[0, 2]]),
+    ("f32", "contiguous", 2, 2, 256, 0, 512, 600, [88, 0], [list(range(1, 512, 2)), list(range(200, 512))]),
+    ("bf16", "contiguous", 1, 2, 64, 0, 1, 4, [3], [[0]]),
+]
+
+
+@pytest.mark.parametrize("case", KEEPS, ids=lambda c: "-".join(map(str, c[:8])))
+def test_tree_keep(case):
+    dt, layout, B, H, D, page, nodes, C, starts, kept = case
+    t = Tree(dt, layout, B, H, H, D, page, 1, [C] * B, spare=0)
+    before = t.cache.clone()
+    want = t.cache.clone()
+    desc = ol.kv_cache(t.cache) if layout == "contiguous" else ol.paged_kv(t.cache, t.table_d, t.table)
+    lists = np.full((B, nodes), -9, np.int32)  # past a row's count: not read
+    for b in range(B):
+        lists[b, : len(kept[b])] = kept[b]
+    starts_h = np.array(starts, np.int32)
+    args = (t.code, desc, t.cache, nodes, starts_h, torch.from_numpy(starts_h).to(DEV),
+            torch.from_numpy(lists).to(DEV), torch.tensor([len(k) for k in kept], dtype=torch.int32, device=DEV), t.ws)
+    ol.ol_tree_keep(*args)
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+    got, t.cache = t.cache, before
+    for plane in (0, 1):
+        for b in range(B):
+            for j, k in enumerate(kept[b]):
+                src = t.token(plane, b, starts[b] + k)
+                at = (plane, b, slice(None), starts[b] + j) if t.table is None else \
+                    (plane, int(t.table[b, (starts[b] + j) // page]), slice(None), (starts[b] + j) % page)
+                want[at] = src
+    bits = torch.int32 if dt == "f32" else torch.int16
+    assert torch.equal(got.view(bits), want.view(bits))
+
+
+@pytest.mark.parametrize("kept,count", [([0, 2, 2, 3], 4), ([0, 3, 1, 2], 3), ([0, 1, 2, 4], 4), ([-1, 1, 2, 3], 2),
+                                        ([0, 1, 2, 3], 5), ([0, 1, 2, 3], -1)])
+def test_tree_keep_leaves_a_row_whose_list_is_wrong(kept, count):
+    t = Tree("bf16", "contiguous", 2, 2, 2, 64, 0, 1, [20, 20], spare=0)
+    before = t.cache.clone()
+    starts = np.array([3, 5], np.int32)
+    lists = torch.tensor([kept, [1, 2, 0, 0]], dtype=torch.int32, device=DEV)
+    ol.ol_tree_keep(t.code, ol.kv_cache(t.cache), t.cache, 4, starts, torch.from_numpy(starts).to(DEV), lists,
+                    torch.tensor([count, 2], dtype=torch.int32, device=DEV), t.ws)
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_GUARD
+    before[:, 1, :, 5:7] = before[:, 1, :, 6:8].clone()
+    assert torch.equal(t.cache, before)
+
+
+# --------------------------------------------------------------- all of it together
+
+@pytest.mark.parametrize("layout,page", [("contiguous", 0), ("paged", 16)])
+def test_speculative_steps_give_the_plain_decode(layout, page):
+    """Two rows: prompts appended with rotation, then rounds of drafted trees (append, attend, keep a path). Every
+    node's output equals that of a plain decode of its path, and after the rounds ol_decode_attention over the cache
+    equals the plain form over the accepted tokens."""
+    B, Hq, H, D, T, G = 2, 8, 2, 128, 9, 4
+    rng = np.random.default_rng(41)
+    gen = torch.Generator(device=DEV).manual_seed(42)
+    t = Tree("bf16", layout, B, Hq, H, D, page, T, [150, 150], seed=43)  # buffers; the tokens are replaced
+    t.cache.fill_(float("nan"))
+    desc = ol.kv_cache(t.cache) if layout == "contiguous" else ol.paged_kv(t.cache, t.table_d, t.table)
+    freq = du.frequencies(D)
+    rope = ol.rope(D, device=DEV)
+    k_ref = [torch.zeros((H, 0, D), device=DEV, dtype=torch.float64) for _ in range(B)]  # rotated in 64 bits
+    v_ref = [torch.zeros((H, 0, D), device=DEV, dtype=torch.float64) for _ in range(B)]
+
+    def project(n):
+        return torch.randn((B, n, Hq + 2 * H, D), generator=gen, device=DEV, dtype=torch.bfloat16).transpose(1, 2) \
+            .split((Hq, H, H), dim=1)
+
+    prompt = np.array([70, 33], np.int32)
+    q, k, v = project(70)
+    zero = np.zeros(B, np.int32)
+    ol.ol_rope_append(t.code, desc, t.cache, rope, 70, k, v, 0, None, None, zero, torch.from_numpy(zero).to(DEV), prompt,
+                      torch.from_numpy(prompt).to(DEV))
+    for b in range(B):
+        n = int(prompt[b])
+        k_ref[b] = du.rotate(k[b, :, :n], torch.arange(n, device=DEV), freq, du.HALF)[0]
+        v_ref[b] = v[b, :, :n].double()
+    length = prompt.copy()
+    for round_ in range(3):
+        q, k, v = project(T)
+        sees, depth = du.random_trees(rng, B, T)
+        counts = np.array([T, T - 1 - round_], np.int32)
+        counts_d = torch.from_numpy(counts).to(DEV)
+        angles = torch.from_numpy((length[:, None] + depth).astype(np.int32)).to(DEV)
+        q_rot = torch.zeros((B, Hq, T, D), device=DEV, dtype=torch.bfloat16)
+        start_d = torch.from_numpy(length).to(DEV)
+        ol.ol_rope_append(t.code, desc, t.cache, rope, T, k, v, Hq, q, q_rot, length, start_d, counts, counts_d, angles)
+        lens = length + counts
+        out = torch.zeros_like(q_rot)
+        ol.ol_tree_attention(t.code, desc, q_rot, Hq, T, lens, torch.from_numpy(lens).to(DEV), counts, counts_d,
+                             torch.from_numpy(du.pack_mask(sees)).to(DEV), angles, 0.0, -1, out, ol.OL_BF16, t.ws,
+                             t.ws_bytes)
+        kept = np.zeros((B, T), np.int32)
+        n_kept = np.zeros(B, np.int32)
+        for b in range(B):
+            n = int(counts[b])
+            at = torch.from_numpy(length[b] + depth[b, :n]).to(DEV)
+            kr = du.rotate(k[b, :, :n], at, freq, du.HALF)[0]
+            qr = du.rotate(q[b, :, :n], at, freq, du.HALF)[0]
+            path = np.nonzero(sees[b, n - 1])[0]  # the last node's ancestors and itself
+            for i in range(n):
+                mine = torch.from_numpy(np.nonzero(sees[b, i])[0]).to(DEV)
+                for g in range(H):
+                    kk = torch.cat((k_ref[b][g], kr[g][mine]))
+                    vv = torch.cat((v_ref[b][g], v[b, g].double()[mine]))
+                    ok = np.ones((1, len(kk)), bool)
+                    want = du.tree_attention(qr[g * G: (g + 1) * G, i: i + 1], kk, vv, ok, D ** -0.5)[0]
+                    # q and K are rounded to bf16 after the rotation, which the plain form is not: two roundings of
+                    # 2^-8 of each product, independent over D of them (a score moves by about 2^-8 of its spread, 1)
+                    assert float((out[b, g * G: (g + 1) * G, i: i + 1].double() - want).abs().max()) < 0.05
+            kept[b, : len(path)], n_kept[b] = path, len(path)
+            pick = torch.from_numpy(path).to(DEV)
+            k_ref[b] = torch.cat((k_ref[b], kr[:, pick]), 1)
+            v_ref[b] = torch.cat((v_ref[b], v[b].double()[:, pick]), 1)
+        ol.ol_tree_keep(t.code, desc, t.cache, T, length, start_d, torch.from_numpy(kept).to(DEV),
+                        torch.from_numpy(n_kept).to(DEV), t.ws)
+        length = length + n_kept
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+    for b in range(B):
+        n = int(length[b])
+        got = t.row(0, b, n).double()
+        tol = 2.0 ** -8 * k_ref[b].abs() + 1e-5
+        assert bool(((got - k_ref[b]).abs() <= tol).all())
+        assert torch.equal(t.row(1, b, n).double(), v_ref[b])
+    # the framework's decode attention reads what was kept
+    q = torch.randn((B, Hq, D), generator=gen, device=DEV, dtype=torch.bfloat16)
+    out = torch.empty_like(q)
+    n = ol.ol_workspace_size(B, Hq, H, D)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    ol.ol_workspace_init(ws, n)
+    fn = ol.ol_decode_attention if layout == "contiguous" else ol.ol_paged_decode_attention
+    fn(desc, q, Hq, length, torch.from_numpy(length).to(DEV), 0.0, -1, out, ol.OL_BF16, ws, n)
+    for b in range(B):
+        for g in range(H):
+            rows = t.row(0, b, int(length[b]))[g], t.row(1, b, int(length[b]))[g]
+            ok = np.ones((1, int(length[b])), bool)
+            want = du.tree_attention(q[b, g * G: (g + 1) * G, None], *rows, ok, D ** -0.5)[0][:, 0]
+            assert float((out[b, g * G: (g + 1) * G].double() - want).abs().max()) < 0.02
