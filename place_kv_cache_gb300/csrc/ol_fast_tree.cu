@@ -1,5 +1,748 @@
+// ol_fast_tree.cu -- attention of drafted trees over a cache on the 5th
+// generation tensor cores: bf16, head_dim 64 or 128, contiguous cache or paged
+// pool with pages of a multiple of 16 tokens.
+//
+// A unit is up to 256 (head, node) rows r = head * nodes + node of one row's kv
+// head: the vectors of q they read are consecutive, and every K/V byte is read
+// once per unit. Its tokens form tiles of 128; equal contiguous shares of all
+// units' tiles go to one CTA per SM (TreeWalk in ol_tree.cuh).
+//
+// Two softmax streams of 128 threads (one row each) work in turn, so that the
+// tensor core has one stream's products while the other one's weights are
+// formed. With more than 128 rows (NQ = 2) the streams have a query tile each
+// and share every K/V tile; with up to 128 rows (NQ = 1) they have the same
+// queries and every second K/V tile each, and are joined at the segment's end.
+//   S = Q K^T      128 x 128 x D, both operands in shared memory, S in TMEM
+//   P = 2^(S - m)  registers, bf16, back to TMEM over S
+//   O += P V       128 x D x 128, P from TMEM, V from shared memory, O in TMEM
+// m is a reference that follows the row's maximum only when that has grown by
+// more than 2^8 (the products are exact powers of two apart), so O is rescaled
+// rarely. Sums and O are fp32; P is rounded to bf16, the type its product with
+// V takes: 2^-9 of each weight on average, as much as the output's own rounding.
+//
+// Warps: 0 producer (TMA; lanes share the boxes of a tile: pages of 16 tokens
+// are boxes of 2 KB), 1 MMA issue, 2-3 fixers, 4-7 and 8-11 the streams. The
+// fixers pass every V tile on and, in tiles that hold drafted tokens or end the
+// row, zero the rows outside the row's tokens and the non-finite elements: a
+// product with P = 0 must not see them. Where a stream meets such an element
+// in a drafted token, it adds the non-finite values of the tokens that its row
+// sees to the outputs at the end (rare, unhurried).
+//
+// Bounds: 4 * D bytes per token and kv head against 4 * D * rows flops: the
+// memory up to 256 rows, then the tensor cores.
 #include "ol_tree.cuh"
+
 namespace ol {
-bool fast_tree_supported(const TreeParams&) { return false; }
-cudaError_t launch_fast_tree(TreeParams&, int, cudaStream_t) { return cudaErrorNotSupported; }
+namespace {
+
+constexpr int kTile = kTreeFastTile;
+constexpr int kThreads = 384;
+constexpr float kLazyLog2 = 8.f;
+
+template <int D, int NQ>
+struct Lay {
+  static constexpr int kHalves = D / 64;                // 64-element (128-byte) column blocks
+  static constexpr int kTileBytes = kTile * D * 2;      // K, V or Q tile
+  static constexpr int kSlots = D == 128 ? (NQ == 1 ? 6 : 5) : 12;
+  // V tiles on their way: V of tile n + kFix comes into the ring only after a
+  // slot of tile n or n + 1 is free, which is after V of tile n was taken
+  static constexpr int kFix = (kSlots + 1) / 2;
+  static constexpr int kQ = 0;
+  static constexpr int kRing = NQ * kTileBytes;
+  static constexpr int kStats = kRing + kSlots * kTileBytes;  // float2 [2][128]: streams' (m, l)
+  static constexpr int kBars = kStats + 2 * 128 * 8;
+  // full, empty [kSlots], fixed [kFix]; qfull, qempty, sfull[2], pready[2], pvdone[2], drain, join
+  static constexpr int kNumBars = 2 * kSlots + kFix + 10;
+  static constexpr int kBad = kBars + kNumBars * 8;     // uint32 [kFix + 1][2]
+  static constexpr int kMisc = kBad + (kFix + 1) * 8;   // TMEM address, abort flag
+  static constexpr int kTotal = kMisc + 16;
+  static_assert(kTotal <= 232448, "shared memory of one CTA");
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  // start, leading and stride offsets in 16 bytes; version 1; 128-byte swizzle
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo_bytes >> 4) << 16 | (uint64_t)(sbo_bytes >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// f32 accumulator, bf16 operands; M = 128
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_mn_major) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define OL_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
+#define OL_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : OL_R8(x, 0), OL_R8(x, 8), OL_R8(x, 16), OL_R8(x, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      OL_W8(x, 0), OL_W8(x, 8), OL_W8(x, 16), OL_W8(x, 24)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// ----------------------------------------------------------------------- roles
+
+template <int D, int NQ>
+struct Bars {
+  using L = Lay<D, NQ>;
+  uint32_t at;
+  __device__ uint32_t full(int s) const { return at + 8 * s; }
+  __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
+  __device__ uint32_t fixed(uint32_t n) const { return at + 8 * (2 * L::kSlots + n % L::kFix); }  // of tile n
+  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kFix); }
+  __device__ uint32_t qempty() const { return qfull() + 8; }
+  __device__ uint32_t sfull(int j) const { return qfull() + 16 + 8 * j; }
+  __device__ uint32_t pready(int j) const { return qfull() + 32 + 8 * j; }
+  __device__ uint32_t pvdone(int j) const { return qfull() + 48 + 8 * j; }
+  __device__ uint32_t drain() const { return qfull() + 64; }
+  __device__ uint32_t join() const { return qfull() + 72; }
+};
+
+// A wait that ends: after about two seconds, or once another warp has given up,
+// it returns false; the CTA then winds down with a device status.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      set_status(status, OL_DEVICE_GUARD);
+      return false;
+    }
+  }
+  return true;
+}
+
+// The same for a whole warp: one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
+}
+
+// Ring places of K (which = 0) and V (1) of the CTA's n-th tile.
+template <int SLOTS>
+__device__ __forceinline__ int ring_slot(uint32_t n, int which) { return (int)((2 * n + which) % SLOTS); }
+template <int SLOTS>
+__device__ __forceinline__ uint32_t ring_phase(uint32_t n, int which) { return ((2 * n + which) / SLOTS) & 1; }
+
+// Lowest token of the row that any node may see.
+__device__ __forceinline__ int row_low(const TreeParams& p, const TreeRow& r) {
+  return p.window < 0 || r.prefix <= p.window ? 0 : r.prefix - p.window;
+}
+// The tile holds tokens that are not the prefix of all rows: drafted ones, the
+// end of the row, or tokens below the window.
+__device__ __forceinline__ bool edge_tile(const TreeRow& r, int low, int t0) {
+  return t0 + kTile > r.prefix || t0 < low;
+}
+// Streams with work on a unit.
+template <int NQ>
+__device__ __forceinline__ int unit_streams(const TreeParams& p, const TreeWalk& w) {
+  return NQ == 2 && p.group * p.nodes - w.qg * p.rows_per_unit <= 128 ? 1 : 2;
+}
+
+struct Maps {
+  CUtensorMap q, kv;
+};
+
+// Bits [a, b) of a 32-bit word (a and b may lie outside it).
+__device__ __forceinline__ uint32_t bit_range(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 32);
+  if (a >= b) return 0;
+  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
+}
+
+// Visibility of tokens [t, t + 32) for a node, as bits.
+__device__ __forceinline__ uint32_t visible_word(const TreeParams& p, const TreeRow& row, int b, int node, int low,
+                                                 int t) {
+  uint32_t bits = bit_range(low - t, row.prefix - t);
+  const int j0 = t - row.prefix;  // drafted index of bit 0
+  if (j0 <= -32 || j0 >= row.count) return bits;
+  uint32_t tree;
+  if (p.mask) {
+    const uint64_t* const m = p.mask + ((size_t)b * p.nodes + node) * p.words;
+    if (j0 < 0) {
+      tree = (uint32_t)m[0] << -j0;
+    } else {
+      const int w = j0 / 64, s = j0 % 64;
+      uint64_t v = m[w] >> s;
+      if (s > 32 && w + 1 < p.words) v |= m[w + 1] << (64 - s);
+      tree = (uint32_t)v;
+    }
+  } else {
+    tree = bit_range(-32, node + 1 - j0);
+  }
+  tree &= bit_range(-j0, row.count - j0);
+  if (p.window >= 0 && tree) {
+    const int at = tree_position(p, row, b, node);
+    for (uint32_t left = tree; left; left &= left - 1) {
+      const int c = __ffs(left) - 1;
+      if ((long long)at - tree_position(p, row, b, j0 + c) > p.window) tree &= ~(1u << c);
+    }
+  }
+  return bits | tree;
+}
+
+// Adds the non-finite elements, in dimensions [d0, d1), of the V of drafted
+// tokens in the segment's tiles that a node sees to what this thread has
+// written for it: to the slot's row `place`, or to row `out` of the output.
+__device__ __noinline__ void add_nonfinite(const TreeParams& p, TreeRow row, int b, int g, int tile0, int tile1, int node,
+                                           int d0, int d1, float* slot, int place, size_t out) {
+  const int a = max(row.start + tile0 * kTile, row.prefix), e = min(row.start + tile1 * kTile, row.len);
+  for (int t = a; t < e; ++t) {
+    if (!tree_sees_drafted(p, row, b, node, t - row.prefix)) continue;
+    const long long at = cache_row(p.cache, 1, b, g, t);
+    if (at < 0) continue;
+    const uint16_t* const v = reinterpret_cast<const uint16_t*>(p.cache.base) + at * p.head_dim;
+    for (int d = d0; d < d1; ++d) {
+      if ((v[d] & 0x7f80u) != 0x7f80u) continue;
+      const float x = bf16_bits_to_float(v[d]);
+      if (slot) {
+        slot[2 * p.rows_per_unit + ((size_t)(d / 4) * p.rows_per_unit + place) * 4 + d % 4] += x;
+      } else if (p.out_dtype == OL_F32) {
+        reinterpret_cast<float*>(p.out)[out * p.head_dim + d] += x;
+      } else {
+        uint16_t& y = reinterpret_cast<uint16_t*>(p.out)[out * p.head_dim + d];
+        y = float_to_bf16_bits(bf16_bits_to_float(y) + x);
+      }
+    }
+  }
+}
+
+template <int D, int NQ, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_constant__ Maps maps,
+                                                                const __grid_constant__ TreeParams p, const int box,
+                                                                const int qbox, const int keep_l2) {
+  using L = Lay<D, NQ>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sa = smem_u32(smem);
+  if (sa % 1024 != 0) {  // the swizzled tiles need it; the launch has no other shared memory
+    if (threadIdx.x == 0) set_status(p.status, OL_DEVICE_GUARD);
+    return;
+  }
+  const Bars<D, NQ> bar{sa + L::kBars};
+  volatile uint32_t* const abort = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
+  volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(smem + L::kBad);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (tid == 0) {
+    prefetch_tensormap(&maps.q);
+    prefetch_tensormap(&maps.kv);
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(bar.full(s), 1);
+      mbar_init(bar.empty(s), 1);
+    }
+    for (int x = 0; x < L::kFix; ++x) mbar_init(bar.fixed(x), 64);
+    mbar_init(bar.qfull(), 1);
+    mbar_init(bar.qempty(), 1);
+    for (int j = 0; j < 2; ++j) {
+      mbar_init(bar.sfull(j), 1);
+      mbar_init(bar.pready(j), 128);
+      mbar_init(bar.pvdone(j), 1);
+    }
+    mbar_init(bar.drain(), 1);
+    mbar_init(bar.join(), 256);
+    fence_mbar_init();
+    *abort = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa + L::kMisc) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  TreeWalk w(p);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t policy = keep_l2 ? policy_evict_normal() : policy_evict_first();
+    const uint64_t keep = policy_evict_normal();
+    uint32_t n = 0, seg = 0, issued = 0;
+    bool ok = true;
+    auto load = [&](int which, int t0) {  // K (0) or V (1) of the tokens from t0
+      const int s = ring_slot<L::kSlots>(n, which);
+      const uint32_t ph = ring_phase<L::kSlots>(n, which);
+      if (!warp_wait(bar.empty(s), ph ^ 1, abort, p.status)) return false;
+      issued = 2 * n + which + 1;
+      const int low = row_low(p, w.row);
+      const int first = max(low - t0, 0) / box, last = (min(w.row.len - t0, kTile) + box - 1) / box;  // boxes
+      if (lane == 0) mbar_arrive_expect_tx(bar.full(s), (uint32_t)(last - first) * box * D * 2);
+      __syncwarp();
+      for (int i = lane; i < (last - first) * L::kHalves; i += 32) {
+        const int x = first + i / L::kHalves, h = i % L::kHalves;
+        const int t = t0 + x * box;
+        int y;
+        if (PAGED) {
+          int page = p.cache.block_table[(size_t)w.b * p.cache.max_pages + t / p.cache.page_size];
+          if (page < 0 || page >= p.cache.num_pages) {
+            set_status(p.status, OL_DEVICE_GUARD);
+            page = 0;
+          }
+          y = ((which * p.cache.num_pages + page) * p.kv_heads + w.g) * p.cache.page_size + t % p.cache.page_size;
+        } else {
+          y = ((which * p.batch + w.b) * p.kv_heads + w.g) * p.cache.capacity + t;
+        }
+        tma_load_2d(sa + L::kRing + s * L::kTileBytes + h * (kTile * 128) + x * box * 128, &maps.kv, h * 64, y,
+                    bar.full(s), policy);
+      }
+      return true;
+    };
+    while (ok && w.next(p)) {
+      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
+        const int t0 = w.row.start + tile * kTile;
+        ok = load(0, t0);
+        if (ok && tile == w.tile0) {
+          // the last segment's queries are read
+          ok = warp_wait(bar.qempty(), (seg & 1) ^ 1, abort, p.status);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(bar.qfull(), (uint32_t)NQ * qbox * D * 2);
+            const int y = (int)tree_out_row(p, w.b, w.g, w.qg * p.rows_per_unit);
+            for (int j = 0; j < NQ; ++j)
+              for (int h = 0; h < L::kHalves; ++h)
+                tma_load_2d(sa + L::kQ + j * L::kTileBytes + h * (kTile * 128), &maps.q, h * 64, y + j * 128,
+                            bar.qfull(), keep);
+          }
+          if (ok) ++seg;
+        }
+        if (ok) ok = load(1, t0);
+      }
+    }
+    if (!ok) {  // copies in flight end before the CTA does
+      if (seg) mbar_wait_bounded(bar.qfull(), (seg - 1) & 1);
+      for (uint32_t i = issued > (uint32_t)L::kSlots ? issued - L::kSlots : 0; i < issued; ++i)
+        mbar_wait_bounded(bar.full(i % L::kSlots), (i / L::kSlots) & 1);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t kDescS = mma_desc(128, false), kDescO = mma_desc(D, true);
+      uint32_t n = 0, seg = 0, nj[2] = {0, 0};  // tiles; segments; tiles of each stream
+      bool ok = true;
+      while (ok && w.next(p)) {
+        const int tiles = w.tile1 - w.tile0;
+        const int streams = unit_streams<NQ>(p, w);
+        ok = wait_or_abort(bar.qfull(), seg & 1, abort, p.status);
+        ++seg;
+        // S of the segment's tile i for stream j
+        auto scores = [&](int i, int j) {
+          const int s = ring_slot<L::kSlots>(n + i, 0);
+          if (NQ == 1 || j == 0)
+            if (!wait_or_abort(bar.full(s), ring_phase<L::kSlots>(n + i, 0), abort, p.status)) return false;
+          const uint32_t q = sa + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, k = sa + L::kRing + s * L::kTileBytes;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = x / 4 * (kTile * 128) + x % 4 * 32;
+            mma_ss(tmem + j * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kDescS, x > 0);
+          }
+          mma_commit(bar.sfull(j));
+          if (NQ == 1 || j == streams - 1) {
+            mma_commit(bar.empty(s));
+            if (i == tiles - 1) mma_commit(bar.qempty());
+          }
+          return true;
+        };
+        auto sums = [&](int i, int j, bool first) {
+          const int s = ring_slot<L::kSlots>(n + i, 1);
+          if (!wait_or_abort(bar.pready(j), nj[j] & 1, abort, p.status)) return false;
+          if (NQ == 1 || j == 0)
+            if (!wait_or_abort(bar.fixed(n + i), (n + i) / L::kFix & 1, abort, p.status)) return false;
+          tmem_fence_after();
+          const uint32_t v = sa + L::kRing + s * L::kTileBytes;
+#pragma unroll
+          for (int x = 0; x < kTile / 16; ++x)
+            mma_ts(tmem + 256 + j * D, tmem + j * 128 + x * 8, smem_desc(v + x * 2048, kTile * 128, 1024), kDescO,
+                   !(first && x == 0));
+          mma_commit(bar.pvdone(j));
+          if (NQ == 1 || j == streams - 1) mma_commit(bar.empty(s));
+          ++nj[j];
+          return true;
+        };
+        if (NQ == 2) {
+          for (int j = 0; ok && j < streams; ++j) ok = scores(0, j);
+          for (int i = 0; ok && i < tiles; ++i)
+            for (int j = 0; ok && j < streams; ++j) {
+              ok = sums(i, j, i == 0);
+              if (ok && i + 1 < tiles) ok = scores(i + 1, j);
+            }
+        } else {
+          for (int i = 0; ok && i < 2 && i < tiles; ++i) ok = scores(i, i);
+          for (int i = 0; ok && i < tiles; ++i) {
+            ok = sums(i, i & 1, i < 2);
+            if (ok && i + 2 < tiles) ok = scores(i + 2, i & 1);
+          }
+        }
+        n += tiles;
+      }
+      if (!ok) {  // products in flight end before TMEM is freed
+        mma_commit(bar.drain());
+        mbar_wait_bounded(bar.drain(), 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ fixers
+    const int me = tid - 64;
+    uint32_t n = 0;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const int low = row_low(p, w.row);
+      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
+        const int s = ring_slot<L::kSlots>(n, 1);
+        ok = warp_wait(bar.full(s), ring_phase<L::kSlots>(n, 1), abort, p.status);
+        const int t0 = w.row.start + tile * kTile;
+        if (ok && edge_tile(w.row, low, t0)) {
+          uint8_t* const v = smem + L::kRing + s * L::kTileBytes;
+          bool found = false;
+          // 16-byte pieces: rows outside [low, len) become zeros, drafted rows lose non-finite elements
+          const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
+          for (int i = me; i < kTile * D / 8; i += 64) {
+            const int r = i / 8 % kTile;  // pieces of 128-byte lines, line after line of each half
+            uint4* const at = reinterpret_cast<uint4*>(v) + i;
+            if (r < r_low || r >= r_end) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else if (r >= r_tree) {
+              uint4 x = *at;
+              uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
+              bool hit = false;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                if ((e[c] & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u, hit = true;
+                if ((e[c] & 0x7f800000u) == 0x7f800000u) e[c] &= 0xffffu, hit = true;
+              }
+              if (hit) *at = x;
+              found |= hit;
+            }
+          }
+          const bool any = __any_sync(0xffffffffu, found);
+          if (lane == 0) bad[2 * (n % L::kFix) + warp - 2] = any;
+          fence_proxy_async_smem();
+        }
+        if (ok) mbar_arrive(bar.fixed(n));
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- streams
+    const int j = (warp - 4) / 4, row = tid % 128;  // TMEM lane
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + j * 128 + lanes, to = tmem + 256 + j * D + lanes;
+    const int R = p.group * p.nodes;
+    float2* const stats = reinterpret_cast<float2*>(smem + L::kStats);
+    uint32_t n = 0, nj = 0;  // the CTA's tiles; this stream's
+    bool ok = true;
+    uint32_t joins = 0;
+    auto join = [&] {  // both streams, 256 threads
+      mbar_arrive(bar.join());
+      return warp_wait(bar.join(), joins++ & 1, abort, p.status);
+    };
+    while (ok && w.next(p)) {
+      const int r = w.qg * p.rows_per_unit + (NQ == 2 ? j * 128 : 0) + row;  // (head, node)
+      const int tiles = w.tile1 - w.tile0;
+      if (NQ == 2 && j >= unit_streams<NQ>(p, w)) {
+        n += tiles;
+        continue;
+      }
+      const bool live = r < R, live_warp = r - lane < R;
+      const int node = r % p.nodes;
+      const int low = p.window < 0 ? 0 : tree_low(p, w.row, w.b, node);
+      const int low_all = row_low(p, w.row);
+      float m = -INFINITY, l = 0.f;  // reference (raw scores) and sum
+      bool nonfinite = false;
+      const int step = NQ == 2 ? 1 : 2;
+      bool first = true;
+      for (int i = NQ == 2 ? 0 : j; ok && i < tiles; i += step, ++nj) {
+        const int t0 = w.row.start + (w.tile0 + i) * kTile;
+        ok = warp_wait(bar.sfull(j), nj & 1, abort, p.status);
+        if (!ok) break;
+        tmem_fence_after();
+        const bool edge = edge_tile(w.row, low_all, t0);
+        if (live_warp) {
+          // S is read twice, 64 columns at a time: a whole row does not fit in
+          // the registers beside the rest
+          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+          const bool masked = edge || __any_sync(0xffffffffu, low > t0);
+          if (masked)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) seen[c] = live ? visible_word(p, w.row, w.b, node, low, t0 + 32 * c) : 0u;
+          auto load = [&](int h, uint32_t* s) {
+            tmem_ld32(ts + 64 * h, s);
+            tmem_ld32(ts + 64 * h + 32, s + 32);
+            tmem_wait_ld();
+            if (masked)
+#pragma unroll
+              for (int x = 0; x < 64; ++x)
+                if (!(seen[2 * h + x / 32] >> (x % 32) & 1)) s[x] = 0xff800000u;  // -inf
+          };
+          uint32_t s[64];
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            load(1 - h, s);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) top[c % 4] = fmaxf(top[c % 4], __uint_as_float(s[c]));
+          }
+          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          const bool grow = live && mx * p.scale_log2 > m * p.scale_log2 + kLazyLog2;  // false for NaN, and -inf both
+          if (__any_sync(0xffffffffu, grow)) {
+            const float m2 = grow ? mx : m;
+            const float f = grow ? exp2f((m - m2) * p.scale_log2) : 1.f;  // 0 where m is -inf
+            m = m2;
+            l *= f;
+            if (!first) {
+              // the products that wrote O are done
+              ok = warp_wait(bar.pvdone(j), (nj & 1) ^ 1, abort, p.status);
+              tmem_fence_after();
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st32(to + 32 * c, o);
+              }
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1) load(1, s);  // the first half is still here
+            uint32_t pk[32];
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float a = fast_exp2(fmaf(__uint_as_float(s[2 * x]), p.scale_log2, base));
+              const float b = fast_exp2(fmaf(__uint_as_float(s[2 * x + 1]), p.scale_log2, base));
+              sum[x & 1] += a;
+              sum[2 + (x & 1)] += b;
+              pk[x] = pack_bf16x2(a, b);
+            }
+            tmem_st32(ts + 32 * h, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        if (edge) {
+          // V is in place; whether a drafted token in it had non-finite elements
+          const uint32_t v = n + i;
+          ok = ok && warp_wait(bar.fixed(v), v / L::kFix & 1, abort, p.status);
+          nonfinite |= (bad[2 * (v % L::kFix)] | bad[2 * (v % L::kFix) + 1]) != 0;
+        }
+        if (!ok) break;
+        first = false;
+        tmem_fence_before();
+        mbar_arrive(bar.pready(j));
+      }
+      n += tiles;
+      if (!ok) break;
+      if (!first) ok = warp_wait(bar.pvdone(j), (nj & 1) ^ 1, abort, p.status);
+      if (!ok) break;
+      tmem_fence_after();
+
+      // the segment's state: m in log2 units
+      float ml = m == -INFINITY ? -INFINITY : m * p.scale_log2;
+      float f0 = 1.f, f1 = 0.f;  // factors of O (of both streams' O)
+      bool has1 = false;
+      if (NQ == 1) {
+        tmem_fence_before();
+        stats[j * 128 + row] = make_float2(ml, l);
+        if (row == 0) bad[2 * L::kFix + j] = nonfinite;  // the same for all threads of a stream
+        if (!(ok = join())) break;
+        tmem_fence_after();
+        nonfinite = (bad[2 * L::kFix] | bad[2 * L::kFix + 1]) != 0;
+        const float2 a = stats[row], b = stats[128 + row];
+        ml = fmaxf(a.x, b.x);
+        const float top = ml == -INFINITY ? 0.f : ml;
+        f0 = exp2f(a.x - top);
+        f1 = exp2f(b.x - top);
+        l = a.y * f0 + b.y * f1;
+        has1 = tiles > 1;
+      }
+      const bool whole = w.whole();
+      float* const slot = whole ? nullptr : tree_slot(p, w.slot);
+      const int place = (NQ == 2 ? j * 128 : 0) + row;  // in the unit
+      const bool mine = live && (!whole || node < w.row.count);
+      if (slot && live && (NQ == 2 || j == 0)) {
+        slot[place] = ml;
+        slot[p.rows_per_unit + place] = l;
+      }
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      if (live_warp) {
+        // NQ == 1: each stream writes half of the dimensions
+        constexpr int kCols = NQ == 2 ? D : D / 2;
+        const int c0 = NQ == 2 ? 0 : j * kCols;
+#pragma unroll 1
+        for (int c = c0; c < c0 + kCols; c += 32) {
+          uint32_t a[32], b[32];
+          const uint32_t t = tmem + 256 + lanes;
+          if (NQ == 2) {
+            tmem_ld32(to + c, a);
+          } else {
+            tmem_ld32(t + c, a);
+            if (has1) tmem_ld32(t + D + c, b);
+          }
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            o[x] = __uint_as_float(a[x]);
+            if (NQ == 1) o[x] = o[x] * f0 + (has1 ? __uint_as_float(b[x]) * f1 : 0.f);
+            o[x] *= inv;
+          }
+          if (mine && slot) {
+            float4* const to4 = reinterpret_cast<float4*>(slot + 2 * p.rows_per_unit);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              to4[(size_t)(c / 4 + x) * p.rows_per_unit + place] =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          } else if (mine) {
+            const size_t at = tree_out_row(p, w.b, w.g, r) * D + c;
+            if (p.out_dtype == OL_F32) {
+              float4* const y = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) y[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            } else {
+              uint4* const y = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                y[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
+                                  pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
+            }
+          }
+        }
+        if (nonfinite && mine)
+          add_nonfinite(p, w.row, w.b, w.g, w.tile0, w.tile1, node, c0, c0 + kCols, slot, place,
+                        tree_out_row(p, w.b, w.g, r));
+      }
+      if (NQ == 1) {  // both streams have read both O before either's next product
+        tmem_fence_before();
+        ok = join();
+      }
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ------------------------------------------------------------------------ host
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+// A bf16 buffer as rows of D elements; boxes of `box` rows x 64 elements, 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const void* base, int D, uint64_t rows, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D * 2};
+  cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t kv_rows(const TreeParams& p) {
+  return p.cache.block_table ? 2ull * p.cache.num_pages * p.kv_heads * p.cache.page_size
+                             : 2ull * p.batch * p.kv_heads * p.cache.capacity;
+}
+
+template <int D, int NQ, bool PAGED>
+cudaError_t launch_cfg(const Maps& maps, const TreeParams& p, int box, int qbox, cudaStream_t s) {
+  auto kern = fast_tree_kernel<D, NQ, PAGED>;
+  static const cudaError_t attr =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NQ>::kTotal);
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(kern, dim3(p.nctas), dim3(kThreads), Lay<D, NQ>::kTotal, s, maps, p, box, qbox,
+                    p.units_per_head > 1 ? 1 : 0);
+}
+
+template <int D>
+cudaError_t launch_dim(const Maps& maps, const TreeParams& p, int box, int qbox, cudaStream_t s) {
+  const bool two = p.rows_per_unit == 256;
+  if (p.cache.block_table)
+    return two ? launch_cfg<D, 2, true>(maps, p, box, qbox, s) : launch_cfg<D, 1, true>(maps, p, box, qbox, s);
+  return two ? launch_cfg<D, 2, false>(maps, p, box, qbox, s) : launch_cfg<D, 1, false>(maps, p, box, qbox, s);
+}
+
+}  // namespace
+
+bool fast_tree_supported(const TreeParams& p) {
+  if (p.dtype != OL_BF16 || (p.head_dim != 64 && p.head_dim != 128)) return false;
+  if (p.cache.block_table && p.cache.page_size % 16 != 0) return false;
+  // TMA row coordinates are 32-bit
+  return kv_rows(p) < (1ull << 31) && (uint64_t)p.batch * p.q_heads * p.nodes + 256 < (1ull << 31);
+}
+
+cudaError_t launch_fast_tree(TreeParams& p, int sms, cudaStream_t s) {
+  const int R = p.group * p.nodes;
+  p.rows_per_unit = tree_fast_rows(p.group, p.nodes);
+  p.units_per_head = (R + p.rows_per_unit - 1) / p.rows_per_unit;
+  p.tile = kTile;
+  p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
+  int box = kTile;
+  if (p.cache.block_table)  // the largest power of two that divides a page
+    while (p.cache.page_size % box != 0) box /= 2;
+  const int qbox = R < 128 ? (R + 7) / 8 * 8 : 128;
+  Maps maps;
+  if (!encode_rows(&maps.q, p.q, p.head_dim, (uint64_t)p.batch * p.q_heads * p.nodes, qbox) ||
+      !encode_rows(&maps.kv, p.cache.base, p.head_dim, kv_rows(p), box))
+    return cudaErrorInvalidValue;
+  return p.head_dim == 128 ? launch_dim<128>(maps, p, box, qbox, s) : launch_dim<64>(maps, p, box, qbox, s);
+}
+
 }  // namespace ol

@@ -163,6 +163,14 @@ CASES = [
     ("bf16", "paged", 2, 8, 2, 128, 16, 10, [500, 300], None, 100, "tree"),
     ("bf16", "paged", 40, 8, 2, 128, 16, 3, list(range(3, 203, 5))),
     ("bf16", "contiguous", 170, 4, 4, 64, 0, 2, [2 + (7 * i) % 300 for i in range(170)]),
+    # many tiles and several segments a CTA, one and two query tiles, both head sizes
+    ("bf16", "contiguous", 4, 32, 8, 128, 0, 64, [6000, 1000, 4001, 6500]),
+    ("bf16", "paged", 4, 32, 8, 128, 16, 64, [6000, 1000, 4001, 6500]),
+    ("bf16", "paged", 4, 32, 8, 128, 16, 16, [6000, 1000, 4001, 6500], [16, 3, 16, 1]),
+    ("bf16", "contiguous", 4, 32, 8, 64, 0, 40, [6000, 1000, 4001, 6500]),
+    ("bf16", "contiguous", 4, 32, 8, 64, 0, 9, [6000, 1000, 4001, 6500]),
+    ("bf16", "paged", 60, 28, 4, 128, 32, 64, [64 + (37 * i) % 700 for i in range(60)]),
+    ("bf16", "paged", 60, 28, 4, 128, 32, 6, [6 + (37 * i) % 700 for i in range(60)]),
     # --- CUDA cores
     ("bf16", "paged", 2, 8, 2, 128, 8, 10, [100, 33]),
     ("bf16", "paged", 2, 8, 2, 128, 7, 10, [100, 33]),
