@@ -608,7 +608,8 @@ OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* up
  * every drafted token as seen (the mask is on the device) and
  * kv_payload_bytes_read the tokens that some node may see, once.
  * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
- * UNSUPPORTED (other layouts, head_dim > 256, nodes > 512), CUDA.
+ * UNSUPPORTED (other layouts, head_dim > 256, nodes > 512, 2^31 tiles of work at
+ * full capacity), CUDA.
  */
 OL_API size_t ol_workspace_size_tree(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                      int32_t nodes);

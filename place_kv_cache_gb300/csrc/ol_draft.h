@@ -49,8 +49,8 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t s);
 constexpr int kTreeMaxNodes = 512;
 constexpr int kTreeMaxCtas = 192;  // CTAs of the tensor-core kernel, one per SM
 constexpr int kTreeGenRows = 32;   // (head, node) rows of a CUDA-core unit
-constexpr int kTreeGenTile = 32;   // tokens of its tile
-constexpr int kTreeFastTile = 128;
+constexpr int kTreeGenTileLog2 = 5;   // tokens of its tile: 32
+constexpr int kTreeFastTileLog2 = 7;  // 128
 
 struct TreeParams {
   CacheRef cache;
@@ -70,7 +70,7 @@ struct TreeParams {
   // work split
   int rows_per_unit;            // (head, node) rows r = head * nodes + node of a unit
   int units_per_head;           // ceil(group * nodes / rows_per_unit)
-  int tile;                     // tokens per tile
+  int tile_log2;                // tokens per tile
   int nctas;                    // the tiles of all units in contiguous equal shares
 };
 
@@ -80,14 +80,14 @@ struct TreeParams {
 struct TreeRow {
   int len, count, prefix, start, ntiles;
 };
-OL_HD inline TreeRow tree_row(int len, int count, int window, int tile) {
+OL_HD inline TreeRow tree_row(int len, int count, int window, int tile_log2) {
   TreeRow r;
   r.len = len;
   r.count = count;
   r.prefix = len - count;
   const int lo = window < 0 || r.prefix <= window ? 0 : r.prefix - window;
-  r.start = lo / tile * tile;
-  r.ntiles = count > 0 ? (len - r.start + tile - 1) / tile : 0;
+  r.start = lo >> tile_log2 << tile_log2;
+  r.ntiles = count > 0 ? (len - r.start + (1 << tile_log2) - 1) >> tile_log2 : 0;
   return r;
 }
 
@@ -101,8 +101,17 @@ inline size_t tree_workspace_bytes(int q_heads, int kv_heads, int head_dim, int 
 }
 
 bool fast_tree_supported(const TreeParams& p);
-cudaError_t launch_fast_tree(TreeParams& p, int sms, cudaStream_t s);
-cudaError_t launch_generic_tree(TreeParams& p, int sms, cudaStream_t s);
+// Fill the work split of a kernel.
+void plan_fast_tree(TreeParams& p, int sms);
+void plan_generic_tree(TreeParams& p, int sms);
+// Tiles are counted in 32 bits on the device, whatever lengths it finds there.
+inline bool tree_counts_fit(const TreeParams& p) {
+  const unsigned __int128 tiles = (unsigned __int128)((p.cache.capacity >> p.tile_log2) + 1) * p.batch * p.kv_heads *
+                                  p.units_per_head;
+  return tiles < (1u << 31);
+}
+cudaError_t launch_fast_tree(const TreeParams& p, cudaStream_t s);
+cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s);
 
 // --------------------------------------------------------------- accepted path

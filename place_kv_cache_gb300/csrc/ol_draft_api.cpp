@@ -329,10 +329,6 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
     stats.kv_payload_bytes_read += 2ll * (lens_host[b] - lo) * c.kv_heads * token_payload(c);
   }
   if ((st = check_owner(c.ranges, c.nranges, c.owner)) != OL_OK) return st;
-  stats.workspace_bytes = (int64_t)need;
-  record(stats);
-  if (fault_injected()) return OL_ERR_INJECTED;
-  if (c.batch == 0) return OL_OK;
   TreeParams p = {};
   p.cache = cache_ref(layout, cache_desc, c);
   p.dtype = c.dtype;
@@ -354,8 +350,17 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
   p.out_dtype = out_dtype;
   p.status = static_cast<int32_t*>(workspace);
   p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
-  const int sms = sm_count_cached();
-  cudaError_t e = fast_tree_supported(p) ? launch_fast_tree(p, sms, s) : launch_generic_tree(p, sms, s);
+  const bool fast = fast_tree_supported(p);
+  if (fast)
+    plan_fast_tree(p, sm_count_cached());
+  else
+    plan_generic_tree(p, sm_count_cached());
+  if (!tree_counts_fit(p)) return OL_ERR_UNSUPPORTED;
+  stats.workspace_bytes = (int64_t)need;
+  record(stats);
+  if (fault_injected()) return OL_ERR_INJECTED;
+  if (c.batch == 0) return OL_OK;
+  cudaError_t e = fast ? launch_fast_tree(p, s) : launch_generic_tree(p, s);
   if (e == cudaSuccess) e = launch_tree_merge(p, s);
   return e == cudaSuccess ? OL_OK : OL_ERR_CUDA;
 }

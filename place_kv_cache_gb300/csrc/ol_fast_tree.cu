@@ -7,18 +7,18 @@
 // once per unit. Its tokens form tiles of 128; equal contiguous shares of all
 // units' tiles go to one CTA per SM (TreeWalk in ol_tree.cuh).
 //
-// Two softmax streams of 128 threads (one row each) work in turn, so that the
-// tensor core has one stream's products while the other one's weights are
-// formed. With more than 128 rows (NQ = 2) the streams have a query tile each
-// and share every K/V tile; with up to 128 rows (NQ = 1) they have the same
-// queries and every second K/V tile each, and are joined at the segment's end.
-//   S = Q K^T      128 x 128 x D, both operands in shared memory, S in TMEM
+// Two softmax streams of 128 threads (one row each) work on halves of tiles, 64
+// tokens a step, each with two S buffers: the tensor core has the next step's
+// scores ready while a step's weights are formed. With more than 128 rows
+// (NQ = 2) a stream has a query tile of its own and takes both halves of every
+// tile; with up to 128 (NQ = 1) both have the same queries and a stream takes its
+// half of every tile, and they are joined at the segment's end.
+//   S = Q K^T      128 x 64 x D, both operands in shared memory, S in TMEM
 //   P = 2^(S - m)  registers, bf16, back to TMEM over S
-//   O += P V       128 x D x 128, P from TMEM, V from shared memory, O in TMEM
+//   O += P V       128 x D x 64, P from TMEM, V from shared memory, O in TMEM
 // m is a reference that follows the row's maximum only when that has grown by
-// more than 2^8 (the products are exact powers of two apart), so O is rescaled
-// rarely. Sums and O are fp32; P is rounded to bf16, the type its product with
-// V takes: 2^-9 of each weight on average, as much as the output's own rounding.
+// more than 2^8, so O is rescaled rarely. Sums and O are fp32; P is rounded to
+// bf16, the type its product with V takes: as much as the output's own rounding.
 //
 // Warps: 0 producer (TMA; lanes share the boxes of a tile: pages of 16 tokens
 // are boxes of 2 KB), 1 MMA issue, 2-3 fixers, 4-7 and 8-11 the streams. The
@@ -35,7 +35,8 @@
 namespace ol {
 namespace {
 
-constexpr int kTile = kTreeFastTile;
+constexpr int kTile = 1 << kTreeFastTileLog2;
+constexpr int kStep = kTile / 2;  // tokens of a step
 constexpr int kThreads = 384;
 constexpr float kLazyLog2 = 8.f;
 
@@ -51,8 +52,8 @@ struct Lay {
   static constexpr int kRing = NQ * kTileBytes;
   static constexpr int kStats = kRing + kSlots * kTileBytes;  // float2 [2][128]: streams' (m, l)
   static constexpr int kBars = kStats + 2 * 128 * 8;
-  // full, empty [kSlots], fixed [kFix]; qfull, qempty, sfull[2], pready[2], pvdone[2], drain, join
-  static constexpr int kNumBars = 2 * kSlots + kFix + 10;
+  // full, empty [kSlots], fixed [kFix]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain, join
+  static constexpr int kNumBars = 2 * kSlots + kFix + 16;
   static constexpr int kBad = kBars + kNumBars * 8;     // uint32 [kFix + 1][2]
   static constexpr int kMisc = kBad + (kFix + 1) * 8;   // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 16;
@@ -110,6 +111,37 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
       : "memory");
 }
 
+// The same value in every lane of a converged warp, known as such to the compiler.
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
+__device__ __forceinline__ uint64_t pack_b32x2(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  return pack_b32x2(__float_as_uint(a), __float_as_uint(b));
+}
+__device__ __forceinline__ void unpack_b32x2(uint64_t x, uint32_t& a, uint32_t& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -124,11 +156,11 @@ struct Bars {
   __device__ uint32_t fixed(uint32_t n) const { return at + 8 * (2 * L::kSlots + n % L::kFix); }  // of tile n
   __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kFix); }
   __device__ uint32_t qempty() const { return qfull() + 8; }
-  __device__ uint32_t sfull(int j) const { return qfull() + 16 + 8 * j; }
-  __device__ uint32_t pready(int j) const { return qfull() + 32 + 8 * j; }
-  __device__ uint32_t pvdone(int j) const { return qfull() + 48 + 8 * j; }
-  __device__ uint32_t drain() const { return qfull() + 64; }
-  __device__ uint32_t join() const { return qfull() + 72; }
+  __device__ uint32_t sfull(int j, int b) const { return qfull() + 16 + 16 * j + 8 * b; }  // S buffer b of stream j
+  __device__ uint32_t pready(int j, int b) const { return qfull() + 48 + 16 * j + 8 * b; }  // P in its place
+  __device__ uint32_t pvdone(int j, int b) const { return qfull() + 80 + 16 * j + 8 * b; }  // and taken
+  __device__ uint32_t drain() const { return qfull() + 112; }
+  __device__ uint32_t join() const { return qfull() + 120; }
 };
 
 // A wait that ends: after about two seconds, or once another warp has given up,
@@ -150,6 +182,12 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 // The same for a whole warp: one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
+}
+
+// The warp's arrival, after all its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
 // Ring places of K (which = 0) and V (1) of the CTA's n-th tile.
@@ -186,8 +224,7 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 }
 
 // Visibility of tokens [t, t + 32) for a node, as bits.
-__device__ __forceinline__ uint32_t visible_word(const TreeParams& p, const TreeRow& row, int b, int node, int low,
-                                                 int t) {
+__device__ __noinline__ uint32_t visible_word(const TreeParams& p, const TreeRow row, int b, int node, int low, int t) {
   uint32_t bits = bit_range(low - t, row.prefix - t);
   const int j0 = t - row.prefix;  // drafted index of bit 0
   if (j0 <= -32 || j0 >= row.count) return bits;
@@ -265,16 +302,19 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       mbar_init(bar.full(s), 1);
       mbar_init(bar.empty(s), 1);
     }
-    for (int x = 0; x < L::kFix; ++x) mbar_init(bar.fixed(x), 64);
+    for (int x = 0; x < L::kFix; ++x) mbar_init(bar.fixed(x), 2);
     mbar_init(bar.qfull(), 1);
     mbar_init(bar.qempty(), 1);
     for (int j = 0; j < 2; ++j) {
-      mbar_init(bar.sfull(j), 1);
-      mbar_init(bar.pready(j), 128);
-      mbar_init(bar.pvdone(j), 1);
+      mbar_init(bar.sfull(j, 0), 1);
+      mbar_init(bar.sfull(j, 1), 1);
+      mbar_init(bar.pready(j, 0), 4);
+      mbar_init(bar.pready(j, 1), 4);
+      mbar_init(bar.pvdone(j, 0), 1);
+      mbar_init(bar.pvdone(j, 1), 1);
     }
     mbar_init(bar.drain(), 1);
-    mbar_init(bar.join(), 256);
+    mbar_init(bar.join(), 8);
     fence_mbar_init();
     *abort = 0;
   }
@@ -352,71 +392,82 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      constexpr uint32_t kDescS = mma_desc(128, false), kDescO = mma_desc(D, true);
-      uint32_t n = 0, seg = 0, nj[2] = {0, 0};  // tiles; segments; tiles of each stream
-      bool ok = true;
-      while (ok && w.next(p)) {
-        const int tiles = w.tile1 - w.tile0;
-        const int streams = unit_streams<NQ>(p, w);
-        ok = wait_or_abort(bar.qfull(), seg & 1, abort, p.status);
-        ++seg;
-        // S of the segment's tile i for stream j
-        auto scores = [&](int i, int j) {
-          const int s = ring_slot<L::kSlots>(n + i, 0);
-          if (NQ == 1 || j == 0)
-            if (!wait_or_abort(bar.full(s), ring_phase<L::kSlots>(n + i, 0), abort, p.status)) return false;
-          const uint32_t q = sa + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, k = sa + L::kRing + s * L::kTileBytes;
+    // The whole warp walks and waits, so that what the products are given stays
+    // in uniform registers; one elected lane issues them. (With lane 0 alone in
+    // the loop, each product waited for its operands: 160 cycles apiece.)
+    constexpr uint32_t kDescS = mma_desc(kStep, false), kDescO = mma_desc(D, true);
+    const uint32_t tm = uniform(tmem), base = uniform(sa);
+    uint32_t n = 0, seg = 0;  // tiles; segments
+    uint32_t phases = 0;      // of the streams' P buffers, a bit each
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const int tiles = uniform(w.tile1 - w.tile0);
+      const int streams = uniform(unit_streams<NQ>(p, w)), steps = NQ * tiles;
+      ok = warp_wait(bar.qfull(), seg & 1, abort, p.status);
+      ++seg;
+      // S of the segment's step i for stream j: tile i and half j, or (NQ = 2) tile i / 2 and half i % 2
+      auto scores = [&](int i, int j) {
+        const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
+        const int s = ring_slot<L::kSlots>(n + tile, 0);
+        if (half == 0 && (NQ == 1 || j == 0))
+          if (!warp_wait(bar.full(s), ring_phase<L::kSlots>(n + tile, 0), abort, p.status)) return false;
+        if (elect_one()) {
+          const uint64_t q = smem_desc(base + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, 16, 1024);
+          const uint64_t k = smem_desc(base + L::kRing + s * L::kTileBytes + half * (kStep * 128), 16, 1024);
+          const uint32_t to = tm + j * 128 + (i & 1) * kStep;
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = x / 4 * (kTile * 128) + x % 4 * 32;
-            mma_ss(tmem + j * 128, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), kDescS, x > 0);
+            constexpr uint32_t kBlock = kTile * 128 / 16, kK = 2;  // column block, 16 elements; in 16 bytes
+            mma_ss(to, q + (x / 4 * kBlock + x % 4 * kK), k + (x / 4 * kBlock + x % 4 * kK), kDescS, x > 0);
           }
-          mma_commit(bar.sfull(j));
-          if (NQ == 1 || j == streams - 1) {
+          mma_commit(bar.sfull(j, i & 1));
+          if (half == 1 && j == streams - 1) {  // K is read
             mma_commit(bar.empty(s));
-            if (i == tiles - 1) mma_commit(bar.qempty());
-          }
-          return true;
-        };
-        auto sums = [&](int i, int j, bool first) {
-          const int s = ring_slot<L::kSlots>(n + i, 1);
-          if (!wait_or_abort(bar.pready(j), nj[j] & 1, abort, p.status)) return false;
-          if (NQ == 1 || j == 0)
-            if (!wait_or_abort(bar.fixed(n + i), (n + i) / L::kFix & 1, abort, p.status)) return false;
-          tmem_fence_after();
-          const uint32_t v = sa + L::kRing + s * L::kTileBytes;
-#pragma unroll
-          for (int x = 0; x < kTile / 16; ++x)
-            mma_ts(tmem + 256 + j * D, tmem + j * 128 + x * 8, smem_desc(v + x * 2048, kTile * 128, 1024), kDescO,
-                   !(first && x == 0));
-          mma_commit(bar.pvdone(j));
-          if (NQ == 1 || j == streams - 1) mma_commit(bar.empty(s));
-          ++nj[j];
-          return true;
-        };
-        if (NQ == 2) {
-          for (int j = 0; ok && j < streams; ++j) ok = scores(0, j);
-          for (int i = 0; ok && i < tiles; ++i)
-            for (int j = 0; ok && j < streams; ++j) {
-              ok = sums(i, j, i == 0);
-              if (ok && i + 1 < tiles) ok = scores(i + 1, j);
-            }
-        } else {
-          for (int i = 0; ok && i < 2 && i < tiles; ++i) ok = scores(i, i);
-          for (int i = 0; ok && i < tiles; ++i) {
-            ok = sums(i, i & 1, i < 2);
-            if (ok && i + 2 < tiles) ok = scores(i + 2, i & 1);
+            if (tile == tiles - 1) mma_commit(bar.qempty());
           }
         }
-        n += tiles;
-      }
-      if (!ok) {  // products in flight end before TMEM is freed
-        mma_commit(bar.drain());
-        mbar_wait_bounded(bar.drain(), 0);
-      }
+        __syncwarp();
+        return true;
+      };
+      auto sums = [&](int i, int j) {
+        const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
+        const int s = ring_slot<L::kSlots>(n + tile, 1);
+        const int buf = 2 * j + (i & 1);
+        if (!warp_wait(bar.pready(j, i & 1), phases >> buf & 1, abort, p.status)) return false;
+        phases ^= 1u << buf;
+        if (half == 0 && (NQ == 1 || j == 0))
+          if (!warp_wait(bar.fixed(n + tile), (n + tile) / L::kFix & 1, abort, p.status)) return false;
+        tmem_fence_after();
+        if (elect_one()) {
+          const uint64_t v = smem_desc(base + L::kRing + s * L::kTileBytes + half * (kStep * 128), kTile * 128, 1024);
+          const uint32_t to = tm + 256 + j * D, from = tm + j * 128 + (i & 1) * kStep;
+#pragma unroll
+          for (int x = 0; x < kStep / 16; ++x) {
+            if (x == 0)
+              mma_ts(to, from, v, kDescO, i > 0);
+            else
+              mma_ts(to, from + x * 8, v + x * (2048 / 16), kDescO, true);
+          }
+          mma_commit(bar.pvdone(j, i & 1));
+          if (half == 1 && j == streams - 1) mma_commit(bar.empty(s));  // V is read
+        }
+        __syncwarp();
+        return true;
+      };
+      for (int i = 0; ok && i < 2 && i < steps; ++i)
+        for (int j = 0; ok && j < streams; ++j) ok = scores(i, j);
+      for (int i = 0; ok && i < steps; ++i)
+        for (int j = 0; ok && j < streams; ++j) {
+          ok = sums(i, j);
+          if (ok && i + 2 < steps) ok = scores(i + 2, j);
+        }
+      n += tiles;
     }
-    __syncwarp();
+    if (!ok) {  // products in flight end before TMEM is freed
+      if (elect_one()) mma_commit(bar.drain());
+      __syncwarp();
+      mbar_wait_bounded(bar.drain(), 0);
+    }
   } else if (warp < 4) {
     // ------------------------------------------------------------------ fixers
     const int me = tid - 64;
@@ -455,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
           if (lane == 0) bad[2 * (n % L::kFix) + warp - 2] = any;
           fence_proxy_async_smem();
         }
-        if (ok) mbar_arrive(bar.fixed(n));
+        if (ok) warp_arrive(bar.fixed(n));
       }
     }
   } else {
@@ -465,11 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint32_t ts = tmem + j * 128 + lanes, to = tmem + 256 + j * D + lanes;
     const int R = p.group * p.nodes;
     float2* const stats = reinterpret_cast<float2*>(smem + L::kStats);
-    uint32_t n = 0, nj = 0;  // the CTA's tiles; this stream's
+    uint32_t n = 0;                // the CTA's tiles
+    uint32_t phases = 0;           // of the S buffers, a bit each
+    // Whether the products with the last P of buffer b are done: a buffer's next
+    // S, and so its next P, comes only after them.
+    auto taken = [&](int b) { return warp_wait(bar.pvdone(j, b), phases >> b & 1 ^ 1, abort, p.status); };
     bool ok = true;
     uint32_t joins = 0;
-    auto join = [&] {  // both streams, 256 threads
-      mbar_arrive(bar.join());
+    auto join = [&] {  // both streams
+      warp_arrive(bar.join());
       return warp_wait(bar.join(), joins++ & 1, abort, p.status);
     };
     while (ok && w.next(p)) {
@@ -485,39 +540,36 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       const int low_all = row_low(p, w.row);
       float m = -INFINITY, l = 0.f;  // reference (raw scores) and sum
       bool nonfinite = false;
-      const int step = NQ == 2 ? 1 : 2;
-      bool first = true;
-      for (int i = NQ == 2 ? 0 : j; ok && i < tiles; i += step, ++nj) {
-        const int t0 = w.row.start + (w.tile0 + i) * kTile;
-        ok = warp_wait(bar.sfull(j), nj & 1, abort, p.status);
+      const int steps = NQ * tiles;
+      for (int i = 0; i < steps; ++i) {
+        const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
+        const int t0 = w.row.start + (w.tile0 + tile) * kTile, t = t0 + half * kStep;
+        ok = warp_wait(bar.sfull(j, i & 1), phases >> (i & 1) & 1, abort, p.status);
+        phases ^= 1u << (i & 1);
         if (!ok) break;
         tmem_fence_after();
         const bool edge = edge_tile(w.row, low_all, t0);
         if (live_warp) {
-          // S is read twice, 64 columns at a time: a whole row does not fit in
-          // the registers beside the rest
-          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-          const bool masked = edge || __any_sync(0xffffffffu, low > t0);
-          if (masked)
+          const uint32_t at = ts + (i & 1) * kStep;
+          uint32_t s[kStep];
+          tmem_ld32(at, s);
+          tmem_ld32(at + 32, s + 32);
+          tmem_wait_ld();
+          if (edge || __any_sync(0xffffffffu, low > t)) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) seen[c] = live ? visible_word(p, w.row, w.b, node, low, t0 + 32 * c) : 0u;
-          auto load = [&](int h, uint32_t* s) {
-            tmem_ld32(ts + 64 * h, s);
-            tmem_ld32(ts + 64 * h + 32, s + 32);
-            tmem_wait_ld();
-            if (masked)
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t bits = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
 #pragma unroll
-              for (int x = 0; x < 64; ++x)
-                if (!(seen[2 * h + x / 32] >> (x % 32) & 1)) s[x] = 0xff800000u;  // -inf
-          };
-          uint32_t s[64];
+              for (int x = 0; x < 32; ++x)
+                if (!(bits >> x & 1)) s[32 * c + x] = 0xff800000u;  // -inf
+            }
+          }
           float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            load(1 - h, s);
+          for (int c = 0; c < kStep; c += 8)
 #pragma unroll
-            for (int c = 0; c < 64; ++c) top[c % 4] = fmaxf(top[c % 4], __uint_as_float(s[c]));
-          }
+            for (int x = 0; x < 4; ++x)
+              top[x] = fmaxf(top[x], fmaxf(__uint_as_float(s[c + 2 * x]), __uint_as_float(s[c + 2 * x + 1])));
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           const bool grow = live && mx * p.scale_log2 > m * p.scale_log2 + kLazyLog2;  // false for NaN, and -inf both
           if (__any_sync(0xffffffffu, grow)) {
@@ -525,61 +577,56 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             const float f = grow ? exp2f((m - m2) * p.scale_log2) : 1.f;  // 0 where m is -inf
             m = m2;
             l *= f;
-            if (!first) {
-              // the products that wrote O are done
-              ok = warp_wait(bar.pvdone(j), (nj & 1) ^ 1, abort, p.status);
+            if (i > 0) {
+              ok = taken(i + 1 & 1);
               tmem_fence_after();
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
-                tmem_ld32(to + 32 * c, o);
+                tmem_ld32(to + c, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                tmem_st32(to + 32 * c, o);
+                tmem_st32(to + c, o);
               }
             }
           }
           const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(base, base);
+          uint64_t sum[2] = {0, 0};
+          uint32_t pk[kStep / 2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (h == 1) load(1, s);  // the first half is still here
-            uint32_t pk[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float a = fast_exp2(fmaf(__uint_as_float(s[2 * x]), p.scale_log2, base));
-              const float b = fast_exp2(fmaf(__uint_as_float(s[2 * x + 1]), p.scale_log2, base));
-              sum[x & 1] += a;
-              sum[2 + (x & 1)] += b;
-              pk[x] = pack_bf16x2(a, b);
-            }
-            tmem_st32(ts + 32 * h, pk);
+          for (int x = 0; x < kStep / 2; ++x) {
+            uint32_t a, b;
+            unpack_b32x2(fma_f32x2(pack_b32x2(s[2 * x], s[2 * x + 1]), scale2, base2), a, b);
+            const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
+            sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
+            pk[x] = pack_bf16x2(ea, eb);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st32(at, pk);
+          uint32_t a, b;
+          unpack_b32x2(add_f32x2(sum[0], sum[1]), a, b);
+          l += __uint_as_float(a) + __uint_as_float(b);
           tmem_wait_st();
         }
         if (edge) {
           // V is in place; whether a drafted token in it had non-finite elements
-          const uint32_t v = n + i;
+          const uint32_t v = n + tile;
           ok = ok && warp_wait(bar.fixed(v), v / L::kFix & 1, abort, p.status);
           nonfinite |= (bad[2 * (v % L::kFix)] | bad[2 * (v % L::kFix) + 1]) != 0;
         }
         if (!ok) break;
-        first = false;
         tmem_fence_before();
-        mbar_arrive(bar.pready(j));
+        warp_arrive(bar.pready(j, i & 1));
       }
       n += tiles;
       if (!ok) break;
-      if (!first) ok = warp_wait(bar.pvdone(j), (nj & 1) ^ 1, abort, p.status);
-      if (!ok) break;
+      if (!(ok = taken(steps + 1 & 1))) break;
       tmem_fence_after();
 
       // the segment's state: m in log2 units
       float ml = m == -INFINITY ? -INFINITY : m * p.scale_log2;
       float f0 = 1.f, f1 = 0.f;  // factors of O (of both streams' O)
-      bool has1 = false;
       if (NQ == 1) {
         tmem_fence_before();
         stats[j * 128 + row] = make_float2(ml, l);
@@ -593,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         f0 = exp2f(a.x - top);
         f1 = exp2f(b.x - top);
         l = a.y * f0 + b.y * f1;
-        has1 = tiles > 1;
       }
       const bool whole = w.whole();
       float* const slot = whole ? nullptr : tree_slot(p, w.slot);
@@ -616,14 +662,14 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             tmem_ld32(to + c, a);
           } else {
             tmem_ld32(t + c, a);
-            if (has1) tmem_ld32(t + D + c, b);
+            tmem_ld32(t + D + c, b);
           }
           tmem_wait_ld();
           float o[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             o[x] = __uint_as_float(a[x]);
-            if (NQ == 1) o[x] = o[x] * f0 + (has1 ? __uint_as_float(b[x]) * f1 : 0.f);
+            if (NQ == 1) o[x] = o[x] * f0 + __uint_as_float(b[x]) * f1;
             o[x] *= inv;
           }
           if (mine && slot) {
@@ -728,12 +774,15 @@ bool fast_tree_supported(const TreeParams& p) {
   return kv_rows(p) < (1ull << 31) && (uint64_t)p.batch * p.q_heads * p.nodes + 256 < (1ull << 31);
 }
 
-cudaError_t launch_fast_tree(TreeParams& p, int sms, cudaStream_t s) {
-  const int R = p.group * p.nodes;
+void plan_fast_tree(TreeParams& p, int sms) {
   p.rows_per_unit = tree_fast_rows(p.group, p.nodes);
-  p.units_per_head = (R + p.rows_per_unit - 1) / p.rows_per_unit;
-  p.tile = kTile;
+  p.units_per_head = (p.group * p.nodes + p.rows_per_unit - 1) / p.rows_per_unit;
+  p.tile_log2 = kTreeFastTileLog2;
   p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
+}
+
+cudaError_t launch_fast_tree(const TreeParams& p, cudaStream_t s) {
+  const int R = p.group * p.nodes;
   int box = kTile;
   if (p.cache.block_table)  // the largest power of two that divides a page
     while (p.cache.page_size % box != 0) box /= 2;

@@ -15,7 +15,7 @@
 namespace ol {
 namespace {
 
-constexpr int RB = kTreeGenRows, TB = kTreeGenTile;
+constexpr int RB = kTreeGenRows, TB = 1 << kTreeGenTileLog2;
 constexpr int kGenThreads = 128;
 constexpr int kPStride = RB + 4;  // P is kept [token][row]
 
@@ -228,50 +228,98 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
 // ------------------------------------------------------------------- the merge
 
 // CTA x merges the unit whose tokens reach from CTA x's share into the next
-// one's (if there is one and it began in share x): rows [32 y, 32 y + 32),
-// lane = row, warps over groups of four dimensions.
+// one's (if there is one and it began in share x): rows [ROWS y, ROWS (y + 1)).
 //   M = max m_s, L = sum l_s 2^(m_s - M), y = sum o_s 2^(m_s - M) / L
+// Thread = (row, group of four dimensions): the slots' layout keeps the rows of
+// a group together. The weights of 32 segments at a time are in shared memory.
+// Bound by reading the partials (L2). ROWS 32 for many units, each cut once or
+// twice; 8 where few units are cut into many segments, to have more CTAs.
 constexpr int kMergeThreads = 256;
+constexpr int kMergeSegs = 32;
+template <int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  pdl_wait();
+  constexpr int kLanes = kMergeThreads / ROWS;    // threads of a row
+  constexpr int kGroups = 64 / kLanes;            // groups of four dimensions per thread, for D up to 256
+  __shared__ float weight[kMergeSegs][ROWS];
+  __shared__ float part[kLanes][ROWS];
   pdl_launch_dependents();
+  // lengths and counts were there before the kernel ahead started its work
   TreeWalk w(p);
   const int first = blockIdx.x;  // the unit's shares are first .. last
   int last;
-  if (!w.split_after(p, last)) return;
-  const int RU = p.rows_per_unit, D = p.head_dim;
-  const int row = blockIdx.y * 32 + lane;  // of the unit
-  const int r = w.qg * RU + row;
-  if (row >= RU || r >= p.group * p.nodes || r % p.nodes >= w.row.count) return;
+  const bool some = w.split_after(p, last);
+  pdl_wait();
+  if (!some) return;
+  const int RU = p.rows_per_unit, D = p.head_dim, D4 = (D + 3) / 4;
+  const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS;
+  const int place = blockIdx.y * ROWS + lr;  // row of the unit
+  const int r = w.qg * RU + place;
+  const bool mine = place < RU && r < p.group * p.nodes && r % p.nodes < w.row.count;
+  const int at = mine ? place : 0;
   // the later shares begin with the unit's segment
   auto slot_of = [&](int c) { return tree_slot(p, c == first ? w.slot : 2 * c); };
   float M = -INFINITY;
-  for (int c = first; c <= last; ++c) M = fmaxf(M, __ldcg(slot_of(c) + row));
+  for (int c = first + lane; c <= last; c += kLanes) M = fmaxf(M, slot_of(c)[at]);
+  part[lane][lr] = M;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) M = fmaxf(M, part[i][lr]);
   const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f;
-  for (int c = first; c <= last; ++c) {
-    const float* const s = slot_of(c);
-    L += __ldcg(s + RU + row) * exp2f(__ldcg(s + row) - base);
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t at = tree_out_row(p, w.b, w.g, r) * D;
-  for (int d4 = warp; d4 * 4 < D; d4 += kMergeThreads / 32) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = first; c <= last; ++c) {
-      const float* const s = slot_of(c);
-      const float f = exp2f(__ldcg(s + row) - base);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(s + 2 * RU) + (size_t)d4 * RU + row);
-      acc.x += o.x * f;
-      acc.y += o.y * f;
-      acc.z += o.z * f;
-      acc.w += o.w * f;
-    }
-    const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  float4 acc[kGroups];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (d4 * 4 + j < D) store_out(p.out, p.out_dtype, at + d4 * 4 + j, v[j]);
+  for (int i = 0; i < kGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c0 = first; c0 <= last; c0 += kMergeSegs) {
+    const int n = min(kMergeSegs, last - c0 + 1);
+    __syncthreads();
+    for (int i = lane; i < n; i += kLanes) {
+      const float* const s = slot_of(c0 + i);
+      const float f = exp2f(s[at] - base);
+      weight[i][lr] = f;
+      L += s[RU + at] * f;
+    }
+    __syncthreads();
+    if (mine)
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float f = weight[i][lr];
+        const float4* const o = reinterpret_cast<const float4*>(slot_of(c0 + i) + 2 * RU) + at;
+#pragma unroll
+        for (int k = 0; k < kGroups; ++k) {
+          const int d4 = lane + k * kLanes;
+          if (d4 >= D4) break;
+          const float4 v = o[(size_t)d4 * RU];
+          acc[k].x += v.x * f;
+          acc[k].y += v.y * f;
+          acc[k].z += v.z * f;
+          acc[k].w += v.w * f;
+        }
+      }
+  }
+  __syncthreads();
+  part[lane][lr] = L;
+  __syncthreads();
+  if (!mine) return;
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) L += part[i][lr];
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const size_t out = tree_out_row(p, w.b, w.g, r) * D;
+#pragma unroll
+  for (int k = 0; k < kGroups; ++k) {
+    const int d = (lane + k * kLanes) * 4;
+    if (d >= D) break;
+    const float v[4] = {acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv};
+    if (D % 4 != 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (d + j < D) store_out(p.out, p.out_dtype, out + d + j, v[j]);
+    } else if (p.out_dtype == OL_F32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + out + d) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + out + d) =
+          make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
   }
 }
 
@@ -322,11 +370,14 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const KeepParam
 
 }  // namespace
 
-cudaError_t launch_generic_tree(TreeParams& p, int sms, cudaStream_t s) {
+void plan_generic_tree(TreeParams& p, int sms) {
   p.rows_per_unit = RB;
   p.units_per_head = (p.group * p.nodes + RB - 1) / RB;
-  p.tile = TB;
+  p.tile_log2 = kTreeGenTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
+}
+
+cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
   const int nc = (p.head_dim + 63) / 64;
   if (p.dtype == OL_F32)
     return nc == 1 ? launch_tree<float, 1>(p, s)
@@ -341,7 +392,9 @@ cudaError_t launch_generic_tree(TreeParams& p, int sms, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
-  return launch_pdl(tree_merge_kernel, dim3(p.nctas, (rows + 31) / 32), dim3(kMergeThreads), 0, s, p);
+  const bool few = (long long)p.batch * p.kv_heads * p.units_per_head * 4 <= p.nctas;
+  if (few) return launch_pdl(tree_merge_kernel<8>, dim3(p.nctas, (rows + 7) / 8), dim3(kMergeThreads), 0, s, p);
+  return launch_pdl(tree_merge_kernel<32>, dim3(p.nctas, (rows + 31) / 32), dim3(kMergeThreads), 0, s, p);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {

@@ -64,14 +64,14 @@ __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
     set_status(p.status, OL_DEVICE_GUARD);
     c = c < 0 ? 0 : min(min(c, p.nodes), n);
   }
-  return tree_row(n, c, p.window, p.tile);
+  return tree_row(n, c, p.window, p.tile_log2);
 }
 
 // The tiles of all units, in the order (row, kv head, row group of the unit,
-// tile), are cut into n = min(CTAs, T) contiguous shares of equal size, none of
-// them empty: CTA c has tiles [c T / n, (c + 1) T / n). A walk gives the CTA its share's segments,
-// one unit's tiles [tile0, tile1) each. A segment that is not its whole unit
-// puts its state into a slot; a share has at most two of them, its first and
+// tile), are cut into n = min(CTAs, T) contiguous shares, none of them empty, of
+// T / n tiles, the first T % n of one more. A walk gives the CTA its share's
+// segments, one unit's tiles [tile0, tile1) each. A segment that is not its whole
+// unit puts its state into a slot; a share has at most two of them, its first and
 // its last segment: slot 2 c for the one that starts the share, else 2 c + 1.
 // Equal shares keep ragged batches balanced to one tile per SM.
 // The constructor is for whole warps; next() may be called by single threads.
@@ -80,54 +80,55 @@ struct TreeWalk {
   TreeRow row;
   int tile0, tile1;
   int slot;
-  long long at, end;       // next tile of the share; its end
-  long long share, total;  // its first tile; all tiles
-  long long shares;
+  int at, end;           // next tile of the share; its end
+  int share, total;      // its first tile; all tiles
+  int each, more;        // tiles of a share; shares of one more
+  int first_nt;          // tiles of row `lane` of the first 32 rows
 
   __device__ __forceinline__ explicit TreeWalk(const TreeParams& p) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, c = blockIdx.x;
     total = 0;
     for (int base = 0; base < p.batch; base += 32) {
       int nt = base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) nt += __shfl_xor_sync(0xffffffffu, nt, o);
-      total += nt;
+      if (base == 0) first_nt = nt;
+      total += __reduce_add_sync(0xffffffffu, nt);
     }
     total *= p.kv_heads * p.units_per_head;
-    shares = total < gridDim.x ? total : gridDim.x;
-    at = share = end = 0;
-    if (blockIdx.x < shares) {
-      at = share = blockIdx.x * total / shares;
-      end = (blockIdx.x + 1) * total / shares;
+    const int shares = min(total, (int)gridDim.x);
+    at = end = share = each = more = tile0 = slot = 0;
+    if (c < shares) {
+      each = total / shares;
+      more = total - each * shares;
+      at = share = c * each + min(c, more);
+      end = share + each + (c < more);
     }
-    tile0 = slot = 0;
     tile1 = at < end ? locate(p, at) : 0;
   }
 
   // Finds the unit of tile x (x < total); returns the tile's index in it.
-  __device__ __forceinline__ int locate(const TreeParams& p, long long x) {
+  __device__ __forceinline__ int locate(const TreeParams& p, int x) {
     const int lane = threadIdx.x & 31;
     const int per_row = p.kv_heads * p.units_per_head;
     b = g = qg = 0;
     row = TreeRow{0, 0, 0, 0, 1};
     for (int base = 0; base < p.batch; base += 32) {
-      const int nt = base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
+      const int nt = base == 0 ? first_nt : base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
       int incl = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      const long long all = (long long)__shfl_sync(0xffffffffu, incl, 31) * per_row;
+      const int all = __shfl_sync(0xffffffffu, incl, 31) * per_row;
       if (x < all) {
-        const int src = __ffs(__ballot_sync(0xffffffffu, x < (long long)incl * per_row)) - 1;
-        x -= (long long)__shfl_sync(0xffffffffu, incl - nt, src) * per_row;
+        const int src = __ffs(__ballot_sync(0xffffffffu, x < incl * per_row)) - 1;
+        x -= __shfl_sync(0xffffffffu, incl - nt, src) * per_row;
         b = base + src;
         row = read_tree_row(p, b);
-        const int unit = (int)(x / row.ntiles);
+        const int unit = x / row.ntiles;
         g = unit / p.units_per_head;
-        qg = unit % p.units_per_head;
-        return (int)(x % row.ntiles);
+        qg = unit - g * p.units_per_head;
+        return x - unit * row.ntiles;
       }
       x -= all;
     }
@@ -152,8 +153,7 @@ struct TreeWalk {
     }
     tile0 = tile1;
     slot = 2 * blockIdx.x + (at == share ? 0 : 1);
-    const long long left = end - at;
-    tile1 = left < row.ntiles - tile0 ? tile0 + (int)left : row.ntiles;
+    tile1 = min(row.ntiles, tile0 + (end - at));
     at += tile1 - tile0;
     return true;
   }
@@ -164,10 +164,11 @@ struct TreeWalk {
   // end. It is found, `slot` is that of its first segment and `last` its last share.
   __device__ __forceinline__ bool split_after(const TreeParams& p, int& last) {
     if (at >= end || end == total) return false;
-    const long long begin = end - 1 - locate(p, end - 1), unit_end = begin + row.ntiles;
-    if (begin < share || unit_end == end) return false;
+    const int begin = end - 1 - locate(p, end - 1), back = begin + row.ntiles - 1;  // the unit's first and last tile
+    if (begin < share || back < end) return false;
     slot = 2 * blockIdx.x + (begin == share ? 0 : 1);
-    last = (int)((unit_end * shares - 1) / total);
+    const int big = more * (each + 1);  // tiles of the shares of one more
+    last = back < big ? back / (each + 1) : more + (back - big) / each;
     return true;
   }
 };
