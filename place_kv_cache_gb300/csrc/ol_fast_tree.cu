@@ -16,17 +16,19 @@
 //   S = Q K^T      128 x 64 x D, both operands in shared memory, S in TMEM
 //   P = 2^(S - m)  registers, bf16, back to TMEM over S
 //   O += P V       128 x D x 64, P from TMEM, V from shared memory, O in TMEM
-// m is a reference that follows the row's maximum only when that has grown by
-// more than 2^8, so O is rescaled rarely. Sums and O are fp32; P is rounded to
-// bf16, the type its product with V takes: as much as the output's own rounding.
+// m is a reference near the row's maximum: it is set from a segment's first
+// scores and again only when a step's weights sum to more than 2^10 (fp32 and
+// bf16 carry such weights as exactly as smaller ones), so the maximum is looked
+// for, and O rescaled, rarely. Sums and O are fp32; P is rounded to bf16, the
+// type its product with V takes: as much as the output's own rounding.
 //
 // Warps: 0 producer (TMA; lanes share the boxes of a tile: pages of 16 tokens
-// are boxes of 2 KB), 1 MMA issue, 2-3 fixers, 4-7 and 8-11 the streams. The
-// fixers pass every V tile on and, in tiles that hold drafted tokens or end the
-// row, zero the rows outside the row's tokens and the non-finite elements: a
-// product with P = 0 must not see them. Where a stream meets such an element
-// in a drafted token, it adds the non-finite values of the tokens that its row
-// sees to the outputs at the end (rare, unhurried).
+// are boxes of 2 KB), 1 and 2 MMA issue for a stream each, 3 fixer, 4-7 and 8-11
+// the streams. The fixer passes every V tile on and, in tiles that hold drafted
+// tokens or end the row, zeroes the rows outside the row's tokens and the
+// non-finite elements: a product with P = 0 must not see them. Where a stream
+// meets such an element in a drafted token, it adds the non-finite values of the
+// tokens that its row sees to the outputs at the end (rare, unhurried).
 //
 // Bounds: 4 * D bytes per token and kv head against 4 * D * rows flops: the
 // memory up to 256 rows, then the tensor cores.
@@ -38,25 +40,26 @@ namespace {
 constexpr int kTile = 1 << kTreeFastTileLog2;
 constexpr int kStep = kTile / 2;  // tokens of a step
 constexpr int kThreads = 384;
-constexpr float kLazyLog2 = 8.f;
+constexpr float kGrown = 1024.f;  // a step's sum of weights that makes a row look for its maximum
 
 template <int D, int NQ>
 struct Lay {
   static constexpr int kHalves = D / 64;                // 64-element (128-byte) column blocks
   static constexpr int kTileBytes = kTile * D * 2;      // K, V or Q tile
-  static constexpr int kSlots = D == 128 ? (NQ == 1 ? 6 : 5) : 12;
-  // V tiles on their way: V of tile n + kFix comes into the ring only after a
-  // slot of tile n or n + 1 is free, which is after V of tile n was taken
-  static constexpr int kFix = (kSlots + 1) / 2;
+  // K and V have rings of their own: whoever waits for a slot sees each of its
+  // phases. K's slots are free earlier (after S) than V's.
+  static constexpr int kK = D == 128 ? (NQ == 1 ? 3 : 2) : 6;
+  static constexpr int kV = D == 128 ? 3 : 6;
+  static constexpr int kSlots = kK + kV;                // K's, then V's
   static constexpr int kQ = 0;
   static constexpr int kRing = NQ * kTileBytes;
   static constexpr int kStats = kRing + kSlots * kTileBytes;  // float2 [2][128]: streams' (m, l)
   static constexpr int kBars = kStats + 2 * 128 * 8;
-  // full, empty [kSlots], fixed [kFix]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain, join
-  static constexpr int kNumBars = 2 * kSlots + kFix + 16;
-  static constexpr int kBad = kBars + kNumBars * 8;     // uint32 [kFix + 1][2]
-  static constexpr int kMisc = kBad + (kFix + 1) * 8;   // TMEM address, abort flag
-  static constexpr int kTotal = kMisc + 16;
+  // full, empty [kSlots], fixed [kV]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain[2], join
+  static constexpr int kNumBars = 2 * kSlots + kV + 17;
+  static constexpr int kBad = kBars + kNumBars * 8;     // uint32 [kV + 2]
+  static constexpr int kMisc = kBad + (kV + 2) * 4;   // TMEM address, abort flag
+  static constexpr int kTotal = kMisc + 8;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
 
@@ -90,7 +93,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define OL_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), "=r"(x[i + 6]), "=r"(x[i + 7])
@@ -102,6 +104,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
       : OL_R8(x, 0), OL_R8(x, 8), OL_R8(x, 16), OL_R8(x, 24)
       : "r"(addr));
+}
+// Waits for the loads; x are registers that a load fills (so that no use of them moves ahead of the wait).
+#define OL_U8(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7])
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U8(x, 0), OL_U8(x, 8), OL_U8(x, 16), OL_U8(x, 24)::"memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
   asm volatile(
@@ -153,14 +160,14 @@ struct Bars {
   uint32_t at;
   __device__ uint32_t full(int s) const { return at + 8 * s; }
   __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
-  __device__ uint32_t fixed(uint32_t n) const { return at + 8 * (2 * L::kSlots + n % L::kFix); }  // of tile n
-  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kFix); }
+  __device__ uint32_t fixed(int v) const { return at + 8 * (2 * L::kSlots - L::kK + v); }  // of V's slot v
+  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kV); }
   __device__ uint32_t qempty() const { return qfull() + 8; }
   __device__ uint32_t sfull(int j, int b) const { return qfull() + 16 + 16 * j + 8 * b; }  // S buffer b of stream j
   __device__ uint32_t pready(int j, int b) const { return qfull() + 48 + 16 * j + 8 * b; }  // P in its place
   __device__ uint32_t pvdone(int j, int b) const { return qfull() + 80 + 16 * j + 8 * b; }  // and taken
-  __device__ uint32_t drain() const { return qfull() + 112; }
-  __device__ uint32_t join() const { return qfull() + 120; }
+  __device__ uint32_t drain(int j) const { return qfull() + 112 + 8 * j; }
+  __device__ uint32_t join() const { return qfull() + 128; }
 };
 
 // A wait that ends: after about two seconds, or once another warp has given up,
@@ -190,11 +197,18 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
-// Ring places of K (which = 0) and V (1) of the CTA's n-th tile.
-template <int SLOTS>
-__device__ __forceinline__ int ring_slot(uint32_t n, int which) { return (int)((2 * n + which) % SLOTS); }
-template <int SLOTS>
-__device__ __forceinline__ uint32_t ring_phase(uint32_t n, int which) { return ((2 * n + which) / SLOTS) & 1; }
+// Walks the slots [first, first + count) of a ring, tile after tile.
+struct Cursor {
+  int slot, first, end;
+  uint32_t phase = 0;
+  __device__ __forceinline__ Cursor(int f, int count) : slot(f), first(f), end(f + count) {}
+  __device__ __forceinline__ void next() {
+    if (++slot == end) {
+      slot = first;
+      phase ^= 1;
+    }
+  }
+};
 
 // Lowest token of the row that any node may see.
 __device__ __forceinline__ int row_low(const TreeParams& p, const TreeRow& r) {
@@ -300,11 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     prefetch_tensormap(&maps.kv);
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(bar.full(s), 1);
-      mbar_init(bar.empty(s), 1);
+      mbar_init(bar.empty(s), 2);
     }
-    for (int x = 0; x < L::kFix; ++x) mbar_init(bar.fixed(x), 2);
+    for (int v = L::kK; v < L::kSlots; ++v) mbar_init(bar.fixed(v), 1);
     mbar_init(bar.qfull(), 1);
-    mbar_init(bar.qempty(), 1);
+    mbar_init(bar.qempty(), 2);
     for (int j = 0; j < 2; ++j) {
       mbar_init(bar.sfull(j, 0), 1);
       mbar_init(bar.sfull(j, 1), 1);
@@ -312,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       mbar_init(bar.pready(j, 1), 4);
       mbar_init(bar.pvdone(j, 0), 1);
       mbar_init(bar.pvdone(j, 1), 1);
+      mbar_init(bar.drain(j), 1);
     }
-    mbar_init(bar.drain(), 1);
     mbar_init(bar.join(), 8);
     fence_mbar_init();
     *abort = 0;
@@ -335,162 +349,208 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     // ---------------------------------------------------------------- producer
     const uint64_t policy = keep_l2 ? policy_evict_normal() : policy_evict_first();
     const uint64_t keep = policy_evict_normal();
-    uint32_t n = 0, seg = 0, issued = 0;
-    bool ok = true;
-    auto load = [&](int which, int t0) {  // K (0) or V (1) of the tokens from t0
-      const int s = ring_slot<L::kSlots>(n, which);
-      const uint32_t ph = ring_phase<L::kSlots>(n, which);
-      if (!warp_wait(bar.empty(s), ph ^ 1, abort, p.status)) return false;
-      issued = 2 * n + which + 1;
-      const int low = row_low(p, w.row);
-      const int first = max(low - t0, 0) / box, last = (min(w.row.len - t0, kTile) + box - 1) / box;  // boxes
-      if (lane == 0) mbar_arrive_expect_tx(bar.full(s), (uint32_t)(last - first) * box * D * 2);
-      __syncwarp();
-      for (int i = lane; i < (last - first) * L::kHalves; i += 32) {
-        const int x = first + i / L::kHalves, h = i % L::kHalves;
-        const int t = t0 + x * box;
-        int y;
-        if (PAGED) {
-          int page = p.cache.block_table[(size_t)w.b * p.cache.max_pages + t / p.cache.page_size];
-          if (page < 0 || page >= p.cache.num_pages) {
-            set_status(p.status, OL_DEVICE_GUARD);
-            page = 0;
-          }
-          y = ((which * p.cache.num_pages + page) * p.kv_heads + w.g) * p.cache.page_size + t % p.cache.page_size;
-        } else {
-          y = ((which * p.batch + w.b) * p.kv_heads + w.g) * p.cache.capacity + t;
+    // One tile ahead: its boxes and this lane's page are known (the table's entry
+    // on its way) before the ring has room for it. Lane = (box, column block).
+    struct Tile {
+      int t0, first, last;  // token; boxes
+      int y;                // cache row of this lane's box in plane K
+      int q;                // row of q of a segment's first tile, else -1
+    } cur = {}, nxt = {};
+    const int x = lane / L::kHalves, h = lane % L::kHalves;
+    const int v_rows = (PAGED ? p.cache.num_pages * p.cache.page_size : p.batch * p.cache.capacity) * p.kv_heads;
+    int tile;
+    auto fetch = [&](Tile& t) {
+      t.q = -1;
+      if (tile == w.tile1) {
+        if (!w.next(p)) return false;
+        tile = w.tile0;
+        t.q = (int)tree_out_row(p, w.b, w.g, w.qg * p.rows_per_unit);
+      }
+      t.t0 = w.row.start + tile++ * kTile;
+      t.first = max(row_low(p, w.row) - t.t0, 0) / box;
+      t.last = (min(w.row.len - t.t0, kTile) + box - 1) / box;
+      const int at = t.t0 + x * box;
+      if (!PAGED) {
+        t.y = (w.b * p.kv_heads + w.g) * p.cache.capacity + at;
+      } else if (x >= t.first && x < t.last) {
+        int page = p.cache.block_table[(size_t)w.b * p.cache.max_pages + at / p.cache.page_size];
+        if (page < 0 || page >= p.cache.num_pages) {
+          set_status(p.status, OL_DEVICE_GUARD);
+          page = 0;
         }
-        tma_load_2d(sa + L::kRing + s * L::kTileBytes + h * (kTile * 128) + x * box * 128, &maps.kv, h * 64, y,
-                    bar.full(s), policy);
+        t.y = (page * p.kv_heads + w.g) * p.cache.page_size + at % p.cache.page_size;
       }
       return true;
     };
-    while (ok && w.next(p)) {
-      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
-        const int t0 = w.row.start + tile * kTile;
-        ok = load(0, t0);
-        if (ok && tile == w.tile0) {
-          // the last segment's queries are read
-          ok = warp_wait(bar.qempty(), (seg & 1) ^ 1, abort, p.status);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(bar.qfull(), (uint32_t)NQ * qbox * D * 2);
-            const int y = (int)tree_out_row(p, w.b, w.g, w.qg * p.rows_per_unit);
-            for (int j = 0; j < NQ; ++j)
-              for (int h = 0; h < L::kHalves; ++h)
-                tma_load_2d(sa + L::kQ + j * L::kTileBytes + h * (kTile * 128), &maps.q, h * 64, y + j * 128,
-                            bar.qfull(), keep);
-          }
-          if (ok) ++seg;
+    Cursor k(0, L::kK), v(L::kK, L::kV);
+    uint32_t seg = 0;
+    bool ok = true;
+    auto load = [&](Cursor& c, int y) {
+      if (!warp_wait(bar.empty(c.slot), c.phase ^ 1, abort, p.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(bar.full(c.slot), (uint32_t)(cur.last - cur.first) * box * D * 2);
+      __syncwarp();
+      if (x >= cur.first && x < cur.last)
+        tma_load_2d(sa + L::kRing + c.slot * L::kTileBytes + h * (kTile * 128) + x * box * 128, &maps.kv, h * 64, y,
+                    bar.full(c.slot), policy);
+      c.next();
+      return true;
+    };
+    tile = w.tile1;  // the first segment begins here
+    bool more = fetch(nxt);
+    while (ok && more) {
+      cur = nxt;
+      more = fetch(nxt);
+      ok = load(k, cur.y);
+      if (ok && cur.q >= 0) {
+        ok = warp_wait(bar.qempty(), (seg & 1) ^ 1, abort, p.status);  // the last segment's queries are read
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(bar.qfull(), (uint32_t)NQ * qbox * D * 2);
+          for (int j = 0; j < NQ; ++j)
+            for (int c = 0; c < L::kHalves; ++c)
+              tma_load_2d(sa + L::kQ + j * L::kTileBytes + c * (kTile * 128), &maps.q, c * 64, cur.q + j * 128,
+                          bar.qfull(), keep);
         }
-        if (ok) ok = load(1, t0);
+        if (ok) ++seg;
       }
+      ok = ok && load(v, cur.y + v_rows);
     }
     if (!ok) {  // copies in flight end before the CTA does
       if (seg) mbar_wait_bounded(bar.qfull(), (seg - 1) & 1);
-      for (uint32_t i = issued > (uint32_t)L::kSlots ? issued - L::kSlots : 0; i < issued; ++i)
-        mbar_wait_bounded(bar.full(i % L::kSlots), (i / L::kSlots) & 1);
+      for (Cursor* c : {&k, &v})  // a slot's last load: of this round before the cursor, else of the one before
+        for (int i = c->first; i < c->end; ++i) mbar_wait_bounded(bar.full(i), i < c->slot ? c->phase : c->phase ^ 1);
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // --------------------------------------------------------------- MMA issue
-    // The whole warp walks and waits, so that what the products are given stays
-    // in uniform registers; one elected lane issues them. (With lane 0 alone in
-    // the loop, each product waited for its operands: 160 cycles apiece.)
+    // A warp per stream. The whole warp walks and waits, so that what the
+    // products are given stays in uniform registers; one elected lane issues
+    // them. (One warp for both streams, at some 1500 cycles a step of waits and
+    // addresses, left the tensor core idle half of the time; lane 0 alone in the
+    // loop, 160 cycles a product for its operands.)
     constexpr uint32_t kDescS = mma_desc(kStep, false), kDescO = mma_desc(D, true);
+    const int j = uniform(warp) - 1;
     const uint32_t tm = uniform(tmem), base = uniform(sa);
-    uint32_t n = 0, seg = 0;  // tiles; segments
-    uint32_t phases = 0;      // of the streams' P buffers, a bit each
+    const uint32_t ts = tm + j * 128, to = tm + 256 + j * D;
+    const uint64_t q = smem_desc(base + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, 16, 1024);
+    Cursor k(0, L::kK), v(L::kK, L::kV);
+    uint32_t seg = 0;         // segments
+    uint32_t pphase = 0;      // of the P buffers, a bit each
     bool ok = true;
+    // S into buffer b from the given half of K
+    auto scores = [&](int half, int b) {
+      if (elect_one()) {
+        const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes + half * (kStep * 128), 16, 1024);
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          constexpr uint32_t kBlock = kTile * 128 / 16, kK = 2;  // column block, 16 elements; in 16 bytes
+          mma_ss(ts + b * kStep, q + (x / 4 * kBlock + x % 4 * kK), kd + (x / 4 * kBlock + x % 4 * kK), kDescS, x > 0);
+        }
+        mma_commit(bar.sfull(j, b));
+      }
+    };
+    auto k_wait = [&] { return warp_wait(bar.full(k.slot), k.phase, abort, p.status); };
+    auto k_read = [&](bool last) {  // this stream's reads of K (of Q) are issued
+      if (elect_one()) {
+        mma_commit(bar.empty(k.slot));
+        if (last) mma_commit(bar.qempty());
+      }
+      k.next();
+    };
+    // O += P V with P of buffer b and the given half of V
+    auto sums = [&](int half, int b, bool first, bool wait_v, bool last_of_v) {
+      if (!warp_wait(bar.pready(j, b), pphase >> b & 1, abort, p.status)) return false;
+      pphase ^= 1u << b;
+      if (wait_v && !warp_wait(bar.fixed(v.slot), v.phase, abort, p.status)) return false;
+      tmem_fence_after();
+      if (elect_one()) {
+        const uint64_t vd =
+            smem_desc(base + L::kRing + v.slot * L::kTileBytes + half * (kStep * 128), kTile * 128, 1024);
+#pragma unroll
+        for (int x = 0; x < kStep / 16; ++x) {
+          if (x == 0)
+            mma_ts(to, ts + b * kStep, vd, kDescO, !first);
+          else
+            mma_ts(to, ts + b * kStep + x * 8, vd + x * (2048 / 16), kDescO, true);
+        }
+        mma_commit(bar.pvdone(j, b));
+        if (last_of_v) mma_commit(bar.empty(v.slot));
+      }
+      if (last_of_v) v.next();
+      return true;
+    };
     while (ok && w.next(p)) {
       const int tiles = uniform(w.tile1 - w.tile0);
-      const int streams = uniform(unit_streams<NQ>(p, w)), steps = NQ * tiles;
       ok = warp_wait(bar.qfull(), seg & 1, abort, p.status);
       ++seg;
-      // S of the segment's step i for stream j: tile i and half j, or (NQ = 2) tile i / 2 and half i % 2
-      auto scores = [&](int i, int j) {
-        const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
-        const int s = ring_slot<L::kSlots>(n + tile, 0);
-        if (half == 0 && (NQ == 1 || j == 0))
-          if (!warp_wait(bar.full(s), ring_phase<L::kSlots>(n + tile, 0), abort, p.status)) return false;
-        if (elect_one()) {
-          const uint64_t q = smem_desc(base + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, 16, 1024);
-          const uint64_t k = smem_desc(base + L::kRing + s * L::kTileBytes + half * (kStep * 128), 16, 1024);
-          const uint32_t to = tm + j * 128 + (i & 1) * kStep;
-#pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
-            constexpr uint32_t kBlock = kTile * 128 / 16, kK = 2;  // column block, 16 elements; in 16 bytes
-            mma_ss(to, q + (x / 4 * kBlock + x % 4 * kK), k + (x / 4 * kBlock + x % 4 * kK), kDescS, x > 0);
-          }
-          mma_commit(bar.sfull(j, i & 1));
-          if (half == 1 && j == streams - 1) {  // K is read
-            mma_commit(bar.empty(s));
-            if (tile == tiles - 1) mma_commit(bar.qempty());
+      if (NQ == 2 && j >= unit_streams<NQ>(p, w)) {
+        // nothing to do but to release what the other stream uses
+        for (int i = 0; ok && i < tiles; ++i) {
+          ok = k_wait();
+          if (ok) warp_arrive(bar.empty(k.slot));
+          ok = ok && warp_wait(bar.fixed(v.slot), v.phase, abort, p.status);
+          if (ok) warp_arrive(bar.empty(v.slot));
+          k.next();
+          v.next();
+        }
+        if (ok) warp_arrive(bar.qempty());
+      } else if (NQ == 2) {
+        ok = ok && k_wait();
+        if (ok) {
+          scores(0, 0);
+          scores(1, 1);
+          k_read(tiles == 1);
+        }
+        for (int i = 0; ok && i < tiles; ++i) {
+          const bool more = i + 1 < tiles;
+          ok = sums(0, 0, i == 0, true, false);
+          if (ok && more && (ok = k_wait())) scores(0, 0);
+          ok = ok && sums(1, 1, false, false, true);
+          if (ok && more) {
+            scores(1, 1);
+            k_read(i + 2 == tiles);
           }
         }
-        __syncwarp();
-        return true;
-      };
-      auto sums = [&](int i, int j) {
-        const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
-        const int s = ring_slot<L::kSlots>(n + tile, 1);
-        const int buf = 2 * j + (i & 1);
-        if (!warp_wait(bar.pready(j, i & 1), phases >> buf & 1, abort, p.status)) return false;
-        phases ^= 1u << buf;
-        if (half == 0 && (NQ == 1 || j == 0))
-          if (!warp_wait(bar.fixed(n + tile), (n + tile) / L::kFix & 1, abort, p.status)) return false;
-        tmem_fence_after();
-        if (elect_one()) {
-          const uint64_t v = smem_desc(base + L::kRing + s * L::kTileBytes + half * (kStep * 128), kTile * 128, 1024);
-          const uint32_t to = tm + 256 + j * D, from = tm + j * 128 + (i & 1) * kStep;
-#pragma unroll
-          for (int x = 0; x < kStep / 16; ++x) {
-            if (x == 0)
-              mma_ts(to, from, v, kDescO, i > 0);
-            else
-              mma_ts(to, from + x * 8, v + x * (2048 / 16), kDescO, true);
+      } else {
+        for (int i = 0; ok && i < 2 && i < tiles; ++i)
+          if ((ok = k_wait())) {
+            scores(j, i);
+            k_read(i + 1 == tiles);
           }
-          mma_commit(bar.pvdone(j, i & 1));
-          if (half == 1 && j == streams - 1) mma_commit(bar.empty(s));  // V is read
+        for (int i = 0; ok && i < tiles; ++i) {
+          ok = sums(j, i & 1, i == 0, true, true);
+          if (ok && i + 2 < tiles && (ok = k_wait())) {
+            scores(j, i & 1);
+            k_read(i + 3 == tiles);
+          }
         }
-        __syncwarp();
-        return true;
-      };
-      for (int i = 0; ok && i < 2 && i < steps; ++i)
-        for (int j = 0; ok && j < streams; ++j) ok = scores(i, j);
-      for (int i = 0; ok && i < steps; ++i)
-        for (int j = 0; ok && j < streams; ++j) {
-          ok = sums(i, j);
-          if (ok && i + 2 < steps) ok = scores(i + 2, j);
-        }
-      n += tiles;
+      }
     }
     if (!ok) {  // products in flight end before TMEM is freed
-      if (elect_one()) mma_commit(bar.drain());
-      __syncwarp();
-      mbar_wait_bounded(bar.drain(), 0);
+      if (elect_one()) mma_commit(bar.drain(j));
+      mbar_wait_bounded(bar.drain(j), 0);
     }
-  } else if (warp < 4) {
-    // ------------------------------------------------------------------ fixers
-    const int me = tid - 64;
-    uint32_t n = 0;
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------- fixer
+    Cursor v(L::kK, L::kV);
     bool ok = true;
     while (ok && w.next(p)) {
       const int low = row_low(p, w.row);
-      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
-        const int s = ring_slot<L::kSlots>(n, 1);
-        ok = warp_wait(bar.full(s), ring_phase<L::kSlots>(n, 1), abort, p.status);
+      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, v.next()) {
+        ok = warp_wait(bar.full(v.slot), v.phase, abort, p.status);
         const int t0 = w.row.start + tile * kTile;
         if (ok && edge_tile(w.row, low, t0)) {
-          uint8_t* const v = smem + L::kRing + s * L::kTileBytes;
-          bool found = false;
-          // 16-byte pieces: rows outside [low, len) become zeros, drafted rows lose non-finite elements
+          // 16-byte pieces, line after line of 128 bytes of each half: rows outside
+          // [low, len) become zeros, drafted rows lose non-finite elements
+          uint4* const at = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes) + lane;
           const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
-          for (int i = me; i < kTile * D / 8; i += 64) {
-            const int r = i / 8 % kTile;  // pieces of 128-byte lines, line after line of each half
-            uint4* const at = reinterpret_cast<uint4*>(v) + i;
+          bool found = false;
+#pragma unroll 4
+          for (int i = 0; i < kTile * D / 8; i += 32) {
+            const int r = (i + lane) / 8 % kTile;
             if (r < r_low || r >= r_end) {
-              *at = make_uint4(0, 0, 0, 0);
+              at[i] = make_uint4(0, 0, 0, 0);
             } else if (r >= r_tree) {
-              uint4 x = *at;
+              uint4 x = at[i];
               uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
               bool hit = false;
 #pragma unroll
@@ -498,15 +558,15 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
                 if ((e[c] & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u, hit = true;
                 if ((e[c] & 0x7f800000u) == 0x7f800000u) e[c] &= 0xffffu, hit = true;
               }
-              if (hit) *at = x;
+              if (hit) at[i] = x;
               found |= hit;
             }
           }
           const bool any = __any_sync(0xffffffffu, found);
-          if (lane == 0) bad[2 * (n % L::kFix) + warp - 2] = any;
+          if (lane == 0) bad[v.slot - L::kK] = any;
           fence_proxy_async_smem();
         }
-        if (ok) warp_arrive(bar.fixed(n));
+        if (ok) warp_arrive(bar.fixed(v.slot));
       }
     }
   } else {
@@ -516,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint32_t ts = tmem + j * 128 + lanes, to = tmem + 256 + j * D + lanes;
     const int R = p.group * p.nodes;
     float2* const stats = reinterpret_cast<float2*>(smem + L::kStats);
-    uint32_t n = 0;                // the CTA's tiles
+    Cursor v(L::kK, L::kV);        // V of the step's tile
     uint32_t phases = 0;           // of the S buffers, a bit each
     // Whether the products with the last P of buffer b are done: a buffer's next
     // S, and so its next P, comes only after them.
@@ -531,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       const int r = w.qg * p.rows_per_unit + (NQ == 2 ? j * 128 : 0) + row;  // (head, node)
       const int tiles = w.tile1 - w.tile0;
       if (NQ == 2 && j >= unit_streams<NQ>(p, w)) {
-        n += tiles;
+        for (int i = 0; i < tiles; ++i) v.next();
         continue;
       }
       const bool live = r < R, live_warp = r - lane < R;
@@ -551,75 +611,88 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         const bool edge = edge_tile(w.row, low_all, t0);
         if (live_warp) {
           const uint32_t at = ts + (i & 1) * kStep;
-          uint32_t s[kStep];
-          tmem_ld32(at, s);
-          tmem_ld32(at + 32, s + 32);
-          tmem_wait_ld();
-          if (edge || __any_sync(0xffffffffu, low > t)) {
+          uint32_t seen[2] = {~0u, ~0u};
+          const bool masked = edge || __any_sync(0xffffffffu, low > t);
+          if (masked)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t bits = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
+            for (int c = 0; c < 2; ++c) seen[c] = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
+          uint32_t s[32], pk[kStep / 2];
+          auto load = [&](int c) {
+            tmem_ld32(at + 32 * c, s);
+            tmem_wait_ld(s);
+            if (masked)
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (!(bits >> x & 1)) s[32 * c + x] = 0xff800000u;  // -inf
-            }
-          }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < kStep; c += 8)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              top[x] = fmaxf(top[x], fmaxf(__uint_as_float(s[c + 2 * x]), __uint_as_float(s[c + 2 * x + 1])));
-          const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          const bool grow = live && mx * p.scale_log2 > m * p.scale_log2 + kLazyLog2;  // false for NaN, and -inf both
-          if (__any_sync(0xffffffffu, grow)) {
-            const float m2 = grow ? mx : m;
-            const float f = grow ? exp2f((m - m2) * p.scale_log2) : 1.f;  // 0 where m is -inf
-            m = m2;
-            l *= f;
-            if (i > 0) {
-              ok = taken(i + 1 & 1);
-              tmem_fence_after();
+                if (!(seen[c] >> x & 1)) s[x] = 0xff800000u;  // -inf
+          };
+          // Weights against the reference as it is, unless there is none yet; their
+          // sum shows whether the maximum has outgrown it, and only then is it looked for.
+          bool look = __any_sync(0xffffffffu, live && m == -INFINITY);
+          float sum_step;
+          for (;;) {
+            if (look) {
+              float mx = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(to + c, o);
-                tmem_wait_ld();
+              for (int c = 0; c < 2; ++c) {
+                load(c);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                tmem_st32(to + c, o);
+                for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
+              }
+              const bool grow = live && mx > m;  // false for NaN, and -inf both
+              if (__any_sync(0xffffffffu, grow)) {
+                const float m2 = grow ? mx : m;
+                const float f = grow ? exp2f((m - m2) * p.scale_log2) : 1.f;  // 0 where m is -inf
+                m = m2;
+                l *= f;
+                if (i > 0) {
+                  ok = taken(i + 1 & 1);
+                  tmem_fence_after();
+#pragma unroll 1
+                  for (int c = 0; c < D; c += 32) {
+                    tmem_ld32(to + c, s);
+                    tmem_wait_ld(s);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * f);
+                    tmem_st32(to + c, s);
+                  }
+                }
               }
             }
-          }
-          const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
-          const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(base, base);
-          uint64_t sum[2] = {0, 0};
-          uint32_t pk[kStep / 2];
+            const float base = m == -INFINITY ? 0.f : -m * p.scale_log2;
+            const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(base, base);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int x = 0; x < kStep / 2; ++x) {
+            for (int c = 0; c < 2; ++c) {
+              load(c);
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                uint32_t a, b;
+                unpack_b32x2(fma_f32x2(pack_b32x2(s[2 * x], s[2 * x + 1]), scale2, base2), a, b);
+                const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
+                sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
+                pk[16 * c + x] = pack_bf16x2(ea, eb);
+              }
+            }
             uint32_t a, b;
-            unpack_b32x2(fma_f32x2(pack_b32x2(s[2 * x], s[2 * x + 1]), scale2, base2), a, b);
-            const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
-            sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
-            pk[x] = pack_bf16x2(ea, eb);
+            unpack_b32x2(add_f32x2(sum[0], sum[1]), a, b);
+            sum_step = __uint_as_float(a) + __uint_as_float(b);
+            if (look || !__any_sync(0xffffffffu, live && !(sum_step <= kGrown))) break;
+            look = true;  // (also for NaN)
           }
           tmem_st32(at, pk);
-          uint32_t a, b;
-          unpack_b32x2(add_f32x2(sum[0], sum[1]), a, b);
-          l += __uint_as_float(a) + __uint_as_float(b);
+          l += sum_step;
           tmem_wait_st();
         }
         if (edge) {
           // V is in place; whether a drafted token in it had non-finite elements
-          const uint32_t v = n + tile;
-          ok = ok && warp_wait(bar.fixed(v), v / L::kFix & 1, abort, p.status);
-          nonfinite |= (bad[2 * (v % L::kFix)] | bad[2 * (v % L::kFix) + 1]) != 0;
+          ok = ok && warp_wait(bar.fixed(v.slot), v.phase, abort, p.status);
+          nonfinite |= bad[v.slot - L::kK] != 0;
         }
         if (!ok) break;
         tmem_fence_before();
         warp_arrive(bar.pready(j, i & 1));
+        if (NQ == 1 || half == 1) v.next();
       }
-      n += tiles;
       if (!ok) break;
       if (!(ok = taken(steps + 1 & 1))) break;
       tmem_fence_after();
@@ -630,10 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       if (NQ == 1) {
         tmem_fence_before();
         stats[j * 128 + row] = make_float2(ml, l);
-        if (row == 0) bad[2 * L::kFix + j] = nonfinite;  // the same for all threads of a stream
+        if (row == 0) bad[L::kV + j] = nonfinite;  // the same for all threads of a stream
         if (!(ok = join())) break;
         tmem_fence_after();
-        nonfinite = (bad[2 * L::kFix] | bad[2 * L::kFix + 1]) != 0;
+        nonfinite = (bad[L::kV] | bad[L::kV + 1]) != 0;
         const float2 a = stats[row], b = stats[128 + row];
         ml = fmaxf(a.x, b.x);
         const float top = ml == -INFINITY ? 0.f : ml;
@@ -664,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             tmem_ld32(t + c, a);
             tmem_ld32(t + D + c, b);
           }
-          tmem_wait_ld();
+          tmem_wait_ld(a);
+          if (NQ == 1) tmem_wait_ld(b);
           float o[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x) {

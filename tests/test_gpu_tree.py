@@ -309,6 +309,20 @@ def test_calls_in_a_row_share_a_workspace_and_repeat_bits():
     assert torch.equal(first, t.out)
 
 
+@pytest.mark.parametrize("layout,page,nodes", [("paged", 64, 256), ("contiguous", 0, 70), ("paged", 16, 16)])
+def test_repeated_calls_over_many_tiles_end_and_repeat_bits(layout, page, nodes):
+    """Loads land in any order and segments of many lengths meet in a CTA: every call ends without a device status."""
+    t = Tree("bf16", layout, 8, 28, 4, 128, page, nodes, [3893, 4047, 5021, 5802, 2139, 2576, 5292, 1000])
+    t.call()
+    t.check()
+    first = t.out.clone()
+    for _ in range(40):
+        t.call()
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+    assert torch.equal(first, t.out)
+
+
 def test_device_lengths_and_pages_that_disagree_are_recorded():
     t = Tree("bf16", "paged", 2, 8, 2, 128, 16, 4, [100, 50], [4, 4])
     t.lens_d.copy_(torch.tensor([100000, -5], dtype=torch.int32))  # clamped to the capacity, and to nothing
