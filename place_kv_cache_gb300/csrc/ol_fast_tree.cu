@@ -186,6 +186,18 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
   return true;
 }
 
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // The same for a whole warp: one answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
@@ -601,43 +613,42 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       float m = -INFINITY, l = 0.f;  // reference (raw scores) and sum
       bool nonfinite = false;
       const int steps = NQ * tiles;
+      uint32_t s[kStep];  // S of the step, on its way while the last step ends
+      auto fetch = [&](int i) {
+        phases ^= 1u << (i & 1);
+        tmem_fence_after();
+        if (live_warp) {
+          tmem_ld32(ts + (i & 1) * kStep, s);
+          tmem_ld32(ts + (i & 1) * kStep + 32, s + 32);
+        }
+      };
+      if (!(ok = warp_wait(bar.sfull(j, 0), phases & 1, abort, p.status))) break;
+      fetch(0);
       for (int i = 0; i < steps; ++i) {
         const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
         const int t0 = w.row.start + (w.tile0 + tile) * kTile, t = t0 + half * kStep;
-        ok = warp_wait(bar.sfull(j, i & 1), phases >> (i & 1) & 1, abort, p.status);
-        phases ^= 1u << (i & 1);
-        if (!ok) break;
-        tmem_fence_after();
         const bool edge = edge_tile(w.row, low_all, t0);
         if (live_warp) {
-          const uint32_t at = ts + (i & 1) * kStep;
-          uint32_t seen[2] = {~0u, ~0u};
-          const bool masked = edge || __any_sync(0xffffffffu, low > t);
-          if (masked)
+          tmem_wait_ld(s);
+          tmem_wait_ld(s + 32);
+          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t)))
 #pragma unroll
-            for (int c = 0; c < 2; ++c) seen[c] = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
-          uint32_t s[32], pk[kStep / 2];
-          auto load = [&](int c) {
-            tmem_ld32(at + 32 * c, s);
-            tmem_wait_ld(s);
-            if (masked)
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t seen = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (!(seen[c] >> x & 1)) s[x] = 0xff800000u;  // -inf
-          };
+                if (!(seen >> x & 1)) s[32 * c + x] = 0xff800000u;  // -inf
+            }
           // Weights against the reference as it is, unless there is none yet; their
           // sum shows whether the maximum has outgrown it, and only then is it looked for.
           bool look = __any_sync(0xffffffffu, live && m == -INFINITY);
           float sum_step;
+          uint32_t pk[kStep / 2];
           for (;;) {
             if (look) {
               float mx = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < 2; ++c) {
-                load(c);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
-              }
+              for (int x = 0; x < kStep; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
               const bool grow = live && mx > m;  // false for NaN, and -inf both
               if (__any_sync(0xffffffffu, grow)) {
                 const float m2 = grow ? mx : m;
@@ -649,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
                   tmem_fence_after();
 #pragma unroll 1
                   for (int c = 0; c < D; c += 32) {
-                    tmem_ld32(to + c, s);
-                    tmem_wait_ld(s);
+                    tmem_ld32(to + c, pk);
+                    tmem_wait_ld(pk);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * f);
-                    tmem_st32(to + c, s);
+                    for (int x = 0; x < 32; ++x) pk[x] = __float_as_uint(__uint_as_float(pk[x]) * f);
+                    tmem_st32(to + c, pk);
                   }
                 }
               }
@@ -662,16 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             const uint64_t scale2 = pack_f32x2(p.scale_log2, p.scale_log2), base2 = pack_f32x2(base, base);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              load(c);
-#pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                uint32_t a, b;
-                unpack_b32x2(fma_f32x2(pack_b32x2(s[2 * x], s[2 * x + 1]), scale2, base2), a, b);
-                const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
-                sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
-                pk[16 * c + x] = pack_bf16x2(ea, eb);
-              }
+            for (int x = 0; x < kStep / 2; ++x) {
+              uint32_t a, b;
+              unpack_b32x2(fma_f32x2(pack_b32x2(s[2 * x], s[2 * x + 1]), scale2, base2), a, b);
+              const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
+              sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
+              pk[x] = pack_bf16x2(ea, eb);
             }
             uint32_t a, b;
             unpack_b32x2(add_f32x2(sum[0], sum[1]), a, b);
@@ -679,10 +686,15 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             if (look || !__any_sync(0xffffffffu, live && !(sum_step <= kGrown))) break;
             look = true;  // (also for NaN)
           }
-          tmem_st32(at, pk);
+          tmem_st32(ts + (i & 1) * kStep, pk);
           l += sum_step;
-          tmem_wait_st();
         }
+        // the next scores, if they are there, come in while P settles
+        const bool next = i + 1 < steps;
+        const uint32_t next_full = bar.sfull(j, i + 1 & 1);
+        bool early = false;
+        if (next && (early = __all_sync(0xffffffffu, mbar_test(next_full, phases >> (i + 1 & 1) & 1)))) fetch(i + 1);
+        if (live_warp) tmem_wait_st();
         if (edge) {
           // V is in place; whether a drafted token in it had non-finite elements
           ok = ok && warp_wait(bar.fixed(v.slot), v.phase, abort, p.status);
@@ -692,6 +704,10 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         tmem_fence_before();
         warp_arrive(bar.pready(j, i & 1));
         if (NQ == 1 || half == 1) v.next();
+        if (next && !early) {
+          if (!(ok = warp_wait(next_full, phases >> (i + 1 & 1) & 1, abort, p.status))) break;
+          fetch(i + 1);
+        }
       }
       if (!ok) break;
       if (!(ok = taken(steps + 1 & 1))) break;
