@@ -22,8 +22,8 @@
 // for, and O rescaled, rarely. Sums and O are fp32; P is rounded to bf16, the
 // type its product with V takes: as much as the output's own rounding.
 //
-// Warps: 0 producer (TMA; lanes share the boxes of a tile: pages of 16 tokens
-// are boxes of 2 KB), 1 and 2 MMA issue for a stream each, 3 fixer, 4-7 and 8-11
+// Warps: 0 producer (TMA; a lane per box of a tile: pages of 16 tokens are
+// boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 fixer, 4-7 and 8-11
 // the streams. The fixer passes every V tile on and, in tiles that hold drafted
 // tokens or end the row, zeroes the rows outside the row's tokens and the
 // non-finite elements: a product with P = 0 must not see them. Where a stream
@@ -362,13 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint64_t policy = keep_l2 ? policy_evict_normal() : policy_evict_first();
     const uint64_t keep = policy_evict_normal();
     // One tile ahead: its boxes and this lane's page are known (the table's entry
-    // on its way) before the ring has room for it. Lane = (box, column block).
+    // on its way) before the ring has room for it. Lane = box.
     struct Tile {
       int t0, first, last;  // token; boxes
       int y;                // cache row of this lane's box in plane K
       int q;                // row of q of a segment's first tile, else -1
     } cur = {}, nxt = {};
-    const int x = lane / L::kHalves, h = lane % L::kHalves;
     const int v_rows = (PAGED ? p.cache.num_pages * p.cache.page_size : p.batch * p.cache.capacity) * p.kv_heads;
     int tile;
     auto fetch = [&](Tile& t) {
@@ -381,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       t.t0 = w.row.start + tile++ * kTile;
       t.first = max(row_low(p, w.row) - t.t0, 0) / box;
       t.last = (min(w.row.len - t.t0, kTile) + box - 1) / box;
-      const int at = t.t0 + x * box;
+      const int at = t.t0 + lane * box;
       if (!PAGED) {
         t.y = (w.b * p.kv_heads + w.g) * p.cache.capacity + at;
-      } else if (x >= t.first && x < t.last) {
+      } else if (lane >= t.first && lane < t.last) {
         int page = p.cache.block_table[(size_t)w.b * p.cache.max_pages + at / p.cache.page_size];
         if (page < 0 || page >= p.cache.num_pages) {
           set_status(p.status, OL_DEVICE_GUARD);
@@ -401,9 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       if (!warp_wait(bar.empty(c.slot), c.phase ^ 1, abort, p.status)) return false;
       if (lane == 0) mbar_arrive_expect_tx(bar.full(c.slot), (uint32_t)(cur.last - cur.first) * box * D * 2);
       __syncwarp();
-      if (x >= cur.first && x < cur.last)
-        tma_load_2d(sa + L::kRing + c.slot * L::kTileBytes + h * (kTile * 128) + x * box * 128, &maps.kv, h * 64, y,
-                    bar.full(c.slot), policy);
+      if (lane >= cur.first && lane < cur.last)
+        tma_load_3d(sa + L::kRing + c.slot * L::kTileBytes + lane * box * (D * 2), &maps.kv, 0, y, 0, bar.full(c.slot),
+                    policy);
       c.next();
       return true;
     };
@@ -419,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
           mbar_arrive_expect_tx(bar.qfull(), (uint32_t)NQ * qbox * D * 2);
           for (int j = 0; j < NQ; ++j)
             for (int c = 0; c < L::kHalves; ++c)
-              tma_load_2d(sa + L::kQ + j * L::kTileBytes + c * (kTile * 128), &maps.q, c * 64, cur.q + j * 128,
+              tma_load_3d(sa + L::kQ + j * L::kTileBytes + c * (kTile * 128), &maps.q, 0, cur.q + j * 128, c,
                           bar.qfull(), keep);
         }
         if (ok) ++seg;
@@ -443,6 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint32_t tm = uniform(tmem), base = uniform(sa);
     const uint32_t ts = tm + j * 128, to = tm + 256 + j * D;
     const uint64_t q = smem_desc(base + L::kQ + (NQ == 2 ? j : 0) * L::kTileBytes, 16, 1024);
+    // A tile is [box][column block][rows of the box][128 bytes]. A step's 64 tokens
+    // are 8 groups of 8 rows, evenly spaced: half a tile, or (boxes of 16 rows) the
+    // first or the last 8 rows of each box.
+    const uint32_t boxes = uniform(box), block = boxes * 128;
+    const uint32_t group = boxes == 16 ? block * L::kHalves : 1024;
+    const uint32_t step = boxes == 16 ? 1024 : boxes == 64 ? block * L::kHalves : kStep * 128;
     Cursor k(0, L::kK), v(L::kK, L::kV);
     uint32_t seg = 0;         // segments
     uint32_t pphase = 0;      // of the P buffers, a bit each
@@ -450,11 +455,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     // S into buffer b from the given half of K
     auto scores = [&](int half, int b) {
       if (elect_one()) {
-        const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes + half * (kStep * 128), 16, 1024);
+        const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes + half * step, 16, group);
 #pragma unroll
         for (int x = 0; x < D / 16; ++x) {
-          constexpr uint32_t kBlock = kTile * 128 / 16, kK = 2;  // column block, 16 elements; in 16 bytes
-          mma_ss(ts + b * kStep, q + (x / 4 * kBlock + x % 4 * kK), kd + (x / 4 * kBlock + x % 4 * kK), kDescS, x > 0);
+          constexpr uint32_t kBlock = kTile * 128 / 16, kK = 2;  // q's column block, 16 elements; in 16 bytes
+          mma_ss(ts + b * kStep, q + (x / 4 * kBlock + x % 4 * kK), kd + (x / 4 * (block / 16) + x % 4 * kK), kDescS,
+                 x > 0);
         }
         mma_commit(bar.sfull(j, b));
       }
@@ -474,14 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       if (wait_v && !warp_wait(bar.fixed(v.slot), v.phase, abort, p.status)) return false;
       tmem_fence_after();
       if (elect_one()) {
-        const uint64_t vd =
-            smem_desc(base + L::kRing + v.slot * L::kTileBytes + half * (kStep * 128), kTile * 128, 1024);
+        const uint64_t vd = smem_desc(base + L::kRing + v.slot * L::kTileBytes + half * step, block, group);
 #pragma unroll
         for (int x = 0; x < kStep / 16; ++x) {
           if (x == 0)
             mma_ts(to, ts + b * kStep, vd, kDescO, !first);
           else
-            mma_ts(to, ts + b * kStep + x * 8, vd + x * (2048 / 16), kDescO, true);
+            mma_ts(to, ts + b * kStep + x * 8, vd + x * (2 * group / 16), kDescO, true);
         }
         mma_commit(bar.pvdone(j, b));
         if (last_of_v) mma_commit(bar.empty(v.slot));
@@ -551,14 +556,16 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         ok = warp_wait(bar.full(v.slot), v.phase, abort, p.status);
         const int t0 = w.row.start + tile * kTile;
         if (ok && edge_tile(w.row, low, t0)) {
-          // 16-byte pieces, line after line of 128 bytes of each half: rows outside
-          // [low, len) become zeros, drafted rows lose non-finite elements
+          // 16-byte pieces, line after line of 128 bytes: rows outside [low, len)
+          // become zeros, drafted rows lose non-finite elements
           uint4* const at = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes) + lane;
+          const int box_log2 = 31 - __clz(box);
           const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
           bool found = false;
 #pragma unroll 4
           for (int i = 0; i < kTile * D / 8; i += 32) {
-            const int r = (i + lane) / 8 % kTile;
+            const int line = (i + lane) / 8;  // [box][column block][row]
+            const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
             if (r < r_low || r >= r_end) {
               at[i] = make_uint4(0, 0, 0, 0);
             } else if (r >= r_tree) {
@@ -626,15 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       fetch(0);
       for (int i = 0; i < steps; ++i) {
         const int tile = NQ == 2 ? i / 2 : i, half = NQ == 2 ? i % 2 : j;
-        const int t0 = w.row.start + (w.tile0 + tile) * kTile, t = t0 + half * kStep;
+        const int t0 = w.row.start + (w.tile0 + tile) * kTile;
         const bool edge = edge_tile(w.row, low_all, t0);
         if (live_warp) {
           tmem_wait_ld(s);
           tmem_wait_ld(s + 32);
-          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t)))
+          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t0)))
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const uint32_t seen = live ? visible_word(p, w.row, w.b, node, low, t + 32 * c) : 0u;
+              uint32_t seen = 0;
+              if (live && box == 16) {  // 8 tokens of each of 4 boxes
+                const uint32_t lo = visible_word(p, w.row, w.b, node, low, t0 + 64 * c);
+                const uint32_t hi = visible_word(p, w.row, w.b, node, low, t0 + 64 * c + 32);
+                seen = __byte_perm(lo, hi, half ? 0x7531 : 0x6420);
+              } else if (live) {
+                seen = visible_word(p, w.row, w.b, node, low, t0 + kStep * half + 32 * c);
+              }
 #pragma unroll
               for (int x = 0; x < 32; ++x)
                 if (!(seen >> x & 1)) s[32 * c + x] = 0xff800000u;  // -inf
@@ -819,15 +833,16 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// A bf16 buffer as rows of D elements; boxes of `box` rows x 64 elements, 128-byte swizzle.
-bool encode_rows(CUtensorMap* map, const void* base, int D, uint64_t rows, int box) {
+// A bf16 buffer as rows of D elements, seen as [column block][row][64 elements];
+// boxes of `box` rows and all (or one) of the column blocks, 128-byte swizzle.
+bool encode_rows(CUtensorMap* map, const void* base, int D, uint64_t rows, int box, bool all_blocks) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)D, rows};
-  cuuint64_t strides[1] = {(cuuint64_t)D * 2};
-  cuuint32_t boxes[2] = {64, (cuuint32_t)box};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, boxes, estr,
+  cuuint64_t dims[3] = {64, rows, (cuuint64_t)D / 64};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+  cuuint32_t boxes[3] = {64, (cuuint32_t)box, all_blocks ? (cuuint32_t)D / 64 : 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -873,13 +888,13 @@ void plan_fast_tree(TreeParams& p, int sms) {
 
 cudaError_t launch_fast_tree(const TreeParams& p, cudaStream_t s) {
   const int R = p.group * p.nodes;
+  // rows of a box: a tile of the contiguous cache, else 128, 64 or 16, what divides a page
   int box = kTile;
-  if (p.cache.block_table)  // the largest power of two that divides a page
-    while (p.cache.page_size % box != 0) box /= 2;
+  if (p.cache.block_table && p.cache.page_size % box != 0) box = p.cache.page_size % 64 == 0 ? 64 : 16;
   const int qbox = R < 128 ? (R + 7) / 8 * 8 : 128;
   Maps maps;
-  if (!encode_rows(&maps.q, p.q, p.head_dim, (uint64_t)p.batch * p.q_heads * p.nodes, qbox) ||
-      !encode_rows(&maps.kv, p.cache.base, p.head_dim, kv_rows(p), box))
+  if (!encode_rows(&maps.q, p.q, p.head_dim, (uint64_t)p.batch * p.q_heads * p.nodes, qbox, false) ||
+      !encode_rows(&maps.kv, p.cache.base, p.head_dim, kv_rows(p), box, true))
     return cudaErrorInvalidValue;
   return p.head_dim == 128 ? launch_dim<128>(maps, p, box, qbox, s) : launch_dim<64>(maps, p, box, qbox, s);
 }
