@@ -52,6 +52,17 @@ constexpr int kTreeGenRows = 32;   // (head, node) rows of a CUDA-core unit
 constexpr int kTreeGenTileLog2 = 5;   // tokens of its tile: 32
 constexpr int kTreeFastTileLog2 = 7;  // 128
 
+// The unit that begins in a CTA's share and reaches past its end, if there is one.
+struct alignas(16) TreeSplit {
+  int last;   // its last share, -1: no such unit
+  int slot;   // slot of its first segment
+  int count;  // nodes of its row
+  int rows;   // live (head, node) rows
+  long long out;  // row of q and out of its row 0
+  int first;      // (head, node) row 0 of the unit
+  int pad;
+};
+
 struct TreeParams {
   CacheRef cache;
   int dtype, batch, q_heads, kv_heads, group, head_dim;
@@ -66,6 +77,7 @@ struct TreeParams {
   void* out;
   int out_dtype;
   int32_t* status;
+  struct TreeSplit* splits;     // [nctas], written by every CTA of the attention for the merge
   float* partials;
   // work split
   int rows_per_unit;            // (head, node) rows r = head * nodes + node of a unit
@@ -93,11 +105,12 @@ OL_HD inline TreeRow tree_row(int len, int count, int window, int tile_log2) {
 
 // One partial slot: m[rows] (log2 domain), l[rows], o[ceil(D / 4)][rows] float4.
 OL_HD inline size_t tree_slot_floats(int rows, int head_dim) { return (size_t)rows * (2 + (head_dim + 3) / 4 * 4); }
+constexpr size_t kTreeSplitBytes = 2 * kTreeMaxCtas * sizeof(TreeSplit);
 inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }
 inline size_t tree_workspace_bytes(int q_heads, int kv_heads, int head_dim, int nodes) {
   const size_t fast = 2ull * kTreeMaxCtas * tree_slot_floats(tree_fast_rows(q_heads / kv_heads, nodes), head_dim);
   const size_t gen = 2ull * 2 * kTreeMaxCtas * tree_slot_floats(kTreeGenRows, head_dim);
-  return kStatusBytes + sizeof(float) * (fast > gen ? fast : gen);
+  return kStatusBytes + kTreeSplitBytes + sizeof(float) * (fast > gen ? fast : gen);
 }
 
 bool fast_tree_supported(const TreeParams& p);

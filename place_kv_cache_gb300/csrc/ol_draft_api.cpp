@@ -349,7 +349,8 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
   p.out = out;
   p.out_dtype = out_dtype;
   p.status = static_cast<int32_t*>(workspace);
-  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes);
+  p.splits = reinterpret_cast<TreeSplit*>(static_cast<char*>(workspace) + kStatusBytes);
+  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes + kTreeSplitBytes);
   const bool fast = fast_tree_supported(p);
   if (fast)
     plan_fast_tree(p, sm_count_cached());

@@ -588,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         if (ok) warp_arrive(bar.fixed(v.slot));
       }
     }
+    if (lane == 0) w.write_split(p);
   } else {
     // ----------------------------------------------------------------- streams
     const int j = (warp - 4) / 4, row = tid % 128;  // TMEM lane

@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
       }
     }
   }
+  if (tid == 0) w.write_split(p);
 }
 
 template <typename T, int NC>
@@ -227,87 +228,104 @@ cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------- the merge
 
-// CTA x merges the unit whose tokens reach from CTA x's share into the next
-// one's (if there is one and it began in share x): rows [ROWS y, ROWS (y + 1)).
+// CTA x merges the unit that begins in share x and reaches past it, if there is
+// one (TreeSplit): rows [ROWS y, ROWS (y + 1)).
 //   M = max m_s, L = sum l_s 2^(m_s - M), y = sum o_s 2^(m_s - M) / L
-// Thread = (row, group of four dimensions): the slots' layout keeps the rows of
-// a group together. The weights of 32 segments at a time are in shared memory.
-// Bound by reading the partials (L2). ROWS 32 for many units, each cut once or
-// twice; 8 where few units are cut into many segments, to have more CTAs.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeSegs = 32;
-template <int ROWS>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
-  constexpr int kLanes = kMergeThreads / ROWS;    // threads of a row
-  constexpr int kGroups = 64 / kLanes;            // groups of four dimensions per thread, for D up to 256
-  __shared__ float weight[kMergeSegs][ROWS];
-  __shared__ float part[kLanes][ROWS];
-  pdl_launch_dependents();
-  // lengths and counts were there before the kernel ahead started its work
-  TreeWalk w(p);
-  const int first = blockIdx.x;  // the unit's shares are first .. last
-  int last;
-  const bool some = w.split_after(p, last);
+// A thread has a row, KG groups of four dimensions (the slots' layout keeps the
+// rows of a group together) and one of G shares of the segments. 16 loads of o
+// are on their way before the weights are known; more segments than that are
+// taken in chunks with a running maximum. Bound by latency for few units (8 rows
+// a CTA, for more CTAs), else by reading the partials from L2 (32 rows).
+template <int ROWS, int THREADS, int D4>  // D4: groups of four dimensions, 32 or 64
+__global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p) {
+  constexpr int kLanes = THREADS / ROWS;  // threads of a row
+  constexpr int G = kLanes > D4 ? kLanes / D4 : 1, KG = kLanes > D4 ? 1 : D4 / kLanes;
+  constexpr int C = 16 / KG, kChunk = C * G;  // segments of a thread and of the CTA at a time
+  static_assert(C >= 2 && kChunk * ROWS <= THREADS, "a thread loads one state");
+  __shared__ float2 state[kChunk][ROWS];  // m, l
+  __shared__ float4 other[G > 1 ? (G - 1) * ROWS * D4 : 1];
+  __shared__ float other_l[G > 1 ? (G - 1) * ROWS : 1];
   pdl_wait();
-  if (!some) return;
-  const int RU = p.rows_per_unit, D = p.head_dim, D4 = (D + 3) / 4;
-  const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS;
+  pdl_launch_dependents();
+  const TreeSplit u = p.splits[blockIdx.x];
+  if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
+  const int RU = p.rows_per_unit, D = p.head_dim;
+  const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS, d0 = lane % D4, grp = lane / D4;
   const int place = blockIdx.y * ROWS + lr;  // row of the unit
-  const int r = w.qg * RU + place;
-  const bool mine = place < RU && r < p.group * p.nodes && r % p.nodes < w.row.count;
-  const int at = mine ? place : 0;
+  const bool mine = place < u.rows && (u.first + place) % p.nodes < u.count;
+  const int first = blockIdx.x, segs = u.last - first + 1;
   // the later shares begin with the unit's segment
-  auto slot_of = [&](int c) { return tree_slot(p, c == first ? w.slot : 2 * c); };
-  float M = -INFINITY;
-  for (int c = first + lane; c <= last; c += kLanes) M = fmaxf(M, slot_of(c)[at]);
-  part[lane][lr] = M;
-  __syncthreads();
+  auto slot_of = [&](int i) { return tree_slot(p, i == 0 ? u.slot : 2 * (first + i)); };
+  float M = -INFINITY, L = 0.f;
+  float4 acc[KG];
 #pragma unroll
-  for (int i = 0; i < kLanes; ++i) M = fmaxf(M, part[i][lr]);
-  const float base = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  float4 acc[kGroups];
+  for (int k = 0; k < KG; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < segs; i0 += kChunk) {
+    float4 v[C][KG];
 #pragma unroll
-  for (int i = 0; i < kGroups; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c0 = first; c0 <= last; c0 += kMergeSegs) {
-    const int n = min(kMergeSegs, last - c0 + 1);
-    __syncthreads();
-    for (int i = lane; i < n; i += kLanes) {
-      const float* const s = slot_of(c0 + i);
-      const float f = exp2f(s[at] - base);
-      weight[i][lr] = f;
-      L += s[RU + at] * f;
+    for (int c = 0; c < C; ++c) {
+      const int i = i0 + grp + c * G;
+      const float4* const o = reinterpret_cast<const float4*>(slot_of(i < segs ? i : 0) + 2 * RU) + place;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        const int d4 = d0 + k * kLanes;
+        v[c][k] = mine && i < segs && d4 * 4 < D ? o[(size_t)d4 * RU] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+    if (threadIdx.x < kChunk * ROWS) {
+      const int i = i0 + threadIdx.x / ROWS;
+      const bool there = i < segs && place < u.rows;
+      const float* const s = slot_of(there ? i : 0);
+      state[threadIdx.x / ROWS][lr] = there ? make_float2(s[place], s[RU + place]) : make_float2(-INFINITY, 0.f);
     }
     __syncthreads();
-    if (mine)
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float f = weight[i][lr];
-        const float4* const o = reinterpret_cast<const float4*>(slot_of(c0 + i) + 2 * RU) + at;
+    float top = M;
 #pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-          const int d4 = lane + k * kLanes;
-          if (d4 >= D4) break;
-          const float4 v = o[(size_t)d4 * RU];
-          acc[k].x += v.x * f;
-          acc[k].y += v.y * f;
-          acc[k].z += v.z * f;
-          acc[k].w += v.w * f;
-        }
+    for (int i = 0; i < kChunk; ++i) top = fmaxf(top, state[i][lr].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    const float keep = exp2f(M - base);
+    M = top;
+    L *= keep;
+#pragma unroll
+    for (int k = 0; k < KG; ++k) acc[k] = make_float4(acc[k].x * keep, acc[k].y * keep, acc[k].z * keep, acc[k].w * keep);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const float2 st = state[grp + c * G][lr];
+      const float f = exp2f(st.x - base);
+      L += st.y * f;
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        acc[k].x += v[c][k].x * f;
+        acc[k].y += v[c][k].y * f;
+        acc[k].z += v[c][k].z * f;
+        acc[k].w += v[c][k].w * f;
       }
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  part[lane][lr] = L;
-  __syncthreads();
+  if (G > 1) {
+    if (grp > 0) {
+      other[((grp - 1) * D4 + d0) * ROWS + lr] = acc[0];
+      if (d0 == 0) other_l[(grp - 1) * ROWS + lr] = L;
+    }
+    __syncthreads();
+    if (grp > 0) return;
+#pragma unroll
+    for (int x = 0; x < G - 1; ++x) {
+      const float4 o = other[(x * D4 + d0) * ROWS + lr];
+      acc[0].x += o.x;
+      acc[0].y += o.y;
+      acc[0].z += o.z;
+      acc[0].w += o.w;
+      L += other_l[x * ROWS + lr];
+    }
+  }
   if (!mine) return;
-  L = 0.f;
-#pragma unroll
-  for (int i = 0; i < kLanes; ++i) L += part[i][lr];
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t out = tree_out_row(p, w.b, w.g, r) * D;
+  const size_t out = (size_t)(u.out + place) * D;
 #pragma unroll
-  for (int k = 0; k < kGroups; ++k) {
-    const int d = (lane + k * kLanes) * 4;
+  for (int k = 0; k < KG; ++k) {
+    const int d = (d0 + k * kLanes) * 4;
     if (d >= D) break;
     const float v[4] = {acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv};
     if (D % 4 != 0) {
@@ -321,6 +339,13 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
           make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     }
   }
+}
+
+template <int ROWS, int THREADS>
+cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
+  const dim3 grid(p.nctas, (rows + ROWS - 1) / ROWS), block(THREADS);
+  return p.head_dim <= 128 ? launch_pdl(tree_merge_kernel<ROWS, THREADS, 32>, grid, block, 0, s, p)
+                           : launch_pdl(tree_merge_kernel<ROWS, THREADS, 64>, grid, block, 0, s, p);
 }
 
 // --------------------------------------------------------------- accepted path
@@ -393,8 +418,7 @@ cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
   const bool few = (long long)p.batch * p.kv_heads * p.units_per_head * 4 <= p.nctas;
-  if (few) return launch_pdl(tree_merge_kernel<8>, dim3(p.nctas, (rows + 7) / 8), dim3(kMergeThreads), 0, s, p);
-  return launch_pdl(tree_merge_kernel<32>, dim3(p.nctas, (rows + 31) / 32), dim3(kMergeThreads), 0, s, p);
+  return few ? launch_merge<8, 512>(p, rows, s) : launch_merge<32, 256>(p, rows, s);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {

@@ -160,16 +160,22 @@ struct TreeWalk {
 
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == row.ntiles; }
 
-  // For the merge: whether a unit begins in this share and reaches past its
-  // end. It is found, `slot` is that of its first segment and `last` its last share.
-  __device__ __forceinline__ bool split_after(const TreeParams& p, int& last) {
-    if (at >= end || end == total) return false;
-    const int begin = end - 1 - locate(p, end - 1), back = begin + row.ntiles - 1;  // the unit's first and last tile
-    if (begin < share || back < end) return false;
-    slot = 2 * blockIdx.x + (begin == share ? 0 : 1);
-    const int big = more * (each + 1);  // tiles of the shares of one more
-    last = back < big ? back / (each + 1) : more + (back - big) / each;
-    return true;
+  // After the share's last segment: what the merge needs of a unit that begins
+  // here and reaches past the share's end. One thread calls it.
+  __device__ __forceinline__ void write_split(const TreeParams& p) const {
+    TreeSplit s = {};
+    s.last = -1;
+    if (share < end && tile0 == 0 && tile1 < row.ntiles) {
+      const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
+      const int big = more * (each + 1);                // tiles of the shares of one more
+      s.last = back < big ? back / (each + 1) : more + (back - big) / each;
+      s.slot = slot;
+      s.count = row.count;
+      s.first = qg * p.rows_per_unit;
+      s.rows = min(p.rows_per_unit, p.group * p.nodes - s.first);
+      s.out = (long long)tree_out_row(p, b, g, s.first);
+    }
+    p.splits[blockIdx.x] = s;
   }
 };
 
