@@ -209,6 +209,25 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
+// Four lanes times four pieces of four words: piece x of lane q becomes piece q of lane x's row.
+__device__ __forceinline__ void quad_transpose(uint32_t* z, int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit *= 2) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x & bit) continue;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t& lo = z[4 * x + y];
+        uint32_t& hi = z[4 * (x | bit) + y];
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+        (up ? lo : hi) = other;
+      }
+    }
+  }
+}
+
 // Walks the slots [first, first + count) of a ring, tile after tile.
 struct Cursor {
   int slot, first, end;
@@ -249,34 +268,35 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
   return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-// Visibility of tokens [t, t + 32) for a node, as bits.
-__device__ __noinline__ uint32_t visible_word(const TreeParams& p, const TreeRow row, int b, int node, int low, int t) {
-  uint32_t bits = bit_range(low - t, row.prefix - t);
-  const int j0 = t - row.prefix;  // drafted index of bit 0
-  if (j0 <= -32 || j0 >= row.count) return bits;
+// Drafted tokens [j0, j0 + 32) among `bits` that lie within the window of a node.
+__device__ __noinline__ uint32_t in_window(const TreeParams& p, const TreeRow row, int b, int node, int j0, uint32_t bits) {
+  const int at = tree_position(p, row, b, node);
+  for (uint32_t left = bits; left; left &= left - 1) {
+    const int c = __ffs(left) - 1;
+    if ((long long)at - tree_position(p, row, b, j0 + c) > p.window) bits &= ~(1u << c);
+  }
+  return bits;
+}
+
+// Visibility of tokens [t, t + 32) for a node, as bits, but for the window among
+// drafted tokens: m are its mask words (NULL: a chain).
+__device__ __noinline__ uint32_t visible_word(const uint64_t* m, int words, int prefix, int count, int node, int low,
+                                              int t) {
+  const uint32_t bits = bit_range(low - t, prefix - t);
+  const int j0 = t - prefix;  // drafted index of bit 0
+  if (j0 <= -32 || j0 >= count) return bits;
   uint32_t tree;
-  if (p.mask) {
-    const uint64_t* const m = p.mask + ((size_t)b * p.nodes + node) * p.words;
-    if (j0 < 0) {
-      tree = (uint32_t)m[0] << -j0;
-    } else {
-      const int w = j0 / 64, s = j0 % 64;
-      uint64_t v = m[w] >> s;
-      if (s > 32 && w + 1 < p.words) v |= m[w + 1] << (64 - s);
-      tree = (uint32_t)v;
-    }
-  } else {
+  if (!m) {
     tree = bit_range(-32, node + 1 - j0);
+  } else if (j0 < 0) {
+    tree = (uint32_t)m[0] << -j0;
+  } else {
+    const int w = j0 / 64, s = j0 % 64;
+    uint64_t v = m[w] >> s;
+    if (s > 32 && w + 1 < words) v |= m[w + 1] << (64 - s);
+    tree = (uint32_t)v;
   }
-  tree &= bit_range(-j0, row.count - j0);
-  if (p.window >= 0 && tree) {
-    const int at = tree_position(p, row, b, node);
-    for (uint32_t left = tree; left; left &= left - 1) {
-      const int c = __ffs(left) - 1;
-      if ((long long)at - tree_position(p, row, b, j0 + c) > p.window) tree &= ~(1u << c);
-    }
-  }
-  return bits | tree;
+  return bits | (tree & bit_range(-j0, count - j0));
 }
 
 // Adds the non-finite elements, in dimensions [d0, d1), of the V of drafted
@@ -618,6 +638,18 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       const int node = r % p.nodes;
       const int low = p.window < 0 ? 0 : tree_low(p, w.row, w.b, node);
       const int low_all = row_low(p, w.row);
+      const uint64_t* const words = p.mask ? p.mask + ((size_t)w.b * p.nodes + node) * p.words : nullptr;
+      if (words)  // on their way to L1 before the tiles that need them
+        for (int x = 0; x < p.words; x += 4) asm volatile("prefetch.global.L1 [%0];" ::"l"(words + x));
+      auto visible = [&](int t) {
+        uint32_t bits = visible_word(words, p.words, w.row.prefix, w.row.count, node, low, t);
+        const int j0 = t - w.row.prefix;
+        if (p.window >= 0 && j0 > -32) {
+          const uint32_t tree = bits & bit_range(-j0, 32);
+          if (tree) bits = (bits ^ tree) | in_window(p, w.row, w.b, node, j0, tree);
+        }
+        return bits;
+      };
       float m = -INFINITY, l = 0.f;  // reference (raw scores) and sum
       bool nonfinite = false;
       const int steps = NQ * tiles;
@@ -644,11 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
             for (int c = 0; c < 2; ++c) {
               uint32_t seen = 0;
               if (live && box == 16) {  // 8 tokens of each of 4 boxes
-                const uint32_t lo = visible_word(p, w.row, w.b, node, low, t0 + 64 * c);
-                const uint32_t hi = visible_word(p, w.row, w.b, node, low, t0 + 64 * c + 32);
-                seen = __byte_perm(lo, hi, half ? 0x7531 : 0x6420);
+                seen = __byte_perm(visible(t0 + 64 * c), visible(t0 + 64 * c + 32), half ? 0x7531 : 0x6420);
               } else if (live) {
-                seen = visible_word(p, w.row, w.b, node, low, t0 + kStep * half + 32 * c);
+                seen = visible(t0 + kStep * half + 32 * c);
               }
 #pragma unroll
               for (int x = 0; x < 32; ++x)
@@ -758,46 +788,57 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         // NQ == 1: each stream writes half of the dimensions
         constexpr int kCols = NQ == 2 ? D : D / 2;
         const int c0 = NQ == 2 ? 0 : j * kCols;
+        const uint32_t t = tmem + 256 + lanes;
+        const size_t at = tree_out_row(p, w.b, w.g, r) * D;
 #pragma unroll 1
         for (int c = c0; c < c0 + kCols; c += 32) {
-          uint32_t a[32], b[32];
-          const uint32_t t = tmem + 256 + lanes;
+          uint32_t o[32];
           if (NQ == 2) {
-            tmem_ld32(to + c, a);
+            tmem_ld32(to + c, o);
+            tmem_wait_ld(o);
           } else {
-            tmem_ld32(t + c, a);
+            uint32_t b[32];
+            tmem_ld32(t + c, o);
             tmem_ld32(t + D + c, b);
+            tmem_wait_ld(o);
+            tmem_wait_ld(b);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              o[x] = __float_as_uint(__uint_as_float(o[x]) * f0 + __uint_as_float(b[x]) * f1);
           }
-          tmem_wait_ld(a);
-          if (NQ == 1) tmem_wait_ld(b);
-          float o[32];
+          if (slot) {
+            float4* const y = reinterpret_cast<float4*>(slot + 2 * p.rows_per_unit) + (size_t)(c / 4) * p.rows_per_unit + place;
+            if (mine)
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            o[x] = __uint_as_float(a[x]);
-            if (NQ == 1) o[x] = o[x] * f0 + __uint_as_float(b[x]) * f1;
-            o[x] *= inv;
-          }
-          if (mine && slot) {
-            float4* const to4 = reinterpret_cast<float4*>(slot + 2 * p.rows_per_unit);
+              for (int x = 0; x < 8; ++x) reinterpret_cast<uint4*>(y)[x * p.rows_per_unit] =
+                  make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          } else if (p.out_dtype == OL_F32) {
+            uint4* const y = reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.out) + at + c);
+            if (mine)
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              to4[(size_t)(c / 4 + x) * p.rows_per_unit + place] =
-                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          } else if (mine) {
-            const size_t at = tree_out_row(p, w.b, w.g, r) * D + c;
-            if (p.out_dtype == OL_F32) {
-              float4* const y = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at);
+              for (int x = 0; x < 8; ++x)
+                y[x] = make_uint4(__float_as_uint(__uint_as_float(o[4 * x]) * inv),
+                                  __float_as_uint(__uint_as_float(o[4 * x + 1]) * inv),
+                                  __float_as_uint(__uint_as_float(o[4 * x + 2]) * inv),
+                                  __float_as_uint(__uint_as_float(o[4 * x + 3]) * inv));
+          } else {
+            // Four lanes exchange their rows' four pieces of 16 bytes, so that
+            // together they write 64 bytes of one row after another.
+            uint32_t z[16];
 #pragma unroll
-              for (int x = 0; x < 8; ++x) y[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            } else {
-              uint4* const y = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + at);
+            for (int x = 0; x < 16; ++x)
+              z[x] = pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+            quad_transpose(z, lane);
+            const unsigned who = __ballot_sync(0xffffffffu, mine);
+            const size_t first = tree_out_row(p, w.b, w.g, r - lane % 4) * D + c + lane % 4 * 8;
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                y[x] = make_uint4(pack_bf16x2(o[8 * x], o[8 * x + 1]), pack_bf16x2(o[8 * x + 2], o[8 * x + 3]),
-                                  pack_bf16x2(o[8 * x + 4], o[8 * x + 5]), pack_bf16x2(o[8 * x + 6], o[8 * x + 7]));
-            }
+            for (int x = 0; x < 4; ++x)
+              if (who >> (lane / 4 * 4 + x) & 1)
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + first + (size_t)x * D) =
+                    make_uint4(z[4 * x], z[4 * x + 1], z[4 * x + 2], z[4 * x + 3]);
           }
         }
+        __syncwarp();  // add_nonfinite reads what other lanes wrote
         if (nonfinite && mine)
           add_nonfinite(p, w.row, w.b, w.g, w.tile0, w.tile1, node, c0, c0 + kCols, slot, place,
                         tree_out_row(p, w.b, w.g, r));
