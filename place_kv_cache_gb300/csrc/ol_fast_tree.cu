@@ -23,12 +23,12 @@
 // type its product with V takes: as much as the output's own rounding.
 //
 // Warps: 0 producer (TMA; a lane per box of a tile: pages of 16 tokens are
-// boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 fixer, 4-7 and 8-11
-// the streams. The fixer passes every V tile on and, in tiles that hold drafted
-// tokens or end the row, zeroes the rows outside the row's tokens and the
-// non-finite elements: a product with P = 0 must not see them. Where a stream
-// meets such an element in a drafted token, it adds the non-finite values of the
-// tokens that its row sees to the outputs at the end (rare, unhurried).
+// boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 the note for the
+// merge, 4-7 and 8-11 the streams. In tiles that hold drafted tokens or end the
+// row, the streams first zero, in V's tile, the rows outside the row's tokens and
+// the non-finite elements of drafted ones: a product with P = 0 must not see them.
+// Where there was such an element, the non-finite values of the tokens that a row
+// sees are added to its outputs at the end (rare, unhurried).
 //
 // Bounds: 4 * D bytes per token and kv head against 4 * D * rows flops: the
 // memory up to 256 rows, then the tensor cores.
@@ -55,11 +55,10 @@ struct Lay {
   static constexpr int kRing = NQ * kTileBytes;
   static constexpr int kStats = kRing + kSlots * kTileBytes;  // float2 [2][128]: streams' (m, l)
   static constexpr int kBars = kStats + 2 * 128 * 8;
-  // full, empty [kSlots], fixed [kV]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain[2], join
-  static constexpr int kNumBars = 2 * kSlots + kV + 17;
-  static constexpr int kBad = kBars + kNumBars * 8;     // uint32 [kV + 2]
-  static constexpr int kMisc = kBad + (kV + 2) * 4;   // TMEM address, abort flag
-  static constexpr int kTotal = kMisc + 8;
+  // full, empty [kSlots], fixed [3]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain[2], join
+  static constexpr int kNumBars = 2 * kSlots + 3 + 17;
+  static constexpr int kMisc = kBars + kNumBars * 8;    // TMEM address, abort flag, whether V had non-finite elements
+  static constexpr int kTotal = kMisc + 12;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
 
@@ -160,8 +159,9 @@ struct Bars {
   uint32_t at;
   __device__ uint32_t full(int s) const { return at + 8 * s; }
   __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
-  __device__ uint32_t fixed(int v) const { return at + 8 * (2 * L::kSlots - L::kK + v); }  // of V's slot v
-  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kV); }
+  // V set to rights by stream x for itself, or (2) by both streams for both
+  __device__ uint32_t fixed(int x) const { return at + 8 * (2 * L::kSlots + x); }
+  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + 3); }
   __device__ uint32_t qempty() const { return qfull() + 8; }
   __device__ uint32_t sfull(int j, int b) const { return qfull() + 16 + 16 * j + 8 * b; }  // S buffer b of stream j
   __device__ uint32_t pready(int j, int b) const { return qfull() + 48 + 16 * j + 8 * b; }  // P in its place
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
   }
   const Bars<D, NQ> bar{sa + L::kBars};
   volatile uint32_t* const abort = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
-  volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(smem + L::kBad);
+  volatile uint32_t* const bad = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 8);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       mbar_init(bar.full(s), 1);
       mbar_init(bar.empty(s), 2);
     }
-    for (int v = L::kK; v < L::kSlots; ++v) mbar_init(bar.fixed(v), 1);
     mbar_init(bar.qfull(), 1);
     mbar_init(bar.qempty(), 2);
     for (int j = 0; j < 2; ++j) {
@@ -359,10 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       mbar_init(bar.pvdone(j, 0), 1);
       mbar_init(bar.pvdone(j, 1), 1);
       mbar_init(bar.drain(j), 1);
+      mbar_init(bar.fixed(j), 4);  // a stream's warps
     }
+    mbar_init(bar.fixed(2), 8);
     mbar_init(bar.join(), 8);
     fence_mbar_init();
     *abort = 0;
+    *bad = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sa + L::kMisc) : "memory");
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     auto sums = [&](int half, int b, bool first, bool wait_v, bool last_of_v) {
       if (!warp_wait(bar.pready(j, b), pphase >> b & 1, abort, p.status)) return false;
       pphase ^= 1u << b;
-      if (wait_v && !warp_wait(bar.fixed(v.slot), v.phase, abort, p.status)) return false;
+      if (wait_v && !warp_wait(bar.full(v.slot), v.phase, abort, p.status)) return false;
       tmem_fence_after();
       if (elect_one()) {
         const uint64_t vd = smem_desc(base + L::kRing + v.slot * L::kTileBytes + half * step, block, group);
@@ -523,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         for (int i = 0; ok && i < tiles; ++i) {
           ok = k_wait();
           if (ok) warp_arrive(bar.empty(k.slot));
-          ok = ok && warp_wait(bar.fixed(v.slot), v.phase, abort, p.status);
+          ok = ok && warp_wait(bar.full(v.slot), v.phase, abort, p.status);
           if (ok) warp_arrive(bar.empty(v.slot));
           k.next();
           v.next();
@@ -567,48 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ------------------------------------------------------------------- fixer
-    Cursor v(L::kK, L::kV);
-    bool ok = true;
-    while (ok && w.next(p)) {
-      const int low = row_low(p, w.row);
-      for (int tile = w.tile0; ok && tile < w.tile1; ++tile, v.next()) {
-        ok = warp_wait(bar.full(v.slot), v.phase, abort, p.status);
-        const int t0 = w.row.start + tile * kTile;
-        if (ok && edge_tile(w.row, low, t0)) {
-          // 16-byte pieces, line after line of 128 bytes: rows outside [low, len)
-          // become zeros, drafted rows lose non-finite elements
-          uint4* const at = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes) + lane;
-          const int box_log2 = 31 - __clz(box);
-          const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
-          bool found = false;
-#pragma unroll 4
-          for (int i = 0; i < kTile * D / 8; i += 32) {
-            const int line = (i + lane) / 8;  // [box][column block][row]
-            const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
-            if (r < r_low || r >= r_end) {
-              at[i] = make_uint4(0, 0, 0, 0);
-            } else if (r >= r_tree) {
-              uint4 x = at[i];
-              uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
-              bool hit = false;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                if ((e[c] & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u, hit = true;
-                if ((e[c] & 0x7f800000u) == 0x7f800000u) e[c] &= 0xffffu, hit = true;
-              }
-              if (hit) at[i] = x;
-              found |= hit;
-            }
-          }
-          const bool any = __any_sync(0xffffffffu, found);
-          if (lane == 0) bad[v.slot - L::kK] = any;
-          fence_proxy_async_smem();
-        }
-        if (ok) warp_arrive(bar.fixed(v.slot));
+    // -------------------------------------------------------------- the merge's note
+    if (lane == 0) {
+      while (w.next(p)) {
       }
+      w.write_split(p);
     }
-    if (lane == 0) w.write_split(p);
   } else {
     // ----------------------------------------------------------------- streams
     const int j = (warp - 4) / 4, row = tid % 128;  // TMEM lane
@@ -616,6 +582,39 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint32_t ts = tmem + j * 128 + lanes, to = tmem + 256 + j * D + lanes;
     const int R = p.group * p.nodes;
     float2* const stats = reinterpret_cast<float2*>(smem + L::kStats);
+    const int box_log2 = 31 - __clz(box);
+    // Half h of a V tile (the tokens of a step): rows outside [low, len) become
+    // zeros, drafted ones lose their non-finite elements.
+    auto fix = [&](uint8_t* v, int h, int low, int prefix, int end) {  // rows of the tile
+      bool found = false;
+#pragma unroll 4
+      for (int i = row; i < kTile * D / 16; i += 128) {
+        // piece i of this half; its line of 128 bytes among [box][column block][row]
+        int line = i / 8;
+        line = box == 16 ? line / 8 * 16 + h * 8 + line % 8
+               : box == 64 ? line + h * 64 * L::kHalves
+                           : line / 64 * 128 + h * 64 + line % 64;
+        const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
+        uint4* const at = reinterpret_cast<uint4*>(v) + line * 8 + i % 8;
+        if (r < low || r >= end) {
+          *at = make_uint4(0, 0, 0, 0);
+        } else if (r >= prefix) {
+          uint4 x = *at;
+          uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
+          bool hit = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if ((e[c] & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u, hit = true;
+            if ((e[c] & 0x7f800000u) == 0x7f800000u) e[c] &= 0xffffu, hit = true;
+          }
+          if (hit) *at = x;
+          found |= hit;
+        }
+      }
+      if (found) *bad = 1;
+      fence_proxy_async_smem();
+    };
+    uint32_t fixes[2] = {0, 0};    // edge tiles set to rights by this stream for itself, by both for both
     Cursor v(L::kK, L::kV);        // V of the step's tile
     uint32_t phases = 0;           // of the S buffers, a bit each
     // Whether the products with the last P of buffer b are done: a buffer's next
@@ -630,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     while (ok && w.next(p)) {
       const int r = w.qg * p.rows_per_unit + (NQ == 2 ? j * 128 : 0) + row;  // (head, node)
       const int tiles = w.tile1 - w.tile0;
-      if (NQ == 2 && j >= unit_streams<NQ>(p, w)) {
+      const int streams = unit_streams<NQ>(p, w);
+      if (j >= streams) {
         for (int i = 0; i < tiles; ++i) v.next();
         continue;
       }
@@ -651,7 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         return bits;
       };
       float m = -INFINITY, l = 0.f;  // reference (raw scores) and sum
-      bool nonfinite = false;
       const int steps = NQ * tiles;
       uint32_t s[kStep];  // S of the step, on its way while the last step ends
       auto fetch = [&](int i) {
@@ -740,10 +739,19 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         bool early = false;
         if (next && (early = __all_sync(0xffffffffu, mbar_test(next_full, phases >> (i + 1 & 1) & 1)))) fetch(i + 1);
         if (live_warp) tmem_wait_st();
-        if (edge) {
-          // V is in place; whether a drafted token in it had non-finite elements
-          ok = ok && warp_wait(bar.fixed(v.slot), v.phase, abort, p.status);
-          nonfinite |= bad[v.slot - L::kK] != 0;
+        if (edge && (NQ == 1 || half == 0)) {
+          ok = ok && warp_wait(bar.full(v.slot), v.phase, abort, p.status);
+          if (ok) {
+            // NQ = 1: each stream needs its own half; two query tiles: both need
+            // both and do one each, unless the other stream has no queries
+            uint8_t* const at = smem + L::kRing + v.slot * L::kTileBytes;
+            const int r_low = low_all - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
+            fix(at, j, r_low, r_tree, r_end);
+            if (NQ == 2 && streams == 1) fix(at, 1, r_low, r_tree, r_end);
+            const int x = NQ == 2 && streams == 2;
+            warp_arrive(bar.fixed(x ? 2 : j));
+            ok = warp_wait(bar.fixed(x ? 2 : j), fixes[x]++ & 1, abort, p.status);
+          }
         }
         if (!ok) break;
         tmem_fence_before();
@@ -764,10 +772,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       if (NQ == 1) {
         tmem_fence_before();
         stats[j * 128 + row] = make_float2(ml, l);
-        if (row == 0) bad[L::kV + j] = nonfinite;  // the same for all threads of a stream
         if (!(ok = join())) break;
         tmem_fence_after();
-        nonfinite = (bad[L::kV] | bad[L::kV + 1]) != 0;
         const float2 a = stats[row], b = stats[128 + row];
         ml = fmaxf(a.x, b.x);
         const float top = ml == -INFINITY ? 0.f : ml;
@@ -839,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
           }
         }
         __syncwarp();  // add_nonfinite reads what other lanes wrote
-        if (nonfinite && mine)
+        if (*bad && mine)  // (of this or an earlier segment)
           add_nonfinite(p, w.row, w.b, w.g, w.tile0, w.tile1, node, c0, c0 + kCols, slot, place,
                         tree_out_row(p, w.b, w.g, r));
       }
