@@ -217,7 +217,7 @@ def _ptr(x) -> Optional[int]:
     if isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):
-        return x.ctypes.data
+        return x.__array_interface__["data"][0]
     if hasattr(x, "data_ptr"):
         _PTR_OF_TYPE[type(x)] = type(x).data_ptr
         return x.data_ptr()
@@ -242,12 +242,31 @@ def _host_i32(a):
     return np.ascontiguousarray(np.asarray(a, dtype=np.int32))
 
 
+_CURRENT_STREAM = None  # () -> handle of the calling thread's current CUDA stream, once CUDA is known to be there
+
+
+def _current_stream_getter():
+    """torch's own lookups behind torch.cuda.current_stream(), without the Stream
+    object that call builds (a large part of a small call's host time)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
 def _stream(stream) -> Optional[int]:
+    global _CURRENT_STREAM
     if stream is None:
+        if _CURRENT_STREAM is not None:
+            return _CURRENT_STREAM()
         try:
             import torch
             if torch.cuda.is_available():
-                return torch.cuda.current_stream().cuda_stream
+                handle = torch.cuda.current_stream().cuda_stream
+                _CURRENT_STREAM = _current_stream_getter()
+                return handle
         except Exception:
             pass
         return None

@@ -84,6 +84,7 @@ struct TreeParams {
   int units_per_head;           // ceil(group * nodes / rows_per_unit)
   int tile_log2;                // tokens per tile
   int nctas;                    // the tiles of all units in contiguous equal shares
+  int extra;                    // tiles that a unit's begin and end cost besides
 };
 
 // A row's tokens as the work split sees them: drafted tokens are
@@ -119,7 +120,7 @@ void plan_fast_tree(TreeParams& p, int sms);
 void plan_generic_tree(TreeParams& p, int sms);
 // Tiles are counted in 32 bits on the device, whatever lengths it finds there.
 inline bool tree_counts_fit(const TreeParams& p) {
-  const unsigned __int128 tiles = (unsigned __int128)((p.cache.capacity >> p.tile_log2) + 1) * p.batch * p.kv_heads *
+  const unsigned __int128 tiles = (unsigned __int128)((p.cache.capacity >> p.tile_log2) + 1 + p.extra) * p.batch * p.kv_heads *
                                   p.units_per_head;
   return tiles < (1u << 31);
 }

@@ -11,7 +11,8 @@
 // Bounds: 2 * D * elt bytes per vector against 3 * rot_dim flops: memory, or
 // the launch itself for a decode step. One CTA takes one token of one row and
 // all of its q, k and v vectors, so the token's sines and cosines are computed
-// once (rot_dim / 2 threads, through shared memory) and serve every head.
+// once (rot_dim / 2 threads, through shared memory) and serve every head. Its
+// first vectors are on their way before the positions are known.
 #include "ol_common.cuh"
 #include "ol_draft.h"
 
@@ -59,87 +60,99 @@ struct Items {
 };
 
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   using P = Piece<T, VE>;
-  __shared__ float2 turn[kRopeMaxHalf];  // (cos, sin) * magnitude of this token
-  const int b = blockIdx.x / p.tokens, t = blockIdx.x % p.tokens;
+  constexpr bool kTwo = Items<VE, HALF>::kTwo;
+  constexpr int NP = kTwo ? VE : VE / 2;  // pairs of an item
+  __shared__ float2 turn[kRopeMaxHalf];   // (cos, sin) * magnitude of this token
+  const int b = blockIdx.x / p.tokens, t = blockIdx.x - b * p.tokens;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthreads = blockDim.x * blockDim.y;
+  const int heads = p.q_heads + 2 * p.kv_heads;
+  const Items<VE, HALF> items(p.rot_dim, p.head_dim);
+  const T* const q_row = reinterpret_cast<const T*>(p.q.data) + b * p.q.sb + t * p.q.st;
+  const T* const k_row = reinterpret_cast<const T*>(p.k.data) + b * p.k.sb + t * p.k.st;
+  const T* const v_row = reinterpret_cast<const T*>(p.v.data) + b * p.v.sb + t * p.v.st;
+  P a[kRopeUnroll], c[kRopeUnroll];
+  // pieces of item i of heads h0, h0 + blockDim.y, ...
+  auto load = [&](int i, int h0) {
+    const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
+    const bool two = kTwo && i < items.rotated;
+#pragma unroll
+    for (int u = 0; u < kRopeUnroll; ++u) {
+      const int h = h0 + u * blockDim.y;
+      if (h >= heads) continue;
+      const int g = h - p.q_heads;
+      const T* const from = g < 0              ? q_row + h * p.q.sh
+                            : g < p.kv_heads ? k_row + g * p.k.sh
+                                             : v_row + (g - p.kv_heads) * p.v.sh;
+      a[u] = *reinterpret_cast<const P*>(from + ea);
+      if (two) c[u] = *reinterpret_cast<const P*>(from + eb);
+    }
+  };
   pdl_wait();
+  pdl_launch_dependents();
   if (p.counts && t >= p.counts[b]) return;
+  load(threadIdx.x, threadIdx.y);  // (every thread has an item: blockDim.x is at most their number)
   const int start = p.positions ? p.positions[b] : 0;
   const long long at = p.angles ? p.angles[(size_t)b * p.tokens + t] : (long long)start + t;
   // where this token's K and V go: element offset of (plane 0, head 0), and the strides
   size_t slot = 0, head_stride = 0, plane_stride = 0;
   if (p.kv_heads) {
-    const CacheRef& c = p.cache;
+    const CacheRef& r = p.cache;
     const long long pos = (long long)start + t;
-    if (start < 0 || pos >= c.capacity) return;  // device guard
-    if (c.block_table) {
-      const int page = c.block_table[(size_t)b * c.max_pages + pos / c.page_size];
-      if (page < 0 || page >= c.num_pages) return;  // device guard
-      head_stride = (size_t)c.page_size * p.head_dim;
-      slot = (size_t)page * c.kv_heads * head_stride + (size_t)(pos % c.page_size) * p.head_dim;
-      plane_stride = (size_t)c.num_pages * c.kv_heads * head_stride;
+    if (start < 0 || pos >= r.capacity) return;  // device guard
+    if (r.block_table) {
+      const int n = (int)pos / r.page_size;
+      const int page = r.block_table[(size_t)b * r.max_pages + n];
+      if (page < 0 || page >= r.num_pages) return;  // device guard
+      head_stride = (size_t)r.page_size * p.head_dim;
+      slot = (size_t)page * r.kv_heads * head_stride + (size_t)((int)pos - n * r.page_size) * p.head_dim;
+      plane_stride = (size_t)r.num_pages * r.kv_heads * head_stride;
     } else {
-      head_stride = (size_t)c.capacity * p.head_dim;
-      slot = (size_t)b * c.kv_heads * head_stride + (size_t)pos * p.head_dim;
-      plane_stride = (size_t)c.batch * c.kv_heads * head_stride;
+      head_stride = (size_t)r.capacity * p.head_dim;
+      slot = (size_t)b * r.kv_heads * head_stride + (size_t)pos * p.head_dim;
+      plane_stride = (size_t)r.batch * r.kv_heads * head_stride;
     }
   }
   for (int i = tid; i < p.rot_dim / 2; i += nthreads) {
     const long long phase = (long long)((unsigned long long)at * p.turns[i]);
-    float s, c;
-    sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
-    turn[i] = make_float2(c * p.magnitude, s * p.magnitude);
+    float s, co;
+    sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &co);
+    turn[i] = make_float2(co * p.magnitude, s * p.magnitude);
   }
   __syncthreads();
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const Items<VE, HALF> items(p.rot_dim, p.head_dim);
+  T* const q_out = reinterpret_cast<T*>(p.q_out.data) + b * p.q_out.sb + t * p.q_out.st;
+  T* const cache = reinterpret_cast<T*>(p.cache.base) + slot;
+  bool loaded = true;  // the first pieces
   for (int i = threadIdx.x; i < items.total; i += blockDim.x) {
-    const bool rotated = i < items.rotated;
-    const bool two = rotated && Items<VE, HALF>::kTwo;
+    const bool rotated = i < items.rotated, two = kTwo && rotated;
     const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
-    constexpr int NP = Items<VE, HALF>::kTwo ? VE : VE / 2;  // pairs of an item
     float2 cs[NP];
     if (rotated)
 #pragma unroll
       for (int j = 0; j < NP; ++j) cs[j] = turn[i * NP + j];
     for (int h0 = threadIdx.y; h0 < heads; h0 += blockDim.y * kRopeUnroll) {
-      P a[kRopeUnroll], c[kRopeUnroll];
-      T* to[kRopeUnroll];
+      if (!loaded) load(i, h0);
+      loaded = false;
 #pragma unroll
       for (int u = 0; u < kRopeUnroll; ++u) {
-        const int h = h0 + u * blockDim.y;
-        to[u] = nullptr;
+        const int h = h0 + u * blockDim.y, g = h - p.q_heads;
         if (h >= heads) continue;
-        const T* from;
-        if (h < p.q_heads) {
-          from = reinterpret_cast<const T*>(p.q.data) + b * p.q.sb + h * p.q.sh + t * p.q.st;
-          to[u] = reinterpret_cast<T*>(p.q_out.data) + b * p.q_out.sb + h * p.q_out.sh + t * p.q_out.st;
-        } else {
-          const int plane = h - p.q_heads >= p.kv_heads, g = h - p.q_heads - (plane ? p.kv_heads : 0);
-          const RopeView& w = plane ? p.v : p.k;
-          from = reinterpret_cast<const T*>(w.data) + b * w.sb + g * w.sh + t * w.st;
-          to[u] = reinterpret_cast<T*>(p.cache.base) + plane * plane_stride + slot + g * head_stride;
-        }
-        a[u] = *reinterpret_cast<const P*>(from + ea);
-        if (two) c[u] = *reinterpret_cast<const P*>(from + eb);
-      }
-#pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
-        if (!to[u]) continue;
-        if (rotated && h0 + u * blockDim.y < p.q_heads + p.kv_heads) {
+        if (rotated && g < p.kv_heads) {
 #pragma unroll
           for (int j = 0; j < NP; ++j) {
-            T& ex = Items<VE, HALF>::kTwo ? a[u].e[j] : a[u].e[2 * j];
-            T& ey = Items<VE, HALF>::kTwo ? c[u].e[j] : a[u].e[(2 * j + 1) % VE];
+            T& ex = kTwo ? a[u].e[j] : a[u].e[2 * j];
+            T& ey = kTwo ? c[u].e[j] : a[u].e[(2 * j + 1) % VE];
             const float x = to_float<T>(ex), y = to_float<T>(ey);
             ex = from_float<T>(x * cs[j].x - y * cs[j].y);
             ey = from_float<T>(x * cs[j].y + y * cs[j].x);
           }
         }
-        *reinterpret_cast<P*>(to[u] + ea) = a[u];
-        if (two) *reinterpret_cast<P*>(to[u] + eb) = c[u];
+        T* const to = g < 0              ? q_out + h * p.q_out.sh
+                      : g < p.kv_heads ? cache + g * head_stride
+                                       : cache + plane_stride + (g - p.kv_heads) * head_stride;
+        *reinterpret_cast<P*>(to + ea) = a[u];
+        if (two) *reinterpret_cast<P*>(to + eb) = c[u];
       }
     }
   }
@@ -151,8 +164,11 @@ cudaError_t launch_style(const RopeParams& p, cudaStream_t s) {
   const int items = (half || VE == 1 ? p.rot_dim / 2 : p.rot_dim) / VE + (p.head_dim - p.rot_dim) / VE;
   const int heads = p.q_heads + 2 * p.kv_heads;
   cudaLaunchConfig_t cfg = {};
+  // as many heads side by side as make all vectors one round of loads, so that
+  // many small CTAs are resident and have their loads in flight
   const int x = items < kRopeThreads ? items : kRopeThreads;
-  const int y = kRopeThreads / x < heads ? kRopeThreads / x : heads;
+  const int fit = kRopeThreads / x, want = (heads + kRopeUnroll - 1) / kRopeUnroll;
+  const int y = fit < want ? fit : want;
   cfg.gridDim = dim3(p.batch * p.tokens, 1, 1);
   cfg.blockDim = dim3(x, y, 1);
   cfg.stream = s;

@@ -400,6 +400,7 @@ void plan_generic_tree(TreeParams& p, int sms) {
   p.units_per_head = (p.group * p.nodes + RB - 1) / RB;
   p.tile_log2 = kTreeGenTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
+  p.extra = 1;
 }
 
 cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {

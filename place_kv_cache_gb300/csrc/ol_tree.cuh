@@ -68,11 +68,12 @@ __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
 }
 
 // The tiles of all units, in the order (row, kv head, row group of the unit,
-// tile), are cut into n = min(CTAs, T) contiguous shares, none of them empty, of
+// tile), each unit's behind `extra` tiles that stand for what a unit costs
+// besides, are cut into n = min(CTAs, T) contiguous shares, none of them empty, of
 // T / n tiles, the first T % n of one more. A walk gives the CTA its share's
 // segments, one unit's tiles [tile0, tile1) each. A segment that is not its whole
-// unit puts its state into a slot; a share has at most two of them, its first and
-// its last segment: slot 2 c for the one that starts the share, else 2 c + 1.
+// unit puts its state into a slot. A share has at most two of them: the end or the
+// middle of a unit (slot 2 c), and a unit's begin (slot 2 c + 1).
 // Equal shares keep ragged batches balanced to one tile per SM.
 // The constructor is for whole warps; next() may be called by single threads.
 struct TreeWalk {
@@ -83,26 +84,31 @@ struct TreeWalk {
   int at, end;           // next tile of the share; its end
   int share, total;      // its first tile; all tiles
   int each, more;        // tiles of a share; shares of one more
+  int v1;                // tiles of the unit, extra ones included, up to `at`
   int first_nt;          // tiles of row `lane` of the first 32 rows
+
+  __device__ __forceinline__ static int tiles(const TreeParams& p, const TreeRow& r) {
+    return r.ntiles > 0 ? r.ntiles + p.extra : 0;
+  }
 
   __device__ __forceinline__ explicit TreeWalk(const TreeParams& p) {
     const int lane = threadIdx.x & 31, c = blockIdx.x;
     total = 0;
     for (int base = 0; base < p.batch; base += 32) {
-      int nt = base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
+      int nt = base + lane < p.batch ? tiles(p, read_tree_row(p, base + lane)) : 0;
       if (base == 0) first_nt = nt;
       total += __reduce_add_sync(0xffffffffu, nt);
     }
     total *= p.kv_heads * p.units_per_head;
     const int shares = min(total, (int)gridDim.x);
-    at = end = share = each = more = tile0 = slot = 0;
+    at = end = share = each = more = tile0 = tile1 = slot = 0;
     if (c < shares) {
       each = total / shares;
       more = total - each * shares;
       at = share = c * each + min(c, more);
       end = share + each + (c < more);
     }
-    tile1 = at < end ? locate(p, at) : 0;
+    v1 = at < end ? locate(p, at) : 0;
   }
 
   // Finds the unit of tile x (x < total); returns the tile's index in it.
@@ -112,7 +118,7 @@ struct TreeWalk {
     b = g = qg = 0;
     row = TreeRow{0, 0, 0, 0, 1};
     for (int base = 0; base < p.batch; base += 32) {
-      const int nt = base == 0 ? first_nt : base + lane < p.batch ? read_tree_row(p, base + lane).ntiles : 0;
+      const int nt = base == 0 ? first_nt : base + lane < p.batch ? tiles(p, read_tree_row(p, base + lane)) : 0;
       int incl = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -123,12 +129,13 @@ struct TreeWalk {
       if (x < all) {
         const int src = __ffs(__ballot_sync(0xffffffffu, x < incl * per_row)) - 1;
         x -= __shfl_sync(0xffffffffu, incl - nt, src) * per_row;
+        const int mine = __shfl_sync(0xffffffffu, nt, src);
         b = base + src;
         row = read_tree_row(p, b);
-        const int unit = x / row.ntiles;
+        const int unit = x / mine;
         g = unit / p.units_per_head;
         qg = unit - g * p.units_per_head;
-        return x - unit * row.ntiles;
+        return x - unit * mine;
       }
       x -= all;
     }
@@ -137,25 +144,31 @@ struct TreeWalk {
 
   // Moves to the share's next segment.
   __device__ __forceinline__ bool next(const TreeParams& p) {
-    if (at >= end) return false;
-    if (tile1 == row.ntiles) {  // the unit is done: the next one
-      tile1 = 0;
-      if (++qg == p.units_per_head) {
-        qg = 0;
-        if (++g == p.kv_heads) {
-          g = 0;
-          do {
-            if (++b >= p.batch) return false;
-            row = read_tree_row(p, b);
-          } while (row.ntiles == 0);
+    while (at < end) {
+      if (v1 == tiles(p, row)) {  // the unit is done: the next one
+        v1 = 0;
+        if (++qg == p.units_per_head) {
+          qg = 0;
+          if (++g == p.kv_heads) {
+            g = 0;
+            do {
+              if (++b >= p.batch) return false;
+              row = read_tree_row(p, b);
+            } while (row.ntiles == 0);
+          }
         }
       }
+      tile0 = max(v1 - p.extra, 0);
+      const int step = min(tiles(p, row) - v1, end - at);
+      v1 += step;
+      at += step;
+      tile1 = max(v1 - p.extra, 0);
+      if (tile1 > tile0) {
+        slot = 2 * blockIdx.x + (tile0 == 0);
+        return true;
+      }
     }
-    tile0 = tile1;
-    slot = 2 * blockIdx.x + (at == share ? 0 : 1);
-    tile1 = min(row.ntiles, tile0 + (end - at));
-    at += tile1 - tile0;
-    return true;
+    return false;
   }
 
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == row.ntiles; }
@@ -165,7 +178,7 @@ struct TreeWalk {
   __device__ __forceinline__ void write_split(const TreeParams& p) const {
     TreeSplit s = {};
     s.last = -1;
-    if (share < end && tile0 == 0 && tile1 < row.ntiles) {
+    if (share < end && tile0 == 0 && tile1 > 0 && tile1 < row.ntiles) {
       const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
       const int big = more * (each + 1);                // tiles of the shares of one more
       s.last = back < big ? back / (each + 1) : more + (back - big) / each;
