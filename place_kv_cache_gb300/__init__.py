@@ -217,7 +217,10 @@ def _ptr(x) -> Optional[int]:
     if isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):
-        return x.__array_interface__["data"][0]
+        try:  # a third of the time of x.ctypes.data
+            return ctypes.addressof(ctypes.c_char.from_buffer(x))
+        except (TypeError, ValueError, BufferError):  # read-only, empty or strided
+            return x.ctypes.data
     if hasattr(x, "data_ptr"):
         _PTR_OF_TYPE[type(x)] = type(x).data_ptr
         return x.data_ptr()
