@@ -3,85 +3,97 @@
 // take), the merge of both kernels' partial results, and the move of an
 // accepted path.
 //
-// A unit is 32 (head, node) rows of one row's kv head; its tokens form tiles of
-// 32. All units' tiles in order are cut into equal contiguous shares, one per
-// CTA (TreeWalk). A CTA runs the online softmax over its segment of a unit with
-// the scores S = Q K^T and the sums O += P V in registers: 4 rows x 2 tokens of
-// S, 4 rows x D / 16 dimensions of O per thread, operands from shared memory in
-// float4. Bound by fp32 FMA issue: 4 * 32 * D flops per token against 2 * D
-// elements read.
+// A unit is 32 or 64 (head, node) rows of one row's kv head; its tokens form tiles
+// of 32. All units' tiles in order are cut into equal shares, one per CTA
+// (TreeWalk). A CTA runs the online softmax over its segment of a unit with the
+// scores S = Q K^T and the sums O += P V in registers: 4 rows x 2 tokens of S,
+// 4 rows x D / 16 dimensions of O per thread, operands from shared memory four
+// dimensions at a time. K and V lie there as they are in the cache; the next tile
+// is copied in meanwhile. Bound by fp32 FMA issue for many rows (4 * D flops per
+// row and token against 2 * D elements a token), by latency for few.
 #include "ol_tree.cuh"
 
 namespace ol {
 namespace {
 
-constexpr int RB = kTreeGenRows, TB = 1 << kTreeGenTileLog2;
-constexpr int kGenThreads = 128;
-constexpr int kPStride = RB + 4;  // P is kept [token][row]
+constexpr int TB = 1 << kTreeGenTileLog2;
+constexpr int kGenStages = 2;
 
 __host__ __device__ inline int padded(int D) { return (D + 3) / 4 * 4; }
-inline size_t gen_smem(int D) { return sizeof(float) * ((size_t)(RB + 2 * TB) * (padded(D) + 4) + TB * kPStride); }
-
-// Vectors [0, n) of D elements (row r at src(r), NULL: zeros) as fp32 in shared
-// memory, row stride ld, zeros up to the padded size and past n up to `rows`.
-template <typename T, typename Src>
-__device__ __forceinline__ void load_rows(float* dst, int ld, int rows, int D, float factor, Src src) {
-  const int Dp = padded(D);
-  constexpr int VE = 16 / sizeof(T);
-  if (D % VE == 0) {
-    const int pieces = D / VE;
-    for (int i = threadIdx.x; i < rows * pieces; i += kGenThreads) {
-      const int r = i / pieces, c = i % pieces;
-      const T* from = src(r);
-      float f[VE];
-      if (from) {
-        const uint4 w = reinterpret_cast<const uint4*>(from)[c];
-        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < VE; ++j)
-          f[j] = sizeof(T) == 4 ? __uint_as_float(x[j % 4])
-                                : bf16_bits_to_float((uint16_t)(x[j / 2 % 4] >> (16 * (j & 1))));
-      }
-#pragma unroll
-      for (int j = 0; j < VE; ++j) dst[r * ld + c * VE + j] = from ? f[j] * factor : 0.f;
-    }
-  } else {
-    for (int i = threadIdx.x; i < rows * Dp; i += kGenThreads) {
-      const int r = i / Dp, d = i % Dp;
-      const T* from = src(r);
-      float f = 0.f;
-      if (from && d < D) {
-        if constexpr (sizeof(T) == 4)
-          f = from[d];
-        else
-          f = bf16_bits_to_float(from[d]);
-      }
-      dst[r * ld + d] = f * factor;
-    }
-  }
+// bytes of a K or V row in shared memory: 16 more, so that 8 rows cover the banks
+template <typename T>
+__host__ __device__ inline int row_bytes(int D) { return (padded(D) * (int)sizeof(T) + 15) / 16 * 16 + 16; }
+template <typename T, int RB>
+inline size_t gen_smem(int D) {
+  return sizeof(float) * ((size_t)RB * (padded(D) + 4) + TB * (RB + 4)) + (size_t)kGenStages * 2 * TB * row_bytes<T>(D);
 }
 
-// NC: chunks of 64 dimensions (16 threads x 4)
-template <typename T, int NC>
-__global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
-  extern __shared__ __align__(16) float smem[];
-  const int D = p.head_dim, Dp = padded(D), ld = Dp + 4;
-  float* const sq = smem;
-  float* const sk = sq + RB * ld;
-  float* const sv = sk + TB * ld;
-  float* const sp = sv + TB * ld;
+__device__ __forceinline__ float4 load4(const float* x) { return *reinterpret_cast<const float4*>(x); }
+__device__ __forceinline__ float4 load4(const uint16_t* x) {
+  const uint2 w = *reinterpret_cast<const uint2*>(x);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_float(x); }
+
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// NC: chunks of 64 dimensions (16 threads x 4); RB: rows of a unit, 4 threads each
+template <typename T, int NC, int RB>
+__global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ TreeParams p) {
+  constexpr int kThreads = 4 * RB, kPer = kThreads / TB;  // threads that copy a row
+  constexpr int kPStride = RB + 4;                        // P is kept [token][row]
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int D = p.head_dim, Dp = padded(D), ldq = Dp + 4, rb = row_bytes<T>(D);
+  float* const sq = reinterpret_cast<float*>(smem);
+  float* const sp = sq + RB * ldq;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(sp + TB * kPStride);
   const int tid = threadIdx.x, rg = tid / 16, cg = tid % 16;  // rows 4 rg .. 4 rg + 3
   const int R = p.group * p.nodes;
+  const bool vec = D * sizeof(T) % 16 == 0;
   pdl_wait();
   pdl_launch_dependents();
   TreeWalk w(p);
   while (w.next(p)) {
     const int r0 = w.qg * RB;
-    const T* const q = reinterpret_cast<const T*>(p.q) +
-                       ((size_t)w.b * p.q_heads + (size_t)w.g * p.group) * p.nodes * D;
+    const int low_all = p.window < 0 || w.row.prefix <= p.window ? 0 : w.row.prefix - p.window;
+    // tile `tile` into stage `tile` % 2
+    auto copy = [&](int tile) {
+      const int j = tid / kPer, lane = tid % kPer, t = w.row.start + tile * TB + j;
+      uint8_t* const to = ring + (tile % kGenStages * 2 * TB + j) * rb;
+      const bool there = t >= low_all && t < w.row.len;
+#pragma unroll
+      for (int plane = 0; plane < 2; ++plane) {
+        const long long row = there ? cache_row(p.cache, plane, w.b, w.g, t) : -1;
+        if (there && row < 0) set_status(p.status, OL_DEVICE_GUARD);
+        const T* const from = reinterpret_cast<const T*>(p.cache.base) + (row < 0 ? 0 : row * D);
+        uint8_t* const dst = to + plane * TB * rb;
+        if (vec) {
+          for (int c = lane * 16; c < D * (int)sizeof(T); c += kPer * 16)
+            copy16(smem_u32(dst + c), reinterpret_cast<const uint8_t*>(from) + c, row >= 0);
+        } else {
+          for (int d = lane; d < Dp; d += kPer)
+            reinterpret_cast<T*>(dst)[d] = row >= 0 && d < D ? from[d] : T(0);
+        }
+      }
+      copies_commit();
+    };
     __syncthreads();  // the last segment's tiles are read
-    load_rows<T>(sq, ld, RB, D, p.scale_log2,
-                 [&](int r) { return r0 + r < R ? q + (size_t)(r0 + r) * D : (const T*)nullptr; });
+    copy(w.tile0);
+    const T* const q = reinterpret_cast<const T*>(p.q) + tree_out_row(p, w.b, w.g, r0) * D;
+    for (int i = tid; i < RB * Dp; i += kThreads) {
+      const int r = i / Dp, d = i - r * Dp;
+      sq[r * ldq + d] = r0 + r < R && d < D ? as_float(q[(size_t)r * D + d]) * p.scale_log2 : 0.f;
+    }
     int node[4];
     int low[4];  // lowest prefix token of the row
 #pragma unroll
@@ -100,37 +112,44 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
     }
     for (int tile = w.tile0; tile < w.tile1; ++tile) {
       const int t0 = w.row.start + tile * TB;
-      __syncthreads();  // the last tile is read
-      auto token = [&](int plane, int j) -> const T* {
-        const int t = t0 + j;
-        if (t >= w.row.len || (p.window >= 0 && t < w.row.prefix - p.window)) return nullptr;
-        const long long at = cache_row(p.cache, plane, w.b, w.g, t);
-        if (at < 0) set_status(p.status, OL_DEVICE_GUARD);
-        return at < 0 ? nullptr : reinterpret_cast<const T*>(p.cache.base) + at * D;
-      };
-      load_rows<T>(sk, ld, TB, D, 1.f, [&](int j) { return token(0, j); });
-      load_rows<T>(sv, ld, TB, D, 1.f, [&](int j) { return token(1, j); });
+      if (tile + 1 < w.tile1) {
+        copy(tile + 1);
+        copies_wait<1>();
+      } else {
+        copies_wait<0>();
+      }
       __syncthreads();
+      const uint8_t* const sk = ring + tile % kGenStages * 2 * TB * rb;
+      const uint8_t* const sv = sk + TB * rb;
       float s[4][2];
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r][0] = s[r][1] = 0.f;
+      const T* const k_lo = reinterpret_cast<const T*>(sk + cg * rb);
+      const T* const k_hi = reinterpret_cast<const T*>(sk + (cg + 16) * rb);
+#pragma unroll 4
       for (int d = 0; d < Dp; d += 4) {
-        const float4 k0 = *reinterpret_cast<const float4*>(sk + cg * ld + d);
-        const float4 k1 = *reinterpret_cast<const float4*>(sk + (cg + 16) * ld + d);
+        const float4 k0 = load4(k_lo + d), k1 = load4(k_hi + d);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float4 a = *reinterpret_cast<const float4*>(sq + (4 * rg + r) * ld + d);
+          const float4 a = *reinterpret_cast<const float4*>(sq + (4 * rg + r) * ldq + d);
           s[r][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
           s[r][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
         }
       }
-      const bool edge = p.window >= 0 || t0 + TB > w.row.prefix;  // some row may not see some token
-      if (edge) {
+      const bool drafted = t0 + TB > w.row.prefix;
+      const bool edge = p.window >= 0 || drafted;  // some row may not see some token
+      if (drafted) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             if (!tree_sees(p, w.row, w.b, node[r], low[r], t0 + cg + 16 * u)) s[r][u] = -INFINITY;
+      } else if (edge) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (t0 + cg + 16 * u < low[r]) s[r][u] = -INFINITY;
       }
       float pr[4][2];
 #pragma unroll
@@ -148,9 +167,7 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
           pr[r][u] = exp2f(s[r][u] - base);
           sum += pr[r][u];
         }
-#pragma unroll
-        for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-        l[r] = l[r] * keep + sum;
+        l[r] = l[r] * keep + sum;  // of this thread's tokens
         if (keep != 1.f)
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -164,7 +181,8 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
       for (int u = 0; u < 2; ++u)
         *reinterpret_cast<float4*>(sp + (cg + 16 * u) * kPStride + 4 * rg) =
             make_float4(pr[0][u], pr[1][u], pr[2][u], pr[3][u]);
-      __syncthreads();
+      __syncwarp();  // P of the warp's eight rows: its own
+#pragma unroll 4
       for (int j = 0; j < TB; ++j) {
         const float4 p4 = *reinterpret_cast<const float4*>(sp + j * kPStride + 4 * rg);
         const float pj[4] = {p4.x, p4.y, p4.z, p4.w};
@@ -172,7 +190,7 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
         for (int c = 0; c < NC; ++c) {
           const int d = c * 64 + cg * 4;
           if (d >= Dp) continue;
-          const float4 v = *reinterpret_cast<const float4*>(sv + j * ld + d);
+          const float4 v = load4(reinterpret_cast<const T*>(sv + j * rb) + d);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if (edge && pj[r] == 0.f) continue;  // a hidden token's V may hold infinities or NaN
@@ -183,7 +201,12 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
           }
         }
       }
+      __syncthreads();  // the stage is read
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], x);
     // the rows that this segment holds alone are done; others go to its slot
     float* const slot = w.whole() ? nullptr : tree_slot(p, w.slot);
 #pragma unroll
@@ -217,13 +240,26 @@ __global__ void __launch_bounds__(kGenThreads) tree_kernel(const TreeParams p) {
   if (tid == 0) w.write_split(p);
 }
 
-template <typename T, int NC>
+template <typename T, int NC, int RB>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
-  const size_t smem = gen_smem(p.head_dim);
   static const cudaError_t attr = cudaFuncSetAttribute(
-      tree_kernel<T, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gen_smem(64 * NC));
+      tree_kernel<T, NC, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gen_smem<T, RB>(64 * NC));
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(tree_kernel<T, NC>, dim3(p.nctas), dim3(kGenThreads), smem, s, p);
+  return launch_pdl(tree_kernel<T, NC, RB>, dim3(p.nctas), dim3(4 * RB), gen_smem<T, RB>(p.head_dim), s, p);
+}
+
+template <typename T>
+cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
+  const int nc = (p.head_dim + 63) / 64;
+  if (p.rows_per_unit == 32)
+    return nc == 1   ? launch_tree<T, 1, 32>(p, s)
+           : nc == 2 ? launch_tree<T, 2, 32>(p, s)
+           : nc == 3 ? launch_tree<T, 3, 32>(p, s)
+                     : launch_tree<T, 4, 32>(p, s);
+  return nc == 1   ? launch_tree<T, 1, 64>(p, s)
+         : nc == 2 ? launch_tree<T, 2, 64>(p, s)
+         : nc == 3 ? launch_tree<T, 3, 64>(p, s)
+                   : launch_tree<T, 4, 64>(p, s);
 }
 
 // ------------------------------------------------------------------- the merge
@@ -396,24 +432,16 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const KeepParam
 }  // namespace
 
 void plan_generic_tree(TreeParams& p, int sms) {
-  p.rows_per_unit = RB;
-  p.units_per_head = (p.group * p.nodes + RB - 1) / RB;
+  // one unit where 64 rows hold all of a kv head's: its K/V are read once
+  p.rows_per_unit = tree_gen_rows(p.group, p.nodes);
+  p.units_per_head = (p.group * p.nodes + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeGenTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
-  p.extra = 1;
+  p.extra = 2;
 }
 
 cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
-  const int nc = (p.head_dim + 63) / 64;
-  if (p.dtype == OL_F32)
-    return nc == 1 ? launch_tree<float, 1>(p, s)
-           : nc == 2 ? launch_tree<float, 2>(p, s)
-           : nc == 3 ? launch_tree<float, 3>(p, s)
-                     : launch_tree<float, 4>(p, s);
-  return nc == 1 ? launch_tree<uint16_t, 1>(p, s)
-         : nc == 2 ? launch_tree<uint16_t, 2>(p, s)
-         : nc == 3 ? launch_tree<uint16_t, 3>(p, s)
-                   : launch_tree<uint16_t, 4>(p, s);
+  return p.dtype == OL_F32 ? launch_rows<float>(p, s) : launch_rows<uint16_t>(p, s);
 }
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
