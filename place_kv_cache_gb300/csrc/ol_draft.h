@@ -105,13 +105,14 @@ OL_HD inline TreeRow tree_row(int len, int count, int window, int tile_log2) {
 
 // One partial slot: m[rows] (log2 domain), l[rows], o[ceil(D / 4)][rows] float4.
 OL_HD inline size_t tree_slot_floats(int rows, int head_dim) { return (size_t)rows * (2 + (head_dim + 3) / 4 * 4); }
-constexpr size_t kTreeSplitBytes = 2 * kTreeMaxCtas * sizeof(TreeSplit);
+constexpr size_t kTreeSplitBytes = 4 * kTreeMaxCtas * sizeof(TreeSplit);
 // (head, node) rows of a unit of the CUDA-core and of the tensor-core kernel
 inline int tree_gen_rows(int group, int nodes) { return group * nodes <= 32 ? 32 : 64; }
 inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }
 inline size_t tree_workspace_bytes(int q_heads, int kv_heads, int head_dim, int nodes) {
   const size_t fast = 2ull * kTreeMaxCtas * tree_slot_floats(tree_fast_rows(q_heads / kv_heads, nodes), head_dim);
-  const size_t gen = 2ull * 2 * kTreeMaxCtas * tree_slot_floats(tree_gen_rows(q_heads / kv_heads, nodes), head_dim);
+  const int rows = tree_gen_rows(q_heads / kv_heads, nodes);
+  const size_t gen = 2ull * (128 / rows) * kTreeMaxCtas * tree_slot_floats(rows, head_dim);
   return kStatusBytes + kTreeSplitBytes + sizeof(float) * (fast > gen ? fast : gen);
 }
 

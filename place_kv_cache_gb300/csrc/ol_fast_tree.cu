@@ -260,14 +260,6 @@ struct Maps {
   CUtensorMap q, kv;
 };
 
-// Bits [a, b) of a 32-bit word (a and b may lie outside it).
-__device__ __forceinline__ uint32_t bit_range(int a, int b) {
-  a = max(a, 0);
-  b = min(b, 32);
-  if (a >= b) return 0;
-  return (b == 32 ? 0xffffffffu : (1u << b) - 1u) & ~((1u << a) - 1u);
-}
-
 // Drafted tokens [j0, j0 + 32) among `bits` that lie within the window of a node.
 __device__ __noinline__ uint32_t in_window(const TreeParams& p, const TreeRow row, int b, int node, int j0, uint32_t bits) {
   const int at = tree_position(p, row, b, node);
@@ -276,27 +268,6 @@ __device__ __noinline__ uint32_t in_window(const TreeParams& p, const TreeRow ro
     if ((long long)at - tree_position(p, row, b, j0 + c) > p.window) bits &= ~(1u << c);
   }
   return bits;
-}
-
-// Visibility of tokens [t, t + 32) for a node, as bits, but for the window among
-// drafted tokens: m are its mask words (NULL: a chain).
-__device__ __noinline__ uint32_t visible_word(const uint64_t* m, int words, int prefix, int count, int node, int low,
-                                              int t) {
-  const uint32_t bits = bit_range(low - t, prefix - t);
-  const int j0 = t - prefix;  // drafted index of bit 0
-  if (j0 <= -32 || j0 >= count) return bits;
-  uint32_t tree;
-  if (!m) {
-    tree = bit_range(-32, node + 1 - j0);
-  } else if (j0 < 0) {
-    tree = (uint32_t)m[0] << -j0;
-  } else {
-    const int w = j0 / 64, s = j0 % 64;
-    uint64_t v = m[w] >> s;
-    if (s > 32 && w + 1 < words) v |= m[w + 1] << (64 - s);
-    tree = (uint32_t)v;
-  }
-  return bits | (tree & bit_range(-j0, count - j0));
 }
 
 // Adds the non-finite elements, in dimensions [d0, d1), of the V of drafted

@@ -25,7 +25,7 @@ template <typename T>
 __host__ __device__ inline int row_bytes(int D) { return (padded(D) * (int)sizeof(T) + 15) / 16 * 16 + 16; }
 template <typename T, int RB>
 inline size_t gen_smem(int D) {
-  return sizeof(float) * ((size_t)RB * (padded(D) + 4) + TB * (RB + 4)) + (size_t)kGenStages * 2 * TB * row_bytes<T>(D);
+  return sizeof(float) * (size_t)TB * (RB + 4) + (size_t)(RB + kGenStages * 2 * TB) * row_bytes<T>(D);
 }
 
 __device__ __forceinline__ float4 load4(const float* x) { return *reinterpret_cast<const float4*>(x); }
@@ -34,8 +34,6 @@ __device__ __forceinline__ float4 load4(const uint16_t* x) {
   return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                      __uint_as_float(w.y & 0xffff0000u));
 }
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(uint16_t x) { return bf16_bits_to_float(x); }
 
 // 16 bytes to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
@@ -47,16 +45,19 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
+// CTAs of RB rows per SM that 128 registers a thread allow (up to 128 dimensions; beyond, half as many)
+constexpr int gen_per_sm(int NC, int RB) { return (NC <= 2 ? 128 : 64) / RB; }
+
 // NC: chunks of 64 dimensions (16 threads x 4); RB: rows of a unit, 4 threads each
 template <typename T, int NC, int RB>
-__global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const __grid_constant__ TreeParams p) {
   constexpr int kThreads = 4 * RB, kPer = kThreads / TB;  // threads that copy a row
   constexpr int kPStride = RB + 4;                        // P is kept [token][row]
   extern __shared__ __align__(16) uint8_t smem[];
-  const int D = p.head_dim, Dp = padded(D), ldq = Dp + 4, rb = row_bytes<T>(D);
-  float* const sq = reinterpret_cast<float*>(smem);
-  float* const sp = sq + RB * ldq;
-  uint8_t* const ring = reinterpret_cast<uint8_t*>(sp + TB * kPStride);
+  const int D = p.head_dim, Dp = padded(D), rb = row_bytes<T>(D);
+  float* const sp = reinterpret_cast<float*>(smem);
+  uint8_t* const sq = reinterpret_cast<uint8_t*>(sp + TB * kPStride);
+  uint8_t* const ring = sq + RB * rb;
   const int tid = threadIdx.x, rg = tid / 16, cg = tid % 16;  // rows 4 rg .. 4 rg + 3
   const int R = p.group * p.nodes;
   const bool vec = D * sizeof(T) % 16 == 0;
@@ -66,40 +67,43 @@ __global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ Tr
   while (w.next(p)) {
     const int r0 = w.qg * RB;
     const int low_all = p.window < 0 || w.row.prefix <= p.window ? 0 : w.row.prefix - p.window;
+    // a row of D elements (or zeros) to shared memory, by `lanes` threads
+    auto copy_row = [&](uint8_t* to, const T* from, bool there, int lane, int lanes) {
+      if (vec) {
+        for (int c = lane * 16; c < D * (int)sizeof(T); c += lanes * 16)
+          copy16(smem_u32(to + c), reinterpret_cast<const uint8_t*>(from) + c, there);
+      } else {
+        for (int d = lane; d < Dp; d += lanes) reinterpret_cast<T*>(to)[d] = there && d < D ? from[d] : T(0);
+      }
+    };
     // tile `tile` into stage `tile` % 2
     auto copy = [&](int tile) {
-      const int j = tid / kPer, lane = tid % kPer, t = w.row.start + tile * TB + j;
+      const int j = tid / kPer, t = w.row.start + tile * TB + j;
       uint8_t* const to = ring + (tile % kGenStages * 2 * TB + j) * rb;
       const bool there = t >= low_all && t < w.row.len;
 #pragma unroll
       for (int plane = 0; plane < 2; ++plane) {
         const long long row = there ? cache_row(p.cache, plane, w.b, w.g, t) : -1;
         if (there && row < 0) set_status(p.status, OL_DEVICE_GUARD);
-        const T* const from = reinterpret_cast<const T*>(p.cache.base) + (row < 0 ? 0 : row * D);
-        uint8_t* const dst = to + plane * TB * rb;
-        if (vec) {
-          for (int c = lane * 16; c < D * (int)sizeof(T); c += kPer * 16)
-            copy16(smem_u32(dst + c), reinterpret_cast<const uint8_t*>(from) + c, row >= 0);
-        } else {
-          for (int d = lane; d < Dp; d += kPer)
-            reinterpret_cast<T*>(dst)[d] = row >= 0 && d < D ? from[d] : T(0);
-        }
+        copy_row(to + plane * TB * rb, reinterpret_cast<const T*>(p.cache.base) + (row < 0 ? 0 : row * D), row >= 0,
+                 tid % kPer, kPer);
       }
       copies_commit();
     };
     __syncthreads();  // the last segment's tiles are read
-    copy(w.tile0);
-    const T* const q = reinterpret_cast<const T*>(p.q) + tree_out_row(p, w.b, w.g, r0) * D;
-    for (int i = tid; i < RB * Dp; i += kThreads) {
-      const int r = i / Dp, d = i - r * Dp;
-      sq[r * ldq + d] = r0 + r < R && d < D ? as_float(q[(size_t)r * D + d]) * p.scale_log2 : 0.f;
+    {
+      const int r = tid / 4;
+      const T* const q = reinterpret_cast<const T*>(p.q) + tree_out_row(p, w.b, w.g, r0) * D;
+      copy_row(sq + r * rb, r0 + r < R ? q + (size_t)r * D : q, r0 + r < R, tid % 4, 4);
     }
+    copy(w.tile0);
     int node[4];
-    int low[4];  // lowest prefix token of the row
+    int at[4], low[4];  // with a window: the rows' positions, their lowest prefix token
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       node[r] = (r0 + 4 * rg + r) % p.nodes;
-      low[r] = p.window < 0 ? 0 : tree_low(p, w.row, w.b, node[r]);
+      at[r] = p.window < 0 ? 0 : tree_position(p, w.row, w.b, node[r]);
+      low[r] = p.window < 0 || at[r] <= p.window ? 0 : at[r] - p.window;
     }
     float m[4], l[4];
     float4 o[4][NC];
@@ -131,20 +135,32 @@ __global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ Tr
         const float4 k0 = load4(k_lo + d), k1 = load4(k_hi + d);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float4 a = *reinterpret_cast<const float4*>(sq + (4 * rg + r) * ldq + d);
+          const float4 a = load4(reinterpret_cast<const T*>(sq + (4 * rg + r) * rb) + d);
           s[r][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
           s[r][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
         }
       }
-      const bool drafted = t0 + TB > w.row.prefix;
-      const bool edge = p.window >= 0 || drafted;  // some row may not see some token
-      if (drafted) {
+      const bool drafted = t0 + TB > w.row.prefix;  // some row may not see some token of the tile
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r) s[r][0] *= p.scale_log2, s[r][1] *= p.scale_log2;
+      if (drafted) {
+        int pos[2] = {0, 0};  // of this thread's tokens
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int j = t0 + cg + 16 * u - w.row.prefix;
+          if (p.window >= 0 && j >= 0 && j < w.row.count) pos[u] = tree_position(p, w.row, w.b, j);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint64_t* const words = p.mask ? p.mask + ((size_t)w.b * p.nodes + node[r]) * p.words : nullptr;
+          const uint32_t seen = visible_word(words, p.words, w.row.prefix, w.row.count, node[r], low[r], t0);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            if (!tree_sees(p, w.row, w.b, node[r], low[r], t0 + cg + 16 * u)) s[r][u] = -INFINITY;
-      } else if (edge) {
+            if (!(seen >> (cg + 16 * u) & 1) || (p.window >= 0 && t0 + cg + 16 * u >= w.row.prefix &&
+                                                 (long long)at[r] - pos[u] > p.window))
+              s[r][u] = -INFINITY;
+        }
+      } else if (p.window >= 0) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -193,7 +209,7 @@ __global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ Tr
           const float4 v = load4(reinterpret_cast<const T*>(sv + j * rb) + d);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            if (edge && pj[r] == 0.f) continue;  // a hidden token's V may hold infinities or NaN
+            if (drafted && pj[r] == 0.f) continue;  // a hidden token's V may hold infinities or NaN
             o[r][c].x += pj[r] * v.x;
             o[r][c].y += pj[r] * v.y;
             o[r][c].z += pj[r] * v.z;
@@ -242,8 +258,13 @@ __global__ void __launch_bounds__(4 * RB) tree_kernel(const __grid_constant__ Tr
 
 template <typename T, int NC, int RB>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      tree_kernel<T, NC, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)gen_smem<T, RB>(64 * NC));
+  static const cudaError_t attr = [] {
+    const cudaError_t e = cudaFuncSetAttribute(tree_kernel<T, NC, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)gen_smem<T, RB>(64 * NC));
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(tree_kernel<T, NC, RB>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
+  }();
   if (attr != cudaSuccess) return attr;
   return launch_pdl(tree_kernel<T, NC, RB>, dim3(p.nctas), dim3(4 * RB), gen_smem<T, RB>(p.head_dim), s, p);
 }
@@ -436,7 +457,12 @@ void plan_generic_tree(TreeParams& p, int sms) {
   p.rows_per_unit = tree_gen_rows(p.group, p.nodes);
   p.units_per_head = (p.group * p.nodes + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeGenTileLog2;
-  p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
+  // as many CTAs as are resident
+  const bool f32 = p.dtype == OL_F32, few = p.rows_per_unit == 32;
+  const size_t smem = f32 ? (few ? gen_smem<float, 32>(p.head_dim) : gen_smem<float, 64>(p.head_dim))
+                          : (few ? gen_smem<uint16_t, 32>(p.head_dim) : gen_smem<uint16_t, 64>(p.head_dim));
+  const int fit = (int)(228 * 1024 / (smem + 1024)), regs = gen_per_sm((p.head_dim + 63) / 64, p.rows_per_unit);
+  p.nctas = (fit < regs ? fit : regs) * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   p.extra = 2;
 }
 
