@@ -51,14 +51,14 @@ constexpr int kTreeMaxCtas = 192;  // CTAs of the tensor-core kernel, one per SM
 constexpr int kTreeGenTileLog2 = 5;   // tokens of its tile: 32
 constexpr int kTreeFastTileLog2 = 7;  // 128
 
-// The unit that begins in a CTA's share and reaches past its end, if there is one.
+// What there is to merge: of the unit that begins in a share and reaches past its
+// end, or of a unit (TreeParams::by_unit).
 struct alignas(16) TreeSplit {
-  int last;   // its last share, -1: no such unit
-  int slot;   // slot of its first segment
+  int first, last;  // shares of the unit's segments; last -1: nothing to merge
   int count;  // nodes of its row
   int rows;   // live (head, node) rows
   long long out;  // row of q and out of its row 0
-  int first;      // (head, node) row 0 of the unit
+  int row0;       // (head, node) row 0 of the unit
   int pad;
 };
 
@@ -76,7 +76,7 @@ struct TreeParams {
   void* out;
   int out_dtype;
   int32_t* status;
-  struct TreeSplit* splits;     // [nctas], written by every CTA of the attention for the merge
+  struct TreeSplit* splits;     // [nctas] or [units], written by the attention's CTAs for the merge
   float* partials;
   // work split
   int rows_per_unit;            // (head, node) rows r = head * nodes + node of a unit
@@ -84,7 +84,11 @@ struct TreeParams {
   int tile_log2;                // tokens per tile
   int nctas;                    // the tiles of all units in contiguous equal shares
   int extra;                    // tiles that a unit's begin and end cost besides
+  int by_unit;                  // 1: few units, each cut into many segments; the merge goes by units
 };
+inline bool tree_few_units(const TreeParams& p) {
+  return (long long)p.batch * p.kv_heads * p.units_per_head * 4 <= p.nctas;
+}
 
 // A row's tokens as the work split sees them: drafted tokens are
 // [prefix, len), tokens [start, len) form ntiles tiles (start is a multiple of

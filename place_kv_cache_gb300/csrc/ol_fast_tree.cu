@@ -541,11 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 3) {
     // -------------------------------------------------------------- the merge's note
-    if (lane == 0) {
-      while (w.next(p)) {
-      }
-      w.write_split(p);
-    }
+    if (lane == 0) w.write_splits(p);
   } else {
     // ----------------------------------------------------------------- streams
     const int j = (warp - 4) / 4, row = tid % 128;  // TMEM lane
@@ -906,6 +902,7 @@ void plan_fast_tree(TreeParams& p, int sms) {
   // Measured (0 / 2 / 4 tiles): 64 nodes over 32 ragged rows (two query tiles) 176 / 155 / 146 us, 16 nodes over 64
   // ragged rows (one) 367 / 360 / 362 us.
   p.extra = p.rows_per_unit == 256 ? 4 : 2;
+  p.by_unit = tree_few_units(p);
 }
 
 cudaError_t launch_fast_tree(const TreeParams& p, cudaStream_t s) {

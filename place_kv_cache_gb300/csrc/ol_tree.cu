@@ -64,6 +64,10 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
   pdl_wait();
   pdl_launch_dependents();
   TreeWalk w(p);
+  if (tid == kThreads - 1) {
+    TreeWalk notes = w;
+    notes.write_splits(p);
+  }
   while (w.next(p)) {
     const int r0 = w.qg * RB;
     const int low_all = p.window < 0 || w.row.prefix <= p.window ? 0 : w.row.prefix - p.window;
@@ -253,7 +257,6 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
       }
     }
   }
-  if (tid == 0) w.write_split(p);
 }
 
 template <typename T, int NC, int RB>
@@ -286,33 +289,33 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
 // ------------------------------------------------------------------- the merge
 
 // CTA x merges the unit that begins in share x and reaches past it, if there is
-// one (TreeSplit): rows [ROWS y, ROWS (y + 1)).
+// one, or unit x (TreeSplit): rows [ROWS y, ROWS (y + 1)).
 //   M = max m_s, L = sum l_s 2^(m_s - M), y = sum o_s 2^(m_s - M) / L
 // A thread has a row, KG groups of four dimensions (the slots' layout keeps the
 // rows of a group together) and one of G shares of the segments. 16 loads of o
 // are on their way before the weights are known; more segments than that are
 // taken in chunks with a running maximum. Bound by latency for few units (8 rows
-// a CTA, for more CTAs), else by reading the partials from L2 (32 rows).
+// a CTA, for more CTAs, 20 loads), else by reading the partials from L2 (32 rows).
 template <int ROWS, int THREADS, int D4>  // D4: groups of four dimensions, 32 or 64
 __global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p) {
   constexpr int kLanes = THREADS / ROWS;  // threads of a row
   constexpr int G = kLanes > D4 ? kLanes / D4 : 1, KG = kLanes > D4 ? 1 : D4 / kLanes;
-  constexpr int C = 16 / KG, kChunk = C * G;  // segments of a thread and of the CTA at a time
+  constexpr int C = (ROWS == 8 && D4 == 32 ? 20 : 16) / KG, kChunk = C * G;  // segments of a thread and of the CTA at a time
   static_assert(C >= 2 && kChunk * ROWS <= THREADS, "a thread loads one state");
   __shared__ float2 state[kChunk][ROWS];  // m, l
   __shared__ float4 other[G > 1 ? (G - 1) * ROWS * D4 : 1];
   __shared__ float other_l[G > 1 ? (G - 1) * ROWS : 1];
   pdl_wait();
   pdl_launch_dependents();
+  if (p.by_unit && read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head)).ntiles == 0) return;  // no note
   const TreeSplit u = p.splits[blockIdx.x];
   if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
   const int RU = p.rows_per_unit, D = p.head_dim;
   const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS, d0 = lane % D4, grp = lane / D4;
   const int place = blockIdx.y * ROWS + lr;  // row of the unit
-  const bool mine = place < u.rows && (u.first + place) % p.nodes < u.count;
-  const int first = blockIdx.x, segs = u.last - first + 1;
-  // the later shares begin with the unit's segment
-  auto slot_of = [&](int i) { return tree_slot(p, i == 0 ? u.slot : 2 * (first + i)); };
+  const bool mine = place < u.rows && (u.row0 + place) % p.nodes < u.count;
+  const int segs = u.last - u.first + 1;
+  auto slot_of = [&](int i) { return tree_slot(p, 2 * (u.first + i) + (i == 0)); };
   float M = -INFINITY, L = 0.f;
   float4 acc[KG];
 #pragma unroll
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p)
 
 template <int ROWS, int THREADS>
 cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
-  const dim3 grid(p.nctas, (rows + ROWS - 1) / ROWS), block(THREADS);
+  const dim3 grid(p.by_unit ? p.batch * p.kv_heads * p.units_per_head : p.nctas, (rows + ROWS - 1) / ROWS), block(THREADS);
   return p.head_dim <= 128 ? launch_pdl(tree_merge_kernel<ROWS, THREADS, 32>, grid, block, 0, s, p)
                            : launch_pdl(tree_merge_kernel<ROWS, THREADS, 64>, grid, block, 0, s, p);
 }
@@ -464,6 +467,7 @@ void plan_generic_tree(TreeParams& p, int sms) {
   const int fit = (int)(228 * 1024 / (smem + 1024)), regs = gen_per_sm((p.head_dim + 63) / 64, p.rows_per_unit);
   p.nctas = (fit < regs ? fit : regs) * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   p.extra = 2;
+  p.by_unit = tree_few_units(p);
 }
 
 cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
@@ -472,8 +476,7 @@ cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
-  const bool few = (long long)p.batch * p.kv_heads * p.units_per_head * 4 <= p.nctas;
-  return few ? launch_merge<8, 512>(p, rows, s) : launch_merge<32, 256>(p, rows, s);
+  return p.by_unit ? launch_merge<8, 512>(p, rows, s) : launch_merge<32, 256>(p, rows, s);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {

@@ -197,22 +197,27 @@ struct TreeWalk {
 
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == row.ntiles; }
 
-  // After the share's last segment: what the merge needs of a unit that begins
-  // here and reaches past the share's end. One thread calls it.
-  __device__ __forceinline__ void write_split(const TreeParams& p) const {
+  // The share's notes for the merge, by one thread, on a walk of its own.
+  __device__ __forceinline__ void write_splits(const TreeParams& p) {
     TreeSplit s = {};
     s.last = -1;
-    if (share < end && tile0 == 0 && tile1 > 0 && tile1 < row.ntiles) {
-      const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
-      const int big = more * (each + 1);                // tiles of the shares of one more
-      s.last = back < big ? back / (each + 1) : more + (back - big) / each;
-      s.slot = slot;
-      s.count = row.count;
-      s.first = qg * p.rows_per_unit;
-      s.rows = min(p.rows_per_unit, p.group * p.nodes - s.first);
-      s.out = (long long)tree_out_row(p, b, g, s.first);
+    while (next(p)) {
+      if (tile0 > 0) continue;  // the unit began in an earlier share
+      s.first = blockIdx.x;
+      s.last = -1;
+      if (tile1 < row.ntiles) {
+        const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
+        const int big = more * (each + 1);                // tiles of the shares of one more
+        s.last = back < big ? back / (each + 1) : more + (back - big) / each;
+        s.count = row.count;
+        s.row0 = qg * p.rows_per_unit;
+        s.rows = min(p.rows_per_unit, p.group * p.nodes - s.row0);
+        s.out = (long long)tree_out_row(p, b, g, s.row0);
+      }
+      if (p.by_unit) p.splits[(b * p.kv_heads + g) * p.units_per_head + qg] = s;
     }
-    p.splits[blockIdx.x] = s;
+    // (only the share's last unit can reach past its end)
+    if (!p.by_unit) p.splits[blockIdx.x] = s;
   }
 };
 
