@@ -12,7 +12,8 @@
 // the launch itself for a decode step. One CTA takes one token of one row and
 // all of its q, k and v vectors, so the token's sines and cosines are computed
 // once (rot_dim / 2 threads, through shared memory) and serve every head. Its
-// first vectors are on their way before the positions are known.
+// first vectors are on their way before the positions are known. Measured:
+// 4 x 4096 fp32 tokens of 40 heads 98.6 us, 6.8 TB/s; in bf16 58 us, 5.8 TB/s.
 #include "ol_common.cuh"
 #include "ol_draft.h"
 
@@ -20,7 +21,6 @@ namespace ol {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;  // vectors in flight per thread
 constexpr int kRopeMaxHalf = 512;
 
 template <typename T>
@@ -49,6 +49,7 @@ struct alignas(sizeof(T) * VE) Piece {
 template <int VE, bool HALF>
 struct Items {
   static constexpr bool kTwo = HALF || VE == 1;  // a rotated item has two pieces
+  static constexpr int kUnroll = kTwo ? 2 : 4;   // items in flight per thread
   int rotated, total;                            // items
   __device__ Items(int rot_dim, int head_dim)
       : rotated(kTwo ? rot_dim / 2 / VE : rot_dim / VE), total(rotated + (head_dim - rot_dim) / VE) {}
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   using P = Piece<T, VE>;
   constexpr bool kTwo = Items<VE, HALF>::kTwo;
   constexpr int NP = kTwo ? VE : VE / 2;  // pairs of an item
+  constexpr int kUnroll = Items<VE, HALF>::kUnroll;
   __shared__ float2 turn[kRopeMaxHalf];   // (cos, sin) * magnitude of this token
   const int b = blockIdx.x / p.tokens, t = blockIdx.x - b * p.tokens;
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthreads = blockDim.x * blockDim.y;
@@ -72,13 +74,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const T* const q_row = reinterpret_cast<const T*>(p.q.data) + b * p.q.sb + t * p.q.st;
   const T* const k_row = reinterpret_cast<const T*>(p.k.data) + b * p.k.sb + t * p.k.st;
   const T* const v_row = reinterpret_cast<const T*>(p.v.data) + b * p.v.sb + t * p.v.st;
-  P a[kRopeUnroll], c[kRopeUnroll];
+  P a[kUnroll], c[kUnroll];
   // pieces of item i of heads h0, h0 + blockDim.y, ...
   auto load = [&](int i, int h0) {
     const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
     const bool two = kTwo && i < items.rotated;
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * blockDim.y;
       if (h >= heads) continue;
       const int g = h - p.q_heads;
@@ -131,11 +133,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     if (rotated)
 #pragma unroll
       for (int j = 0; j < NP; ++j) cs[j] = turn[i * NP + j];
-    for (int h0 = threadIdx.y; h0 < heads; h0 += blockDim.y * kRopeUnroll) {
+    for (int h0 = threadIdx.y; h0 < heads; h0 += blockDim.y * kUnroll) {
       if (!loaded) load(i, h0);
       loaded = false;
 #pragma unroll
-      for (int u = 0; u < kRopeUnroll; ++u) {
+      for (int u = 0; u < kUnroll; ++u) {
         const int h = h0 + u * blockDim.y, g = h - p.q_heads;
         if (h >= heads) continue;
         if (rotated && g < p.kv_heads) {
@@ -158,16 +160,22 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-template <typename T, int VE>
+template <typename T, int VE, bool HALF>
 cudaError_t launch_style(const RopeParams& p, cudaStream_t s) {
-  const bool half = p.style == OL_ROPE_HALF;
-  const int items = (half || VE == 1 ? p.rot_dim / 2 : p.rot_dim) / VE + (p.head_dim - p.rot_dim) / VE;
+  using I = Items<VE, HALF>;
+  const int items = (I::kTwo ? p.rot_dim / 2 : p.rot_dim) / VE + (p.head_dim - p.rot_dim) / VE;
   const int heads = p.q_heads + 2 * p.kv_heads;
   cudaLaunchConfig_t cfg = {};
-  // as many heads side by side as make all vectors one round of loads, so that
-  // many small CTAs are resident and have their loads in flight
-  const int x = items < kRopeThreads ? items : kRopeThreads;
-  const int fit = kRopeThreads / x, want = (heads + kRopeUnroll - 1) / kRopeUnroll;
+  // 16-bit vectors of many tokens: CTAs of 64 threads, whose loads and stores
+  // interleave finer (4 x 4096 tokens of 32 + 2 * 8 heads of 128: half style
+  // 69 us against 90 of 256 threads, interleaved 91 against 110). fp32 has twice
+  // the bytes a thread: 118 us of 256 threads against 122 of 64, 122 against
+  // 130. A few tokens are one wave either way: all of a token's vectors in one
+  // round of loads (a decode step's append 3.4 us).
+  const bool many = (long long)p.batch * p.tokens > 2048;
+  const int most = sizeof(T) == 2 && many ? 64 : kRopeThreads;
+  const int x = items < most ? items : most;
+  const int fit = most / x, want = (heads + I::kUnroll - 1) / I::kUnroll;
   const int y = fit < want ? fit : want;
   cfg.gridDim = dim3(p.batch * p.tokens, 1, 1);
   cfg.blockDim = dim3(x, y, 1);
@@ -177,15 +185,20 @@ cudaError_t launch_style(const RopeParams& p, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return half ? cudaLaunchKernelEx(&cfg, rope_kernel<T, VE, true>, p)
-              : cudaLaunchKernelEx(&cfg, rope_kernel<T, VE, false>, p);
+  return cudaLaunchKernelEx(&cfg, rope_kernel<T, VE, HALF>, p);
+}
+
+template <typename T>
+cudaError_t launch_type(const RopeParams& p, cudaStream_t s) {
+  constexpr int VE = 16 / sizeof(T);
+  if (p.style == OL_ROPE_HALF) return p.vec ? launch_style<T, VE, true>(p, s) : launch_style<T, 1, true>(p, s);
+  return p.vec ? launch_style<T, VE, false>(p, s) : launch_style<T, 1, false>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t s) {
-  if (p.dtype == OL_F32) return p.vec ? launch_style<float, 4>(p, s) : launch_style<float, 1>(p, s);
-  return p.vec ? launch_style<uint16_t, 8>(p, s) : launch_style<uint16_t, 1>(p, s);
+  return p.dtype == OL_F32 ? launch_type<float>(p, s) : launch_type<uint16_t>(p, s);
 }
 
 }  // namespace ol
