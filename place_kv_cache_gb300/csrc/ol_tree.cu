@@ -412,24 +412,37 @@ cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
 
 // One CTA per (row, kv head, plane) moves the kept tokens' vectors. kept ascends
 // strictly, so kept[j] >= j and vector j's source is behind every place written
-// before it: a pass reads its vectors, waits for the CTA, then writes them.
+// before it: a pass reads its vectors, waits for the CTA, then writes them. The
+// places of the first 512 tokens are looked up once, with the check of the list.
+// Bound by a chain of latencies (count, list, table, vectors) for small trees.
 constexpr int kKeepThreads = 256;
 constexpr int kKeepUnroll = 4;
+constexpr int kKeepRows = 512;
 
 template <typename P>  // the piece that a thread moves
-__global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const KeepParams p, int pieces) {
+__global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const __grid_constant__ KeepParams p, int pieces) {
+  __shared__ long long from[kKeepRows], to[kKeepRows];
   const CacheRef& c = p.cache;
-  const int g = blockIdx.x % c.kv_heads, b = blockIdx.x / c.kv_heads, plane = blockIdx.y;
+  const int b = blockIdx.x / c.kv_heads, g = blockIdx.x - b * c.kv_heads, plane = blockIdx.y;
   pdl_wait();
   pdl_launch_dependents();
   const int start = p.starts[b], n = p.counts[b];
   const int32_t* const kept = p.kept + (size_t)b * p.nodes;
+  auto place = [&](int t) { return cache_row(c, plane, b, g, start + t); };
   bool bad = n < 0 || n > p.nodes || start < 0 || (long long)start + p.nodes > c.capacity;
   if (!bad)
     for (int j = threadIdx.x; j < n; j += kKeepThreads) {
-      const int k = kept[j];
-      bad |= k < 0 || k >= p.nodes || (j > 0 && kept[j - 1] >= k) || cache_row(c, 0, b, g, start + k) < 0 ||
-             cache_row(c, 0, b, g, start + j) < 0;
+      const int k = kept[j], last = j > 0 ? kept[j - 1] : -1;
+      if (k <= last || k >= p.nodes) {
+        bad = true;
+        break;
+      }
+      const long long src = place(k), dst = place(j);
+      bad |= src < 0 || dst < 0;
+      if (j < kKeepRows) {
+        from[j] = src;
+        to[j] = dst;
+      }
     }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) set_status(p.status, OL_DEVICE_GUARD);
@@ -441,14 +454,14 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const KeepParam
     P v[kKeepUnroll];
 #pragma unroll
     for (int u = 0; u < kKeepUnroll; ++u) {
-      const int i = i0 + u * kKeepThreads + threadIdx.x;
-      if (i < total) v[u] = base[cache_row(c, plane, b, g, start + kept[i / pieces]) * pieces + i % pieces];
+      const int i = i0 + u * kKeepThreads + threadIdx.x, j = i / pieces;
+      if (i < total) v[u] = base[(j < kKeepRows ? from[j] : place(kept[j])) * pieces + (i - j * pieces)];
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < kKeepUnroll; ++u) {
-      const int i = i0 + u * kKeepThreads + threadIdx.x;
-      if (i < total) base[cache_row(c, plane, b, g, start + i / pieces) * pieces + i % pieces] = v[u];
+      const int i = i0 + u * kKeepThreads + threadIdx.x, j = i / pieces;
+      if (i < total) base[(j < kKeepRows ? to[j] : place(j)) * pieces + (i - j * pieces)] = v[u];
     }
   }
 }
