@@ -204,27 +204,35 @@ def _status_string(s: int) -> str:
 # lookup instead of the generic checks on every call of a per-step function
 _PTR_OF_TYPE = {}
 _I32 = np.dtype(np.int32)
+_addressof, _CHAR = ctypes.addressof, ctypes.c_char
 _TORCH_I32 = None  # torch.int32, once torch is in use
+
+
+def _np_ptr(x) -> int:
+    try:  # a third of the time of x.ctypes.data
+        return _addressof(_CHAR.from_buffer(x))
+    except (TypeError, ValueError, BufferError):  # read-only, empty or strided
+        return x.ctypes.data
 
 
 def _ptr(x) -> Optional[int]:
     """Address of a torch tensor / numpy array / int (None stays NULL)."""
-    get = _PTR_OF_TYPE.get(type(x))
+    t = type(x)
+    get = _PTR_OF_TYPE.get(t)
     if get is not None:
         return get(x)
     if x is None:
         return None
+    if t is np.ndarray:
+        return _np_ptr(x)
     if isinstance(x, int):
         return x
     if isinstance(x, np.ndarray):
-        try:  # a third of the time of x.ctypes.data
-            return ctypes.addressof(ctypes.c_char.from_buffer(x))
-        except (TypeError, ValueError, BufferError):  # read-only, empty or strided
-            return x.ctypes.data
+        return x.ctypes.data
     if hasattr(x, "data_ptr"):
-        _PTR_OF_TYPE[type(x)] = type(x).data_ptr
+        _PTR_OF_TYPE[t] = t.data_ptr
         return x.data_ptr()
-    raise TypeError(f"cannot take the address of {type(x)}")
+    raise TypeError(f"cannot take the address of {t}")
 
 
 def _host_i32(a):
@@ -234,7 +242,7 @@ def _host_i32(a):
         return None
     global _TORCH_I32
     if type(a) is np.ndarray:
-        if a.dtype == _I32 and a.flags.c_contiguous:
+        if (a.dtype is _I32 or a.dtype == _I32) and a.flags.c_contiguous:
             return a
     elif type(a) in _PTR_OF_TYPE or hasattr(a, "data_ptr"):
         if _TORCH_I32 is None:
@@ -585,7 +593,7 @@ def ol_hpaged_chunk_step(kv: HPagedKV, updated, q, q_heads: int, new_len: int, n
 
 def _ref(struct):
     """The address of a descriptor (None stays NULL)."""
-    return None if struct is None else ctypes.addressof(struct)
+    return None if struct is None else _addressof(struct)
 
 
 def _rows(x):
