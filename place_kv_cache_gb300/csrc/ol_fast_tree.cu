@@ -23,10 +23,10 @@
 // type its product with V takes: as much as the output's own rounding.
 //
 // Warps: 0 producer (TMA; a lane per box of a tile: pages of 16 tokens are
-// boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 the note for the
-// merge, 4-7 and 8-11 the streams. In tiles that hold drafted tokens or end the
-// row, the streams first zero, in V's tile, the rows outside the row's tokens and
-// the non-finite elements of drafted ones: a product with P = 0 must not see them.
+// boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 V's tiles and the
+// note for the merge, 4-7 and 8-11 the streams. In tiles that hold drafted tokens
+// or end the row, warp 3 first zeroes the rows outside the row's tokens and the
+// non-finite elements of drafted ones: a product with P = 0 must not see them.
 // Where there was such an element, the non-finite values of the tokens that a row
 // sees are added to its outputs at the end (rare, unhurried).
 //
@@ -55,8 +55,8 @@ struct Lay {
   static constexpr int kRing = NQ * kTileBytes;
   static constexpr int kStats = kRing + kSlots * kTileBytes;  // float2 [2][128]: streams' (m, l)
   static constexpr int kBars = kStats + 2 * 128 * 8;
-  // full, empty [kSlots], fixed [3]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain[2], join
-  static constexpr int kNumBars = 2 * kSlots + 3 + 17;
+  // full, empty [kSlots], landed [kV]; qfull, qempty, sfull[2][2], pready[2][2], pvdone[2][2], drain[2], join
+  static constexpr int kNumBars = 2 * kSlots + kV + 17;
   static constexpr int kMisc = kBars + kNumBars * 8;    // TMEM address, abort flag, whether V had non-finite elements
   static constexpr int kTotal = kMisc + 12;
   static_assert(kTotal <= 232448, "shared memory of one CTA");
@@ -159,9 +159,9 @@ struct Bars {
   uint32_t at;
   __device__ uint32_t full(int s) const { return at + 8 * s; }
   __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
-  // V set to rights by stream x for itself, or (2) by both streams for both
-  __device__ uint32_t fixed(int x) const { return at + 8 * (2 * L::kSlots + x); }
-  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + 3); }
+  // V's copies are there; its slot is full once warp 3 has set it to rights
+  __device__ uint32_t landed(int s) const { return at + 8 * (2 * L::kSlots + s - L::kK); }
+  __device__ uint32_t qfull() const { return at + 8 * (2 * L::kSlots + L::kV); }
   __device__ uint32_t qempty() const { return qfull() + 8; }
   __device__ uint32_t sfull(int j, int b) const { return qfull() + 16 + 16 * j + 8 * b; }  // S buffer b of stream j
   __device__ uint32_t pready(int j, int b) const { return qfull() + 48 + 16 * j + 8 * b; }  // P in its place
@@ -329,9 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       mbar_init(bar.pvdone(j, 0), 1);
       mbar_init(bar.pvdone(j, 1), 1);
       mbar_init(bar.drain(j), 1);
-      mbar_init(bar.fixed(j), 4);  // a stream's warps
     }
-    mbar_init(bar.fixed(2), 8);
+    for (int s = L::kK; s < L::kSlots; ++s) mbar_init(bar.landed(s), 1);
     mbar_init(bar.join(), 8);
     fence_mbar_init();
     *abort = 0;
@@ -391,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     bool ok = true;
     auto load = [&](Cursor& c, int y) {
       if (!warp_wait(bar.empty(c.slot), c.phase ^ 1, abort, p.status)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(bar.full(c.slot), (uint32_t)(cur.last - cur.first) * box * D * 2);
+      const uint32_t there = c.first == 0 ? bar.full(c.slot) : bar.landed(c.slot);
+      if (lane == 0) mbar_arrive_expect_tx(there, (uint32_t)(cur.last - cur.first) * box * D * 2);
       __syncwarp();
       if (lane >= cur.first && lane < cur.last)
-        tma_load_3d(sa + L::kRing + c.slot * L::kTileBytes + lane * box * (D * 2), &maps.kv, 0, y, 0, bar.full(c.slot),
-                    policy);
+        tma_load_3d(sa + L::kRing + c.slot * L::kTileBytes + lane * box * (D * 2), &maps.kv, 0, y, 0, there, policy);
       c.next();
       return true;
     };
@@ -421,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     if (!ok) {  // copies in flight end before the CTA does
       if (seg) mbar_wait_bounded(bar.qfull(), (seg - 1) & 1);
       for (Cursor* c : {&k, &v})  // a slot's last load: of this round before the cursor, else of the one before
-        for (int i = c->first; i < c->end; ++i) mbar_wait_bounded(bar.full(i), i < c->slot ? c->phase : c->phase ^ 1);
+        for (int i = c->first; i < c->end; ++i)
+          mbar_wait_bounded(c->first == 0 ? bar.full(i) : bar.landed(i), i < c->slot ? c->phase : c->phase ^ 1);
     }
   } else if (warp < 3) {
     // --------------------------------------------------------------- MMA issue
@@ -540,8 +540,70 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     }
     __syncwarp();
   } else if (warp == 3) {
-    // -------------------------------------------------------------- the merge's note
-    if (lane == 0) w.write_splits(p);
+    // ------------------------------------------------- V to rights, the merge's note
+    // Rows of a V tile outside the row's tokens become zeros, drafted ones lose
+    // their non-finite elements, before the tile counts as full. A tile or two
+    // ahead of the products, so that its time is hidden; in the streams it was not
+    // (256 nodes over 8 rows 138 us, here 126).
+    if (lane == 0) {
+      TreeWalk notes(w);
+      notes.write_splits(p);
+    }
+    __syncwarp();
+    const int box_log2 = 31 - __clz(box);
+    Cursor v(L::kK, L::kV);
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const int low = row_low(p, w.row);
+      for (int i = w.tile0; i < w.tile1; ++i) {
+        if (!(ok = warp_wait(bar.landed(v.slot), v.phase, abort, p.status))) break;
+        const int t0 = w.row.start + i * kTile;
+        if (edge_tile(w.row, low, t0)) {
+          uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes);
+          const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;  // rows of the tile
+          constexpr int kAhead = 8, kPieces = kTile * D / 8;  // pieces of 16 bytes: of a lane at a time, all
+          bool found = false;
+#pragma unroll 1
+          for (int x0 = lane; x0 < kPieces; x0 += 32 * kAhead) {
+            uint4 x[kAhead];
+            bool zero[kAhead], hit = false;
+#pragma unroll
+            for (int c = 0; c < kAhead; ++c) {
+              const int line = (x0 + 32 * c) / 8;  // of 128 bytes, among [box][column block][row]
+              const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
+              zero[c] = r < r_low || r >= r_end;
+              x[c] = make_uint4(0, 0, 0, 0);
+              if (!zero[c] && r >= r_tree) x[c] = tile[x0 + 32 * c];
+            }
+#pragma unroll
+            for (int c = 0; c < kAhead; ++c) {
+              if (zero[c]) tile[x0 + 32 * c] = x[c];
+              // an exponent of ones carries into the sign's place
+              auto full = [](uint32_t e) { return (e & 0x7f807f80u) + 0x00800080u; };
+              hit |= ((full(x[c].x) | full(x[c].y) | full(x[c].z) | full(x[c].w)) & 0x80008000u) != 0;
+            }
+            if (hit) {
+              found = true;
+#pragma unroll
+              for (int c = 0; c < kAhead; ++c) {
+                uint32_t* const e = reinterpret_cast<uint32_t*>(&x[c]);
+                bool one = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, one = true;
+                  if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0xffffu, one = true;
+                }
+                if (one) tile[x0 + 32 * c] = x[c];
+              }
+            }
+          }
+          if (found) *bad = 1;
+          fence_proxy_async_smem();
+        }
+        warp_arrive(bar.full(v.slot));
+        v.next();
+      }
+    }
   } else {
     // ----------------------------------------------------------------- streams
     const int j = (warp - 4) / 4, row = tid % 128;  // TMEM lane
@@ -549,40 +611,6 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     const uint32_t ts = tmem + j * 128 + lanes, to = tmem + 256 + j * D + lanes;
     const int R = p.group * p.nodes;
     float2* const stats = reinterpret_cast<float2*>(smem + L::kStats);
-    const int box_log2 = 31 - __clz(box);
-    // Half h of a V tile (the tokens of a step): rows outside [low, len) become
-    // zeros, drafted ones lose their non-finite elements.
-    auto fix = [&](uint8_t* v, int h, int low, int prefix, int end) {  // rows of the tile
-      bool found = false;
-#pragma unroll 4
-      for (int i = row; i < kTile * D / 16; i += 128) {
-        // piece i of this half; its line of 128 bytes among [box][column block][row]
-        int line = i / 8;
-        line = box == 16 ? line / 8 * 16 + h * 8 + line % 8
-               : box == 64 ? line + h * 64 * L::kHalves
-                           : line / 64 * 128 + h * 64 + line % 64;
-        const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
-        uint4* const at = reinterpret_cast<uint4*>(v) + line * 8 + i % 8;
-        if (r < low || r >= end) {
-          *at = make_uint4(0, 0, 0, 0);
-        } else if (r >= prefix) {
-          uint4 x = *at;
-          uint32_t* const e = reinterpret_cast<uint32_t*>(&x);
-          bool hit = false;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if ((e[c] & 0x7f80u) == 0x7f80u) e[c] &= 0xffff0000u, hit = true;
-            if ((e[c] & 0x7f800000u) == 0x7f800000u) e[c] &= 0xffffu, hit = true;
-          }
-          if (hit) *at = x;
-          found |= hit;
-        }
-      }
-      if (found) *bad = 1;
-      fence_proxy_async_smem();
-    };
-    uint32_t fixes[2] = {0, 0};    // edge tiles set to rights by this stream for itself, by both for both
-    Cursor v(L::kK, L::kV);        // V of the step's tile
     uint32_t phases = 0;           // of the S buffers, a bit each
     // Whether the products with the last P of buffer b are done: a buffer's next
     // S, and so its next P, comes only after them.
@@ -596,11 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     while (ok && w.next(p)) {
       const int r = w.qg * p.rows_per_unit + (NQ == 2 ? j * 128 : 0) + row;  // (head, node)
       const int tiles = w.tile1 - w.tile0;
-      const int streams = unit_streams<NQ>(p, w);
-      if (j >= streams) {
-        for (int i = 0; i < tiles; ++i) v.next();
-        continue;
-      }
+      if (j >= unit_streams<NQ>(p, w)) continue;
       const bool live = r < R, live_warp = r - lane < R;
       const int node = r % p.nodes;
       const int low = p.window < 0 ? 0 : tree_low(p, w.row, w.b, node);
@@ -706,24 +730,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         bool early = false;
         if (next && (early = __all_sync(0xffffffffu, mbar_test(next_full, phases >> (i + 1 & 1) & 1)))) fetch(i + 1);
         if (live_warp) tmem_wait_st();
-        if (edge && (NQ == 1 || half == 0)) {
-          ok = ok && warp_wait(bar.full(v.slot), v.phase, abort, p.status);
-          if (ok) {
-            // NQ = 1: each stream needs its own half; two query tiles: both need
-            // both and do one each, unless the other stream has no queries
-            uint8_t* const at = smem + L::kRing + v.slot * L::kTileBytes;
-            const int r_low = low_all - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
-            fix(at, j, r_low, r_tree, r_end);
-            if (NQ == 2 && streams == 1) fix(at, 1, r_low, r_tree, r_end);
-            const int x = NQ == 2 && streams == 2;
-            warp_arrive(bar.fixed(x ? 2 : j));
-            ok = warp_wait(bar.fixed(x ? 2 : j), fixes[x]++ & 1, abort, p.status);
-          }
-        }
         if (!ok) break;
         tmem_fence_before();
         warp_arrive(bar.pready(j, i & 1));
-        if (NQ == 1 || half == 1) v.next();
         if (next && !early) {
           if (!(ok = warp_wait(next_full, phases >> (i + 1 & 1) & 1, abort, p.status))) break;
           fetch(i + 1);
