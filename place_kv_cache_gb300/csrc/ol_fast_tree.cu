@@ -908,9 +908,9 @@ void plan_fast_tree(TreeParams& p, int sms) {
   p.units_per_head = (p.group * p.nodes + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
-  // Measured (0 / 2 / 4 tiles): 64 nodes over 32 ragged rows (two query tiles) 176 / 155 / 146 us, 16 nodes over 64
-  // ragged rows (one) 367 / 360 / 362 us.
-  p.extra = p.rows_per_unit == 256 ? 4 : 2;
+  // Measured (0 / 2 / 3 / 4 tiles): 64 nodes over 32 ragged rows (two query tiles) 160 / 142 / 139 / 140 us, 16 nodes
+  // over 64 ragged rows (one) 361 / 360 / 360 / 362 us.
+  p.extra = p.rows_per_unit == 256 ? 3 : 2;
   p.by_unit = tree_few_units(p);
 }
 
