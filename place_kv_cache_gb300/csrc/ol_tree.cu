@@ -292,15 +292,17 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
 // one, or unit x (TreeSplit): rows [ROWS y, ROWS (y + 1)).
 //   M = max m_s, L = sum l_s 2^(m_s - M), y = sum o_s 2^(m_s - M) / L
 // A thread has a row, KG groups of four dimensions (the slots' layout keeps the
-// rows of a group together) and one of G shares of the segments. 16 loads of o
-// are on their way before the weights are known; more segments than that are
-// taken in chunks with a running maximum. Bound by latency for few units (8 rows
-// a CTA, for more CTAs, 20 loads), else by reading the partials from L2 (32 rows).
+// rows of a group together) and one of G shares of the segments. Its first loads
+// of o are on their way before the weights are known; more segments than those are
+// taken in chunks with a running maximum. Bound by latency for few units: 8 rows a
+// CTA, for more CTAs, 20 loads a thread. Else by reading the partials from L2, for
+// which many resident warps do more than many loads each: 16 rows a CTA, 8 loads,
+// four CTAs an SM (64 nodes over 32 rows 137 us in all; 32 rows, 16 loads 141).
 template <int ROWS, int THREADS, int D4>  // D4: groups of four dimensions, 32 or 64
-__global__ void __launch_bounds__(THREADS) tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(const TreeParams p) {
   constexpr int kLanes = THREADS / ROWS;  // threads of a row
   constexpr int G = kLanes > D4 ? kLanes / D4 : 1, KG = kLanes > D4 ? 1 : D4 / kLanes;
-  constexpr int C = (ROWS == 8 && D4 == 32 ? 20 : 16) / KG, kChunk = C * G;  // segments of a thread and of the CTA at a time
+  constexpr int C = (ROWS > 8 ? 8 : D4 == 32 ? 20 : 16) / KG, kChunk = C * G;  // segments of a thread and of the CTA at a time
   static_assert(C >= 2 && kChunk * ROWS <= THREADS, "a thread loads one state");
   __shared__ float2 state[kChunk][ROWS];  // m, l
   __shared__ float4 other[G > 1 ? (G - 1) * ROWS * D4 : 1];
@@ -489,7 +491,7 @@ cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
-  return p.by_unit ? launch_merge<8, 512>(p, rows, s) : launch_merge<32, 256>(p, rows, s);
+  return p.by_unit ? launch_merge<8, 512>(p, rows, s) : launch_merge<16, 256>(p, rows, s);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {
