@@ -601,12 +601,14 @@ OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* up
  * to others may hold infinities or NaN; a prefix token behind a window must be
  * finite while other nodes still see it).
  * ws_bytes >= ol_workspace_size_tree(batch, q_heads, kv_heads, head_dim, nodes);
- * the workspace needs ol_workspace_init once. Lengths, counts and the block
- * table are read on the device: a captured launch replays with the values it
- * finds there (up to the capacity); out-of-range ones are clamped and recorded
- * as OL_DEVICE_GUARD. Two launches. In the statistics attended_tokens counts
- * every drafted token as seen (the mask is on the device) and
- * kv_payload_bytes_read the tokens that some node may see, once.
+ * the workspace needs ol_workspace_init once and may be that of decode steps and
+ * of chunked steps of up to `nodes` tokens of the same batch and kv heads (their
+ * ticket counters stay as they are). Lengths, counts and the block table are
+ * read on the device: a captured launch replays with the values it finds there
+ * (up to the capacity); out-of-range ones are clamped and recorded as
+ * OL_DEVICE_GUARD. Two launches. In the statistics attended_tokens counts every
+ * drafted token as seen (the mask is on the device) and kv_payload_bytes_read
+ * the tokens that some node may see, once.
  * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (other layouts, head_dim > 256, nodes > 512, 2^31 tiles of work at
  * full capacity), CUDA.

@@ -113,11 +113,16 @@ constexpr size_t kTreeSplitBytes = 4 * kTreeMaxCtas * sizeof(TreeSplit);
 // (head, node) rows of a unit of the CUDA-core and of the tensor-core kernel
 inline int tree_gen_rows(int group, int nodes) { return group * nodes <= 32 ? 32 : 64; }
 inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }
-inline size_t tree_workspace_bytes(int q_heads, int kv_heads, int head_dim, int nodes) {
+// Notes and partial slots lie behind the ticket counters of decode steps and of
+// chunked steps of up to `nodes` tokens of this batch, which stay as they are.
+inline size_t tree_splits_offset(int batch, int kv_heads, int nodes) {
+  return partials_offset(batch, kv_heads, nodes);
+}
+inline size_t tree_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim, int nodes) {
   const size_t fast = 2ull * kTreeMaxCtas * tree_slot_floats(tree_fast_rows(q_heads / kv_heads, nodes), head_dim);
   const int rows = tree_gen_rows(q_heads / kv_heads, nodes);
   const size_t gen = 2ull * (128 / rows) * kTreeMaxCtas * tree_slot_floats(rows, head_dim);
-  return kStatusBytes + kTreeSplitBytes + sizeof(float) * (fast > gen ? fast : gen);
+  return tree_splits_offset(batch, kv_heads, nodes) + kTreeSplitBytes + sizeof(float) * (fast > gen ? fast : gen);
 }
 
 bool fast_tree_supported(const TreeParams& p);

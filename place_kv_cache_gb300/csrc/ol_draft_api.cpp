@@ -290,7 +290,7 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
   }
   const int words = (nodes + 63) / 64;
   const size_t vectors = (size_t)c.batch * q_heads * nodes;
-  const size_t need = tree_workspace_bytes(q_heads, c.kv_heads, c.head_dim, nodes);
+  const size_t need = tree_workspace_bytes(c.batch, q_heads, c.kv_heads, c.head_dim, nodes);
   if (ws_bytes < need) return OL_ERR_WORKSPACE;
   const Range ro = range_of(out, vectors * c.head_dim * elt_bytes(out_dtype)), rw = range_of(workspace, need);
   const size_t tree = (size_t)c.batch * nodes;
@@ -349,8 +349,9 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
   p.out = out;
   p.out_dtype = out_dtype;
   p.status = static_cast<int32_t*>(workspace);
-  p.splits = reinterpret_cast<TreeSplit*>(static_cast<char*>(workspace) + kStatusBytes);
-  p.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + kStatusBytes + kTreeSplitBytes);
+  char* const splits = static_cast<char*>(workspace) + tree_splits_offset(c.batch, c.kv_heads, nodes);
+  p.splits = reinterpret_cast<TreeSplit*>(splits);
+  p.partials = reinterpret_cast<float*>(splits + kTreeSplitBytes);
   const bool fast = fast_tree_supported(p);
   if (fast)
     plan_fast_tree(p, sm_count_cached());
@@ -463,7 +464,7 @@ ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* updated, 
 
 size_t ol_workspace_size_tree(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t nodes) {
   if (batch < 0 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0 || nodes < 1) return 0;
-  return tree_workspace_bytes(q_heads, kv_heads, head_dim, nodes);
+  return tree_workspace_bytes(batch, q_heads, kv_heads, head_dim, nodes);
 }
 
 ol_status ol_tree_attention(int32_t layout, const void* cache_desc, const void* q, int32_t q_heads, int32_t nodes,

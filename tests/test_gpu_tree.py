@@ -323,6 +323,40 @@ def test_repeated_calls_over_many_tiles_end_and_repeat_bits(layout, page, nodes)
     assert torch.equal(first, t.out)
 
 
+def test_tree_decode_and_chunk_share_a_workspace():
+    """Tickets of decode and chunked steps stay at zero under a tree's notes and slots, and the other way round."""
+    t = Tree("bf16", "contiguous", 2, 28, 4, 128, 0, 16, [3000, 2000])
+    chunk = 5
+    size = max(t.ws_bytes, ol.ol_workspace_size(2, 28, 4, 128), ol.ol_workspace_size_chunk(2, 28, 4, 128, chunk))
+    shared = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    q = torch.randn((2, 28, 128), generator=t.gen, device=DEV, dtype=torch.bfloat16)
+    qc = torch.randn((2, 28, chunk, 128), generator=t.gen, device=DEV, dtype=torch.bfloat16)
+    kv = torch.stack([torch.stack([t.row(p, b, int(t.lens[b]))[:, -chunk:] for b in range(2)]) for p in (0, 1)])
+    desc = ol.kv_cache(t.cache)
+
+    def decode(ws):
+        out = torch.full_like(q, -77.0)
+        ol.ol_decode_attention(desc, q, 28, t.lens, t.lens_d, 0.0, -1, out, ol.OL_BF16, ws, ws.numel())
+        return out
+
+    def chunked(ws):  # rewrites the last tokens with what they hold
+        out = torch.full_like(qc, -77.0)
+        ol.ol_chunk_step(t.code, desc, t.cache, qc, 28, chunk, kv.contiguous(), t.lens, t.lens_d, 0.0, -1, out,
+                         ol.OL_BF16, ws, ws.numel())
+        return out
+
+    fresh = [f(torch.zeros_like(shared)) for f in (decode, chunked)]
+    t.ws, t.ws_bytes = shared, size
+    for f, want in zip((decode, chunked), fresh):
+        t.out.fill_(-77.0)
+        t.call()
+        assert torch.equal(f(shared), want)
+        shared.zero_()                               # chunked and decode steps have tickets in different places
+    decode(shared)
+    t.call()
+    t.check()
+
+
 def test_device_lengths_and_pages_that_disagree_are_recorded():
     t = Tree("bf16", "paged", 2, 8, 2, 128, 16, 4, [100, 50], [4, 4])
     t.lens_d.copy_(torch.tensor([100000, -5], dtype=torch.int32))  # clamped to the capacity, and to nothing
