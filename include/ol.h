@@ -562,12 +562,13 @@ OL_API ol_status ol_rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch,
  *            that the rotation uses where they are not the cache's, as for a tree
  *            of drafted tokens (its depths) or a context whose start was dropped.
  *   q, q_out both NULL with q_heads 0: K and V alone. q_out may equal q (in
- *            place), also where q, k and v interleave in one projection's output;
- *            any other q_out must not overlap the extents of q, k or v.
+ *            place), also where q, k and v interleave, with the same strides, in
+ *            one projection's output (OL_ERR_ALIAS where they share elements); any
+ *            other q_out must not overlap the extents of q, k or v.
  * Every written page must be in [0, num_pages) and is written once: by one row,
- * through one entry of its table (OL_ERR_PAGE). The kernel reads positions, counts and the block table
- * on the device, so a captured launch replays with the values it finds there;
- * a token whose place is not in the cache is skipped.
+ * through one entry of its table (OL_ERR_PAGE). The kernel reads positions,
+ * counts and the block table on the device, so a captured launch replays with
+ * the values it finds there; a token whose place is not in the cache is skipped.
  * Errors: NULL, ALIAS, READONLY, CAPACITY, SHAPE, DTYPE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (other layouts; head_dim > 1024), CUDA.
  */

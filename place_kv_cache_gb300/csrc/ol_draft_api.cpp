@@ -123,6 +123,46 @@ bool same_view(const ol_rows& a, const ol_rows& b) {
          a.stride_token == b.stride_token;
 }
 
+// Whether a vector of `a`, a view that may be written (check_rows), and one of `b`
+// may share an element. Views of other strides than a's may; else two vectors are
+// delta + sum n_i s_i elements apart, n_i being differences of their indices, and
+// as each stride reaches past what the smaller ones span, only the two n_i
+// around zero can bring that below head_dim.
+bool may_share(const ol_rows& a, const Dims& da, const ol_rows& b, const Dims& db, size_t es) {
+  struct Dim {
+    int64_t stride, lo, hi;  // lo <= n <= hi
+  } dim[3];
+  const int64_t sa[3] = {a.stride_batch, a.stride_head, a.stride_token}, sb[3] = {b.stride_batch, b.stride_head, b.stride_token};
+  const int64_t na[3] = {da.batch, da.heads, da.tokens}, nb[3] = {db.batch, db.heads, db.tokens};
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (na[i] == 1 && nb[i] == 1) continue;
+    if (na[i] > 1 && nb[i] > 1 && sa[i] != sb[i]) return true;
+    if (na[i] < nb[i]) return true;  // (a's strides say nothing about so many)
+    dim[n++] = {sa[i], 1 - na[i], nb[i] - 1};
+  }
+  const int64_t bytes = static_cast<char*>(b.data) - static_cast<char*>(a.data);
+  if (bytes % (int64_t)es != 0) return true;
+  std::sort(dim, dim + n, [](const Dim& x, const Dim& y) { return x.stride > y.stride; });
+  int64_t apart[8] = {bytes / (int64_t)es};
+  int count = 1;
+  for (int i = 0; i < n; ++i) {
+    int64_t next[8];
+    int m = 0;
+    for (int c = 0; c < count && m < 8; ++c) {
+      int64_t k = -apart[c] / dim[i].stride;
+      if (k * dim[i].stride > -apart[c]) --k;  // floor
+      for (int64_t x : {k, k + 1})
+        if (x >= dim[i].lo && x <= dim[i].hi) next[m++] = apart[c] + x * dim[i].stride;
+    }
+    std::copy(next, next + m, apart);
+    count = m;
+  }
+  for (int c = 0; c < count; ++c)
+    if (apart[c] < da.head_dim && -apart[c] < da.head_dim) return true;
+  return false;
+}
+
 // Every vector of the view starts on a 16-byte boundary.
 bool rows_aligned(const ol_rows& r, const Dims& d, size_t es) {
   const int64_t ve = 16 / es;
@@ -216,7 +256,12 @@ ol_status rope_append(int32_t layout, const void* cache_desc, void* updated, con
   if (q) {
     if ((st = check_rows(q, dq, es, false, rq)) != OL_OK) return st;
     if ((st = check_rows(q_out, dq, es, true, ro)) != OL_OK) return st;
-    if (!same_view(*q, *q_out) && (overlaps(ro, rq) || overlaps(ro, rk) || overlaps(ro, rv))) return OL_ERR_ALIAS;
+    if (!same_view(*q, *q_out)) {
+      if (overlaps(ro, rq) || overlaps(ro, rk) || overlaps(ro, rv)) return OL_ERR_ALIAS;
+    } else if (!dq.empty()) {
+      if (overlaps(ro, rk) && may_share(*q_out, dq, *k, dk, es)) return OL_ERR_ALIAS;
+      if (overlaps(ro, rv) && may_share(*q_out, dq, *v, dk, es)) return OL_ERR_ALIAS;
+    }
   }
   int64_t appended = 0;
   for (int b = 0; b < c.batch; ++b) {

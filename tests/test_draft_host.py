@@ -194,6 +194,38 @@ def test_rope_append_passes_and_refuses():
     assert append(n=-1) == ol.OL_ERR_SHAPE
 
 
+def test_rope_append_in_place_refuses_shared_elements():
+    """q in place in one projection's output with k and v: taken where the vectors interleave, refused where they meet."""
+    rng = np.random.default_rng(3)
+    seen = set()
+    for _ in range(400):
+        order = rng.permutation(3)
+        sizes, strides = np.array([B, HQ + 2 * HKV + int(rng.integers(0, 3)), T]), [0, 0, 0]
+        step = D + int(rng.integers(0, 2)) * 8
+        for i in order:                                  # batch, heads, tokens, in any order of nesting
+            strides[i] = int(step)
+            step = step * sizes[i]
+        at = {"k": int(rng.integers(0, 12)), "v": int(rng.integers(0, 12))}
+        shift = int(rng.choice([0, 0, 8, -8, D - 8]))
+        view = lambda head, more=0: ol.Rows(BASE + 2 * (head * strides[1] + more), *strides)  # noqa: E731
+
+        def elements(first, heads):
+            i = np.indices((B, heads, T, D)).reshape(4, -1)
+            return set((first + i[0] * strides[0] + i[1] * strides[1] + i[2] * strides[2] + i[3]).tolist())
+        q = elements(0, HQ)
+        k, v = elements(at["k"] * strides[1] + shift, HKV), elements(at["v"] * strides[1], HKV)
+        want = ol.OL_ERR_ALIAS if q & (k | v) else ol.OL_ERR_INJECTED
+        if at["k"] * strides[1] + shift < 0:
+            continue
+        got = append(q=view(0), q_out=view(0), k=view(at["k"], shift), v=view(at["v"]))
+        assert got == want, (strides, at, shift)
+        seen.add((got, shift))
+    assert len(seen) > 5
+    other = ol.Rows(BASE + 2 * HQ * D, 10 * T * D, D, 12 * D)  # no projection's output has q with other strides
+    mine = ol.Rows(BASE, 12 * T * D, D, 12 * D)
+    assert append(q=mine, q_out=mine, k=other) == ol.OL_ERR_ALIAS
+
+
 def test_rope_append_checks_the_pages_it_writes():
     def st(table, **k):
         return append(desc=paged(np.array(table, np.int32)), layout=ol.OL_LAYOUT_PAGED, **k)
