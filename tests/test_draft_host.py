@@ -295,6 +295,19 @@ def test_tree_attention_passes_and_refuses():
     assert tree(ws_bytes=WS_BYTES - 1) == ol.OL_ERR_WORKSPACE
 
 
+def test_tree_attention_counts_its_work_in_32_bits():
+    """A cache of 2^31 rows is beyond the tensor-core kernel: tiles of 32 tokens of units of 64 (head, node) rows,
+    2^31 of which are refused, and fewer are not."""
+    def st(capacity, nodes):
+        batch, far = 8, 1 << 45
+        desc = ol.kv_cache(BASE - far, dims=(batch, HKV, capacity, D), dtype=ol.OL_BF16)
+        return tree(desc=desc, nodes=nodes, lens=[nodes] * batch, mask=None, positions=None, ws_bytes=1 << 40,
+                    ws=BASE + far)
+    assert st((1 << 31) - 1, 32) == ol.OL_ERR_UNSUPPORTED               # 2^26 tiles, 8 rows, 2 heads, 2 units
+    assert st((1 << 31) - 1, 16) == ol.OL_ERR_INJECTED                  # 1 unit
+    assert st((1 << 30) - 200, 32) == ol.OL_ERR_INJECTED                # half the tiles
+
+
 def test_tree_attention_checks_the_pages_it_reads():
     def st(table, **k):
         return tree(desc=paged(np.array(table, np.int32)), layout=ol.OL_LAYOUT_PAGED, **k)

@@ -184,6 +184,14 @@ CASES = [
     ("f32", "paged", 2, 16, 2, 64, 5, 40, [400, 40], None, 50, "tree", "bf16"),
     ("f32", "contiguous", 2, 4, 1, 256, 0, 70, [200, 70], None, 10, "chain"),
     ("f32", "contiguous", 2, 4, 1, 192, 0, 6, [200, 6], None, -1, "empty"),
+    # every CTA with several segments, units of one and of two and more row groups
+    ("f32", "paged", 16, 16, 4, 128, 16, 24, [24 + (211 * i) % 2500 for i in range(16)]),
+    ("f32", "contiguous", 30, 8, 4, 64, 0, 7, [7 + (97 * i) % 1500 for i in range(30)], [i % 8 for i in range(30)]),
+    ("bf16", "paged", 12, 16, 4, 96, 32, 20, [20 + (211 * i) % 2500 for i in range(12)], None, 300, "random"),
+    # the widest trees on both kernels, any mask, a window among the drafted tokens
+    ("bf16", "contiguous", 2, 8, 2, 128, 0, 512, [512, 1500], [512, 300], 64, "random"),
+    ("bf16", "paged", 2, 2, 2, 64, 16, 511, [511, 900], None, 100, "chain"),
+    ("f32", "contiguous", 1, 2, 1, 64, 0, 512, [700], None, -1, "random"),
 ]
 
 
@@ -294,6 +302,23 @@ def test_replays_follow_the_device_lengths(dt):
             t.check()
 
 
+@pytest.mark.parametrize("D", [128, 64])
+def test_non_finite_values_in_a_tree_that_crosses_tiles_and_segments(D):
+    """Drafted tokens with infinities over several tiles, in units of two query tiles that several CTAs share."""
+    t = Tree("bf16", "paged", 5, 16, 4, D, 64, 200, [3000, 200, 2111, 1000, 500], seed=17)
+    for b in range(5):
+        first = int(t.lens[b]) - 200
+        for j in (0, 70, 130, 199):
+            t.token(1, b, first + j)[:, j % D] = float("inf") if j % 20 else float("nan")
+        t.sees[b, :, 130] = False                        # seen by a few nodes only
+        t.sees[b, ::9, 130] = True
+        t.sees[b, :, 0] = False
+        t.sees[b, 5, 0] = True
+    t.mask = torch.from_numpy(du.pack_mask(t.sees)).to(DEV)
+    t.call()
+    t.check()
+
+
 def test_calls_in_a_row_share_a_workspace_and_repeat_bits():
     t = Tree("bf16", "contiguous", 2, 28, 4, 128, 0, 16, [3000, 400])
     t.call()
@@ -383,6 +408,9 @@ KEEPS = [
     ("bf16", "contiguous", 1, 1, 5, 0, 3, 5, [2], [[0, 2]]),
     ("f32", "contiguous", 2, 2, 256, 0, 512, 600, [88, 0], [list(range(1, 512, 2)), list(range(200, 512))]),
     ("bf16", "contiguous", 1, 2, 64, 0, 1, 4, [3], [[0]]),
+    # more nodes than a CTA looks up at once
+    ("bf16", "paged", 2, 2, 64, 16, 700, 1000, [100, 300], [list(range(3, 700)), list(range(0, 700, 3))]),
+    ("f32", "contiguous", 1, 1, 128, 0, 600, 600, [0], [list(range(1, 600))]),
 ]
 
 
