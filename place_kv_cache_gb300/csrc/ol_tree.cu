@@ -9,8 +9,14 @@
 // scores S = Q K^T and the sums O += P V in registers: 4 rows x 2 tokens of S,
 // 4 rows x D / 16 dimensions of O per thread, operands from shared memory four
 // dimensions at a time. K and V lie there as they are in the cache; the next tile
-// is copied in meanwhile. Bound by fp32 FMA issue for many rows (4 * D flops per
-// row and token against 2 * D elements a token), by latency for few.
+// is copied in meanwhile. Bound for many rows by fp32 FMAs and the shared-memory
+// loads that feed them (4 * D flops per row and token against 2 * D elements a
+// token; fp32 trees of 16 over 64 rows of 4000 tokens 1750 us, 38 TFLOP/s), by
+// latency for few (5 nodes, 6 rows, a window of 1000: 22 us). The loops over
+// dimensions and tokens hold no branch: one in the sums, past the head's end,
+// kept their loads from running ahead (2170 us and 26 us).
+#include <type_traits>
+
 #include "ol_tree.cuh"
 
 namespace ol {
@@ -140,8 +146,8 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float4 a = load4(reinterpret_cast<const T*>(sq + (4 * rg + r) * rb) + d);
-          s[r][0] += a.x * k0.x + a.y * k0.y + a.z * k0.z + a.w * k0.w;
-          s[r][1] += a.x * k1.x + a.y * k1.y + a.z * k1.z + a.w * k1.w;
+          s[r][0] = fmaf(a.w, k0.w, fmaf(a.z, k0.z, fmaf(a.y, k0.y, fmaf(a.x, k0.x, s[r][0]))));
+          s[r][1] = fmaf(a.w, k1.w, fmaf(a.z, k1.z, fmaf(a.y, k1.y, fmaf(a.x, k1.x, s[r][1]))));
         }
       }
       const bool drafted = t0 + TB > w.row.prefix;  // some row may not see some token of the tile
@@ -154,10 +160,15 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
           const int j = t0 + cg + 16 * u - w.row.prefix;
           if (p.window >= 0 && j >= 0 && j < w.row.count) pos[u] = tree_position(p, w.row, w.b, j);
         }
+        const int j0 = t0 - w.row.prefix;
+        uint32_t bits[4] = {};  // all rows' on their way together
+        if (p.mask && j0 < w.row.count)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            bits[r] = mask_bits(p.mask + ((size_t)w.b * p.nodes + node[r]) * p.words, p.words, j0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const uint64_t* const words = p.mask ? p.mask + ((size_t)w.b * p.nodes + node[r]) * p.words : nullptr;
-          const uint32_t seen = visible_word(words, p.words, w.row.prefix, w.row.count, node[r], low[r], t0);
+          const uint32_t seen = visible_bits(!p.mask, bits[r], w.row.prefix, w.row.count, node[r], low[r], t0);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             if (!(seen >> (cg + 16 * u) & 1) || (p.window >= 0 && t0 + cg + 16 * u >= w.row.prefix &&
@@ -202,25 +213,32 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
         *reinterpret_cast<float4*>(sp + (cg + 16 * u) * kPStride + 4 * rg) =
             make_float4(pr[0][u], pr[1][u], pr[2][u], pr[3][u]);
       __syncwarp();  // P of the warp's eight rows: its own
+      int dims[NC];  // (past the head: some other dimension, for sums that no one reads)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) dims[c] = c * 64 + cg * 4 < Dp ? c * 64 + cg * 4 : 0;
+      auto add = [&](auto hidden) {  // whether there may be tokens hidden from some row: their V may hold infinities or NaN
 #pragma unroll 4
-      for (int j = 0; j < TB; ++j) {
-        const float4 p4 = *reinterpret_cast<const float4*>(sp + j * kPStride + 4 * rg);
-        const float pj[4] = {p4.x, p4.y, p4.z, p4.w};
+        for (int j = 0; j < TB; ++j) {
+          const float4 p4 = *reinterpret_cast<const float4*>(sp + j * kPStride + 4 * rg);
+          const float pj[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int d = c * 64 + cg * 4;
-          if (d >= Dp) continue;
-          const float4 v = load4(reinterpret_cast<const T*>(sv + j * rb) + d);
+          for (int c = 0; c < NC; ++c) {
+            const float4 v = load4(reinterpret_cast<const T*>(sv + j * rb) + dims[c]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (drafted && pj[r] == 0.f) continue;  // a hidden token's V may hold infinities or NaN
-            o[r][c].x += pj[r] * v.x;
-            o[r][c].y += pj[r] * v.y;
-            o[r][c].z += pj[r] * v.z;
-            o[r][c].w += pj[r] * v.w;
+            for (int r = 0; r < 4; ++r) {
+              if (decltype(hidden)::value && pj[r] == 0.f) continue;
+              o[r][c].x += pj[r] * v.x;
+              o[r][c].y += pj[r] * v.y;
+              o[r][c].z += pj[r] * v.z;
+              o[r][c].w += pj[r] * v.w;
+            }
           }
         }
-      }
+      };
+      if (drafted)
+        add(std::true_type());
+      else
+        add(std::false_type());
       __syncthreads();  // the stage is read
     }
 #pragma unroll

@@ -58,24 +58,24 @@ __device__ __forceinline__ uint32_t bit_range(int a, int b) {
 }
 
 // Visibility of tokens [t, t + 32) for a node, as bits, but for the window among
-// drafted tokens: m are its mask words (NULL: a chain).
+// drafted tokens. v: the drafted ones' mask bits (mask_bits; ignored for a chain).
+__device__ __forceinline__ uint32_t visible_bits(bool chain, uint32_t v, int prefix, int count, int node, int low, int t) {
+  const int j0 = t - prefix;  // drafted index of bit 0
+  const uint32_t tree = chain ? bit_range(-32, node + 1 - j0) : v;
+  return bit_range(low - t, prefix - t) | (tree & bit_range(-j0, count - j0));
+}
+// Bits [j0, j0 + 32) of a node's mask words m, which have bits [j0, j0 + 32) or more (j0 > -32).
+__device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int j0) {
+  if (j0 < 0) return (uint32_t)m[0] << -j0;
+  const int w = j0 / 64, s = j0 % 64;
+  uint64_t v = m[w] >> s;
+  if (s > 32 && w + 1 < words) v |= m[w + 1] << (64 - s);
+  return (uint32_t)v;
+}
 static __device__ __noinline__ uint32_t visible_word(const uint64_t* m, int words, int prefix, int count, int node, int low,
                                               int t) {
-  const uint32_t bits = bit_range(low - t, prefix - t);
-  const int j0 = t - prefix;  // drafted index of bit 0
-  if (j0 <= -32 || j0 >= count) return bits;
-  uint32_t tree;
-  if (!m) {
-    tree = bit_range(-32, node + 1 - j0);
-  } else if (j0 < 0) {
-    tree = (uint32_t)m[0] << -j0;
-  } else {
-    const int w = j0 / 64, s = j0 % 64;
-    uint64_t v = m[w] >> s;
-    if (s > 32 && w + 1 < words) v |= m[w + 1] << (64 - s);
-    tree = (uint32_t)v;
-  }
-  return bits | (tree & bit_range(-j0, count - j0));
+  const int j0 = t - prefix;
+  return visible_bits(!m, m && j0 > -32 && j0 < count ? mask_bits(m, words, j0) : 0, prefix, count, node, low, t);
 }
 
 __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
