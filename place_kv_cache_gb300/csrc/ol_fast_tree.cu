@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     }
     if (!ok) {  // copies in flight end before the CTA does
       if (seg) mbar_wait_bounded(bar.qfull(), (seg - 1) & 1);
-      for (Cursor* c : {&k, &v})  // a slot's last load: of this round before the cursor, else of the one before
+      for (Cursor* c : {&k, &v})  // a slot's last load: of this lap before the cursor, else of the one before
         for (int i = c->first; i < c->end; ++i)
           mbar_wait_bounded(c->first == 0 ? bar.full(i) : bar.landed(i), i < c->slot ? c->phase : c->phase ^ 1);
     }
