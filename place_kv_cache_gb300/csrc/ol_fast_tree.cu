@@ -632,12 +632,16 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
       const uint64_t* const words = p.mask ? p.mask + ((size_t)w.b * p.nodes + node) * p.words : nullptr;
       if (words)  // on their way to L1 before the tiles that need them
         for (int x = 0; x < p.words; x += 4) asm volatile("prefetch.global.L1 [%0];" ::"l"(words + x));
-      auto visible = [&](int t) {
-        uint32_t bits = visible_word(words, p.words, w.row.prefix, w.row.count, node, low, t);
+      auto visible = [&](int t) {  // tokens [t, t + 64)
+        uint64_t bits = visible64(words, p.words, w.row.prefix, w.row.count, node, low, t);
         const int j0 = t - w.row.prefix;
-        if (p.window >= 0 && j0 > -32) {
-          const uint32_t tree = bits & bit_range(-j0, 32);
-          if (tree) bits = (bits ^ tree) | in_window(p, w.row, w.b, node, j0, tree);
+        if (p.window >= 0 && j0 > -64) {
+          const uint64_t tree = bits & bit_range64(-j0, 64);
+          uint32_t lo = (uint32_t)tree, hi = (uint32_t)(tree >> 32);
+          bits ^= tree;
+          if (lo) lo = in_window(p, w.row, w.b, node, j0, lo);
+          if (hi) hi = in_window(p, w.row, w.b, node, j0 + 32, hi);
+          bits |= (uint64_t)hi << 32 | lo;
         }
         return bits;
       };
@@ -661,19 +665,21 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         if (live_warp) {
           tmem_wait_ld(s);
           tmem_wait_ld(s + 32);
-          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t0)))
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t seen = 0;
-              if (live && box == 16) {  // 8 tokens of each of 4 boxes
-                seen = __byte_perm(visible(t0 + 64 * c), visible(t0 + 64 * c + 32), half ? 0x7531 : 0x6420);
-              } else if (live) {
-                seen = visible(t0 + kStep * half + 32 * c);
-              }
-#pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (!(seen >> x & 1)) s[32 * c + x] = 0xff800000u;  // -inf
+          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t0))) {
+            uint32_t seen[2] = {0, 0};
+            if (live && box == 16) {  // 8 tokens of each of 8 boxes
+              const uint64_t a = visible(t0), b = visible(t0 + 64);
+              seen[0] = __byte_perm((uint32_t)a, (uint32_t)(a >> 32), half ? 0x7531 : 0x6420);
+              seen[1] = __byte_perm((uint32_t)b, (uint32_t)(b >> 32), half ? 0x7531 : 0x6420);
+            } else if (live) {
+              const uint64_t a = visible(t0 + kStep * half);
+              seen[0] = (uint32_t)a;
+              seen[1] = (uint32_t)(a >> 32);
             }
+#pragma unroll
+            for (int x = 0; x < kStep; ++x)
+              if (!(seen[x / 32] >> (x % 32) & 1)) s[x] = 0xff800000u;  // -inf
+          }
           // Weights against the reference as it is, unless there is none yet; their
           // sum shows whether the maximum has outgrown it, and only then is it looked for.
           bool look = __any_sync(0xffffffffu, live && m == -INFINITY);

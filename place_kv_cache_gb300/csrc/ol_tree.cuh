@@ -72,10 +72,28 @@ __device__ __forceinline__ uint32_t mask_bits(const uint64_t* m, int words, int 
   if (s > 32 && w + 1 < words) v |= m[w + 1] << (64 - s);
   return (uint32_t)v;
 }
-static __device__ __noinline__ uint32_t visible_word(const uint64_t* m, int words, int prefix, int count, int node, int low,
-                                              int t) {
+// The same for tokens [t, t + 64) of a node with mask words m (NULL: a chain).
+__device__ __forceinline__ uint64_t bit_range64(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 64);
+  return a >= b ? 0 : ~0ull >> (64 - b) & ~0ull << a;
+}
+static __device__ __noinline__ uint64_t visible64(const uint64_t* m, int words, int prefix, int count, int node, int low,
+                                                  int t) {
+  const uint64_t bits = bit_range64(low - t, prefix - t);
   const int j0 = t - prefix;
-  return visible_bits(!m, m && j0 > -32 && j0 < count ? mask_bits(m, words, j0) : 0, prefix, count, node, low, t);
+  if (j0 <= -64 || j0 >= count) return bits;
+  uint64_t tree;
+  if (!m) {
+    tree = bit_range64(0, node + 1 - j0);
+  } else if (j0 < 0) {
+    tree = m[0] << -j0;
+  } else {
+    const int w = j0 / 64, s = j0 % 64;
+    const uint64_t a = m[w], b = s && w + 1 < words ? m[w + 1] : 0;
+    tree = a >> s | (s ? b << (64 - s) : 0);
+  }
+  return bits | (tree & bit_range64(-j0, count - j0));
 }
 
 __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
