@@ -203,6 +203,28 @@ def test_tree_attention(case):
     t.check()
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_random_trees(seed):
+    """Shapes drawn over both kernels: heads, pages, groups, lengths, counts, windows, masks, output types."""
+    rng = np.random.default_rng(1000 + seed)
+    dt = "f32" if rng.random() < 0.25 else "bf16"
+    D = int(rng.choice([64, 128, 128, 64, 96, 40] if dt == "bf16" else [64, 128, 33]))
+    layout, page = ("contiguous", 0) if rng.random() < 0.5 else ("paged", int(rng.choice([16, 16, 32, 48, 64, 128, 10])))
+    H, G = int(rng.integers(1, 6)), int(rng.integers(1, 9))
+    nodes = int(rng.choice([1, 2, 5, 8, 17, 33, 64, 90]))
+    B = int(rng.integers(1, 41 if nodes < 20 else 7))
+    counts = None
+    if rng.random() < 0.5:
+        counts = rng.integers(0, nodes + 1, B)
+    prefix = rng.integers(0, int(rng.choice([3, 140, 1500])), B)
+    lens = prefix + (nodes if counts is None else counts)
+    window = int(rng.choice([-1, -1, 0, 7, 130, 1000]))
+    t = Tree(dt, layout, B, H * G, H, D, page, nodes, lens, counts, window, str(rng.choice(["tree", "random", "chain"])),
+             str(rng.choice(["f32", "bf16"])), seed=seed)
+    t.call()
+    t.check()
+
+
 def test_tree_attention_explicit_scale_and_no_positions():
     t = Tree("bf16", "contiguous", 2, 8, 2, 128, 0, 9, [200, 100], positions=False)
     t.call(scale=0.25)
