@@ -35,7 +35,8 @@
  *   value and the kernels read no lens_dev; a call captured in a CUDA graph
  *   replays the lengths (and launch size) it was captured with.
  * - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
- *   stream). Calls on one workspace must not overlap on the GPU.
+ *   stream) of the current device, on which every device pointer lives. Calls
+ *   on one workspace must not overlap on the GPU.
  * - Alignment: every device pointer must be 16-byte aligned (OL_ERR_ALIGN).
  * - dtype: OL_BF16 (bit pattern of bfloat16) or OL_F32. q and new K/V share
  *   the cache's dtype; the attention output is OL_BF16 or OL_F32.

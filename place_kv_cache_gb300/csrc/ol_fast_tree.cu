@@ -885,8 +885,10 @@ uint64_t kv_rows(const TreeParams& p) {
 template <int D, int NQ, bool PAGED>
 cudaError_t launch_cfg(const Maps& maps, const TreeParams& p, int box, int qbox, cudaStream_t s) {
   auto kern = fast_tree_kernel<D, NQ, PAGED>;
-  static const cudaError_t attr =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NQ>::kTotal);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NQ>::kTotal);
+  });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(kern, dim3(p.nctas), dim3(kThreads), Lay<D, NQ>::kTotal, s, maps, p, box, qbox,
                     p.units_per_head > 1 ? 1 : 0);

@@ -279,13 +279,14 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
 
 template <typename T, int NC, int RB>
 cudaError_t launch_tree(const TreeParams& p, cudaStream_t s) {
-  static const cudaError_t attr = [] {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [] {
     const cudaError_t e = cudaFuncSetAttribute(tree_kernel<T, NC, RB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)gen_smem<T, RB>(64 * NC));
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(tree_kernel<T, NC, RB>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared);
-  }();
+  });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(tree_kernel<T, NC, RB>, dim3(p.nctas), dim3(4 * RB), gen_smem<T, RB>(p.head_dim), s, p);
 }

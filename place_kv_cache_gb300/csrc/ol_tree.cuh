@@ -2,6 +2,8 @@
 // share of the work, visibility, addresses of cache rows, outputs and slots.
 #pragma once
 
+#include <atomic>
+
 #include "ol_common.cuh"
 #include "ol_draft.h"
 
@@ -238,6 +240,19 @@ struct TreeWalk {
     if (!p.by_unit) p.splits[blockIdx.x] = s;
   }
 };
+
+// Sets a kernel's attributes (f) before its first launch on each device.
+template <typename F>
+inline cudaError_t once_per_device(std::atomic<uint64_t>& done, F f) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = f();
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
 
 // A launch that may begin while the kernel ahead of it in the stream drains;
 // the kernels wait for it (griddepcontrol.wait) before they touch memory.
