@@ -256,3 +256,40 @@ def test_rope_append_captured_replays_with_device_positions():
                 assert bool(((cache[0][slot(b, p)].double() - want).abs() <= tol + 1e-6).all())
                 written += 2 * H
         assert int((cache != 0).any(-1).sum()) == written
+
+
+def test_offsets_past_32_bits():
+    """A cache of 2.25e9 elements: tokens appended at a row's end and kept there are those of a small cache; vectors
+    that lie 1.1e9 elements apart are rotated in place."""
+    H, D, C, T = 8, 128, 1100000, 6
+    gen = torch.Generator(device=DEV).manual_seed(77)
+    big = torch.zeros((2, 1, H, C, D), device=DEV, dtype=torch.bfloat16)
+    small = torch.zeros((2, 1, H, 16, D), device=DEV, dtype=torch.bfloat16)
+    k, v = (torch.randn((1, H, T, D), generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    rope = ol.rope(D, device=DEV)
+    at = torch.arange(C - T, C, dtype=torch.int32, device=DEV).view(1, T)
+    for cache, start in ((big, C - T), (small, 10)):
+        first = np.array([start], np.int32)
+        first_d = torch.from_numpy(first).to(DEV)
+        ol.ol_rope_append(ol.OL_LAYOUT_CONTIGUOUS, ol.kv_cache(cache), cache, rope, T, k, v, 0, None, None, first, first_d,
+                          angles_dev=at)
+    torch.cuda.synchronize()
+    assert torch.equal(big[:, :, :, C - T:], small[:, :, :, 10:]) and bool((small[:, :, :, 10:] != 0).any())
+    kept = torch.tensor([[1, 2, 5, 0, 0, 0]], dtype=torch.int32, device=DEV)
+    first = np.array([C - T], np.int32)
+    ol.ol_tree_keep(ol.OL_LAYOUT_CONTIGUOUS, ol.kv_cache(big), big, T, first, torch.from_numpy(first).to(DEV), kept,
+                    torch.tensor([3], dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(big[:, :, :, C - T: C - 3], small[:, :, :, [11, 12, 15]])
+    flat, stride = big.view(-1), 1120000000
+    ends = [flat[i * stride: i * stride + 4 * D] for i in range(3 if 2 * stride + 4 * D <= flat.numel() else 2)]
+    for e in ends:
+        e.copy_(torch.randn(4 * D, generator=gen, device=DEV))
+    want = [torch.empty((1, 2, 2, D), device=DEV, dtype=torch.bfloat16) for _ in ends]
+    where = torch.tensor([[5, 900]] * len(ends), dtype=torch.int32, device=DEV)
+    for e, w in zip(ends, want):
+        ol.ol_rope_rows(rope, ol.OL_BF16, 1, 2, 2, D, e.view(1, 2, 2, D), w, where[:1], True)
+    view = ol.Rows(big.data_ptr(), stride, 2 * D, D)
+    ol.ol_rope_rows(rope, ol.OL_BF16, len(ends), 2, 2, D, view, view, where, True)
+    torch.cuda.synchronize()
+    assert len(ends) == 3 and all(torch.equal(e.view(1, 2, 2, D), w) for e, w in zip(ends, want))
