@@ -14,13 +14,16 @@
 // tile; with up to 128 (NQ = 1) both have the same queries and a stream takes its
 // half of every tile, and they are joined at the segment's end.
 //   S = Q K^T      128 x 64 x D, both operands in shared memory, S in TMEM
-//   P = 2^(S - m)  registers, bf16, back to TMEM over S
-//   O += P V       128 x D x 64, P from TMEM, V from shared memory, O in TMEM
+//   P = 2^(S - m)  registers, back to TMEM over S: its bf16 part and its remainder's
+//   O += P V       128 x D x 64 for each of the two, P from TMEM, V from shared memory,
+//                  O in TMEM
 // m is a reference near the row's maximum: it is set from a segment's first
 // scores and again only when a step's weights sum to more than 2^10 (fp32 and
 // bf16 carry such weights as exactly as smaller ones), so the maximum is looked
-// for, and O rescaled, rarely. Sums and O are fp32; P is rounded to bf16, the
-// type its product with V takes: as much as the output's own rounding.
+// for, and O rescaled, rarely. Sums and O are fp32. P's product takes bf16: P is the
+// sum of its bf16 part and of the remainder's, 16 bits together, as the weights of the
+// decode and chunked steps are (one part alone: 3.5e-3 off in fp32 outputs near 1,
+// as much again as the output's own rounding in bf16 ones).
 //
 // Warps: 0 producer (TMA; a lane per box of a tile: pages of 16 tokens are
 // boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 V's tiles and the
@@ -480,10 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         const uint64_t vd = smem_desc(base + L::kRing + v.slot * L::kTileBytes + half * step, block, group);
 #pragma unroll
         for (int x = 0; x < kStep / 16; ++x) {
+          const uint64_t v16 = vd + x * (2 * group / 16);  // 16 tokens: times P, times its remainder
           if (x == 0)
-            mma_ts(to, ts + b * kStep, vd, kDescO, !first);
+            mma_ts(to, ts + b * kStep, v16, kDescO, !first);
           else
-            mma_ts(to, ts + b * kStep + x * 8, vd + x * (2 * group / 16), kDescO, true);
+            mma_ts(to, ts + b * kStep + x * 8, v16, kDescO, true);
+          mma_ts(to, ts + b * kStep + kStep / 2 + x * 8, v16, kDescO, true);
         }
         mma_commit(bar.pvdone(j, b));
         if (last_of_v) mma_commit(bar.empty(v.slot));
@@ -667,29 +672,30 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
         const int t0 = w.row.start + (w.tile0 + tile) * kTile;
         const bool edge = edge_tile(w.row, low_all, t0);
         if (live_warp) {
-          tmem_wait_ld(s);
-          tmem_wait_ld(s + 32);
-          if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t0))) {
-            uint32_t seen[2] = {0, 0};
-            if (live && box == 16) {  // 8 tokens of each of 8 boxes
-              const uint64_t a = visible(t0), b = visible(t0 + 64);
-              seen[0] = __byte_perm((uint32_t)a, (uint32_t)(a >> 32), half ? 0x7531 : 0x6420);
-              seen[1] = __byte_perm((uint32_t)b, (uint32_t)(b >> 32), half ? 0x7531 : 0x6420);
-            } else if (live) {
-              const uint64_t a = visible(t0 + kStep * half);
-              seen[0] = (uint32_t)a;
-              seen[1] = (uint32_t)(a >> 32);
-            }
-#pragma unroll
-            for (int x = 0; x < kStep; ++x)
-              if (!(seen[x / 32] >> (x % 32) & 1)) s[x] = 0xff800000u;  // -inf
-          }
           // Weights against the reference as it is, unless there is none yet; their
-          // sum shows whether the maximum has outgrown it, and only then is it looked for.
+          // sum shows whether the maximum has outgrown it, and only then is it looked
+          // for, with S read again: the weights' remainders take its registers.
           bool look = __any_sync(0xffffffffu, live && m == -INFINITY);
           float sum_step;
           uint32_t pk[kStep / 2];
           for (;;) {
+            tmem_wait_ld(s);
+            tmem_wait_ld(s + 32);
+            if (edge || (p.window >= 0 && __any_sync(0xffffffffu, low > t0))) {
+              uint32_t seen[2] = {0, 0};
+              if (live && box == 16) {  // 8 tokens of each of 8 boxes
+                const uint64_t a = visible(t0), b = visible(t0 + 64);
+                seen[0] = __byte_perm((uint32_t)a, (uint32_t)(a >> 32), half ? 0x7531 : 0x6420);
+                seen[1] = __byte_perm((uint32_t)b, (uint32_t)(b >> 32), half ? 0x7531 : 0x6420);
+              } else if (live) {
+                const uint64_t a = visible(t0 + kStep * half);
+                seen[0] = (uint32_t)a;
+                seen[1] = (uint32_t)(a >> 32);
+              }
+#pragma unroll
+              for (int x = 0; x < kStep; ++x)
+                if (!(seen[x / 32] >> (x % 32) & 1)) s[x] = 0xff800000u;  // -inf
+            }
             if (look) {
               float mx = -INFINITY;
 #pragma unroll
@@ -724,14 +730,18 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
               const float ea = fast_exp2(__uint_as_float(a)), eb = fast_exp2(__uint_as_float(b));
               sum[x & 1] = add_f32x2(sum[x & 1], pack_f32x2(ea, eb));
               pk[x] = pack_bf16x2(ea, eb);
+              s[x] = pack_bf16x2(ea - __uint_as_float(pk[x] << 16), eb - __uint_as_float(pk[x] & 0xffff0000u));
             }
             uint32_t a, b;
             unpack_b32x2(add_f32x2(sum[0], sum[1]), a, b);
             sum_step = __uint_as_float(a) + __uint_as_float(b);
             if (look || !__any_sync(0xffffffffu, live && !(sum_step <= kGrown))) break;
             look = true;  // (also for NaN)
+            tmem_ld32(ts + (i & 1) * kStep, s);
+            tmem_ld32(ts + (i & 1) * kStep + 32, s + 32);
           }
           tmem_st32(ts + (i & 1) * kStep, pk);
+          tmem_st32(ts + (i & 1) * kStep + kStep / 2, s);
           l += sum_step;
         }
         // the next scores, if they are there, come in while P settles

@@ -225,6 +225,40 @@ def test_random_trees(seed):
     t.check()
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [
+    # layout, B, Hq, H, D, page, nodes, lens: rows of few tokens, where a weight's rounding is not averaged away
+    ("contiguous", 3, 8, 8, 128, 0, 1, [2, 3, 9]),
+    ("contiguous", 4, 28, 4, 128, 0, 8, [8, 11, 30, 90]),
+    ("contiguous", 3, 16, 2, 64, 0, 7, [7, 9, 140]),
+    ("contiguous", 3, 32, 8, 128, 0, 64, [64, 70, 130]),
+    ("contiguous", 2, 16, 2, 64, 0, 33, [33, 36]),
+    ("paged", 4, 8, 2, 128, 16, 5, [5, 7, 20, 140]),
+    ("paged", 3, 32, 8, 128, 16, 40, [40, 43, 150]),
+    ("paged", 3, 28, 4, 128, 64, 50, [50, 60, 131]),
+    ("paged", 2, 8, 2, 64, 128, 6, [6, 150]),
+], ids=lambda c: "-".join(map(str, c[:7])))
+def test_weights_of_the_tensor_core_kernel_keep_16_bits(case, out):
+    """V is multiplied by a weight's bf16 part and by the bf16 of its remainder, as in the decode and chunked steps:
+    each is off by at most 2^-8 of itself, together by 2^-16 of the weight."""
+    layout, B, Hq, H, D, page, nodes, lens = case
+    t = Tree("bf16", layout, B, Hq, H, D, page, nodes, lens, out=out, seed=23)
+    t.call()
+    torch.cuda.synchronize()
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+    G, step = Hq // H, torch.finfo(t.out_dtype).eps / 2
+    for b in range(B):
+        n = int(t.lens[b])
+        ok = du.visible(n, nodes, t.sees[b], t.at[b], -1)
+        for g in range(H):
+            want, pv, _, size = du.tree_attention(t.q[b, g * G: (g + 1) * G], t.row(0, b, n)[g], t.row(1, b, n)[g], ok,
+                                                  D ** -0.5)
+            tol = du.tree_tolerance(want, pv, size, D, n, torch.float64, False) + 2.0 ** -16 * pv
+            tol = tol + step * (want.abs() + tol)
+            off = (t.out[b, g * G: (g + 1) * G].double() - want).abs() - tol
+            assert float(off.max()) <= 0, f"row {b} head {g}: {float(off.max()):.3e} more than the bound"
+
+
 def test_tree_attention_explicit_scale_and_no_positions():
     t = Tree("bf16", "contiguous", 2, 8, 2, 128, 0, 9, [200, 100], positions=False)
     t.call(scale=0.25)
