@@ -598,10 +598,9 @@ OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* up
  *             NULL: prefix length + i; required with both a mask and a window.
  * q and out [batch, q_heads, nodes, head_dim] (q in the cache's dtype, out in
  * out_dtype), as ol_chunk_step. scale <= 0 selects 1/sqrt(head_dim). A node that
- * sees nothing gives 0; what a node does not see has no influence on its output,
- * whatever K and V hold there (drafted tokens hidden from some nodes and visible
- * to others may hold infinities or NaN; a prefix token behind a window must be
- * finite while other nodes still see it).
+ * sees nothing gives 0; what a node does not see, drafted tokens and those of the
+ * prefix behind its window, has no influence on its output, whatever K and V hold
+ * there: infinities and NaN reach the nodes that see them.
  * ws_bytes >= ol_workspace_size_tree(batch, q_heads, kv_heads, head_dim, nodes);
  * the workspace needs ol_workspace_init once and may be that of decode steps and
  * of chunked steps of up to `nodes` tokens of the same batch and kv heads (their

@@ -27,9 +27,10 @@
 //
 // Warps: 0 producer (TMA; a lane per box of a tile: pages of 16 tokens are
 // boxes of 16 rows), 1 and 2 MMA issue for a stream each, 3 V's tiles and the
-// note for the merge, 4-7 and 8-11 the streams. In tiles that hold drafted tokens
-// or end the row, warp 3 first zeroes the rows outside the row's tokens and the
-// non-finite elements of drafted ones: a product with P = 0 must not see them.
+// note for the merge, 4-7 and 8-11 the streams. In tiles that hold drafted tokens,
+// tokens behind some node's window or the row's end, warp 3 first zeroes the rows outside
+// the row's tokens and the non-finite elements of tokens that are hidden from some node:
+// a product with P = 0 must not see them.
 // Where there was such an element, the non-finite values of the tokens that a row
 // sees are added to its outputs at the end (rare, unhurried).
 //
@@ -252,6 +253,14 @@ struct Cursor {
 __device__ __forceinline__ int row_low(const TreeParams& p, const TreeRow& r) {
   return p.window < 0 || r.prefix <= p.window ? 0 : r.prefix - p.window;
 }
+// End of the prefix tokens that a window hides from some node: tokens from
+// row_low to this one are seen by some nodes only (or by none). Whole warps.
+__device__ __forceinline__ int row_hidden_end(const TreeParams& p, const TreeRow& r, int b) {
+  if (p.window < 0) return 0;
+  int end = 0;
+  for (int n = threadIdx.x % 32; n < r.count; n += 32) end = max(end, tree_low(p, r, b, n));
+  return min(__reduce_max_sync(0xffffffffu, end), r.prefix);
+}
 // The tile holds tokens that are not the prefix of all rows: drafted ones, the
 // end of the row, or tokens below the window.
 __device__ __forceinline__ bool edge_tile(const TreeRow& r, int low, int t0) {
@@ -267,6 +276,12 @@ struct Maps {
   CUtensorMap q, kv;
 };
 
+// Whether one of eight bf16 elements is infinite or NaN: its exponent of ones carries into the sign's place.
+__device__ __forceinline__ bool nonfinite_in(uint4 x) {
+  auto full = [](uint32_t e) { return (e & 0x7f807f80u) + 0x00800080u; };
+  return ((full(x.x) | full(x.y) | full(x.z) | full(x.w)) & 0x80008000u) != 0;
+}
+
 // Drafted tokens [j0, j0 + 32) among `bits` that lie within the window of a node.
 __device__ __noinline__ uint32_t in_window(const TreeParams& p, const TreeRow row, int b, int node, int j0, uint32_t bits) {
   const int at = tree_position(p, row, b, node);
@@ -277,27 +292,35 @@ __device__ __noinline__ uint32_t in_window(const TreeParams& p, const TreeRow ro
   return bits;
 }
 
-// Adds the non-finite elements, in dimensions [d0, d1), of the V of drafted
-// tokens in the segment's tiles that a node sees to what this thread has
-// written for it: to the slot's row `place`, or to row `out` of the output.
+// Adds the non-finite elements, in dimensions [d0, d1), of the V of the segment's
+// tokens that are hidden from some node, [low_all, hidden_end) and the drafted
+// ones, and that this node sees, to what this thread has written for it: to the
+// slot's row `place`, or to row `out` of the output.
 __device__ __noinline__ void add_nonfinite(const TreeParams& p, TreeRow row, int b, int g, int tile0, int tile1, int node,
-                                           int d0, int d1, float* slot, int place, size_t out) {
-  const int a = max(row.start + tile0 * kTile, row.prefix), e = min(row.start + tile1 * kTile, row.len);
+                                           int low_all, int hidden_end, int d0, int d1, float* slot, int place, size_t out) {
+  const int a = max(row.start + tile0 * kTile, low_all), e = min(row.start + tile1 * kTile, row.len);
+  const int low = p.window < 0 ? 0 : tree_low(p, row, b, node);
   for (int t = a; t < e; ++t) {
-    if (!tree_sees_drafted(p, row, b, node, t - row.prefix)) continue;
+    if (t < row.prefix && t >= hidden_end) t = row.prefix;  // what all nodes see is in the products
+    if (t >= e) break;
+    if (t < row.prefix ? t < low : !tree_sees_drafted(p, row, b, node, t - row.prefix)) continue;
     const long long at = cache_row(p.cache, 1, b, g, t);
     if (at < 0) continue;
     const uint16_t* const v = reinterpret_cast<const uint16_t*>(p.cache.base) + at * p.head_dim;
-    for (int d = d0; d < d1; ++d) {
-      if ((v[d] & 0x7f80u) != 0x7f80u) continue;
-      const float x = bf16_bits_to_float(v[d]);
-      if (slot) {
-        slot[2 * p.rows_per_unit + ((size_t)(d / 4) * p.rows_per_unit + place) * 4 + d % 4] += x;
-      } else if (p.out_dtype == OL_F32) {
-        reinterpret_cast<float*>(p.out)[out * p.head_dim + d] += x;
-      } else {
-        uint16_t& y = reinterpret_cast<uint16_t*>(p.out)[out * p.head_dim + d];
-        y = float_to_bf16_bits(bf16_bits_to_float(y) + x);
+    for (int d8 = d0; d8 < d1; d8 += 8) {
+      const uint4 x8 = *reinterpret_cast<const uint4*>(v + d8);
+      if (!nonfinite_in(x8)) continue;
+      for (int d = d8; d < d8 + 8; ++d) {
+        if ((v[d] & 0x7f80u) != 0x7f80u) continue;
+        const float x = bf16_bits_to_float(v[d]);
+        if (slot) {
+          slot[2 * p.rows_per_unit + ((size_t)(d / 4) * p.rows_per_unit + place) * 4 + d % 4] += x;
+        } else if (p.out_dtype == OL_F32) {
+          reinterpret_cast<float*>(p.out)[out * p.head_dim + d] += x;
+        } else {
+          uint16_t& y = reinterpret_cast<uint16_t*>(p.out)[out * p.head_dim + d];
+          y = float_to_bf16_bits(bf16_bits_to_float(y) + x);
+        }
       }
     }
   }
@@ -550,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------- V to rights, the merge's note
-    // Rows of a V tile outside the row's tokens become zeros, drafted ones lose
-    // their non-finite elements, before the tile counts as full. A tile or two
+    // Rows of a V tile outside the row's tokens become zeros, tokens hidden from some
+    // node lose their non-finite elements, before the tile counts as full. A tile or two
     // ahead of the products, so that its time is hidden; in the streams it was not
     // (256 nodes over 8 rows 138 us, here 126).
     if (lane == 0) {
@@ -563,13 +586,14 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
     Cursor v(L::kK, L::kV);
     bool ok = true;
     while (ok && w.next(p)) {
-      const int low = row_low(p, w.row);
+      const int low = row_low(p, w.row), hidden_end = row_hidden_end(p, w.row, w.b);
       for (int i = w.tile0; i < w.tile1; ++i) {
         if (!(ok = warp_wait(bar.landed(v.slot), v.phase, abort, p.status))) break;
         const int t0 = w.row.start + i * kTile;
-        if (edge_tile(w.row, low, t0)) {
+        if (edge_tile(w.row, max(low, hidden_end), t0)) {
           uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes);
-          const int r_low = low - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;  // rows of the tile
+          // rows of the tile
+          const int r_low = low - t0, r_hidden = hidden_end - t0, r_tree = w.row.prefix - t0, r_end = w.row.len - t0;
           constexpr int kAhead = 8, kPieces = kTile * D / 8;  // pieces of 16 bytes: of a lane at a time, all
           bool found = false;
 #pragma unroll 1
@@ -582,14 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
               const int r = (line >> box_log2) / L::kHalves << box_log2 | (line & (box - 1));
               zero[c] = r < r_low || r >= r_end;
               x[c] = make_uint4(0, 0, 0, 0);
-              if (!zero[c] && r >= r_tree) x[c] = tile[x0 + 32 * c];
+              if (!zero[c] && (r >= r_tree || r < r_hidden)) x[c] = tile[x0 + 32 * c];
             }
 #pragma unroll
             for (int c = 0; c < kAhead; ++c) {
               if (zero[c]) tile[x0 + 32 * c] = x[c];
-              // an exponent of ones carries into the sign's place
-              auto full = [](uint32_t e) { return (e & 0x7f807f80u) + 0x00800080u; };
-              hit |= ((full(x[c].x) | full(x[c].y) | full(x[c].z) | full(x[c].w)) & 0x80008000u) != 0;
+              hit |= nonfinite_in(x[c]);
             }
             if (hit) {
               found = true;
@@ -841,8 +863,10 @@ __global__ void __launch_bounds__(kThreads, 1) fast_tree_kernel(const __grid_con
           }
         }
         __syncwarp();  // add_nonfinite reads what other lanes wrote
-        if (*bad && mine)  // (of this or an earlier segment)
-          add_nonfinite(p, w.row, w.b, w.g, w.tile0, w.tile1, node, c0, c0 + kCols, slot, place,
+        const bool any_bad = __any_sync(0xffffffffu, *bad != 0);  // (of this or an earlier segment)
+        const int hidden_end = any_bad ? row_hidden_end(p, w.row, w.b) : 0;
+        if (any_bad && mine)
+          add_nonfinite(p, w.row, w.b, w.g, w.tile0, w.tile1, node, low_all, hidden_end, c0, c0 + kCols, slot, place,
                         tree_out_row(p, w.b, w.g, r));
       }
       if (NQ == 1) {  // both streams have read both O before either's next product

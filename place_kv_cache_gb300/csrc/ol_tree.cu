@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
           s[r][1] = fmaf(a.w, k1.w, fmaf(a.z, k1.z, fmaf(a.y, k1.y, fmaf(a.x, k1.x, s[r][1]))));
         }
       }
-      const bool drafted = t0 + TB > w.row.prefix;  // some row may not see some token of the tile
+      const bool drafted = t0 + TB > w.row.prefix;
+      bool some = drafted;  // some row of the warp may not see some token of the tile
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r][0] *= p.scale_log2, s[r][1] *= p.scale_log2;
       if (drafted) {
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            if (t0 + cg + 16 * u < low[r]) s[r][u] = -INFINITY;
+            if (t0 + cg + 16 * u < low[r]) s[r][u] = -INFINITY, some = true;
+        some = __any_sync(0xffffffffu, some);
       }
       float pr[4][2];
 #pragma unroll
@@ -235,7 +237,7 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
           }
         }
       };
-      if (drafted)
+      if (some)
         add(std::true_type());
       else
         add(std::false_type());

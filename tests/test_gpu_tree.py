@@ -285,6 +285,42 @@ def test_hidden_infinities_and_nan(dt, D):
     assert not torch.isfinite(t.out[:, :, 3, 3]).any() and torch.isfinite(t.out[:, :, 0]).all()
 
 
+@pytest.mark.parametrize("far", [0, 1, 300])
+@pytest.mark.parametrize("dt,layout,page,H,Hq,D,nodes", [
+    ("bf16", "contiguous", 0, 2, 8, 128, 12), ("bf16", "paged", 16, 2, 8, 128, 12), ("bf16", "paged", 64, 2, 8, 64, 9),
+    ("bf16", "contiguous", 0, 2, 8, 128, 64), ("bf16", "paged", 16, 1, 8, 128, 70), ("bf16", "contiguous", 0, 2, 8, 96, 12),
+    ("f32", "contiguous", 0, 2, 8, 128, 12), ("f32", "paged", 16, 2, 4, 80, 20)])
+def test_infinities_and_nan_of_the_prefix_behind_a_window(dt, layout, page, H, Hq, D, nodes, far):
+    """Prefix tokens that the window hides from some nodes, or from all: only those that see them are touched.
+    Positions lie near one another, `far` behind the prefix, or over 300 tokens (several tiles)."""
+    t = Tree(dt, layout, 3, Hq, H, D, page, nodes, [nodes + 900, nodes + 433, nodes + 150], window=200, seed=51)
+    prefix = t.lens - nodes
+    if far == 300:
+        t.at = (prefix[:, None] + t.rng.integers(0, far, (3, nodes))).astype(np.int32)
+        t.at[:, 0] = prefix
+    else:
+        t.at = t.at + far
+    t.at_d = torch.from_numpy(t.at).to(DEV)
+    touched = 0
+    for b in range(3):
+        low = np.maximum(t.at[b].astype(np.int64) - 200, 0)  # each node's lowest prefix token
+        for x in sorted({int(low.min()) - 1, int(low.min()), int(np.median(low)), int(low.max()) - 1}):
+            if 0 <= x < min(int(low.max()), int(prefix[b])):  # hidden from some node
+                t.token(1, b, x)[:, x % D] = float("inf") if x % 2 else float("nan")
+                if x < low.min():
+                    t.token(0, b, x)[:] = float("nan")
+                    t.token(1, b, x)[:] = float("nan")
+                touched += 1
+        x = int(prefix[b]) - 200
+        if 0 <= x < low.min():                               # seen by none, although a node at the prefix's end would
+            t.token(0, b, x)[:] = float("nan")
+            t.token(1, b, x)[:] = -float("inf")
+            touched += 1
+    assert touched >= 3
+    t.call()
+    t.check()
+
+
 def test_large_scores_and_equal_scores():
     t = Tree("bf16", "contiguous", 1, 4, 1, 128, 0, 6, [900], seed=4)
     t.q.mul_(16)                                     # weights concentrate: the running maximum moves often
