@@ -108,7 +108,7 @@ OL_HD inline TreeRow tree_row(int len, int count, int window, int tile_log2) {
   r.prefix = len - count;
   const int lo = window < 0 || r.prefix <= window ? 0 : r.prefix - window;
   r.start = lo >> tile_log2 << tile_log2;
-  r.ntiles = count > 0 ? (len - r.start + (1 << tile_log2) - 1) >> tile_log2 : 0;
+  r.ntiles = count > 0 ? ((len - r.start - 1) >> tile_log2) + 1 : 0;  // (len may be 2^31 - 1)
   return r;
 }
 

@@ -88,12 +88,12 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
     };
     // tile `tile` into stage `tile` % 2
     auto copy = [&](int tile) {
-      const int j = tid / kPer, t = w.row.start + tile * TB + j;
+      const int j = tid / kPer, t0 = w.row.start + tile * TB;
       uint8_t* const to = ring + (tile % kGenStages * 2 * TB + j) * rb;
-      const bool there = t >= low_all && t < w.row.len;
+      const bool there = j >= low_all - t0 && j < w.row.len - t0;  // (t0 + TB may pass 2^31)
 #pragma unroll
       for (int plane = 0; plane < 2; ++plane) {
-        const long long row = there ? cache_row(p.cache, plane, w.b, w.g, t) : -1;
+        const long long row = there ? cache_row(p.cache, plane, w.b, w.g, t0 + j) : -1;
         if (there && row < 0) set_status(p.status, OL_DEVICE_GUARD);
         copy_row(to + plane * TB * rb, reinterpret_cast<const T*>(p.cache.base) + (row < 0 ? 0 : row * D), row >= 0,
                  tid % kPer, kPer);
@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
           s[r][1] = fmaf(a.w, k1.w, fmaf(a.z, k1.z, fmaf(a.y, k1.y, fmaf(a.x, k1.x, s[r][1]))));
         }
       }
-      const bool drafted = t0 + TB > w.row.prefix;
+      const int j0 = t0 - w.row.prefix;  // index among the drafted of the tile's first token
+      const bool drafted = j0 > -TB;
       bool some = drafted;  // some row of the warp may not see some token of the tile
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[r][0] *= p.scale_log2, s[r][1] *= p.scale_log2;
@@ -158,10 +159,9 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
         int pos[2] = {0, 0};  // of this thread's tokens
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int j = t0 + cg + 16 * u - w.row.prefix;
+          const int j = j0 + cg + 16 * u;
           if (p.window >= 0 && j >= 0 && j < w.row.count) pos[u] = tree_position(p, w.row, w.b, j);
         }
-        const int j0 = t0 - w.row.prefix;
         uint32_t bits[4] = {};  // all rows' on their way together
         if (p.mask && j0 < w.row.count)
 #pragma unroll
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(4 * RB, gen_per_sm(NC, RB)) tree_kernel(const 
           const uint32_t seen = visible_bits(!p.mask, bits[r], w.row.prefix, w.row.count, node[r], low[r], t0);
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            if (!(seen >> (cg + 16 * u) & 1) || (p.window >= 0 && t0 + cg + 16 * u >= w.row.prefix &&
+            if (!(seen >> (cg + 16 * u) & 1) || (p.window >= 0 && j0 + cg + 16 * u >= 0 &&
                                                  (long long)at[r] - pos[u] > p.window))
               s[r][u] = -INFINITY;
         }

@@ -29,7 +29,7 @@ __device__ __forceinline__ float* tree_slot(const TreeParams& p, int slot) {
 
 // Position of a node: no lower than its row's prefix length.
 __device__ __forceinline__ int tree_position(const TreeParams& p, const TreeRow& row, int b, int node) {
-  if (!p.node_pos) return row.prefix + node;
+  if (!p.node_pos) return row.prefix + min(node, row.count);  // (of nodes past the count: whatever fits an int)
   return max(row.prefix, p.node_pos[(size_t)b * p.nodes + node]);
 }
 

@@ -3,6 +3,9 @@ the scalings' formulas, and every refusal, on the host before any launch. Device
 pointers are fake aligned addresses; valid requests are stopped right after
 validation by the host fault-injection switch, so nothing reaches the GPU."""
 import math
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -306,6 +309,35 @@ def test_tree_attention_counts_its_work_in_32_bits():
     assert st((1 << 31) - 1, 32) == ol.OL_ERR_UNSUPPORTED               # 2^26 tiles, 8 rows, 2 heads, 2 units
     assert st((1 << 31) - 1, 16) == ol.OL_ERR_INJECTED                  # 1 unit
     assert st((1 << 30) - 200, 32) == ol.OL_ERR_INJECTED                # half the tiles
+
+
+def test_a_rows_tiles_up_to_the_largest_length(tmp_path):
+    """The work split's tiles of a row, against Python's integers: lengths up to 2^31 - 1, with and without a window."""
+    cases = []
+    for log2 in (5, 7):
+        for length in [1, 2, 31, 32, 33, 128, 129] + [2 ** 31 - 1 - d for d in (0, 1, 30, 31, 32, 127, 128, 129, 300)]:
+            for count in sorted({0, 1, min(length, 7), min(length, 512)}):
+                for window in (-1, 0, 100, 2 ** 31 - 1):
+                    cases.append((length, count, window, log2))
+    source = tmp_path / "rows.cpp"
+    source.write_text('#include <cstdio>\n#include "ol_draft.h"\nint main() {\n  int n, c, w, t;\n'
+                      "  while (scanf(\"%d %d %d %d\", &n, &c, &w, &t) == 4) {\n"
+                      "    const ol::TreeRow r = ol::tree_row(n, c, w, t);\n"
+                      '    printf("%d %d %d\\n", r.prefix, r.start, r.ntiles);\n  }\n}\n')
+    exe = str(tmp_path / "rows")
+    csrc = os.path.join(os.path.dirname(ol.__file__), "csrc")
+    cuda = next((d for d in (os.environ.get("CUDA_HOME"), "/usr/local/cuda") if d and os.path.isdir(d)), None)
+    if cuda is None or shutil.which("g++") is None:
+        pytest.skip("no host compiler or no CUDA headers")
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, "-I", os.path.join(cuda, "include"), str(source), "-o", exe],
+                   check=True)
+    got = subprocess.run([exe], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True,
+                         check=True).stdout.split("\n")
+    for (length, count, window, log2), line in zip(cases, got):
+        prefix = length - count
+        start = (0 if window < 0 else max(0, prefix - window)) >> log2 << log2
+        tiles = -(-(length - start) // 2 ** log2) if count else 0
+        assert line == f"{prefix} {start} {tiles}", (length, count, window, log2)
 
 
 def test_tree_attention_checks_the_pages_it_reads():

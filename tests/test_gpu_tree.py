@@ -358,6 +358,46 @@ def test_one_long_row_past_32_bit_offsets():
     assert ol.ol_workspace_status(ws) == ol.OL_DEVICE_OK
 
 
+@pytest.mark.parametrize("window", [-1, 100, 0])
+@pytest.mark.parametrize("short", [0, 1, 31, 40])
+def test_the_longest_row(short, window):
+    """A contiguous cache of 2^31 - 1 tokens of one element: lengths at which a tile's end passes 2^31."""
+    C, nodes = 2 ** 31 - 1, 5
+    n = C - short
+    cache = torch.zeros((2, 1, 1, C, 1), device=DEV, dtype=torch.bfloat16)
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    last = 200
+    for plane in (0, 1):
+        cache[plane, 0, 0, n - last: n] = torch.randn((last, 1), generator=gen, device=DEV).to(torch.bfloat16)
+        cache[plane, 0, 0, n:] = float("nan")
+    if window < 0:  # what lies before counts by its number: keys of zero, weights of one, values of zero
+        cache[0, 0, 0, n - last: n] *= 8
+    q = torch.randn((1, 2, nodes, 1), generator=gen, device=DEV).to(torch.bfloat16) * 4
+    out = torch.full((1, 2, nodes, 1), -77.0, device=DEV)
+    lens = np.array([n], np.int32)
+    sees, depth = du.random_trees(np.random.default_rng(3), 1, nodes)
+    at = np.minimum(n - nodes + depth, 2 ** 31 - 1).astype(np.int32)
+    size = ol.ol_workspace_size_tree(1, 2, 1, 1, nodes)
+    ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    ol.ol_tree_attention(ol.OL_LAYOUT_CONTIGUOUS, ol.kv_cache(cache), q, 2, nodes, lens, torch.from_numpy(lens).to(DEV),
+                         None, None, torch.from_numpy(du.pack_mask(sees)).to(DEV), torch.from_numpy(at).to(DEV), 1.0, window,
+                         out, ol.OL_F32, ws, size)
+    k, v = cache[0, 0, 0, n - last: n].double(), cache[1, 0, 0, n - last: n].double()
+    ok = torch.from_numpy(du.visible(last, nodes, sees[0], at[0].astype(np.int64) - (n - last), window)).to(DEV)
+    s = torch.where(ok, q[0].double() * k[:, 0], -torch.inf)           # [2, nodes, last]
+    before = n - last if window < 0 else 0                             # tokens of score 0 and value 0
+    top = torch.clamp(s.amax(-1, keepdim=True), min=0.0 if before else -torch.inf)
+    p = torch.exp(s - top)
+    total = p.sum(-1, keepdim=True) + before * torch.exp(-top)
+    want, pv = (p * v[:, 0]).sum(-1) / total[..., 0], (p * v[:, 0].abs()).sum(-1) / total[..., 0]
+    # sums of n positive terms in fp32 over some 600 CTAs of 16 threads a row, then their merge
+    tol = du.tree_tolerance(want, pv, s[ok.expand_as(s)].abs().max(), 1, n / 9000 + 700, torch.float32, False)
+    assert ol.ol_workspace_status(ws) == ol.OL_DEVICE_OK
+    assert bool(((out[0, ..., 0].double() - want).abs() <= tol).all())
+    del cache
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_replays_follow_the_device_lengths(dt):
     """A captured call replays with the lengths, counts and masks on the device; two captured calls with workspaces
