@@ -640,6 +640,19 @@ OL_API ol_status ol_tree_attention(int32_t layout, const void* cache_desc, const
 OL_API ol_status ol_tree_keep(int32_t layout, const void* cache_desc, void* updated, int32_t nodes,
                               const int32_t* starts_host, const int32_t* starts_dev, const int32_t* kept_dev,
                               const int32_t* kept_counts_dev, void* workspace, ol_stream stream);
+/*
+ * ol_tree_keep where rows drafted fewer tokens than `nodes`, as counts of
+ * ol_rope_append and ol_tree_attention say: row b has drafted tokens
+ * 0 .. counts[b] - 1 (0 <= counts[b] <= nodes; both NULL: nodes), its kept list
+ * lies in [0, counts[b]), and the host checks starts[b] + counts[b] <= capacity
+ * and the pages of those tokens only: a short row may end at its cache's
+ * capacity, and its table may name no page past its tokens. The kernel reads
+ * counts_dev. kept_dev stays [batch, nodes]. Errors: as ol_tree_keep.
+ */
+OL_API ol_status ol_tree_keep_counted(int32_t layout, const void* cache_desc, void* updated, int32_t nodes,
+                                      const int32_t* starts_host, const int32_t* starts_dev,
+                                      const int32_t* counts_host, const int32_t* counts_dev, const int32_t* kept_dev,
+                                      const int32_t* kept_counts_dev, void* workspace, ol_stream stream);
 
 /*
  * Storage statistics of a call (page "Persistent input/output feedback",

@@ -42,7 +42,8 @@ SYMBOLS = ("ol_status_string", "ol_version", "ol_workspace_size", "ol_workspace_
            "ol_decode_step_host", "ol_last_call_stats", "ol_total_stats", "ol_reset_stats",
            "ol_workspace_size_chunk", "ol_chunk_step", "ol_hpaged_append", "ol_hpaged_decode_attention",
            "ol_hpaged_decode_step", "ol_hpaged_quantize", "ol_hpaged_chunk_step", "ol_rope_turns", "ol_rope_rows",
-           "ol_rope_append", "ol_workspace_size_tree", "ol_tree_attention", "ol_tree_keep")
+           "ol_rope_append", "ol_workspace_size_tree", "ol_tree_attention", "ol_tree_keep",
+           "ol_tree_keep_counted")
 
 
 class Stats(ctypes.Structure):
@@ -184,6 +185,7 @@ def load(build_if_missing: bool = True, variant: str = ""):
         "ol_workspace_size_tree": (sz, [i32, i32, i32, i32, i32]),
         "ol_tree_attention": (st, [i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, f32, i32, vp, i32, vp, sz, vp]),
         "ol_tree_keep": (st, [i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
+        "ol_tree_keep_counted": (st, [i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -651,3 +653,12 @@ def ol_tree_keep(layout: int, desc, updated, nodes: int, starts_host, starts_dev
     sh = _host_i32(starts_host)
     _check(load().ol_tree_keep(layout, _ref(desc), _ptr(updated), nodes, _ptr(sh), _ptr(starts_dev), _ptr(kept_dev),
                                _ptr(kept_counts_dev), _ptr(workspace), _stream(stream)), "ol_tree_keep")
+
+
+def ol_tree_keep_counted(layout: int, desc, updated, nodes: int, starts_host, starts_dev, counts_host, counts_dev,
+                         kept_dev, kept_counts_dev, workspace=None, stream=None):
+    """ol_tree_keep of rows that drafted counts[b] <= nodes tokens (None: all rows have `nodes`)."""
+    sh, ch = _host_i32(starts_host), _host_i32(counts_host)
+    _check(load().ol_tree_keep_counted(layout, _ref(desc), _ptr(updated), nodes, _ptr(sh), _ptr(starts_dev), _ptr(ch),
+                                       _ptr(counts_dev), _ptr(kept_dev), _ptr(kept_counts_dev), _ptr(workspace),
+                                       _stream(stream)), "ol_tree_keep_counted")

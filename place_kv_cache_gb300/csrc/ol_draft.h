@@ -151,7 +151,8 @@ struct KeepParams {
   int dtype, head_dim, nodes;
   const int32_t* starts;  // [batch]
   const int32_t* kept;    // [batch, nodes]
-  const int32_t* counts;  // [batch]
+  const int32_t* counts;  // [batch], of kept
+  const int32_t* drafted; // [batch], or NULL: nodes
   int32_t* status;        // or NULL
 };
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s);

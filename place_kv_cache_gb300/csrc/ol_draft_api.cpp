@@ -422,26 +422,31 @@ ol_status tree_attention(int32_t layout, const void* cache_desc, const void* q, 
 }
 
 ol_status tree_keep(int32_t layout, const void* cache_desc, void* updated, int32_t nodes, const int32_t* starts_host,
-                    const int32_t* starts_dev, const int32_t* kept_dev, const int32_t* kept_counts_dev,
-                    void* workspace, cudaStream_t s) {
+                    const int32_t* starts_dev, const int32_t* counts_host, const int32_t* counts_dev,
+                    const int32_t* kept_dev, const int32_t* kept_counts_dev, void* workspace, cudaStream_t s) {
   CacheView c;
   ol_status st = view_dense(layout, cache_desc, c);
   if (st != OL_OK) return st;
   if ((st = writable(c, updated)) != OL_OK) return st;
-  if (!starts_host || !starts_dev || !kept_dev || !kept_counts_dev) return OL_ERR_NULL;
+  if (!starts_host || !starts_dev || !kept_dev || !kept_counts_dev || !counts_host != !counts_dev) return OL_ERR_NULL;
   if (nodes < 1) return OL_ERR_SHAPE;
-  if (!aligned16(starts_dev) || !aligned16(kept_dev) || !aligned16(kept_counts_dev) || !aligned16(workspace))
+  if (!aligned16(starts_dev) || !aligned16(counts_dev) || !aligned16(kept_dev) || !aligned16(kept_counts_dev) ||
+      !aligned16(workspace))
     return OL_ERR_ALIGN;
-  for (int b = 0; b < c.batch; ++b)
-    if (starts_host[b] < 0 || (long long)starts_host[b] + nodes > c.capacity) return OL_ERR_CAPACITY;
+  for (int b = 0; b < c.batch; ++b) {
+    const int n = counts_host ? counts_host[b] : nodes;
+    if (n < 0 || n > nodes) return OL_ERR_SHAPE;
+    if (starts_host[b] < 0 || (long long)starts_host[b] + n > c.capacity) return OL_ERR_CAPACITY;
+  }
   if ((st = no_overlap(c, starts_dev, sizeof(int32_t) * (size_t)c.batch)) != OL_OK ||
+      (counts_dev && (st = no_overlap(c, counts_dev, sizeof(int32_t) * (size_t)c.batch)) != OL_OK) ||
       (st = no_overlap(c, kept_dev, sizeof(int32_t) * (size_t)c.batch * nodes)) != OL_OK ||
       (st = no_overlap(c, kept_counts_dev, sizeof(int32_t) * (size_t)c.batch)) != OL_OK ||
       (st = no_overlap(c, workspace, kStatusBytes)) != OL_OK ||
       (st = table_overlap(layout, cache_desc, c)) != OL_OK)
     return st;
   if (layout == OL_LAYOUT_PAGED &&
-      (st = check_written_pages(static_cast<const ol_paged_kv*>(cache_desc), starts_host, nullptr, nodes)) != OL_OK)
+      (st = check_written_pages(static_cast<const ol_paged_kv*>(cache_desc), starts_host, counts_host, nodes)) != OL_OK)
     return st;
   if ((st = check_owner(c.ranges, c.nranges, c.owner)) != OL_OK) return st;
   ol_stats stats = {};  // what moves is known on the device only: the call alone is counted
@@ -457,6 +462,7 @@ ol_status tree_keep(int32_t layout, const void* cache_desc, void* updated, int32
   p.starts = starts_dev;
   p.kept = kept_dev;
   p.counts = kept_counts_dev;
+  p.drafted = counts_dev;
   p.status = static_cast<int32_t*>(workspace);
   return launch_tree_keep(p, s) == cudaSuccess ? OL_OK : OL_ERR_CUDA;
 }
@@ -537,8 +543,18 @@ ol_status ol_tree_keep(int32_t layout, const void* cache_desc, void* updated, in
                        const int32_t* starts_host, const int32_t* starts_dev, const int32_t* kept_dev,
                        const int32_t* kept_counts_dev, void* workspace, ol_stream stream) {
   return guarded_call([&] {
-    return tree_keep(layout, cache_desc, updated, nodes, starts_host, starts_dev, kept_dev, kept_counts_dev,
-                     workspace, static_cast<cudaStream_t>(stream));
+    return tree_keep(layout, cache_desc, updated, nodes, starts_host, starts_dev, nullptr, nullptr, kept_dev,
+                     kept_counts_dev, workspace, static_cast<cudaStream_t>(stream));
+  });
+}
+
+ol_status ol_tree_keep_counted(int32_t layout, const void* cache_desc, void* updated, int32_t nodes,
+                               const int32_t* starts_host, const int32_t* starts_dev, const int32_t* counts_host,
+                               const int32_t* counts_dev, const int32_t* kept_dev, const int32_t* kept_counts_dev,
+                               void* workspace, ol_stream stream) {
+  return guarded_call([&] {
+    return tree_keep(layout, cache_desc, updated, nodes, starts_host, starts_dev, counts_host, counts_dev, kept_dev,
+                     kept_counts_dev, workspace, static_cast<cudaStream_t>(stream));
   });
 }
 

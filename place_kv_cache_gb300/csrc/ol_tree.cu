@@ -453,14 +453,14 @@ __global__ void __launch_bounds__(kKeepThreads) tree_keep_kernel(const __grid_co
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   pdl_wait();
   pdl_launch_dependents();
-  const int start = p.starts[b], n = p.counts[b];
+  const int start = p.starts[b], n = p.counts[b], drafted = p.drafted ? p.drafted[b] : p.nodes;
   const int32_t* const kept = p.kept + (size_t)b * p.nodes;
   auto place = [&](int t) { return cache_row(c, plane, b, g, start + t); };
-  bool bad = n < 0 || n > p.nodes || start < 0 || (long long)start + p.nodes > c.capacity;
+  bool bad = n < 0 || n > drafted || drafted > p.nodes || start < 0 || (long long)start + drafted > c.capacity;
   if (!bad)
     for (int j = tid; j < n; j += blockDim.x * blockDim.y) {
       const int k = kept[j], last = j > 0 ? kept[j - 1] : -1;
-      if (k <= last || k >= p.nodes) {
+      if (k <= last || k >= drafted) {
         bad = true;
         break;
       }

@@ -391,3 +391,39 @@ def test_tree_keep_passes_and_refuses():
     assert keep(desc=paged(shared), layout=ol.OL_LAYOUT_PAGED) == ol.OL_ERR_PAGE
     outside = np.array([[8, 1, 2, 3], [4, 5, 6, 7]], np.int32)
     assert keep(desc=paged(outside), layout=ol.OL_LAYOUT_PAGED) == ol.OL_ERR_PAGE
+
+
+def keep_counted(counts, counts_dev=BASE + 94 * MB, desc=None, layout=ol.OL_LAYOUT_CONTIGUOUS, nodes=T, starts=(3, 60),
+                 updated=CACHE):
+    return status_of(ol.ol_tree_keep_counted, layout, contiguous() if desc is None else desc, updated, nodes,
+                     np.array(starts, np.int32), BASE + 91 * MB, counts, counts_dev, BASE + 92 * MB, BASE + 93 * MB,
+                     stream=0)
+
+
+def test_tree_keep_counted_checks_the_tokens_that_rows_drafted():
+    """A short row that ends at its capacity, or whose table names no page (or a shared one) past its tokens, passes."""
+    n = lambda *x: np.array(x, np.int32)  # noqa: E731
+    assert keep_counted(None, None) == ol.OL_ERR_INJECTED
+    assert keep_counted(n(4, 4)) == ol.OL_ERR_INJECTED
+    assert keep_counted(n(0, 0)) == ol.OL_ERR_INJECTED
+    assert keep_counted(n(4, 1), starts=(3, 63)) == ol.OL_ERR_INJECTED
+    assert keep_counted(n(4, 0), starts=(3, 64)) == ol.OL_ERR_INJECTED
+    assert keep_counted(n(4, 2), starts=(3, 63)) == ol.OL_ERR_CAPACITY
+    assert keep_counted(None, None, starts=(3, 63)) == ol.OL_ERR_CAPACITY
+    assert keep_counted(n(4, 1), starts=(3, -1)) == ol.OL_ERR_CAPACITY
+    assert keep_counted(n(5, 1)) == ol.OL_ERR_SHAPE
+    assert keep_counted(n(4, -1)) == ol.OL_ERR_SHAPE
+    assert keep_counted(n(4, 1), None) == ol.OL_ERR_NULL
+    assert keep_counted(None) == ol.OL_ERR_NULL
+    assert keep_counted(n(4, 1), CACHE) == ol.OL_ERR_ALIAS
+    assert keep_counted(n(4, 1), BASE + 94 * MB + 4) == ol.OL_ERR_ALIGN
+    assert keep_counted(n(4, 1), desc=contiguous(access=ol.OL_READ_ONLY)) == ol.OL_ERR_READONLY
+    assert keep_counted(n(4, 1), updated=BASE) == ol.OL_ERR_ALIAS
+
+    def st(table, counts, starts=(14, 30)):
+        return keep_counted(counts, desc=paged(np.array(table, np.int32)), layout=ol.OL_LAYOUT_PAGED, starts=starts)
+    missing, padded = [[0, -1, -1, -1], [4, 5, -1, -1]], [[1, 0, 0, 0], [4, 5, 0, 0]]
+    assert st(missing, n(2, 2)) == st(padded, n(2, 2)) == ol.OL_ERR_INJECTED
+    assert st(missing, n(3, 2)) == ol.OL_ERR_PAGE
+    assert st(padded, n(3, 3)) == ol.OL_ERR_PAGE                       # page 0 for two rows
+    assert st([[0, 1, 2, 3], [4, 0, 6, 7]], n(2, 2)) == ol.OL_ERR_PAGE

@@ -589,6 +589,54 @@ def test_tree_keep_leaves_a_row_whose_list_is_wrong(kept, count):
     assert torch.equal(t.cache, before)
 
 
+@pytest.mark.parametrize("dt,layout,page", [("bf16", "contiguous", 0), ("bf16", "paged", 16), ("f32", "paged", 8)])
+def test_ragged_trees_at_the_end_of_their_cache(dt, layout, page):
+    """Rows that drafted 0 to 6 of 6 nodes, two of them at the end of their cache, tables without pages past a row's
+    tokens: appended, attended and kept."""
+    B, Hq, H, D, T, C = 4, 8, 2, 64, 6, 48
+    t = Tree(dt, layout, B, Hq, H, D, page, T, [C, C, 17, 16], [4, 6, 1, 0], spare=0, seed=61)
+    start = t.lens - t.counts
+    if page:
+        for b in range(B):
+            t.table[b, -(-int(t.lens[b]) // page):] = -1
+        t.table_d.copy_(torch.from_numpy(t.table))
+        desc = ol.paged_kv(t.cache, t.table_d, t.table)
+    else:
+        desc = ol.kv_cache(t.cache)
+    start_d = torch.from_numpy(start).to(DEV)
+    qkv = torch.randn((B, T, Hq + 2 * H, D), generator=t.gen, device=DEV, dtype=t.dtype).transpose(1, 2)
+    q, k, v = qkv.split((Hq, H, H), dim=1)
+    ol.ol_rope_append(t.code, desc, t.cache, ol.rope(D, device=DEV), T, k, v, Hq, q, t.q, start, start_d, t.counts,
+                      t.counts_d, t.at_d)
+    t.call()
+    t.check()
+    lists = np.full((B, T), 77, np.int32)
+    lists[0, :2], lists[1, :3], lists[2, :1] = [1, 3], [0, 2, 5], [0]
+    kept = torch.tensor([2, 3, 1, 0], dtype=torch.int32, device=DEV)
+    lists_d = torch.from_numpy(lists).to(DEV)
+    want = [[t.row(p, b, int(t.lens[b])).clone() for b in range(B)] for p in (0, 1)]
+    before = t.cache.clone()
+    ol.ol_tree_keep_counted(t.code, desc, t.cache, T, start, start_d, t.counts, t.counts_d, lists_d, kept, t.ws)
+    for p in (0, 1):
+        for b in range(B):
+            n = int(kept[b])
+            want[p][b][:, start[b]: start[b] + n] = want[p][b][:, start[b] + lists[b, :n]].clone()
+            assert torch.equal(t.row(p, b, int(t.lens[b])), want[p][b])
+    bits = torch.int32 if dt == "f32" else torch.int16
+    changed = (t.cache.view(bits) != before.view(bits)).any(-1).sum()
+    assert int(changed) <= 2 * H * (2 + 2) and ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_OK
+    with pytest.raises(ol.OlError):  # without the counts: row 0 leaves its cache, or its table
+        ol.ol_tree_keep(t.code, desc, t.cache, T, start, start_d, lists_d, kept, t.ws)
+    # a list that names what the row did not draft, and a count on the device past `nodes`: the row stays
+    before = t.cache.clone()
+    lists_d[0, 1] = 4
+    t.counts_d[1] = T + 1
+    kept[2] = 2
+    ol.ol_tree_keep_counted(t.code, desc, t.cache, T, start, start_d, t.counts, t.counts_d, lists_d, kept, t.ws)
+    assert ol.ol_workspace_status(t.ws) == ol.OL_DEVICE_GUARD
+    assert torch.equal(t.cache.view(bits), before.view(bits))
+
+
 # --------------------------------------------------------------- all of it together
 
 @pytest.mark.parametrize("layout,page", [("contiguous", 0), ("paged", 16)])
