@@ -470,6 +470,10 @@ OL_API ol_status ol_hpaged_quantize(const ol_hpaged_kv* cache, void* updated, co
  * Two launches on `stream` (contiguous and paged: the append, then one
  * attention launch whose grid slice z serves query token z; INT4: the
  * attention, then the append); every check runs before the first.
+ * The workspace keeps ticket counters for every query token. A step of fewer
+ * query tokens per row (a decode step has one) leaves partial results where a
+ * longer step's counters lie: keep a workspace for each, or call
+ * ol_workspace_init before the longer step.
  */
 OL_API size_t ol_workspace_size_chunk(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
                                       int32_t new_len);
@@ -602,9 +606,10 @@ OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* up
  * prefix behind its window, has no influence on its output, whatever K and V hold
  * there: infinities and NaN reach the nodes that see them.
  * ws_bytes >= ol_workspace_size_tree(batch, q_heads, kv_heads, head_dim, nodes);
- * the workspace needs ol_workspace_init once and may be that of decode steps and
- * of chunked steps of up to `nodes` tokens of the same batch and kv heads (their
- * ticket counters stay as they are). Lengths, counts and the block table are
+ * the workspace needs ol_workspace_init once. It may be that of decode steps, or
+ * that of chunked steps of up to `nodes` tokens, of the same batch and kv heads:
+ * a tree call leaves their ticket counters as they are. (Those two do not share
+ * one: see ol_workspace_size_chunk.) Lengths, counts and the block table are
  * read on the device: a captured launch replays with the values it finds there
  * (up to the capacity); out-of-range ones are clamped and recorded as
  * OL_DEVICE_GUARD. Two launches. In the statistics attended_tokens counts every

@@ -119,7 +119,8 @@ constexpr size_t kTreeSplitBytes = 4 * kTreeMaxCtas * sizeof(TreeSplit);
 inline int tree_gen_rows(int group, int nodes) { return group * nodes <= 32 ? 32 : 64; }
 inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }
 // Notes and partial slots lie behind the ticket counters of decode steps and of
-// chunked steps of up to `nodes` tokens of this batch, which stay as they are.
+// chunked steps of up to `nodes` tokens of this batch, which stay as they are. (A
+// decode step's own partial slots lie over those of chunked steps.)
 inline size_t tree_splits_offset(int batch, int kv_heads, int nodes) {
   return partials_offset(batch, kv_heads, nodes);
 }

@@ -514,6 +514,47 @@ def test_tree_decode_and_chunk_share_a_workspace():
     t.check()
 
 
+@pytest.mark.parametrize("dt,nodes,chunk", [("bf16", 16, 16), ("f32", 16, 16), ("bf16", 40, 24)])
+def test_a_workspace_alternates_between_trees_and_steps(dt, nodes, chunk):
+    """Batches whose chunked steps' tickets reach past a decode step's: trees between chunked steps, then (zeroed once)
+    trees between decode steps; the tickets stay zero and every result is that of a workspace of its own."""
+    B, Hq, H, D = 16, 32, 8, 128
+    t = Tree(dt, "contiguous", B, Hq, H, D, 0, nodes, [400 + 131 * b for b in range(B)], out=dt)
+    size = max(t.ws_bytes, ol.ol_workspace_size_chunk(B, Hq, H, D, chunk))
+    tickets = 256 + 4 * chunk * B * H  # behind the status word
+    shared = torch.zeros(size, dtype=torch.uint8, device=DEV)
+    q = torch.randn((B, Hq, D), generator=t.gen, device=DEV, dtype=t.dtype)
+    qc = torch.randn((B, Hq, chunk, D), generator=t.gen, device=DEV, dtype=t.dtype)
+    kv = torch.stack([torch.stack([t.row(p, b, int(t.lens[b]))[:, -chunk:] for b in range(B)]) for p in (0, 1)]).contiguous()
+    desc = ol.kv_cache(t.cache)
+
+    def decode(ws):
+        out = torch.full_like(q, -77.0)
+        ol.ol_decode_attention(desc, q, Hq, t.lens, t.lens_d, 0.0, -1, out, CODE[t.dtype], ws, ws.numel())
+        return out
+
+    def chunked(ws):  # rewrites the last tokens with what they hold
+        out = torch.full_like(qc, -77.0)
+        ol.ol_chunk_step(t.code, desc, t.cache, qc, Hq, chunk, kv, t.lens, t.lens_d, 0.0, -1, out, CODE[t.dtype], ws,
+                         ws.numel())
+        return out
+
+    t.call()
+    tree = t.out.clone()
+    t.ws, t.ws_bytes = shared, size
+    for step in (chunked, decode):
+        want = step(torch.zeros_like(shared))
+        shared.zero_()
+        for _ in range(3):
+            t.out.fill_(-77.0)
+            t.call()
+            assert torch.equal(t.out, tree)
+            if step is chunked:
+                assert not bool(shared[:tickets].any())
+            assert torch.equal(step(shared), want)
+    assert ol.ol_workspace_status(shared) == ol.OL_DEVICE_OK
+
+
 def test_device_lengths_and_pages_that_disagree_are_recorded():
     t = Tree("bf16", "paged", 2, 8, 2, 128, 16, 4, [100, 50], [4, 4])
     t.lens_d.copy_(torch.tensor([100000, -5], dtype=torch.int32))  # clamped to the capacity, and to nothing
