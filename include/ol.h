@@ -664,7 +664,7 @@ OL_API ol_status ol_tree_keep_counted(int32_t layout, const void* cache_desc, vo
  * sections Opt-in storage auditing through runtime events and Optional
  * heterogeneous paged KV: the storage_* reports and the direct call's
  * copied / dequantized byte counts). The library records them, on the
- * calling host thread, for every append, attention or decode-step call that
+ * calling host thread, for every append, attention, decode-step or rotation call that
  * passes validation (also when the launch then fails: the counts describe the
  * work the call requested). They are host arithmetic on the call's sizes; no
  * device work is added.

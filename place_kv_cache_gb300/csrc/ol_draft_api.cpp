@@ -236,6 +236,9 @@ ol_status rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch, int32_t h
   if (overlaps(ro, range_of(positions_dev, sizeof(int32_t) * (size_t)batch * (per_token ? tokens : 1))) ||
       overlaps(ro, range_of(rope->turns, sizeof(uint64_t) * (size_t)(rope->rot_dim / 2))))
     return OL_ERR_ALIAS;
+  ol_stats stats = {};  // no cache takes part: the call alone is counted
+  stats.calls = 1;
+  record(stats);
   if (fault_injected()) return OL_ERR_INJECTED;
   if (d.empty()) return OL_OK;
   RopeParams p = rope_params(*rope, dtype, batch, tokens, head_dim);

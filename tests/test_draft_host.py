@@ -134,6 +134,19 @@ def test_rope_rows_passes_and_refuses():
     assert rows_call(batch=1 << 16, tokens=1 << 15, heads=1, src=ol.Rows(BASE, 0, 0, 0)) == ol.OL_ERR_UNSUPPORTED
 
 
+def test_rope_rows_is_a_recorded_call():
+    """As every call that passes its checks; one that does not leaves the record as it was."""
+    ol.ol_reset_stats()
+    assert append() == ol.OL_ERR_INJECTED
+    assert ol.ol_last_call_stats()["storage_append_copied_bytes"] > 0
+    assert rows_call() == ol.OL_ERR_INJECTED
+    last, total = ol.ol_last_call_stats(), ol.ol_total_stats()
+    assert last["calls"] == 1 and total["calls"] == 2
+    assert all(v == 0 for k, v in last.items() if k != "calls")
+    assert rows_call(heads=-1) == ol.OL_ERR_SHAPE
+    assert ol.ol_total_stats() == total and ol.ol_last_call_stats() == last
+
+
 # ------------------------------------------------------------------------- append
 
 CACHE = BASE + 100 * MB
