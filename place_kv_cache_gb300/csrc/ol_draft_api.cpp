@@ -448,6 +448,17 @@ ol_status tree_keep(int32_t layout, const void* cache_desc, void* updated, int32
       (st = no_overlap(c, workspace, kStatusBytes)) != OL_OK ||
       (st = table_overlap(layout, cache_desc, c)) != OL_OK)
     return st;
+  const Range status = range_of(workspace, workspace ? sizeof(int32_t) : 0);
+  for (const Range& r : {range_of(starts_dev, sizeof(int32_t) * (size_t)c.batch),
+                         range_of(counts_dev, counts_dev ? sizeof(int32_t) * (size_t)c.batch : 0),
+                         range_of(kept_dev, sizeof(int32_t) * (size_t)c.batch * nodes),
+                         range_of(kept_counts_dev, sizeof(int32_t) * (size_t)c.batch)})
+    if (overlaps(r, status)) return OL_ERR_ALIAS;
+  if (layout == OL_LAYOUT_PAGED) {
+    const ol_paged_kv* pk = static_cast<const ol_paged_kv*>(cache_desc);
+    if (overlaps(status, range_of(pk->block_table, sizeof(int32_t) * (size_t)pk->batch * pk->max_pages)))
+      return OL_ERR_ALIAS;
+  }
   if (layout == OL_LAYOUT_PAGED &&
       (st = check_written_pages(static_cast<const ol_paged_kv*>(cache_desc), starts_host, counts_host, nodes)) != OL_OK)
     return st;

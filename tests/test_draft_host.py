@@ -406,6 +406,15 @@ def test_tree_keep_passes_and_refuses():
     assert keep(desc=paged(outside), layout=ol.OL_LAYOUT_PAGED) == ol.OL_ERR_PAGE
 
 
+def test_tree_keep_refuses_a_status_word_over_what_it_reads():
+    """The kernel writes the status word while other CTAs read the lists."""
+    for at in (BASE + 91 * MB, BASE + 92 * MB, BASE + 93 * MB):  # starts, kept, counts
+        assert keep(ws=at) == ol.OL_ERR_ALIAS
+        assert keep(ws=at + 16) == (ol.OL_ERR_ALIAS if at == BASE + 92 * MB else ol.OL_ERR_INJECTED)  # 32 bytes and 8
+        assert keep(ws=at - 16) == keep(ws=at + 32) == ol.OL_ERR_INJECTED
+    assert keep(desc=paged(), layout=ol.OL_LAYOUT_PAGED, ws=BASE + 90 * MB) == ol.OL_ERR_ALIAS
+
+
 def keep_counted(counts, counts_dev=BASE + 94 * MB, desc=None, layout=ol.OL_LAYOUT_CONTIGUOUS, nodes=T, starts=(3, 60),
                  updated=CACHE):
     return status_of(ol.ol_tree_keep_counted, layout, contiguous() if desc is None else desc, updated, nodes,
