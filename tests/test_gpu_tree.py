@@ -239,8 +239,8 @@ def test_random_trees(seed):
     ("paged", 2, 8, 2, 64, 128, 6, [6, 150]),
 ], ids=lambda c: "-".join(map(str, c[:7])))
 def test_weights_of_the_tensor_core_kernel_keep_16_bits(case, out):
-    """V is multiplied by a weight's bf16 part and by the bf16 of its remainder, as in the decode and chunked steps:
-    each is off by at most 2^-8 of itself, together by 2^-16 of the weight."""
+    """V is multiplied by a weight's leading 8 bits and by the bf16 of its remainder, as in the decode and chunked steps:
+    of a weight in [1, 2) the remainder is below 2^-7, where bf16 numbers lie 2^-15 apart: off by at most 2^-16."""
     layout, B, Hq, H, D, page, nodes, lens = case
     t = Tree("bf16", layout, B, Hq, H, D, page, nodes, lens, out=out, seed=23)
     t.call()
@@ -319,6 +319,21 @@ def test_infinities_and_nan_of_the_prefix_behind_a_window(dt, layout, page, H, H
     assert touched >= 3
     t.call()
     t.check()
+
+
+@pytest.mark.parametrize("dt,nodes,D", [("bf16", 12, 128), ("bf16", 64, 128), ("bf16", 9, 64), ("f32", 12, 128)])
+def test_infinities_that_every_node_sees_stay_infinities(dt, nodes, D):
+    """V of prefix tokens with infinities of one sign in an element: infinite outputs of that sign, not NaN, whatever
+    the token's weight: the row's largest (a power of two), small ones, and equal ones."""
+    for q_scale in (1.0, 0.0):
+        t = Tree(dt, "contiguous", 2, 8, 2, D, 0, nodes, [nodes + 700, nodes + 40], seed=71)
+        t.q.mul_(q_scale)
+        for b in range(2):
+            for x in range(0, int(t.lens[b]) - nodes, 3):
+                t.token(1, b, x)[:, x % D] = float("inf") if x % D % 2 else -float("inf")
+        t.call()
+        t.check()
+        assert bool(torch.isinf(t.out).any()) and not bool(torch.isnan(t.out).any())
 
 
 def test_large_scores_and_equal_scores():
