@@ -490,9 +490,9 @@ OL_API ol_status ol_chunk_step(int32_t layout, const void* cache_desc, void* upd
  * their bits. OL_ROPE_HALF pairs element i with i + rot_dim / 2,
  * OL_ROPE_INTERLEAVED 2i with 2i + 1.
  *   turns     device [rot_dim / 2]: f_i / (2 pi), the turns per position, in
- *             units of 2^-64 turn (ol_rope_turns fills such a table). The angle
- *             is taken modulo a turn in 64-bit integers, so it loses nothing at
- *             far positions.
+ *             units of 2^-64 turn (ol_rope_turns fills such a table, to a few
+ *             2^-56 turn). The angle is taken modulo a turn in 64-bit integers, so
+ *             that a far position adds no error but its multiple of the table's.
  *   rot_dim   even, 2 .. head_dim
  *   magnitude factor of the rotated part, positive and finite (1: a pure rotation)
  */
@@ -615,6 +615,10 @@ OL_API ol_status ol_rope_append(int32_t layout, const void* cache_desc, void* up
  * OL_DEVICE_GUARD. Two launches. In the statistics attended_tokens counts every
  * drafted token as seen (the mask is on the device) and kv_payload_bytes_read
  * the tokens that some node may see, once.
+ * bf16 caches with head_dim 64 or 128, pages of a multiple of 16 tokens and fewer
+ * than 2^31 vectors in both planes run on the tensor cores; every other one on the
+ * CUDA cores, ten to twenty-five times slower a token where many rows make the
+ * products count.
  * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (other layouts, head_dim > 256, nodes > 512, 2^31 tiles of work at
  * full capacity), CUDA.

@@ -88,8 +88,8 @@ struct TreeParams {
 };
 // Few units of many segments are merged by units, 8 rows a CTA, while those CTAs
 // are one wave; else by shares. Measured (bf16, 8 kv heads, 4000 tokens; by units /
-// by shares): 2 rows of 64 (head, node) rows 17.1 / 18.0 us, 2 of 256 34.0 / 28.0
-// us, 4 of 64 25.5 / 22.9 us, 4 of 256 51.7 / 34.2 us.
+// by shares): 2 rows of 64 (head, node) rows 16.3 / 17.2 us, 2 of 256 34.7 / 28.4
+// us, 4 of 64 24.4 / 22.3 us, 4 of 256 54.5 / 36.2 us.
 inline bool tree_few_units(const TreeParams& p) {
   const int all = p.group * p.nodes, rows = all < p.rows_per_unit ? all : p.rows_per_unit;
   return (long long)p.batch * p.kv_heads * p.units_per_head * ((rows + 7) / 8) <= p.nctas;

@@ -34,12 +34,20 @@
 // Where there was such an element, the non-finite values of the tokens that a row
 // sees are added to its outputs at the end (rare, unhurried).
 //
-// Bounds: 4 * D bytes per token and kv head against 4 * D * rows flops. Up to 128
-// rows the memory (16 nodes over 64 rows of 8000 tokens, group 4: 311 us, 6.7
-// TB/s). With two query tiles the shared memory that feeds the products: a tile of
-// 128 tokens moves 192 KB for S (a stream's queries are read for each 64 tokens),
-// 128 KB for O and 64 KB in, 3070 cycles at 128 bytes a cycle; 3700 are measured (64
-// nodes over 64 rows of 4000: 241 us, 1113 TFLOP/s).
+// Bounds: 4 * D bytes per token and kv head against 4 * D * rows flops (of which
+// P V's are done twice). Up to 128 rows the memory (16 nodes over 64 rows of 8000
+// tokens, group 4: 307 us, 6.8 TB/s; 8192 tokens in pages of 16: 352 us, 6.1 TB/s).
+// With two query tiles the products: a tile of 128 tokens takes 32 of S, 49 cycles
+// each (the 6 KB that they read from shared memory; the tensor core's own time is
+// 32), and 32 of P V, 65 cycles each (the tensor core's), 3650 in all. Beside them
+// the shared memory moves 192 KB for S (a stream's queries are read for each 64
+// tokens), 128 KB of V and 64 KB in, 3070 cycles at 128 bytes a cycle. 4200 to 4900
+// cycles are measured (64 nodes over 64 rows of 4000: 286 us, 935 TFLOP/s; the
+// tensor pipe is busy 70 % of a launch of 27 tiles an SM), the rest are waits between a
+// step's scores, weights and sums. Under seconds of it the power limit takes the clock
+// to 1.7 GHz (315 us). With one product of P V it was 241 us: the price of the 16 bits.
+// (Figures of trials at other places of this file are from then: 64 nodes over 32 rows
+// 137 us, now 163; 256 over 8 rows 126, now 145.)
 #include "ol_tree.cuh"
 
 namespace ol {
@@ -965,8 +973,8 @@ void plan_fast_tree(TreeParams& p, int sms) {
   p.units_per_head = (p.group * p.nodes + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
-  // Measured (0 / 2 / 3 / 4 tiles): 64 nodes over 32 ragged rows (two query tiles) 160 / 142 / 139 / 140 us, 16 nodes
-  // over 64 ragged rows (one) 361 / 360 / 360 / 362 us.
+  // Measured (0 / 2 / 3 / 4 tiles): 64 nodes over 32 ragged rows (two query tiles) 182 / 161 / 162 / 162 us, 16 nodes
+  // over 64 ragged rows (one) 383 / 378 / 378 / 381 us.
   p.extra = p.rows_per_unit == 256 ? 3 : 2;
   p.by_unit = tree_few_units(p);
 }

@@ -11,7 +11,7 @@
 // dimensions at a time. K and V lie there as they are in the cache; the next tile
 // is copied in meanwhile. Bound for many rows by fp32 FMAs and the shared-memory
 // loads that feed them (4 * D flops per row and token against 2 * D elements a
-// token; fp32 trees of 16 over 64 rows of 4000 tokens 1750 us, 38 TFLOP/s), by
+// token; fp32 trees of 16 over 64 rows of 4000 tokens 1800 us, 37 TFLOP/s), by
 // latency for few (5 nodes, 6 rows, a window of 1000: 22 us). The loops over
 // dimensions and tokens hold no branch: one in the sums, past the head's end,
 // kept their loads from running ahead (2170 us and 26 us).
@@ -440,7 +440,9 @@ cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
 // Thread (x, y) has piece x of every step-th token: no division in the loops.
 // Bound by a chain of latencies (count, list, table, vectors) for small trees, of
 // which small CTAs start more at once: 16 nodes over 64 paged rows 3.2 us, 4.8 with
-// CTAs of 256 threads; 64 fp32 nodes over 128 rows (67 MB) 16 us with either.
+// CTAs of 256 threads; 64 fp32 nodes over 128 rows (67 MB) 16 us with either: the
+// chain's latencies, 1.7 times over (2048 CTAs, 8 an SM by registers); with the
+// cache's tokens in L2 9 us.
 constexpr int kKeepThreads = 128;
 constexpr int kKeepUnroll = 4;
 constexpr int kKeepRows = 512;
