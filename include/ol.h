@@ -555,6 +555,43 @@ OL_API ol_status ol_rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch,
                               int32_t per_token, ol_stream stream);
 
 /*
+ * Norms of queries and keys for each head, and their rotation, in one pass and
+ * one launch. A vector x [head_dim] of a head becomes
+ *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset),
+ * w being q_weight or k_weight, and y's leading rot_dim elements are rotated as
+ * ol_rope_rows does: fp32 throughout, one rounding to the row's dtype.
+ *   q_weight, k_weight  device [head_dim] of the rows' dtype, shared by the heads
+ *                 (NULL: ones)
+ *   eps           positive and finite
+ *   weight_offset finite: 0, or 1 for weights that are stored as their difference from 1
+ * A NaN or an infinity in a vector reaches that vector's outputs alone. Squares are
+ * summed in fp32: elements above 1e18 overflow it and give 0.
+ */
+typedef struct ol_head_norm {
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  float weight_offset;
+} ol_head_norm;
+
+/*
+ * Views q, q_out [batch, q_heads, tokens, head_dim] and k, k_out [batch, kv_heads,
+ * tokens, head_dim], for example of a fused projection's output and of new K/V
+ * before an append. Either pair may be absent (both NULL with 0 heads). rope NULL
+ * (with positions_dev NULL): the norms alone. positions_dev and per_token as
+ * ol_rope_rows. q_out may equal q, and k_out k (same pointer and strides: in place),
+ * also where q and k interleave in one projection's output (OL_ERR_ALIAS where they
+ * share elements); any other q_out or k_out must not overlap the extent of another
+ * view of the call.
+ * Errors: NULL, SHAPE, DTYPE, ALIAS, ALIGN, UNSUPPORTED (head_dim > 1024, or
+ * batch * tokens >= 2^31), CUDA.
+ */
+OL_API ol_status ol_norm_rope_rows(const ol_rope* rope, const ol_head_norm* norm, int32_t dtype, int32_t batch,
+                                   int32_t tokens, int32_t head_dim, int32_t q_heads, const ol_rows* q,
+                                   const ol_rows* q_out, int32_t kv_heads, const ol_rows* k, const ol_rows* k_out,
+                                   const int32_t* positions_dev, int32_t per_token, ol_stream stream);
+
+/*
  * Append with rotary positions, one launch: for every row b, tokens
  * t = 0 .. counts[b] - 1 of k are rotated and, with the same tokens of v
  * unrotated, written at cache positions positions[b] + t (contiguous or paged
@@ -662,6 +699,100 @@ OL_API ol_status ol_tree_keep_counted(int32_t layout, const void* cache_desc, vo
                                       const int32_t* starts_host, const int32_t* starts_dev,
                                       const int32_t* counts_host, const int32_t* counts_dev, const int32_t* kept_dev,
                                       const int32_t* kept_counts_dev, void* workspace, ol_stream stream);
+
+/*
+ * E4M3 cache: K and V as 8-bit floats (4 exponent, 3 mantissa bits, largest value
+ * 448), with one fp32 scale for each block of `block` tokens of one kv head and
+ * plane: value = code * scale. Contiguous or paged:
+ *   codes   uint8 [2, batch, kv_heads, capacity, head_dim], or the pool
+ *           [2, num_pages, kv_heads, page_size, head_dim]; the alias pointer
+ *   scales  float [2, batch, kv_heads, ceil(capacity / block)], or
+ *           [2, num_pages, kv_heads, page_size / block]
+ *   block_table, block_table_host  as ol_paged_kv; both NULL: contiguous, and
+ *           num_pages, page_size, max_pages are 0 (for a pool capacity is 0)
+ *   block   16, 32, 64 or 128 tokens; a page is a multiple of it
+ * head_dim is a multiple of 16, up to 256. A scale is 0 (the block's values are
+ * all 0), finite and at least 2^-80, or NaN (every value of the block is NaN).
+ */
+typedef struct ol_fp8_kv {
+  uint8_t* codes;
+  float* scales;
+  const int32_t* block_table;
+  const int32_t* block_table_host;
+  int32_t batch, kv_heads, capacity, head_dim;
+  int32_t num_pages, page_size, max_pages;
+  int32_t block;
+  int32_t access;
+  uint64_t owner;
+} ol_fp8_kv;
+
+/*
+ * Append to an E4M3 cache, quantising on the way, in place, one launch: tokens
+ * t = 0 .. counts[b] - 1 of the views k and v (new_len tokens per row, kv_heads
+ * heads, dtype OL_BF16 or OL_F32) are written at positions positions[b] + t.
+ * Per block of tokens, head and plane, with a = the largest |x| of the call's
+ * tokens in the block:
+ *   - a block that the call begins takes scale s = a / 448 (at least 2^-80; 0
+ *     where a is 0);
+ *   - a block that holds earlier tokens keeps its scale s while a <= 448 s, else
+ *     takes s 2^k, k the least that fits, and the earlier codes become those of
+ *     c 2^-k: exact but for values below 2^-6 (of the new scale), so a block that
+ *     grows token by token does not drift. A scale of 0 is replaced as if the
+ *     block began.
+ *   - code = x / s, the fp32 quotient rounded to E4M3 (nearest, ties to even).
+ * An infinity or NaN makes its block's scale NaN, for as long as the block is not
+ * begun anew. Slots behind a row's tokens are not written; tokens past counts[b]
+ * are not read. counts, positions, the pages that are written (each by one row,
+ * through one entry) and what the kernel reads on the device: as ol_rope_append.
+ * Errors: NULL, ALIAS, READONLY, CAPACITY, SHAPE, DTYPE, BUSY, PAGE, ALIGN,
+ * UNSUPPORTED (head_dim no multiple of 16 or > 256), CUDA.
+ */
+OL_API ol_status ol_fp8kv_append(const ol_fp8_kv* kv, void* updated, int32_t dtype, int32_t new_len, const ol_rows* k,
+                                 const ol_rows* v, const int32_t* positions_host, const int32_t* positions_dev,
+                                 const int32_t* counts_host, const int32_t* counts_dev, ol_stream stream);
+
+/*
+ * Read an E4M3 cache back: for every row b, tokens starts[b] .. starts[b] +
+ * counts[b] - 1 (both counts NULL: `tokens` of them) into tokens 0 .. counts[b] - 1
+ * of the views k_out and v_out (`tokens` per row, kv_heads heads, dtype OL_BF16 or
+ * OL_F32): code * scale in fp32, rounded once. Either view may be NULL. Vectors
+ * past a row's count are not written. Starts, counts and the block table are read
+ * on the device; a token whose place is not in the cache is skipped.
+ * Errors: as ol_fp8kv_append, but for READONLY.
+ */
+OL_API ol_status ol_fp8kv_read(const ol_fp8_kv* kv, int32_t dtype, int32_t tokens, const ol_rows* k_out,
+                               const ol_rows* v_out, const int32_t* starts_host, const int32_t* starts_dev,
+                               const int32_t* counts_host, const int32_t* counts_dev, ol_stream stream);
+
+/*
+ * Attention over an E4M3 cache (read-only use of it): the last counts[b] of row
+ * b's lens[b] cached tokens are the positions of its queries (both counts NULL:
+ * new_len of them; 0 .. new_len, at most lens[b]). Query i, at position p =
+ * lens[b] - counts[b] + i, attends tokens [max(0, p - window), p] (window < 0: [0,
+ * p]), all of them as the cache holds them, its own among them. A decode step has
+ * new_len 1, after ol_fp8kv_append of its token.
+ * q and out [batch, q_heads, new_len, head_dim], q in dtype (OL_BF16 or OL_F32),
+ * out in out_dtype. scale <= 0 selects 1/sqrt(head_dim). Outputs past a row's count
+ * are not written. What a query does not see has no influence on its output,
+ * whatever codes and scales stand there.
+ * ws_bytes >= ol_workspace_size_fp8kv(batch, q_heads, kv_heads, head_dim, new_len);
+ * the workspace needs ol_workspace_init once and may be shared as that of
+ * ol_tree_attention with `nodes` = new_len. Lengths, counts and the block table are read
+ * on the device: a captured launch replays with the values it finds there (up to the
+ * capacity); out-of-range ones are clamped and recorded as OL_DEVICE_GUARD. Two
+ * launches. Bytes and tokens in the statistics are those of the tokens that some
+ * query may see.
+ * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
+ * UNSUPPORTED (head_dim no multiple of 16 or > 256, new_len > 512, 2^31 tiles of work
+ * at full capacity), CUDA.
+ */
+OL_API size_t ol_workspace_size_fp8kv(int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                      int32_t new_len);
+OL_API ol_status ol_fp8kv_attention(const ol_fp8_kv* kv, int32_t dtype, const void* q, int32_t q_heads,
+                                    int32_t new_len, const int32_t* lens_host, const int32_t* lens_dev,
+                                    const int32_t* counts_host, const int32_t* counts_dev, float scale,
+                                    int32_t window, void* out, int32_t out_dtype, void* workspace, size_t ws_bytes,
+                                    ol_stream stream);
 
 /*
  * Storage statistics of a call (page "Persistent input/output feedback",

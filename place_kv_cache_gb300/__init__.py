@@ -43,7 +43,8 @@ SYMBOLS = ("ol_status_string", "ol_version", "ol_workspace_size", "ol_workspace_
            "ol_workspace_size_chunk", "ol_chunk_step", "ol_hpaged_append", "ol_hpaged_decode_attention",
            "ol_hpaged_decode_step", "ol_hpaged_quantize", "ol_hpaged_chunk_step", "ol_rope_turns", "ol_rope_rows",
            "ol_rope_append", "ol_workspace_size_tree", "ol_tree_attention", "ol_tree_keep",
-           "ol_tree_keep_counted")
+           "ol_tree_keep_counted", "ol_norm_rope_rows", "ol_fp8kv_append", "ol_fp8kv_read", "ol_workspace_size_fp8kv",
+           "ol_fp8kv_attention")
 
 
 class Stats(ctypes.Structure):
@@ -117,6 +118,21 @@ class Rows(ctypes.Structure):
                 ("stride_token", ctypes.c_int64)]
 
 
+class HeadNorm(ctypes.Structure):
+    """ol_head_norm: weights of the norms of queries and keys, eps, what is added to the weights."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class Fp8KV(ctypes.Structure):
+    """ol_fp8_kv: E4M3 codes with a scale per block of tokens and head, contiguous or paged."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("block_table_host", ctypes.c_void_p), ("batch", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("access", ctypes.c_int32), ("owner", ctypes.c_uint64)]
+
+
 _lib = None
 
 
@@ -186,6 +202,11 @@ def load(build_if_missing: bool = True, variant: str = ""):
         "ol_tree_attention": (st, [i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, f32, i32, vp, i32, vp, sz, vp]),
         "ol_tree_keep": (st, [i32, vp, vp, i32, vp, vp, vp, vp, vp, vp]),
         "ol_tree_keep_counted": (st, [i32, vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp]),
+        "ol_norm_rope_rows": (st, [vp, vp, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, vp, i32, vp]),
+        "ol_fp8kv_append": (st, [vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "ol_fp8kv_read": (st, [vp, i32, i32, vp, vp, vp, vp, vp, vp, vp]),
+        "ol_workspace_size_fp8kv": (sz, [i32, i32, i32, i32, i32]),
+        "ol_fp8kv_attention": (st, [vp, i32, vp, i32, i32, vp, vp, vp, vp, f32, i32, vp, i32, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -395,6 +416,30 @@ def rope(rot_dim: int, *, style: int = OL_ROPE_HALF, base: float = 10000.0, scal
     r = Rope(_ptr(turns), rot_dim, style, magnitude)
     r._refs = (turns,)
     return r
+
+
+def head_norm(q_weight=None, k_weight=None, *, eps: float = 1e-6, weight_offset: float = 0.0) -> HeadNorm:
+    """Norms of queries and keys: weights [head_dim] on the device (None: ones), shared by the heads."""
+    n = HeadNorm(_ptr(q_weight), _ptr(k_weight), eps, weight_offset)
+    n._refs = (q_weight, k_weight)
+    return n
+
+
+def fp8_kv(codes, scales, block_table=None, block_table_host=None, *, block: int, access: int = OL_READ_WRITE,
+           owner: int = 0, dims=None) -> Fp8KV:
+    """Descriptor of an E4M3 cache: codes [2, B, Hkv, C, D] (8-bit floats or bytes) with scales [2, B, Hkv,
+    ceil(C / block)], or, with block tables, a pool [2, P, Hkv, S, D] with scales [2, P, Hkv, S / block]. ``dims`` are
+    the last four sizes of raw pointers' codes."""
+    n, H, S, D = codes.shape[1:] if dims is None else dims
+    bt_host = _host_i32(block_table_host)
+    if bt_host is None:
+        d = Fp8KV(_ptr(codes), _ptr(scales), None, None, n, H, S, D, 0, 0, 0, block, access, owner)
+    else:
+        B, M = bt_host.shape
+        d = Fp8KV(_ptr(codes), _ptr(scales), _ptr(block_table), _ptr(bt_host), B, H, 0, D, n, S, M, block, access,
+                  owner)
+    d._refs = (codes, scales, block_table, bt_host)  # the descriptor keeps the buffers it points to alive
+    return d
 
 
 # ------------------------------------------------------------------ calls
@@ -662,3 +707,46 @@ def ol_tree_keep_counted(layout: int, desc, updated, nodes: int, starts_host, st
     _check(load().ol_tree_keep_counted(layout, _ref(desc), _ptr(updated), nodes, _ptr(sh), _ptr(starts_dev), _ptr(ch),
                                        _ptr(counts_dev), _ptr(kept_dev), _ptr(kept_counts_dev), _ptr(workspace),
                                        _stream(stream)), "ol_tree_keep_counted")
+
+
+def ol_norm_rope_rows(rope: Optional[Rope], norm: HeadNorm, dtype: int, batch: int, tokens: int, head_dim: int,
+                      q_heads: int, q, q_out, kv_heads: int, k, k_out, positions_dev, per_token: bool, stream=None):
+    """Norms of q and k for each head and their rotation: views, or tensors [B, H, T, D] (None with 0 heads; out the
+    same as in: in place). rope None: the norms alone."""
+    q, q_out, k, k_out = _rows(q), _rows(q_out), _rows(k), _rows(k_out)
+    _check(load().ol_norm_rope_rows(_ref(rope), _ref(norm), dtype, batch, tokens, head_dim, q_heads, _ref(q),
+                                    _ref(q_out), kv_heads, _ref(k), _ref(k_out), _ptr(positions_dev), int(per_token),
+                                    _stream(stream)), "ol_norm_rope_rows")
+
+
+def ol_fp8kv_append(kv: Fp8KV, updated, dtype: int, new_len: int, k, v, positions_host, positions_dev,
+                    counts_host=None, counts_dev=None, stream=None):
+    """k and v (views, or tensors [B, Hkv, new_len, D]) quantised to E4M3 at positions[b]; counts: tokens per row."""
+    ph, ch = _host_i32(positions_host), _host_i32(counts_host)
+    k, v = _rows(k), _rows(v)
+    _check(load().ol_fp8kv_append(_ref(kv), _ptr(updated), dtype, new_len, _ref(k), _ref(v), _ptr(ph),
+                                  _ptr(positions_dev), _ptr(ch), _ptr(counts_dev), _stream(stream)), "ol_fp8kv_append")
+
+
+def ol_fp8kv_read(kv: Fp8KV, dtype: int, tokens: int, k_out, v_out, starts_host, starts_dev, counts_host=None,
+                  counts_dev=None, stream=None):
+    """Tokens starts[b] .. + counts[b] of every row into k_out and v_out (views, or tensors [B, Hkv, tokens, D])."""
+    sh, ch = _host_i32(starts_host), _host_i32(counts_host)
+    k_out, v_out = _rows(k_out), _rows(v_out)
+    _check(load().ol_fp8kv_read(_ref(kv), dtype, tokens, _ref(k_out), _ref(v_out), _ptr(sh), _ptr(starts_dev),
+                                _ptr(ch), _ptr(counts_dev), _stream(stream)), "ol_fp8kv_read")
+
+
+def ol_workspace_size_fp8kv(batch: int, q_heads: int, kv_heads: int, head_dim: int, new_len: int) -> int:
+    return load().ol_workspace_size_fp8kv(batch, q_heads, kv_heads, head_dim, new_len)
+
+
+def ol_fp8kv_attention(kv: Fp8KV, dtype: int, q, q_heads: int, new_len: int, lens_host, lens_dev, counts_host,
+                       counts_dev, scale: float, window: int, out, out_dtype: int, workspace, ws_bytes: int,
+                       stream=None):
+    """Attention over an E4M3 cache: q and out [B, Hq, new_len, D]; the last counts[b] cached tokens of a row are its
+    queries' positions (None: all rows have new_len)."""
+    lh, ch = _host_i32(lens_host), _host_i32(counts_host)
+    _check(load().ol_fp8kv_attention(_ref(kv), dtype, _ptr(q), q_heads, new_len, _ptr(lh), _ptr(lens_dev), _ptr(ch),
+                                     _ptr(counts_dev), scale, window, _ptr(out), out_dtype, _ptr(workspace), ws_bytes,
+                                     _stream(stream)), "ol_fp8kv_attention")

@@ -1,57 +1,16 @@
 // ol_draft_api.cpp -- the C ABI of the operators around drafted tokens (see
 // include/ol.h): rotary positions, the rotating append, attention of a tree
-// over a cache, the accepted path's move. Host-side validation and dispatch;
+// over a cache, the accepted path's move, and the norms of queries and keys
+// with their rotation. Host-side validation and dispatch;
 // as in ol_api.cpp every check runs before any launch.
 #include <algorithm>
 #include <cmath>
 #include <vector>
 
-#include "ol_draft.h"
+#include "ol_fp8.h"
 #include "ol_host.h"
 
 namespace ol {
-namespace {
-
-// Host memory exhausted (the page checks keep a table) ends a call with a
-// status, never with an exception through the C boundary.
-template <typename F>
-ol_status guarded_call(F&& f) {
-  try {
-    return f();
-  } catch (...) {
-    return OL_ERR_CUDA;
-  }
-}
-
-ol_status view_dense(int layout, const void* desc, CacheView& v) {
-  if (layout == OL_LAYOUT_CONTIGUOUS) return view_contiguous(static_cast<const ol_kv_cache*>(desc), v);
-  if (layout == OL_LAYOUT_PAGED) return view_paged(static_cast<const ol_paged_kv*>(desc), v);
-  return OL_ERR_UNSUPPORTED;
-}
-
-CacheRef cache_ref(int layout, const void* desc, const CacheView& v) {
-  CacheRef r = {};
-  r.batch = v.batch;
-  r.kv_heads = v.kv_heads;
-  r.capacity = v.capacity;
-  if (layout == OL_LAYOUT_PAGED) {
-    const ol_paged_kv* c = static_cast<const ol_paged_kv*>(desc);
-    r.base = c->data;
-    r.block_table = c->block_table;
-    r.num_pages = c->num_pages;
-    r.page_size = c->page_size;
-    r.max_pages = c->max_pages;
-  } else {
-    r.base = static_cast<const ol_kv_cache*>(desc)->data;
-  }
-  return r;
-}
-
-ol_status table_overlap(int layout, const void* desc, const CacheView& v) {
-  if (layout != OL_LAYOUT_PAGED) return OL_OK;
-  const ol_paged_kv* c = static_cast<const ol_paged_kv*>(desc);
-  return no_overlap(v, c->block_table, sizeof(int32_t) * (size_t)c->batch * c->max_pages);
-}
 
 // Whether one of a row's entries [first, end) is outside the pool: bit 31 of
 // x | (pages - 1 - x) is set for such an x. A function of its own, without an early
@@ -87,15 +46,10 @@ ol_status check_written_pages(const ol_paged_kv* c, const int32_t* first, const 
 
 // ------------------------------------------------------------- views of vectors
 
-struct Dims {
-  int64_t batch, heads, tokens, head_dim;
-  bool empty() const { return batch == 0 || heads == 0 || tokens == 0; }
-};
-
-constexpr int64_t kMaxStride = 1ll << 40;
+static constexpr int64_t kMaxStride = 1ll << 40;
 
 // Bytes from a view's first element to its last one's end (0: no element).
-unsigned __int128 rows_bytes(const ol_rows& r, const Dims& d, size_t es) {
+static unsigned __int128 rows_bytes(const ol_rows& r, const Dims& d, size_t es) {
   if (d.empty()) return 0;
   const unsigned __int128 last = (unsigned __int128)(d.batch - 1) * r.stride_batch +
                                  (unsigned __int128)(d.heads - 1) * r.stride_head +
@@ -181,16 +135,53 @@ bool rows_aligned(const ol_rows& r, const Dims& d, size_t es) {
          (d.heads == 1 || r.stride_head % ve == 0) && (d.tokens == 1 || r.stride_token % ve == 0);
 }
 
+namespace {
+
+ol_status view_dense(int layout, const void* desc, CacheView& v) {
+  if (layout == OL_LAYOUT_CONTIGUOUS) return view_contiguous(static_cast<const ol_kv_cache*>(desc), v);
+  if (layout == OL_LAYOUT_PAGED) return view_paged(static_cast<const ol_paged_kv*>(desc), v);
+  return OL_ERR_UNSUPPORTED;
+}
+
+CacheRef cache_ref(int layout, const void* desc, const CacheView& v) {
+  CacheRef r = {};
+  r.batch = v.batch;
+  r.kv_heads = v.kv_heads;
+  r.capacity = v.capacity;
+  if (layout == OL_LAYOUT_PAGED) {
+    const ol_paged_kv* c = static_cast<const ol_paged_kv*>(desc);
+    r.base = c->data;
+    r.block_table = c->block_table;
+    r.num_pages = c->num_pages;
+    r.page_size = c->page_size;
+    r.max_pages = c->max_pages;
+  } else {
+    r.base = static_cast<const ol_kv_cache*>(desc)->data;
+  }
+  return r;
+}
+
+ol_status table_overlap(int layout, const void* desc, const CacheView& v) {
+  if (layout != OL_LAYOUT_PAGED) return OL_OK;
+  const ol_paged_kv* c = static_cast<const ol_paged_kv*>(desc);
+  return no_overlap(v, c->block_table, sizeof(int32_t) * (size_t)c->batch * c->max_pages);
+}
+
 RopeView rope_view(const ol_rows* r) {
   return {static_cast<char*>(r->data), r->stride_batch, r->stride_head, r->stride_token};
 }
 
 constexpr int kRopeMaxDim = 1024;
 
-ol_status check_rope(const ol_rope* rope, int dtype, int64_t batch, int64_t tokens, int head_dim) {
-  if (!rope || !rope->turns) return OL_ERR_NULL;
+ol_status check_vectors(int dtype, int64_t batch, int64_t tokens, int head_dim) {
   if (!valid_dtype(dtype)) return OL_ERR_DTYPE;
   if (batch < 0 || tokens < 0 || head_dim <= 0) return OL_ERR_SHAPE;
+  return OL_OK;
+}
+ol_status check_rope(const ol_rope* rope, int dtype, int64_t batch, int64_t tokens, int head_dim) {
+  if (!rope || !rope->turns) return OL_ERR_NULL;
+  const ol_status st = check_vectors(dtype, batch, tokens, head_dim);
+  if (st != OL_OK) return st;
   if (rope->rot_dim < 2 || rope->rot_dim % 2 != 0 || rope->rot_dim > head_dim) return OL_ERR_SHAPE;
   if (rope->style != OL_ROPE_HALF && rope->style != OL_ROPE_INTERLEAVED) return OL_ERR_SHAPE;
   if (!(rope->magnitude > 0.f) || !std::isfinite(rope->magnitude)) return OL_ERR_SHAPE;
@@ -248,6 +239,89 @@ ol_status rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch, int32_t h
   (per_token ? p.angles : p.positions) = positions_dev;
   p.vec = rope_pieces(*rope, head_dim, es) && rows_aligned(*in, d, es) && rows_aligned(*out, d, es);
   return launch_rope(p, s) == cudaSuccess ? OL_OK : OL_ERR_CUDA;
+}
+
+// A view that is written meets another one of as many rows and tokens: extents that overlap are taken
+// only in place and where no element is shared (may_share wants the one of more heads
+// first, with vectors apart from one another).
+bool meets(const ol_rows& out, const Dims& d_out, Range r_out, bool in_place, const ol_rows& other, const Dims& d_other,
+           Range r_other, size_t es) {
+  if (!overlaps(r_out, r_other)) return false;
+  if (!in_place) return true;
+  if (d_out.heads >= d_other.heads) return may_share(out, d_out, other, d_other, es);
+  Range r;
+  return check_rows(&other, d_other, es, true, r) != OL_OK || may_share(other, d_other, out, d_out, es);
+}
+
+ol_status norm_rope_rows(const ol_rope* rope, const ol_head_norm* norm, int32_t dtype, int32_t batch, int32_t tokens,
+                         int32_t head_dim, int32_t q_heads, const ol_rows* q, const ol_rows* q_out, int32_t kv_heads,
+                         const ol_rows* k, const ol_rows* k_out, const int32_t* positions_dev, int32_t per_token,
+                         cudaStream_t s) {
+  if (!norm) return OL_ERR_NULL;
+  ol_status st = rope ? check_rope(rope, dtype, batch, tokens, head_dim) : check_vectors(dtype, batch, tokens, head_dim);
+  if (st != OL_OK) return st;
+  if (head_dim > kRopeMaxDim || (int64_t)batch * tokens >= (1ll << 31)) return OL_ERR_UNSUPPORTED;
+  if (!rope != !positions_dev || !q != !q_out || !k != !k_out || (!q && !k)) return OL_ERR_NULL;
+  if ((q ? q_heads <= 0 : q_heads != 0) || (k ? kv_heads <= 0 : kv_heads != 0)) return OL_ERR_SHAPE;
+  if (!(norm->eps > 0.f) || !std::isfinite(norm->eps) || !std::isfinite(norm->weight_offset)) return OL_ERR_SHAPE;
+  if (!aligned16(positions_dev) || !aligned16(norm->q_weight) || !aligned16(norm->k_weight)) return OL_ERR_ALIGN;
+  const size_t es = elt_bytes(dtype);
+  const Dims dims[2] = {{batch, q_heads, tokens, head_dim}, {batch, kv_heads, tokens, head_dim}};
+  const ol_rows* const in[2] = {q, k};
+  const ol_rows* const out[2] = {q_out, k_out};
+  Range ri[2] = {{0, 0}, {0, 0}}, ro[2] = {{0, 0}, {0, 0}};
+  bool same[2] = {false, false};
+  for (int i = 0; i < 2; ++i) {
+    if (!in[i]) continue;
+    if ((st = check_rows(in[i], dims[i], es, false, ri[i])) != OL_OK) return st;
+    if ((st = check_rows(out[i], dims[i], es, true, ro[i])) != OL_OK) return st;
+    same[i] = same_view(*in[i], *out[i]);
+  }
+  const Range small[] = {
+      range_of(positions_dev, positions_dev ? sizeof(int32_t) * (size_t)batch * (per_token ? tokens : 1) : 0),
+      range_of(rope ? rope->turns : nullptr, rope ? sizeof(uint64_t) * (size_t)(rope->rot_dim / 2) : 0),
+      range_of(norm->q_weight, norm->q_weight ? es * head_dim : 0),
+      range_of(norm->k_weight, norm->k_weight ? es * head_dim : 0)};
+  for (int i = 0; i < 2; ++i) {
+    for (const Range& r : small)
+      if (overlaps(r, ro[i])) return OL_ERR_ALIAS;
+    if (!same[i] && overlaps(ro[i], ri[i])) return OL_ERR_ALIAS;
+    const int o = 1 - i;
+    if (!in[0] || !in[1]) continue;
+    if (meets(*out[i], dims[i], ro[i], same[i], *in[o], dims[o], ri[o], es)) return OL_ERR_ALIAS;
+    if (meets(*out[i], dims[i], ro[i], same[i], *out[o], dims[o], ro[o], es)) return OL_ERR_ALIAS;
+  }
+  ol_stats stats = {};  // no cache takes part: the call alone is counted
+  stats.calls = 1;
+  record(stats);
+  if (fault_injected()) return OL_ERR_INJECTED;
+  if (batch == 0 || tokens == 0) return OL_OK;
+  NormRopeParams p = {};
+  if (rope) {
+    p.turns = rope->turns;
+    p.rot_dim = rope->rot_dim;
+    p.style = rope->style;
+    p.magnitude = rope->magnitude;
+    (per_token ? p.angles : p.positions) = positions_dev;
+  }
+  p.weight[0] = norm->q_weight;
+  p.weight[1] = norm->k_weight;
+  p.eps = norm->eps;
+  p.weight_offset = norm->weight_offset;
+  p.dtype = dtype;
+  p.head_dim = head_dim;
+  p.batch = batch;
+  p.tokens = tokens;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.vec = rope ? rope_pieces(*rope, head_dim, es) : head_dim % (int)(16 / es) == 0;
+  for (int i = 0; i < 2; ++i)
+    if (in[i]) {
+      p.in[i] = rope_view(in[i]);
+      p.out[i] = rope_view(out[i]);
+      p.vec = p.vec && rows_aligned(*in[i], dims[i], es) && rows_aligned(*out[i], dims[i], es);
+    }
+  return launch_norm_rope(p, s) == cudaSuccess ? OL_OK : OL_ERR_CUDA;
 }
 
 ol_status rope_append(int32_t layout, const void* cache_desc, void* updated, const ol_rope* rope, int32_t new_len,
@@ -523,6 +597,16 @@ ol_status ol_rope_rows(const ol_rope* rope, int32_t dtype, int32_t batch, int32_
   return guarded_call([&] {
     return rope_rows(rope, dtype, batch, heads, tokens, head_dim, in, out, positions_dev, per_token,
                      static_cast<cudaStream_t>(stream));
+  });
+}
+
+ol_status ol_norm_rope_rows(const ol_rope* rope, const ol_head_norm* norm, int32_t dtype, int32_t batch, int32_t tokens,
+                            int32_t head_dim, int32_t q_heads, const ol_rows* q, const ol_rows* q_out,
+                            int32_t kv_heads, const ol_rows* k, const ol_rows* k_out, const int32_t* positions_dev,
+                            int32_t per_token, ol_stream stream) {
+  return guarded_call([&] {
+    return norm_rope_rows(rope, norm, dtype, batch, tokens, head_dim, q_heads, q, q_out, kv_heads, k, k_out,
+                          positions_dev, per_token, static_cast<cudaStream_t>(stream));
   });
 }
 

@@ -1,0 +1,43 @@
+// ol_fp8.cuh -- device helpers of the E4M3 cache: places of tokens and of their
+// blocks' scales, conversions.
+#pragma once
+
+#include "ol_common.cuh"
+#include "ol_fp8.h"
+
+namespace ol {
+
+// Vector index (in head_dim codes) of token t in a plane, and the index of its
+// block's scale; false where the block table names no page of the pool.
+__device__ __forceinline__ bool fp8_place(const Fp8Cache& c, int plane, int b, int g, int t, long long& row,
+                                          long long& scale) {
+  if (!c.block_table) {
+    const long long head = ((long long)plane * c.batch + b) * c.kv_heads + g;
+    row = head * c.capacity + t;
+    scale = head * ((c.capacity + (1 << c.block_log2) - 1) >> c.block_log2) + (t >> c.block_log2);
+    return true;
+  }
+  const int at = t / c.page_size;
+  const int page = c.block_table[(size_t)b * c.max_pages + at];
+  if (page < 0 || page >= c.num_pages) return false;
+  const long long head = ((long long)plane * c.num_pages + page) * c.kv_heads + g;
+  const int slot = t - at * c.page_size;
+  row = head * c.page_size + slot;
+  scale = head * (c.page_size >> c.block_log2) + (slot >> c.block_log2);
+  return true;
+}
+
+// Two values as E4M3, lo in the lower byte: nearest, ties to even, beyond 448 saturated.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The values of two codes (exact), of the lower 16 bits.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+  return __half22float2(*reinterpret_cast<__half2*>(&r));
+}
+
+}  // namespace ol

@@ -47,4 +47,33 @@ void record(const ol_stats& s);
 // Stored payload bytes of one token of one kv head in one plane (K or V).
 int64_t token_payload(const CacheView& v);
 
+// ------------------------------------------- views of vectors, written pages (ol_draft_api.cpp)
+
+struct Dims {
+  int64_t batch, heads, tokens, head_dim;
+  bool empty() const { return batch == 0 || heads == 0 || tokens == 0; }
+};
+// A view's pointer, strides and extent; `out` also wants vectors that do not overlap one another.
+ol_status check_rows(const ol_rows* r, const Dims& d, size_t es, bool out, Range& range);
+bool same_view(const ol_rows& a, const ol_rows& b);
+// Whether a vector of `a`, a view that may be written, and one of `b` may share an element.
+bool may_share(const ol_rows& a, const Dims& da, const ol_rows& b, const Dims& db, size_t es);
+// Every vector of the view starts on a 16-byte boundary.
+bool rows_aligned(const ol_rows& r, const Dims& d, size_t es);
+// Whether one of a row's block-table entries [first, end) is outside the pool.
+bool pages_outside(const int32_t* row, int first, int end, int num_pages);
+// Pages that tokens [first[b], first[b] + n_b) of the rows are written to: in the pool, and none of them twice.
+ol_status check_written_pages(const ol_paged_kv* c, const int32_t* first, const int32_t* counts, int n);
+
+// Host memory exhausted (the page checks keep a table) ends a call with a
+// status, never with an exception through the C boundary.
+template <typename F>
+ol_status guarded_call(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return OL_ERR_CUDA;
+  }
+}
+
 }  // namespace ol
