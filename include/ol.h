@@ -773,8 +773,10 @@ OL_API ol_status ol_fp8kv_read(const ol_fp8_kv* kv, int32_t dtype, int32_t token
  * new_len 1, after ol_fp8kv_append of its token.
  * q and out [batch, q_heads, new_len, head_dim], q in dtype (OL_BF16 or OL_F32),
  * out in out_dtype. scale <= 0 selects 1/sqrt(head_dim). Outputs past a row's count
- * are not written. What a query does not see has no influence on its output,
- * whatever codes and scales stand there.
+ * are not written. What a query does not see has no influence on its output:
+ * scales may be NaN there, and behind a row's tokens and its window codes too. (Codes
+ * of NaN, 0x7f and 0xff, which ol_fp8kv_append never writes, may not stand among the
+ * tokens that some query of the row sees.)
  * ws_bytes >= ol_workspace_size_fp8kv(batch, q_heads, kv_heads, head_dim, new_len);
  * the workspace needs ol_workspace_init once and may be shared as that of
  * ol_tree_attention with `nodes` = new_len. Lengths, counts and the block table are read
@@ -782,6 +784,8 @@ OL_API ol_status ol_fp8kv_read(const ol_fp8_kv* kv, int32_t dtype, int32_t token
  * capacity); out-of-range ones are clamped and recorded as OL_DEVICE_GUARD. Two
  * launches. Bytes and tokens in the statistics are those of the tokens that some
  * query may see.
+ * bf16 queries with head_dim 64 or 128 (fewer than 2^31 vectors in both planes) run on
+ * the tensor cores, with the codes as they are; every other call on the CUDA cores.
  * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (head_dim no multiple of 16 or > 256, new_len > 512, 2^31 tiles of work
  * at full capacity), CUDA.

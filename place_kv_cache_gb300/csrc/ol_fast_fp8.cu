@@ -1,0 +1,892 @@
+// ol_fast_fp8.cu -- attention over an E4M3 cache on the 5th generation tensor
+// cores: bf16 queries, head_dim 64 or 128, contiguous cache or paged pool.
+//
+// A unit is NC = 8, 16 or 32 (head, query) columns c = head * new_len + query of one
+// row's kv head. Its tokens form tiles of 128; equal contiguous shares of all
+// units' tiles go to one CTA per SM (TreeWalk in ol_tree.cuh), whose two streams of
+// 128 threads take the tiles of a segment in turn. K and V go to the tensor cores as
+// they lie in the cache, with the tokens (for V the dimensions) as the products' 128
+// rows, so that the columns may be few and nothing is unpacked:
+//   S = K Q'    128 tokens x 2 NC x D.  Q' holds each q, times a power of two, in two
+//               E4M3 parts: the second is the first's remainder, times 16. The 8 bits
+//               of a bf16 number are both parts' 4, but for elements below 2^-17 of the
+//               vector's largest.
+//   y = (S0 + S1 / 16) s_k scale log2(e) + log2(s_v), with the token's block's scales
+//   P = 2^(y - m)   a thread per token; V's scale is in it
+//   O += V P'   D x 4 NC x 128 tokens.  P' holds P in four E4M3 parts, each times 16:
+//               16 bits, and steps of 2^-21 where m keeps the largest between 2^5 and
+//               2^8, so that the many small weights beside a large one are not lost.
+//   l += P / s_v    in fp32
+// The reference m of a column belongs to a stream: it is looked for (and O rescaled)
+// only when a token's y passes it by 2^3; O = sum of the parts' columns over 16^k.
+// The join of the streams and the segments' merge know states (m, l, o) as those of
+// the tree kernels.
+//
+// Warps: 0 producer (TMA, a lane per box of a tile), 1 MMA issue, 2 queries' parts and
+// the tiles' scales, 3 V's rows outside the row's tokens (zeros: P = 0 times a NaN code
+// must not be NaN) and the note for the merge, 4-7 and 8-11 the streams.
+#include "ol_fp8.cuh"
+#include "ol_tree.cuh"
+
+namespace ol {
+namespace {
+
+constexpr int kTile = 1 << kTreeFastTileLog2;
+constexpr int kThreads = 384;
+constexpr int kScales = 8;        // tiles whose scales are known ahead
+constexpr float kTop = 5.f;       // log2 of the largest P when a reference is set
+constexpr float kGrown = 8.f;     // and of what makes a stream look for a new one
+
+template <int D, int NC>
+struct Lay {
+  static constexpr int kTileBytes = kTile * D;
+  static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries
+  static constexpr int kPBytes = kTile * 4 * NC;        // four parts of P
+  static constexpr int kQ = 0;                          // two buffers
+  static constexpr int kP = kQ + 2 * kQBytes;           // one of each stream
+  static constexpr int kRing = kP + 2 * kPBytes;
+  static constexpr int kSmall = 8192;                   // what follows the ring
+  static constexpr int kSlots = (232448 - kSmall - kRing) / kTileBytes < 24 ? (232448 - kSmall - kRing) / kTileBytes : 24;
+  static constexpr int kK = kSlots / 2, kV = kSlots - kK;
+  static constexpr int kCols = kRing + kSlots * kTileBytes;   // float2 [2 buffers][NC]: q's inverse factor, query index
+  static constexpr int kTab = kCols + 2 * NC * 8;             // float2 [8 warps][NC]: that factor, minus the reference
+  static constexpr int kTops = kTab + 8 * NC * 8;             // float [8 warps][NC]: maxima
+  static constexpr int kSums = kTops + 8 * NC * 4;            // float [8 warps][NC]: factors, sums
+  static constexpr int kRho = kSums + 8 * NC * 4;             // float [2][NC]: the streams' references
+  static constexpr int kSc = kRho + 2 * NC * 4;               // float4 [kScales][8 blocks]
+  static constexpr int kFlag = kSc + kScales * 8 * 16;        // uint32 [2 streams][2]
+  static constexpr int kBars = kFlag + 16;
+  // k full, empty; v landed, full, empty; q full, empty [2]; scales full, empty; s full, free, P ready, taken, vote [2];
+  // join, drain
+  static constexpr int kNumBars = 2 * kK + 3 * kV + 4 + 2 * kScales + 10 + 2;
+  static constexpr int kMisc = kBars + kNumBars * 8;          // TMEM address, abort flag
+  static constexpr int kTotal = kMisc + 8;
+  static_assert(kTotal <= 232448 && kK >= 4, "shared memory of one CTA");
+  static_assert(kRing % 1024 == 0 && kP % 1024 == 0 && kQBytes % 512 == 0, "swizzled tiles");
+  static constexpr int kTmem = NC == 8 ? 128 : NC == 16 ? 256 : 512;  // columns: 2 streams of 2 NC (S) and 4 NC (O)
+};
+
+// ------------------------------------------------------------------ tcgen05
+
+enum : uint32_t { kSwizzle32 = 6, kSwizzle64 = 4, kSwizzle128 = 2 };
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo_bytes, uint32_t sbo_bytes, uint32_t swizzle) {
+  // start, leading and stride offsets in 16 bytes; version 1
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lbo_bytes >> 4) << 16 | (uint64_t)(sbo_bytes >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)swizzle << 61;
+}
+// f32 accumulator, E4M3 operands, M = 128
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool mn_major) {
+  return 1u << 4 | (mn_major ? 3u << 15 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
+}
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define OL_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+#define OL_R16(x, i) OL_R4(x, i), OL_R4(x, i + 4), OL_R4(x, i + 8), OL_R4(x, i + 12)
+#define OL_U4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
+#define OL_U16(x, i) OL_U4(x, i), OL_U4(x, i + 4), OL_U4(x, i + 8), OL_U4(x, i + 12)
+#define OL_W4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
+#define OL_W16(x, i) OL_W4(x, i), OL_W4(x, i + 4), OL_W4(x, i + 8), OL_W4(x, i + 12)
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : OL_R16(x, 0)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : OL_R4(x, 0) : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      OL_W16(x, 0)
+      : "memory");
+}
+// Waits for the loads; x are registers that a load fills (so that no use of them moves ahead of the wait).
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U16(x, 0)::"memory");
+}
+__device__ __forceinline__ void tmem_wait_ld4(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U4(x, 0)::"memory");
+}
+
+template <typename T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A wait that ends: after about two seconds, or once another warp has given up,
+// it returns false; the CTA then winds down with a device status.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      set_status(status, OL_DEVICE_GUARD);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
+}
+// The warp's arrival, after all its lanes' work.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+template <int D, int NC>
+struct Bars {
+  using L = Lay<D, NC>;
+  uint32_t at;
+  __device__ uint32_t k_full(int s) const { return at + 8 * s; }
+  __device__ uint32_t k_empty(int s) const { return at + 8 * (L::kK + s); }
+  // V's copies are there; its slot is full once warp 3 has set it to rights
+  __device__ uint32_t landed(int s) const { return at + 8 * (2 * L::kK + s); }
+  __device__ uint32_t v_full(int s) const { return at + 8 * (2 * L::kK + L::kV + s); }
+  __device__ uint32_t v_empty(int s) const { return at + 8 * (2 * L::kK + 2 * L::kV + s); }
+  __device__ uint32_t q_full(int i) const { return at + 8 * (2 * L::kK + 3 * L::kV + i); }
+  __device__ uint32_t q_empty(int i) const { return q_full(2 + i); }
+  __device__ uint32_t sc_full(int i) const { return q_full(4 + i); }
+  __device__ uint32_t sc_empty(int i) const { return q_full(4 + kScales + i); }
+  __device__ uint32_t s_full(int j) const { return q_full(4 + 2 * kScales + j); }
+  __device__ uint32_t s_free(int j) const { return s_full(2 + j); }    // S is in the stream's registers
+  __device__ uint32_t p_ready(int j) const { return s_full(4 + j); }
+  __device__ uint32_t p_taken(int j) const { return s_full(6 + j); }   // the products with P are done
+  __device__ uint32_t vote(int j) const { return s_full(8 + j); }
+  __device__ uint32_t join() const { return s_full(10); }
+  __device__ uint32_t drain() const { return s_full(11); }
+};
+
+// A place in a ring of N, and the parity of its lap.
+template <int N>
+struct Cursor {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// Lowest token of the row that any query sees, and the lowest that all see.
+__device__ __forceinline__ int row_low(const TreeParams& p, const TreeRow& r) {
+  return p.window < 0 || r.prefix <= p.window ? 0 : r.prefix - p.window;
+}
+__device__ __forceinline__ int all_low(const TreeParams& p, const TreeRow& r) {
+  return p.window < 0 || r.len - 1 <= p.window ? 0 : r.len - 1 - p.window;
+}
+
+// Largest value of a warp, as a signed integer's order (no NaN).
+__device__ __forceinline__ float warp_max(float x) {
+  const int b = __float_as_int(x), key = b ^ (b >> 31 & 0x7fffffff);
+  const int top = __reduce_max_sync(0xffffffffu, key);
+  return __int_as_float(top ^ (top >> 31 & 0x7fffffff));
+}
+
+template <int D, int NC, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
+                                                               const __grid_constant__ Fp8AttnParams fp, const int box) {
+  using L = Lay<D, NC>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const TreeParams& p = fp.t;
+  const Fp8Cache& fc = fp.cache;
+  const uint32_t sa = smem_u32(smem);
+  if (sa % 1024 != 0) {  // the swizzled tiles need it; the launch has no other shared memory
+    if (threadIdx.x == 0) set_status(p.status, OL_DEVICE_GUARD);
+    return;
+  }
+  const Bars<D, NC> bar{sa + L::kBars};
+  volatile uint32_t* const abort = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+
+  if (tid == 0) {
+    prefetch_tensormap(&map);
+    for (int s = 0; s < L::kK; ++s) {
+      mbar_init(bar.k_full(s), 1);
+      mbar_init(bar.k_empty(s), 1);
+    }
+    for (int s = 0; s < L::kV; ++s) {
+      mbar_init(bar.landed(s), 1);
+      mbar_init(bar.v_full(s), 1);
+      mbar_init(bar.v_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.q_full(i), 1);
+      mbar_init(bar.q_empty(i), 9);  // the products' and every stream warp's
+      mbar_init(bar.s_full(i), 1);
+      mbar_init(bar.s_free(i), 4);
+      mbar_init(bar.p_ready(i), 4);
+      mbar_init(bar.p_taken(i), 1);
+      mbar_init(bar.vote(i), 4);
+    }
+    for (int i = 0; i < kScales; ++i) {
+      mbar_init(bar.sc_full(i), 1);
+      mbar_init(bar.sc_empty(i), 4);
+    }
+    mbar_init(bar.join(), 8);
+    mbar_init(bar.drain(), 1);
+    fence_mbar_init();
+    *abort = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa + L::kMisc), "n"(L::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc);
+  pdl_wait();
+  pdl_launch_dependents();
+
+  TreeWalk w(p);
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    const uint64_t policy = p.units_per_head > 1 ? policy_evict_normal() : policy_evict_first();
+    // One tile ahead: its boxes and this lane's page are known (the table's entry
+    // on its way) before the ring has room for it. Lane = box.
+    struct Tile {
+      int first, last;  // boxes
+      int y;            // cache row of this lane's box in plane K
+    } cur = {}, nxt = {};
+    const int v_rows = (PAGED ? fc.num_pages * fc.page_size : fc.batch * fc.capacity) * fc.kv_heads;
+    int tile = w.tile1;  // none yet
+    auto fetch = [&](Tile& t) {
+      if (tile == w.tile1) {
+        if (!w.next(p)) return false;
+        tile = w.tile0;
+      }
+      const int t0 = w.row.start + tile++ * kTile;
+      t.first = max(row_low(p, w.row) - t0, 0) / box;
+      t.last = (min(w.row.len - t0, kTile) + box - 1) / box;
+      const int at = t0 + lane * box;
+      if (!PAGED) {
+        t.y = (w.b * fc.kv_heads + w.g) * fc.capacity + at;
+      } else if (lane >= t.first && lane < t.last) {
+        int page = fc.block_table[(size_t)w.b * fc.max_pages + at / fc.page_size];
+        if (page < 0 || page >= fc.num_pages) {
+          set_status(p.status, OL_DEVICE_GUARD);
+          page = 0;
+        }
+        t.y = (page * fc.kv_heads + w.g) * fc.page_size + at % fc.page_size;
+      }
+      return true;
+    };
+    Cursor<L::kK> k;
+    Cursor<L::kV> v;
+    bool ok = true;
+    auto load = [&](uint32_t to, int y, uint32_t empty, uint32_t there, uint32_t phase) {
+      if (!warp_wait(empty, phase ^ 1, abort, p.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(there, (uint32_t)(cur.last - cur.first) * box * D);
+      __syncwarp();
+      if (lane >= cur.first && lane < cur.last) tma_load_2d(to + lane * box * D, &map, 0, y, there, policy);
+      return true;
+    };
+    bool more = fetch(nxt);
+    while (ok && more) {
+      cur = nxt;
+      more = fetch(nxt);
+      ok = load(sa + L::kRing + k.slot * L::kTileBytes, cur.y, bar.k_empty(k.slot), bar.k_full(k.slot), k.phase);
+      if (ok) k.next();
+      ok = ok && load(sa + L::kRing + (L::kK + v.slot) * L::kTileBytes, cur.y + v_rows, bar.v_empty(v.slot),
+                      bar.landed(v.slot), v.phase);
+      if (ok) v.next();
+    }
+    if (!ok) {  // copies in flight end before the CTA does; a slot's last load: of this lap before the cursor, else of the one before
+      for (int i = 0; i < L::kK; ++i) mbar_wait_bounded(bar.k_full(i), i < k.slot ? k.phase : k.phase ^ 1);
+      for (int i = 0; i < L::kV; ++i) mbar_wait_bounded(bar.landed(i), i < v.slot ? v.phase : v.phase ^ 1);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA issue
+    // The whole warp walks and waits, so that what the products are given stays in
+    // uniform registers; one elected lane issues them.
+    constexpr uint32_t kDescS = mma_desc(2 * NC, false), kDescO = mma_desc(4 * NC, true);
+    constexpr uint32_t kRowSwizzle = D == 128 ? kSwizzle128 : kSwizzle64;  // rows of D bytes: K, V, Q'
+    constexpr uint32_t kPSwizzle = NC == 32 ? kSwizzle128 : NC == 16 ? kSwizzle64 : kSwizzle32;
+    const uint32_t tm = uniform(tmem), base = uniform(sa);
+    Cursor<L::kK> k;
+    Cursor<L::kV> v;
+    uint32_t seg = 0;
+    uint32_t sphase = 0, pphase = 0;  // of the streams, a bit each
+    bool ok = true;
+    auto scores = [&](int j, bool last) {  // S of stream j from the next tile of K
+      tmem_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes, 16, 8 * D, kRowSwizzle);
+        const uint64_t qd = smem_desc(base + L::kQ + (seg & 1) * L::kQBytes, 16, 8 * D, kRowSwizzle);
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) mma_fp8(tm + j * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, x > 0);
+        mma_commit(bar.s_full(j));
+        mma_commit(bar.k_empty(k.slot));
+        if (last) mma_commit(bar.q_empty(seg & 1));
+      }
+      __syncwarp();
+      k.next();
+    };
+    // (a stream's first S finds its buffer free: the phase before the first)
+    auto s_wait = [&](int j) {
+      if (!warp_wait(bar.s_free(j), sphase >> j & 1 ^ 1, abort, p.status)) return false;
+      sphase ^= 1u << j;
+      return warp_wait(bar.k_full(k.slot), k.phase, abort, p.status);
+    };
+    while (ok && w.next(p)) {
+      const int tiles = uniform(w.tile1 - w.tile0);
+      ok = warp_wait(bar.q_full(seg & 1), seg >> 1 & 1, abort, p.status);
+      for (int i = 0; ok && i < 2 && i < tiles; ++i)
+        if ((ok = s_wait(i))) scores(i, i + 1 == tiles);
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int j = i & 1;
+        bool issued = i + 2 >= tiles;
+        if (!issued && __all_sync(0xffffffffu, mbar_test(bar.s_free(j), sphase >> j & 1 ^ 1) &&
+                                                   mbar_test(bar.k_full(k.slot), k.phase))) {
+          sphase ^= 1u << j;
+          scores(j, i + 3 == tiles);
+          issued = true;
+        }
+        ok = warp_wait(bar.p_ready(j), pphase >> j & 1, abort, p.status) &&
+             warp_wait(bar.v_full(v.slot), v.phase, abort, p.status);
+        if (!ok) break;
+        pphase ^= 1u << j;
+        tmem_fence_after();
+        if (elect_one()) {
+          // V's second half of the 128 rows is its first again where D is 64
+          const uint64_t vd = smem_desc(base + L::kRing + (L::kK + v.slot) * L::kTileBytes, 0, 8 * D, kRowSwizzle);
+          const uint64_t pd = smem_desc(base + L::kP + j * L::kPBytes, 0, 8 * 4 * NC, kPSwizzle);
+#pragma unroll
+          for (int x = 0; x < kTile / 32; ++x)
+            mma_fp8(tm + 4 * NC + j * 4 * NC, vd + x * (32 * D / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 1 || x > 0);
+          mma_commit(bar.p_taken(j));
+          mma_commit(bar.v_empty(v.slot));
+        }
+        __syncwarp();
+        v.next();
+        if (!issued && (ok = s_wait(j))) scores(j, i + 3 == tiles);
+      }
+      ++seg;
+    }
+    if (!ok) {  // products in flight end before TMEM is freed
+      if (elect_one()) mma_commit(bar.drain());
+      mbar_wait_bounded(bar.drain(), 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------- queries' parts, tiles' scales
+    // Lane = (plane, block of the tile). Table entries are on their way two tiles
+    // ahead, scales one.
+    struct Ahead {
+      int t0;             // first token
+      int b, g, qg;
+      bool first;         // of its segment
+      bool there;         // this lane's block holds tokens that some query sees
+      int page;
+      float scale;
+    } a0 = {}, a1 = {}, a2 = {};
+    const int plane = lane >> 3, block = lane & 7, blocks = kTile >> fc.block_log2;
+    int tile = w.tile1;
+    auto fetch_page = [&](Ahead& a) {
+      a.first = tile == w.tile1;
+      if (a.first) {
+        if (!w.next(p)) return false;
+        tile = w.tile0;
+      }
+      a.t0 = w.row.start + tile++ * kTile;
+      a.b = w.b;
+      a.g = w.g;
+      a.qg = w.qg;
+      const int t = a.t0 + (block << fc.block_log2);
+      a.there = plane < 2 && block < blocks && t < w.row.len && t + (1 << fc.block_log2) > row_low(p, w.row);
+      if (PAGED && a.there) a.page = fc.block_table[(size_t)w.b * fc.max_pages + t / fc.page_size];
+      return true;
+    };
+    auto fetch_scale = [&](Ahead& a) {
+      a.scale = 0.f;
+      if (!a.there) return;
+      const int t = a.t0 + (block << fc.block_log2);
+      long long at;
+      if (!PAGED) {
+        at = (((long long)plane * fc.batch + a.b) * fc.kv_heads + a.g) *
+                 ((fc.capacity + (1 << fc.block_log2) - 1) >> fc.block_log2) + (t >> fc.block_log2);
+      } else {
+        const int page = a.page < 0 || a.page >= fc.num_pages ? 0 : a.page;  // (the producer records it)
+        at = (((long long)plane * fc.num_pages + page) * fc.kv_heads + a.g) * (fc.page_size >> fc.block_log2) +
+             (t % fc.page_size >> fc.block_log2);
+      }
+      a.scale = fc.scales[at];
+    };
+    Cursor<kScales> sc;
+    uint32_t seg = 0;
+    bool ok = true;
+    bool more2 = fetch_page(a2), more1 = false;
+    if (more2) fetch_scale(a2);
+    bool more0 = more2;
+    a0 = a2;
+    more1 = more0 && fetch_page(a1);
+    while (ok && more0) {
+      more2 = more1 && fetch_page(a2);
+      if (more1) fetch_scale(a1);
+      if (a0.first) {
+        // Q': rows [part][column] of D bytes, swizzled
+        const int buf = seg & 1;
+        if (!(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
+        ++seg;
+        constexpr int E = D / 32;  // elements of a lane
+        const int R = p.group * p.nodes, r0 = a0.qg * NC;
+        const uint16_t* const q = reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, a0.b, a0.g, r0) * D + lane * E;
+        uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
+        float2* const cols = reinterpret_cast<float2*>(smem + L::kCols) + buf * NC;
+#pragma unroll 1
+        for (int c0 = 0; c0 < NC; c0 += 8) {
+          uint32_t x[8][E / 2];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e)
+              x[c][e] = r0 + c0 + c < R ? reinterpret_cast<const uint32_t*>(q + (size_t)(c0 + c) * D)[e] : 0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) top = max(top, max(x[c][e] << 16 & 0x7fff0000u, x[c][e] & 0x7fff0000u));
+            top = __reduce_max_sync(0xffffffffu, top);
+            // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
+            const int up = min(7 - ((int)(top >> 23) - 127), 126);
+            const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
+            const bool finite = top < 0x7f800000u;
+            uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) {
+              const float u = __uint_as_float(x[c][e] << 16) * factor, z = __uint_as_float(x[c][e] & 0xffff0000u) * factor;
+              hi[e] = finite ? e4m3x2(u, z) : 0x7f7fu;
+              const float2 h = from_e4m3x2(hi[e]);
+              lo[e] = finite ? e4m3x2((u - h.x) * 16.f, (z - h.y) * 16.f) : 0;
+            }
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const int n = part * NC + c0 + c, chunk = lane * E / 16, sw = D == 128 ? n & 7 : n >> 1 & 3;
+              uint8_t* const at = to + n * D + ((chunk ^ sw) << 4) + lane * E % 16;
+              const uint32_t* const z = part ? lo : hi;
+              if (E == 4)
+                *reinterpret_cast<uint32_t*>(at) = z[0] | z[E / 2 - 1] << 16;
+              else
+                *reinterpret_cast<uint16_t*>(at) = (uint16_t)z[0];
+            }
+            if (lane == 0)
+              cols[c0 + c] = make_float2(1.f / factor, __int_as_float((r0 + c0 + c) % p.nodes));
+          }
+        }
+        fence_proxy_async_smem();
+        warp_arrive(bar.q_full(buf));
+      }
+      if (!(ok = warp_wait(bar.sc_empty(sc.slot), sc.phase ^ 1, abort, p.status))) break;
+      float* const e = reinterpret_cast<float*>(smem + L::kSc) + (sc.slot * 8 + block) * 4;
+      if (plane == 0) e[0] = a0.scale * p.scale_log2;
+      if (plane == 1) {
+        // no scale: values of 0, whatever the weight; one that is far below all others
+        const float s = a0.scale == 0.f ? kFp8LeastScale : a0.scale;
+        e[1] = log2f(s);
+        e[2] = 1.f / s;
+      }
+      warp_arrive(bar.sc_full(sc.slot));
+      sc.next();
+      a0 = a1;
+      a1 = a2;
+      more0 = more1;
+      more1 = more2;
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------- V's edges, the merge's note
+    if (lane == 0) {
+      TreeWalk notes(w);
+      notes.write_splits(p);
+    }
+    __syncwarp();
+    Cursor<L::kV> v;
+    bool ok = true;
+    while (ok && w.next(p)) {
+      const int low = row_low(p, w.row);
+      for (int i = w.tile0; i < w.tile1; ++i) {
+        if (!(ok = warp_wait(bar.landed(v.slot), v.phase, abort, p.status))) break;
+        const int t0 = w.row.start + i * kTile;
+        const int r_low = low - t0, r_end = w.row.len - t0;
+        if (r_low > 0 || r_end < kTile) {
+          uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + (L::kK + v.slot) * L::kTileBytes);
+          for (int x = lane; x < kTile * D / 16; x += 32) {
+            const int r = x / (D / 16);
+            if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        warp_arrive(bar.v_full(v.slot));
+        v.next();
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- streams
+    const int j = (warp - 4) / 4, me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of O
+    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+    const uint32_t ts = tmem + j * 2 * NC + lanes, to = tmem + 4 * NC + lanes;  // O of stream 0; of stream 1 behind it
+    const float4* const tab = reinterpret_cast<const float4*>(smem + L::kTab) + me * (NC / 2);  // of two columns each
+    float2* const mine = reinterpret_cast<float2*>(smem + L::kTab) + me * NC + lane % NC;
+    float* const tops = reinterpret_cast<float*>(smem + L::kTops);
+    float* const sums = reinterpret_cast<float*>(smem + L::kSums);  // factors, and at the end l, of each warp
+    float* const rho = reinterpret_cast<float*>(smem + L::kRho);
+    volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag) + j * 2;
+    constexpr int kSwBits = NC == 32 ? 7 : NC == 16 ? 3 : 1, kSwShift = NC == 32 ? 0 : NC == 16 ? 1 : 2;
+    uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP + j * L::kPBytes) + row * (NC / 4);
+    const int p_sw = row >> kSwShift & kSwBits;  // the swizzle of this row's chunks
+    const int R = p.group * p.nodes;
+    Cursor<kScales> sc;
+    uint32_t count = 0;    // of this stream's tiles
+    uint32_t votes = 0, joins = 0, seg = 0;
+    bool ok = true;
+    auto vote = [&] {  // the stream's warps
+      warp_arrive(bar.vote(j));
+      return warp_wait(bar.vote(j), votes++ & 1, abort, p.status);
+    };
+    auto join = [&] {  // both streams'
+      warp_arrive(bar.join());
+      return warp_wait(bar.join(), joins++ & 1, abort, p.status);
+    };
+    while (ok && w.next(p)) {
+      const int tiles = w.tile1 - w.tile0, buf = seg & 1;
+      if (!(ok = warp_wait(bar.q_full(buf), seg >> 1 & 1, abort, p.status))) break;
+      ++seg;
+      const float2* const cols = reinterpret_cast<const float2*>(smem + L::kCols) + buf * NC;
+      if (lane < NC) *mine = make_float2(cols[lane].x, INFINITY);  // no reference
+      __syncwarp();
+      const int low_all = all_low(p, w.row);
+      float l[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
+      for (int i = 0; i < tiles; ++i, sc.next()) {
+        if ((i & 1) != j) continue;
+        const int t0 = w.row.start + (w.tile0 + i) * kTile;
+        if (!(ok = warp_wait(bar.sc_full(sc.slot), sc.phase, abort, p.status))) break;
+        // K's scale times the softmax's, log2 of V's, its inverse
+        const float4 e = reinterpret_cast<const float4*>(smem + L::kSc)[sc.slot * 8 + (row >> fc.block_log2)];
+        warp_arrive(bar.sc_empty(sc.slot));
+        if (!(ok = warp_wait(bar.s_full(j), count & 1, abort, p.status))) break;
+        ++count;
+        tmem_fence_after();
+        uint32_t hidden = 0;  // columns that do not see this thread's token
+        if (t0 + kTile - 1 > w.row.prefix || t0 < low_all) {
+          const int t = t0 + row;
+          for (int c = 0; c < NC; ++c) {
+            const int at = w.row.prefix + min(__float_as_int(cols[c].y), w.row.count - 1);
+            if (t > at || (p.window >= 0 && t < at - p.window)) hidden |= 1u << c;
+          }
+        }
+        const bool edge = __any_sync(0xffffffffu, hidden != 0);
+        float y[NC];
+        // Pass 0: exponents against the references as they are. Where one is outgrown, pass 1
+        // looks for the columns' maxima, and pass 2 has the new references.
+        for (int pass = 0; ok; ++pass) {
+          const bool raw = pass == 1;
+          bool over = false;
+          constexpr int kPart = NC < 16 ? NC : 16;  // columns at a time
+#pragma unroll
+          for (int c0 = 0; c0 < NC; c0 += kPart) {
+            uint32_t s[2 * kPart];
+            if (NC == 8) {
+              tmem_ld16(ts, s);
+              tmem_wait_ld16(s);
+            } else {
+              tmem_ld16(ts + c0, s);
+              tmem_ld16(ts + NC + c0, s + kPart);
+              tmem_wait_ld16(s);
+              tmem_wait_ld16(s + kPart);
+            }
+#pragma unroll
+            for (int c = 0; c < kPart; c += 2) {
+              const float4 f = tab[(c0 + c) / 2];
+              const float a = fmaf(__uint_as_float(s[kPart + c]), 0.0625f, __uint_as_float(s[c])) * e.x;
+              const float b = fmaf(__uint_as_float(s[kPart + c + 1]), 0.0625f, __uint_as_float(s[c + 1])) * e.x;
+              y[c0 + c] = fmaf(a, f.x, e.y + (raw ? 0.f : f.y));
+              y[c0 + c + 1] = fmaf(b, f.z, e.y + (raw ? 0.f : f.w));
+            }
+          }
+          if (edge)
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (hidden >> c & 1) y[c] = -INFINITY;
+          if (pass == 2) break;
+          if (pass == 0) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) over |= y[c] > kGrown;
+            // (the flag holds the number of the tile that raised it)
+            if (__any_sync(0xffffffffu, over) && lane == 0) flag[count & 1] = count;
+            ok = vote();
+            if (!ok || flag[count & 1] != count) break;
+            continue;
+          }
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            const float top = warp_max(fmaxf(y[c], -INFINITY));  // (a NaN is no maximum)
+            if (lane == 0) tops[me * NC + c] = top;
+          }
+          if (!(ok = vote())) break;
+          if (lane < NC) {
+            float top = tops[j * 4 * NC + lane];
+#pragma unroll
+            for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[(j * 4 + x) * NC + lane]);
+            const float old = mine->y, minus = fminf(old, kTop - top);  // the references only rise
+            mine->y = minus;
+            sums[me * NC + lane] = old == INFINITY ? 0.f : exp2f(minus - old);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int c = 0; c < NC; ++c) l[c] *= sums[me * NC + c];
+          if (i >= 2) {  // what the stream's earlier tiles of the segment have summed up
+            if (!(ok = warp_wait(bar.p_taken(j), count & 1, abort, p.status))) break;
+            tmem_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < 4 * NC; x += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + j * 4 * NC + x, o);
+              tmem_wait_ld16(o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) * sums[me * NC + (x + k) % NC]);
+              tmem_st16(to + j * 4 * NC + x, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        if (!ok) break;
+        tmem_fence_before();
+        warp_arrive(bar.s_free(j));
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          y[c] = fast_exp2(y[c]);
+          l[c] += edge && (hidden >> c & 1) ? 0.f : y[c] * e.z;  // (a hidden token's scale may be NaN)
+        }
+        uint32_t z[NC];  // the row of P': parts, columns in turn, a byte each
+#pragma unroll
+        for (int c = 0; c < NC; c += 4)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = e4m3x2(y[c], y[c + 1]), b = e4m3x2(y[c + 2], y[c + 3]);
+            z[(k * NC + c) / 4] = a | b << 16;
+            if (k == 3) break;
+            const float2 fa = from_e4m3x2(a), fb = from_e4m3x2(b);
+            y[c] = (y[c] - fa.x) * 16.f;
+            y[c + 1] = (y[c + 1] - fa.y) * 16.f;
+            y[c + 2] = (y[c + 2] - fb.x) * 16.f;
+            y[c + 3] = (y[c + 3] - fb.y) * 16.f;
+          }
+        if (!(ok = warp_wait(bar.p_taken(j), count & 1, abort, p.status))) break;  // the last P is read
+#pragma unroll
+        for (int x = 0; x < NC / 4; ++x) p_row[x ^ p_sw] = make_uint4(z[4 * x], z[4 * x + 1], z[4 * x + 2], z[4 * x + 3]);
+        fence_proxy_async_smem();
+        tmem_fence_before();
+        warp_arrive(bar.p_ready(j));
+      }
+      if (!ok) break;
+      if (tiles > j && !(ok = warp_wait(bar.p_taken(j), count + 1 & 1, abort, p.status))) break;
+
+      // The segment's state: l over the warp's lanes (a step halves the columns that a
+      // lane holds, then the lanes of a column are summed), and the references.
+#pragma unroll
+      for (int n = NC / 2, o = 16; n > 0; n /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int c = 0; c < n; ++c) {
+          const float give = up ? l[c] : l[c + n], keep = up ? l[c + n] : l[c];
+          l[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+#pragma unroll
+      for (int o = 16 / NC; o > 0; o /= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      // lane's column: its upper bits
+      if (lane % (32 / NC) == 0) sums[me * NC + lane / (32 / NC)] = l[0];
+      if (me % 4 == 0 && lane < NC) rho[j * NC + lane] = -mine->y;
+      tmem_fence_before();
+      if (!(ok = join())) break;
+      tmem_fence_after();
+
+      const bool whole = w.whole();
+      float* const slot = whole ? nullptr : tree_slot(p, w.slot);
+      const int r0 = w.qg * NC;
+      const size_t out = tree_out_row(p, w.b, w.g, r0) * D + row;
+      // each stream writes half of the columns, four at a time
+#pragma unroll 1
+      for (int c0 = j * (NC / 2); c0 < (j + 1) * (NC / 2); c0 += 4) {
+        uint32_t o[2][4][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (x < tiles) tmem_ld4(to + x * 4 * NC + k * NC + c0, o[x][k]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (x < tiles) tmem_wait_ld4(o[x][k]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = c0 + c, place = col;
+          const float ra = rho[col], rb = rho[NC + col], m = fmaxf(ra, rb), base = m == -INFINITY ? 0.f : m;
+          const float f[2] = {exp2f(ra - base), exp2f(rb - base)};
+          float total = 0.f, sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (x >= tiles) continue;
+            const float* const la = sums + x * 4 * NC + col;
+            total += (la[0] + la[NC] + la[2 * NC] + la[3 * NC]) * f[x];
+            const float v = fmaf(fmaf(fmaf(__uint_as_float(o[x][3][c]), 0.0625f, __uint_as_float(o[x][2][c])), 0.0625f,
+                                      __uint_as_float(o[x][1][c])), 0.0625f, __uint_as_float(o[x][0][c]));
+            sum += v * f[x];
+          }
+          if (r0 + col >= R) continue;
+          if (slot) {
+            if (row == 0) {
+              slot[place] = m;
+              slot[NC + place] = total;
+            }
+            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
+          } else if (row < D && __float_as_int(cols[col].y) < w.row.count) {
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            store_out(p.out, p.out_dtype, out + (size_t)col * D, sum * inv);
+          }
+        }
+      }
+      tmem_fence_before();
+      if (!(ok = join())) break;  // both streams have read both O before either's next product
+      warp_arrive(bar.q_empty(buf));
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(L::kTmem));
+  }
+}
+
+// ------------------------------------------------------------------------ host
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+uint64_t code_rows(const Fp8Cache& c) {
+  return c.block_table ? 2ull * c.num_pages * c.kv_heads * c.page_size : 2ull * c.batch * c.kv_heads * c.capacity;
+}
+
+// The codes as rows of D bytes; boxes of `box` rows, swizzled by the row's size.
+bool encode_codes(CUtensorMap* map, const Fp8Cache& c, int box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, code_rows(c)};
+  cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+  cuuint32_t boxes[2] = {(cuuint32_t)c.head_dim, (cuuint32_t)box};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NC, bool PAGED>
+cudaError_t launch_cfg(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
+  auto kern = fast_fp8_kernel<D, NC, PAGED>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t attr = once_per_device(done, [kern] {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NC>::kTotal);
+  });
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(kern, dim3(p.t.nctas), dim3(kThreads), Lay<D, NC>::kTotal, s, map, p, box);
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_cols(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
+  return p.t.rows_per_unit == 8    ? launch_cfg<D, 8, PAGED>(map, p, box, s)
+         : p.t.rows_per_unit == 16 ? launch_cfg<D, 16, PAGED>(map, p, box, s)
+                                   : launch_cfg<D, 32, PAGED>(map, p, box, s);
+}
+
+template <int D>
+cudaError_t launch_dim(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
+  return p.cache.block_table ? launch_cols<D, true>(map, p, box, s) : launch_cols<D, false>(map, p, box, s);
+}
+
+}  // namespace
+
+bool fast_fp8_supported(const Fp8AttnParams& p) {
+  if (p.t.dtype != OL_BF16 || (p.t.head_dim != 64 && p.t.head_dim != 128)) return false;
+  const uint64_t rows = code_rows(p.cache);
+  return rows > 0 && rows < (1ull << 31);  // TMA row coordinates are 32-bit
+}
+
+void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
+  TreeParams& p = fp.t;
+  const int columns = p.group * p.nodes;
+  p.rows_per_unit = columns <= 8 ? 8 : columns <= 16 ? 16 : 32;
+  p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
+  p.tile_log2 = kTreeFastTileLog2;
+  p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
+  p.extra = 2;
+  p.by_unit = tree_few_units(p);
+}
+
+cudaError_t launch_fast_fp8(const Fp8AttnParams& p, cudaStream_t s) {
+  // rows of a box: a tile of the contiguous cache, else the most that divides a page
+  int box = kTile;
+  if (p.cache.block_table)
+    while (p.cache.page_size % box != 0) box /= 2;  // (a page is a multiple of 16 tokens)
+  CUtensorMap map;
+  if (!encode_codes(&map, p.cache, box)) return cudaErrorInvalidValue;
+  return p.t.head_dim == 128 ? launch_dim<128>(map, p, box, s) : launch_dim<64>(map, p, box, s);
+}
+
+}  // namespace ol

@@ -472,8 +472,4 @@ cudaError_t launch_generic_fp8(const Fp8AttnParams& p, cudaStream_t s) {
   return p.t.dtype == OL_F32 ? launch_attention_type<float>(p, s) : launch_attention_type<uint16_t>(p, s);
 }
 
-bool fast_fp8_supported(const Fp8AttnParams&) { return false; }
-void plan_fast_fp8(Fp8AttnParams&, int) {}
-cudaError_t launch_fast_fp8(const Fp8AttnParams&, cudaStream_t) { return cudaErrorNotSupported; }
-
 }  // namespace ol
