@@ -22,9 +22,11 @@
 // The join of the streams and the segments' merge know states (m, l, o) as those of
 // the tree kernels.
 //
-// Warps: 0 producer (TMA, a lane per box of a tile), 1 MMA issue, 2 queries' parts and
-// the tiles' scales, 3 V's rows outside the row's tokens (zeros: P = 0 times a NaN code
-// must not be NaN) and the note for the merge, 4-7 and 8-11 the streams.
+// Warps: 0 the walk and the producer (TMA, a lane per box of a tile), 1 MMA issue, 2
+// queries' parts and the tiles' scales, 3 V's rows outside the row's tokens (zeros: P = 0
+// times a NaN code must not be NaN), 4-7 and 8-11 the streams. The others learn of the
+// segments from the first, through a ring: the walk in line in each of them, and the
+// loops of waits (wait_long), made the kernel outgrow the instruction cache.
 #include "ol_fp8.cuh"
 #include "ol_tree.cuh"
 
@@ -34,6 +36,7 @@ namespace {
 constexpr int kTile = 1 << kTreeFastTileLog2;
 constexpr int kThreads = 384;
 constexpr int kScales = 8;        // tiles whose scales are known ahead
+constexpr int kSegs = 8;          // segments known ahead
 constexpr float kTop = 5.f;       // log2 of the largest P when a reference is set
 constexpr float kGrown = 8.f;     // and of what makes a stream look for a new one
 
@@ -53,12 +56,13 @@ struct Lay {
   static constexpr int kTops = kTab + 8 * NC * 8;             // float [8 warps][NC]: maxima
   static constexpr int kSums = kTops + 8 * NC * 4;            // float [8 warps][NC]: factors, sums
   static constexpr int kRho = kSums + 8 * NC * 4;             // float [2][NC]: the streams' references
-  static constexpr int kSc = kRho + 2 * NC * 4;               // float4 [kScales][8 blocks]
-  static constexpr int kFlag = kSc + kScales * 8 * 16;        // uint32 [2 streams][2]
+  static constexpr int kSc = kRho + 2 * NC * 4;               // float [kScales][2 planes][8 blocks]
+  static constexpr int kSeg = kSc + kScales * 16 * 4;         // Seg [kSegs]
+  static constexpr int kFlag = kSeg + kSegs * 48;             // uint32 [2 streams][2]
   static constexpr int kBars = kFlag + 16;
   // k full, empty; v landed, full, empty; q full, empty [2]; scales full, empty; s full, free, P ready, taken, vote [2];
-  // join, drain
-  static constexpr int kNumBars = 2 * kK + 3 * kV + 4 + 2 * kScales + 10 + 2;
+  // join, drain; segments full, empty
+  static constexpr int kNumBars = 2 * kK + 3 * kV + 4 + 2 * kScales + 10 + 2 + 2 * kSegs;
   static constexpr int kMisc = kBars + kNumBars * 8;          // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 8;
   static_assert(kTotal <= 232448 && kK >= 4, "shared memory of one CTA");
@@ -97,7 +101,6 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 #define OL_U4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
 #define OL_U16(x, i) OL_U4(x, i), OL_U4(x, i + 4), OL_U4(x, i + 8), OL_U4(x, i + 12)
 #define OL_W4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
-#define OL_W16(x, i) OL_W4(x, i), OL_W4(x, i + 4), OL_W4(x, i + 8), OL_W4(x, i + 12)
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
@@ -108,12 +111,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
 __device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t* x) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : OL_R4(x, 0) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      OL_W16(x, 0)
-      : "memory");
+__device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), OL_W4(x, 0) : "memory");
 }
 // Waits for the loads; x are registers that a load fills (so that no use of them moves ahead of the wait).
 __device__ __forceinline__ void tmem_wait_ld16(uint32_t* x) {
@@ -145,22 +144,25 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // A wait that ends: after about two seconds, or once another warp has given up,
-// it returns false; the CTA then winds down with a device status.
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;
+// it returns false; the CTA then winds down with a device status. The loop is a
+// function of its own: in line at every wait it made the kernel's code outgrow the
+// instruction cache.
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t abort_at, int32_t* status) {
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
-    if (*abort) return false;
+    if (lds_u32(abort_at)) return false;
     if (clock64() - t0 > kWaitLimitCycles) {
-      *abort = 1;
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(abort_at), "r"(1) : "memory");
       set_status(status, OL_DEVICE_GUARD);
       return false;
     }
   }
   return true;
 }
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort, int32_t* status) {
-  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort, status));
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t abort_at, int32_t* status) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) ok = __all_sync(0xffffffffu, wait_long(bar, parity, abort_at, status));
+  return ok;
 }
 // The warp's arrival, after all its lanes' work.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
@@ -189,6 +191,8 @@ struct Bars {
   __device__ uint32_t vote(int j) const { return s_full(8 + j); }
   __device__ uint32_t join() const { return s_full(10); }
   __device__ uint32_t drain() const { return s_full(11); }
+  __device__ uint32_t seg_full(int i) const { return s_full(12 + i); }
+  __device__ uint32_t seg_empty(int i) const { return s_full(12 + kSegs + i); }
 };
 
 // A place in a ring of N, and the parity of its lap.
@@ -204,13 +208,19 @@ struct Cursor {
   }
 };
 
+// A segment as the roles see it: tiles [0, tiles) of 128 tokens from token t0 on, of
+// columns [unit's first, ..) of kv head g of row b.
+struct alignas(16) Seg {
+  int t0, tiles;             // tiles 0: the share's end
+  int b, g, qg;
+  int len, count, prefix;    // of the row
+  int slot;                  // of the partial results, or -1: the unit is whole
+  int pad[3];
+};
+
 // Lowest token of the row that any query sees, and the lowest that all see.
-__device__ __forceinline__ int row_low(const TreeParams& p, const TreeRow& r) {
-  return p.window < 0 || r.prefix <= p.window ? 0 : r.prefix - p.window;
-}
-__device__ __forceinline__ int all_low(const TreeParams& p, const TreeRow& r) {
-  return p.window < 0 || r.len - 1 <= p.window ? 0 : r.len - 1 - p.window;
-}
+__device__ __forceinline__ int row_low(int window, int prefix) { return window < 0 || prefix <= window ? 0 : prefix - window; }
+__device__ __forceinline__ int all_low(int window, int len) { return window < 0 || len - 1 <= window ? 0 : len - 1 - window; }
 
 // Largest value of a warp, as a signed integer's order (no NaN).
 __device__ __forceinline__ float warp_max(float x) {
@@ -232,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
     return;
   }
   const Bars<D, NC> bar{sa + L::kBars};
-  volatile uint32_t* const abort = reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4);
+  const uint32_t abort = sa + L::kMisc + 4;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
   if (tid == 0) {
@@ -256,13 +266,17 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       mbar_init(bar.vote(i), 4);
     }
     for (int i = 0; i < kScales; ++i) {
-      mbar_init(bar.sc_full(i), 1);
+      mbar_init(bar.sc_full(i), 32);  // a lane's copies
       mbar_init(bar.sc_empty(i), 4);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(bar.seg_full(i), 1);
+      mbar_init(bar.seg_empty(i), 11);  // all warps but the producer
     }
     mbar_init(bar.join(), 8);
     mbar_init(bar.drain(), 1);
     fence_mbar_init();
-    *abort = 0;
+    *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4) = 0;
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
   }
   if (warp == 1) {
@@ -277,43 +291,91 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
   pdl_wait();
   pdl_launch_dependents();
 
-  TreeWalk w(p);
+  // The next segment, for a whole warp; false: there is none, or the wait was given up.
+  Cursor<kSegs> segs;
+  auto next_seg = [&](Seg& g, bool& ok) {
+    ok = warp_wait(bar.seg_full(segs.slot), segs.phase, abort, p.status);
+    if (!ok) return false;
+    const int4* const from = reinterpret_cast<const int4*>(smem + L::kSeg + segs.slot * sizeof(Seg));
+    const int4 x = from[0], y = from[1], z = from[2];
+    warp_arrive(bar.seg_empty(segs.slot));
+    segs.next();
+    g = Seg{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w, z.x, {0, 0, 0}};
+    return g.tiles > 0;
+  };
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- producer
+    // ------------------------------------------------------- the walk, producer
+    TreeWalk w(p);
     const uint64_t policy = p.units_per_head > 1 ? policy_evict_normal() : policy_evict_first();
-    // One tile ahead: its boxes and this lane's page are known (the table's entry
-    // on its way) before the ring has room for it. Lane = box.
+    // Three tiles ahead: their boxes and this lane's page are known (the table's entries
+    // on their way) before the ring has room for them. Lane = box.
     struct Tile {
       int first, last;  // boxes
-      int y;            // cache row of this lane's box in plane K
-    } cur = {}, nxt = {};
+      int y;            // cache row of this lane's box in plane K, or in its page
+      int page;
+      bool more;        // there is such a tile
+    } ahead[3], cur;
     const int v_rows = (PAGED ? fc.num_pages * fc.page_size : fc.batch * fc.capacity) * fc.kv_heads;
-    int tile = w.tile1;  // none yet
+    const int step_pages = PAGED ? kTile / fc.page_size : 0, step_slots = PAGED ? kTile - step_pages * fc.page_size : 0;
+    bool ok = true;
+    int tile = 0, t0 = 0, entry = 0, slot = 0;  // of the next tile: its first token, this lane's entry in the table and slot in its page
+    TreeSplit note = {};
+    note.last = -1;
     auto fetch = [&](Tile& t) {
       if (tile == w.tile1) {
-        if (!w.next(p)) return false;
-        tile = w.tile0;
-      }
-      const int t0 = w.row.start + tile++ * kTile;
-      t.first = max(row_low(p, w.row) - t0, 0) / box;
-      t.last = (min(w.row.len - t0, kTile) + box - 1) / box;
-      const int at = t0 + lane * box;
-      if (!PAGED) {
-        t.y = (w.b * fc.kv_heads + w.g) * fc.capacity + at;
-      } else if (lane >= t.first && lane < t.last) {
-        int page = fc.block_table[(size_t)w.b * fc.max_pages + at / fc.page_size];
-        if (page < 0 || page >= fc.num_pages) {
-          set_status(p.status, OL_DEVICE_GUARD);
-          page = 0;
+        t.more = w.next(p);
+        // to the other roles
+        if (!(ok = warp_wait(bar.seg_empty(segs.slot), segs.phase ^ 1, abort, p.status))) {
+          t.more = false;
+          return;
         }
-        t.y = (page * fc.kv_heads + w.g) * fc.page_size + at % fc.page_size;
+        if (t.more) {
+          tile = w.tile0;
+          t0 = w.row.start + tile * kTile;
+          const int at = t0 + lane * box;
+          if (PAGED) {
+            entry = at / fc.page_size;
+            slot = at - entry * fc.page_size;
+          }
+        }
+        if (lane == 0) {
+          *reinterpret_cast<Seg*>(smem + L::kSeg + segs.slot * sizeof(Seg)) =
+              Seg{t0, t.more ? w.tile1 - w.tile0 : 0, w.b, w.g, w.qg, w.row.len, w.row.count, w.row.prefix,
+                  w.whole() ? -1 : w.slot, {0, 0, 0}};
+          if (t.more && w.tile0 == 0) {
+            note = w.note(p);
+            if (p.by_unit) p.splits[w.unit(p)] = note;
+          }
+          // (only the share's last unit can reach past its end)
+          if (!t.more && !p.by_unit) p.splits[blockIdx.x] = note;
+        }
+        warp_arrive(bar.seg_full(segs.slot));
+        segs.next();
+        if (!t.more) return;
       }
-      return true;
+      t.first = max(row_low(p.window, w.row.prefix) - t0, 0) / box;
+      t.last = (min(w.row.len - t0, kTile) + box - 1) / box;
+      if (PAGED) {
+        t.page = lane >= t.first && lane < t.last ? fc.block_table[(size_t)w.b * fc.max_pages + entry] : 0;
+        t.y = w.g * fc.page_size + slot;
+        entry += step_pages;
+        slot += step_slots;
+        if (slot >= fc.page_size) slot -= fc.page_size, ++entry;
+      } else {
+        t.y = (w.b * fc.kv_heads + w.g) * fc.capacity + t0 + lane * box;
+      }
+      ++tile;
+      t0 += kTile;
+    };
+    auto cache_row_of = [&](const Tile& t) {
+      if (!PAGED) return t.y;
+      const bool bad = t.page < 0 || t.page >= fc.num_pages;
+      if (bad) set_status(p.status, OL_DEVICE_GUARD);
+      return (bad ? 0 : t.page) * fc.kv_heads * fc.page_size + t.y;
     };
     Cursor<L::kK> k;
     Cursor<L::kV> v;
-    bool ok = true;
     auto load = [&](uint32_t to, int y, uint32_t empty, uint32_t there, uint32_t phase) {
       if (!warp_wait(empty, phase ^ 1, abort, p.status)) return false;
       if (lane == 0) mbar_arrive_expect_tx(there, (uint32_t)(cur.last - cur.first) * box * D);
@@ -321,13 +383,25 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       if (lane >= cur.first && lane < cur.last) tma_load_2d(to + lane * box * D, &map, 0, y, there, policy);
       return true;
     };
-    bool more = fetch(nxt);
-    while (ok && more) {
-      cur = nxt;
-      more = fetch(nxt);
-      ok = load(sa + L::kRing + k.slot * L::kTileBytes, cur.y, bar.k_empty(k.slot), bar.k_full(k.slot), k.phase);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      ahead[i].more = true;
+      if (i > 0) ahead[i].more = ahead[i - 1].more;
+      if (ahead[i].more) {
+        tile = i == 0 ? w.tile1 : tile;  // (none yet)
+        fetch(ahead[i]);
+      }
+    }
+    while (ok && ahead[0].more) {
+      cur = ahead[0];
+      ahead[0] = ahead[1];
+      ahead[1] = ahead[2];
+      if (ahead[1].more) fetch(ahead[2]);
+      if (!ok) break;
+      const int y = cache_row_of(cur);
+      ok = load(sa + L::kRing + k.slot * L::kTileBytes, y, bar.k_empty(k.slot), bar.k_full(k.slot), k.phase);
       if (ok) k.next();
-      ok = ok && load(sa + L::kRing + (L::kK + v.slot) * L::kTileBytes, cur.y + v_rows, bar.v_empty(v.slot),
+      ok = ok && load(sa + L::kRing + (L::kK + v.slot) * L::kTileBytes, y + v_rows, bar.v_empty(v.slot),
                       bar.landed(v.slot), v.phase);
       if (ok) v.next();
     }
@@ -368,8 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       sphase ^= 1u << j;
       return warp_wait(bar.k_full(k.slot), k.phase, abort, p.status);
     };
-    while (ok && w.next(p)) {
-      const int tiles = uniform(w.tile1 - w.tile0);
+    Seg g;
+    while (next_seg(g, ok)) {
+      const int tiles = uniform(g.tiles);
       ok = warp_wait(bar.q_full(seg & 1), seg >> 1 & 1, abort, p.status);
       for (int i = 0; ok && i < 2 && i < tiles; ++i)
         if ((ok = s_wait(i))) scores(i, i + 1 == tiles);
@@ -401,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
         v.next();
         if (!issued && (ok = s_wait(j))) scores(j, i + 3 == tiles);
       }
+      if (!ok) break;
       ++seg;
     }
     if (!ok) {  // products in flight end before TMEM is freed
@@ -410,145 +486,143 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------- queries' parts, tiles' scales
-    // Lane = (plane, block of the tile). Table entries are on their way two tiles
-    // ahead, scales one.
+    // Lane = (plane, block of the tile). Table entries are on their way three tiles
+    // ahead, scales as far as their ring goes.
     struct Ahead {
-      int t0;             // first token
-      int b, g, qg;
-      bool first;         // of its segment
-      bool there;         // this lane's block holds tokens that some query sees
-      int page;
-      float scale;
-    } a0 = {}, a1 = {}, a2 = {};
-    const int plane = lane >> 3, block = lane & 7, blocks = kTile >> fc.block_log2;
-    int tile = w.tile1;
-    auto fetch_page = [&](Ahead& a) {
-      a.first = tile == w.tile1;
-      if (a.first) {
-        if (!w.next(p)) return false;
-        tile = w.tile0;
+      int b, g, qg;       // qg -1: not the segment's first tile
+      int at, page;       // of this lane's block: its scale's index (in its page), its page
+      bool more;          // there is such a tile
+      bool there;         // the block holds tokens that some query sees
+    } ahead[3], a0;
+    const int plane = lane >> 3, block = lane & 7, blocks = kTile >> fc.block_log2, size = 1 << fc.block_log2;
+    const int step_pages = PAGED ? kTile / fc.page_size : 0, step_slots = PAGED ? kTile - step_pages * fc.page_size : 0;
+    bool ok = true;
+    Seg g;
+    g.tiles = 0;
+    int tile = 0, t = 0, entry = 0, slot = 0;  // of the next tile: this lane's block's first token, its entry in the table and slot
+    auto fetch = [&](Ahead& a) {
+      a.qg = -1;
+      a.more = true;
+      if (tile == g.tiles) {
+        if (!(a.more = next_seg(g, ok))) return;
+        a.qg = g.qg;
+        tile = 0;
+        t = g.t0 + (block << fc.block_log2);
+        if (PAGED) {
+          entry = t / fc.page_size;
+          slot = t - entry * fc.page_size;
+        }
       }
-      a.t0 = w.row.start + tile++ * kTile;
-      a.b = w.b;
-      a.g = w.g;
-      a.qg = w.qg;
-      const int t = a.t0 + (block << fc.block_log2);
-      a.there = plane < 2 && block < blocks && t < w.row.len && t + (1 << fc.block_log2) > row_low(p, w.row);
-      if (PAGED && a.there) a.page = fc.block_table[(size_t)w.b * fc.max_pages + t / fc.page_size];
-      return true;
-    };
-    auto fetch_scale = [&](Ahead& a) {
-      a.scale = 0.f;
-      if (!a.there) return;
-      const int t = a.t0 + (block << fc.block_log2);
-      long long at;
-      if (!PAGED) {
-        at = (((long long)plane * fc.batch + a.b) * fc.kv_heads + a.g) *
-                 ((fc.capacity + (1 << fc.block_log2) - 1) >> fc.block_log2) + (t >> fc.block_log2);
+      a.b = g.b;
+      a.g = g.g;
+      a.there = plane < 2 && block < blocks && t < g.len && t + size > row_low(p.window, g.prefix);
+      if (PAGED) {
+        a.page = a.there ? fc.block_table[(size_t)g.b * fc.max_pages + entry] : 0;
+        a.at = slot >> fc.block_log2;
+        entry += step_pages;
+        slot += step_slots;
+        if (slot >= fc.page_size) slot -= fc.page_size, ++entry;
       } else {
-        const int page = a.page < 0 || a.page >= fc.num_pages ? 0 : a.page;  // (the producer records it)
-        at = (((long long)plane * fc.num_pages + page) * fc.kv_heads + a.g) * (fc.page_size >> fc.block_log2) +
-             (t % fc.page_size >> fc.block_log2);
+        a.at = t >> fc.block_log2;
       }
-      a.scale = fc.scales[at];
+      ++tile;
+      t += kTile;
+    };
+    const int per_head = (PAGED ? fc.page_size : fc.capacity + size - 1) >> fc.block_log2;
+    auto scale_of = [&](const Ahead& a) -> const float* {
+      if (!a.there) return fc.scales;
+      const int head = !PAGED ? a.b : a.page < 0 || a.page >= fc.num_pages ? 0 : a.page;  // (the producer records it)
+      return fc.scales + (((long long)plane * (PAGED ? fc.num_pages : fc.batch) + head) * fc.kv_heads + a.g) * per_head + a.at;
     };
     Cursor<kScales> sc;
     uint32_t seg = 0;
-    bool ok = true;
-    bool more2 = fetch_page(a2), more1 = false;
-    if (more2) fetch_scale(a2);
-    bool more0 = more2;
-    a0 = a2;
-    more1 = more0 && fetch_page(a1);
-    while (ok && more0) {
-      more2 = more1 && fetch_page(a2);
-      if (more1) fetch_scale(a1);
-      if (a0.first) {
-        // Q': rows [part][column] of D bytes, swizzled
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      ahead[i].more = i == 0 || ahead[i - 1].more;
+      if (ahead[i].more) fetch(ahead[i]);
+    }
+    while (ok && ahead[0].more) {
+      a0 = ahead[0];
+      ahead[0] = ahead[1];
+      ahead[1] = ahead[2];
+      if (ahead[1].more) fetch(ahead[2]);
+      if (!ok) break;
+      if (!(ok = warp_wait(bar.sc_empty(sc.slot), sc.phase ^ 1, abort, p.status))) break;
+      if (plane < 2) {
+        const uint32_t to = sa + L::kSc + (sc.slot * 16 + lane) * 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(scale_of(a0)), "r"(a0.there ? 4 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar.sc_full(sc.slot)) : "memory");
+      sc.next();
+      if (a0.qg >= 0) {
+        // Q': rows [part][column] of D bytes, swizzled. Four lanes have a column, E elements each.
         const int buf = seg & 1;
         if (!(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
         ++seg;
-        constexpr int E = D / 32;  // elements of a lane
-        const int R = p.group * p.nodes, r0 = a0.qg * NC;
-        const uint16_t* const q = reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, a0.b, a0.g, r0) * D + lane * E;
+        constexpr int E = D / 4;
+        const int R = p.group * p.nodes, r0 = a0.qg * NC, part = lane & 3;
         uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
         float2* const cols = reinterpret_cast<float2*>(smem + L::kCols) + buf * NC;
 #pragma unroll 1
-        for (int c0 = 0; c0 < NC; c0 += 8) {
-          uint32_t x[8][E / 2];
+        for (int c = lane >> 2; c < NC; c += 8) {
+          const int r = r0 + c;
+          uint4 x[E / 8];
+          const uint4* const q =
+              reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, a0.b, a0.g, r) * D) + part * (E / 8);
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
+          for (int e = 0; e < E / 8; ++e) x[e] = r < R ? q[e] : make_uint4(0, 0, 0, 0);
+          uint32_t top = 0;
 #pragma unroll
-            for (int e = 0; e < E / 2; ++e)
-              x[c][e] = r0 + c0 + c < R ? reinterpret_cast<const uint32_t*>(q + (size_t)(c0 + c) * D)[e] : 0;
+          for (int e = 0; e < E / 8; ++e) {
+            const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) top = max(top, max(x[c][e] << 16 & 0x7fff0000u, x[c][e] & 0x7fff0000u));
-            top = __reduce_max_sync(0xffffffffu, top);
-            // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
-            const int up = min(7 - ((int)(top >> 23) - 127), 126);
-            const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
-            const bool finite = top < 0x7f800000u;
-            uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-              const float u = __uint_as_float(x[c][e] << 16) * factor, z = __uint_as_float(x[c][e] & 0xffff0000u) * factor;
-              hi[e] = finite ? e4m3x2(u, z) : 0x7f7fu;
-              const float2 h = from_e4m3x2(hi[e]);
-              lo[e] = finite ? e4m3x2((u - h.x) * 16.f, (z - h.y) * 16.f) : 0;
-            }
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const int n = part * NC + c0 + c, chunk = lane * E / 16, sw = D == 128 ? n & 7 : n >> 1 & 3;
-              uint8_t* const at = to + n * D + ((chunk ^ sw) << 4) + lane * E % 16;
-              const uint32_t* const z = part ? lo : hi;
-              if (E == 4)
-                *reinterpret_cast<uint32_t*>(at) = z[0] | z[E / 2 - 1] << 16;
-              else
-                *reinterpret_cast<uint16_t*>(at) = (uint16_t)z[0];
-            }
-            if (lane == 0)
-              cols[c0 + c] = make_float2(1.f / factor, __int_as_float((r0 + c0 + c) % p.nodes));
+            for (int k = 0; k < 4; ++k) top = max(top, max(z[k] << 16 & 0x7fff0000u, z[k] & 0x7fff0000u));
           }
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
+          const int up = min(7 - ((int)(top >> 23) - 127), 126);
+          const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
+          const bool finite = top < 0x7f800000u;
+          const int sw = D == 128 ? c & 7 : c >> 1 & 3;  // (both parts' rows: NC is a multiple of 8)
+#pragma unroll
+          for (int e = 0; e < E / 8; ++e) {
+            const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float u = __uint_as_float(z[k] << 16) * factor, v = __uint_as_float(z[k] & 0xffff0000u) * factor;
+              const uint32_t two = finite ? e4m3x2(u, v) : 0x7f7fu;
+              const float2 h = from_e4m3x2(two);
+              hi[k / 2] |= two << (k % 2 * 16);
+              lo[k / 2] |= (finite ? e4m3x2((u - h.x) * 16.f, (v - h.y) * 16.f) : 0) << (k % 2 * 16);
+            }
+            const int d = part * E + e * 8;
+            uint8_t* const at = to + c * D + ((d / 16 ^ sw) << 4) + d % 16;
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + NC * D) = make_uint2(lo[0], lo[1]);
+          }
+          if (part == 0) cols[c] = make_float2(1.f / factor, __int_as_float(r % p.nodes));
         }
         fence_proxy_async_smem();
         warp_arrive(bar.q_full(buf));
       }
-      if (!(ok = warp_wait(bar.sc_empty(sc.slot), sc.phase ^ 1, abort, p.status))) break;
-      float* const e = reinterpret_cast<float*>(smem + L::kSc) + (sc.slot * 8 + block) * 4;
-      if (plane == 0) e[0] = a0.scale * p.scale_log2;
-      if (plane == 1) {
-        // no scale: values of 0, whatever the weight; one that is far below all others
-        const float s = a0.scale == 0.f ? kFp8LeastScale : a0.scale;
-        e[1] = log2f(s);
-        e[2] = 1.f / s;
-      }
-      warp_arrive(bar.sc_full(sc.slot));
-      sc.next();
-      a0 = a1;
-      a1 = a2;
-      more0 = more1;
-      more1 = more2;
     }
+    // copies in flight end before the CTA does
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 3) {
-    // ------------------------------------------- V's edges, the merge's note
-    if (lane == 0) {
-      TreeWalk notes(w);
-      notes.write_splits(p);
-    }
-    __syncwarp();
+    // ------------------------------------------------------------------ V's edges
     Cursor<L::kV> v;
     bool ok = true;
-    while (ok && w.next(p)) {
-      const int low = row_low(p, w.row);
-      for (int i = w.tile0; i < w.tile1; ++i) {
+    Seg g;
+    while (ok && next_seg(g, ok)) {
+      int r_low = row_low(p.window, g.prefix) - g.t0, r_end = g.len - g.t0;  // rows of the tile
+      for (int i = 0; i < g.tiles; ++i, r_low -= kTile, r_end -= kTile) {
         if (!(ok = warp_wait(bar.landed(v.slot), v.phase, abort, p.status))) break;
-        const int t0 = w.row.start + i * kTile;
-        const int r_low = low - t0, r_end = w.row.len - t0;
         if (r_low > 0 || r_end < kTile) {
           uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + (L::kK + v.slot) * L::kTileBytes);
+#pragma unroll 1
           for (int x = lane; x < kTile * D / 16; x += 32) {
             const int r = x / (D / 16);
             if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
@@ -586,42 +660,43 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       warp_arrive(bar.join());
       return warp_wait(bar.join(), joins++ & 1, abort, p.status);
     };
-    while (ok && w.next(p)) {
-      const int tiles = w.tile1 - w.tile0, buf = seg & 1;
+    Seg g;
+    while (ok && next_seg(g, ok)) {
+      const int tiles = g.tiles, buf = seg & 1;
       if (!(ok = warp_wait(bar.q_full(buf), seg >> 1 & 1, abort, p.status))) break;
       ++seg;
       const float2* const cols = reinterpret_cast<const float2*>(smem + L::kCols) + buf * NC;
       if (lane < NC) *mine = make_float2(cols[lane].x, INFINITY);  // no reference
       __syncwarp();
-      const int low_all = all_low(p, w.row);
+      const int low_all = all_low(p.window, g.len);
       float l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) l[c] = 0.f;
       for (int i = 0; i < tiles; ++i, sc.next()) {
         if ((i & 1) != j) continue;
-        const int t0 = w.row.start + (w.tile0 + i) * kTile;
+        const int t0 = g.t0 + i * kTile;
         if (!(ok = warp_wait(bar.sc_full(sc.slot), sc.phase, abort, p.status))) break;
-        // K's scale times the softmax's, log2 of V's, its inverse
-        const float4 e = reinterpret_cast<const float4*>(smem + L::kSc)[sc.slot * 8 + (row >> fc.block_log2)];
+        const float* const scales = reinterpret_cast<const float*>(smem + L::kSc) + sc.slot * 16 + (row >> fc.block_log2);
+        const float k_scale = scales[0] * p.scale_log2;
+        // no scale: values of 0, whatever the weight; one that is far below all others
+        const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
         warp_arrive(bar.sc_empty(sc.slot));
+        const float v_log2 = __log2f(v_scale), v_inv = __frcp_rn(v_scale);
         if (!(ok = warp_wait(bar.s_full(j), count & 1, abort, p.status))) break;
         ++count;
         tmem_fence_after();
         uint32_t hidden = 0;  // columns that do not see this thread's token
-        if (t0 + kTile - 1 > w.row.prefix || t0 < low_all) {
+        if (t0 + kTile - 1 > g.prefix || t0 < low_all) {
           const int t = t0 + row;
+#pragma unroll 1
           for (int c = 0; c < NC; ++c) {
-            const int at = w.row.prefix + min(__float_as_int(cols[c].y), w.row.count - 1);
+            const int at = g.prefix + min(__float_as_int(cols[c].y), g.count - 1);
             if (t > at || (p.window >= 0 && t < at - p.window)) hidden |= 1u << c;
           }
         }
         const bool edge = __any_sync(0xffffffffu, hidden != 0);
         float y[NC];
-        // Pass 0: exponents against the references as they are. Where one is outgrown, pass 1
-        // looks for the columns' maxima, and pass 2 has the new references.
-        for (int pass = 0; ok; ++pass) {
-          const bool raw = pass == 1;
-          bool over = false;
+        auto exponents = [&] {  // against the references
           constexpr int kPart = NC < 16 ? NC : 16;  // columns at a time
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += kPart) {
@@ -638,30 +713,41 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
 #pragma unroll
             for (int c = 0; c < kPart; c += 2) {
               const float4 f = tab[(c0 + c) / 2];
-              const float a = fmaf(__uint_as_float(s[kPart + c]), 0.0625f, __uint_as_float(s[c])) * e.x;
-              const float b = fmaf(__uint_as_float(s[kPart + c + 1]), 0.0625f, __uint_as_float(s[c + 1])) * e.x;
-              y[c0 + c] = fmaf(a, f.x, e.y + (raw ? 0.f : f.y));
-              y[c0 + c + 1] = fmaf(b, f.z, e.y + (raw ? 0.f : f.w));
+              const float a = fmaf(__uint_as_float(s[kPart + c]), 0.0625f, __uint_as_float(s[c])) * k_scale;
+              const float b = fmaf(__uint_as_float(s[kPart + c + 1]), 0.0625f, __uint_as_float(s[c + 1])) * k_scale;
+              y[c0 + c] = fmaf(a, f.x, v_log2 + f.y);
+              y[c0 + c + 1] = fmaf(b, f.z, v_log2 + f.w);
             }
           }
           if (edge)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
               if (hidden >> c & 1) y[c] = -INFINITY;
-          if (pass == 2) break;
-          if (pass == 0) {
+        };
+        for (bool looked = false;;) {
+          exponents();
+          if (looked) break;
+          float most = y[0];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) over |= y[c] > kGrown;
-            // (the flag holds the number of the tile that raised it)
-            if (__any_sync(0xffffffffu, over) && lane == 0) flag[count & 1] = count;
-            ok = vote();
-            if (!ok || flag[count & 1] != count) break;
-            continue;
-          }
+          for (int c = 1; c < NC; ++c) most = fmaxf(most, y[c]);
+          // (the flag holds the number of the tile that raised it)
+          if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
+          if (!(ok = vote()) || flag[count & 1] != count) break;
+          // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
+#pragma unroll 1
+          for (int c = 0; c < NC; c += 4) {
+            uint32_t hi[4], lo[4];
+            tmem_ld4(ts + c, hi);
+            tmem_ld4(ts + NC + c, lo);
+            tmem_wait_ld4(hi);
+            tmem_wait_ld4(lo);
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            const float top = warp_max(fmaxf(y[c], -INFINITY));  // (a NaN is no maximum)
-            if (lane == 0) tops[me * NC + c] = top;
+            for (int k = 0; k < 4; ++k) {
+              const float x = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k])) * k_scale;
+              const float raw = fmaf(x, cols[c + k].x, v_log2);
+              const float top = warp_max(hidden >> (c + k) & 1 ? -INFINITY : fmaxf(raw, -INFINITY));  // (a NaN is no maximum)
+              if (lane == 0) tops[me * NC + c + k] = top;
+            }
           }
           if (!(ok = vote())) break;
           if (lane < NC) {
@@ -679,17 +765,17 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
             if (!(ok = warp_wait(bar.p_taken(j), count & 1, abort, p.status))) break;
             tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < 4 * NC; x += 16) {
-              uint32_t o[16];
-              tmem_ld16(to + j * 4 * NC + x, o);
-              tmem_wait_ld16(o);
+            for (int x = 0; x < 4 * NC; x += 4) {
+              uint32_t o[4];
+              tmem_ld4(to + j * 4 * NC + x, o);
+              tmem_wait_ld4(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                o[k] = __float_as_uint(__uint_as_float(o[k]) * sums[me * NC + (x + k) % NC]);
-              tmem_st16(to + j * 4 * NC + x, o);
+              for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sums[me * NC + (x + k) % NC]);
+              tmem_st4(to + j * 4 * NC + x, o);
             }
             tmem_wait_st();
           }
+          looked = true;
         }
         if (!ok) break;
         tmem_fence_before();
@@ -697,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           y[c] = fast_exp2(y[c]);
-          l[c] += edge && (hidden >> c & 1) ? 0.f : y[c] * e.z;  // (a hidden token's scale may be NaN)
+          l[c] += edge && (hidden >> c & 1) ? 0.f : y[c] * v_inv;  // (a hidden token's scale may be NaN)
         }
         uint32_t z[NC];  // the row of P': parts, columns in turn, a byte each
 #pragma unroll
@@ -743,10 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       if (!(ok = join())) break;
       tmem_fence_after();
 
-      const bool whole = w.whole();
-      float* const slot = whole ? nullptr : tree_slot(p, w.slot);
-      const int r0 = w.qg * NC;
-      const size_t out = tree_out_row(p, w.b, w.g, r0) * D + row;
+      float* const slot = g.slot < 0 ? nullptr : tree_slot(p, g.slot);
+      const int r0 = g.qg * NC;
+      const size_t out = tree_out_row(p, g.b, g.g, r0) * D + row;
       // each stream writes half of the columns, four at a time
 #pragma unroll 1
       for (int c0 = j * (NC / 2); c0 < (j + 1) * (NC / 2); c0 += 4) {
@@ -783,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
               slot[NC + place] = total;
             }
             if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
-          } else if (row < D && __float_as_int(cols[col].y) < w.row.count) {
+          } else if (row < D && __float_as_int(cols[col].y) < g.count) {
             const float inv = total == 0.f ? 0.f : 1.f / total;
             store_out(p.out, p.out_dtype, out + (size_t)col * D, sum * inv);
           }

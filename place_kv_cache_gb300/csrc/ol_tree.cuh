@@ -217,24 +217,34 @@ struct TreeWalk {
 
   __device__ __forceinline__ bool whole() const { return tile0 == 0 && tile1 == row.ntiles; }
 
+  // The merge's note of the unit that the segment begins (tile0 is 0).
+  __device__ __forceinline__ TreeSplit note(const TreeParams& p) const {
+    TreeSplit s = {};
+    s.first = blockIdx.x;
+    s.last = -1;
+    if (tile1 < row.ntiles) {
+      const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
+      const int big = more * (each + 1);                // tiles of the shares of one more
+      s.last = back < big ? back / (each + 1) : more + (back - big) / each;
+      s.count = row.count;
+      s.row0 = qg * p.rows_per_unit;
+      s.rows = min(p.rows_per_unit, p.group * p.nodes - s.row0);
+      s.out = (long long)tree_out_row(p, b, g, s.row0);
+    }
+    return s;
+  }
+  __device__ __forceinline__ int unit(const TreeParams& p) const {
+    return (b * p.kv_heads + g) * p.units_per_head + qg;
+  }
+
   // The share's notes for the merge, by one thread, on a walk of its own.
   __device__ __forceinline__ void write_splits(const TreeParams& p) {
     TreeSplit s = {};
     s.last = -1;
     while (next(p)) {
       if (tile0 > 0) continue;  // the unit began in an earlier share
-      s.first = blockIdx.x;
-      s.last = -1;
-      if (tile1 < row.ntiles) {
-        const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
-        const int big = more * (each + 1);                // tiles of the shares of one more
-        s.last = back < big ? back / (each + 1) : more + (back - big) / each;
-        s.count = row.count;
-        s.row0 = qg * p.rows_per_unit;
-        s.rows = min(p.rows_per_unit, p.group * p.nodes - s.row0);
-        s.out = (long long)tree_out_row(p, b, g, s.row0);
-      }
-      if (p.by_unit) p.splits[(b * p.kv_heads + g) * p.units_per_head + qg] = s;
+      s = note(p);
+      if (p.by_unit) p.splits[unit(p)] = s;
     }
     // (only the share's last unit can reach past its end)
     if (!p.by_unit) p.splits[blockIdx.x] = s;
