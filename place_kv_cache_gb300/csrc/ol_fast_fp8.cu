@@ -3,10 +3,10 @@
 //
 // A unit is NC = 8, 16 or 32 (head, query) columns c = head * new_len + query of one
 // row's kv head. Its tokens form tiles of 128; equal contiguous shares of all
-// units' tiles go to one CTA per SM (TreeWalk in ol_tree.cuh), whose two streams of
-// 128 threads take the tiles of a segment in turn. K and V go to the tensor cores as
-// they lie in the cache, with the tokens (for V the dimensions) as the products' 128
-// rows, so that the columns may be few and nothing is unpacked:
+// units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh): while one ends a
+// segment or waits, the other has the SM. K and V go to the tensor cores as they lie
+// in the cache, with the tokens (for V the dimensions) as the products' 128 rows, so
+// that the columns may be few and nothing is unpacked:
 //   S = K Q'    128 tokens x 2 NC x D.  Q' holds each q, times a power of two, in two
 //               E4M3 parts: the second is the first's remainder, times 16. The 8 bits
 //               of a bf16 number are both parts' 4, but for elements below 2^-17 of the
@@ -17,14 +17,13 @@
 //               16 bits, and steps of 2^-21 where m keeps the largest between 2^5 and
 //               2^8, so that the many small weights beside a large one are not lost.
 //   l += P / s_v    in fp32
-// The reference m of a column belongs to a stream: it is looked for (and O rescaled)
-// only when a token's y passes it by 2^3; O = sum of the parts' columns over 16^k.
-// The join of the streams and the segments' merge know states (m, l, o) as those of
-// the tree kernels.
+// The reference m of a column is looked for (and O rescaled) only when a token's y
+// passes it by 2^3; O = sum of the parts' columns over 16^k. The segments' merge knows
+// states (m, l, o) as those of the tree kernels.
 //
-// Warps: 0 the walk and the producer (TMA, a lane per box of a tile), 1 MMA issue, 2
-// queries' parts and the tiles' scales, 3 V's rows outside the row's tokens (zeros: P = 0
-// times a NaN code must not be NaN), 4-7 and 8-11 the streams. The others learn of the
+// Warps: 0 the walk and the producer (TMA, a lane per box of a tile), 1 MMA issue (and
+// zeros for V's rows outside the row's tokens: P = 0 times a NaN code must not be NaN),
+// 2 the tiles' scales, 3 the queries' parts, 4-7 the softmax. The others learn of the
 // segments from the first, through a ring: the walk in line in each of them, and the
 // loops of waits (wait_long), made the kernel outgrow the instruction cache.
 #include "ol_fp8.cuh"
@@ -34,11 +33,12 @@ namespace ol {
 namespace {
 
 constexpr int kTile = 1 << kTreeFastTileLog2;
-constexpr int kThreads = 384;
+constexpr int kThreads = 256;
 constexpr int kScales = 8;        // tiles whose scales are known ahead
 constexpr int kSegs = 8;          // segments known ahead
 constexpr float kTop = 5.f;       // log2 of the largest P when a reference is set
-constexpr float kGrown = 8.f;     // and of what makes a stream look for a new one
+constexpr float kGrown = 8.f;     // and of what makes a new one necessary
+constexpr int kMostSmem = (233472 - 2 * 1024) / 2;  // of one of two CTAs
 
 template <int D, int NC>
 struct Lay {
@@ -46,28 +46,27 @@ struct Lay {
   static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries
   static constexpr int kPBytes = kTile * 4 * NC;        // four parts of P
   static constexpr int kQ = 0;                          // two buffers
-  static constexpr int kP = kQ + 2 * kQBytes;           // one of each stream
-  static constexpr int kRing = kP + 2 * kPBytes;
-  static constexpr int kSmall = 8192;                   // what follows the ring
-  static constexpr int kSlots = (232448 - kSmall - kRing) / kTileBytes < 24 ? (232448 - kSmall - kRing) / kTileBytes : 24;
-  static constexpr int kK = kSlots / 2, kV = kSlots - kK;
+  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn
+  static constexpr int kSmall = 1536 + NC * 96;          // what follows the ring, at most
+  static constexpr int kFit = (kMostSmem - kSmall - kRing) / kTileBytes;
+  static constexpr int kSlots = kFit < 12 ? kFit : 12;
   static constexpr int kCols = kRing + kSlots * kTileBytes;   // float2 [2 buffers][NC]: q's inverse factor, query index
-  static constexpr int kTab = kCols + 2 * NC * 8;             // float2 [8 warps][NC]: that factor, minus the reference
-  static constexpr int kTops = kTab + 8 * NC * 8;             // float [8 warps][NC]: maxima
-  static constexpr int kSums = kTops + 8 * NC * 4;            // float [8 warps][NC]: factors, sums
-  static constexpr int kRho = kSums + 8 * NC * 4;             // float [2][NC]: the streams' references
-  static constexpr int kSc = kRho + 2 * NC * 4;               // float [kScales][2 planes][8 blocks]
+  static constexpr int kTab = kCols + 2 * NC * 8;             // [4 warps][NC / 2]: that factor of two columns, minus their references
+  static constexpr int kTops = kTab + 4 * NC * 8;             // float [4 warps][NC]: maxima
+  static constexpr int kSums = kTops + 4 * NC * 4;            // float [4 warps][NC]: l
+  static constexpr int kGrow = kSums + 4 * NC * 4;            // float [4 warps][NC]: what O is multiplied by
+  static constexpr int kSc = kGrow + 4 * NC * 4;              // float [kScales][2 planes][8 blocks]
   static constexpr int kSeg = kSc + kScales * 16 * 4;         // Seg [kSegs]
-  static constexpr int kFlag = kSeg + kSegs * 48;             // uint32 [2 streams][2]
+  static constexpr int kFlag = kSeg + kSegs * 48;             // uint32 [2]
   static constexpr int kBars = kFlag + 16;
-  // k full, empty; v landed, full, empty; q full, empty [2]; scales full, empty; s full, free, P ready, taken, vote [2];
-  // join, drain; segments full, empty
-  static constexpr int kNumBars = 2 * kK + 3 * kV + 4 + 2 * kScales + 10 + 2 + 2 * kSegs;
+  // slots full, empty; q full, empty [2]; s full, free [2]; P ready, taken, vote, drain; scales and segments full, empty
+  static constexpr int kNumBars = 2 * kSlots + 4 + 4 + 4 + 2 * kScales + 2 * kSegs;
   static constexpr int kMisc = kBars + kNumBars * 8;          // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 8;
-  static_assert(kTotal <= 232448 && kK >= 4, "shared memory of one CTA");
+  static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of two CTAs");
   static_assert(kRing % 1024 == 0 && kP % 1024 == 0 && kQBytes % 512 == 0, "swizzled tiles");
-  static constexpr int kTmem = NC == 8 ? 128 : NC == 16 ? 256 : 512;  // columns: 2 streams of 2 NC (S) and 4 NC (O)
+  static constexpr int kTmem = 8 * NC;  // columns: two S of 2 NC, O of 4 NC; 64, 128 or 256
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -174,25 +173,20 @@ template <int D, int NC>
 struct Bars {
   using L = Lay<D, NC>;
   uint32_t at;
-  __device__ uint32_t k_full(int s) const { return at + 8 * s; }
-  __device__ uint32_t k_empty(int s) const { return at + 8 * (L::kK + s); }
-  // V's copies are there; its slot is full once warp 3 has set it to rights
-  __device__ uint32_t landed(int s) const { return at + 8 * (2 * L::kK + s); }
-  __device__ uint32_t v_full(int s) const { return at + 8 * (2 * L::kK + L::kV + s); }
-  __device__ uint32_t v_empty(int s) const { return at + 8 * (2 * L::kK + 2 * L::kV + s); }
-  __device__ uint32_t q_full(int i) const { return at + 8 * (2 * L::kK + 3 * L::kV + i); }
+  __device__ uint32_t full(int s) const { return at + 8 * s; }
+  __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
+  __device__ uint32_t q_full(int i) const { return at + 8 * (2 * L::kSlots + i); }
   __device__ uint32_t q_empty(int i) const { return q_full(2 + i); }
-  __device__ uint32_t sc_full(int i) const { return q_full(4 + i); }
-  __device__ uint32_t sc_empty(int i) const { return q_full(4 + kScales + i); }
-  __device__ uint32_t s_full(int j) const { return q_full(4 + 2 * kScales + j); }
-  __device__ uint32_t s_free(int j) const { return s_full(2 + j); }    // S is in the stream's registers
-  __device__ uint32_t p_ready(int j) const { return s_full(4 + j); }
-  __device__ uint32_t p_taken(int j) const { return s_full(6 + j); }   // the products with P are done
-  __device__ uint32_t vote(int j) const { return s_full(8 + j); }
-  __device__ uint32_t join() const { return s_full(10); }
-  __device__ uint32_t drain() const { return s_full(11); }
-  __device__ uint32_t seg_full(int i) const { return s_full(12 + i); }
-  __device__ uint32_t seg_empty(int i) const { return s_full(12 + kSegs + i); }
+  __device__ uint32_t s_full(int i) const { return q_full(4 + i); }
+  __device__ uint32_t s_free(int i) const { return q_full(6 + i); }  // S is in registers
+  __device__ uint32_t p_ready() const { return q_full(8); }
+  __device__ uint32_t p_taken() const { return q_full(9); }          // the products with P are done
+  __device__ uint32_t vote() const { return q_full(10); }
+  __device__ uint32_t drain() const { return q_full(11); }
+  __device__ uint32_t sc_full(int i) const { return q_full(12 + i); }
+  __device__ uint32_t sc_empty(int i) const { return q_full(12 + kScales + i); }
+  __device__ uint32_t seg_full(int i) const { return q_full(12 + 2 * kScales + i); }
+  __device__ uint32_t seg_empty(int i) const { return q_full(12 + 2 * kScales + kSegs + i); }
 };
 
 // A place in a ring of N, and the parity of its lap.
@@ -229,8 +223,61 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(top ^ (top >> 31 & 0x7fffffff));
 }
 
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(__half2 x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&x)));
+  return r;
+}
+__device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
+  return *reinterpret_cast<__half2*>(&r);
+}
+// The four parts of two weights, a byte each, those of the first weight in the lower
+// bytes. The first two remainders in fp32; what is left then has at most 12 bits above
+// 2^-24 of the parts' scale, for which fp16 does (off by 2^-20 of the weight).
+__device__ __forceinline__ void four_parts(uint64_t w, uint32_t (&part)[4]) {
+  const uint64_t sixteen = pack2(16.f, 16.f), minus = pack2(-16.f, -16.f);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float2 x = unpack2(w);
+    part[k] = e4m3x2(x.x, x.y);
+    const float2 e = from_e4m3x2(part[k]);
+    w = fma2(pack2(e.x, e.y), minus, mul2(w, sixteen));  // exact: 16 (x - e)
+  }
+  const float2 x = unpack2(w);
+  const __half2 r = __floats2half2_rn(x.x, x.y);
+  part[2] = e4m3x2_of_half2(r);
+  part[3] = e4m3x2_of_half2(__hmul2(__hsub2(r, half2_of_e4m3x2(part[2])), __float2half2_rn(16.f)));
+}
+
 template <int D, int NC, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
+__global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
                                                                const __grid_constant__ Fp8AttnParams fp, const int box) {
   using L = Lay<D, NC>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -247,37 +294,31 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
 
   if (tid == 0) {
     prefetch_tensormap(&map);
-    for (int s = 0; s < L::kK; ++s) {
-      mbar_init(bar.k_full(s), 1);
-      mbar_init(bar.k_empty(s), 1);
-    }
-    for (int s = 0; s < L::kV; ++s) {
-      mbar_init(bar.landed(s), 1);
-      mbar_init(bar.v_full(s), 1);
-      mbar_init(bar.v_empty(s), 1);
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar.full(i), 1);
+      mbar_init(bar.empty(i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.q_full(i), 1);
-      mbar_init(bar.q_empty(i), 9);  // the products' and every stream warp's
+      mbar_init(bar.q_empty(i), 5);  // the products' and the softmax warps'
       mbar_init(bar.s_full(i), 1);
       mbar_init(bar.s_free(i), 4);
-      mbar_init(bar.p_ready(i), 4);
-      mbar_init(bar.p_taken(i), 1);
-      mbar_init(bar.vote(i), 4);
     }
+    mbar_init(bar.p_ready(), 4);
+    mbar_init(bar.p_taken(), 1);
+    mbar_init(bar.vote(), 4);
+    mbar_init(bar.drain(), 1);
     for (int i = 0; i < kScales; ++i) {
       mbar_init(bar.sc_full(i), 32);  // a lane's copies
       mbar_init(bar.sc_empty(i), 4);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar.seg_full(i), 1);
-      mbar_init(bar.seg_empty(i), 11);  // all warps but the producer
+      mbar_init(bar.seg_empty(i), 7);  // all warps but the producer
     }
-    mbar_init(bar.join(), 8);
-    mbar_init(bar.drain(), 1);
     fence_mbar_init();
     *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4) = 0;
-    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
+    for (int i = 0; i < 2; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa + L::kMisc), "n"(L::kTmem)
@@ -374,23 +415,21 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       if (bad) set_status(p.status, OL_DEVICE_GUARD);
       return (bad ? 0 : t.page) * fc.kv_heads * fc.page_size + t.y;
     };
-    Cursor<L::kK> k;
-    Cursor<L::kV> v;
-    auto load = [&](uint32_t to, int y, uint32_t empty, uint32_t there, uint32_t phase) {
-      if (!warp_wait(empty, phase ^ 1, abort, p.status)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(there, (uint32_t)(cur.last - cur.first) * box * D);
+    Cursor<L::kSlots> ring;
+    auto load = [&](int y) {
+      if (!warp_wait(bar.empty(ring.slot), ring.phase ^ 1, abort, p.status)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(bar.full(ring.slot), (uint32_t)(cur.last - cur.first) * box * D);
       __syncwarp();
-      if (lane >= cur.first && lane < cur.last) tma_load_2d(to + lane * box * D, &map, 0, y, there, policy);
+      if (lane >= cur.first && lane < cur.last)
+        tma_load_2d(sa + L::kRing + ring.slot * L::kTileBytes + lane * box * D, &map, 0, y, bar.full(ring.slot), policy);
+      ring.next();
       return true;
     };
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      ahead[i].more = true;
-      if (i > 0) ahead[i].more = ahead[i - 1].more;
-      if (ahead[i].more) {
-        tile = i == 0 ? w.tile1 : tile;  // (none yet)
-        fetch(ahead[i]);
-      }
+      ahead[i].more = i == 0 || ahead[i - 1].more;
+      if (i == 0) tile = w.tile1;  // (none yet)
+      if (ahead[i].more) fetch(ahead[i]);
     }
     while (ok && ahead[0].more) {
       cur = ahead[0];
@@ -399,16 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       if (ahead[1].more) fetch(ahead[2]);
       if (!ok) break;
       const int y = cache_row_of(cur);
-      ok = load(sa + L::kRing + k.slot * L::kTileBytes, y, bar.k_empty(k.slot), bar.k_full(k.slot), k.phase);
-      if (ok) k.next();
-      ok = ok && load(sa + L::kRing + (L::kK + v.slot) * L::kTileBytes, y + v_rows, bar.v_empty(v.slot),
-                      bar.landed(v.slot), v.phase);
-      if (ok) v.next();
+      ok = load(y) && load(y + v_rows);
     }
-    if (!ok) {  // copies in flight end before the CTA does; a slot's last load: of this lap before the cursor, else of the one before
-      for (int i = 0; i < L::kK; ++i) mbar_wait_bounded(bar.k_full(i), i < k.slot ? k.phase : k.phase ^ 1);
-      for (int i = 0; i < L::kV; ++i) mbar_wait_bounded(bar.landed(i), i < v.slot ? v.phase : v.phase ^ 1);
-    }
+    if (!ok)  // copies in flight end before the CTA does; a slot's last load: of this lap before the cursor, else of the one before
+      for (int i = 0; i < L::kSlots; ++i) mbar_wait_bounded(bar.full(i), i < ring.slot ? ring.phase : ring.phase ^ 1);
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA issue
     // The whole warp walks and waits, so that what the products are given stays in
@@ -417,64 +450,75 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
     constexpr uint32_t kRowSwizzle = D == 128 ? kSwizzle128 : kSwizzle64;  // rows of D bytes: K, V, Q'
     constexpr uint32_t kPSwizzle = NC == 32 ? kSwizzle128 : NC == 16 ? kSwizzle64 : kSwizzle32;
     const uint32_t tm = uniform(tmem), base = uniform(sa);
-    Cursor<L::kK> k;
-    Cursor<L::kV> v;
-    uint32_t seg = 0;
-    uint32_t sphase = 0, pphase = 0;  // of the streams, a bit each
+    Cursor<L::kSlots> k, v;  // slots of the next S's K, of the next product's V
+    v.next();
+    uint32_t seg = 0, s_count = 0, p_count = 0;
     bool ok = true;
-    auto scores = [&](int j, bool last) {  // S of stream j from the next tile of K
+    const auto s_phase = [&] { return s_count >> 1 & 1; };
+    auto scores = [&](bool last) {  // S of the next tile, into the next buffer
       tmem_fence_after();
       if (elect_one()) {
         const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes, 16, 8 * D, kRowSwizzle);
         const uint64_t qd = smem_desc(base + L::kQ + (seg & 1) * L::kQBytes, 16, 8 * D, kRowSwizzle);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) mma_fp8(tm + j * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, x > 0);
-        mma_commit(bar.s_full(j));
-        mma_commit(bar.k_empty(k.slot));
+        for (int x = 0; x < D / 32; ++x) mma_fp8(tm + (s_count & 1) * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, x > 0);
+        mma_commit(bar.s_full(s_count & 1));
+        mma_commit(bar.empty(k.slot));
         if (last) mma_commit(bar.q_empty(seg & 1));
       }
       __syncwarp();
+      ++s_count;
+      k.next();
       k.next();
     };
-    // (a stream's first S finds its buffer free: the phase before the first)
-    auto s_wait = [&](int j) {
-      if (!warp_wait(bar.s_free(j), sphase >> j & 1 ^ 1, abort, p.status)) return false;
-      sphase ^= 1u << j;
-      return warp_wait(bar.k_full(k.slot), k.phase, abort, p.status);
+    // (a buffer's first S finds it free: the phase before the first)
+    auto scores_wait = [&] {
+      return warp_wait(bar.s_free(s_count & 1), s_phase() ^ 1, abort, p.status) &&
+             warp_wait(bar.full(k.slot), k.phase, abort, p.status);
     };
     Seg g;
     while (next_seg(g, ok)) {
       const int tiles = uniform(g.tiles);
-      ok = warp_wait(bar.q_full(seg & 1), seg >> 1 & 1, abort, p.status);
-      for (int i = 0; ok && i < 2 && i < tiles; ++i)
-        if ((ok = s_wait(i))) scores(i, i + 1 == tiles);
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int j = i & 1;
-        bool issued = i + 2 >= tiles;
-        if (!issued && __all_sync(0xffffffffu, mbar_test(bar.s_free(j), sphase >> j & 1 ^ 1) &&
-                                                   mbar_test(bar.k_full(k.slot), k.phase))) {
-          sphase ^= 1u << j;
-          scores(j, i + 3 == tiles);
+      ok = warp_wait(bar.q_full(seg & 1), seg >> 1 & 1, abort, p.status) && scores_wait();
+      if (!ok) break;
+      scores(tiles == 1);
+      int r_low = row_low(p.window, g.prefix) - g.t0, r_end = g.len - g.t0;  // rows of the tile
+      for (int i = 0; ok && i < tiles; ++i, r_low -= kTile, r_end -= kTile) {
+        // the next tile's S ahead of this one's sums, if its K is there
+        bool issued = i + 1 == tiles;
+        if (!issued && __all_sync(0xffffffffu, mbar_test(bar.s_free(s_count & 1), s_phase() ^ 1) &&
+                                                   mbar_test(bar.full(k.slot), k.phase))) {
+          scores(i + 2 == tiles);
           issued = true;
         }
-        ok = warp_wait(bar.p_ready(j), pphase >> j & 1, abort, p.status) &&
-             warp_wait(bar.v_full(v.slot), v.phase, abort, p.status);
-        if (!ok) break;
-        pphase ^= 1u << j;
+        if (!(ok = warp_wait(bar.full(v.slot), v.phase, abort, p.status))) break;
+        if (r_low > 0 || r_end < kTile) {
+          uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes);
+#pragma unroll 1
+          for (int x = lane; x < kTile * D / 16; x += 32) {
+            const int r = x / (D / 16);
+            if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (!(ok = warp_wait(bar.p_ready(), p_count & 1, abort, p.status))) break;
+        ++p_count;
         tmem_fence_after();
         if (elect_one()) {
           // V's second half of the 128 rows is its first again where D is 64
-          const uint64_t vd = smem_desc(base + L::kRing + (L::kK + v.slot) * L::kTileBytes, 0, 8 * D, kRowSwizzle);
-          const uint64_t pd = smem_desc(base + L::kP + j * L::kPBytes, 0, 8 * 4 * NC, kPSwizzle);
+          const uint64_t vd = smem_desc(base + L::kRing + v.slot * L::kTileBytes, 0, 8 * D, kRowSwizzle);
+          const uint64_t pd = smem_desc(base + L::kP, 0, 8 * 4 * NC, kPSwizzle);
 #pragma unroll
           for (int x = 0; x < kTile / 32; ++x)
-            mma_fp8(tm + 4 * NC + j * 4 * NC, vd + x * (32 * D / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 1 || x > 0);
-          mma_commit(bar.p_taken(j));
-          mma_commit(bar.v_empty(v.slot));
+            mma_fp8(tm + 4 * NC, vd + x * (32 * D / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 0 || x > 0);
+          mma_commit(bar.p_taken());
+          mma_commit(bar.empty(v.slot));
         }
         __syncwarp();
         v.next();
-        if (!issued && (ok = s_wait(j))) scores(j, i + 3 == tiles);
+        v.next();
+        if (!issued && (ok = scores_wait())) scores(i + 2 == tiles);
       }
       if (!ok) break;
       ++seg;
@@ -485,11 +529,11 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
     }
     __syncwarp();
   } else if (warp == 2) {
-    // ------------------------------------------------- queries' parts, tiles' scales
+    // -------------------------------------------------------------- tiles' scales
     // Lane = (plane, block of the tile). Table entries are on their way three tiles
     // ahead, scales as far as their ring goes.
     struct Ahead {
-      int b, g, qg;       // qg -1: not the segment's first tile
+      int b, g;
       int at, page;       // of this lane's block: its scale's index (in its page), its page
       bool more;          // there is such a tile
       bool there;         // the block holds tokens that some query sees
@@ -501,11 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
     g.tiles = 0;
     int tile = 0, t = 0, entry = 0, slot = 0;  // of the next tile: this lane's block's first token, its entry in the table and slot
     auto fetch = [&](Ahead& a) {
-      a.qg = -1;
       a.more = true;
       if (tile == g.tiles) {
         if (!(a.more = next_seg(g, ok))) return;
-        a.qg = g.qg;
         tile = 0;
         t = g.t0 + (block << fc.block_log2);
         if (PAGED) {
@@ -535,7 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       return fc.scales + (((long long)plane * (PAGED ? fc.num_pages : fc.batch) + head) * fc.kv_heads + a.g) * per_head + a.at;
     };
     Cursor<kScales> sc;
-    uint32_t seg = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       ahead[i].more = i == 0 || ahead[i - 1].more;
@@ -555,134 +596,118 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar.sc_full(sc.slot)) : "memory");
       sc.next();
-      if (a0.qg >= 0) {
-        // Q': rows [part][column] of D bytes, swizzled. Four lanes have a column, E elements each.
-        const int buf = seg & 1;
-        if (!(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
-        ++seg;
-        constexpr int E = D / 4;
-        const int R = p.group * p.nodes, r0 = a0.qg * NC, part = lane & 3;
-        uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
-        float2* const cols = reinterpret_cast<float2*>(smem + L::kCols) + buf * NC;
-#pragma unroll 1
-        for (int c = lane >> 2; c < NC; c += 8) {
-          const int r = r0 + c;
-          uint4 x[E / 8];
-          const uint4* const q =
-              reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, a0.b, a0.g, r) * D) + part * (E / 8);
-#pragma unroll
-          for (int e = 0; e < E / 8; ++e) x[e] = r < R ? q[e] : make_uint4(0, 0, 0, 0);
-          uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < E / 8; ++e) {
-            const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) top = max(top, max(z[k] << 16 & 0x7fff0000u, z[k] & 0x7fff0000u));
-          }
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
-          const int up = min(7 - ((int)(top >> 23) - 127), 126);
-          const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
-          const bool finite = top < 0x7f800000u;
-          const int sw = D == 128 ? c & 7 : c >> 1 & 3;  // (both parts' rows: NC is a multiple of 8)
-#pragma unroll
-          for (int e = 0; e < E / 8; ++e) {
-            const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float u = __uint_as_float(z[k] << 16) * factor, v = __uint_as_float(z[k] & 0xffff0000u) * factor;
-              const uint32_t two = finite ? e4m3x2(u, v) : 0x7f7fu;
-              const float2 h = from_e4m3x2(two);
-              hi[k / 2] |= two << (k % 2 * 16);
-              lo[k / 2] |= (finite ? e4m3x2((u - h.x) * 16.f, (v - h.y) * 16.f) : 0) << (k % 2 * 16);
-            }
-            const int d = part * E + e * 8;
-            uint8_t* const at = to + c * D + ((d / 16 ^ sw) << 4) + d % 16;
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + NC * D) = make_uint2(lo[0], lo[1]);
-          }
-          if (part == 0) cols[c] = make_float2(1.f / factor, __int_as_float(r % p.nodes));
-        }
-        fence_proxy_async_smem();
-        warp_arrive(bar.q_full(buf));
-      }
     }
     // copies in flight end before the CTA does
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 3) {
-    // ------------------------------------------------------------------ V's edges
-    Cursor<L::kV> v;
+    // ------------------------------------------------------------ queries' parts
+    // Q': rows [part][column] of D bytes, swizzled. Four lanes have a column, E elements each.
+    constexpr int E = D / 4;
+    const int R = p.group * p.nodes, part = lane & 3;
+    uint32_t seg = 0;
     bool ok = true;
     Seg g;
-    while (ok && next_seg(g, ok)) {
-      int r_low = row_low(p.window, g.prefix) - g.t0, r_end = g.len - g.t0;  // rows of the tile
-      for (int i = 0; i < g.tiles; ++i, r_low -= kTile, r_end -= kTile) {
-        if (!(ok = warp_wait(bar.landed(v.slot), v.phase, abort, p.status))) break;
-        if (r_low > 0 || r_end < kTile) {
-          uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + (L::kK + v.slot) * L::kTileBytes);
+    while (next_seg(g, ok)) {
+      const int buf = seg & 1, r0 = g.qg * NC;
+      uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
+      float2* const cols = reinterpret_cast<float2*>(smem + L::kCols) + buf * NC;
+      const uint4* const q =
+          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, r0) * D) + part * (E / 8);
 #pragma unroll 1
-          for (int x = lane; x < kTile * D / 16; x += 32) {
-            const int r = x / (D / 16);
-            if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+      for (int c = lane >> 2; c < NC; c += 8) {
+        uint4 x[E / 8];
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) x[e] = r0 + c < R ? q[c * (D / 8) + e] : make_uint4(0, 0, 0, 0);
+        if (c < 8 && !(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) {
+          const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max(top, max(z[k] << 16 & 0x7fff0000u, z[k] & 0x7fff0000u));
         }
-        warp_arrive(bar.v_full(v.slot));
-        v.next();
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
+        const int up = min(7 - ((int)(top >> 23) - 127), 126);
+        const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
+        const bool finite = top < 0x7f800000u;  // else: NaN codes, so that the column's outputs are NaN
+        const int sw = D == 128 ? c & 7 : c >> 1 & 3;  // (of both parts' rows: NC is a multiple of 8)
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) {
+          const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+          uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float u = __uint_as_float(z[k] << 16) * factor, v = __uint_as_float(z[k] & 0xffff0000u) * factor;
+            const uint32_t two = finite ? e4m3x2(u, v) : 0x7f7fu;
+            const float2 h = from_e4m3x2(two);
+            hi[k / 2] |= two << (k % 2 * 16);
+            lo[k / 2] |= (finite ? e4m3x2((u - h.x) * 16.f, (v - h.y) * 16.f) : 0) << (k % 2 * 16);
+          }
+          const int d = part * E + e * 8;
+          uint8_t* const at = to + c * D + ((d / 16 ^ sw) << 4) + d % 16;
+          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(at + NC * D) = make_uint2(lo[0], lo[1]);
+        }
+        if (part == 0) cols[c] = make_float2(1.f / factor, __int_as_float((r0 + c) % p.nodes));
       }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      warp_arrive(bar.q_full(buf));
+      ++seg;
     }
   } else {
-    // ----------------------------------------------------------------- streams
-    const int j = (warp - 4) / 4, me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of O
-    const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-    const uint32_t ts = tmem + j * 2 * NC + lanes, to = tmem + 4 * NC + lanes;  // O of stream 0; of stream 1 behind it
-    const float4* const tab = reinterpret_cast<const float4*>(smem + L::kTab) + me * (NC / 2);  // of two columns each
-    float2* const mine = reinterpret_cast<float2*>(smem + L::kTab) + me * NC + lane % NC;
+    // ----------------------------------------------------------------- softmax
+    const int me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of O
+    const uint32_t lanes = (uint32_t)(me * 32) << 16;
+    const uint32_t to = tmem + 4 * NC + lanes;  // O
+    float* const tab = reinterpret_cast<float*>(smem + L::kTab) + me * NC * 2;  // of two columns: factors, minus references
+    float* const mine = tab + lane % NC / 2 * 4 + lane % 2;
     float* const tops = reinterpret_cast<float*>(smem + L::kTops);
-    float* const sums = reinterpret_cast<float*>(smem + L::kSums);  // factors, and at the end l, of each warp
-    float* const rho = reinterpret_cast<float*>(smem + L::kRho);
-    volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag) + j * 2;
+    float* const grow = reinterpret_cast<float*>(smem + L::kGrow) + me * NC;
+    float* const sums = reinterpret_cast<float*>(smem + L::kSums);
+    volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag);
     constexpr int kSwBits = NC == 32 ? 7 : NC == 16 ? 3 : 1, kSwShift = NC == 32 ? 0 : NC == 16 ? 1 : 2;
-    uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP + j * L::kPBytes) + row * (NC / 4);
+    uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP) + row * (NC / 4);
     const int p_sw = row >> kSwShift & kSwBits;  // the swizzle of this row's chunks
+    constexpr int kPart = NC < 16 ? NC : 16;     // columns at a time
     const int R = p.group * p.nodes;
     Cursor<kScales> sc;
-    uint32_t count = 0;    // of this stream's tiles
-    uint32_t votes = 0, joins = 0, seg = 0;
+    uint32_t count = 0;  // of tiles
+    uint32_t votes = 0, seg = 0;
     bool ok = true;
-    auto vote = [&] {  // the stream's warps
-      warp_arrive(bar.vote(j));
-      return warp_wait(bar.vote(j), votes++ & 1, abort, p.status);
-    };
-    auto join = [&] {  // both streams'
-      warp_arrive(bar.join());
-      return warp_wait(bar.join(), joins++ & 1, abort, p.status);
+    auto vote = [&] {
+      warp_arrive(bar.vote());
+      return warp_wait(bar.vote(), votes++ & 1, abort, p.status);
     };
     Seg g;
-    while (ok && next_seg(g, ok)) {
-      const int tiles = g.tiles, buf = seg & 1;
+    while (next_seg(g, ok)) {
+      const int buf = seg & 1;
       if (!(ok = warp_wait(bar.q_full(buf), seg >> 1 & 1, abort, p.status))) break;
       ++seg;
       const float2* const cols = reinterpret_cast<const float2*>(smem + L::kCols) + buf * NC;
-      if (lane < NC) *mine = make_float2(cols[lane].x, INFINITY);  // no reference
+      if (lane < NC) {
+        mine[0] = cols[lane].x;
+        mine[2] = INFINITY;  // no reference
+      }
       __syncwarp();
       const int low_all = all_low(p.window, g.len);
-      float l[NC];
+      uint64_t l[NC / 2];  // of two columns
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = 0.f;
-      for (int i = 0; i < tiles; ++i, sc.next()) {
-        if ((i & 1) != j) continue;
+      for (int c = 0; c < NC / 2; ++c) l[c] = 0;
+      for (int i = 0; i < g.tiles; ++i, sc.next()) {
         const int t0 = g.t0 + i * kTile;
         if (!(ok = warp_wait(bar.sc_full(sc.slot), sc.phase, abort, p.status))) break;
         const float* const scales = reinterpret_cast<const float*>(smem + L::kSc) + sc.slot * 16 + (row >> fc.block_log2);
         const float k_scale = scales[0] * p.scale_log2;
-        // no scale: values of 0, whatever the weight; one that is far below all others
+        // No scale: values of 0, whatever the weight; one that is far below all others. NaN
+        // comes in by its logarithm, and only for columns that see the token.
         const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
         warp_arrive(bar.sc_empty(sc.slot));
-        const float v_log2 = __log2f(v_scale), v_inv = __frcp_rn(v_scale);
-        if (!(ok = warp_wait(bar.s_full(j), count & 1, abort, p.status))) break;
+        const float v_log2 = __log2f(v_scale), v_inv = v_scale == v_scale ? __frcp_rn(v_scale) : 1.f;
+        const uint32_t ts = tmem + (count & 1) * 2 * NC + lanes;
+        if (!(ok = warp_wait(bar.s_full(count & 1), count >> 1 & 1, abort, p.status))) break;
         ++count;
         tmem_fence_after();
         uint32_t hidden = 0;  // columns that do not see this thread's token
@@ -696,36 +721,29 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
         }
         const bool edge = __any_sync(0xffffffffu, hidden != 0);
         float y[NC];
-        auto exponents = [&] {  // against the references
-          constexpr int kPart = NC < 16 ? NC : 16;  // columns at a time
+        for (bool looked = false;;) {
+          const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
           for (int c0 = 0; c0 < NC; c0 += kPart) {
             uint32_t s[2 * kPart];
-            if (NC == 8) {
-              tmem_ld16(ts, s);
-              tmem_wait_ld16(s);
-            } else {
-              tmem_ld16(ts + c0, s);
-              tmem_ld16(ts + NC + c0, s + kPart);
-              tmem_wait_ld16(s);
-              tmem_wait_ld16(s + kPart);
-            }
+            tmem_ld16(ts + c0, s);
+            if (NC > 8) tmem_ld16(ts + NC + c0, s + 16 % (2 * kPart));
+            tmem_wait_ld16(s);
+            if (NC > 8) tmem_wait_ld16(s + 16 % (2 * kPart));
 #pragma unroll
             for (int c = 0; c < kPart; c += 2) {
-              const float4 f = tab[(c0 + c) / 2];
-              const float a = fmaf(__uint_as_float(s[kPart + c]), 0.0625f, __uint_as_float(s[c])) * k_scale;
-              const float b = fmaf(__uint_as_float(s[kPart + c + 1]), 0.0625f, __uint_as_float(s[c + 1])) * k_scale;
-              y[c0 + c] = fmaf(a, f.x, v_log2 + f.y);
-              y[c0 + c + 1] = fmaf(b, f.z, v_log2 + f.w);
+              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(tab + (c0 + c) * 2);
+              const uint64_t hi = pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+              const uint64_t lo = pack2(__uint_as_float(s[kPart + c]), __uint_as_float(s[kPart + c + 1]));
+              const float2 z = unpack2(fma2(mul2(fma2(lo, part2, hi), k2), f.x, add2(v2, f.y)));
+              y[c0 + c] = z.x;
+              y[c0 + c + 1] = z.y;
             }
           }
           if (edge)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
               if (hidden >> c & 1) y[c] = -INFINITY;
-        };
-        for (bool looked = false;;) {
-          exponents();
           if (looked) break;
           float most = y[0];
 #pragma unroll
@@ -751,27 +769,27 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
           }
           if (!(ok = vote())) break;
           if (lane < NC) {
-            float top = tops[j * 4 * NC + lane];
+            float top = tops[lane];
 #pragma unroll
-            for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[(j * 4 + x) * NC + lane]);
-            const float old = mine->y, minus = fminf(old, kTop - top);  // the references only rise
-            mine->y = minus;
-            sums[me * NC + lane] = old == INFINITY ? 0.f : exp2f(minus - old);
+            for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[x * NC + lane]);
+            const float old = mine[2], minus = fminf(old, kTop - top);  // the references only rise
+            mine[2] = minus;
+            grow[lane] = old == INFINITY ? 0.f : exp2f(minus - old);
           }
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < NC; ++c) l[c] *= sums[me * NC + c];
-          if (i >= 2) {  // what the stream's earlier tiles of the segment have summed up
-            if (!(ok = warp_wait(bar.p_taken(j), count & 1, abort, p.status))) break;
+          for (int c = 0; c < NC / 2; ++c) l[c] = mul2(l[c], reinterpret_cast<const uint64_t*>(grow)[c]);
+          if (i > 0) {  // what the segment's earlier tiles have summed up
+            if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;
             tmem_fence_after();
 #pragma unroll 1
             for (int x = 0; x < 4 * NC; x += 4) {
               uint32_t o[4];
-              tmem_ld4(to + j * 4 * NC + x, o);
+              tmem_ld4(to + x, o);
               tmem_wait_ld4(o);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sums[me * NC + (x + k) % NC]);
-              tmem_st4(to + j * 4 * NC + x, o);
+              for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * grow[(x + k) % NC]);
+              tmem_st4(to + x, o);
             }
             tmem_wait_st();
           }
@@ -779,103 +797,96 @@ __global__ void __launch_bounds__(kThreads, 1) fast_fp8_kernel(const __grid_cons
         }
         if (!ok) break;
         tmem_fence_before();
-        warp_arrive(bar.s_free(j));
+        warp_arrive(bar.s_free(count + 1 & 1));
+        const uint64_t inv2 = pack2(v_inv, v_inv);
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          y[c] = fast_exp2(y[c]);
-          l[c] += edge && (hidden >> c & 1) ? 0.f : y[c] * v_inv;  // (a hidden token's scale may be NaN)
-        }
-        uint32_t z[NC];  // the row of P': parts, columns in turn, a byte each
+        for (int c0 = 0; c0 < NC; c0 += kPart) {
+          uint32_t z[4][kPart / 4];  // P' of this row: parts, a byte a column
 #pragma unroll
-        for (int c = 0; c < NC; c += 4)
+          for (int c = 0; c < kPart; c += 4) {
+            uint32_t part[2][4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t a = e4m3x2(y[c], y[c + 1]), b = e4m3x2(y[c + 2], y[c + 3]);
-            z[(k * NC + c) / 4] = a | b << 16;
-            if (k == 3) break;
-            const float2 fa = from_e4m3x2(a), fb = from_e4m3x2(b);
-            y[c] = (y[c] - fa.x) * 16.f;
-            y[c + 1] = (y[c + 1] - fa.y) * 16.f;
-            y[c + 2] = (y[c + 2] - fb.x) * 16.f;
-            y[c + 3] = (y[c + 3] - fb.y) * 16.f;
+            for (int h = 0; h < 2; ++h) {
+              const int x = c0 + c + 2 * h;
+              const uint64_t w2 = pack2(fast_exp2(y[x]), fast_exp2(y[x + 1]));
+              l[x / 2] = fma2(w2, inv2, l[x / 2]);
+              four_parts(w2, part[h]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
           }
-        if (!(ok = warp_wait(bar.p_taken(j), count & 1, abort, p.status))) break;  // the last P is read
+          if (c0 == 0 && !(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;  // the last P is read
+          if (NC == 8) {
+            p_row[0 ^ p_sw] = make_uint4(z[0][0], z[0][1], z[1][0], z[1][1]);
+            p_row[1 ^ p_sw] = make_uint4(z[2][0], z[2][1], z[3][0], z[3][1]);
+          } else {
 #pragma unroll
-        for (int x = 0; x < NC / 4; ++x) p_row[x ^ p_sw] = make_uint4(z[4 * x], z[4 * x + 1], z[4 * x + 2], z[4 * x + 3]);
+            for (int k = 0; k < 4; ++k)
+              p_row[(k * (NC / 16) + c0 / 16) ^ p_sw] =
+                  make_uint4(z[k][0], z[k][1], z[k][2 % (kPart / 4)], z[k][3 % (kPart / 4)]);
+          }
+        }
+        if (!ok) break;
         fence_proxy_async_smem();
         tmem_fence_before();
-        warp_arrive(bar.p_ready(j));
+        warp_arrive(bar.p_ready());
       }
       if (!ok) break;
-      if (tiles > j && !(ok = warp_wait(bar.p_taken(j), count + 1 & 1, abort, p.status))) break;
 
-      // The segment's state: l over the warp's lanes (a step halves the columns that a
-      // lane holds, then the lanes of a column are summed), and the references.
+      // The segment's state. l over the warp's lanes: a step halves the columns that a
+      // lane holds, then the lanes of a column are summed.
+      float t[NC];
+#pragma unroll
+      for (int c = 0; c < NC; c += 2) {
+        const float2 x = unpack2(l[c / 2]);
+        t[c] = x.x;
+        t[c + 1] = x.y;
+      }
 #pragma unroll
       for (int n = NC / 2, o = 16; n > 0; n /= 2, o /= 2) {
         const bool up = lane & o;
 #pragma unroll
         for (int c = 0; c < n; ++c) {
-          const float give = up ? l[c] : l[c + n], keep = up ? l[c + n] : l[c];
-          l[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          const float give = up ? t[c] : t[c + n], keep = up ? t[c + n] : t[c];
+          t[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
       }
 #pragma unroll
-      for (int o = 16 / NC; o > 0; o /= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+      for (int o = 16 / NC; o > 0; o /= 2) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
       // lane's column: its upper bits
-      if (lane % (32 / NC) == 0) sums[me * NC + lane / (32 / NC)] = l[0];
-      if (me % 4 == 0 && lane < NC) rho[j * NC + lane] = -mine->y;
-      tmem_fence_before();
-      if (!(ok = join())) break;
+      if (lane % (32 / NC) == 0) sums[me * NC + lane / (32 / NC)] = t[0];
+      if (!(ok = vote())) break;
+      if (!(ok = warp_wait(bar.p_taken(), count + 1 & 1, abort, p.status))) break;
       tmem_fence_after();
-
       float* const slot = g.slot < 0 ? nullptr : tree_slot(p, g.slot);
       const int r0 = g.qg * NC;
       const size_t out = tree_out_row(p, g.b, g.g, r0) * D + row;
-      // each stream writes half of the columns, four at a time
 #pragma unroll 1
-      for (int c0 = j * (NC / 2); c0 < (j + 1) * (NC / 2); c0 += 4) {
-        uint32_t o[2][4][4];
+      for (int c0 = 0; c0 < NC && r0 + c0 < R; c0 += 4) {
+        uint32_t o[4][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+        for (int k = 0; k < 4; ++k) tmem_ld4(to + k * NC + c0, o[k]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (x < tiles) tmem_ld4(to + x * 4 * NC + k * NC + c0, o[x][k]);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (x < tiles) tmem_wait_ld4(o[x][k]);
+        for (int k = 0; k < 4; ++k) tmem_wait_ld4(o[k]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int col = c0 + c, place = col;
-          const float ra = rho[col], rb = rho[NC + col], m = fmaxf(ra, rb), base = m == -INFINITY ? 0.f : m;
-          const float f[2] = {exp2f(ra - base), exp2f(rb - base)};
-          float total = 0.f, sum = 0.f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (x >= tiles) continue;
-            const float* const la = sums + x * 4 * NC + col;
-            total += (la[0] + la[NC] + la[2 * NC] + la[3 * NC]) * f[x];
-            const float v = fmaf(fmaf(fmaf(__uint_as_float(o[x][3][c]), 0.0625f, __uint_as_float(o[x][2][c])), 0.0625f,
-                                      __uint_as_float(o[x][1][c])), 0.0625f, __uint_as_float(o[x][0][c]));
-            sum += v * f[x];
-          }
+          const int col = c0 + c;
           if (r0 + col >= R) continue;
+          const float total = sums[col] + sums[NC + col] + sums[2 * NC + col] + sums[3 * NC + col];
+          const float sum = fmaf(fmaf(fmaf(__uint_as_float(o[3][c]), 0.0625f, __uint_as_float(o[2][c])), 0.0625f,
+                                      __uint_as_float(o[1][c])), 0.0625f, __uint_as_float(o[0][c]));
           if (slot) {
             if (row == 0) {
-              slot[place] = m;
-              slot[NC + place] = total;
+              slot[col] = -tab[col / 2 * 4 + 2 + col % 2];
+              slot[NC + col] = total;
             }
-            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
+            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + col) * 4 + row % 4] = sum;
           } else if (row < D && __float_as_int(cols[col].y) < g.count) {
-            const float inv = total == 0.f ? 0.f : 1.f / total;
-            store_out(p.out, p.out_dtype, out + (size_t)col * D, sum * inv);
+            store_out(p.out, p.out_dtype, out + (size_t)col * D, total == 0.f ? 0.f : sum / total);
           }
         }
       }
       tmem_fence_before();
-      if (!(ok = join())) break;  // both streams have read both O before either's next product
       warp_arrive(bar.q_empty(buf));
     }
   }
@@ -927,7 +938,9 @@ cudaError_t launch_cfg(const CUtensorMap& map, const Fp8AttnParams& p, int box, 
   auto kern = fast_fp8_kernel<D, NC, PAGED>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t attr = once_per_device(done, [kern] {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NC>::kTotal);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NC>::kTotal);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(kern, dim3(p.t.nctas), dim3(kThreads), Lay<D, NC>::kTotal, s, map, p, box);
@@ -959,7 +972,7 @@ void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   p.rows_per_unit = columns <= 8 ? 8 : columns <= 16 ? 16 : 32;
   p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
-  p.nctas = sms < kTreeMaxCtas ? sms : kTreeMaxCtas;
+  p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   p.extra = 2;
   p.by_unit = tree_few_units(p);
 }
