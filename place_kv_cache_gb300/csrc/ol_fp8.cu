@@ -29,6 +29,37 @@ struct alignas(sizeof(T) * N) Pack {
   T e[N];
 };
 
+// The codes of N = 8, 4 or 1 elements.
+template <int N>
+using Codes = std::conditional_t<N == 8, uint2, std::conditional_t<N == 4, uint32_t, uint8_t>>;
+
+// N codes times s, rounded to T.
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> values_of(Codes<N> z, float s) {
+  Pack<T, N> w;
+  auto two = [&](uint32_t codes, int j) {  // elements j, j + 1
+    const float2 v = from_e4m3x2(codes);
+    if constexpr (sizeof(T) == 2) {
+      *reinterpret_cast<uint32_t*>(&w.e[j]) = pack_bf16x2(v.x * s, v.y * s);
+    } else {
+      w.e[j] = v.x * s;
+      w.e[j + 1] = v.y * s;
+    }
+  };
+  if constexpr (N == 8) {
+    two(z.x, 0);
+    two(z.x >> 16, 2);
+    two(z.y, 4);
+    two(z.y >> 16, 6);
+  } else if constexpr (N == 4) {
+    two(z, 0);
+    two(z >> 16, 2);
+  } else {
+    w.e[0] = rounded_to<T>(from_e4m3x2(z).x * s);
+  }
+  return w;
+}
+
 // ---------------------------------------------------------------------- append
 
 // The scale that a block takes for a largest new element `most` (its bits, of the
@@ -55,15 +86,24 @@ __device__ __forceinline__ float block_scale(uint32_t most, bool begun, float ol
 
 // One CTA per block of tokens, head and plane that the call may reach. Its new
 // elements stay in registers between the search for the largest and their
-// quantising: KEEP pieces of VE elements a thread.
+// quantising: KEEP pieces of VE elements a thread, every blockDim.x-th.
+// The quotient x / s is x times the rounded inverse, set right by its remainder:
+// q = x r, q + (x - q s) r is x / s rounded to nearest where r is 1 / s rounded to
+// nearest (Markstein, Computation of elementary functions on the IBM RISC System/6000,
+// 1990); the remainder is exact for all quotients that do not round to a code of 0.
 template <typename T, int VE, int KEEP>
-__global__ void __launch_bounds__(VE == 8 ? 512 : 1024) fp8_append_kernel(const __grid_constant__ Fp8AppendParams p) {
+__global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
+    fp8_append_kernel(const __grid_constant__ Fp8AppendParams p) {
   using P = Pack<T, VE>;
   __shared__ uint32_t tops[32];
   const Fp8Cache& c = p.cache;
   const int plane = blockIdx.y, tid = threadIdx.x;
   const int unit = blockIdx.x / c.kv_heads, g = blockIdx.x - unit * c.kv_heads;
   const int b = unit / p.blocks, nth = unit - b * p.blocks;
+  const int pieces = c.head_dim / VE;
+  // piece tid of the block's, and the way to every next one of this thread
+  const int t_first = tid / pieces, x_first = tid - t_first * pieces;
+  const int t_step = blockDim.x / pieces, x_step = blockDim.x - t_step * pieces;
   pdl_wait();
   pdl_launch_dependents();
   const int start = p.positions[b], n = p.counts ? p.counts[b] : p.new_len;
@@ -71,29 +111,38 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024) fp8_append_kernel(const 
   const int end = min(c.capacity - start, n) + start;
   const int first = ((start >> c.block_log2) + nth) << c.block_log2;  // the block's first token
   if (first >= end) return;
-  const int lo = max(start, first), hi = min(end, first + (1 << c.block_log2));
+  const int lo = max(start, first), tokens = min(end, first + (1 << c.block_log2)) - lo;
+  const RopeView& in = p.in[plane];
+  const T* const from = reinterpret_cast<const T*>(in.data) + b * in.sb + g * in.sh + (long long)(lo - start) * in.st;
+  P x[KEEP];
+  int t = t_first, d = x_first;
+  auto next = [&] {
+    t += t_step;
+    d += x_step;
+    if (d >= pieces) d -= pieces, ++t;
+  };
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u, next())
+    if (t < tokens) x[u] = *reinterpret_cast<const P*>(from + t * in.st + d * VE);
   long long row, at;
   if (!fp8_place(c, plane, b, g, first, row, at)) return;  // (device guard)
   const bool begun = lo > first;
   const float old = begun ? c.scales[at] : 0.f;
-  const RopeView& in = p.in[plane];
-  const T* const from = reinterpret_cast<const T*>(in.data) + b * in.sb + g * in.sh + (long long)(lo - start) * in.st;
-  const int pieces = c.head_dim / VE, total = (hi - lo) * pieces;
-  P x[KEEP];
   uint32_t most = 0;
+  t = t_first, d = x_first;
 #pragma unroll
-  for (int u = 0; u < KEEP; ++u) {
-    const int i = tid + u * blockDim.x;
-    if (i < total) {
-      const int t = i / pieces;
-      x[u] = *reinterpret_cast<const P*>(from + t * in.st + (i - t * pieces) * VE);
+  for (int u = 0; u < KEEP; ++u, next())
+    if (t < tokens) {
+      if constexpr (VE == 8) {  // the absolute values' bits, two at a time
+        const uint32_t* const w = reinterpret_cast<const uint32_t*>(&x[u]);
+        most = __vmaxu2(most, __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                       __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) most = abs_max(most, value_of<T>(x[u].e[j]));
+      }
     }
-  }
-#pragma unroll
-  for (int u = 0; u < KEEP; ++u)
-    if (tid + u * (int)blockDim.x < total)
-#pragma unroll
-      for (int j = 0; j < VE; ++j) most = abs_max(most, value_of<T>(x[u].e[j]));
+  if constexpr (VE == 8) most = max(most << 16, most & 0xffff0000u);
   most = __reduce_max_sync(0xffffffffu, most);
   if (blockDim.x > 32) {
     if (tid % 32 == 0) tops[tid / 32] = most;
@@ -112,20 +161,27 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024) fp8_append_kernel(const 
     }
   }
   const bool coded = scale > 0.f;  // false for 0 and NaN
+  const float inverse = coded ? __frcp_rn(scale) : 0.f;
+  auto quotient = [&](float v) {
+    const float q = v * inverse;
+    return fmaf(fmaf(-q, scale, v), inverse, q);
+  };
+  uint8_t* const to = codes + (long long)(lo - first) * c.head_dim;
+  t = t_first, d = x_first;
 #pragma unroll
-  for (int u = 0; u < KEEP; ++u) {
-    const int i = tid + u * blockDim.x;
-    if (i >= total) continue;
-    Pack<uint8_t, VE> y;
-#pragma unroll
-    for (int j = 0; j < VE; j += VE > 1 ? 2 : 1) {
-      const float v0 = value_of<T>(x[u].e[j]), v1 = value_of<T>(x[u].e[VE > 1 ? j + 1 : j]);
-      const uint32_t two = coded ? e4m3x2(__fdiv_rn(v0, scale), __fdiv_rn(v1, scale)) : 0;
-      y.e[j] = (uint8_t)two;
-      if (VE > 1) y.e[VE > 1 ? j + 1 : j] = (uint8_t)(two >> 8);
-    }
-    const int t = i / pieces;
-    *reinterpret_cast<Pack<uint8_t, VE>*>(codes + (long long)(lo - first + t) * c.head_dim + (i - t * pieces) * VE) = y;
+  for (int u = 0; u < KEEP; ++u, next()) {
+    if (t >= tokens) continue;
+    auto two = [&](int j) {
+      return coded ? e4m3x2(quotient(value_of<T>(x[u].e[j])), quotient(value_of<T>(x[u].e[VE > 1 ? j + 1 : j]))) : 0u;
+    };
+    Codes<VE> y;
+    if constexpr (VE == 8)
+      y = make_uint2(two(0) | two(2) << 16, two(4) | two(6) << 16);
+    else if constexpr (VE == 4)
+      y = two(0) | two(2) << 16;
+    else
+      y = (uint8_t)two(0);
+    *reinterpret_cast<Codes<VE>*>(to + t * c.head_dim + d * VE) = y;
   }
   if (tid == 0) c.scales[at] = scale;  // (every thread has read the old one)
 }
@@ -141,58 +197,64 @@ cudaError_t launch_append_cfg(const Fp8AppendParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------------ read
 
-constexpr int kReadUnroll = 4;
+constexpr int kReadThreads = 256, kReadUnroll = 8, kReadMost = 128;
 
-// A CTA reads a run of one row's tokens of a head and plane; a thread has VE
-// consecutive elements (16 bytes of output) of every step-th token.
+// A CTA reads a run of one row's tokens of a head, K and V: places and scales are
+// looked up once a token, then a thread has VE consecutive elements (16 bytes of
+// output) of up to 8 tokens, all on their way together.
 template <typename T, int VE>
-__global__ void __launch_bounds__(256) fp8_read_kernel(const __grid_constant__ Fp8ReadParams p, int runs) {
+__global__ void __launch_bounds__(kReadThreads, 3) fp8_read_kernel(const __grid_constant__ Fp8ReadParams p, int runs, int run_tokens) {
+  __shared__ long long rows[2][kReadMost];  // of the token's codes; -1: it is not read
+  __shared__ float scales[2][kReadMost];
   const Fp8Cache& c = p.cache;
-  const int plane = p.out[0].data ? (int)blockIdx.y : 1;
   const int unit = blockIdx.x / c.kv_heads, g = blockIdx.x - unit * c.kv_heads;
-  const int b = unit / runs, run = unit - b * runs;
+  const int b = unit / runs, first = (unit - b * runs) * run_tokens, tid = threadIdx.x;
+  const int pieces = c.head_dim / VE, y = tid / pieces, x = tid - y * pieces, step = kReadThreads / pieces;
   pdl_wait();
   pdl_launch_dependents();
   const int start = p.starts[b], n = min(p.counts ? p.counts[b] : p.tokens, p.tokens);
-  if (start < 0) return;  // (device guard)
-  const RopeView& out = p.out[plane];
-  T* const to = reinterpret_cast<T*>(out.data) + b * out.sb + g * out.sh;
-  const int t0 = run * (int)blockDim.y * kReadUnroll + threadIdx.y, pieces = c.head_dim / VE;
-  for (int x = threadIdx.x; x < pieces; x += blockDim.x) {
-    Pack<uint8_t, VE> y[kReadUnroll];
-    float scale[kReadUnroll];
-    bool there[kReadUnroll];
+  if (start < 0 || first >= n) return;  // (device guard)
+  for (int i = tid; i < 2 * run_tokens; i += kReadThreads) {
+    const int plane = i >= run_tokens, t = i - plane * run_tokens;
+    long long row = -1, at;
+    if (p.out[plane].data && first + t < n && (long long)start + first + t < c.capacity &&
+        fp8_place(c, plane, b, g, start + first + t, row, at))
+      scales[plane][t] = c.scales[at];
+    else
+      row = -1;
+    rows[plane][t] = row;
+  }
+  __syncthreads();
+  if (y >= step) return;
+#pragma unroll
+  for (int plane = 0; plane < 2; ++plane) {
+    const RopeView& out = p.out[plane];
+    if (!out.data) continue;
+    T* const to = reinterpret_cast<T*>(out.data) + b * out.sb + g * out.sh + (long long)first * out.st + x * VE;
+    Codes<VE> z[kReadUnroll];
+    long long row[kReadUnroll];
 #pragma unroll
     for (int u = 0; u < kReadUnroll; ++u) {
-      const int t = t0 + u * blockDim.y;
-      long long row, at;
-      there[u] = t < n && (long long)start + t < c.capacity && fp8_place(c, plane, b, g, start + t, row, at);
-      if (!there[u]) continue;
-      y[u] = *reinterpret_cast<const Pack<uint8_t, VE>*>(c.codes + row * c.head_dim + x * VE);
-      scale[u] = c.scales[at];
+      const int t = y + u * step;
+      row[u] = t < run_tokens ? rows[plane][t] : -1;
+      if (row[u] >= 0) z[u] = *reinterpret_cast<const Codes<VE>*>(c.codes + row[u] * c.head_dim + x * VE);
     }
 #pragma unroll
     for (int u = 0; u < kReadUnroll; ++u) {
-      if (!there[u]) continue;
-      Pack<T, VE> z;
-#pragma unroll
-      for (int j = 0; j < VE; j += VE > 1 ? 2 : 1) {
-        const float2 v = from_e4m3x2(VE > 1 ? y[u].e[j] | (uint32_t)y[u].e[VE > 1 ? j + 1 : j] << 8 : y[u].e[j]);
-        z.e[j] = rounded_to<T>(v.x * scale[u]);
-        if (VE > 1) z.e[VE > 1 ? j + 1 : j] = rounded_to<T>(v.y * scale[u]);
-      }
-      *reinterpret_cast<Pack<T, VE>*>(to + (t0 + u * (long long)blockDim.y) * out.st + x * VE) = z;
+      const int t = y + u * step;
+      if (row[u] < 0) continue;
+      *reinterpret_cast<Pack<T, VE>*>(to + t * out.st) = values_of<T, VE>(z[u], scales[plane][t]);
     }
   }
 }
 
 template <typename T, int VE>
 cudaError_t launch_read_cfg(const Fp8ReadParams& p, cudaStream_t s) {
-  const int pieces = p.cache.head_dim / VE, x = pieces < 256 ? pieces : 256, y = 256 / x;
-  const int runs = (p.tokens + y * kReadUnroll - 1) / (y * kReadUnroll);
-  const int planes = (p.out[0].data != nullptr) + (p.out[1].data != nullptr);
-  return launch_pdl(fp8_read_kernel<T, VE>, dim3((unsigned)p.cache.batch * runs * p.cache.kv_heads, planes), dim3(x, y), 0,
-                    s, p, runs);
+  const int step = kReadThreads / (p.cache.head_dim / VE), run = step * kReadUnroll;  // tokens a pass, and a CTA
+  const int tokens = run < kReadMost ? run : kReadMost;
+  const int runs = (p.tokens + tokens - 1) / tokens;
+  return launch_pdl(fp8_read_kernel<T, VE>, dim3((unsigned)p.cache.batch * runs * p.cache.kv_heads), dim3(kReadThreads), 0, s,
+                    p, runs, tokens);
 }
 
 // ------------------------------------------------------- attention, CUDA cores

@@ -5,10 +5,12 @@
 //   rot_dim elements turn by their position's angle (ol_rope.cu has the table's
 //   arithmetic).
 //
-// One CTA takes one token of one row and all of its q and k vectors, so that the
-// token's sines and cosines are computed once. A group of LANES lanes has a vector:
-// it is read once, its squares are summed by shuffles in fp32, and it is written
-// once. Bounds: 2 * D * elt bytes a vector: memory, or the launch for a decode step.
+// Vectors of up to 32 items (16-byte pieces, see Items) go by warps: a warp has a
+// token and its vectors, or a slice of them, and nothing to wait for but its loads. A
+// group of lanes has a vector, a lane the same item of all of them, so its weights, sines
+// and cosines stay in registers (the groups compute a share of these each). Others, and
+// views without 16-byte alignment, go by CTAs that keep them in shared memory.
+// Bounds: 2 * D * elt bytes a vector: memory, or the launch for a decode step.
 #include "ol_common.cuh"
 #include "ol_fp8.h"
 
@@ -17,6 +19,7 @@ namespace {
 
 constexpr int kNormThreads = 256;
 constexpr int kMaxHalf = 512;
+constexpr int kManyWarps = 8192;  // fewer tokens are cut into slices of their vectors
 
 __device__ __forceinline__ float value_of(float x) { return x; }
 __device__ __forceinline__ float value_of(uint16_t x) { return bf16_bits_to_float(x); }
@@ -48,143 +51,327 @@ struct Items {
   __device__ int second(int i, int rot) const { return HALF ? rot / 2 + i * VE : 2 * i + 1; }
 };
 
-// NI items of a vector a lane.
-template <typename T, int VE, bool HALF, int NI>
-__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int lanes) {
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t two_of(const float* x) { return pack2(x[0], x[1]); }
+__device__ __forceinline__ uint64_t two_of(const uint16_t* x) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(x);
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void put_two(float* to, uint64_t x) { *reinterpret_cast<float2*>(to) = unpack2(x); }
+__device__ __forceinline__ void put_two(uint16_t* to, uint64_t x) {
+  const float2 v = unpack2(x);
+  *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(v.x, v.y);
+}
+
+__device__ __forceinline__ float2 turned(const NormRopeParams& p, long long at, int pair) {  // (cos, sin) * magnitude
+  const long long phase = (long long)((unsigned long long)at * p.turns[pair]);
+  float s, c;
+  sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
+  return make_float2(c * p.magnitude, s * p.magnitude);
+}
+__device__ __forceinline__ long long position(const NormRopeParams& p, int token, int b, int t) {
+  return p.angles ? p.angles[token] : (long long)p.positions[b] + t;
+}
+
+constexpr int kWarps = 4;  // of a CTA, each with its own work
+
+// Warp x has slice x % slices of token x / slices: `per_slice` of the vectors, 32 / lanes
+// * U at a time, the next ones on their way while these are worked on. A lane turns its
+// item's pairs as
+//   (x, y) -> r (x (w_x cos, w_x sin) + y (-w_y sin, w_y cos)),   r = 1 / sqrt(mean + eps),
+// with the products of weights, cosines and sines in registers (elements past the
+// rotated part: cos 1, sin 0).
+template <typename T, int VE, bool HALF, int U>
+__global__ void __launch_bounds__(32 * kWarps, VE == 8 && HALF ? 6 : 8)
+    norm_rope_warp_kernel(const __grid_constant__ NormRopeParams p, int lanes, int slices, int per_slice) {
   using P = Piece<T, VE>;
   using I = Items<VE, HALF>;
-  constexpr int NP = I::kTwo ? VE : VE / 2;    // pairs of an item
-  constexpr int U = NI == 1 ? 2 : 1;           // vectors of a group in flight
-  __shared__ float2 turn[kMaxHalf];
-  const int b = blockIdx.x / p.tokens, t = blockIdx.x - b * p.tokens;
-  const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
-  const int heads = p.q_heads + p.kv_heads;
+  constexpr int NP = HALF ? VE : VE / 2;  // pairs of an item
+  __shared__ float2 turn[kWarps][32 * NP];
+  const unsigned warp = blockIdx.x * kWarps + threadIdx.x / 32;  // (up to 2^31 + 2)
+  if (warp / slices >= (unsigned)p.batch * p.tokens) return;
+  const int token = warp / slices, slice = warp - token * slices;
+  const int wl = threadIdx.x % 32, lane = wl & (lanes - 1), group = wl / lanes, groups = 32 / lanes;
   const I items(p.rot_dim, p.head_dim);
-  const T* const q = reinterpret_cast<const T*>(p.in[0].data) + b * p.in[0].sb + t * p.in[0].st;
-  const T* const k = reinterpret_cast<const T*>(p.in[1].data) + b * p.in[1].sb + t * p.in[1].st;
-  P x[U][NI], z[U][NI];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * groups;
-      if (h >= heads) continue;
-      const T* const from = h < p.q_heads ? q + h * p.in[0].sh : k + (h - p.q_heads) * p.in[1].sh;
-#pragma unroll
-      for (int n = 0; n < NI; ++n) {
-        const int i = lane + n * lanes;
-        if (i >= items.total) continue;
-        x[u][n] = *reinterpret_cast<const P*>(from + items.first(i, p.rot_dim));
-        if (I::kTwo && i < items.rotated) z[u][n] = *reinterpret_cast<const P*>(from + items.second(i, p.rot_dim));
-      }
-    }
-  };
+  const bool mine = lane < items.total, rotated = lane < items.rotated, two = HALF && rotated;
+  const int ea = items.first(lane, p.rot_dim), eb = items.second(lane, p.rot_dim);
+  const int b = token / p.tokens, t = token - b * p.tokens;
+  const float per = 1.f / p.head_dim;
+  float2* const mine_turn = turn[threadIdx.x / 32] + lane * NP;
+  bool turned_yet = false;
   pdl_wait();
   pdl_launch_dependents();
-  load(group);
-  if (p.turns) {
-    const long long at = p.angles ? p.angles[(size_t)b * p.tokens + t] : (long long)p.positions[b] + t;
-    for (int i = threadIdx.x; i < p.rot_dim / 2; i += blockDim.x) {
-      const long long phase = (long long)((unsigned long long)at * p.turns[i]);
-      float s, c;
-      sincospif(__ll2float_rn(phase) * 0x1p-63f, &s, &c);
-      turn[i] = make_float2(c * p.magnitude, s * p.magnitude);
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    // this slice's heads of q, then of k
+    const int before = kind ? p.q_heads : 0, heads = kind ? p.kv_heads : p.q_heads;
+    const int first = max(slice * per_slice - before, 0), last = min((slice + 1) * per_slice - before, heads);
+    if (first >= last) continue;
+    const long long in_step = kind ? p.in[1].sh : p.in[0].sh, out_step = kind ? p.out[1].sh : p.out[0].sh;
+    const T* const in = reinterpret_cast<const T*>(kind ? p.in[1].data : p.in[0].data) +
+                        (kind ? b * p.in[1].sb + t * p.in[1].st : b * p.in[0].sb + t * p.in[0].st) + ea;
+    T* const out = reinterpret_cast<T*>(kind ? p.out[1].data : p.out[0].data) +
+                   (kind ? b * p.out[1].sb + t * p.out[1].st : b * p.out[0].sb + t * p.out[0].st) + ea;
+    const T* const weight = reinterpret_cast<const T*>(kind ? p.weight[1] : p.weight[0]);
+    P x[U], z[U];
+    auto load = [&](int h0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * groups;
+        if (h >= last || !mine) continue;
+        const T* const from = in + h * in_step;
+        x[u] = *reinterpret_cast<const P*>(from);
+        if (two) z[u] = *reinterpret_cast<const P*>(from + (eb - ea));
+      }
+    };
+    load(first + group);
+    if (p.turns && !turned_yet) {  // group g computes pairs g, g + groups, ... of the lanes' items
+      turned_yet = true;
+      const long long at = position(p, token, b, t);
+      if (rotated)
+        for (int j = group; j < NP; j += groups) mine_turn[j] = turned(p, at, lane * NP + j);
+      __syncwarp();
     }
-    __syncthreads();
-  }
-  T* const q_out = reinterpret_cast<T*>(p.out[0].data) + b * p.out[0].sb + t * p.out[0].st;
-  T* const k_out = reinterpret_cast<T*>(p.out[1].data) + b * p.out[1].sb + t * p.out[1].st;
-  const float per = 1.f / p.head_dim;
-  for (int h0 = group; h0 - group < heads; h0 += groups * U) {  // (whole warps: the shuffles)
-    if (h0 != group) load(h0);
-    float sum[U];
+    // of pairs (HALF: two at a time, (x, y) being the pieces' elements)
+    uint64_t cx[VE / 2], sx[HALF ? VE / 2 : 1], sy[VE / 2], cy[HALF ? VE / 2 : 1];
+    {
+      P wa, wb;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      sum[u] = 0.f;
+      for (int j = 0; j < VE; ++j) wa.e[j] = wb.e[j] = rounded_to<T>(1.f);
+      if (weight && mine) {
+        wa = *reinterpret_cast<const P*>(weight + ea);
+        if (two) wb = *reinterpret_cast<const P*>(weight + eb);
+      }
+      const float offset = weight ? p.weight_offset : 0.f;
 #pragma unroll
-      for (int n = 0; n < NI; ++n) {
-        const int i = lane + n * lanes;
-        if (i >= items.total || h0 + u * groups >= heads) continue;
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          const float v = value_of(x[u][n].e[j]);
-          sum[u] = fmaf(v, v, sum[u]);
+      for (int j = 0; j < VE / 2; ++j) {
+        const float a0 = value_of(wa.e[2 * j]) + offset, a1 = value_of(wa.e[2 * j + 1]) + offset;
+        if (HALF) {
+          const float b0 = value_of(wb.e[2 * j]) + offset, b1 = value_of(wb.e[2 * j + 1]) + offset;
+          const float2 u = rotated ? mine_turn[(2 * j) % NP] : make_float2(1.f, 0.f);
+          const float2 v = rotated ? mine_turn[(2 * j + 1) % NP] : make_float2(1.f, 0.f);
+          cx[j] = pack2(a0 * u.x, a1 * v.x);
+          sx[j % (HALF ? VE / 2 : 1)] = pack2(a0 * u.y, a1 * v.y);
+          sy[j] = pack2(-b0 * u.y, -b1 * v.y);
+          cy[j % (HALF ? VE / 2 : 1)] = pack2(b0 * u.x, b1 * v.x);
+        } else {
+          const float2 u = rotated ? mine_turn[j % NP] : make_float2(1.f, 0.f);
+          cx[j] = pack2(a0 * u.x, a0 * u.y);
+          sy[j] = pack2(-a1 * u.y, a1 * u.x);
         }
-        if (I::kTwo && i < items.rotated)
-#pragma unroll
-          for (int j = 0; j < VE; ++j) {
-            const float v = value_of(z[u][n].e[j]);
-            sum[u] = fmaf(v, v, sum[u]);
-          }
       }
     }
-    for (int o = lanes / 2; o > 0; o >>= 1)
+    for (int h0 = first + group; h0 - group < last; h0 += groups * U) {  // (whole warps: the shuffles)
+      uint64_t va[U][VE / 2], vb[U][HALF ? VE / 2 : 1];
+      float sum[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+      for (int u = 0; u < U; ++u) {
+        uint64_t s2 = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + u * groups;
-      if (h >= heads) continue;
-      const bool is_q = h < p.q_heads;
-      const float r = 1.f / sqrtf(fmaf(sum[u], per, p.eps));
-      const T* const weight = reinterpret_cast<const T*>(p.weight[is_q ? 0 : 1]);
-      T* const to = is_q ? q_out + h * p.out[0].sh : k_out + (h - p.q_heads) * p.out[1].sh;
-#pragma unroll
-      for (int n = 0; n < NI; ++n) {
-        const int i = lane + n * lanes;
-        if (i >= items.total) continue;
-        const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
-        const bool rotated = i < items.rotated, two = I::kTwo && rotated;
-        P wa, wb;
-        if (weight) {
-          wa = *reinterpret_cast<const P*>(weight + ea);
-          if (two) wb = *reinterpret_cast<const P*>(weight + eb);
-        }
-        auto normed = [&](T e, T w) { return value_of(e) * r * (weight ? value_of(w) + p.weight_offset : 1.f); };
-        float ya[VE], yb[VE];
-#pragma unroll
-        for (int j = 0; j < VE; ++j) {
-          ya[j] = normed(x[u][n].e[j], wa.e[j]);
-          if (two) yb[j] = normed(z[u][n].e[j], wb.e[j]);
-        }
-        if (rotated)
-#pragma unroll
-          for (int j = 0; j < NP; ++j) {
-            const float2 cs = turn[i * NP + j];
-            float& a = I::kTwo ? ya[j] : ya[2 * j];
-            float& c = I::kTwo ? yb[j] : ya[(2 * j + 1) % VE];
-            const float a0 = a, c0 = c;
-            a = a0 * cs.x - c0 * cs.y;
-            c = a0 * cs.y + c0 * cs.x;
+        for (int j = 0; j < VE / 2; ++j) {
+          va[u][j] = mine ? two_of(&x[u].e[2 * j]) : 0;
+          s2 = fma2(va[u][j], va[u][j], s2);
+          if (HALF) {
+            uint64_t& y = vb[u][j % (HALF ? VE / 2 : 1)];
+            y = two ? two_of(&z[u].e[2 * j]) : 0;
+            s2 = fma2(y, y, s2);
           }
+        }
+        const float2 s = unpack2(s2);
+        sum[u] = s.x + s.y;
+      }
+      load(h0 + groups * U);
+      for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + u * groups;
+        if (h >= last || !mine) continue;
+        const float r = rsqrtf(fmaf(sum[u], per, p.eps));
+        const uint64_t r2 = pack2(r, r);
+        T* const to = out + h * out_step;
         P y;
 #pragma unroll
-        for (int j = 0; j < VE; ++j) y.e[j] = rounded_to<T>(ya[j]);
-        *reinterpret_cast<P*>(to + ea) = y;
-        if (two) {
+        for (int j = 0; j < VE / 2; ++j) {
+          if (HALF) {
+            put_two(&y.e[2 * j], mul2(r2, fma2(vb[u][j % (HALF ? VE / 2 : 1)], sy[j], mul2(va[u][j], cx[j]))));
+          } else {
+            const float2 v = unpack2(va[u][j]);
+            put_two(&y.e[2 * j], mul2(r2, fma2(pack2(v.y, v.y), sy[j], mul2(pack2(v.x, v.x), cx[j]))));
+          }
+        }
+        *reinterpret_cast<P*>(to) = y;
+        if (HALF && two) {
 #pragma unroll
-          for (int j = 0; j < VE; ++j) y.e[j] = rounded_to<T>(yb[j]);
-          *reinterpret_cast<P*>(to + eb) = y;
+          for (int j = 0; j < VE / 2; ++j)
+            put_two(&y.e[2 * j], mul2(r2, fma2(vb[u][j % (HALF ? VE / 2 : 1)], cy[j % (HALF ? VE / 2 : 1)],
+                                               mul2(va[u][j], sx[j % (HALF ? VE / 2 : 1)]))));
+          *reinterpret_cast<P*>(to + (eb - ea)) = y;
         }
       }
     }
   }
 }
 
+// NI items of a vector a lane, a token a CTA.
 template <typename T, int VE, bool HALF, int NI>
-cudaError_t launch_items(const NormRopeParams& p, int lanes, cudaStream_t s) {
-  constexpr int U = NI == 1 ? 2 : 1;
+__global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p, int lanes) {
+  using P = Piece<T, VE>;
+  using I = Items<VE, HALF>;
+  constexpr int NP = I::kTwo ? VE : VE / 2;    // pairs of an item
+  __shared__ float2 turn[kMaxHalf];
+  extern __shared__ __align__(16) float weights[];  // [q, k][head_dim], the offset added
+  const int b = blockIdx.x / p.tokens, t = blockIdx.x - b * p.tokens;
+  const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = blockDim.x / lanes;
   const int heads = p.q_heads + p.kv_heads;
-  const int want = ((heads + U - 1) / U * lanes + 31) / 32 * 32;
+  const I items(p.rot_dim, p.head_dim);
+  P x[NI], z[NI];
+  auto load = [&](int h) {
+    if (h >= heads) return;
+    const bool is_q = h < p.q_heads;
+    const RopeView& in = p.in[is_q ? 0 : 1];
+    const T* const from = reinterpret_cast<const T*>(in.data) + b * in.sb + t * in.st + (is_q ? h : h - p.q_heads) * in.sh;
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+      const int i = lane + n * lanes;
+      if (i >= items.total) continue;
+      x[n] = *reinterpret_cast<const P*>(from + items.first(i, p.rot_dim));
+      if (I::kTwo && i < items.rotated) z[n] = *reinterpret_cast<const P*>(from + items.second(i, p.rot_dim));
+    }
+  };
+  pdl_wait();
+  pdl_launch_dependents();
+  load(group);
+  if (p.turns) {
+    const long long at = position(p, blockIdx.x, b, t);
+    for (int i = threadIdx.x; i < p.rot_dim / 2; i += blockDim.x) turn[i] = turned(p, at, i);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k == 0 ? p.q_heads : p.kv_heads)
+      for (int i = threadIdx.x; i < p.head_dim; i += blockDim.x)
+        weights[k * p.head_dim + i] =
+            p.weight[k] ? value_of(reinterpret_cast<const T*>(p.weight[k])[i]) + p.weight_offset : 1.f;
+  __syncthreads();
+  const float per = 1.f / p.head_dim;
+  for (int h = group; h - group < heads; h += groups) {  // (whole warps: the shuffles)
+    if (h != group) load(h);
+    float sum = 0.f;
+    if (h < heads)
+#pragma unroll
+      for (int n = 0; n < NI; ++n) {
+        const int i = lane + n * lanes;
+        if (i >= items.total) continue;
+#pragma unroll
+        for (int j = 0; j < VE; ++j) {
+          const float v = value_of(x[n].e[j]);
+          sum = fmaf(v, v, sum);
+        }
+        if (I::kTwo && i < items.rotated)
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float v = value_of(z[n].e[j]);
+            sum = fmaf(v, v, sum);
+          }
+      }
+    for (int o = lanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (h >= heads) continue;
+    const bool is_q = h < p.q_heads;
+    const float r = 1.f / sqrtf(fmaf(sum, per, p.eps));
+    const float* const weight = weights + (is_q ? 0 : p.head_dim);
+    const RopeView& out = p.out[is_q ? 0 : 1];
+    T* const to = reinterpret_cast<T*>(out.data) + b * out.sb + t * out.st + (is_q ? h : h - p.q_heads) * out.sh;
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+      const int i = lane + n * lanes;
+      if (i >= items.total) continue;
+      const int ea = items.first(i, p.rot_dim), eb = items.second(i, p.rot_dim);
+      const bool rotated = i < items.rotated, two = I::kTwo && rotated;
+      float ya[VE], yb[VE];
+#pragma unroll
+      for (int j = 0; j < VE; ++j) {
+        ya[j] = value_of(x[n].e[j]) * (r * weight[ea + j]);
+        yb[j] = two ? value_of(z[n].e[j]) * (r * weight[eb + j]) : 0.f;
+      }
+      if (rotated)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const float2 cs = turn[i * NP + j];
+          float& a = I::kTwo ? ya[j] : ya[2 * j];
+          float& c = I::kTwo ? yb[j] : ya[(2 * j + 1) % VE];
+          const float a0 = a, c0 = c;
+          a = a0 * cs.x - c0 * cs.y;
+          c = a0 * cs.y + c0 * cs.x;
+        }
+      P y;
+#pragma unroll
+      for (int j = 0; j < VE; ++j) y.e[j] = rounded_to<T>(ya[j]);
+      *reinterpret_cast<P*>(to + ea) = y;
+      if (two) {
+#pragma unroll
+        for (int j = 0; j < VE; ++j) y.e[j] = rounded_to<T>(yb[j]);
+        *reinterpret_cast<P*>(to + eb) = y;
+      }
+    }
+  }
+}
+
+template <typename... Args>
+cudaError_t launch_pdl(void (*kernel)(Args...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.batch * p.tokens);
-  cfg.blockDim = dim3(want < kNormThreads ? want : kNormThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<T, VE, HALF, NI>, p, lanes);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int VE, bool HALF, int NI>
+cudaError_t launch_items(const NormRopeParams& p, int lanes, cudaStream_t s) {
+  const int want = ((p.q_heads + p.kv_heads) * lanes + 31) / 32 * 32;
+  return launch_pdl(norm_rope_kernel<T, VE, HALF, NI>, (unsigned)p.batch * p.tokens, want < kNormThreads ? want : kNormThreads,
+                    2 * sizeof(float) * p.head_dim, s, p, lanes);
+}
+
+template <typename T, int VE, bool HALF>
+cudaError_t launch_warps(const NormRopeParams& p, int lanes, cudaStream_t s) {
+  // 16 bytes of 16-bit pairs take twice the registers: two vectors in flight a lane spill (4 x 4096
+  // tokens of 32 + 8 heads of 128 90 us, with one 66); fp32 (half of 3 x 2047 tokens of 32 heads of 96) 33 and 41.
+  constexpr int U = VE == 8 && HALF ? 1 : 2;
+  const int heads = p.q_heads + p.kv_heads, tokens = p.batch * p.tokens, step = 32 / lanes * U;
+  const int rounds = (heads + step - 1) / step;
+  int slices = (kManyWarps + tokens - 1) / tokens;
+  if (slices > rounds) slices = rounds;
+  const int per_slice = (rounds + slices - 1) / slices * step;
+  slices = (heads + per_slice - 1) / per_slice;
+  const long long warps = (long long)tokens * slices;
+  return launch_pdl(norm_rope_warp_kernel<T, VE, HALF, U>, (unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, 0, s, p,
+                    lanes, slices, per_slice);
 }
 
 template <typename T, int VE, bool HALF>
@@ -192,9 +379,15 @@ cudaError_t launch_style(const NormRopeParams& p, cudaStream_t s) {
   const int items = Items<VE, HALF>(p.rot_dim, p.head_dim).total;
   int lanes = 1;
   while (lanes < 32 && lanes < items) lanes *= 2;
-  if (items <= 32) return launch_items<T, VE, HALF, 1>(p, lanes, s);
-  if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
-  return launch_items<T, VE, HALF, VE == 1 ? 32 : 8>(p, lanes, s);  // head_dim is 1024 at most
+  if constexpr (VE > 1) {
+    if (items <= 32) return launch_warps<T, VE, HALF>(p, lanes, s);
+    if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
+    return launch_items<T, VE, HALF, 8>(p, lanes, s);  // head_dim is 1024 at most
+  } else {
+    if (items <= 32) return launch_items<T, VE, HALF, 1>(p, lanes, s);
+    if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
+    return launch_items<T, VE, HALF, 32>(p, lanes, s);
+  }
 }
 
 template <typename T>
