@@ -57,7 +57,7 @@ struct alignas(16) TreeSplit {
   int first, last;  // shares of the unit's segments; last -1: nothing to merge
   int count;  // nodes of its row
   int rows;   // live (head, node) rows
-  long long out;  // row of q and out of its row 0
+  long long out;  // row of q and out of its row 0 (compact: of the kv head's)
   int row0;       // (head, node) row 0 of the unit
   int pad;
 };
@@ -85,6 +85,7 @@ struct TreeParams {
   int nctas;                    // the tiles of all units in contiguous equal shares
   int extra;                    // tiles that a unit's begin and end cost besides
   int by_unit;                  // 1: few units, each cut into many segments; the merge goes by units
+  int compact;                  // 1: a row's live (head, node) rows only, r = head * count + node; else r = head * nodes + node
 };
 // Few units of many segments are merged by units, 8 rows a CTA, while those CTAs
 // are one wave; else by shares. Measured (bf16, 8 kv heads, 4000 tokens; by units /

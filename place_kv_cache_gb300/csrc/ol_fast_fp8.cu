@@ -1,8 +1,8 @@
 // ol_fast_fp8.cu -- attention over an E4M3 cache on the 5th generation tensor
 // cores: bf16 queries, head_dim 64 or 128, contiguous cache or paged pool.
 //
-// A unit is NC = 8, 16 or 32 (head, query) columns c = head * new_len + query of one
-// row's kv head. Its tokens form tiles of 128; equal contiguous shares of all
+// A unit is NC = 8, 16 or 32 (head, query) columns c = head * count + query of one
+// row's kv head (queries that the row has not take no part). Its tokens form tiles of 128; equal contiguous shares of all
 // units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh): while one ends a
 // segment or waits, the other has the SM. K and V go to the tensor cores as they lie
 // in the cache, with the tokens (for V the dimensions) as the products' 128 rows, so
@@ -23,7 +23,8 @@
 //
 // Warps: 0 the walk and the producer (TMA, a lane per box of a tile), 1 MMA issue (and
 // zeros for V's rows outside the row's tokens: P = 0 times a NaN code must not be NaN),
-// 2 the tiles' scales, 3 the queries' parts, 4-7 the softmax. The others learn of the
+// 2 the tiles' scales, 3 the queries' parts, 4-7 the softmax; of 32 columns in two groups
+// of four warps, 16 columns each (more warps to hide each other's latencies). The others learn of the
 // segments from the first, through a ring: the walk in line in each of them, and the
 // loops of waits (wait_long), made the kernel outgrow the instruction cache.
 #include "ol_fp8.cuh"
@@ -33,7 +34,8 @@ namespace ol {
 namespace {
 
 constexpr int kTile = 1 << kTreeFastTileLog2;
-constexpr int kThreads = 256;
+constexpr int groups_of(int NC) { return NC == 32 ? 2 : 1; }  // of softmax warps
+constexpr int threads_of(int NC) { return 128 + 128 * groups_of(NC); }
 constexpr int kScales = 8;        // tiles whose scales are known ahead
 constexpr int kSegs = 8;          // segments known ahead
 constexpr float kTop = 5.f;       // log2 of the largest P when a reference is set
@@ -48,20 +50,21 @@ struct Lay {
   static constexpr int kQ = 0;                          // two buffers
   static constexpr int kP = kQ + 2 * kQBytes;
   static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn
-  static constexpr int kSmall = 1536 + NC * 96;          // what follows the ring, at most
+  static constexpr int kSmall = 1536 + NC * 112;          // what follows the ring, at most
   static constexpr int kFit = (kMostSmem - kSmall - kRing) / kTileBytes;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
-  static constexpr int kCols = kRing + kSlots * kTileBytes;   // float2 [2 buffers][NC]: q's inverse factor, query index
-  static constexpr int kTab = kCols + 2 * NC * 8;             // [4 warps][NC / 2]: that factor of two columns, minus their references
-  static constexpr int kTops = kTab + 4 * NC * 8;             // float [4 warps][NC]: maxima
-  static constexpr int kSums = kTops + 4 * NC * 4;            // float [4 warps][NC]: l
-  static constexpr int kGrow = kSums + 4 * NC * 4;            // float [4 warps][NC]: what O is multiplied by
+  static constexpr int kGroups = groups_of(NC), kMine = NC / kGroups;  // columns of a group
+  static constexpr int kCols = kRing + kSlots * kTileBytes;   // Col [2 buffers][NC]
+  static constexpr int kTab = kCols + 2 * NC * 16;            // [warps][kMine / 2]: q's inverse factor of two columns, minus their references
+  static constexpr int kTops = kTab + 4 * NC * 8;             // float [warps][kMine]: maxima
+  static constexpr int kSums = kTops + 4 * NC * 4;            // float [warps][kMine]: l
+  static constexpr int kGrow = kSums + 4 * NC * 4;            // float [warps][kMine]: what O is multiplied by
   static constexpr int kSc = kGrow + 4 * NC * 4;              // float [kScales][2 planes][8 blocks]
   static constexpr int kSeg = kSc + kScales * 16 * 4;         // Seg [kSegs]
-  static constexpr int kFlag = kSeg + kSegs * 48;             // uint32 [2]
+  static constexpr int kFlag = kSeg + kSegs * 48;             // uint32 [groups][2]
   static constexpr int kBars = kFlag + 16;
-  // slots full, empty; q full, empty [2]; s full, free [2]; P ready, taken, vote, drain; scales and segments full, empty
-  static constexpr int kNumBars = 2 * kSlots + 4 + 4 + 4 + 2 * kScales + 2 * kSegs;
+  // slots full, empty; q full, empty [2]; s full, free [2]; P ready, taken, votes, drain; scales and segments full, empty
+  static constexpr int kNumBars = 2 * kSlots + 4 + 4 + 5 + 2 * kScales + 2 * kSegs;
   static constexpr int kMisc = kBars + kNumBars * 8;          // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 8;
   static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of two CTAs");
@@ -96,16 +99,12 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 #define OL_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
-#define OL_R16(x, i) OL_R4(x, i), OL_R4(x, i + 4), OL_R4(x, i + 8), OL_R4(x, i + 12)
 #define OL_U4(x, i) "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3])
-#define OL_U16(x, i) OL_U4(x, i), OL_U4(x, i + 4), OL_U4(x, i + 8), OL_U4(x, i + 12)
 #define OL_W4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : OL_R16(x, 0)
-      : "r"(addr));
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t* x) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : OL_R4(x, 0), OL_R4(x, 4)
+               : "r"(addr));
 }
 __device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t* x) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : OL_R4(x, 0) : "r"(addr));
@@ -114,8 +113,8 @@ __device__ __forceinline__ void tmem_st4(uint32_t addr, const uint32_t* x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), OL_W4(x, 0) : "memory");
 }
 // Waits for the loads; x are registers that a load fills (so that no use of them moves ahead of the wait).
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t* x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U16(x, 0)::"memory");
+__device__ __forceinline__ void tmem_wait_ld8(uint32_t* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U4(x, 0), OL_U4(x, 4)::"memory");
 }
 __device__ __forceinline__ void tmem_wait_ld4(uint32_t* x) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : OL_U4(x, 0)::"memory");
@@ -181,12 +180,12 @@ struct Bars {
   __device__ uint32_t s_free(int i) const { return q_full(6 + i); }  // S is in registers
   __device__ uint32_t p_ready() const { return q_full(8); }
   __device__ uint32_t p_taken() const { return q_full(9); }          // the products with P are done
-  __device__ uint32_t vote() const { return q_full(10); }
-  __device__ uint32_t drain() const { return q_full(11); }
-  __device__ uint32_t sc_full(int i) const { return q_full(12 + i); }
-  __device__ uint32_t sc_empty(int i) const { return q_full(12 + kScales + i); }
-  __device__ uint32_t seg_full(int i) const { return q_full(12 + 2 * kScales + i); }
-  __device__ uint32_t seg_empty(int i) const { return q_full(12 + 2 * kScales + kSegs + i); }
+  __device__ uint32_t vote(int group) const { return q_full(10 + group); }
+  __device__ uint32_t drain() const { return q_full(12); }
+  __device__ uint32_t sc_full(int i) const { return q_full(13 + i); }
+  __device__ uint32_t sc_empty(int i) const { return q_full(13 + kScales + i); }
+  __device__ uint32_t seg_full(int i) const { return q_full(13 + 2 * kScales + i); }
+  __device__ uint32_t seg_empty(int i) const { return q_full(13 + 2 * kScales + kSegs + i); }
 };
 
 // A place in a ring of N, and the parity of its lap.
@@ -200,6 +199,12 @@ struct Cursor {
       phase ^= 1;
     }
   }
+};
+
+// A column: q's inverse factor, its query, its row of out counted from the kv head's first.
+struct alignas(16) Col {
+  float factor;
+  int query, row, pad;
 };
 
 // A segment as the roles see it: tiles [0, tiles) of 128 tokens from token t0 on, of
@@ -277,9 +282,10 @@ __device__ __forceinline__ void four_parts(uint64_t w, uint32_t (&part)[4]) {
 }
 
 template <int D, int NC, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
+__global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
                                                                const __grid_constant__ Fp8AttnParams fp, const int box) {
   using L = Lay<D, NC>;
+  constexpr int kWarps = 4 * L::kGroups;  // of the softmax
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = fp.t;
   const Fp8Cache& fc = fp.cache;
@@ -300,25 +306,26 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.q_full(i), 1);
-      mbar_init(bar.q_empty(i), 5);  // the products' and the softmax warps'
+      mbar_init(bar.q_empty(i), 1 + kWarps);  // the products' and the softmax warps'
       mbar_init(bar.s_full(i), 1);
-      mbar_init(bar.s_free(i), 4);
+      mbar_init(bar.s_free(i), kWarps);
     }
-    mbar_init(bar.p_ready(), 4);
+    mbar_init(bar.p_ready(), kWarps);
     mbar_init(bar.p_taken(), 1);
-    mbar_init(bar.vote(), 4);
+    mbar_init(bar.vote(0), 4);
+    mbar_init(bar.vote(1), 4);
     mbar_init(bar.drain(), 1);
     for (int i = 0; i < kScales; ++i) {
       mbar_init(bar.sc_full(i), 32);  // a lane's copies
-      mbar_init(bar.sc_empty(i), 4);
+      mbar_init(bar.sc_empty(i), kWarps);
     }
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(bar.seg_full(i), 1);
-      mbar_init(bar.seg_empty(i), 7);  // all warps but the producer
+      mbar_init(bar.seg_empty(i), 3 + kWarps);  // all warps but the producer
     }
     fence_mbar_init();
     *reinterpret_cast<volatile uint32_t*>(smem + L::kMisc + 4) = 0;
-    for (int i = 0; i < 2; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(smem + L::kFlag)[i] = 0;
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(sa + L::kMisc), "n"(L::kTmem)
@@ -603,21 +610,22 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
     // ------------------------------------------------------------ queries' parts
     // Q': rows [part][column] of D bytes, swizzled. Four lanes have a column, E elements each.
     constexpr int E = D / 4;
-    const int R = p.group * p.nodes, part = lane & 3;
+    const int part = lane & 3;
     uint32_t seg = 0;
     bool ok = true;
     Seg g;
     while (next_seg(g, ok)) {
-      const int buf = seg & 1, r0 = g.qg * NC;
+      const int buf = seg & 1, r0 = g.qg * NC, R = p.group * g.count;
       uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
-      float2* const cols = reinterpret_cast<float2*>(smem + L::kCols) + buf * NC;
+      Col* const cols = reinterpret_cast<Col*>(smem + L::kCols) + buf * NC;
       const uint4* const q =
-          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, r0) * D) + part * (E / 8);
+          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * D) + part * (E / 8);
 #pragma unroll 1
       for (int c = lane >> 2; c < NC; c += 8) {
+        const int head = (r0 + c) / g.count, query = r0 + c - head * g.count, live = head * p.nodes + query;
         uint4 x[E / 8];
 #pragma unroll
-        for (int e = 0; e < E / 8; ++e) x[e] = r0 + c < R ? q[c * (D / 8) + e] : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < E / 8; ++e) x[e] = r0 + c < R ? q[(size_t)live * (D / 8) + e] : make_uint4(0, 0, 0, 0);
         if (c < 8 && !(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
         uint32_t top = 0;
 #pragma unroll
@@ -650,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
           *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(at + NC * D) = make_uint2(lo[0], lo[1]);
         }
-        if (part == 0) cols[c] = make_float2(1.f / factor, __int_as_float((r0 + c) % p.nodes));
+        if (part == 0) cols[c] = Col{1.f / factor, query, live, 0};
       }
       if (!ok) break;
       fence_proxy_async_smem();
@@ -659,43 +667,44 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
     }
   } else {
     // ----------------------------------------------------------------- softmax
+    constexpr int kMine = L::kMine;
     const int me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of O
-    const uint32_t lanes = (uint32_t)(me * 32) << 16;
-    const uint32_t to = tmem + 4 * NC + lanes;  // O
-    float* const tab = reinterpret_cast<float*>(smem + L::kTab) + me * NC * 2;  // of two columns: factors, minus references
-    float* const mine = tab + lane % NC / 2 * 4 + lane % 2;
-    float* const tops = reinterpret_cast<float*>(smem + L::kTops);
-    float* const grow = reinterpret_cast<float*>(smem + L::kGrow) + me * NC;
-    float* const sums = reinterpret_cast<float*>(smem + L::kSums);
-    volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag);
+    const int group = me / 4, first = group * kMine;  // this group's columns
+    const uint32_t lanes = (uint32_t)(me % 4 * 32) << 16;
+    const uint32_t to = tmem + 4 * NC + first + lanes;  // O of these columns, the parts NC apart
+    float* const tab = reinterpret_cast<float*>(smem + L::kTab) + me * kMine * 2;  // of two columns: factors, minus references
+    float* const mine = tab + lane % kMine / 2 * 4 + lane % 2;
+    float* const tops = reinterpret_cast<float*>(smem + L::kTops) + group * 4 * kMine;
+    float* const grow = reinterpret_cast<float*>(smem + L::kGrow) + me * kMine;
+    float* const sums = reinterpret_cast<float*>(smem + L::kSums) + group * 4 * kMine;
+    volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag) + group * 2;
     constexpr int kSwBits = NC == 32 ? 7 : NC == 16 ? 3 : 1, kSwShift = NC == 32 ? 0 : NC == 16 ? 1 : 2;
     uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP) + row * (NC / 4);
     const int p_sw = row >> kSwShift & kSwBits;  // the swizzle of this row's chunks
-    constexpr int kPart = NC < 16 ? NC : 16;     // columns at a time
-    const int R = p.group * p.nodes;
+    constexpr int kStep = 8;                     // columns whose scores are looked at at a time
     Cursor<kScales> sc;
     uint32_t count = 0;  // of tiles
     uint32_t votes = 0, seg = 0;
     bool ok = true;
     auto vote = [&] {
-      warp_arrive(bar.vote());
-      return warp_wait(bar.vote(), votes++ & 1, abort, p.status);
+      warp_arrive(bar.vote(group));
+      return warp_wait(bar.vote(group), votes++ & 1, abort, p.status);
     };
     Seg g;
     while (next_seg(g, ok)) {
       const int buf = seg & 1;
       if (!(ok = warp_wait(bar.q_full(buf), seg >> 1 & 1, abort, p.status))) break;
       ++seg;
-      const float2* const cols = reinterpret_cast<const float2*>(smem + L::kCols) + buf * NC;
-      if (lane < NC) {
-        mine[0] = cols[lane].x;
+      const Col* const cols = reinterpret_cast<const Col*>(smem + L::kCols) + buf * NC + first;
+      if (lane < kMine) {
+        mine[0] = cols[lane].factor;
         mine[2] = INFINITY;  // no reference
       }
       __syncwarp();
       const int low_all = all_low(p.window, g.len);
-      uint64_t l[NC / 2];  // of two columns
+      uint64_t l[kMine / 2];  // of two columns
 #pragma unroll
-      for (int c = 0; c < NC / 2; ++c) l[c] = 0;
+      for (int c = 0; c < kMine / 2; ++c) l[c] = 0;
       for (int i = 0; i < g.tiles; ++i, sc.next()) {
         const int t0 = g.t0 + i * kTile;
         if (!(ok = warp_wait(bar.sc_full(sc.slot), sc.phase, abort, p.status))) break;
@@ -706,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
         const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
         warp_arrive(bar.sc_empty(sc.slot));
         const float v_log2 = __log2f(v_scale), v_inv = v_scale == v_scale ? __frcp_rn(v_scale) : 1.f;
-        const uint32_t ts = tmem + (count & 1) * 2 * NC + lanes;
+        const uint32_t ts = tmem + (count & 1) * 2 * NC + first + lanes;
         if (!(ok = warp_wait(bar.s_full(count & 1), count >> 1 & 1, abort, p.status))) break;
         ++count;
         tmem_fence_after();
@@ -714,46 +723,46 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
         if (t0 + kTile - 1 > g.prefix || t0 < low_all) {
           const int t = t0 + row;
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            const int at = g.prefix + min(__float_as_int(cols[c].y), g.count - 1);
+          for (int c = 0; c < kMine; ++c) {
+            const int at = g.prefix + cols[c].query;
             if (t > at || (p.window >= 0 && t < at - p.window)) hidden |= 1u << c;
           }
         }
         const bool edge = __any_sync(0xffffffffu, hidden != 0);
-        float y[NC];
+        float y[kMine];
         for (bool looked = false;;) {
           const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
-          for (int c0 = 0; c0 < NC; c0 += kPart) {
-            uint32_t s[2 * kPart];
-            tmem_ld16(ts + c0, s);
-            if (NC > 8) tmem_ld16(ts + NC + c0, s + 16 % (2 * kPart));
-            tmem_wait_ld16(s);
-            if (NC > 8) tmem_wait_ld16(s + 16 % (2 * kPart));
+          for (int c0 = 0; c0 < kMine; c0 += kStep) {
+            uint32_t hi[kStep], lo[kStep];
+            tmem_ld8(ts + c0, hi);
+            tmem_ld8(ts + NC + c0, lo);
+            tmem_wait_ld8(hi);
+            tmem_wait_ld8(lo);
 #pragma unroll
-            for (int c = 0; c < kPart; c += 2) {
+            for (int c = 0; c < kStep; c += 2) {
               const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(tab + (c0 + c) * 2);
-              const uint64_t hi = pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-              const uint64_t lo = pack2(__uint_as_float(s[kPart + c]), __uint_as_float(s[kPart + c + 1]));
-              const float2 z = unpack2(fma2(mul2(fma2(lo, part2, hi), k2), f.x, add2(v2, f.y)));
+              const uint64_t s0 = pack2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1]));
+              const uint64_t s1 = pack2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1]));
+              const float2 z = unpack2(fma2(mul2(fma2(s1, part2, s0), k2), f.x, add2(v2, f.y)));
               y[c0 + c] = z.x;
               y[c0 + c + 1] = z.y;
             }
           }
           if (edge)
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
+            for (int c = 0; c < kMine; ++c)
               if (hidden >> c & 1) y[c] = -INFINITY;
           if (looked) break;
           float most = y[0];
 #pragma unroll
-          for (int c = 1; c < NC; ++c) most = fmaxf(most, y[c]);
+          for (int c = 1; c < kMine; ++c) most = fmaxf(most, y[c]);
           // (the flag holds the number of the tile that raised it)
           if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
           if (!(ok = vote()) || flag[count & 1] != count) break;
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
 #pragma unroll 1
-          for (int c = 0; c < NC; c += 4) {
+          for (int c = 0; c < kMine; c += 4) {
             uint32_t hi[4], lo[4];
             tmem_ld4(ts + c, hi);
             tmem_ld4(ts + NC + c, lo);
@@ -762,34 +771,35 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float x = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k])) * k_scale;
-              const float raw = fmaf(x, cols[c + k].x, v_log2);
+              const float raw = fmaf(x, cols[c + k].factor, v_log2);
               const float top = warp_max(hidden >> (c + k) & 1 ? -INFINITY : fmaxf(raw, -INFINITY));  // (a NaN is no maximum)
-              if (lane == 0) tops[me * NC + c + k] = top;
+              if (lane == 0) tops[me % 4 * kMine + c + k] = top;
             }
           }
           if (!(ok = vote())) break;
-          if (lane < NC) {
+          if (lane < kMine) {
             float top = tops[lane];
 #pragma unroll
-            for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[x * NC + lane]);
+            for (int x = 1; x < 4; ++x) top = fmaxf(top, tops[x * kMine + lane]);
             const float old = mine[2], minus = fminf(old, kTop - top);  // the references only rise
             mine[2] = minus;
             grow[lane] = old == INFINITY ? 0.f : exp2f(minus - old);
           }
           __syncwarp();
 #pragma unroll
-          for (int c = 0; c < NC / 2; ++c) l[c] = mul2(l[c], reinterpret_cast<const uint64_t*>(grow)[c]);
+          for (int c = 0; c < kMine / 2; ++c) l[c] = mul2(l[c], reinterpret_cast<const uint64_t*>(grow)[c]);
           if (i > 0) {  // what the segment's earlier tiles have summed up
             if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;
             tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < 4 * NC; x += 4) {
+            for (int x = 0; x < 4 * kMine; x += 4) {
+              const int part = x / kMine, c = x - part * kMine;
               uint32_t o[4];
-              tmem_ld4(to + x, o);
+              tmem_ld4(to + part * NC + c, o);
               tmem_wait_ld4(o);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * grow[(x + k) % NC]);
-              tmem_st4(to + x, o);
+              for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * grow[c + k]);
+              tmem_st4(to + part * NC + c, o);
             }
             tmem_wait_st();
           }
@@ -799,34 +809,29 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
         tmem_fence_before();
         warp_arrive(bar.s_free(count + 1 & 1));
         const uint64_t inv2 = pack2(v_inv, v_inv);
+        uint32_t z[4][kMine / 4];  // P' of this row: parts, a byte a column
 #pragma unroll
-        for (int c0 = 0; c0 < NC; c0 += kPart) {
-          uint32_t z[4][kPart / 4];  // P' of this row: parts, a byte a column
+        for (int c = 0; c < kMine; c += 4) {
+          uint32_t part[2][4];
 #pragma unroll
-          for (int c = 0; c < kPart; c += 4) {
-            uint32_t part[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int x = c0 + c + 2 * h;
-              const uint64_t w2 = pack2(fast_exp2(y[x]), fast_exp2(y[x + 1]));
-              l[x / 2] = fma2(w2, inv2, l[x / 2]);
-              four_parts(w2, part[h]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
+          for (int h = 0; h < 2; ++h) {
+            const int x = c + 2 * h;
+            const uint64_t w2 = pack2(fast_exp2(y[x]), fast_exp2(y[x + 1]));
+            l[x / 2] = fma2(w2, inv2, l[x / 2]);
+            four_parts(w2, part[h]);
           }
-          if (c0 == 0 && !(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;  // the last P is read
-          if (NC == 8) {
-            p_row[0 ^ p_sw] = make_uint4(z[0][0], z[0][1], z[1][0], z[1][1]);
-            p_row[1 ^ p_sw] = make_uint4(z[2][0], z[2][1], z[3][0], z[3][1]);
-          } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              p_row[(k * (NC / 16) + c0 / 16) ^ p_sw] =
-                  make_uint4(z[k][0], z[k][1], z[k][2 % (kPart / 4)], z[k][3 % (kPart / 4)]);
-          }
+          for (int k = 0; k < 4; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
         }
-        if (!ok) break;
+        if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;  // the last P is read
+        if constexpr (kMine == 8) {
+          p_row[0 ^ p_sw] = make_uint4(z[0][0], z[0][1], z[1][0], z[1][1]);
+          p_row[1 ^ p_sw] = make_uint4(z[2][0], z[2][1], z[3][0], z[3][1]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            p_row[(k * (NC / 16) + group) ^ p_sw] = make_uint4(z[k][0], z[k][1], z[k][2], z[k][3]);
+        }
         fence_proxy_async_smem();
         tmem_fence_before();
         warp_arrive(bar.p_ready());
@@ -835,15 +840,15 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
 
       // The segment's state. l over the warp's lanes: a step halves the columns that a
       // lane holds, then the lanes of a column are summed.
-      float t[NC];
+      float t[kMine];
 #pragma unroll
-      for (int c = 0; c < NC; c += 2) {
+      for (int c = 0; c < kMine; c += 2) {
         const float2 x = unpack2(l[c / 2]);
         t[c] = x.x;
         t[c + 1] = x.y;
       }
 #pragma unroll
-      for (int n = NC / 2, o = 16; n > 0; n /= 2, o /= 2) {
+      for (int n = kMine / 2, o = 16; n > 0; n /= 2, o /= 2) {
         const bool up = lane & o;
 #pragma unroll
         for (int c = 0; c < n; ++c) {
@@ -852,17 +857,17 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
         }
       }
 #pragma unroll
-      for (int o = 16 / NC; o > 0; o /= 2) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+      for (int o = 16 / kMine; o > 0; o /= 2) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
       // lane's column: its upper bits
-      if (lane % (32 / NC) == 0) sums[me * NC + lane / (32 / NC)] = t[0];
+      if (lane % (32 / kMine) == 0) sums[me % 4 * kMine + lane / (32 / kMine)] = t[0];
       if (!(ok = vote())) break;
       if (!(ok = warp_wait(bar.p_taken(), count + 1 & 1, abort, p.status))) break;
       tmem_fence_after();
       float* const slot = g.slot < 0 ? nullptr : tree_slot(p, g.slot);
-      const int r0 = g.qg * NC;
-      const size_t out = tree_out_row(p, g.b, g.g, r0) * D + row;
+      const int live = p.group * g.count - g.qg * NC - first;  // columns that there are
+      const size_t out = tree_out_row(p, g.b, g.g, 0) * D + row;
 #pragma unroll 1
-      for (int c0 = 0; c0 < NC && r0 + c0 < R; c0 += 4) {
+      for (int c0 = 0; c0 < kMine && c0 < live; c0 += 4) {
         uint32_t o[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld4(to + k * NC + c0, o[k]);
@@ -870,19 +875,19 @@ __global__ void __launch_bounds__(kThreads, 2) fast_fp8_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k) tmem_wait_ld4(o[k]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int col = c0 + c;
-          if (r0 + col >= R) continue;
-          const float total = sums[col] + sums[NC + col] + sums[2 * NC + col] + sums[3 * NC + col];
+          const int col = c0 + c, place = first + col;
+          if (col >= live) continue;
+          const float total = sums[col] + sums[kMine + col] + sums[2 * kMine + col] + sums[3 * kMine + col];
           const float sum = fmaf(fmaf(fmaf(__uint_as_float(o[3][c]), 0.0625f, __uint_as_float(o[2][c])), 0.0625f,
                                       __uint_as_float(o[1][c])), 0.0625f, __uint_as_float(o[0][c]));
           if (slot) {
             if (row == 0) {
-              slot[col] = -tab[col / 2 * 4 + 2 + col % 2];
-              slot[NC + col] = total;
+              slot[place] = -tab[col / 2 * 4 + 2 + col % 2];
+              slot[NC + place] = total;
             }
-            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + col) * 4 + row % 4] = sum;
-          } else if (row < D && __float_as_int(cols[col].y) < g.count) {
-            store_out(p.out, p.out_dtype, out + (size_t)col * D, total == 0.f ? 0.f : sum / total);
+            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
+          } else if (row < D) {
+            store_out(p.out, p.out_dtype, out + (size_t)cols[col].row * D, total == 0.f ? 0.f : sum / total);
           }
         }
       }
@@ -943,7 +948,7 @@ cudaError_t launch_cfg(const CUtensorMap& map, const Fp8AttnParams& p, int box, 
     return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(kern, dim3(p.t.nctas), dim3(kThreads), Lay<D, NC>::kTotal, s, map, p, box);
+  return launch_pdl(kern, dim3(p.t.nctas), dim3(threads_of(NC)), Lay<D, NC>::kTotal, s, map, p, box);
 }
 
 template <int D, bool PAGED>
@@ -974,6 +979,7 @@ void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   p.extra = 2;
+  p.compact = 1;
   p.by_unit = tree_few_units(p);
 }
 

@@ -259,8 +259,8 @@ cudaError_t launch_read_cfg(const Fp8ReadParams& p, cudaStream_t s) {
 
 // ------------------------------------------------------- attention, CUDA cores
 
-// A unit is 32 or 64 (head, query) rows of one row's kv head, its tokens form tiles
-// of 32; all units' tiles in equal shares, one per CTA (TreeWalk). Scores and sums
+// A unit is 32 or 64 (head, query) rows r = head * count + query of one row's kv head,
+// its tokens form tiles of 32; all units' tiles in equal shares, one per CTA (TreeWalk). Scores and sums
 // in registers: 4 rows x 2 tokens of S, 4 rows x D / 16 dimensions of O a thread. A
 // tile's codes come into registers while the tile before is worked on, and lie in
 // shared memory as fp32 values, their scales multiplied in.
@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(4 * RB) fp8_attention_kernel(const __grid_cons
   float* const sk = sq + RB * Dp;
   float* const sv = sk + TB * Dp;
   const int tid = threadIdx.x, rg = tid / 16, cg = tid % 16;
-  const int R = p.group * p.nodes;
   pdl_wait();
   pdl_launch_dependents();
   TreeWalk w(p);
@@ -292,7 +291,8 @@ __global__ void __launch_bounds__(4 * RB) fp8_attention_kernel(const __grid_cons
     notes.write_splits(p);
   }
   while (w.next(p)) {
-    const int r0 = w.qg * RB;
+    const int r0 = w.qg * RB, R = p.group * w.row.count;
+    const size_t base_row = tree_out_row(p, w.b, w.g, 0);  // of q and out
     const int low_all = p.window < 0 || w.row.prefix <= p.window ? 0 : w.row.prefix - p.window;
     uint4 code[kPieces];
     float scale[kPieces];
@@ -332,17 +332,19 @@ __global__ void __launch_bounds__(4 * RB) fp8_attention_kernel(const __grid_cons
       }
     };
     __syncthreads();  // the last segment's queries and tiles are read
-    for (int i = tid; i < RB * per_row * 16; i += kThreads) {
-      const int r = i / D, d = i - r * D;
-      sq[r * Dp + d] = r0 + r < R ? value_of<T>(reinterpret_cast<const T*>(p.q)[tree_out_row(p, w.b, w.g, r0 + r) * D + d])
-                                  : 0.f;
+    {
+      const int r = tid / 4;  // four threads a row
+      const T* const q = reinterpret_cast<const T*>(p.q) +
+                         (base_row + (r0 + r < R ? tree_live_row(p, w.row.count, r0 + r) : 0)) * D;
+      for (int d = tid % 4 * 4; d < D; d += 16)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sq[r * Dp + d + e] = r0 + r < R ? value_of<T>(q[d + e]) : 0.f;
     }
     fetch(w.tile0);
-    int node[4], at[4], low[4];
+    int at[4], low[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      node[r] = (r0 + 4 * rg + r) % p.nodes;
-      at[r] = w.row.prefix + min(node[r], w.row.count);
+      at[r] = w.row.prefix + (r0 + 4 * rg + r) % w.row.count;
       low[r] = p.window < 0 || at[r] <= p.window ? 0 : at[r] - p.window;
     }
     float m[4], l[4];
@@ -462,9 +464,9 @@ __global__ void __launch_bounds__(4 * RB) fp8_attention_kernel(const __grid_cons
           const int d4 = c * 16 + cg;
           if (d4 * 4 < D) reinterpret_cast<float4*>(slot + 2 * RB)[d4 * RB + row] = o[r][c];
         }
-      } else if (node[r] < w.row.count) {
+      } else {
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-        const size_t out = tree_out_row(p, w.b, w.g, r0 + row) * D;
+        const size_t out = (base_row + tree_live_row(p, w.row.count, r0 + row)) * D;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int d = c * 64 + cg * 4;
@@ -527,6 +529,7 @@ void plan_generic_fp8(Fp8AttnParams& fp, int sms) {
   const int fit = (int)(228 * 1024 / (smem + 1024)), most = 128 / p.rows_per_unit;  // (the workspace's slots)
   p.nctas = (fit < most ? fit : most) * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   p.extra = 2;
+  p.compact = 1;
   p.by_unit = tree_few_units(p);
 }
 

@@ -330,13 +330,16 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   __shared__ float other_l[G > 1 ? (G - 1) * ROWS : 1];
   pdl_wait();
   pdl_launch_dependents();
-  if (p.by_unit && read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head)).ntiles == 0) return;  // no note
+  if (p.by_unit) {
+    const TreeRow row = read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head));
+    if (row.ntiles == 0 || (int)blockIdx.x % p.units_per_head >= tree_units(p, row)) return;  // no note
+  }
   const TreeSplit u = p.splits[blockIdx.x];
   if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
   const int RU = p.rows_per_unit, D = p.head_dim;
   const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS, d0 = lane % D4, grp = lane / D4;
   const int place = blockIdx.y * ROWS + lr;  // row of the unit
-  const bool mine = place < u.rows && (u.row0 + place) % p.nodes < u.count;
+  const bool mine = place < u.rows && (p.compact || (u.row0 + place) % p.nodes < u.count);
   const int segs = u.last - u.first + 1;
   auto slot_of = [&](int i) { return tree_slot(p, 2 * (u.first + i) + (i == 0)); };
   float M = -INFINITY, L = 0.f;
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   }
   if (!mine) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t out = (size_t)(u.out + place) * D;
+  const size_t out = (size_t)(u.out + (p.compact ? tree_live_row(p, u.count, u.row0 + place) : place)) * D;
 #pragma unroll
   for (int k = 0; k < KG; ++k) {
     const int d = (d0 + k * kLanes) * 4;

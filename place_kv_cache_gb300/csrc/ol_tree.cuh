@@ -111,6 +111,17 @@ __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
   return tree_row(n, c, p.window, p.tile_log2);
 }
 
+// Units of a row's kv head.
+__device__ __forceinline__ int tree_units(const TreeParams& p, const TreeRow& r) {
+  return p.compact ? (p.group * r.count + p.rows_per_unit - 1) / p.rows_per_unit : p.units_per_head;
+}
+// Row r of a kv head's, as its row of q and out counted from the kv head's first.
+__device__ __forceinline__ int tree_live_row(const TreeParams& p, int count, int r) {
+  if (!p.compact) return r;
+  const int head = r / count;
+  return head * p.nodes + (r - head * count);
+}
+
 // The tiles of all units, in the order (row, kv head, row group of the unit,
 // tile), each unit's behind `extra` tiles that stand for what a unit costs
 // besides, are cut into n = min(CTAs, T) contiguous shares, none of them empty, of
@@ -129,21 +140,24 @@ struct TreeWalk {
   int share, total;      // its first tile; all tiles
   int each, more;        // tiles of a share; shares of one more
   int v1;                // tiles of the unit, extra ones included, up to `at`
-  int first_nt;          // tiles of row `lane` of the first 32 rows
+  int first_nt;          // tiles of a kv head of row `lane` of the first 32 rows
 
   __device__ __forceinline__ static int tiles(const TreeParams& p, const TreeRow& r) {
     return r.ntiles > 0 ? r.ntiles + p.extra : 0;
+  }
+  __device__ __forceinline__ static int head_tiles(const TreeParams& p, const TreeRow& r) {
+    return tiles(p, r) * tree_units(p, r);
   }
 
   __device__ __forceinline__ explicit TreeWalk(const TreeParams& p) {
     const int lane = threadIdx.x & 31, c = blockIdx.x;
     total = 0;
     for (int base = 0; base < p.batch; base += 32) {
-      int nt = base + lane < p.batch ? tiles(p, read_tree_row(p, base + lane)) : 0;
+      int nt = base + lane < p.batch ? head_tiles(p, read_tree_row(p, base + lane)) : 0;
       if (base == 0) first_nt = nt;
       total += __reduce_add_sync(0xffffffffu, nt);
     }
-    total *= p.kv_heads * p.units_per_head;
+    total *= p.kv_heads;
     const int shares = min(total, (int)gridDim.x);
     at = end = share = each = more = tile0 = tile1 = slot = 0;
     if (c < shares) {
@@ -158,11 +172,11 @@ struct TreeWalk {
   // Finds the unit of tile x (x < total); returns the tile's index in it.
   __device__ __forceinline__ int locate(const TreeParams& p, int x) {
     const int lane = threadIdx.x & 31;
-    const int per_row = p.kv_heads * p.units_per_head;
+    const int per_row = p.kv_heads;
     b = g = qg = 0;
     row = TreeRow{0, 0, 0, 0, 1};
     for (int base = 0; base < p.batch; base += 32) {
-      const int nt = base == 0 ? first_nt : base + lane < p.batch ? tiles(p, read_tree_row(p, base + lane)) : 0;
+      const int nt = base == 0 ? first_nt : base + lane < p.batch ? head_tiles(p, read_tree_row(p, base + lane)) : 0;
       int incl = nt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -173,12 +187,12 @@ struct TreeWalk {
       if (x < all) {
         const int src = __ffs(__ballot_sync(0xffffffffu, x < incl * per_row)) - 1;
         x -= __shfl_sync(0xffffffffu, incl - nt, src) * per_row;
-        const int mine = __shfl_sync(0xffffffffu, nt, src);
         b = base + src;
         row = read_tree_row(p, b);
+        const int mine = tiles(p, row), units = tree_units(p, row);
         const int unit = x / mine;
-        g = unit / p.units_per_head;
-        qg = unit - g * p.units_per_head;
+        g = unit / units;
+        qg = unit - g * units;
         return x - unit * mine;
       }
       x -= all;
@@ -191,7 +205,7 @@ struct TreeWalk {
     while (at < end) {
       if (v1 == tiles(p, row)) {  // the unit is done: the next one
         v1 = 0;
-        if (++qg == p.units_per_head) {
+        if (++qg == tree_units(p, row)) {
           qg = 0;
           if (++g == p.kv_heads) {
             g = 0;
@@ -228,8 +242,8 @@ struct TreeWalk {
       s.last = back < big ? back / (each + 1) : more + (back - big) / each;
       s.count = row.count;
       s.row0 = qg * p.rows_per_unit;
-      s.rows = min(p.rows_per_unit, p.group * p.nodes - s.row0);
-      s.out = (long long)tree_out_row(p, b, g, s.row0);
+      s.rows = min(p.rows_per_unit, p.group * (p.compact ? row.count : p.nodes) - s.row0);
+      s.out = (long long)tree_out_row(p, b, g, p.compact ? 0 : s.row0);
     }
     return s;
   }
