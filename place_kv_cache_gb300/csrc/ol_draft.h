@@ -85,6 +85,8 @@ struct TreeParams {
   int nctas;                    // the tiles of all units in contiguous equal shares
   int extra;                    // tiles that a unit's begin and end cost besides
   int by_unit;                  // 1: few units, each cut into many segments; the merge goes by units
+  int pool;                     // shares beyond one a CTA, at most: small ones for the CTAs that are done first
+  uint32_t* ticket;             // the next of them, 0 between calls (pool > 0)
   int compact;                  // 1: a row's live (head, node) rows only, r = head * count + node; else r = head * nodes + node
 };
 // Few units of many segments are merged by units, 8 rows a CTA, while those CTAs
@@ -115,7 +117,9 @@ OL_HD inline TreeRow tree_row(int len, int count, int window, int tile_log2) {
 
 // One partial slot: m[rows] (log2 domain), l[rows], o[ceil(D / 4)][rows] float4.
 OL_HD inline size_t tree_slot_floats(int rows, int head_dim) { return (size_t)rows * (2 + (head_dim + 3) / 4 * 4); }
-constexpr size_t kTreeSplitBytes = 4 * kTreeMaxCtas * sizeof(TreeSplit);
+constexpr int kTreeMaxShares = 4 * kTreeMaxCtas;
+constexpr size_t kTreeSplitBytes = kTreeMaxShares * sizeof(TreeSplit);
+constexpr int kTreeTicketWord = 16;  // of the workspace's status area
 // (head, node) rows of a unit of the CUDA-core and of the tensor-core kernel
 inline int tree_gen_rows(int group, int nodes) { return group * nodes <= 32 ? 32 : 64; }
 inline int tree_fast_rows(int group, int nodes) { return group * nodes <= 128 ? 128 : 256; }

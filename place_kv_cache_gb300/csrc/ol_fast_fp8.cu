@@ -371,8 +371,19 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     TreeSplit note = {};
     note.last = -1;
     auto fetch = [&](Tile& t) {
+      t.more = true;
       if (tile == w.tile1) {
         t.more = w.next(p);
+        while (!t.more && w.pool > 0) {  // the share is done: another one, while there are
+          uint32_t i = 0;
+          if (lane == 0) i = atomicAdd(p.ticket, 1u);
+          i = __shfl_sync(0xffffffffu, i, 0);
+          if (i >= (uint32_t)w.pool) break;  // (whatever stood in a workspace that was not initialised)
+          if (lane == 0 && !p.by_unit) p.splits[w.id] = note;
+          note.last = -1;
+          w.begin(p, gridDim.x + i);
+          t.more = w.next(p);
+        }
         // to the other roles
         if (!(ok = warp_wait(bar.seg_empty(segs.slot), segs.phase ^ 1, abort, p.status))) {
           t.more = false;
@@ -396,7 +407,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             if (p.by_unit) p.splits[w.unit(p)] = note;
           }
           // (only the share's last unit can reach past its end)
-          if (!t.more && !p.by_unit) p.splits[blockIdx.x] = note;
+          if (!t.more && !p.by_unit) {
+            p.splits[w.id] = note;
+            // notes of shares that are not there
+            for (int i = gridDim.x + blockIdx.x; i < (int)gridDim.x + p.pool; i += gridDim.x)
+              if (i - (int)gridDim.x >= w.pool) p.splits[i].last = -1;
+          }
         }
         warp_arrive(bar.seg_full(segs.slot));
         segs.next();
@@ -432,20 +448,29 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       ring.next();
       return true;
     };
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      ahead[i].more = i == 0 || ahead[i - 1].more;
-      if (i == 0) tile = w.tile1;  // (none yet)
-      if (ahead[i].more) fetch(ahead[i]);
-    }
-    while (ok && ahead[0].more) {
-      cur = ahead[0];
+    tile = w.tile1;  // (none yet)
+    ahead[1].more = ahead[2].more = false;
+    bool first = true, ended = false;
+    while (ok) {
       ahead[0] = ahead[1];
       ahead[1] = ahead[2];
-      if (ahead[1].more) fetch(ahead[2]);
-      if (!ok) break;
-      const int y = cache_row_of(cur);
-      ok = load(y) && load(y + v_rows);
+      ahead[2].more = false;
+      if (!ended) {
+        fetch(ahead[2]);
+        ended = !ahead[2].more;
+        if (!ok) break;
+      }
+      cur = ahead[0];
+      if (first) {  // the first tile at once
+        cur = ahead[2];
+        ahead[2].more = first = false;
+      }
+      if (cur.more) {
+        const int y = cache_row_of(cur);
+        ok = load(y) && load(y + v_rows);
+      } else if (ended && !ahead[1].more && !ahead[2].more) {
+        break;
+      }
     }
     if (!ok)  // copies in flight end before the CTA does; a slot's last load: of this lap before the cursor, else of the one before
       for (int i = 0; i < L::kSlots; ++i) mbar_wait_bounded(bar.full(i), i < ring.slot ? ring.phase : ring.phase ^ 1);
@@ -620,13 +645,24 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       Col* const cols = reinterpret_cast<Col*>(smem + L::kCols) + buf * NC;
       const uint4* const q =
           reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * D) + part * (E / 8);
+      uint4 x[E / 8], next[E / 8];
+      int query, live, next_query, next_live;
+      auto load = [&](int c) {
+        const int head = (r0 + c) / g.count;
+        next_query = r0 + c - head * g.count;
+        next_live = head * p.nodes + next_query;
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) next[e] = r0 + c < R ? q[(size_t)next_live * (D / 8) + e] : make_uint4(0, 0, 0, 0);
+      };
+      load(lane >> 2);
+      if (!(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
 #pragma unroll 1
       for (int c = lane >> 2; c < NC; c += 8) {
-        const int head = (r0 + c) / g.count, query = r0 + c - head * g.count, live = head * p.nodes + query;
-        uint4 x[E / 8];
 #pragma unroll
-        for (int e = 0; e < E / 8; ++e) x[e] = r0 + c < R ? q[(size_t)live * (D / 8) + e] : make_uint4(0, 0, 0, 0);
-        if (c < 8 && !(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
+        for (int e = 0; e < E / 8; ++e) x[e] = next[e];
+        query = next_query;
+        live = next_live;
+        if (c + 8 < NC) load(c + 8);
         uint32_t top = 0;
 #pragma unroll
         for (int e = 0; e < E / 8; ++e) {
@@ -660,7 +696,6 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         }
         if (part == 0) cols[c] = Col{1.f / factor, query, live, 0};
       }
-      if (!ok) break;
       fence_proxy_async_smem();
       warp_arrive(bar.q_full(buf));
       ++seg;
@@ -731,6 +766,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         const bool edge = __any_sync(0xffffffffu, hidden != 0);
         float y[kMine];
         for (bool looked = false;;) {
+          if (i > 0 || looked) {  // (a segment's first tile has nothing to compare with)
           const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
           for (int c0 = 0; c0 < kMine; c0 += kStep) {
@@ -760,6 +796,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
           // (the flag holds the number of the tile that raised it)
           if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
           if (!(ok = vote()) || flag[count & 1] != count) break;
+          }
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
 #pragma unroll 1
           for (int c = 0; c < kMine; c += 4) {
@@ -830,7 +867,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            p_row[(k * (NC / 16) + group) ^ p_sw] = make_uint4(z[k][0], z[k][1], z[k][2], z[k][3]);
+#pragma unroll
+            for (int h = 0; h < kMine / 16; ++h)
+              p_row[(k * (NC / 16) + first / 16 + h) ^ p_sw] =
+                  make_uint4(z[k][4 * h], z[k][4 * h + 1], z[k][4 * h + 2], z[k][4 * h + 3]);
         }
         fence_proxy_async_smem();
         tmem_fence_before();
@@ -861,6 +901,11 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       // lane's column: its upper bits
       if (lane % (32 / kMine) == 0) sums[me % 4 * kMine + lane / (32 / kMine)] = t[0];
       if (!(ok = vote())) break;
+      if (lane < kMine) {
+        const float total = sums[lane] + sums[kMine + lane] + sums[2 * kMine + lane] + sums[3 * kMine + lane];
+        grow[lane] = g.slot >= 0 ? total : total == 0.f ? 0.f : 1.f / total;  // (for outputs its inverse)
+      }
+      __syncwarp();
       if (!(ok = warp_wait(bar.p_taken(), count + 1 & 1, abort, p.status))) break;
       tmem_fence_after();
       float* const slot = g.slot < 0 ? nullptr : tree_slot(p, g.slot);
@@ -877,17 +922,16 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         for (int c = 0; c < 4; ++c) {
           const int col = c0 + c, place = first + col;
           if (col >= live) continue;
-          const float total = sums[col] + sums[kMine + col] + sums[2 * kMine + col] + sums[3 * kMine + col];
           const float sum = fmaf(fmaf(fmaf(__uint_as_float(o[3][c]), 0.0625f, __uint_as_float(o[2][c])), 0.0625f,
                                       __uint_as_float(o[1][c])), 0.0625f, __uint_as_float(o[0][c]));
           if (slot) {
             if (row == 0) {
               slot[place] = -tab[col / 2 * 4 + 2 + col % 2];
-              slot[NC + place] = total;
+              slot[NC + place] = grow[col];
             }
             if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
           } else if (row < D) {
-            store_out(p.out, p.out_dtype, out + (size_t)cols[col].row * D, total == 0.f ? 0.f : sum / total);
+            store_out(p.out, p.out_dtype, out + (size_t)cols[col].row * D, sum * grow[col]);
           }
         }
       }
@@ -978,8 +1022,15 @@ void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
-  p.extra = 2;
+  // (0 / 1 / 2 / 3 tiles: chunks of 4 tokens over 32 ragged rows - / 68 / 65 / 63 us; longer shares do not feel it)
+  p.extra = 3;
   p.compact = 1;
+  // (every share, and the CTAs' two places beyond, has a note and two partial slots in the workspace of a tree call)
+  // Where the memory sets the pace, SMs differ in what they get of it: the last shares are for those that are ahead.
+  // (64 rows of 8192 tokens, one query of 4 heads a kv head: 166 us, with the pool 161; ragged rows to 16384 in pages of
+  // 16 189 and 183.) Where the SM itself does, shares are equal as they are (16 columns 167 and 185 us, heads of 64
+  // 105 and 110).
+  p.pool = p.rows_per_unit > 8 || p.head_dim < 128 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
   p.by_unit = tree_few_units(p);
 }
 

@@ -276,6 +276,7 @@ ol_status fp8_attention(const ol_fp8_kv* kv, int32_t dtype, const void* q, int32
   char* const splits = static_cast<char*>(workspace) + tree_splits_offset(c.batch, c.kv_heads, new_len);
   t.splits = reinterpret_cast<TreeSplit*>(splits);
   t.partials = reinterpret_cast<float*>(splits + kTreeSplitBytes);
+  t.ticket = static_cast<uint32_t*>(workspace) + kTreeTicketWord;
   const bool fast = fast_fp8_supported(p);
   if (fast)
     plan_fast_fp8(p, sm_count_cached());

@@ -330,12 +330,21 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   __shared__ float other_l[G > 1 ? (G - 1) * ROWS : 1];
   pdl_wait();
   pdl_launch_dependents();
+  if (p.pool > 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
   if (p.by_unit) {
     const TreeRow row = read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head));
     if (row.ntiles == 0 || (int)blockIdx.x % p.units_per_head >= tree_units(p, row)) return;  // no note
   }
   const TreeSplit u = p.splits[blockIdx.x];
   if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
+  // (a note that no one wrote: the workspace was not initialised, or a launch before failed)
+  if (p.pool > 0 && (u.first < 0 || u.last >= p.nctas + p.pool || u.rows > p.rows_per_unit || u.row0 < 0 || u.count < 1 ||
+                     u.out < 0 || u.out + (p.compact ? (long long)(p.group - 1) * p.nodes + u.count : u.rows) >
+                                      (long long)p.batch * p.q_heads * p.nodes ||
+                     u.row0 + u.rows > p.group * u.count)) {
+    set_status(p.status, OL_DEVICE_GUARD);
+    return;
+  }
   const int RU = p.rows_per_unit, D = p.head_dim;
   const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS, d0 = lane % D4, grp = lane / D4;
   const int place = blockIdx.y * ROWS + lr;  // row of the unit
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
 
 template <int ROWS, int THREADS>
 cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
-  const dim3 grid(p.by_unit ? p.batch * p.kv_heads * p.units_per_head : p.nctas, (rows + ROWS - 1) / ROWS), block(THREADS);
+  const dim3 grid(p.by_unit ? p.batch * p.kv_heads * p.units_per_head : p.nctas + p.pool, (rows + ROWS - 1) / ROWS), block(THREADS);
   return p.head_dim <= 128 ? launch_pdl(tree_merge_kernel<ROWS, THREADS, 32>, grid, block, 0, s, p)
                            : launch_pdl(tree_merge_kernel<ROWS, THREADS, 64>, grid, block, 0, s, p);
 }

@@ -130,6 +130,10 @@ __device__ __forceinline__ int tree_live_row(const TreeParams& p, int count, int
 // unit puts its state into a slot. A share has at most two of them: the end or the
 // middle of a unit (slot 2 c), and a unit's begin (slot 2 c + 1).
 // Equal shares keep ragged batches balanced to one tile per SM.
+// With a pool (p.pool > 0), the last tenth to sixth of the tiles is cut into small
+// shares, numbered behind those of the CTAs, for whoever is done (SMs differ by up to a
+// sixth in what the memory gives them): the first half of them of three times the
+// tiles of the second. What a share is does not depend on who takes it.
 // The constructor is for whole warps; next() may be called by single threads.
 struct TreeWalk {
   int b, g, qg;
@@ -140,6 +144,8 @@ struct TreeWalk {
   int share, total;      // its first tile; all tiles
   int each, more;        // tiles of a share; shares of one more
   int v1;                // tiles of the unit, extra ones included, up to `at`
+  int id, shares;        // the share; shares of a CTA each
+  int small, pool_at, pool;  // pool: tiles of its smaller shares, first tile, shares
   int first_nt;          // tiles of a kv head of row `lane` of the first 32 rows
 
   __device__ __forceinline__ static int tiles(const TreeParams& p, const TreeRow& r) {
@@ -158,15 +164,46 @@ struct TreeWalk {
       total += __reduce_add_sync(0xffffffffu, nt);
     }
     total *= p.kv_heads;
-    const int shares = min(total, (int)gridDim.x);
-    at = end = share = each = more = tile0 = tile1 = slot = 0;
-    if (c < shares) {
-      each = total / shares;
-      more = total - each * shares;
-      at = share = c * each + min(c, more);
-      end = share + each + (c < more);
+    shares = min(total, (int)gridDim.x);
+    share = each = more = tile0 = tile1 = slot = pool = small = 0;
+    pool_at = total;
+    if (shares > 0) {
+      if (p.pool > 0 && total >= 64 * shares) {  // (less would not pay for the shares' own begins and ends)
+        small = min(total / (24 * shares), 6);
+        pool = min(p.pool, total / (12 * small)) & ~1;
+        pool_at = total - pool * 2 * small;
+      }
+      each = pool_at / shares;
+      more = pool_at - each * shares;
     }
+    begin(p, c);
+  }
+
+  // Goes to the begin of a share.
+  __device__ __forceinline__ void begin(const TreeParams& p, int i) {
+    id = i;
+    at = end = 0;
+    if (i < shares) {
+      at = i * each + min(i, more);
+      end = at + each + (i < more);
+    } else if (i - (int)gridDim.x < pool && i >= (int)gridDim.x) {
+      const int k = i - gridDim.x, big = min(k, pool / 2);
+      at = pool_at + (k + 2 * big) * small;
+      end = at + (k < pool / 2 ? 3 : 1) * small;
+    }
+    share = at;
     v1 = at < end ? locate(p, at) : 0;
+    tile0 = tile1 = 0;
+  }
+
+  // The share that has tile x.
+  __device__ __forceinline__ int share_of(int x) const {
+    if (x >= pool_at) {
+      const int k = (x - pool_at) / small, half = pool / 2;  // in small shares
+      return gridDim.x + (k < 3 * half ? k / 3 : k - 2 * half);
+    }
+    const int big = more * (each + 1);  // tiles of the shares of one more
+    return x < big ? x / (each + 1) : more + (x - big) / each;
   }
 
   // Finds the unit of tile x (x < total); returns the tile's index in it.
@@ -222,7 +259,7 @@ struct TreeWalk {
       at += step;
       tile1 = max(v1 - p.extra, 0);
       if (tile1 > tile0) {
-        slot = 2 * blockIdx.x + (tile0 == 0);
+        slot = 2 * id + (tile0 == 0);
         return true;
       }
     }
@@ -234,12 +271,10 @@ struct TreeWalk {
   // The merge's note of the unit that the segment begins (tile0 is 0).
   __device__ __forceinline__ TreeSplit note(const TreeParams& p) const {
     TreeSplit s = {};
-    s.first = blockIdx.x;
+    s.first = id;
     s.last = -1;
     if (tile1 < row.ntiles) {
-      const int back = end + (row.ntiles - tile1) - 1;  // the unit's last tile
-      const int big = more * (each + 1);                // tiles of the shares of one more
-      s.last = back < big ? back / (each + 1) : more + (back - big) / each;
+      s.last = share_of(end + (row.ntiles - tile1) - 1);  // of the unit's last tile
       s.count = row.count;
       s.row0 = qg * p.rows_per_unit;
       s.rows = min(p.rows_per_unit, p.group * (p.compact ? row.count : p.nodes) - s.row0);
