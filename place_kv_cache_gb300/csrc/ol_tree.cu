@@ -331,11 +331,11 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   pdl_wait();
   pdl_launch_dependents();
   if (p.pool > 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
+  const TreeSplit u = p.splits[blockIdx.x];  // (on its way beside the row's length)
   if (p.by_unit) {
     const TreeRow row = read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head));
     if (row.ntiles == 0 || (int)blockIdx.x % p.units_per_head >= tree_units(p, row)) return;  // no note
   }
-  const TreeSplit u = p.splits[blockIdx.x];
   if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
   // (a note that no one wrote: the workspace was not initialised, or a launch before failed)
   if (p.pool > 0 && (u.first < 0 || u.last >= p.nctas + p.pool || u.rows > p.rows_per_unit || u.row0 < 0 || u.count < 1 ||
@@ -541,7 +541,11 @@ cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
-  return p.by_unit ? launch_merge<8, 512>(p, rows, s) : launch_merge<16, 256>(p, rows, s);
+  if (!p.by_unit) return launch_merge<16, 256>(p, rows, s);
+  // Few rows of few units: their partial results through more SMs (7 rows of 4 units of 33 segments 13.2 us in all, with
+  // two rows a CTA 12.4; 4 rows of 8 units 18.1 and 15.6). With more rows there are CTAs enough (40 rows of 12 units
+  // 24.0 and 25.4).
+  return p.compact && rows <= 8 ? launch_merge<2, 256>(p, rows, s) : launch_merge<8, 512>(p, rows, s);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {
