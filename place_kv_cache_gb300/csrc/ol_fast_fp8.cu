@@ -228,6 +228,11 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(top ^ (top >> 31 & 0x7fffffff));
 }
 
+__device__ __forceinline__ float fast_inverse(float x) {  // off by one unit in the last place
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -749,7 +754,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         // comes in by its logarithm, and only for columns that see the token.
         const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
         warp_arrive(bar.sc_empty(sc.slot));
-        const float v_log2 = __log2f(v_scale), v_inv = v_scale == v_scale ? __frcp_rn(v_scale) : 1.f;
+        const float v_log2 = __log2f(v_scale), v_inv = v_scale == v_scale ? fast_inverse(v_scale) : 1.f;
         const uint32_t ts = tmem + (count & 1) * 2 * NC + first + lanes;
         if (!(ok = warp_wait(bar.s_full(count & 1), count >> 1 & 1, abort, p.status))) break;
         ++count;
@@ -790,9 +795,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             for (int c = 0; c < kMine; ++c)
               if (hidden >> c & 1) y[c] = -INFINITY;
           if (looked) break;
-          float most = y[0];
+          float most4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-          for (int c = 1; c < kMine; ++c) most = fmaxf(most, y[c]);
+          for (int c = 4; c < kMine; ++c) most4[c % 4] = fmaxf(most4[c % 4], y[c]);
+          const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
           // (the flag holds the number of the tile that raised it)
           if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
           if (!(ok = vote()) || flag[count & 1] != count) break;
