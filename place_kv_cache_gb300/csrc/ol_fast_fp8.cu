@@ -47,8 +47,9 @@ struct Lay {
   static constexpr int kTileBytes = kTile * D;
   static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries
   static constexpr int kPBytes = kTile * 4 * NC;        // four parts of P
-  static constexpr int kQ = 0;                          // two buffers
-  static constexpr int kP = kQ + 2 * kQBytes;
+  static constexpr int kQBuffers = NC == 32 ? 1 : 2;    // (room for one more tile of K or V)
+  static constexpr int kQ = 0;
+  static constexpr int kP = kQ + kQBuffers * kQBytes;
   static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn
   static constexpr int kSmall = 1536 + NC * 112;          // what follows the ring, at most
   static constexpr int kFit = (kMostSmem - kSmall - kRing) / kTileBytes;
@@ -344,6 +345,8 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
   pdl_wait();
   pdl_launch_dependents();
 
+  const auto q_buffer = [](uint32_t seg) { return (int)(seg % L::kQBuffers); };
+  const auto q_phase = [](uint32_t seg) { return seg / L::kQBuffers & 1; };
   // The next segment, for a whole warp; false: there is none, or the wait was given up.
   Cursor<kSegs> segs;
   auto next_seg = [&](Seg& g, bool& ok) {
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       int y;            // cache row of this lane's box in plane K, or in its page
       int page;
       bool more;        // there is such a tile
-    } ahead[3], cur;
+    } ahead[3], cur = {};
     const int v_rows = (PAGED ? fc.num_pages * fc.page_size : fc.batch * fc.capacity) * fc.kv_heads;
     const int step_pages = PAGED ? kTile / fc.page_size : 0, step_slots = PAGED ? kTile - step_pages * fc.page_size : 0;
     bool ok = true;
@@ -496,12 +499,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       tmem_fence_after();
       if (elect_one()) {
         const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes, 16, 8 * D, kRowSwizzle);
-        const uint64_t qd = smem_desc(base + L::kQ + (seg & 1) * L::kQBytes, 16, 8 * D, kRowSwizzle);
+        const uint64_t qd = smem_desc(base + L::kQ + q_buffer(seg) * L::kQBytes, 16, 8 * D, kRowSwizzle);
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) mma_fp8(tm + (s_count & 1) * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, x > 0);
         mma_commit(bar.s_full(s_count & 1));
         mma_commit(bar.empty(k.slot));
-        if (last) mma_commit(bar.q_empty(seg & 1));
+        if (last) mma_commit(bar.q_empty(q_buffer(seg)));
       }
       __syncwarp();
       ++s_count;
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     Seg g;
     while (next_seg(g, ok)) {
       const int tiles = uniform(g.tiles);
-      ok = warp_wait(bar.q_full(seg & 1), seg >> 1 & 1, abort, p.status) && scores_wait();
+      ok = warp_wait(bar.q_full(q_buffer(seg)), q_phase(seg), abort, p.status) && scores_wait();
       if (!ok) break;
       scores(tiles == 1);
       int r_low = row_low(p.window, g.prefix) - g.t0, r_end = g.len - g.t0;  // rows of the tile
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     bool ok = true;
     Seg g;
     while (next_seg(g, ok)) {
-      const int buf = seg & 1, r0 = g.qg * NC, R = p.group * g.count;
+      const int buf = q_buffer(seg), r0 = g.qg * NC, R = p.group * g.count;
       uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
       Col* const cols = reinterpret_cast<Col*>(smem + L::kCols) + buf * NC;
       const uint4* const q =
@@ -660,7 +663,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         for (int e = 0; e < E / 8; ++e) next[e] = r0 + c < R ? q[(size_t)next_live * (D / 8) + e] : make_uint4(0, 0, 0, 0);
       };
       load(lane >> 2);
-      if (!(ok = warp_wait(bar.q_empty(buf), seg >> 1 & 1 ^ 1, abort, p.status))) break;
+      if (!(ok = warp_wait(bar.q_empty(buf), q_phase(seg) ^ 1, abort, p.status))) break;
 #pragma unroll 1
       for (int c = lane >> 2; c < NC; c += 8) {
 #pragma unroll
@@ -732,8 +735,8 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     };
     Seg g;
     while (next_seg(g, ok)) {
-      const int buf = seg & 1;
-      if (!(ok = warp_wait(bar.q_full(buf), seg >> 1 & 1, abort, p.status))) break;
+      const int buf = q_buffer(seg);
+      if (!(ok = warp_wait(bar.q_full(buf), q_phase(seg), abort, p.status))) break;
       ++seg;
       const Col* const cols = reinterpret_cast<const Col*>(smem + L::kCols) + buf * NC + first;
       if (lane < kMine) {
