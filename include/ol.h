@@ -741,8 +741,9 @@ typedef struct ol_fp8_kv {
  *     block began.
  *   - code = x / s, the fp32 quotient rounded to E4M3 (nearest, ties to even).
  * An infinity or NaN makes its block's scale NaN, for as long as the block is not
- * begun anew. Slots behind a row's tokens are not written; tokens past counts[b]
- * are not read. counts, positions, the pages that are written (each by one row,
+ * begun anew; so does a stored scale that is negative or infinite. The appended tokens
+ * are the row's last: what stood behind them in their last block is not written, but
+ * may no longer fit that block's scale. Tokens past counts[b] are not read. counts, positions, the pages that are written (each by one row,
  * through one entry) and what the kernel reads on the device: as ol_rope_append.
  * Errors: NULL, ALIAS, READONLY, CAPACITY, SHAPE, DTYPE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (head_dim no multiple of 16 or > 256), CUDA.

@@ -71,7 +71,8 @@ __device__ __forceinline__ float block_scale(uint32_t most, bool begun, float ol
   const float a = __uint_as_float(most);
   const bool finite = most < 0x7f800000u;
   if (begun && old != 0.f) {
-    if (!finite || !(old == old)) return __uint_as_float(0x7fc00000u);
+    // (a scale that is no number above 0, which no append has written, would never reach a)
+    if (!finite || !(old > 0.f) || !(old < INFINITY)) return __uint_as_float(0x7fc00000u);
     float limit = kFp8Top * old;
     while (a > limit) {  // few rounds: a token's largest element against its block's
       limit *= 2.f;

@@ -123,6 +123,7 @@ APPENDS = [
     ("bf16", 2, 4, 300, 128, 64, 0, 200, [7, 100], [193, 200]), ("bf16", 2, 1, 300, 256, 128, 128, 256, [0, 127], None),
     ("bf16", 2, 3, 77, 80, 16, 0, 33, [44, 1], None), ("bf16", 1, 1, 17, 16, 128, 0, 17, [0], None),
     ("f32", 2, 2, 100, 128, 16, 16, 5, [14, 95], None), ("f32", 2, 2, 260, 256, 128, 0, 129, [130, 0], [128, 129]),
+    ("bf16", 2, 2, 200, 128, 16, 48, 50, [40, 95], None), ("bf16", 2, 1, 600, 64, 32, 256, 300, [255, 31], [300, 7]),
     ("f32", 1, 8, 64, 96, 32, 32, 64, [0], None), ("f32", 4, 2, 50, 48, 16, 0, 3, [47, 0, 15, 29], [3, 2, 1, 0]),
 ]
 
@@ -365,6 +366,12 @@ SHAPES = [
     ("f32", 1, 4, 1, 64, 128, 0, 40, [200], None, -1, None), ("f32", 2, 2, 2, 256, 16, 16, 2, [90, 2], None, -1, "bf16"),
     ("f32", 3, 4, 2, 16, 16, 16, 2, [70, 2, 31], None, -1, None), ("f32", 2, 12, 4, 160, 32, 0, 9, [70, 200], None, -1, None),
     ("bf16", 40, 8, 2, 128, 16, 16, 1, list(range(1, 41)), None, -1, None),
+    ("bf16", 3, 8, 2, 128, 16, 48, 2, [500, 49, 129], None, -1, None), ("bf16", 2, 8, 2, 64, 16, 80, 3, [700, 81], None, 333, None),
+    ("bf16", 2, 8, 2, 128, 32, 256, 1, [1000, 257], None, -1, None), ("f32", 2, 8, 2, 128, 16, 48, 2, [200, 49], None, -1, None),
+    ("bf16", 5, 8, 2, 128, 16, 16, 4, [0, 4, 700, 0, 33], [0, 4, 1, 0, 3], -1, None),
+    ("f32", 3, 8, 2, 80, 16, 16, 4, [0, 4, 70], [0, 4, 1], -1, None),
+    ("bf16", 3, 28, 4, 128, 32, 32, 512, [512, 600, 900], [512, 1, 77], -1, None),
+    ("bf16", 2, 64, 1, 64, 64, 0, 7, [300, 1000], [7, 3], 64, "f32"), ("bf16", 33, 4, 4, 128, 16, 0, 1, [9] * 33, None, 3, None),
 ]
 
 
@@ -376,6 +383,104 @@ def test_attention(case):
     a.out.fill_(-77.0)
     a.call(scale=0.3)
     a.check(scale=0.3)
+
+
+@pytest.mark.parametrize("Hq,H,D,T,seed", [(8, 8, 128, 1, 1), (28, 4, 128, 3, 2), (16, 2, 64, 9, 3), (12, 4, 96, 2, 4)])
+def test_drawn_rows(Hq, H, D, T, seed):
+    """Batches past one warp's, of lengths and counts of every kind, in pages in any order."""
+    rng = np.random.default_rng(seed)
+    lens = np.minimum(np.exp(rng.uniform(0, 7.5, 50)).astype(np.int32), 1500)
+    counts = np.minimum(rng.integers(0, T + 1, 50), lens).astype(np.int32)
+    a = Attention("bf16" if D != 96 else "f32", 50, Hq, H, D, 16, 32, T, lens, counts, -1 if seed % 2 else 100, seed=seed)
+    a.call()
+    a.check()
+
+
+def test_shares_of_the_pool():
+    """Rows long enough that the last tiles go to whoever is done first: right, and the same bits every time."""
+    lens = [11000 + 37 * b for b in range(30)]  # 90 tiles a row and head: more than 64 for each of 304 CTAs
+    a = Attention("bf16", 30, 32, 8, 128, 128, 0, 1, lens, out="f32")
+    a.call()
+    first = a.out.clone()
+    for _ in range(4):
+        a.out.fill_(-77.0)
+        a.call()
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, first)
+    for b in (0, 13, 29):  # against the definition
+        ok = du.visible(lens[b], 1, None, None, -1)
+        (kc, ks), (vc, vs) = a.c.row(0, b), a.c.row(1, b)
+        ks, vs = (x.repeat_interleave(128, 1)[:, : lens[b]] for x in (ks, vs))
+        for g in range(8):
+            want, *sizes = fu.attention(a.q[b, g * 4: g * 4 + 4], kc[g, : lens[b]], ks[g], vc[g, : lens[b]], vs[g], ok,
+                                        128 ** -0.5)
+            tol = fu.attention_tolerance(want, *sizes, 128, lens[b], torch.float32, True)
+            assert bool(((first[b, g * 4: g * 4 + 4].double() - want).abs() <= tol).all())
+    assert ol.ol_workspace_status(a.ws) == ol.OL_DEVICE_OK
+
+
+@pytest.mark.parametrize("D,C", [(128, 1 << 25), (16, 1 << 30)])
+def test_past_32_bit_offsets(D, C):
+    """Codes past 2^32 bytes, and (heads of 16) more than 2^31 vectors: append, read back, attention at a cache's end."""
+    H, T, block, window = 2 if D == 128 else 1, 3, 128, 200
+    if torch.cuda.mem_get_info()[0] < 2 * H * C * D * 1.3:
+        pytest.skip("no room")
+    c = Cache.__new__(Cache)
+    c.B, c.H, c.D, c.block, c.page, c.C, c.table, c.table_d = 1, H, D, block, 0, C, None, None
+    c.gen = torch.Generator(device=DEV).manual_seed(3)
+    c.codes = torch.empty((2, 1, H, C, D), dtype=torch.uint8, device=DEV)
+    c.scales = torch.empty((2, 1, H, C // block), device=DEV)
+    c.desc = ol.fp8_kv(c.codes, c.scales, block=block)
+    first = C - 260
+    at = first // block * block
+    k, v = torch.randn((2, 1, H, 260, D), generator=c.gen, device=DEV).bfloat16()
+    c.scales[..., at // block] = 1.0
+    c.append([first], [260], k, v, ragged=False)
+    want = []
+    for plane, x in ((0, k), (1, v)):
+        tail = c.codes[plane, 0, :, at:].view(E4M3).double()
+        scales = c.scales[plane, 0, :, at // block:].double()
+        for g in range(H):
+            codes, s = tail[g].clone(), torch.ones_like(scales[g])
+            fu.append_row(codes, s, block, first - at, x[0, g].double())
+            assert torch.equal(codes[first - at:], tail[g, first - at:]) and torch.equal(s, scales[g])
+        want.append((tail, scales))
+    out = torch.empty((2, 1, H, 260, D), device=DEV)
+    start = np.array([first], np.int32)
+    ol.ol_fp8kv_read(c.desc, ol.OL_F32, 260, out[0], out[1], start, dev(start))
+    for plane in (0, 1):
+        values = (want[plane][0].float() * want[plane][1].float().repeat_interleave(block, 1)[..., None])[:, first - at:]
+        assert torch.equal(out[plane, 0], values)
+    lens = np.array([C], np.int32)
+    for dtype in (torch.bfloat16, torch.float32):
+        q = torch.randn((1, 2 * H, T, D), generator=c.gen, device=DEV).to(dtype)
+        y = torch.empty_like(q)
+        n = ol.ol_workspace_size_fp8kv(1, 2 * H, H, D, T)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        ol.ol_workspace_init(ws, n)
+        ol.ol_fp8kv_attention(c.desc, CODE[dtype], q, 2 * H, T, lens, dev(lens), None, None, 0.0, window, y, CODE[dtype], ws, n)
+        assert ol.ol_workspace_status(ws) == ol.OL_DEVICE_OK
+        m = C - at
+        ok = du.visible(C - at, T, None, None, window)
+        for g in range(H):
+            wide = [s[g].repeat_interleave(block)[:m] for _, s in want]
+            exact, *sizes = fu.attention(q[0, 2 * g: 2 * g + 2], want[0][0][g], wide[0], want[1][0][g], wide[1], ok, D ** -0.5)
+            tol = fu.attention_tolerance(exact, *sizes, D, m, dtype, dtype == torch.bfloat16 and D == 128)
+            assert bool(((y[0, 2 * g: 2 * g + 2].double() - exact).abs() <= tol).all())
+
+
+def test_scales_that_no_append_writes():
+    """A negative or infinite scale under an append makes its block NaN, and ends."""
+    c = Cache(1, 3, 32, 64, 16)
+    c.fill([8])
+    c.scales[:, 0, 0, 0], c.scales[:, 0, 1, 0], c.scales[:, 0, 2, 0] = -1.0, float("inf"), 1e-44
+    k, v = torch.randn((2, 1, 3, 2, 64), generator=c.gen, device=DEV)
+    c.append([8], [2], k, v)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(c.scales[:, 0, :2, 0]).all())
+    grown = c.scales[:, 0, 2, 0].double()
+    most = torch.stack((k, v))[:, 0, 2].abs().amax((1, 2)).double()
+    assert bool((448 * grown >= most * (1 - 2.0 ** -23)).all()) and bool((448 * grown < 2.1 * most).all())
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
