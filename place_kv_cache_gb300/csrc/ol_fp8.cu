@@ -163,18 +163,18 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
   }
   const bool coded = scale > 0.f;  // false for 0 and NaN
   const float inverse = coded ? __frcp_rn(scale) : 0.f;
-  auto quotient = [&](float v) {
-    const float q = v * inverse;
-    return fmaf(fmaf(-q, scale, v), inverse, q);
+  const uint64_t inverse2 = pack2(inverse, inverse), minus2 = pack2(-scale, -scale);
+  auto coded_pair = [&](float v0, float v1) {
+    const uint64_t v = pack2(v0, v1), q = mul2(v, inverse2);
+    const float2 r = unpack2(fma2(fma2(q, minus2, v), inverse2, q));
+    return coded ? e4m3x2(r.x, r.y) : 0u;
   };
   uint8_t* const to = codes + (long long)(lo - first) * c.head_dim;
   t = t_first, d = x_first;
 #pragma unroll
   for (int u = 0; u < KEEP; ++u, next()) {
     if (t >= tokens) continue;
-    auto two = [&](int j) {
-      return coded ? e4m3x2(quotient(value_of<T>(x[u].e[j])), quotient(value_of<T>(x[u].e[VE > 1 ? j + 1 : j]))) : 0u;
-    };
+    auto two = [&](int j) { return coded_pair(value_of<T>(x[u].e[j]), value_of<T>(x[u].e[VE > 1 ? j + 1 : j])); };
     Codes<VE> y;
     if constexpr (VE == 8)
       y = make_uint2(two(0) | two(2) << 16, two(4) | two(6) << 16);
@@ -204,7 +204,7 @@ constexpr int kReadThreads = 256, kReadUnroll = 8, kReadMost = 128;
 // looked up once a token, then a thread has VE consecutive elements (16 bytes of
 // output) of up to 8 tokens, all on their way together.
 template <typename T, int VE>
-__global__ void __launch_bounds__(kReadThreads, 3) fp8_read_kernel(const __grid_constant__ Fp8ReadParams p, int runs, int run_tokens) {
+__global__ void __launch_bounds__(kReadThreads, 4) fp8_read_kernel(const __grid_constant__ Fp8ReadParams p, int runs, int run_tokens) {
   __shared__ long long rows[2][kReadMost];  // of the token's codes; -1: it is not read
   __shared__ float scales[2][kReadMost];
   const Fp8Cache& c = p.cache;

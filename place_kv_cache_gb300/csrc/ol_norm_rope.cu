@@ -31,7 +31,7 @@ template <>
 __device__ __forceinline__ uint16_t rounded_to<uint16_t>(float x) { return float_to_bf16_bits(x); }
 
 template <typename T, int VE>
-struct alignas(sizeof(T) * VE) Piece {
+struct alignas(sizeof(T) * VE < 16 ? sizeof(T) * VE : 16) Piece {  // of 16 bytes, or of two times 16
   T e[VE];
 };
 
@@ -51,26 +51,6 @@ struct Items {
   __device__ int second(int i, int rot) const { return HALF ? rot / 2 + i * VE : 2 * i + 1; }
 };
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t two_of(const float* x) { return pack2(x[0], x[1]); }
 __device__ __forceinline__ uint64_t two_of(const uint16_t* x) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(x);
@@ -101,7 +81,7 @@ constexpr int kWarps = 4;  // of a CTA, each with its own work
 // with the products of weights, cosines and sines in registers (elements past the
 // rotated part: cos 1, sin 0).
 template <typename T, int VE, bool HALF, int U>
-__global__ void __launch_bounds__(32 * kWarps, VE == 8 && HALF ? 6 : 8)
+__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 && (HALF || VE == 16) ? 6 : 8)
     norm_rope_warp_kernel(const __grid_constant__ NormRopeParams p, int lanes, int slices, int per_slice) {
   using P = Piece<T, VE>;
   using I = Items<VE, HALF>;
@@ -362,7 +342,7 @@ template <typename T, int VE, bool HALF>
 cudaError_t launch_warps(const NormRopeParams& p, int lanes, cudaStream_t s) {
   // 16 bytes of 16-bit pairs take twice the registers: two vectors in flight a lane spill (4 x 4096
   // tokens of 32 + 8 heads of 128 90 us, with one 66); fp32 (half of 3 x 2047 tokens of 32 heads of 96) 33 and 41.
-  constexpr int U = VE == 8 && HALF ? 1 : 2;
+  constexpr int U = sizeof(T) == 2 && (HALF || VE == 16) ? 1 : 2;
   const int heads = p.q_heads + p.kv_heads, tokens = p.batch * p.tokens, step = 32 / lanes * U;
   const int rounds = (heads + step - 1) / step;
   int slices = (kManyWarps + tokens - 1) / tokens;
@@ -381,8 +361,11 @@ cudaError_t launch_style(const NormRopeParams& p, cudaStream_t s) {
   while (lanes < 32 && lanes < items) lanes *= 2;
   if constexpr (VE > 1) {
     if (items <= 32) return launch_warps<T, VE, HALF>(p, lanes, s);
-    if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
-    return launch_items<T, VE, HALF, 8>(p, lanes, s);  // head_dim is 1024 at most
+    if constexpr (sizeof(T) * VE == 16) {
+      if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
+      return launch_items<T, VE, HALF, 8>(p, lanes, s);  // head_dim is 1024 at most
+    }
+    return cudaErrorInvalidValue;  // (not asked for)
   } else {
     if (items <= 32) return launch_items<T, VE, HALF, 1>(p, lanes, s);
     if (items <= 128) return launch_items<T, VE, HALF, 4>(p, lanes, s);
@@ -393,8 +376,11 @@ cudaError_t launch_style(const NormRopeParams& p, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_type(const NormRopeParams& p, cudaStream_t s) {
   constexpr int VE = 16 / sizeof(T);
-  if (p.style == OL_ROPE_HALF) return p.vec ? launch_style<T, VE, true>(p, s) : launch_style<T, 1, true>(p, s);
-  return p.vec ? launch_style<T, VE, false>(p, s) : launch_style<T, 1, false>(p, s);
+  if (!p.vec) return p.style == OL_ROPE_HALF ? launch_style<T, 1, true>(p, s) : launch_style<T, 1, false>(p, s);
+  if (p.style == OL_ROPE_HALF) return launch_style<T, VE, true>(p, s);
+  // Adjacent pairs: two pieces a lane, as the half style has, where they fit: half the steps of a sum.
+  if (p.rot_dim % (2 * VE) == 0 && p.head_dim % (2 * VE) == 0 && p.head_dim <= 64 * VE) return launch_style<T, 2 * VE, false>(p, s);
+  return launch_style<T, VE, false>(p, s);
 }
 
 }  // namespace
