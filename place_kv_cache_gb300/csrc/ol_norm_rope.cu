@@ -5,12 +5,18 @@
 //   rot_dim elements turn by their position's angle (ol_rope.cu has the table's
 //   arithmetic).
 //
-// Vectors of up to 32 items (16-byte pieces, see Items) go by warps: a warp has a
-// token and its vectors, or a slice of them, and nothing to wait for but its loads. A
-// group of lanes has a vector, a lane the same item of all of them, so its weights, sines
-// and cosines stay in registers (the groups compute a share of these each). Others, and
-// views without 16-byte alignment, go by CTAs that keep them in shared memory.
-// Bounds: 2 * D * elt bytes a vector: memory, or the launch for a decode step.
+// Vectors of up to 32 items (16-byte pieces or two of them, see WarpItems) go by warps: a
+// warp has a token and its vectors, or a slice of them, and nothing to wait for but its
+// loads. A group of lanes has a vector, a lane the same item of all of them, so its weights,
+// sines and cosines stay in registers (the groups compute a share of these each). Others,
+// and views without 16-byte alignment, go by CTAs that keep them in shared memory.
+//
+// Bounds: 2 * D * elt bytes a vector. 4 x 4096 tokens of 32 + 8 bf16 heads of 128: 63.6 us
+// (5.3 TB/s, 78 % of a copy's rate; CTAs with the tables in shared memory: 121); 3 x 2047
+// fp32 tokens of 28 + 4 heads of 96, 48 rotated: 31.9 us (4.7 TB/s). What is left is the
+// issue of about 10 instructions an element pair (2.4 to 2.9 a cycle) at 7 to 9 CTAs an SM.
+// A decode step (64 rows of one token) is the launch and its chain of loads, 2.8 us:
+// tokens fewer than kManyWarps are cut into slices of their vectors.
 #include "ol_common.cuh"
 #include "ol_fp8.h"
 
@@ -51,6 +57,20 @@ struct Items {
   __device__ int second(int i, int rot) const { return HALF ? rot / 2 + i * VE : 2 * i + 1; }
 };
 
+// The same for a warp's vectors: of the half style's tail two pieces as well, a half tail
+// apart, where it has an even number of them.
+template <int VE, bool HALF>
+struct WarpItems {
+  int rotated, total, apart;  // apart: of an item's two pieces past the rotated part; 0: it has one
+  __host__ __device__ WarpItems(int rot, int dim) {
+    const int tail = dim - rot;
+    rotated = HALF ? rot / 2 / VE : rot / VE;
+    apart = HALF && tail % (2 * VE) == 0 ? tail / 2 : 0;
+    total = rotated + tail / VE / (apart ? 2 : 1);
+  }
+  __device__ int first(int i, int rot) const { return i < rotated ? i * VE : rot + (i - rotated) * VE; }
+};
+
 __device__ __forceinline__ uint64_t two_of(const float* x) { return pack2(x[0], x[1]); }
 __device__ __forceinline__ uint64_t two_of(const uint16_t* x) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(x);
@@ -79,12 +99,16 @@ constexpr int kWarps = 4;  // of a CTA, each with its own work
 // item's pairs as
 //   (x, y) -> r (x (w_x cos, w_x sin) + y (-w_y sin, w_y cos)),   r = 1 / sqrt(mean + eps),
 // with the products of weights, cosines and sines in registers (elements past the
-// rotated part: cos 1, sin 0).
-template <typename T, int VE, bool HALF, int U>
-__global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 && (HALF || VE == 16) ? 6 : 8)
+// rotated part by their weights alone).
+template <typename T, int VE, bool HALF>
+constexpr int ctas_of() {  // of an SM: the best of 5 to 9 (a few bytes spilled cost less than fewer warps)
+  return sizeof(T) == 4 ? 9 : HALF || VE == 16 ? 7 : 6;
+}
+template <typename T, int VE, bool HALF, bool TAIL, int U>  // TAIL: past the rotated part there are elements
+__global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
     norm_rope_warp_kernel(const __grid_constant__ NormRopeParams p, int lanes, int slices, int per_slice) {
   using P = Piece<T, VE>;
-  using I = Items<VE, HALF>;
+  using I = WarpItems<VE, HALF>;
   constexpr int NP = HALF ? VE : VE / 2;  // pairs of an item
   __shared__ float2 turn[kWarps][32 * NP];
   const unsigned warp = blockIdx.x * kWarps + threadIdx.x / 32;  // (up to 2^31 + 2)
@@ -92,8 +116,8 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 && (HALF || VE == 
   const int token = warp / slices, slice = warp - token * slices;
   const int wl = threadIdx.x % 32, lane = wl & (lanes - 1), group = wl / lanes, groups = 32 / lanes;
   const I items(p.rot_dim, p.head_dim);
-  const bool mine = lane < items.total, rotated = lane < items.rotated, two = HALF && rotated;
-  const int ea = items.first(lane, p.rot_dim), eb = items.second(lane, p.rot_dim);
+  const bool mine = lane < items.total, rotated = TAIL ? lane < items.rotated : mine, two = HALF && mine && (rotated || items.apart);
+  const int ea = items.first(lane, p.rot_dim), eb = ea + (rotated ? p.rot_dim / 2 : items.apart);
   const int b = token / p.tokens, t = token - b * p.tokens;
   const float per = 1.f / p.head_dim;
   float2* const mine_turn = turn[threadIdx.x / 32] + lane * NP;
@@ -155,7 +179,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 && (HALF || VE == 
           cy[j % (HALF ? VE / 2 : 1)] = pack2(b0 * u.x, b1 * v.x);
         } else {
           const float2 u = rotated ? mine_turn[j % NP] : make_float2(1.f, 0.f);
-          cx[j] = pack2(a0 * u.x, a0 * u.y);
+          cx[j] = rotated ? pack2(a0 * u.x, a0 * u.y) : pack2(a0, a1);
           sy[j] = pack2(-a1 * u.y, a1 * u.x);
         }
       }
@@ -194,18 +218,24 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 2 && (HALF || VE == 
 #pragma unroll
         for (int j = 0; j < VE / 2; ++j) {
           if (HALF) {
-            put_two(&y.e[2 * j], mul2(r2, fma2(vb[u][j % (HALF ? VE / 2 : 1)], sy[j], mul2(va[u][j], cx[j]))));
+            uint64_t v = mul2(va[u][j], cx[j]);
+            if (!TAIL || rotated) v = fma2(vb[u][j % (HALF ? VE / 2 : 1)], sy[j], v);  // (0 times an infinity elsewhere)
+            put_two(&y.e[2 * j], mul2(r2, v));
           } else {
-            const float2 v = unpack2(va[u][j]);
-            put_two(&y.e[2 * j], mul2(r2, fma2(pack2(v.y, v.y), sy[j], mul2(pack2(v.x, v.x), cx[j]))));
+            const float2 e = unpack2(va[u][j]);
+            uint64_t v = mul2(pack2(e.x, !TAIL || rotated ? e.x : e.y), cx[j]);
+            if (!TAIL || rotated) v = fma2(pack2(e.y, e.y), sy[j], v);
+            put_two(&y.e[2 * j], mul2(r2, v));
           }
         }
         *reinterpret_cast<P*>(to) = y;
         if (HALF && two) {
 #pragma unroll
-          for (int j = 0; j < VE / 2; ++j)
-            put_two(&y.e[2 * j], mul2(r2, fma2(vb[u][j % (HALF ? VE / 2 : 1)], cy[j % (HALF ? VE / 2 : 1)],
-                                               mul2(va[u][j], sx[j % (HALF ? VE / 2 : 1)]))));
+          for (int j = 0; j < VE / 2; ++j) {
+            uint64_t v = mul2(vb[u][j % (HALF ? VE / 2 : 1)], cy[j % (HALF ? VE / 2 : 1)]);
+            if (!TAIL || rotated) v = fma2(va[u][j], sx[j % (HALF ? VE / 2 : 1)], v);
+            put_two(&y.e[2 * j], mul2(r2, v));
+          }
           *reinterpret_cast<P*>(to + (eb - ea)) = y;
         }
       }
@@ -340,9 +370,10 @@ cudaError_t launch_items(const NormRopeParams& p, int lanes, cudaStream_t s) {
 
 template <typename T, int VE, bool HALF>
 cudaError_t launch_warps(const NormRopeParams& p, int lanes, cudaStream_t s) {
-  // 16 bytes of 16-bit pairs take twice the registers: two vectors in flight a lane spill (4 x 4096
-  // tokens of 32 + 8 heads of 128 90 us, with one 66); fp32 (half of 3 x 2047 tokens of 32 heads of 96) 33 and 41.
-  constexpr int U = sizeof(T) == 2 && (HALF || VE == 16) ? 1 : 2;
+  // Two pieces of a vector a lane: a second vector in flight spills (4 x 4096 tokens of 32 + 8
+  // heads of 128, half style: bf16 90 us, with one 66; fp32 122 and 108). One piece: it pays
+  // (interleaved bf16 of 136 111 us, with one 120; fp32 of 100 97 and 124).
+  constexpr int U = HALF || sizeof(T) * VE == 32 ? 1 : 2;
   const int heads = p.q_heads + p.kv_heads, tokens = p.batch * p.tokens, step = 32 / lanes * U;
   const int rounds = (heads + step - 1) / step;
   int slices = (kManyWarps + tokens - 1) / tokens;
@@ -350,13 +381,15 @@ cudaError_t launch_warps(const NormRopeParams& p, int lanes, cudaStream_t s) {
   const int per_slice = (rounds + slices - 1) / slices * step;
   slices = (heads + per_slice - 1) / per_slice;
   const long long warps = (long long)tokens * slices;
-  return launch_pdl(norm_rope_warp_kernel<T, VE, HALF, U>, (unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, 0, s, p,
-                    lanes, slices, per_slice);
+  const auto kernel = p.rot_dim == p.head_dim ? norm_rope_warp_kernel<T, VE, HALF, false, U> : norm_rope_warp_kernel<T, VE, HALF, true, U>;
+  return launch_pdl(kernel, (unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, 0, s, p, lanes, slices, per_slice);
 }
 
 template <typename T, int VE, bool HALF>
 cudaError_t launch_style(const NormRopeParams& p, cudaStream_t s) {
-  const int items = Items<VE, HALF>(p.rot_dim, p.head_dim).total;
+  int items = Items<VE, HALF>(p.rot_dim, p.head_dim).total;
+  const int warp_items = VE > 1 ? WarpItems<VE, HALF>(p.rot_dim, p.head_dim).total : 64;
+  if (warp_items < items && warp_items <= 32) items = warp_items;
   int lanes = 1;
   while (lanes < 32 && lanes < items) lanes *= 2;
   if constexpr (VE > 1) {

@@ -136,6 +136,23 @@ def test_zeros_large_and_nonfinite_vectors_stay_apart():
     assert bool((y[0, 1] == 0).all())
 
 
+@STYLES
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("D, rot", [(128, 64), (96, 48), (80, 64), (64, 16), (72, 16), (120, 104), (48, 16)])
+def test_an_infinity_past_the_rotated_part(D, rot, dt, style):
+    """The vector's norm is infinite: every other element, its neighbours of the tail among them, comes out as 0."""
+    x = torch.randn((1, 3, 1, D), device=DEV, dtype=TORCH[dt])
+    for at in (rot, D - 1, (rot + D) // 2):
+        z = x.clone()
+        z[0, 1, 0, at] = float("-inf")
+        y = torch.full_like(x, 3.0)
+        ol.ol_norm_rope_rows(ol.rope(rot, style=style, device=DEV), ol.head_norm(), CODE[TORCH[dt]], 1, 1, D, 3, z, y, 0,
+                             None, None, torch.tensor([9], dtype=torch.int32, device=DEV), False)
+        rest = torch.arange(D, device=DEV) != at
+        assert bool(torch.isnan(y[0, 1, 0, at])) and bool((y[0, 1, 0][rest] == 0).all())
+        assert bool((y[0, ::2].abs() > 0).any(-1).all()) and bool(torch.isfinite(y[0, ::2]).all())
+
+
 def test_streams_graphs_and_two_rotations():
     """A captured call replays with the positions it finds; calls on two streams at once keep apart."""
     B, H, T, D = 4, 8, 1, 128
