@@ -1,8 +1,9 @@
 // ol_fast_fp8.cu -- attention over an E4M3 cache on the 5th generation tensor
-// cores: bf16 queries, head_dim 64 or 128, contiguous cache or paged pool.
+// cores: bf16 queries, contiguous cache or paged pool.
 //
-// A unit is NC = 8, 16 or 32 (head, query) columns c = head * count + query of one
-// row's kv head (queries that the row has not take no part). Its tokens form tiles of 128; equal contiguous shares of all
+// A unit is NC = 8, 16 or 32 (head, query) columns c = head * count + query of one row's
+// kv head (queries that the row has not take no part). Its tokens form tiles of 128; equal
+// contiguous shares of all
 // units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh): while one ends a
 // segment or waits, the other has the SM. K and V go to the tensor cores as they lie
 // in the cache, with the tokens (for V the dimensions) as the products' 128 rows, so
@@ -21,12 +22,27 @@
 // passes it by 2^3; O = sum of the parts' columns over 16^k. The segments' merge knows
 // states (m, l, o) as those of the tree kernels.
 //
+// Heads that are not 64 or 128 are taken as the next of 64, 128 and 256, with zeros behind
+// (the copies' own: no bytes are read for them). One of 256 has two halves of K, V and Q'
+// (rows of 128 bytes are what a swizzle holds) and two accumulators O.
+//
 // Warps: 0 the walk and the producer (TMA, a lane per box of a tile), 1 MMA issue (and
 // zeros for V's rows outside the row's tokens: P = 0 times a NaN code must not be NaN),
 // 2 the tiles' scales, 3 the queries' parts, 4-7 the softmax; of 32 columns in two groups
-// of four warps, 16 columns each (more warps to hide each other's latencies). The others learn of the
-// segments from the first, through a ring: the walk in line in each of them, and the
-// loops of waits (wait_long), made the kernel outgrow the instruction cache.
+// of four warps, 16 columns each (more warps to hide each other's latencies: 64 queries over
+// 8 rows to 6000 tokens 138 and 69 us). The others learn of the segments from the first,
+// through a ring: the walk in line in each of them, and the loops of waits (wait_long), made
+// the kernel outgrow the instruction cache (258 and 160 us for the first line below).
+//
+// Bounds and times (us; 8 kv heads, 4 query heads each, unless said otherwise):
+//   64 rows of 8192, 1 query          161   memory: 6.7 TB/s of codes, 99 % of a copy's rate
+//   the same in pages of 16           171   6.3 TB/s: boxes of 2 KB
+//   64 rows to 16384, pages of 16     183   5.9 TB/s: ragged ends beside the above
+//   heads of 256, 64 rows of 4096     166   6.5 TB/s
+//   heads of 64, 64 rows of 8192       97   5.6 TB/s: the softmax warps' chain of a tile
+//   heads of 80, 64 rows of 8192      236   2.8 TB/s: rows that straddle lines in the copies
+//   the first with 4 / 8 queries      165 / 220   the conversion of P, 64 bits of parts a column
+//   1 row of 4097, 7 heads a kv head   12   the chain walk, first tile, two tiles, merge
 #include "ol_fp8.cuh"
 #include "ol_tree.cuh"
 
@@ -42,15 +58,18 @@ constexpr float kTop = 5.f;       // log2 of the largest P when a reference is s
 constexpr float kGrown = 8.f;     // and of what makes a new one necessary
 constexpr int kMostSmem = (233472 - 2 * 1024) / 2;  // of one of two CTAs
 
+// D: 64, 128 or 256 elements, what heads up to it take: the copies put zeros behind a
+// row of the cache, and there are none of its bytes to read.
 template <int D, int NC>
 struct Lay {
-  static constexpr int kTileBytes = kTile * D;
-  static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries
+  static constexpr int kHalves = D == 256 ? 2 : 1, W = D / kHalves;  // of a row, W bytes each: what a swizzled row holds
+  static constexpr int kTileBytes = kTile * W;          // a slot of the ring
+  static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries; [halves] of it
   static constexpr int kPBytes = kTile * 4 * NC;        // four parts of P
   static constexpr int kQBuffers = NC == 32 ? 1 : 2;    // (room for one more tile of K or V)
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + kQBuffers * kQBytes;
-  static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn
+  static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn, half after half
   static constexpr int kSmall = 1536 + NC * 112;          // what follows the ring, at most
   static constexpr int kFit = (kMostSmem - kSmall - kRing) / kTileBytes;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
@@ -70,7 +89,8 @@ struct Lay {
   static constexpr int kTotal = kMisc + 8;
   static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of two CTAs");
   static_assert(kRing % 1024 == 0 && kP % 1024 == 0 && kQBytes % 512 == 0, "swizzled tiles");
-  static constexpr int kTmem = 8 * NC;  // columns: two S of 2 NC, O of 4 NC; 64, 128 or 256
+  static constexpr int kTmem = 8 * NC * kHalves;  // columns: two S of 2 NC, O of 4 NC a half; 64, 128 or 256
+  static_assert(kTmem <= 256, "of one of two CTAs");
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -199,6 +219,9 @@ struct Cursor {
       slot = 0;
       phase ^= 1;
     }
+  }
+  __device__ __forceinline__ void skip(int n) {
+    for (; n > 0; --n) next();
   }
 };
 
@@ -422,12 +445,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       return (bad ? 0 : t.page) * fc.kv_heads * fc.page_size + t.y;
     };
     Cursor<L::kSlots> ring;
-    auto load = [&](int y) {
+    auto load = [&](int x, int y) {
       if (!warp_wait(bar.empty(ring.slot), ring.phase ^ 1, abort, p.status)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(bar.full(ring.slot), (uint32_t)(cur.last - cur.first) * box * D);
+      if (lane == 0) mbar_arrive_expect_tx(bar.full(ring.slot), (uint32_t)(cur.last - cur.first) * box * L::W);
       __syncwarp();
       if (lane >= cur.first && lane < cur.last)
-        tma_load_2d(sa + L::kRing + ring.slot * L::kTileBytes + lane * box * D, &map, 0, y, bar.full(ring.slot), policy);
+        tma_load_2d(sa + L::kRing + ring.slot * L::kTileBytes + lane * box * L::W, &map, x, y, bar.full(ring.slot), policy);
       ring.next();
       return true;
     };
@@ -450,7 +473,9 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       }
       if (cur.more) {
         const int y = cache_row_of(cur);
-        ok = load(y) && load(y + v_rows);
+        for (int plane = 0; plane < 2; ++plane)
+#pragma unroll
+          for (int x = 0; x < D; x += L::W) ok = ok && load(x, y + plane * v_rows);
       } else if (ended && !ahead[1].more && !ahead[2].more) {
         break;
       }
@@ -462,34 +487,50 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     // The whole warp walks and waits, so that what the products are given stays in
     // uniform registers; one elected lane issues them.
     constexpr uint32_t kDescS = mma_desc(2 * NC, false), kDescO = mma_desc(4 * NC, true);
-    constexpr uint32_t kRowSwizzle = D == 128 ? kSwizzle128 : kSwizzle64;  // rows of D bytes: K, V, Q'
+    constexpr uint32_t kRowSwizzle = L::W == 128 ? kSwizzle128 : kSwizzle64;  // rows of W bytes: K, V, Q'
     constexpr uint32_t kPSwizzle = NC == 32 ? kSwizzle128 : NC == 16 ? kSwizzle64 : kSwizzle32;
     const uint32_t tm = uniform(tmem), base = uniform(sa);
     Cursor<L::kSlots> k, v;  // slots of the next S's K, of the next product's V
-    v.next();
+    v.skip(L::kHalves);
     uint32_t seg = 0, s_count = 0, p_count = 0;
     bool ok = true;
     const auto s_phase = [&] { return s_count >> 1 & 1; };
     auto scores = [&](bool last) {  // S of the next tile, into the next buffer
       tmem_fence_after();
       if (elect_one()) {
-        const uint64_t kd = smem_desc(base + L::kRing + k.slot * L::kTileBytes, 16, 8 * D, kRowSwizzle);
-        const uint64_t qd = smem_desc(base + L::kQ + q_buffer(seg) * L::kQBytes, 16, 8 * D, kRowSwizzle);
+        Cursor<L::kSlots> half = k;
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) mma_fp8(tm + (s_count & 1) * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, x > 0);
+        for (int h = 0; h < L::kHalves; ++h, half.next()) {
+          const uint64_t kd = smem_desc(base + L::kRing + half.slot * L::kTileBytes, 16, 8 * L::W, kRowSwizzle);
+          const uint64_t qd =
+              smem_desc(base + L::kQ + q_buffer(seg) * L::kQBytes + h * 2 * NC * L::W, 16, 8 * L::W, kRowSwizzle);
+#pragma unroll
+          for (int x = 0; x < L::W / 32; ++x)
+            mma_fp8(tm + (s_count & 1) * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, h > 0 || x > 0);
+          mma_commit(bar.empty(half.slot));
+        }
         mma_commit(bar.s_full(s_count & 1));
-        mma_commit(bar.empty(k.slot));
         if (last) mma_commit(bar.q_empty(q_buffer(seg)));
       }
       __syncwarp();
       ++s_count;
-      k.next();
-      k.next();
+      k.skip(2 * L::kHalves);
     };
     // (a buffer's first S finds it free: the phase before the first)
     auto scores_wait = [&] {
-      return warp_wait(bar.s_free(s_count & 1), s_phase() ^ 1, abort, p.status) &&
-             warp_wait(bar.full(k.slot), k.phase, abort, p.status);
+      bool there = warp_wait(bar.s_free(s_count & 1), s_phase() ^ 1, abort, p.status);
+      Cursor<L::kSlots> half = k;
+#pragma unroll
+      for (int h = 0; h < L::kHalves; ++h, half.next())
+        there = there && warp_wait(bar.full(half.slot), half.phase, abort, p.status);
+      return there;
+    };
+    auto scores_ready = [&] {
+      bool there = mbar_test(bar.s_free(s_count & 1), s_phase() ^ 1);
+      Cursor<L::kSlots> half = k;
+#pragma unroll
+      for (int h = 0; h < L::kHalves; ++h, half.next()) there = there && mbar_test(bar.full(half.slot), half.phase);
+      return __all_sync(0xffffffffu, there);
     };
     Seg g;
     while (next_seg(g, ok)) {
@@ -501,18 +542,24 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       for (int i = 0; ok && i < tiles; ++i, r_low -= kTile, r_end -= kTile) {
         // the next tile's S ahead of this one's sums, if its K is there
         bool issued = i + 1 == tiles;
-        if (!issued && __all_sync(0xffffffffu, mbar_test(bar.s_free(s_count & 1), s_phase() ^ 1) &&
-                                                   mbar_test(bar.full(k.slot), k.phase))) {
+        if (!issued && scores_ready()) {
           scores(i + 2 == tiles);
           issued = true;
         }
-        if (!(ok = warp_wait(bar.full(v.slot), v.phase, abort, p.status))) break;
+        Cursor<L::kSlots> half = v;
+#pragma unroll
+        for (int h = 0; h < L::kHalves; ++h, half.next()) ok = ok && warp_wait(bar.full(half.slot), half.phase, abort, p.status);
+        if (!ok) break;
         if (r_low > 0 || r_end < kTile) {
-          uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + v.slot * L::kTileBytes);
+          half = v;
 #pragma unroll 1
-          for (int x = lane; x < kTile * D / 16; x += 32) {
-            const int r = x / (D / 16);
-            if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
+          for (int h = 0; h < L::kHalves; ++h, half.next()) {
+            uint4* const tile = reinterpret_cast<uint4*>(smem + L::kRing + half.slot * L::kTileBytes);
+#pragma unroll 1
+            for (int x = lane; x < kTile * L::W / 16; x += 32) {
+              const int r = x / (L::W / 16);
+              if (r < r_low || r >= r_end) tile[x] = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -521,18 +568,21 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         ++p_count;
         tmem_fence_after();
         if (elect_one()) {
-          // V's second half of the 128 rows is its first again where D is 64
-          const uint64_t vd = smem_desc(base + L::kRing + v.slot * L::kTileBytes, 0, 8 * D, kRowSwizzle);
+          // V's second half of the 128 rows is its first again where W is 64
           const uint64_t pd = smem_desc(base + L::kP, 0, 8 * 4 * NC, kPSwizzle);
+          half = v;
 #pragma unroll
-          for (int x = 0; x < kTile / 32; ++x)
-            mma_fp8(tm + 4 * NC, vd + x * (32 * D / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 0 || x > 0);
+          for (int h = 0; h < L::kHalves; ++h, half.next()) {
+            const uint64_t vd = smem_desc(base + L::kRing + half.slot * L::kTileBytes, 0, 8 * L::W, kRowSwizzle);
+#pragma unroll
+            for (int x = 0; x < kTile / 32; ++x)
+              mma_fp8(tm + (h + 1) * 4 * NC, vd + x * (32 * L::W / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 0 || x > 0);
+            mma_commit(bar.empty(half.slot));
+          }
           mma_commit(bar.p_taken());
-          mma_commit(bar.empty(v.slot));
         }
         __syncwarp();
-        v.next();
-        v.next();
+        v.skip(2 * L::kHalves);
         if (!issued && (ok = scores_wait())) scores(i + 2 == tiles);
       }
       if (!ok) break;
@@ -616,9 +666,9 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 3) {
     // ------------------------------------------------------------ queries' parts
-    // Q': rows [part][column] of D bytes, swizzled. Four lanes have a column, E elements each.
+    // Q': rows [half][part][column] of W bytes, swizzled. Four lanes have a column, E elements each.
     constexpr int E = D / 4;
-    const int part = lane & 3;
+    const int part = lane & 3, pieces = p.head_dim / 8 - part * (E / 8);  // of 8 elements that there are
     uint32_t seg = 0;
     bool ok = true;
     Seg g;
@@ -627,7 +677,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
       Col* const cols = reinterpret_cast<Col*>(smem + L::kCols) + buf * NC;
       const uint4* const q =
-          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * D) + part * (E / 8);
+          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * p.head_dim) + part * (E / 8);
       uint4 x[E / 8], next[E / 8];
       int query, live, next_query, next_live;
       auto load = [&](int c) {
@@ -635,7 +685,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         next_query = r0 + c - head * g.count;
         next_live = head * p.nodes + next_query;
 #pragma unroll
-        for (int e = 0; e < E / 8; ++e) next[e] = r0 + c < R ? q[(size_t)next_live * (D / 8) + e] : make_uint4(0, 0, 0, 0);
+        for (int e = 0; e < E / 8; ++e) next[e] = r0 + c < R && e < pieces ? q[(size_t)next_live * (p.head_dim / 8) + e] : make_uint4(0, 0, 0, 0);
       };
       load(lane >> 2);
       if (!(ok = warp_wait(bar.q_empty(buf), q_phase(seg) ^ 1, abort, p.status))) break;
@@ -659,7 +709,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         const int up = min(7 - ((int)(top >> 23) - 127), 126);
         const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
         const bool finite = top < 0x7f800000u;  // else: NaN codes, so that the column's outputs are NaN
-        const int sw = D == 128 ? c & 7 : c >> 1 & 3;  // (of both parts' rows: NC is a multiple of 8)
+        const int sw = L::W == 128 ? c & 7 : c >> 1 & 3;  // (of both parts' rows: NC is a multiple of 8)
 #pragma unroll
         for (int e = 0; e < E / 8; ++e) {
           const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
@@ -672,10 +722,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             hi[k / 2] |= two << (k % 2 * 16);
             lo[k / 2] |= (finite ? e4m3x2((u - h.x) * 16.f, (v - h.y) * 16.f) : 0) << (k % 2 * 16);
           }
-          const int d = part * E + e * 8;
-          uint8_t* const at = to + c * D + ((d / 16 ^ sw) << 4) + d % 16;
+          const int d = part * E + e * 8, in = d % L::W;
+          uint8_t* const at = to + (d / L::W * 2 * NC + c) * L::W + ((in / 16 ^ sw) << 4) + in % 16;
           *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(at + NC * D) = make_uint2(lo[0], lo[1]);
+          *reinterpret_cast<uint2*>(at + NC * L::W) = make_uint2(lo[0], lo[1]);
         }
         if (part == 0) cols[c] = Col{1.f / factor, query, live, 0};
       }
@@ -686,10 +736,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
   } else {
     // ----------------------------------------------------------------- softmax
     constexpr int kMine = L::kMine;
-    const int me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of O
+    const int me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of a half of O
     const int group = me / 4, first = group * kMine;  // this group's columns
     const uint32_t lanes = (uint32_t)(me % 4 * 32) << 16;
-    const uint32_t to = tmem + 4 * NC + first + lanes;  // O of these columns, the parts NC apart
+    const uint32_t to = tmem + 4 * NC + first + lanes;  // O of these columns, the parts NC apart, the halves 4 NC
     float* const tab = reinterpret_cast<float*>(smem + L::kTab) + me * kMine * 2;  // of two columns: factors, minus references
     float* const mine = tab + lane % kMine / 2 * 4 + lane % 2;
     float* const tops = reinterpret_cast<float*>(smem + L::kTops) + group * 4 * kMine;
@@ -750,36 +800,36 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         float y[kMine];
         for (bool looked = false;;) {
           if (i > 0 || looked) {  // (a segment's first tile has nothing to compare with)
-          const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
+            const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
-          for (int c0 = 0; c0 < kMine; c0 += kStep) {
-            uint32_t hi[kStep], lo[kStep];
-            tmem_ld8(ts + c0, hi);
-            tmem_ld8(ts + NC + c0, lo);
-            tmem_wait_ld8(hi);
-            tmem_wait_ld8(lo);
+            for (int c0 = 0; c0 < kMine; c0 += kStep) {
+              uint32_t hi[kStep], lo[kStep];
+              tmem_ld8(ts + c0, hi);
+              tmem_ld8(ts + NC + c0, lo);
+              tmem_wait_ld8(hi);
+              tmem_wait_ld8(lo);
 #pragma unroll
-            for (int c = 0; c < kStep; c += 2) {
-              const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(tab + (c0 + c) * 2);
-              const uint64_t s0 = pack2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1]));
-              const uint64_t s1 = pack2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1]));
-              const float2 z = unpack2(fma2(mul2(fma2(s1, part2, s0), k2), f.x, add2(v2, f.y)));
-              y[c0 + c] = z.x;
-              y[c0 + c + 1] = z.y;
+              for (int c = 0; c < kStep; c += 2) {
+                const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(tab + (c0 + c) * 2);
+                const uint64_t s0 = pack2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1]));
+                const uint64_t s1 = pack2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1]));
+                const float2 z = unpack2(fma2(mul2(fma2(s1, part2, s0), k2), f.x, add2(v2, f.y)));
+                y[c0 + c] = z.x;
+                y[c0 + c + 1] = z.y;
+              }
             }
-          }
-          if (edge)
+            if (edge)
 #pragma unroll
-            for (int c = 0; c < kMine; ++c)
-              if (hidden >> c & 1) y[c] = -INFINITY;
-          if (looked) break;
-          float most4[4] = {y[0], y[1], y[2], y[3]};
+              for (int c = 0; c < kMine; ++c)
+                if (hidden >> c & 1) y[c] = -INFINITY;
+            if (looked) break;
+            float most4[4] = {y[0], y[1], y[2], y[3]};
 #pragma unroll
-          for (int c = 4; c < kMine; ++c) most4[c % 4] = fmaxf(most4[c % 4], y[c]);
-          const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
-          // (the flag holds the number of the tile that raised it)
-          if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
-          if (!(ok = vote()) || flag[count & 1] != count) break;
+            for (int c = 4; c < kMine; ++c) most4[c % 4] = fmaxf(most4[c % 4], y[c]);
+            const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
+            // (the flag holds the number of the tile that raised it)
+            if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
+            if (!(ok = vote()) || flag[count & 1] != count) break;
           }
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
 #pragma unroll 1
@@ -813,8 +863,8 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;
             tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < 4 * kMine; x += 4) {
-              const int part = x / kMine, c = x - part * kMine;
+            for (int x = 0; x < 4 * kMine * L::kHalves; x += 4) {
+              const int part = x / kMine, c = x - part * kMine;  // (of both halves)
               uint32_t o[4];
               tmem_ld4(to + part * NC + c, o);
               tmem_wait_ld4(o);
@@ -894,12 +944,14 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       tmem_fence_after();
       float* const slot = g.slot < 0 ? nullptr : tree_slot(p, g.slot);
       const int live = p.group * g.count - g.qg * NC - first;  // columns that there are
-      const size_t out = tree_out_row(p, g.b, g.g, 0) * D + row;
+      const size_t out = tree_out_row(p, g.b, g.g, 0) * p.head_dim;
 #pragma unroll 1
-      for (int c0 = 0; c0 < kMine && c0 < live; c0 += 4) {
+      for (int x = 0; x < kMine * L::kHalves; x += 4) {
+        const int c0 = x % kMine, half = x / kMine, d = half * 128 + row;
+        if (c0 >= live) continue;
         uint32_t o[4][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld4(to + k * NC + c0, o[k]);
+        for (int k = 0; k < 4; ++k) tmem_ld4(to + half * 4 * NC + k * NC + c0, o[k]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_wait_ld4(o[k]);
 #pragma unroll
@@ -909,13 +961,13 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
           const float sum = fmaf(fmaf(fmaf(__uint_as_float(o[3][c]), 0.0625f, __uint_as_float(o[2][c])), 0.0625f,
                                       __uint_as_float(o[1][c])), 0.0625f, __uint_as_float(o[0][c]));
           if (slot) {
-            if (row == 0) {
+            if (d == 0) {
               slot[place] = -tab[col / 2 * 4 + 2 + col % 2];
               slot[NC + place] = grow[col];
             }
-            if (row < D) slot[2 * NC + ((size_t)(row / 4) * NC + place) * 4 + row % 4] = sum;
-          } else if (row < D) {
-            store_out(p.out, p.out_dtype, out + (size_t)cols[col].row * D, sum * grow[col]);
+            if (d < p.head_dim) slot[2 * NC + ((size_t)(d / 4) * NC + place) * 4 + d % 4] = sum;
+          } else if (d < p.head_dim) {
+            store_out(p.out, p.out_dtype, out + (size_t)cols[col].row * p.head_dim + d, sum * grow[col]);
           }
         }
       }
@@ -953,16 +1005,16 @@ uint64_t code_rows(const Fp8Cache& c) {
   return c.block_table ? 2ull * c.num_pages * c.kv_heads * c.page_size : 2ull * c.batch * c.kv_heads * c.capacity;
 }
 
-// The codes as rows of D bytes; boxes of `box` rows, swizzled by the row's size.
-bool encode_codes(CUtensorMap* map, const Fp8Cache& c, int box) {
+// The codes as rows of head_dim bytes; boxes of `box` rows and `width` bytes (zeros past head_dim).
+bool encode_codes(CUtensorMap* map, const Fp8Cache& c, int box, int width) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, code_rows(c)};
   cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
-  cuuint32_t boxes[2] = {(cuuint32_t)c.head_dim, (cuuint32_t)box};
+  cuuint32_t boxes[2] = {(cuuint32_t)width, (cuuint32_t)box};
   cuuint32_t estr[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -981,7 +1033,10 @@ cudaError_t launch_cfg(const CUtensorMap& map, const Fp8AttnParams& p, int box, 
 
 template <int D, bool PAGED>
 cudaError_t launch_cols(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
-  return p.t.rows_per_unit == 8    ? launch_cfg<D, 8, PAGED>(map, p, box, s)
+  if constexpr (D == 256)
+    return p.t.rows_per_unit == 8 ? launch_cfg<D, 8, PAGED>(map, p, box, s) : launch_cfg<D, 16, PAGED>(map, p, box, s);
+  else
+    return p.t.rows_per_unit == 8    ? launch_cfg<D, 8, PAGED>(map, p, box, s)
          : p.t.rows_per_unit == 16 ? launch_cfg<D, 16, PAGED>(map, p, box, s)
                                    : launch_cfg<D, 32, PAGED>(map, p, box, s);
 }
@@ -994,7 +1049,7 @@ cudaError_t launch_dim(const CUtensorMap& map, const Fp8AttnParams& p, int box, 
 }  // namespace
 
 bool fast_fp8_supported(const Fp8AttnParams& p) {
-  if (p.t.dtype != OL_BF16 || (p.t.head_dim != 64 && p.t.head_dim != 128)) return false;
+  if (p.t.dtype != OL_BF16) return false;
   const uint64_t rows = code_rows(p.cache);
   return rows > 0 && rows < (1ull << 31);  // TMA row coordinates are 32-bit
 }
@@ -1002,7 +1057,7 @@ bool fast_fp8_supported(const Fp8AttnParams& p) {
 void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   TreeParams& p = fp.t;
   const int columns = p.group * p.nodes;
-  p.rows_per_unit = columns <= 8 ? 8 : columns <= 16 ? 16 : 32;
+  p.rows_per_unit = columns <= 8 ? 8 : columns <= 16 || p.head_dim > 128 ? 16 : 32;  // (TMEM has no room for 32 of two halves)
   p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
@@ -1012,9 +1067,9 @@ void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   // (every share, and the CTAs' two places beyond, has a note and two partial slots in the workspace of a tree call)
   // Where the memory sets the pace, SMs differ in what they get of it: the last shares are for those that are ahead.
   // (64 rows of 8192 tokens, one query of 4 heads a kv head: 166 us, with the pool 161; ragged rows to 16384 in pages of
-  // 16 189 and 183.) Where the SM itself does, shares are equal as they are (16 columns 167 and 185 us, heads of 64
-  // 105 and 110).
-  p.pool = p.rows_per_unit > 8 || p.head_dim < 128 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
+  // 16 189 and 183; heads of 80 242 and 236.) Where the SM itself does, shares are equal as they are (16 columns 167 and
+  // 185 us, heads of 64 105 and 110).
+  p.pool = p.rows_per_unit > 8 || p.head_dim <= 64 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
   p.by_unit = tree_few_units(p);
 }
 
@@ -1024,8 +1079,9 @@ cudaError_t launch_fast_fp8(const Fp8AttnParams& p, cudaStream_t s) {
   if (p.cache.block_table)
     while (p.cache.page_size % box != 0) box /= 2;  // (a page is a multiple of 16 tokens)
   CUtensorMap map;
-  if (!encode_codes(&map, p.cache, box)) return cudaErrorInvalidValue;
-  return p.t.head_dim == 128 ? launch_dim<128>(map, p, box, s) : launch_dim<64>(map, p, box, s);
+  const int dim = p.t.head_dim;
+  if (!encode_codes(&map, p.cache, box, dim > 64 ? 128 : 64)) return cudaErrorInvalidValue;
+  return dim > 128 ? launch_dim<256>(map, p, box, s) : dim > 64 ? launch_dim<128>(map, p, box, s) : launch_dim<64>(map, p, box, s);
 }
 
 }  // namespace ol

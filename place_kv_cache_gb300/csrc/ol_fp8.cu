@@ -1,6 +1,6 @@
 // ol_fp8.cu -- the E4M3 cache: the append that quantises, reading back, and
-// attention on CUDA cores (fp32 queries, head sizes that the tensor-core kernel of
-// ol_fast_fp8.cu does not take).
+// attention on CUDA cores (fp32 queries, caches of more vectors than the tensor-core kernel of
+// ol_fast_fp8.cu counts).
 #include <type_traits>
 
 #include "ol_fp8.cuh"

@@ -309,7 +309,7 @@ class Attention:
         ol.ol_workspace_init(self.ws, self.ws_bytes)
         self.out_buf, payload = guarded(self.q.numel() * self.out_dtype.itemsize)
         self.out = payload.view(self.out_dtype).view(self.q.shape).fill_(-77.0)
-        self.tensor_cores = self.dtype == torch.bfloat16 and D in (64, 128)
+        self.tensor_cores = self.dtype == torch.bfloat16
 
     def call(self, scale=0.0, stream=None, out=None, ws=None):
         c = self.c
@@ -372,6 +372,14 @@ SHAPES = [
     ("f32", 3, 8, 2, 80, 16, 16, 4, [0, 4, 70], [0, 4, 1], -1, None),
     ("bf16", 3, 28, 4, 128, 32, 32, 512, [512, 600, 900], [512, 1, 77], -1, None),
     ("bf16", 2, 64, 1, 64, 64, 0, 7, [300, 1000], [7, 3], 64, "f32"), ("bf16", 33, 4, 4, 128, 16, 0, 1, [9] * 33, None, 3, None),
+    # heads that the tensor cores take with zeros behind, and those of two halves
+    ("bf16", 3, 8, 2, 16, 16, 16, 3, [50, 400, 3], None, -1, "f32"), ("bf16", 2, 28, 4, 48, 32, 0, 2, [131, 700], None, 90, None),
+    ("bf16", 2, 16, 2, 80, 128, 0, 1, [1000, 129], None, -1, "f32"), ("bf16", 2, 8, 1, 96, 16, 48, 9, [300, 60], [9, 4], -1, None),
+    ("bf16", 5, 8, 2, 112, 16, 16, 3, [0, 3, 700, 0, 33], [0, 3, 1, 0, 2], -1, "f32"),
+    ("bf16", 2, 4, 2, 144, 16, 16, 2, [257, 31], None, -1, "f32"), ("bf16", 2, 8, 2, 160, 64, 64, 4, [600, 64], None, 130, None),
+    ("bf16", 1, 28, 4, 256, 128, 0, 1, [4097], None, -1, "f32"), ("bf16", 4, 32, 8, 256, 16, 16, 1, [128, 127, 1000, 3], None, -1, None),
+    ("bf16", 3, 28, 4, 256, 32, 32, 40, [512, 600, 90], [40, 1, 17], -1, None),
+    ("bf16", 2, 16, 1, 240, 64, 128, 7, [900, 7], None, 20, "f32"),
 ]
 
 
@@ -385,7 +393,8 @@ def test_attention(case):
     a.check(scale=0.3)
 
 
-@pytest.mark.parametrize("Hq,H,D,T,seed", [(8, 8, 128, 1, 1), (28, 4, 128, 3, 2), (16, 2, 64, 9, 3), (12, 4, 96, 2, 4)])
+@pytest.mark.parametrize("Hq,H,D,T,seed", [(8, 8, 128, 1, 1), (28, 4, 128, 3, 2), (16, 2, 64, 9, 3), (12, 4, 96, 2, 4), (8, 2, 80, 3, 5),
+                                           (8, 8, 256, 2, 6), (28, 4, 192, 3, 7)])
 def test_drawn_rows(Hq, H, D, T, seed):
     """Batches past one warp's, of lengths and counts of every kind, in pages in any order."""
     rng = np.random.default_rng(seed)
@@ -465,7 +474,7 @@ def test_past_32_bit_offsets(D, C):
         for g in range(H):
             wide = [s[g].repeat_interleave(block)[:m] for _, s in want]
             exact, *sizes = fu.attention(q[0, 2 * g: 2 * g + 2], want[0][0][g], wide[0], want[1][0][g], wide[1], ok, D ** -0.5)
-            tol = fu.attention_tolerance(exact, *sizes, D, m, dtype, dtype == torch.bfloat16 and D == 128)
+            tol = fu.attention_tolerance(exact, *sizes, D, m, dtype, dtype == torch.bfloat16 and D == 128)  # (more vectors than the tensor cores' copies count: CUDA cores)
             assert bool(((y[0, 2 * g: 2 * g + 2].double() - exact).abs() <= tol).all())
 
 
