@@ -785,8 +785,8 @@ OL_API ol_status ol_fp8kv_read(const ol_fp8_kv* kv, int32_t dtype, int32_t token
  * capacity); out-of-range ones are clamped and recorded as OL_DEVICE_GUARD. Two
  * launches. Bytes and tokens in the statistics are those of the tokens that some
  * query may see.
- * bf16 queries (with fewer than 2^31 vectors in both planes) run on the tensor cores,
- * with the codes as they are; every other call on the CUDA cores.
+ * The products run on the tensor cores, with the codes as they are: queries and weights
+ * in E4M3 parts, 8 and 16 bits of them for bf16 queries, 24 for fp32 ones.
  * Errors: NULL, ALIAS, CAPACITY, SHAPE, DTYPE, WORKSPACE, BUSY, PAGE, ALIGN,
  * UNSUPPORTED (head_dim no multiple of 16 or > 256, new_len > 512, 2^31 tiles of work
  * at full capacity), CUDA.

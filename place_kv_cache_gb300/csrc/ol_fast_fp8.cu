@@ -1,13 +1,12 @@
 // ol_fast_fp8.cu -- attention over an E4M3 cache on the 5th generation tensor
-// cores: bf16 queries, contiguous cache or paged pool.
+// cores: bf16 or fp32 queries, contiguous cache or paged pool.
 //
 // A unit is NC = 8, 16 or 32 (head, query) columns c = head * count + query of one row's
 // kv head (queries that the row has not take no part). Its tokens form tiles of 128; equal
-// contiguous shares of all
-// units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh): while one ends a
-// segment or waits, the other has the SM. K and V go to the tensor cores as they lie
-// in the cache, with the tokens (for V the dimensions) as the products' 128 rows, so
-// that the columns may be few and nothing is unpacked:
+// contiguous shares of all units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh):
+// while one ends a segment or waits, the other has the SM. K and V go to the tensor cores
+// as they lie in the cache, with the tokens (for V the dimensions) as the products' 128
+// rows, so that the columns may be few and nothing is unpacked:
 //   S = K Q'    128 tokens x 2 NC x D.  Q' holds each q, times a power of two, in two
 //               E4M3 parts: the second is the first's remainder, times 16. The 8 bits
 //               of a bf16 number are both parts' 4, but for elements below 2^-17 of the
@@ -21,6 +20,10 @@
 // The reference m of a column is looked for (and O rescaled) only when a token's y
 // passes it by 2^3; O = sum of the parts' columns over 16^k. The segments' merge knows
 // states (m, l, o) as those of the tree kernels.
+//
+// That is for bf16 queries. fp32 ones take six parts of each, 24 bits, in units of 8 columns
+// (two S of 48 columns and O of 64 fill TMEM); the sums in the tensor cores keep what is above
+// 2^-25 of the largest product, as fp32 sums would.
 //
 // Heads that are not 64 or 128 are taken as the next of 64, 128 and 256, with zeros behind
 // (the copies' own: no bytes are read for them). One of 256 has two halves of K, V and Q'
@@ -41,8 +44,13 @@
 //   heads of 256, 64 rows of 4096     166   6.5 TB/s
 //   heads of 64, 64 rows of 8192       97   5.6 TB/s: the softmax warps' chain of a tile
 //   heads of 80, 64 rows of 8192      236   2.8 TB/s: rows that straddle lines in the copies
-//   the first with 4 / 8 queries      165 / 220   the conversion of P, 64 bits of parts a column
+//   the first with 4 / 8 queries      165 / 220   P's parts: 32 bits of codes a weight
+//   fp32 queries, 64 rows of 2048      54   as the first line would take 40 (the merge, and shares'
+//                                           begins and ends, weigh more); 8 queries 182: four units
+//                                           of 8 columns read K and V in turn, from L2
 //   1 row of 4097, 7 heads a kv head   12   the chain walk, first tile, two tiles, merge
+// fp32 queries on CUDA cores (groups of lanes with a token each, packed fp32 products)
+// took 127 and 715 us for those two lines: 24 TFLOP/s, a third of them the products' issue.
 #include "ol_fp8.cuh"
 #include "ol_tree.cuh"
 
@@ -60,12 +68,16 @@ constexpr int kMostSmem = (233472 - 2 * 1024) / 2;  // of one of two CTAs
 
 // D: 64, 128 or 256 elements, what heads up to it take: the copies put zeros behind a
 // row of the cache, and there are none of its bytes to read.
-template <int D, int NC>
+// WIDE: fp32 queries, whose 24 bits (and those of P beside them) take six parts.
+template <int D, int NC, bool WIDE>
 struct Lay {
+  static constexpr int kQParts = WIDE ? 6 : 2, kPParts = WIDE ? 6 : 4;
+  static constexpr int kSN = kQParts * NC;              // columns of S
+  static constexpr int kON = WIDE ? 8 * NC : 4 * NC;    // of O, and bytes of a row of P' (a swizzle's width: two parts of zeros)
   static constexpr int kHalves = D == 256 ? 2 : 1, W = D / kHalves;  // of a row, W bytes each: what a swizzled row holds
   static constexpr int kTileBytes = kTile * W;          // a slot of the ring
-  static constexpr int kQBytes = 2 * NC * D;            // both parts of the queries; [halves] of it
-  static constexpr int kPBytes = kTile * 4 * NC;        // four parts of P
+  static constexpr int kQBytes = kSN * D;               // the queries' parts; [halves] of it
+  static constexpr int kPBytes = kTile * kON;           // the parts of P
   static constexpr int kQBuffers = NC == 32 ? 1 : 2;    // (room for one more tile of K or V)
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + kQBuffers * kQBytes;
@@ -89,8 +101,9 @@ struct Lay {
   static constexpr int kTotal = kMisc + 8;
   static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of two CTAs");
   static_assert(kRing % 1024 == 0 && kP % 1024 == 0 && kQBytes % 512 == 0, "swizzled tiles");
-  static constexpr int kTmem = 8 * NC * kHalves;  // columns: two S of 2 NC, O of 4 NC a half; 64, 128 or 256
-  static_assert(kTmem <= 256, "of one of two CTAs");
+  // TMEM's columns: two S, O of each half; 64, 128 or 256
+  static constexpr int kO = 2 * kSN, kUsed = kO + kON * kHalves, kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256, "of one of two CTAs");
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -189,9 +202,8 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
-template <int D, int NC>
+template <typename L>
 struct Bars {
-  using L = Lay<D, NC>;
   uint32_t at;
   __device__ uint32_t full(int s) const { return at + 8 * s; }
   __device__ uint32_t empty(int s) const { return at + 8 * (L::kSlots + s); }
@@ -267,13 +279,15 @@ __device__ __forceinline__ __half2 half2_of_e4m3x2(uint32_t x) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)x));
   return *reinterpret_cast<__half2*>(&r);
 }
-// The four parts of two weights, a byte each, those of the first weight in the lower
-// bytes. The first two remainders in fp32; what is left then has at most 12 bits above
-// 2^-24 of the parts' scale, for which fp16 does (off by 2^-20 of the weight).
-__device__ __forceinline__ void four_parts(uint64_t w, uint32_t (&part)[4]) {
+// The N parts of two weights, a byte each, those of the first weight in the lower
+// bytes. All remainders but the last two's in fp32; what is left then has at most 12 bits
+// above 2^-24 of the parts' scale (of six parts 8), for which fp16 does (off by 2^-20 of the
+// weight, or not at all).
+template <int N>
+__device__ __forceinline__ void parts_of(uint64_t w, uint32_t (&part)[N]) {
   const uint64_t sixteen = pack2(16.f, 16.f), minus = pack2(-16.f, -16.f);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < N - 2; ++k) {
     const float2 x = unpack2(w);
     part[k] = e4m3x2(x.x, x.y);
     const float2 e = from_e4m3x2(part[k]);
@@ -281,14 +295,14 @@ __device__ __forceinline__ void four_parts(uint64_t w, uint32_t (&part)[4]) {
   }
   const float2 x = unpack2(w);
   const __half2 r = __floats2half2_rn(x.x, x.y);
-  part[2] = e4m3x2_of_half2(r);
-  part[3] = e4m3x2_of_half2(__hmul2(__hsub2(r, half2_of_e4m3x2(part[2])), __float2half2_rn(16.f)));
+  part[N - 2] = e4m3x2_of_half2(r);
+  part[N - 1] = e4m3x2_of_half2(__hmul2(__hsub2(r, half2_of_e4m3x2(part[N - 2])), __float2half2_rn(16.f)));
 }
 
-template <int D, int NC, bool PAGED>
+template <int D, int NC, bool PAGED, bool WIDE>
 __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
                                                                const __grid_constant__ Fp8AttnParams fp, const int box) {
-  using L = Lay<D, NC>;
+  using L = Lay<D, NC, WIDE>;
   constexpr int kWarps = 4 * L::kGroups;  // of the softmax
   extern __shared__ __align__(1024) uint8_t smem[];
   const TreeParams& p = fp.t;
@@ -298,7 +312,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     if (threadIdx.x == 0) set_status(p.status, OL_DEVICE_GUARD);
     return;
   }
-  const Bars<D, NC> bar{sa + L::kBars};
+  const Bars<L> bar{sa + L::kBars};
   const uint32_t abort = sa + L::kMisc + 4;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
 
@@ -366,11 +380,11 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     // on their way) before the ring has room for them. Lane = box.
     struct Tile {
       int first, last;  // boxes
-      int y;            // cache row of this lane's box in plane K, or in its page
-      int page;
+      int y;            // row of this lane's box in its page, or in the kv head
+      int page, head;   // the page; the kv head, of the batch where there are no pages
       bool more;        // there is such a tile
     } ahead[3], cur = {};
-    const int v_rows = (PAGED ? fc.num_pages * fc.page_size : fc.batch * fc.capacity) * fc.kv_heads;
+    const int heads = (PAGED ? fc.num_pages : fc.batch) * fc.kv_heads;  // of a plane, in all pages or rows
     const int step_pages = PAGED ? kTile / fc.page_size : 0, step_slots = PAGED ? kTile - step_pages * fc.page_size : 0;
     bool ok = true;
     int tile = 0, t0 = 0, entry = 0, slot = 0;  // of the next tile: its first token, this lane's entry in the table and slot in its page
@@ -428,29 +442,30 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       t.last = (min(w.row.len - t0, kTile) + box - 1) / box;
       if (PAGED) {
         t.page = lane >= t.first && lane < t.last ? fc.block_table[(size_t)w.b * fc.max_pages + entry] : 0;
-        t.y = w.g * fc.page_size + slot;
+        t.y = slot;
         entry += step_pages;
         slot += step_slots;
         if (slot >= fc.page_size) slot -= fc.page_size, ++entry;
       } else {
-        t.y = (w.b * fc.kv_heads + w.g) * fc.capacity + t0 + lane * box;
+        t.y = t0 + lane * box;
       }
+      t.head = PAGED ? w.g : w.b * fc.kv_heads + w.g;
       ++tile;
       t0 += kTile;
     };
-    auto cache_row_of = [&](const Tile& t) {
-      if (!PAGED) return t.y;
+    auto head_of = [&](const Tile& t) {  // of plane K
+      if (!PAGED) return t.head;
       const bool bad = t.page < 0 || t.page >= fc.num_pages;
       if (bad) set_status(p.status, OL_DEVICE_GUARD);
-      return (bad ? 0 : t.page) * fc.kv_heads * fc.page_size + t.y;
+      return (bad ? 0 : t.page) * fc.kv_heads + t.head;
     };
     Cursor<L::kSlots> ring;
-    auto load = [&](int x, int y) {
+    auto load = [&](int x, int head) {
       if (!warp_wait(bar.empty(ring.slot), ring.phase ^ 1, abort, p.status)) return false;
       if (lane == 0) mbar_arrive_expect_tx(bar.full(ring.slot), (uint32_t)(cur.last - cur.first) * box * L::W);
       __syncwarp();
       if (lane >= cur.first && lane < cur.last)
-        tma_load_2d(sa + L::kRing + ring.slot * L::kTileBytes + lane * box * L::W, &map, x, y, bar.full(ring.slot), policy);
+        tma_load_3d(sa + L::kRing + ring.slot * L::kTileBytes + lane * box * L::W, &map, x, cur.y, head, bar.full(ring.slot), policy);
       ring.next();
       return true;
     };
@@ -472,10 +487,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         ahead[2].more = first = false;
       }
       if (cur.more) {
-        const int y = cache_row_of(cur);
+        const int head = head_of(cur);
         for (int plane = 0; plane < 2; ++plane)
 #pragma unroll
-          for (int x = 0; x < D; x += L::W) ok = ok && load(x, y + plane * v_rows);
+          for (int x = 0; x < D; x += L::W) ok = ok && load(x, head + plane * heads);
       } else if (ended && !ahead[1].more && !ahead[2].more) {
         break;
       }
@@ -486,9 +501,9 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     // --------------------------------------------------------------- MMA issue
     // The whole warp walks and waits, so that what the products are given stays in
     // uniform registers; one elected lane issues them.
-    constexpr uint32_t kDescS = mma_desc(2 * NC, false), kDescO = mma_desc(4 * NC, true);
+    constexpr uint32_t kDescS = mma_desc(L::kSN, false), kDescO = mma_desc(L::kON, true);
     constexpr uint32_t kRowSwizzle = L::W == 128 ? kSwizzle128 : kSwizzle64;  // rows of W bytes: K, V, Q'
-    constexpr uint32_t kPSwizzle = NC == 32 ? kSwizzle128 : NC == 16 ? kSwizzle64 : kSwizzle32;
+    constexpr uint32_t kPSwizzle = L::kON == 128 ? kSwizzle128 : L::kON == 64 ? kSwizzle64 : kSwizzle32;
     const uint32_t tm = uniform(tmem), base = uniform(sa);
     Cursor<L::kSlots> k, v;  // slots of the next S's K, of the next product's V
     v.skip(L::kHalves);
@@ -503,10 +518,10 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         for (int h = 0; h < L::kHalves; ++h, half.next()) {
           const uint64_t kd = smem_desc(base + L::kRing + half.slot * L::kTileBytes, 16, 8 * L::W, kRowSwizzle);
           const uint64_t qd =
-              smem_desc(base + L::kQ + q_buffer(seg) * L::kQBytes + h * 2 * NC * L::W, 16, 8 * L::W, kRowSwizzle);
+              smem_desc(base + L::kQ + q_buffer(seg) * L::kQBytes + h * L::kSN * L::W, 16, 8 * L::W, kRowSwizzle);
 #pragma unroll
           for (int x = 0; x < L::W / 32; ++x)
-            mma_fp8(tm + (s_count & 1) * 2 * NC, kd + 2 * x, qd + 2 * x, kDescS, h > 0 || x > 0);
+            mma_fp8(tm + (s_count & 1) * L::kSN, kd + 2 * x, qd + 2 * x, kDescS, h > 0 || x > 0);
           mma_commit(bar.empty(half.slot));
         }
         mma_commit(bar.s_full(s_count & 1));
@@ -569,14 +584,14 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         tmem_fence_after();
         if (elect_one()) {
           // V's second half of the 128 rows is its first again where W is 64
-          const uint64_t pd = smem_desc(base + L::kP, 0, 8 * 4 * NC, kPSwizzle);
+          const uint64_t pd = smem_desc(base + L::kP, 0, 8 * L::kON, kPSwizzle);
           half = v;
 #pragma unroll
           for (int h = 0; h < L::kHalves; ++h, half.next()) {
             const uint64_t vd = smem_desc(base + L::kRing + half.slot * L::kTileBytes, 0, 8 * L::W, kRowSwizzle);
 #pragma unroll
             for (int x = 0; x < kTile / 32; ++x)
-              mma_fp8(tm + (h + 1) * 4 * NC, vd + x * (32 * L::W / 16), pd + x * (32 * 4 * NC / 16), kDescO, i > 0 || x > 0);
+              mma_fp8(tm + L::kO + h * L::kON, vd + x * (32 * L::W / 16), pd + x * (32 * L::kON / 16), kDescO, i > 0 || x > 0);
             mma_commit(bar.empty(half.slot));
           }
           mma_commit(bar.p_taken());
@@ -669,6 +684,17 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     // Q': rows [half][part][column] of W bytes, swizzled. Four lanes have a column, E elements each.
     constexpr int E = D / 4;
     const int part = lane & 3, pieces = p.head_dim / 8 - part * (E / 8);  // of 8 elements that there are
+    // 2^(7 - exponent) of the largest element, given its absolute value's bits: it comes to lie between 2^7 and
+    // 2^8 (numbers below 2^-119 stay smaller)
+    auto factor_of = [](uint32_t top) {
+      const int up = min(7 - ((int)(top >> 23) - 127), 126);
+      return top == 0 ? 1.f : __int_as_float((127 + up) << 23);
+    };
+    auto place_of = [](int c, int e, int part) {  // of elements 8 e .. of this lane's, in the first part
+      const int d = part * E + e * 8, in = d % L::W;
+      const int sw = L::W == 128 ? c & 7 : c >> 1 & 3;  // (of all parts' rows: NC is a multiple of 8)
+      return (d / L::W * L::kSN + c) * L::W + ((in / 16 ^ sw) << 4) + in % 16;
+    };
     uint32_t seg = 0;
     bool ok = true;
     Seg g;
@@ -676,8 +702,53 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       const int buf = q_buffer(seg), r0 = g.qg * NC, R = p.group * g.count;
       uint8_t* const to = smem + L::kQ + buf * L::kQBytes;
       Col* const cols = reinterpret_cast<Col*>(smem + L::kCols) + buf * NC;
+      if constexpr (WIDE) {  // (eight columns: a lane has its part of one)
+        const int c = lane >> 2, head = (r0 + c) / g.count, query = r0 + c - head * g.count, live = head * p.nodes + query;
+        const float4* const q = reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(p.q) + (tree_out_row(p, g.b, g.g, 0) + live) * p.head_dim + part * E);
+        const int mine = r0 + c < R ? pieces : 0;
+        auto load = [&](int e, float (&x)[8]) {
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f), a = e < mine ? q[2 * e] : zero, z = e < mine ? q[2 * e + 1] : zero;
+          x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = z.x, x[5] = z.y, x[6] = z.z, x[7] = z.w;
+        };
+        float x[8];
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int e = 0; e < E / 8; ++e) {
+          load(e, x);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float factor = factor_of(top);
+        const bool finite = top < 0x7f800000u;  // else: NaN codes, so that the column's outputs are NaN
+        if (!(ok = warp_wait(bar.q_empty(buf), q_phase(seg) ^ 1, abort, p.status))) break;
+#pragma unroll 2
+        for (int e = 0; e < E / 8; ++e) {  // (once more, now from L1)
+          load(e, x);
+          uint8_t* const at = to + place_of(c, e, part);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] *= factor;
+#pragma unroll
+          for (int n = 0; n < L::kQParts; ++n) {
+            uint32_t z[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t two = finite ? e4m3x2(x[2 * k], x[2 * k + 1]) : n == 0 ? 0x7f7fu : 0u;
+              const float2 h = from_e4m3x2(two);
+              z[k / 2] |= two << (k % 2 * 16);
+              x[2 * k] = (x[2 * k] - h.x) * 16.f;
+              x[2 * k + 1] = (x[2 * k + 1] - h.y) * 16.f;
+            }
+            *reinterpret_cast<uint2*>(at + n * NC * L::W) = make_uint2(z[0], z[1]);
+          }
+        }
+        if (part == 0) cols[c] = Col{1.f / factor, query, live, 0};
+      } else {
       const uint4* const q =
-          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * p.head_dim) + part * (E / 8);
+          reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + tree_out_row(p, g.b, g.g, 0) * p.head_dim) +
+          part * (E / 8);
       uint4 x[E / 8], next[E / 8];
       int query, live, next_query, next_live;
       auto load = [&](int c) {
@@ -705,11 +776,8 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(7 - exponent): the largest element between 2^7 and 2^8 (numbers below 2^-119 stay smaller)
-        const int up = min(7 - ((int)(top >> 23) - 127), 126);
-        const float factor = top == 0 ? 1.f : __int_as_float((127 + up) << 23);
+        const float factor = factor_of(top);
         const bool finite = top < 0x7f800000u;  // else: NaN codes, so that the column's outputs are NaN
-        const int sw = L::W == 128 ? c & 7 : c >> 1 & 3;  // (of both parts' rows: NC is a multiple of 8)
 #pragma unroll
         for (int e = 0; e < E / 8; ++e) {
           const uint32_t z[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
@@ -722,12 +790,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             hi[k / 2] |= two << (k % 2 * 16);
             lo[k / 2] |= (finite ? e4m3x2((u - h.x) * 16.f, (v - h.y) * 16.f) : 0) << (k % 2 * 16);
           }
-          const int d = part * E + e * 8, in = d % L::W;
-          uint8_t* const at = to + (d / L::W * 2 * NC + c) * L::W + ((in / 16 ^ sw) << 4) + in % 16;
+          uint8_t* const at = to + place_of(c, e, part);
           *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(at + NC * L::W) = make_uint2(lo[0], lo[1]);
         }
         if (part == 0) cols[c] = Col{1.f / factor, query, live, 0};
+      }
       }
       fence_proxy_async_smem();
       warp_arrive(bar.q_full(buf));
@@ -739,17 +807,18 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     const int me = warp - 4, row = tid % 128;  // row: token of a tile, dimension of a half of O
     const int group = me / 4, first = group * kMine;  // this group's columns
     const uint32_t lanes = (uint32_t)(me % 4 * 32) << 16;
-    const uint32_t to = tmem + 4 * NC + first + lanes;  // O of these columns, the parts NC apart, the halves 4 NC
+    const uint32_t to = tmem + L::kO + first + lanes;  // O of these columns, the parts NC apart, the halves kON
     float* const tab = reinterpret_cast<float*>(smem + L::kTab) + me * kMine * 2;  // of two columns: factors, minus references
     float* const mine = tab + lane % kMine / 2 * 4 + lane % 2;
     float* const tops = reinterpret_cast<float*>(smem + L::kTops) + group * 4 * kMine;
     float* const grow = reinterpret_cast<float*>(smem + L::kGrow) + me * kMine;
     float* const sums = reinterpret_cast<float*>(smem + L::kSums) + group * 4 * kMine;
     volatile uint32_t* const flag = reinterpret_cast<volatile uint32_t*>(smem + L::kFlag) + group * 2;
-    constexpr int kSwBits = NC == 32 ? 7 : NC == 16 ? 3 : 1, kSwShift = NC == 32 ? 0 : NC == 16 ? 1 : 2;
-    uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP) + row * (NC / 4);
+    constexpr int kSwBits = L::kON / 16 - 1, kSwShift = L::kON == 128 ? 0 : L::kON == 64 ? 1 : 2;
+    uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP) + row * (L::kON / 16);
     const int p_sw = row >> kSwShift & kSwBits;  // the swizzle of this row's chunks
     constexpr int kStep = 8;                     // columns whose scores are looked at at a time
+    if (WIDE) p_row[3 ^ p_sw] = make_uint4(0, 0, 0, 0);  // the parts that there are not
     Cursor<kScales> sc;
     uint32_t count = 0;  // of tiles
     uint32_t votes = 0, seg = 0;
@@ -782,8 +851,9 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         // comes in by its logarithm, and only for columns that see the token.
         const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
         warp_arrive(bar.sc_empty(sc.slot));
-        const float v_log2 = __log2f(v_scale), v_inv = v_scale == v_scale ? fast_inverse(v_scale) : 1.f;
-        const uint32_t ts = tmem + (count & 1) * 2 * NC + first + lanes;
+        const float v_log2 = WIDE ? log2f(v_scale) : __log2f(v_scale);  // (fp32 outputs would see the latter's 2^-22)
+        const float v_inv = v_scale != v_scale ? 1.f : WIDE ? __frcp_rn(v_scale) : fast_inverse(v_scale);
+        const uint32_t ts = tmem + (count & 1) * L::kSN + first + lanes;
         if (!(ok = warp_wait(bar.s_full(count & 1), count >> 1 & 1, abort, p.status))) break;
         ++count;
         tmem_fence_after();
@@ -803,19 +873,21 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
             for (int c0 = 0; c0 < kMine; c0 += kStep) {
-              uint32_t hi[kStep], lo[kStep];
-              tmem_ld8(ts + c0, hi);
-              tmem_ld8(ts + NC + c0, lo);
-              tmem_wait_ld8(hi);
-              tmem_wait_ld8(lo);
+              uint32_t z[L::kQParts][kStep];
+#pragma unroll
+              for (int k = 0; k < L::kQParts; ++k) tmem_ld8(ts + k * NC + c0, z[k]);
+#pragma unroll
+              for (int k = 0; k < L::kQParts; ++k) tmem_wait_ld8(z[k]);
 #pragma unroll
               for (int c = 0; c < kStep; c += 2) {
                 const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(tab + (c0 + c) * 2);
-                const uint64_t s0 = pack2(__uint_as_float(hi[c]), __uint_as_float(hi[c + 1]));
-                const uint64_t s1 = pack2(__uint_as_float(lo[c]), __uint_as_float(lo[c + 1]));
-                const float2 z = unpack2(fma2(mul2(fma2(s1, part2, s0), k2), f.x, add2(v2, f.y)));
-                y[c0 + c] = z.x;
-                y[c0 + c + 1] = z.y;
+                auto two = [&](int k) { return pack2(__uint_as_float(z[k][c]), __uint_as_float(z[k][c + 1])); };
+                uint64_t sum = two(L::kQParts - 1);
+#pragma unroll
+                for (int k = L::kQParts - 2; k >= 0; --k) sum = fma2(sum, part2, two(k));
+                const float2 x = unpack2(fma2(mul2(sum, k2), f.x, add2(v2, f.y)));
+                y[c0 + c] = x.x;
+                y[c0 + c + 1] = x.y;
               }
             }
             if (edge)
@@ -834,14 +906,17 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
 #pragma unroll 1
           for (int c = 0; c < kMine; c += 4) {
-            uint32_t hi[4], lo[4];
-            tmem_ld4(ts + c, hi);
-            tmem_ld4(ts + NC + c, lo);
-            tmem_wait_ld4(hi);
-            tmem_wait_ld4(lo);
+            uint32_t z[L::kQParts][4];
+#pragma unroll
+            for (int n = 0; n < L::kQParts; ++n) tmem_ld4(ts + n * NC + c, z[n]);
+#pragma unroll
+            for (int n = 0; n < L::kQParts; ++n) tmem_wait_ld4(z[n]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float x = fmaf(__uint_as_float(lo[k]), 0.0625f, __uint_as_float(hi[k])) * k_scale;
+              float x = __uint_as_float(z[L::kQParts - 1][k]);
+#pragma unroll
+              for (int n = L::kQParts - 2; n >= 0; --n) x = fmaf(x, 0.0625f, __uint_as_float(z[n][k]));
+              x *= k_scale;
               const float raw = fmaf(x, cols[c + k].factor, v_log2);
               const float top = warp_max(hidden >> (c + k) & 1 ? -INFINITY : fmaxf(raw, -INFINITY));  // (a NaN is no maximum)
               if (lane == 0) tops[me % 4 * kMine + c + k] = top;
@@ -863,14 +938,15 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;
             tmem_fence_after();
 #pragma unroll 1
-            for (int x = 0; x < 4 * kMine * L::kHalves; x += 4) {
-              const int part = x / kMine, c = x - part * kMine;  // (of both halves)
+            for (int x = 0; x < L::kPParts * kMine * L::kHalves; x += 4) {
+              const int part = x / kMine, c = x - part * kMine, half = part / L::kPParts;  // (part: of both halves')
+              const uint32_t at = to + half * L::kON + (part - half * L::kPParts) * NC + c;
               uint32_t o[4];
-              tmem_ld4(to + part * NC + c, o);
+              tmem_ld4(at, o);
               tmem_wait_ld4(o);
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * grow[c + k]);
-              tmem_st4(to + part * NC + c, o);
+              tmem_st4(at, o);
             }
             tmem_wait_st();
           }
@@ -880,24 +956,24 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         tmem_fence_before();
         warp_arrive(bar.s_free(count + 1 & 1));
         const uint64_t inv2 = pack2(v_inv, v_inv);
-        uint32_t z[4][kMine / 4];  // P' of this row: parts, a byte a column
+        uint32_t z[L::kPParts][kMine / 4];  // P' of this row: parts, a byte a column
 #pragma unroll
         for (int c = 0; c < kMine; c += 4) {
-          uint32_t part[2][4];
+          uint32_t part[2][L::kPParts];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int x = c + 2 * h;
             const uint64_t w2 = pack2(fast_exp2(y[x]), fast_exp2(y[x + 1]));
             l[x / 2] = fma2(w2, inv2, l[x / 2]);
-            four_parts(w2, part[h]);
+            parts_of(w2, part[h]);
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
+          for (int k = 0; k < L::kPParts; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
         }
         if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;  // the last P is read
         if constexpr (kMine == 8) {
-          p_row[0 ^ p_sw] = make_uint4(z[0][0], z[0][1], z[1][0], z[1][1]);
-          p_row[1 ^ p_sw] = make_uint4(z[2][0], z[2][1], z[3][0], z[3][1]);
+#pragma unroll
+          for (int k = 0; k < L::kPParts; k += 2) p_row[k / 2 ^ p_sw] = make_uint4(z[k][0], z[k][1], z[k + 1][0], z[k + 1][1]);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -949,17 +1025,18 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       for (int x = 0; x < kMine * L::kHalves; x += 4) {
         const int c0 = x % kMine, half = x / kMine, d = half * 128 + row;
         if (c0 >= live) continue;
-        uint32_t o[4][4];
+        uint32_t o[L::kPParts][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld4(to + half * 4 * NC + k * NC + c0, o[k]);
+        for (int k = 0; k < L::kPParts; ++k) tmem_ld4(to + half * L::kON + k * NC + c0, o[k]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_wait_ld4(o[k]);
+        for (int k = 0; k < L::kPParts; ++k) tmem_wait_ld4(o[k]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int col = c0 + c, place = first + col;
           if (col >= live) continue;
-          const float sum = fmaf(fmaf(fmaf(__uint_as_float(o[3][c]), 0.0625f, __uint_as_float(o[2][c])), 0.0625f,
-                                      __uint_as_float(o[1][c])), 0.0625f, __uint_as_float(o[0][c]));
+          float sum = __uint_as_float(o[L::kPParts - 1][c]);
+#pragma unroll
+          for (int k = L::kPParts - 2; k >= 0; --k) sum = fmaf(sum, 0.0625f, __uint_as_float(o[k][c]));
           if (slot) {
             if (d == 0) {
               slot[place] = -tab[col / 2 * 4 + 2 + col % 2];
@@ -1001,44 +1078,42 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-uint64_t code_rows(const Fp8Cache& c) {
-  return c.block_table ? 2ull * c.num_pages * c.kv_heads * c.page_size : 2ull * c.batch * c.kv_heads * c.capacity;
-}
-
-// The codes as rows of head_dim bytes; boxes of `box` rows and `width` bytes (zeros past head_dim).
+// The codes as [planes, pages or rows, kv heads][tokens][head_dim]; boxes of `box` tokens
+// and `width` bytes (zeros past head_dim and past the tokens).
 bool encode_codes(CUtensorMap* map, const Fp8Cache& c, int box, int width) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, code_rows(c)};
-  cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
-  cuuint32_t boxes[2] = {(cuuint32_t)width, (cuuint32_t)box};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, c.codes, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const cuuint64_t d = c.head_dim, tokens = c.block_table ? c.page_size : c.capacity;
+  cuuint64_t dims[3] = {d, tokens, 2ull * (c.block_table ? c.num_pages : c.batch) * c.kv_heads};
+  cuuint64_t strides[2] = {d, d * tokens};
+  cuuint32_t boxes[3] = {(cuuint32_t)width, (cuuint32_t)box, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.codes, dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NC, bool PAGED>
+template <int D, int NC, bool PAGED, bool WIDE = false>
 cudaError_t launch_cfg(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
-  auto kern = fast_fp8_kernel<D, NC, PAGED>;
+  using L = Lay<D, NC, WIDE>;
+  auto kern = fast_fp8_kernel<D, NC, PAGED, WIDE>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t attr = once_per_device(done, [kern] {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, NC>::kTotal);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
     if (e != cudaSuccess) return e;
     return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(kern, dim3(p.t.nctas), dim3(threads_of(NC)), Lay<D, NC>::kTotal, s, map, p, box);
+  return launch_pdl(kern, dim3(p.t.nctas), dim3(threads_of(NC)), L::kTotal, s, map, p, box);
 }
 
 template <int D, bool PAGED>
 cudaError_t launch_cols(const CUtensorMap& map, const Fp8AttnParams& p, int box, cudaStream_t s) {
-  if constexpr (D == 256)
-    return p.t.rows_per_unit == 8 ? launch_cfg<D, 8, PAGED>(map, p, box, s) : launch_cfg<D, 16, PAGED>(map, p, box, s);
-  else
-    return p.t.rows_per_unit == 8    ? launch_cfg<D, 8, PAGED>(map, p, box, s)
-         : p.t.rows_per_unit == 16 ? launch_cfg<D, 16, PAGED>(map, p, box, s)
-                                   : launch_cfg<D, 32, PAGED>(map, p, box, s);
+  if (p.t.dtype == OL_F32) return launch_cfg<D, 8, PAGED, true>(map, p, box, s);
+  if (p.t.rows_per_unit == 8) return launch_cfg<D, 8, PAGED>(map, p, box, s);
+  if constexpr (D < 256)
+    if (p.t.rows_per_unit == 32) return launch_cfg<D, 32, PAGED>(map, p, box, s);
+  return launch_cfg<D, 16, PAGED>(map, p, box, s);
 }
 
 template <int D>
@@ -1048,16 +1123,11 @@ cudaError_t launch_dim(const CUtensorMap& map, const Fp8AttnParams& p, int box, 
 
 }  // namespace
 
-bool fast_fp8_supported(const Fp8AttnParams& p) {
-  if (p.t.dtype != OL_BF16) return false;
-  const uint64_t rows = code_rows(p.cache);
-  return rows > 0 && rows < (1ull << 31);  // TMA row coordinates are 32-bit
-}
-
-void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
+void plan_fp8_attention(Fp8AttnParams& fp, int sms) {
   TreeParams& p = fp.t;
   const int columns = p.group * p.nodes;
-  p.rows_per_unit = columns <= 8 ? 8 : columns <= 16 || p.head_dim > 128 ? 16 : 32;  // (TMEM has no room for 32 of two halves)
+  // (TMEM has no room for 32 columns of two halves, nor for 16 of six parts)
+  p.rows_per_unit = columns <= 8 || p.dtype == OL_F32 ? 8 : columns <= 16 || p.head_dim > 128 ? 16 : 32;
   p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
   p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
@@ -1069,11 +1139,11 @@ void plan_fast_fp8(Fp8AttnParams& fp, int sms) {
   // (64 rows of 8192 tokens, one query of 4 heads a kv head: 166 us, with the pool 161; ragged rows to 16384 in pages of
   // 16 189 and 183; heads of 80 242 and 236.) Where the SM itself does, shares are equal as they are (16 columns 167 and
   // 185 us, heads of 64 105 and 110).
-  p.pool = p.rows_per_unit > 8 || p.head_dim <= 64 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
+  p.pool = columns > 8 || p.head_dim <= 64 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
   p.by_unit = tree_few_units(p);
 }
 
-cudaError_t launch_fast_fp8(const Fp8AttnParams& p, cudaStream_t s) {
+cudaError_t launch_fp8_attention(const Fp8AttnParams& p, cudaStream_t s) {
   // rows of a box: a tile of the contiguous cache, else the most that divides a page
   int box = kTile;
   if (p.cache.block_table)

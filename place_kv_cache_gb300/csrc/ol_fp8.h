@@ -1,7 +1,6 @@
 // ol_fp8.h -- parameter blocks and launchers of the operators of an E4M3 cache:
-// the quantising append and reading back (ol_fp8.cu), attention on CUDA cores
-// (ol_fp8.cu) and on the tensor cores (ol_fast_fp8.cu), and the norms of queries
-// and keys with their rotation (ol_norm_rope.cu). Not part of the public ABI.
+// the quantising append and reading back (ol_fp8.cu), attention (ol_fast_fp8.cu), and
+// the norms of queries and keys with their rotation (ol_norm_rope.cu). Not part of the public ABI.
 #pragma once
 
 #include "ol_draft.h"
@@ -48,11 +47,8 @@ struct Fp8AttnParams {
   TreeParams t;
   Fp8Cache cache;
 };
-bool fast_fp8_supported(const Fp8AttnParams& p);
-void plan_fast_fp8(Fp8AttnParams& p, int sms);
-void plan_generic_fp8(Fp8AttnParams& p, int sms);
-cudaError_t launch_fast_fp8(const Fp8AttnParams& p, cudaStream_t s);
-cudaError_t launch_generic_fp8(const Fp8AttnParams& p, cudaStream_t s);
+void plan_fp8_attention(Fp8AttnParams& p, int sms);
+cudaError_t launch_fp8_attention(const Fp8AttnParams& p, cudaStream_t s);
 
 struct NormRopeParams {
   const uint64_t* turns;     // NULL: no rotation (rot_dim 0)

@@ -277,17 +277,13 @@ ol_status fp8_attention(const ol_fp8_kv* kv, int32_t dtype, const void* q, int32
   t.splits = reinterpret_cast<TreeSplit*>(splits);
   t.partials = reinterpret_cast<float*>(splits + kTreeSplitBytes);
   t.ticket = static_cast<uint32_t*>(workspace) + kTreeTicketWord;
-  const bool fast = fast_fp8_supported(p);
-  if (fast)
-    plan_fast_fp8(p, sm_count_cached());
-  else
-    plan_generic_fp8(p, sm_count_cached());
+  plan_fp8_attention(p, sm_count_cached());
   if (!tree_counts_fit(t)) return OL_ERR_UNSUPPORTED;
   stats.workspace_bytes = (int64_t)need;
   record(stats);
   if (fault_injected()) return OL_ERR_INJECTED;
   if (c.batch == 0) return OL_OK;
-  cudaError_t e = fast ? launch_fast_fp8(p, s) : launch_generic_fp8(p, s);
+  cudaError_t e = launch_fp8_attention(p, s);
   if (e == cudaSuccess) e = launch_tree_merge(t, s);
   return e == cudaSuccess ? OL_OK : OL_ERR_CUDA;
 }
