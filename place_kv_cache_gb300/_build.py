@@ -19,7 +19,8 @@ SOURCES = ["ol_api.cpp", "ol_append.cu", "ol_generic.cu", "ol_fast_bf16.cu", "ol
            "ol_hpaged.cu", "ol_fast_hpaged.cu", "ol_draft_api.cpp", "ol_rope.cu", "ol_tree.cu", "ol_fast_tree.cu",
            "ol_fp8_api.cpp", "ol_fp8.cu", "ol_fast_fp8.cu", "ol_norm_rope.cu"]
 HEADERS = ["ol_internal.h", "ol_launch.h", "ol_common.cuh", "ol_merge.cuh", "ol_fast_bf16_kernel.inc", "ol_hpaged.cuh",
-           "ol_host.h", "ol_draft.h", "ol_tree.cuh", "ol_fp8.h", "ol_fp8.cuh", os.path.join("..", "..", "include", "ol.h")]
+           "ol_host.h", "ol_draft.h", "ol_tree.cuh", "ol_fp8.h", "ol_fp8.cuh", "ol_pairs.cuh",
+           os.path.join("..", "..", "include", "ol.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-Xptxas", "-warn-spills"]

@@ -52,6 +52,7 @@
 // fp32 queries on CUDA cores (groups of lanes with a token each, packed fp32 products)
 // took 127 and 715 us for those two lines: 24 TFLOP/s, a third of them the products' issue.
 #include "ol_fp8.cuh"
+#include "ol_pairs.cuh"
 #include "ol_tree.cuh"
 
 namespace ol {

@@ -19,6 +19,7 @@
 // tokens fewer than kManyWarps are cut into slices of their vectors.
 #include "ol_common.cuh"
 #include "ol_fp8.h"
+#include "ol_pairs.cuh"
 
 namespace ol {
 namespace {
