@@ -11,15 +11,14 @@
 //               E4M3 parts: the second is the first's remainder, times 16. The 8 bits
 //               of a bf16 number are both parts' 4, but for elements below 2^-17 of the
 //               vector's largest.
-//   y = (S0 + S1 / 16) s_k scale log2(e) + log2(s_v), with the token's block's scales
-//   P = 2^(y - m)   a thread per token; V's scale is in it
-//   O += V P'   D x 4 NC x 128 tokens.  P' holds P in four E4M3 parts, each times 16:
-//               16 bits, and steps of 2^-21 where m keeps the largest between 2^5 and
-//               2^8, so that the many small weights beside a large one are not lost.
-//   l += P / s_v    in fp32
-// The reference m of a column is looked for (and O rescaled) only when a token's y
-// passes it by 2^3; O = sum of the parts' columns over 16^k. The segments' merge knows
-// states (m, l, o) as those of the tree kernels.
+//   y = (S0 + S1 / 16) s_k scale log2(e) - m, with the token's block's scale
+//   l += 2^y        in fp32, a thread per token
+//   P = 2^y s_v     O += V P'   D x 4 NC x 128 tokens.  P' holds P in four E4M3 parts, each
+//               times 16: 16 bits, and steps of 2^-21 where m keeps the largest between 2^5
+//               and 2^8, so that the many small weights beside a large one are not lost.
+// The reference m of a column is looked for (and O rescaled) only when a token's P passes
+// 2^8; O = sum of the parts' columns over 16^k. The segments' merge knows states (m, l, o)
+// as those of the tree kernels.
 //
 // That is for bf16 queries. fp32 ones take six parts of each, 24 bits, in units of 8 columns
 // (two S of 48 columns and O of 64 fill TMEM); the sums in the tensor cores keep what is above
@@ -44,9 +43,9 @@
 //   heads of 256, 64 rows of 4096     166   6.5 TB/s
 //   heads of 64, 64 rows of 8192       97   5.6 TB/s: the softmax warps' chain of a tile
 //   heads of 80, 64 rows of 8192      236   2.8 TB/s: rows that straddle lines in the copies
-//   the first with 4 / 8 queries      165 / 220   P's parts: 32 bits of codes a weight
-//   fp32 queries, 64 rows of 2048      54   as the first line would take 40 (the merge, and shares'
-//                                           begins and ends, weigh more); 8 queries 182: four units
+//   the first with 4 / 8 queries      164 / 227   P's parts: 32 bits of codes a weight
+//   fp32 queries, 64 rows of 2048      52   as the first line would take 40 (the merge, and shares'
+//                                           begins and ends, weigh more); 8 queries 175: four units
 //                                           of 8 columns read K and V in turn, from L2
 //   1 row of 4097, 7 heads a kv head   12   the chain walk, first tile, two tiles, merge
 // fp32 queries on CUDA cores (groups of lanes with a token each, packed fp32 products)
@@ -265,11 +264,6 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(top ^ (top >> 31 & 0x7fffffff));
 }
 
-__device__ __forceinline__ float fast_inverse(float x) {  // off by one unit in the last place
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(__half2 x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&x)));
@@ -847,13 +841,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         const int t0 = g.t0 + i * kTile;
         if (!(ok = warp_wait(bar.sc_full(sc.slot), sc.phase, abort, p.status))) break;
         const float* const scales = reinterpret_cast<const float*>(smem + L::kSc) + sc.slot * 16 + (row >> fc.block_log2);
-        const float k_scale = scales[0] * p.scale_log2;
-        // No scale: values of 0, whatever the weight; one that is far below all others. NaN
-        // comes in by its logarithm, and only for columns that see the token.
-        const float v_scale = scales[8] == 0.f ? kFp8LeastScale : scales[8];
+        // V's scale of NaN comes in by the scores, and so only for columns that see the token.
+        const bool good = scales[8] == scales[8];
+        const float k_scale = scales[0] * p.scale_log2 + (good ? 0.f : scales[8]), v_scale = good ? scales[8] : 1.f;
         warp_arrive(bar.sc_empty(sc.slot));
-        const float v_log2 = WIDE ? log2f(v_scale) : __log2f(v_scale);  // (fp32 outputs would see the latter's 2^-22)
-        const float v_inv = v_scale != v_scale ? 1.f : WIDE ? __frcp_rn(v_scale) : fast_inverse(v_scale);
+        // (for the references: no lower than the least scale's, so that 2^(y - m) stays far below overflow)
+        const float v_log2 = fmaxf(__log2f(v_scale), -80.f);
         const uint32_t ts = tmem + (count & 1) * L::kSN + first + lanes;
         if (!(ok = warp_wait(bar.s_full(count & 1), count >> 1 & 1, abort, p.status))) break;
         ++count;
@@ -871,7 +864,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         float y[kMine];
         for (bool looked = false;;) {
           if (i > 0 || looked) {  // (a segment's first tile has nothing to compare with)
-            const uint64_t k2 = pack2(k_scale, k_scale), v2 = pack2(v_log2, v_log2), part2 = pack2(0.0625f, 0.0625f);
+            const uint64_t k2 = pack2(k_scale, k_scale), part2 = pack2(0.0625f, 0.0625f);
 #pragma unroll
             for (int c0 = 0; c0 < kMine; c0 += kStep) {
               uint32_t z[L::kQParts][kStep];
@@ -886,7 +879,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
                 uint64_t sum = two(L::kQParts - 1);
 #pragma unroll
                 for (int k = L::kQParts - 2; k >= 0; --k) sum = fma2(sum, part2, two(k));
-                const float2 x = unpack2(fma2(mul2(sum, k2), f.x, add2(v2, f.y)));
+                const float2 x = unpack2(fma2(mul2(sum, k2), f.x, f.y));
                 y[c0 + c] = x.x;
                 y[c0 + c + 1] = x.y;
               }
@@ -901,7 +894,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
             for (int c = 4; c < kMine; ++c) most4[c % 4] = fmaxf(most4[c % 4], y[c]);
             const float most = fmaxf(fmaxf(most4[0], most4[1]), fmaxf(most4[2], most4[3]));
             // (the flag holds the number of the tile that raised it)
-            if (__any_sync(0xffffffffu, most > kGrown) && lane == 0) flag[count & 1] = count;
+            if (__any_sync(0xffffffffu, most > kGrown - v_log2) && lane == 0) flag[count & 1] = count;
             if (!(ok = vote()) || flag[count & 1] != count) break;
           }
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
@@ -956,7 +949,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         if (!ok) break;
         tmem_fence_before();
         warp_arrive(bar.s_free(count + 1 & 1));
-        const uint64_t inv2 = pack2(v_inv, v_inv);
+        const uint64_t v2 = pack2(v_scale, v_scale);
         uint32_t z[L::kPParts][kMine / 4];  // P' of this row: parts, a byte a column
 #pragma unroll
         for (int c = 0; c < kMine; c += 4) {
@@ -965,12 +958,17 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
           for (int h = 0; h < 2; ++h) {
             const int x = c + 2 * h;
             const uint64_t w2 = pack2(fast_exp2(y[x]), fast_exp2(y[x + 1]));
-            l[x / 2] = fma2(w2, inv2, l[x / 2]);
-            parts_of(w2, part[h]);
+            parts_of(mul2(w2, v2), part[h]);
+            const float2 w = unpack2(w2);
+            y[x] = w.x;
+            y[x + 1] = w.y;
           }
 #pragma unroll
           for (int k = 0; k < L::kPParts; ++k) z[k][c / 4] = part[0][k] | part[1][k] << 16;
         }
+        // (in the loop above these sums cost 32 columns 5 %)
+#pragma unroll
+        for (int c = 0; c < kMine; c += 2) l[c / 2] = add2(l[c / 2], pack2(y[c], y[c + 1]));
         if (!(ok = warp_wait(bar.p_taken(), count & 1, abort, p.status))) break;  // the last P is read
         if constexpr (kMine == 8) {
 #pragma unroll

@@ -282,7 +282,7 @@ ol_status fp8_attention(const ol_fp8_kv* kv, int32_t dtype, const void* q, int32
   stats.workspace_bytes = (int64_t)need;
   record(stats);
   if (fault_injected()) return OL_ERR_INJECTED;
-  if (c.batch == 0) return OL_OK;
+  if (c.batch == 0 || c.capacity == 0) return OL_OK;  // (there are no tokens)
   cudaError_t e = launch_fp8_attention(p, s);
   if (e == cudaSuccess) e = launch_tree_merge(t, s);
   return e == cudaSuccess ? OL_OK : OL_ERR_CUDA;

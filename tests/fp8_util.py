@@ -98,14 +98,14 @@ def attention_tolerance(out, pv, size, coarse, peak, D, n, out_dtype, wide):
     takes 32 products and the sum before; each is cut at 2^-25 of the largest, the sum rounded: 33 2^-25 + 2^-23 a step, less
     than 32 of the chain's 2^-23.) Then what the parts leave out.
     bf16 queries: q is held in two E4M3 parts, off by 2^-14 where q's largest element is 2^7 or more
-    (2^-21 of it, for each product); a score, the logarithm of V's scale and the reference are added in fp32 (three
-    roundings of |s| + |log2 scale| + 9 <= 1.45 size + 40, and 2^-21 of the logarithm); a weight in four E4M3 parts is
+    (2^-21 of it, for each product); a score and the reference (a score and the logarithm of V's scale) are added in fp32
+    (three roundings of |s| + |log2 scale| + 9 <= 1.45 size + 40, and 2^-21 for weights times scale); a weight in four E4M3 parts is
     off by 2^-16 of itself, and by at most 2^-26 of the largest weight times scale (parts of 2^5 and more for that,
     steps of 2^-9 / 16^3), times a code of up to 448.
     fp32 queries (wide): six parts, each of which leaves 2^-4 of what it is given: q off by 2^-24 of each element, and by
     half a step of the last part, 2^-10 / 16^5 = 2^-30, where q's largest is 2^7 or more: 2^-37 of it. Three more roundings of
-    the score (products with the scale, the parts' sum), log2f's 2^-23 of |log2 scale|: eight of them. A weight off by 2^-24 of
-    itself and by 2^-30 / 2^5 of the largest; two roundings of the inverse scale."""
+    the score (products with the scale, the parts' sum), and room for |log2 scale| up to 80: eight of them. A weight off by 2^-24 of
+    itself and by 2^-30 / 2^5 of the largest; its product with the scale 2^-24."""
     rel = 2 * (D + 5) * 2.0 ** -23 * size + 2 * 2.0 ** -22 + 2 * (n + 40) * 2.0 ** -23 + 2.0 ** -23
     tol = rel * pv
     if wide:

@@ -518,6 +518,29 @@ def test_scales_far_apart_zero_and_small(dt):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_scales_of_v_from_the_least_to_large(dt):
+    """Blocks of V from 2^-80 to 2^60, and of scale 0 whatever their codes: no token loses its part of the sum."""
+    a = Attention(dt, 2, 8, 2, 128, 16, 16, 3, [700, 130], out="f32")
+    some = torch.tensor([2.0 ** -80, 2.0 ** -40, 1.0, 2.0 ** 40, 2.0 ** 60, 0.0], device=DEV)
+    a.c.scales[1] = some[torch.randint(0, 6, a.c.scales[1].shape, generator=a.c.gen, device=DEV)]
+    a.call()
+    a.check()
+    a.c.scales[1] = some[torch.randint(0, 2, a.c.scales[1].shape, generator=a.c.gen, device=DEV) * 5]  # 2^-80 and 0
+    a.out.fill_(-77.0)
+    a.call()
+    a.check()
+
+
+def test_a_cache_of_no_tokens():
+    a = Attention("bf16", 2, 8, 2, 128, 16, 0, 3, [5, 7], [3, 3])
+    a.c.desc.capacity = 0
+    a.lens[:], a.counts[:] = 0, 0
+    a.call()
+    torch.cuda.synchronize()
+    assert bool((a.out == -77.0).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_a_heavy_token_among_many(dt):
     """One token with most of the weight and thousands that share the rest: none of their weight is lost."""
     n = 8000
