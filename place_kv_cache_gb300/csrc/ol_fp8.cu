@@ -86,7 +86,7 @@ __device__ __forceinline__ float block_scale(uint32_t most, bool begun, float ol
 
 // One CTA per block of tokens, head and plane that the call may reach. Its new
 // elements stay in registers between the search for the largest and their
-// quantising: KEEP pieces of VE elements a thread, every blockDim.x-th.
+// quantising: a piece of VE elements of up to KEEP tokens a thread.
 // The quotient x / s is x times the rounded inverse, set right by its remainder:
 // q = x r, q + (x - q s) r is x / s rounded to nearest where r is 1 / s rounded to
 // nearest (Markstein, Computation of elementary functions on the IBM RISC System/6000,
@@ -94,8 +94,8 @@ __device__ __forceinline__ float block_scale(uint32_t most, bool begun, float ol
 // Bounds: an element's 2 or 4 bytes in, 1 out. 4 ragged prompts of up to 4096 bf16 tokens
 // (8 heads of 128, blocks of 64; 54 MB) 12.7 us, 4.2 TB/s: issue (3 instructions a cycle) and
 // one wave's chain counts, tokens, maximum, codes; the places by divisions took 43. A decode
-// step (64 paged rows of a token) 2.9 us: the launch and that chain. Pieces of one element
-// (views without 16-byte alignment) keep 32 of them and spill: no call of a model's makes them.
+// step (64 paged rows of a token) 2.9 us: the launch and that chain. (Two CTAs of 512 threads an
+// SM: three spill, 14.5 us.)
 template <typename T, int VE, int KEEP>
 __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
     fp8_append_kernel(const __grid_constant__ Fp8AppendParams p) {
@@ -106,9 +106,8 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
   const int unit = blockIdx.x / c.kv_heads, g = blockIdx.x - unit * c.kv_heads;
   const int b = unit / p.blocks, nth = unit - b * p.blocks;
   const int pieces = c.head_dim / VE;
-  // piece tid of the block's, and the way to every next one of this thread
-  const int t_first = tid / pieces, x_first = tid - t_first * pieces;
-  const int t_step = blockDim.x / pieces, x_step = blockDim.x - t_step * pieces;
+  // piece x of tokens y, y + step, ..: one column of the block (threads past the last whole row have none)
+  const int step = blockDim.x / pieces, y = tid / pieces, x0 = tid - y * pieces;
   pdl_wait();
   pdl_launch_dependents();
   const int start = p.positions[b], n = p.counts ? p.counts[b] : p.new_len;
@@ -120,24 +119,20 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
   const RopeView& in = p.in[plane];
   const T* const from = reinterpret_cast<const T*>(in.data) + b * in.sb + g * in.sh + (long long)(lo - start) * in.st;
   P x[KEEP];
-  int t = t_first, d = x_first;
-  auto next = [&] {
-    t += t_step;
-    d += x_step;
-    if (d >= pieces) d -= pieces, ++t;
-  };
+  const int mine = y < step && y < tokens ? (tokens - y + step - 1) / step : 0;  // of the thread's pieces
+  const T* const src = from + y * in.st + x0 * VE;
+  const long long src_step = step * in.st;
 #pragma unroll
-  for (int u = 0; u < KEEP; ++u, next())
-    if (t < tokens) x[u] = *reinterpret_cast<const P*>(from + t * in.st + d * VE);
+  for (int u = 0; u < KEEP; ++u)
+    if (u < mine) x[u] = *reinterpret_cast<const P*>(src + u * src_step);
   long long row, at;
   if (!fp8_place(c, plane, b, g, first, row, at)) return;  // (device guard)
   const bool begun = lo > first;
   const float old = begun ? c.scales[at] : 0.f;
   uint32_t most = 0;
-  t = t_first, d = x_first;
 #pragma unroll
-  for (int u = 0; u < KEEP; ++u, next())
-    if (t < tokens) {
+  for (int u = 0; u < KEEP; ++u)
+    if (u < mine) {
       if constexpr (VE == 8) {  // the absolute values' bits, two at a time
         const uint32_t* const w = reinterpret_cast<const uint32_t*>(&x[u]);
         most = __vmaxu2(most, __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
@@ -173,20 +168,19 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
     const float2 r = unpack2(fma2(fma2(q, minus2, v), inverse2, q));
     return coded ? e4m3x2(r.x, r.y) : 0u;
   };
-  uint8_t* const to = codes + (long long)(lo - first) * c.head_dim;
-  t = t_first, d = x_first;
+  uint8_t* const to = codes + (lo - first + y) * c.head_dim + x0 * VE;
 #pragma unroll
-  for (int u = 0; u < KEEP; ++u, next()) {
-    if (t >= tokens) continue;
+  for (int u = 0; u < KEEP; ++u) {
+    if (u >= mine) continue;
     auto two = [&](int j) { return coded_pair(value_of<T>(x[u].e[j]), value_of<T>(x[u].e[VE > 1 ? j + 1 : j])); };
-    Codes<VE> y;
+    Codes<VE> z;
     if constexpr (VE == 8)
-      y = make_uint2(two(0) | two(2) << 16, two(4) | two(6) << 16);
+      z = make_uint2(two(0) | two(2) << 16, two(4) | two(6) << 16);
     else if constexpr (VE == 4)
-      y = two(0) | two(2) << 16;
+      z = two(0) | two(2) << 16;
     else
-      y = (uint8_t)two(0);
-    *reinterpret_cast<Codes<VE>*>(to + t * c.head_dim + d * VE) = y;
+      z = (uint8_t)two(0);
+    *reinterpret_cast<Codes<VE>*>(to + u * step * c.head_dim) = z;
   }
   if (tid == 0) c.scales[at] = scale;  // (every thread has read the old one)
 }
@@ -194,8 +188,8 @@ __global__ void __launch_bounds__(VE == 8 ? 512 : 1024, VE == 8 ? 2 : 1)
 template <typename T, int VE, int KEEP>
 cudaError_t launch_append_cfg(const Fp8AppendParams& p, cudaStream_t s) {
   const int block = 1 << p.cache.block_log2, tokens = p.new_len < block ? p.new_len : block;
-  const int pieces = tokens * (p.cache.head_dim / VE);
-  const int threads = ((pieces + KEEP - 1) / KEEP + 31) / 32 * 32;
+  const int pieces = p.cache.head_dim / VE, rows = (tokens + KEEP - 1) / KEEP;  // of a token; of threads
+  const int threads = (rows * pieces + 31) / 32 * 32;
   return launch_pdl(fp8_append_kernel<T, VE, KEEP>, dim3((unsigned)p.cache.batch * p.blocks * p.cache.kv_heads, 2),
                     dim3(threads), 0, s, p);
 }
