@@ -257,13 +257,12 @@ struct alignas(16) Seg {
 __device__ __forceinline__ int row_low(int window, int prefix) { return window < 0 || prefix <= window ? 0 : prefix - window; }
 __device__ __forceinline__ int all_low(int window, int len) { return window < 0 || len - 1 <= window ? 0 : len - 1 - window; }
 
-// Largest value of a warp, as a signed integer's order (no NaN).
+// Largest value of a warp (no NaN).
 __device__ __forceinline__ float warp_max(float x) {
-  const int b = __float_as_int(x), key = b ^ (b >> 31 & 0x7fffffff);
-  const int top = __reduce_max_sync(0xffffffffu, key);
-  return __int_as_float(top ^ (top >> 31 & 0x7fffffff));
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
-
 __device__ __forceinline__ uint32_t e4m3x2_of_half2(__half2 x) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&x)));
@@ -812,7 +811,7 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
     constexpr int kSwBits = L::kON / 16 - 1, kSwShift = L::kON == 128 ? 0 : L::kON == 64 ? 1 : 2;
     uint4* const p_row = reinterpret_cast<uint4*>(smem + L::kP) + row * (L::kON / 16);
     const int p_sw = row >> kSwShift & kSwBits;  // the swizzle of this row's chunks
-    constexpr int kStep = 8;                     // columns whose scores are looked at at a time
+    constexpr int kStep = 8;                     // columns whose scores (and sums, in the end) are looked at at a time
     if (WIDE) p_row[3 ^ p_sw] = make_uint4(0, 0, 0, 0);  // the parts that there are not
     Cursor<kScales> sc;
     uint32_t count = 0;  // of tiles
@@ -854,10 +853,12 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
         uint32_t hidden = 0;  // columns that do not see this thread's token
         if (t0 + kTile - 1 > g.prefix || t0 < low_all) {
           const int t = t0 + row;
-#pragma unroll 1
-          for (int c = 0; c < kMine; ++c) {
-            const int at = g.prefix + cols[c].query;
-            if (t > at || (p.window >= 0 && t < at - p.window)) hidden |= 1u << c;
+          auto unseen = [&](int at) { return t > at || (p.window >= 0 && t < at - p.window); };
+          if (g.count == 1) {
+            hidden = unseen(g.prefix) ? ~0u : 0u;
+          } else {
+#pragma unroll 8
+            for (int c = 0; c < kMine; ++c) hidden |= (uint32_t)unseen(g.prefix + cols[c].query) << c;
           }
         }
         const bool edge = __any_sync(0xffffffffu, hidden != 0);
@@ -899,22 +900,24 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
           }
           // A reference is outgrown: the columns' maxima are looked for, and there are new ones.
 #pragma unroll 1
-          for (int c = 0; c < kMine; c += 4) {
-            uint32_t z[L::kQParts][4];
+          for (int c0 = 0; c0 < kMine; c0 += kStep) {
+            uint32_t z[L::kQParts][kStep];
 #pragma unroll
-            for (int n = 0; n < L::kQParts; ++n) tmem_ld4(ts + n * NC + c, z[n]);
+            for (int n = 0; n < L::kQParts; ++n) tmem_ld8(ts + n * NC + c0, z[n]);
 #pragma unroll
-            for (int n = 0; n < L::kQParts; ++n) tmem_wait_ld4(z[n]);
+            for (int n = 0; n < L::kQParts; ++n) tmem_wait_ld8(z[n]);
+            float top[kStep];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float x = __uint_as_float(z[L::kQParts - 1][k]);
+            for (int c = 0; c < kStep; ++c) {
+              float x = __uint_as_float(z[L::kQParts - 1][c]);
 #pragma unroll
-              for (int n = L::kQParts - 2; n >= 0; --n) x = fmaf(x, 0.0625f, __uint_as_float(z[n][k]));
-              x *= k_scale;
-              const float raw = fmaf(x, cols[c + k].factor, v_log2);
-              const float top = warp_max(hidden >> (c + k) & 1 ? -INFINITY : fmaxf(raw, -INFINITY));  // (a NaN is no maximum)
-              if (lane == 0) tops[me % 4 * kMine + c + k] = top;
+              for (int n = L::kQParts - 2; n >= 0; --n) x = fmaf(x, 0.0625f, __uint_as_float(z[n][c]));
+              const float raw = fmaf(x * k_scale, cols[c0 + c].factor, v_log2);
+              top[c] = warp_max(hidden >> (c0 + c) & 1 ? -INFINITY : fmaxf(raw, -INFINITY));  // (a NaN is no maximum)
             }
+            if (lane == 0)
+#pragma unroll
+              for (int c = 0; c < kStep; ++c) tops[me % 4 * kMine + c0 + c] = top[c];
           }
           if (!(ok = vote())) break;
           if (lane < kMine) {
@@ -1021,18 +1024,18 @@ __global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __gri
       const int live = p.group * g.count - g.qg * NC - first;  // columns that there are
       const size_t out = tree_out_row(p, g.b, g.g, 0) * p.head_dim;
 #pragma unroll 1
-      for (int x = 0; x < kMine * L::kHalves; x += 4) {
+      for (int x = 0; x < kMine * L::kHalves; x += kStep) {
         const int c0 = x % kMine, half = x / kMine, d = half * 128 + row;
         if (c0 >= live) continue;
-        uint32_t o[L::kPParts][4];
+        uint32_t o[L::kPParts][kStep];
 #pragma unroll
-        for (int k = 0; k < L::kPParts; ++k) tmem_ld4(to + half * L::kON + k * NC + c0, o[k]);
+        for (int k = 0; k < L::kPParts; ++k) tmem_ld8(to + half * L::kON + k * NC + c0, o[k]);
 #pragma unroll
-        for (int k = 0; k < L::kPParts; ++k) tmem_wait_ld4(o[k]);
+        for (int k = 0; k < L::kPParts; ++k) tmem_wait_ld8(o[k]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kStep; ++c) {
           const int col = c0 + c, place = first + col;
-          if (col >= live) continue;
+          if (col >= live) break;
           float sum = __uint_as_float(o[L::kPParts - 1][c]);
 #pragma unroll
           for (int k = L::kPParts - 2; k >= 0; --k) sum = fmaf(sum, 0.0625f, __uint_as_float(o[k][c]));
