@@ -3,8 +3,8 @@
 //
 // A unit is NC = 8, 16 or 32 (head, query) columns c = head * count + query of one row's
 // kv head (queries that the row has not take no part). Its tokens form tiles of 128; equal
-// contiguous shares of all units' tiles go to two CTAs per SM (TreeWalk in ol_tree.cuh):
-// while one ends a segment or waits, the other has the SM. K and V go to the tensor cores
+// contiguous shares of all units' tiles go to two (heads of 64: three) CTAs per SM (TreeWalk in
+// ol_tree.cuh): while one ends a segment or waits, the others have the SM. K and V go to the tensor cores
 // as they lie in the cache, with the tokens (for V the dimensions) as the products' 128
 // rows, so that the columns may be few and nothing is unpacked:
 //   S = K Q'    128 tokens x 2 NC x D.  Q' holds each q, times a power of two, in two
@@ -32,7 +32,7 @@
 // zeros for V's rows outside the row's tokens: P = 0 times a NaN code must not be NaN),
 // 2 the tiles' scales, 3 the queries' parts, 4-7 the softmax; of 32 columns in two groups
 // of four warps, 16 columns each (more warps to hide each other's latencies: 64 queries over
-// 8 rows to 6000 tokens 138 and 69 us). The others learn of the segments from the first,
+// 8 rows to 6000 tokens 138 and 73 us; now 66). The others learn of the segments from the first,
 // through a ring: the walk in line in each of them, and the loops of waits (wait_long), made
 // the kernel outgrow the instruction cache (258 and 160 us for the first line below).
 //
@@ -41,9 +41,9 @@
 //   the same in pages of 16           171   6.3 TB/s: boxes of 2 KB
 //   64 rows to 16384, pages of 16     183   5.9 TB/s: ragged ends beside the above
 //   heads of 256, 64 rows of 4096     166   6.5 TB/s
-//   heads of 64, 64 rows of 8192       97   5.6 TB/s: the softmax warps' chain of a tile
+//   heads of 64, 64 rows of 8192       94   5.7 TB/s: the softmax warps' chain of a tile
 //   heads of 80, 64 rows of 8192      236   2.8 TB/s: rows that straddle lines in the copies
-//   the first with 4 / 8 queries      164 / 227   P's parts: 32 bits of codes a weight
+//   the first with 4 / 8 queries      164 / 202   P's parts: 32 bits of codes a weight
 //   fp32 queries, 64 rows of 2048      52   as the first line would take 40 (the merge, and shares'
 //                                           begins and ends, weigh more); 8 queries 175: four units
 //                                           of 8 columns read K and V in turn, from L2
@@ -64,7 +64,10 @@ constexpr int kScales = 8;        // tiles whose scales are known ahead
 constexpr int kSegs = 8;          // segments known ahead
 constexpr float kTop = 5.f;       // log2 of the largest P when a reference is set
 constexpr float kGrown = 8.f;     // and of what makes a new one necessary
-constexpr int kMostSmem = (233472 - 2 * 1024) / 2;  // of one of two CTAs
+// CTAs of an SM. Heads of 64 have tiles of half the bytes: three hide more of a tile's chain (64 rows
+// of 8192, 1 / 4 queries 97.5 / 129 and 93.4 / 121 us); with larger ones three rings are too short to
+// keep the memory busy (heads of 128 162 and 173 us, but 256 rows of 64 tokens 33.4 and 31.3).
+constexpr int ctas_of(int D, int NC, bool WIDE) { return D == 64 && NC <= 16 && !WIDE ? 3 : 2; }
 
 // D: 64, 128 or 256 elements, what heads up to it take: the copies put zeros behind a
 // row of the cache, and there are none of its bytes to read.
@@ -82,6 +85,7 @@ struct Lay {
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + kQBuffers * kQBytes;
   static constexpr int kRing = kP + kPBytes;            // K and V tiles in turn, half after half
+  static constexpr int kCtas = ctas_of(D, NC, WIDE), kMostSmem = (233472 - kCtas * 1024) / kCtas;
   static constexpr int kSmall = 1536 + NC * 112;          // what follows the ring, at most
   static constexpr int kFit = (kMostSmem - kSmall - kRing) / kTileBytes;
   static constexpr int kSlots = kFit < 12 ? kFit : 12;
@@ -99,11 +103,11 @@ struct Lay {
   static constexpr int kNumBars = 2 * kSlots + 4 + 4 + 5 + 2 * kScales + 2 * kSegs;
   static constexpr int kMisc = kBars + kNumBars * 8;          // TMEM address, abort flag
   static constexpr int kTotal = kMisc + 8;
-  static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of two CTAs");
+  static_assert(kTotal <= kMostSmem && kSlots >= 4, "shared memory of one of the CTAs");
   static_assert(kRing % 1024 == 0 && kP % 1024 == 0 && kQBytes % 512 == 0, "swizzled tiles");
   // TMEM's columns: two S, O of each half; 64, 128 or 256
   static constexpr int kO = 2 * kSN, kUsed = kO + kON * kHalves, kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
-  static_assert(kUsed <= 256, "of one of two CTAs");
+  static_assert(kUsed <= kTmem && kTmem * kCtas <= 512, "all CTAs' accumulators");
 };
 
 // ------------------------------------------------------------------ tcgen05
@@ -294,7 +298,7 @@ __device__ __forceinline__ void parts_of(uint64_t w, uint32_t (&part)[N]) {
 }
 
 template <int D, int NC, bool PAGED, bool WIDE>
-__global__ void __launch_bounds__(threads_of(NC), 2) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
+__global__ void __launch_bounds__(threads_of(NC), ctas_of(D, NC, WIDE)) fast_fp8_kernel(const __grid_constant__ CUtensorMap map,
                                                                const __grid_constant__ Fp8AttnParams fp, const int box) {
   using L = Lay<D, NC, WIDE>;
   constexpr int kWarps = 4 * L::kGroups;  // of the softmax
@@ -1132,7 +1136,8 @@ void plan_fp8_attention(Fp8AttnParams& fp, int sms) {
   p.rows_per_unit = columns <= 8 || p.dtype == OL_F32 ? 8 : columns <= 16 || p.head_dim > 128 ? 16 : 32;
   p.units_per_head = (columns + p.rows_per_unit - 1) / p.rows_per_unit;
   p.tile_log2 = kTreeFastTileLog2;
-  p.nctas = 2 * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
+  const int dim = p.head_dim <= 64 ? 64 : p.head_dim <= 128 ? 128 : 256;
+  p.nctas = ctas_of(dim, p.rows_per_unit, p.dtype == OL_F32) * (sms < kTreeMaxCtas ? sms : kTreeMaxCtas);
   // (0 / 1 / 2 / 3 tiles: chunks of 4 tokens over 32 ragged rows - / 68 / 65 / 63 us; longer shares do not feel it)
   p.extra = 3;
   p.compact = 1;
@@ -1140,7 +1145,7 @@ void plan_fp8_attention(Fp8AttnParams& fp, int sms) {
   // Where the memory sets the pace, SMs differ in what they get of it: the last shares are for those that are ahead.
   // (64 rows of 8192 tokens, one query of 4 heads a kv head: 166 us, with the pool 161; ragged rows to 16384 in pages of
   // 16 189 and 183; heads of 80 242 and 236.) Where the SM itself does, shares are equal as they are (16 columns 167 and
-  // 185 us, heads of 64 105 and 110).
+  // 185 us, heads of 64 94 and 98).
   p.pool = columns > 8 || p.head_dim <= 64 ? 0 : 752 - p.nctas < 448 ? 752 - p.nctas : 448;
   p.by_unit = tree_few_units(p);
 }
