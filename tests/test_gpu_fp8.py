@@ -666,6 +666,65 @@ def test_the_workspace_serves_a_tree_call_too():
 
 # ------------------------------------------------------ the operators as they are used
 
+def test_the_pool_in_a_captured_call():
+    """The shares' counter is 0 again after every replay, also of a graph with two calls."""
+    a = Attention("f32", 16, 8, 8, 128, 64, 0, 1, [20000 + b for b in range(16)], seed=4)  # 156 tiles a row and head: 65 a CTA
+    a.call()
+    first = a.out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.call()
+        a.call()
+    for _ in range(3):
+        a.out.fill_(-77.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a.out, first)
+    assert ol.ol_workspace_status(a.ws) == ol.OL_DEVICE_OK
+
+
+@pytest.mark.parametrize("dt,D,window", [("bf16", 128, -1), ("f32", 64, 20), ("bf16", 256, -1)])
+def test_a_captured_decode_step(dt, D, window):
+    """Norms with rotation, append and attention in one graph: replayed with the positions it finds, it leaves the cache
+    and gives the outputs of the calls one by one."""
+    B, Hq, H, block, steps = 3, 8, 2, 16, 20
+    start = [5, 40, 0]
+    one, two = (Cache(B, H, 64, D, block, 16, seed=11) for _ in range(2))
+    for c in (one, two):
+        c.fill(start)
+    assert torch.equal(one.codes, two.codes) and torch.equal(one.scales[~one.scales.isnan()], two.scales[~two.scales.isnan()])
+    rope, norm, dtype = ol.rope(D, device=DEV), ol.head_norm(), TORCH[dt]
+    qkv = torch.zeros((B, 1, Hq + 2 * H, D), device=DEV, dtype=dtype)
+    q, k, v = qkv.transpose(1, 2).split((Hq, H, H), dim=1)
+    qr, kr = torch.empty((B, Hq, 1, D), device=DEV, dtype=dtype), torch.empty((B, H, 1, D), device=DEV, dtype=dtype)
+    at, lens = np.array(start, np.int32), np.array(start, np.int32) + 1
+    at_d, lens_d = dev(at), dev(lens)
+    n = ol.ol_workspace_size_fp8kv(B, Hq, H, D, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    ol.ol_workspace_init(ws, n)
+
+    def step(c, out, at, lens):
+        ol.ol_norm_rope_rows(rope, norm, CODE[dtype], B, 1, D, Hq, q, qr, H, k, kr, at_d, False)
+        ol.ol_fp8kv_append(c.desc, c.codes, CODE[dtype], 1, kr, v, at, at_d)
+        ol.ol_fp8kv_attention(c.desc, CODE[dtype], qr, Hq, 1, lens, lens_d, None, None, 0.0, window, out, CODE[dtype], ws, n)
+
+    outs = [torch.empty((B, Hq, 1, D), device=DEV, dtype=dtype) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(one, outs[0], at, lens)
+    for i in range(steps):
+        qkv.normal_(generator=one.gen)
+        at_d.copy_(dev(at + i))
+        lens_d.copy_(dev(lens + i))
+        graph.replay()
+        step(two, outs[1], at + i, lens + i)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and not bool(outs[0].isnan().any())
+    assert torch.equal(one.codes, two.codes)
+    assert torch.equal(one.scales.nan_to_num(nan=-1.0), two.scales.nan_to_num(nan=-1.0))
+    assert ol.ol_workspace_status(ws) == ol.OL_DEVICE_OK
+
+
 @pytest.mark.parametrize("page", [0, 32])
 def test_a_prompt_then_steps(page):
     """A projection's output normed and rotated, appended, attended: a ragged prompt in chunks, then single tokens; the
