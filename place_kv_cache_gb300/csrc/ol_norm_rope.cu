@@ -11,10 +11,10 @@
 // sines and cosines stay in registers (the groups compute a share of these each). Others,
 // and views without 16-byte alignment, go by CTAs that keep them in shared memory.
 //
-// Bounds: 2 * D * elt bytes a vector. 4 x 4096 tokens of 32 + 8 bf16 heads of 128: 63.6 us
-// (5.3 TB/s, 78 % of a copy's rate; CTAs with the tables in shared memory: 121); 3 x 2047
-// fp32 tokens of 28 + 4 heads of 96, 48 rotated: 31.9 us (4.7 TB/s). What is left is the
-// issue of about 10 instructions an element pair (2.4 to 2.9 a cycle) at 7 to 9 CTAs an SM.
+// Bounds: 2 * D * elt bytes a vector. 4 x 4096 tokens of 32 + 8 bf16 heads of 128: 56 us
+// (6.0 TB/s, 89 % of a copy's rate; CTAs with the tables in shared memory 121, a warp's next
+// vector in registers 64: too few bytes on their way); 3 x 2047 fp32 tokens of 28 + 4 heads
+// of 96, 48 rotated: 30.5 us (5.0 TB/s: 12 of 16 lanes have elements).
 // A decode step (64 rows of one token) is the launch and its chain of loads, 2.8 us:
 // tokens fewer than kManyWarps are cut into slices of their vectors.
 #include "ol_common.cuh"
@@ -93,7 +93,16 @@ __device__ __forceinline__ long long position(const NormRopeParams& p, int token
   return p.angles ? p.angles[token] : (long long)p.positions[b] + t;
 }
 
-constexpr int kWarps = 4;  // of a CTA, each with its own work
+constexpr int kWarps = 4;   // of a CTA, each with its own work
+constexpr int kStages = 4;  // steps of a warp, the one at work among them (2 / 3 / 4: the line of 56 us 64.5 / 56.4 / 55.8)
+
+// 16 bytes from global to shared memory, past L1; a thread's copies in groups.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Warp x has slice x % slices of token x / slices: `per_slice` of the vectors, 32 / lanes
 // * U at a time, the next ones on their way while these are worked on. A lane turns its
@@ -103,7 +112,7 @@ constexpr int kWarps = 4;  // of a CTA, each with its own work
 // rotated part by their weights alone).
 template <typename T, int VE, bool HALF>
 constexpr int ctas_of() {  // of an SM: the best of 5 to 9 (a few bytes spilled cost less than fewer warps)
-  return sizeof(T) == 4 ? 9 : HALF || VE == 16 ? 7 : 6;
+  return sizeof(T) == 4 ? 8 : 6;
 }
 template <typename T, int VE, bool HALF, bool TAIL, int U>  // TAIL: past the rotated part there are elements
 __global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
@@ -111,7 +120,11 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
   using P = Piece<T, VE>;
   using I = WarpItems<VE, HALF>;
   constexpr int NP = HALF ? VE : VE / 2;  // pairs of an item
+  constexpr int kPer = 16 / sizeof(T);  // elements of a copy; a lane has two a step
+  constexpr bool kWide = sizeof(P) == 32;
+  static_assert((HALF ? 2 : 1) * U * sizeof(P) == 32, "two copies a lane and step");
   __shared__ float2 turn[kWarps][32 * NP];
+  __shared__ uint4 ring[kWarps][kStages][2][32];
   const unsigned warp = blockIdx.x * kWarps + threadIdx.x / 32;  // (up to 2^31 + 2)
   if (warp / slices >= (unsigned)p.batch * p.tokens) return;
   const int token = warp / slices, slice = warp - token * slices;
@@ -137,18 +150,25 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
     T* const out = reinterpret_cast<T*>(kind ? p.out[1].data : p.out[0].data) +
                    (kind ? b * p.out[1].sb + t * p.out[1].st : b * p.out[0].sb + t * p.out[0].st) + ea;
     const T* const weight = reinterpret_cast<const T*>(kind ? p.weight[1] : p.weight[0]);
-    P x[U], z[U];
-    auto load = [&](int h0) {
+    // (wide pieces: the group's lanes copy neighbouring 16 bytes, each reads its own 32)
+    uint4(*const slots)[2][32] = ring[threadIdx.x / 32];
+    const int in_group = group * 2 * lanes;
+    auto fetch = [&](int h0, int stage) {  // a lane's pieces of a step
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + u * groups;
-        if (h >= last || !mine) continue;
-        const T* const from = in + h * in_step;
-        x[u] = *reinterpret_cast<const P*>(from);
-        if (two) z[u] = *reinterpret_cast<const P*>(from + (eb - ea));
+      for (int c = 0; c < 2; ++c) {
+        const int h = U == 2 ? h0 + c * groups : h0;
+        if (kWide) {
+          const int j = c * lanes + lane;
+          if (h < last && j < 2 * items.total) copy16(smem_u32(&slots[stage][0][in_group + j]), in + h * in_step + (j * kPer - ea));
+          continue;
+        }
+        if (h >= last || !(HALF && c == 1 ? two : mine)) continue;
+        copy16(smem_u32(&slots[stage][c][wl]), in + h * in_step + (HALF && c == 1 ? eb - ea : 0));
       }
+      copies_commit();
     };
-    load(first + group);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + group + i * groups * U, i);
     if (p.turns && !turned_yet) {  // group g computes pairs g, g + groups, ... of the lanes' items
       turned_yet = true;
       const long long at = position(p, token, b, t);
@@ -185,7 +205,23 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
         }
       }
     }
+    int stage = 0;
     for (int h0 = first + group; h0 - group < last; h0 += groups * U) {  // (whole warps: the shuffles)
+      copies_wait<kStages - 2>();
+      if (kWide) __syncwarp();
+      P x[U], z[U];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint4 piece = kWide ? slots[stage][0][in_group + 2 * lane + c] : slots[stage][c][wl];
+        if (HALF)
+          *reinterpret_cast<uint4*>(c ? &z[0] : &x[0]) = piece;
+        else if (U == 2)
+          *reinterpret_cast<uint4*>(&x[c % U]) = piece;
+        else
+          reinterpret_cast<uint4*>(&x[0])[c] = piece;
+      }
+      fetch(h0 + (kStages - 1) * groups * U, stage ? stage - 1 : kStages - 1);  // (the slot that was read last)
+      if (++stage == kStages) stage = 0;
       uint64_t va[U][VE / 2], vb[U][HALF ? VE / 2 : 1];
       float sum[U];
 #pragma unroll
@@ -204,7 +240,6 @@ __global__ void __launch_bounds__(32 * kWarps, ctas_of<T, VE, HALF>())
         const float2 s = unpack2(s2);
         sum[u] = s.x + s.y;
       }
-      load(h0 + groups * U);
       for (int o = lanes / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int u = 0; u < U; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], o);
@@ -371,9 +406,7 @@ cudaError_t launch_items(const NormRopeParams& p, int lanes, cudaStream_t s) {
 
 template <typename T, int VE, bool HALF>
 cudaError_t launch_warps(const NormRopeParams& p, int lanes, cudaStream_t s) {
-  // Two pieces of a vector a lane: a second vector in flight spills (4 x 4096 tokens of 32 + 8
-  // heads of 128, half style: bf16 90 us, with one 66; fp32 122 and 108). One piece: it pays
-  // (interleaved bf16 of 136 111 us, with one 120; fp32 of 100 97 and 124).
+  // 32 bytes a lane and step: two pieces of a vector, or one piece of two vectors.
   constexpr int U = HALF || sizeof(T) * VE == 32 ? 1 : 2;
   const int heads = p.q_heads + p.kv_heads, tokens = p.batch * p.tokens, step = 32 / lanes * U;
   const int rounds = (heads + step - 1) / step;
