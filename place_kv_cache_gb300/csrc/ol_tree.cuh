@@ -115,9 +115,8 @@ __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
 __device__ __forceinline__ int tree_units(const TreeParams& p, const TreeRow& r) {
   return p.compact ? (p.group * r.count + p.rows_per_unit - 1) / p.rows_per_unit : p.units_per_head;
 }
-// Row r of a kv head's, as its row of q and out counted from the kv head's first.
+// Row r of a kv head's (compact), as its row of q and out counted from the kv head's first.
 __device__ __forceinline__ int tree_live_row(const TreeParams& p, int count, int r) {
-  if (!p.compact) return r;
   const int head = r / count;
   return head * p.nodes + (r - head * count);
 }
