@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(threads_of(NC), ctas_of(D, NC, WIDE)) fast_fp8
 
   if (warp == 0) {
     // ------------------------------------------------------- the walk, producer
-    TreeWalk w(p);
+    TreeWalkOf<true> w(p);
     const uint64_t policy = p.units_per_head > 1 ? policy_evict_normal() : policy_evict_first();
     // Three tiles ahead: their boxes and this lane's page are known (the table's entries
     // on their way) before the ring has room for them. Lane = box.

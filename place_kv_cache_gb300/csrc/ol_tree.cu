@@ -319,7 +319,7 @@ cudaError_t launch_rows(const TreeParams& p, cudaStream_t s) {
 // CTA, for more CTAs, 20 loads a thread. Else by reading the partials from L2, for
 // which many resident warps do more than many loads each: 16 rows a CTA, 8 loads,
 // four CTAs an SM (64 nodes over 32 rows 137 us in all; 32 rows, 16 loads 141).
-template <int ROWS, int THREADS, int D4>  // D4: groups of four dimensions, 32 or 64
+template <int ROWS, int THREADS, int D4, bool COMPACT>  // D4: groups of four dimensions, 32 or 64
 __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(const TreeParams p) {
   constexpr int kLanes = THREADS / ROWS;  // threads of a row
   constexpr int G = kLanes > D4 ? kLanes / D4 : 1, KG = kLanes > D4 ? 1 : D4 / kLanes;
@@ -330,16 +330,16 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   __shared__ float other_l[G > 1 ? (G - 1) * ROWS : 1];
   pdl_wait();
   pdl_launch_dependents();
-  if (p.pool > 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
+  if (COMPACT && p.pool > 0 && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ticket = 0;
   const TreeSplit u = p.splits[blockIdx.x];  // (on its way beside the row's length)
   if (p.by_unit) {
     const TreeRow row = read_tree_row(p, blockIdx.x / (p.kv_heads * p.units_per_head));
-    if (row.ntiles == 0 || (int)blockIdx.x % p.units_per_head >= tree_units(p, row)) return;  // no note
+    if (row.ntiles == 0 || (int)blockIdx.x % p.units_per_head >= tree_units<COMPACT>(p, row)) return;  // no note
   }
   if (u.last < 0 || (int)blockIdx.y * ROWS >= u.rows) return;
   // (a note that no one wrote: the workspace was not initialised, or a launch before failed)
-  if (p.pool > 0 && (u.first < 0 || u.last >= p.nctas + p.pool || u.rows > p.rows_per_unit || u.row0 < 0 || u.count < 1 ||
-                     u.out < 0 || u.out + (p.compact ? (long long)(p.group - 1) * p.nodes + u.count : u.rows) >
+  if (COMPACT && p.pool > 0 && (u.first < 0 || u.last >= p.nctas + p.pool || u.rows > p.rows_per_unit || u.row0 < 0 || u.count < 1 ||
+                     u.out < 0 || u.out + (long long)(p.group - 1) * p.nodes + u.count >
                                       (long long)p.batch * p.q_heads * p.nodes ||
                      u.row0 + u.rows > p.group * u.count)) {
     set_status(p.status, OL_DEVICE_GUARD);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   const int RU = p.rows_per_unit, D = p.head_dim;
   const int lr = threadIdx.x % ROWS, lane = threadIdx.x / ROWS, d0 = lane % D4, grp = lane / D4;
   const int place = blockIdx.y * ROWS + lr;  // row of the unit
-  const bool mine = place < u.rows && (p.compact || (u.row0 + place) % p.nodes < u.count);
+  const bool mine = place < u.rows && (COMPACT || (u.row0 + place) % p.nodes < u.count);
   const int segs = u.last - u.first + 1;
   auto slot_of = [&](int i) { return tree_slot(p, 2 * (u.first + i) + (i == 0)); };
   float M = -INFINITY, L = 0.f;
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   }
   if (!mine) return;
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const size_t out = (size_t)(u.out + (p.compact ? tree_live_row(p, u.count, u.row0 + place) : place)) * D;
+  const size_t out = (size_t)(u.out + (COMPACT ? tree_live_row(p, u.count, u.row0 + place) : place)) * D;
 #pragma unroll
   for (int k = 0; k < KG; ++k) {
     const int d = (d0 + k * kLanes) * 4;
@@ -436,11 +436,11 @@ __global__ void __launch_bounds__(THREADS, ROWS > 8 ? 4 : 1) tree_merge_kernel(c
   }
 }
 
-template <int ROWS, int THREADS>
+template <int ROWS, int THREADS, bool COMPACT>
 cudaError_t launch_merge(const TreeParams& p, int rows, cudaStream_t s) {
   const dim3 grid(p.by_unit ? p.batch * p.kv_heads * p.units_per_head : p.nctas + p.pool, (rows + ROWS - 1) / ROWS), block(THREADS);
-  return p.head_dim <= 128 ? launch_pdl(tree_merge_kernel<ROWS, THREADS, 32>, grid, block, 0, s, p)
-                           : launch_pdl(tree_merge_kernel<ROWS, THREADS, 64>, grid, block, 0, s, p);
+  return p.head_dim <= 128 ? launch_pdl(tree_merge_kernel<ROWS, THREADS, 32, COMPACT>, grid, block, 0, s, p)
+                           : launch_pdl(tree_merge_kernel<ROWS, THREADS, 64, COMPACT>, grid, block, 0, s, p);
 }
 
 // --------------------------------------------------------------- accepted path
@@ -541,11 +541,12 @@ cudaError_t launch_generic_tree(const TreeParams& p, cudaStream_t s) {
 
 cudaError_t launch_tree_merge(const TreeParams& p, cudaStream_t s) {
   const int rows = p.group * p.nodes < p.rows_per_unit ? p.group * p.nodes : p.rows_per_unit;
-  if (!p.by_unit) return launch_merge<16, 256>(p, rows, s);
+  if (!p.compact) return p.by_unit ? launch_merge<8, 512, false>(p, rows, s) : launch_merge<16, 256, false>(p, rows, s);
+  if (!p.by_unit) return launch_merge<16, 256, true>(p, rows, s);
   // Few rows of few units: their partial results through more SMs (7 rows of 4 units of 33 segments 13.2 us in all, with
   // two rows a CTA 12.4; 4 rows of 8 units 18.1 and 15.6). With more rows there are CTAs enough (40 rows of 12 units
   // 24.0 and 25.4).
-  return p.compact && rows <= 8 ? launch_merge<2, 256>(p, rows, s) : launch_merge<8, 512>(p, rows, s);
+  return rows <= 8 ? launch_merge<2, 256, true>(p, rows, s) : launch_merge<8, 512, true>(p, rows, s);
 }
 
 cudaError_t launch_tree_keep(const KeepParams& p, cudaStream_t s) {

@@ -111,9 +111,11 @@ __device__ __forceinline__ TreeRow read_tree_row(const TreeParams& p, int b) {
   return tree_row(n, c, p.window, p.tile_log2);
 }
 
-// Units of a row's kv head.
+// Units of a row's kv head. (COMPACT is TreeParams::compact throughout, known to the compiler: as a
+// value of the call's it cost small trees 4 %.)
+template <bool COMPACT>
 __device__ __forceinline__ int tree_units(const TreeParams& p, const TreeRow& r) {
-  return p.compact ? (p.group * r.count + p.rows_per_unit - 1) / p.rows_per_unit : p.units_per_head;
+  return COMPACT ? (p.group * r.count + p.rows_per_unit - 1) / p.rows_per_unit : p.units_per_head;
 }
 // Row r of a kv head's (compact), as its row of q and out counted from the kv head's first.
 __device__ __forceinline__ int tree_live_row(const TreeParams& p, int count, int r) {
@@ -134,7 +136,8 @@ __device__ __forceinline__ int tree_live_row(const TreeParams& p, int count, int
 // sixth in what the memory gives them): the first half of them of three times the
 // tiles of the second. What a share is does not depend on who takes it.
 // The constructor is for whole warps; next() may be called by single threads.
-struct TreeWalk {
+template <bool COMPACT>
+struct TreeWalkOf {
   int b, g, qg;
   TreeRow row;
   int tile0, tile1;
@@ -151,10 +154,10 @@ struct TreeWalk {
     return r.ntiles > 0 ? r.ntiles + p.extra : 0;
   }
   __device__ __forceinline__ static int head_tiles(const TreeParams& p, const TreeRow& r) {
-    return tiles(p, r) * tree_units(p, r);
+    return tiles(p, r) * tree_units<COMPACT>(p, r);
   }
 
-  __device__ __forceinline__ explicit TreeWalk(const TreeParams& p) {
+  __device__ __forceinline__ explicit TreeWalkOf(const TreeParams& p) {
     const int lane = threadIdx.x & 31, c = blockIdx.x;
     total = 0;
     for (int base = 0; base < p.batch; base += 32) {
@@ -167,7 +170,7 @@ struct TreeWalk {
     share = each = more = tile0 = tile1 = slot = pool = small = 0;
     pool_at = total;
     if (shares > 0) {
-      if (p.pool > 0 && total >= 64 * shares) {  // (less would not pay for the shares' own begins and ends)
+      if (COMPACT && p.pool > 0 && total >= 64 * shares) {  // (less would not pay for the shares' own begins and ends)
         small = min(total / (24 * shares), 6);
         pool = min(p.pool, total / (12 * small)) & ~1;
         pool_at = total - pool * 2 * small;
@@ -185,7 +188,7 @@ struct TreeWalk {
     if (i < shares) {
       at = i * each + min(i, more);
       end = at + each + (i < more);
-    } else if (i - (int)gridDim.x < pool && i >= (int)gridDim.x) {
+    } else if (COMPACT && i - (int)gridDim.x < pool && i >= (int)gridDim.x) {
       const int k = i - gridDim.x, big = min(k, pool / 2);
       at = pool_at + (k + 2 * big) * small;
       end = at + (k < pool / 2 ? 3 : 1) * small;
@@ -197,7 +200,7 @@ struct TreeWalk {
 
   // The share that has tile x.
   __device__ __forceinline__ int share_of(int x) const {
-    if (x >= pool_at) {
+    if (COMPACT && x >= pool_at) {
       const int k = (x - pool_at) / small, half = pool / 2;  // in small shares
       return gridDim.x + (k < 3 * half ? k / 3 : k - 2 * half);
     }
@@ -225,7 +228,7 @@ struct TreeWalk {
         x -= __shfl_sync(0xffffffffu, incl - nt, src) * per_row;
         b = base + src;
         row = read_tree_row(p, b);
-        const int mine = tiles(p, row), units = tree_units(p, row);
+        const int mine = tiles(p, row), units = tree_units<COMPACT>(p, row);
         const int unit = x / mine;
         g = unit / units;
         qg = unit - g * units;
@@ -241,7 +244,7 @@ struct TreeWalk {
     while (at < end) {
       if (v1 == tiles(p, row)) {  // the unit is done: the next one
         v1 = 0;
-        if (++qg == tree_units(p, row)) {
+        if (++qg == tree_units<COMPACT>(p, row)) {
           qg = 0;
           if (++g == p.kv_heads) {
             g = 0;
@@ -276,8 +279,8 @@ struct TreeWalk {
       s.last = share_of(end + (row.ntiles - tile1) - 1);  // of the unit's last tile
       s.count = row.count;
       s.row0 = qg * p.rows_per_unit;
-      s.rows = min(p.rows_per_unit, p.group * (p.compact ? row.count : p.nodes) - s.row0);
-      s.out = (long long)tree_out_row(p, b, g, p.compact ? 0 : s.row0);
+      s.rows = min(p.rows_per_unit, p.group * (COMPACT ? row.count : p.nodes) - s.row0);
+      s.out = (long long)tree_out_row(p, b, g, COMPACT ? 0 : s.row0);
     }
     return s;
   }
@@ -298,6 +301,8 @@ struct TreeWalk {
     if (!p.by_unit) p.splits[blockIdx.x] = s;
   }
 };
+
+using TreeWalk = TreeWalkOf<false>;
 
 // Sets a kernel's attributes (f) before its first launch on each device.
 template <typename F>
